@@ -365,6 +365,8 @@ def _plain(s):
         held = torch.arange(L, device=device)[None] < s["lens"][:, None]
         return [q, keys.transpose(1, 2)[held].bfloat16(), values.transpose(1, 2)[held].bfloat16()]
     k, v = _cached(s)
+    if op == "prefill_q4":   # a chunk attends to the cache as it is read back: rounded to bf16 once
+        k, v = k.bfloat16().float(), v.bfloat16().float()
     L = k.shape[2]
     key = torch.arange(L, device=device)
     G = Hq // Hkv
@@ -500,6 +502,8 @@ def exact(case, seed):
             lses.append(torch.full((n, Hq), -math.inf, dtype=torch.float64, device=device))
             continue
         k, v = _exact_rows(s["cache"], s["table"][b], L)
+        if op == "prefill_q4":
+            k, v = (x.float().to(torch.bfloat16).double() for x in (k, v))
         o, l = torch.empty_like(q), torch.empty(n, Hq, dtype=torch.float64, device=device)
         hidden = None
         if op == "prefill_q4" and s["causal"]:
