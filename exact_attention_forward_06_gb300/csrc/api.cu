@@ -460,6 +460,16 @@ attn_status_t check_decode_args(const void *q, const void *k_pages, const void *
     return ATTN_OK;
 }
 
+attn_status_t device_state(int *sm_count, unsigned **status, uint64_t *budget_ns) {
+    DeviceInfo *di = nullptr;
+    const attn_status_t st = device_info(&di);
+    if (st != ATTN_OK) return st;
+    *sm_count = di->sm_count;
+    *status = di->status;
+    *budget_ns = budget();
+    return ATTN_OK;
+}
+
 }  // namespace attn
 
 extern "C" {

@@ -15,4 +15,8 @@ attn_status_t check_decode_args(const void *q, const void *k_pages, const void *
                                 const int32_t *seqlens, const void *out, const float *lse, int B, int Hq, int Hkv,
                                 int d, int page_size, int num_pages, int max_blocks_per_seq, float scale);
 
+// The current device's status word and SM count, and the wait budget: the
+// device is looked up once and must be one that the kernels are built for.
+attn_status_t device_state(int *sm_count, unsigned **status, uint64_t *budget_ns);
+
 }  // namespace attn

@@ -1,0 +1,77 @@
+// cache_ops.h -- host-side interface of the kernels around the paged cache:
+// head norms with the position rotation, the appends into the bf16 and the
+// 4-bit cache, and the attention over the 4-bit cache.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "attn.h"
+
+namespace attn {
+
+// The rotation and norms shared by attn_qk_norm_rope and the appends.
+struct RotateParams {
+    const void *q_weight;  // bf16 [d] or nullptr
+    const void *k_weight;
+    float eps;
+    const int32_t *positions;  // [n_axes][tokens] or nullptr
+    int n_axes;
+    const attn_rope_pair_t *rope;
+    int rotary_dim;
+    int interleaved;
+    unsigned *status;
+};
+
+struct NormRopeParams {
+    RotateParams r;
+    const void *q, *k;  // k may be nullptr (Hkv 0)
+    void *q_out, *k_out;
+    int B, S, Hq, Hkv, bhsd;
+    int64_t q_stride[3], k_stride[3];  // batch, position, head (elements)
+};
+
+struct AppendParams {
+    RotateParams r;
+    const void *q, *k, *v;  // q may be nullptr (Hq 0)
+    void *q_out;
+    void *k_pages, *v_pages;  // bf16 pools, or
+    void *cache;              // the 4-bit cache
+    const int32_t *block_table, *seqlens, *cu;  // cu nullptr: one token per sequence
+    int B, total, Hq, Hkv, num_pages, max_blocks;
+    int64_t q_stride, k_stride, v_stride;  // elements per token
+};
+
+struct GatherQ4Params {
+    const void *cache;
+    const int32_t *block_table, *seqlens, *cu_k;
+    void *k_out, *v_out;
+    int B, Hkv, total_k, num_pages, max_blocks;
+    unsigned *status;
+};
+
+struct DecodeQ4Params {
+    const void *q, *cache;
+    const int32_t *block_table, *seqlens;
+    void *out;
+    float *lse;
+    float *o_part;    // [B * Hq][nsplit][d], nsplit > 1 only
+    float *lse_part;  // [B * Hq][nsplit]
+    int B, Hq, Hkv, num_pages, max_blocks, nsplit, pages_per_split;
+    float scale_log2;
+    unsigned *status;
+    uint64_t budget_ns;
+};
+
+cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream);
+cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
+cudaError_t launch_gather_q4(const GatherQ4Params &p, cudaStream_t stream);
+// cu_k[0 .. B] from seqlens; a length outside [0, 16 max_blocks], or one that
+// takes the sum past max_total, counts as 0 and is reported.
+cudaError_t launch_q4_offsets(const int32_t *seqlens, int32_t *cu_k, int32_t *lens_out, int B, int max_blocks,
+                              int max_total, unsigned *status, cudaStream_t stream);
+void decode_q4_split_plan(int B, int Hq, int Hkv, int max_blocks, int *nsplit, int *pages_per_split);
+cudaError_t launch_decode_q4(const DecodeQ4Params &p, cudaStream_t stream);
+
+}  // namespace attn

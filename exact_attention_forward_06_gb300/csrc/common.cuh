@@ -38,6 +38,12 @@ enum WaitSite : unsigned {
     kSiteEpilogueSlot = 18,
     kSiteItem = 19,
     kSiteStoreCmd = 20,
+    kSiteAppendOffsets = 21,
+    kSiteRopeAxis = 22,
+    kSiteQ4Offsets = 23,
+    kSiteQ4Table = 24,
+    kSiteQ4Seqlen = 25,
+    kSiteQ4Page = 26,
 };
 
 // First error wins; the site is informative only.

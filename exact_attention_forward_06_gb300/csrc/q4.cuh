@@ -1,0 +1,54 @@
+// q4.cuh -- the 4-bit cache block (one page of one KV head, keys and values):
+// byte offsets, and the quantisation of a 32-channel group.
+#pragma once
+
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace attn {
+namespace q4 {
+
+constexpr int PAGE = 16;
+constexpr int D = 128;
+constexpr int BLOCK = 2560;
+constexpr int V_CODES = 1024;
+constexpr int K_SCALES = 2048;   // [token][group]
+constexpr int K_CENTERS = 2176;  // [token][group]
+constexpr int V_SCALES = 2304;   // [token][group]
+constexpr int V_CENTERS = 2432;  // [group][token]
+
+// Key codes of channels 8 w .. 8 w + 7 of token t: a 32-bit word.
+__host__ __device__ constexpr int k_word(int t, int w) { return t * 64 + (w & 3) * 16 + (w >> 2) * 4; }
+// Value codes of channels 32 g + 4 r .. + 3 of token t: a 16-bit half-word.
+__host__ __device__ constexpr int v_half(int t, int g, int r) {
+    return V_CODES + r * 128 + ((t & 7) >> 1) * 32 + (((t >> 3) ^ (r & 1)) << 4) + (t & 1) * 8 + g * 2;
+}
+
+// Center and scale (bf16 bits) of a group with largest member hi and smallest
+// lo, all bf16 values; `finite` says whether every member is finite.
+struct GroupScale {
+    uint16_t z, s;
+};
+
+__device__ __forceinline__ GroupScale group_scale(float hi, float lo, bool finite) {
+    if (!finite) return GroupScale{0x7fff, 0x7fff};
+    const float mid = __fadd_rn(__fmul_rn(0.5f, hi), __fmul_rn(0.5f, lo));
+    const uint32_t z = ptx::pack_bf16x2(mid, 0.f) & 0xffffu;
+    const float zf = __uint_as_float(z << 16);
+    const float dev = fmaxf(__fsub_rn(hi, zf), __fsub_rn(zf, lo));
+    const uint32_t s = ptx::pack_bf16x2(__fmul_rn(dev, (float)(2.0 / 15.0)), 0.f) & 0xffffu;
+    return GroupScale{(uint16_t)z, (uint16_t)s};
+}
+
+// The code of x.  A true division: the definition's rounding, not that of a
+// multiplication by a reciprocal.
+__device__ __forceinline__ uint32_t code_of(float x, GroupScale gs) {
+    const float s = __uint_as_float((uint32_t)gs.s << 16);
+    if (!(s > 0.f)) return 0;
+    const float t = __fadd_rn(__fdiv_rn(__fsub_rn(x, __uint_as_float((uint32_t)gs.z << 16)), s), 7.5f);
+    return (uint32_t)fminf(fmaxf(rintf(t), 0.f), 15.f);
+}
+
+}  // namespace q4
+}  // namespace attn

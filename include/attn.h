@@ -362,6 +362,192 @@ attn_status_t attn_decode_paged_noalloc(const void *q, const void *k_pages, cons
                                         int num_pages, int max_blocks_per_seq, float scale, void *stream);
 
 /*
+ * attn_rope_pair_t -- one rotated pair of channels: `turns` is the pair's
+ * angle per position as a fraction of a full turn in units of 2^-64 (so
+ * frequency / (2 pi) * 2^64, rounded), `axis` the position axis it turns with.
+ * position * turns modulo 2^64 is then the exact fraction of a turn, however
+ * far the position: no angle loses precision.  A negative frequency is its
+ * two's complement.  A plan is an array of rotary_dim / 2 of these in DEVICE
+ * memory, 16-byte aligned, made once by the caller; `reserved` is not read.
+ */
+typedef struct {
+    uint64_t turns;
+    uint32_t axis;
+    uint32_t reserved;
+} attn_rope_pair_t;
+
+/*
+ * attn_qk_norm_rope -- root-mean-square norm of every query and key head and
+ * the position rotation, in one pass over q and k.  For each head vector x:
+ *
+ *     y_c = x_c * w_c / sqrt(mean_c x_c^2 + eps)       (weight given; else y = x)
+ *     (y_a, y_b) -> (y_a cos t - y_b sin t, y_a sin t + y_b cos t),
+ *                   t = position[axis_i] * frequency_i, for each pair i
+ *
+ * computed in fp32 and rounded to bf16 once (to nearest even).  Pair i of
+ * rotary_dim / 2 is channels (i, i + rotary_dim / 2), or (2i, 2i + 1) with
+ * interleaved != 0; channels from rotary_dim on are not rotated.
+ *
+ * q, k: bf16, the element (b, s, h, c) at b * stride_b + s * stride_s +
+ *      h * stride_h + c (strides in elements, multiples of 8): views of a fused
+ *      projection need no copy.  k may be NULL (k_out is then not written and
+ *      Hkv not read).
+ * q_out, k_out: bf16, dense in `layout` ([B][S][H][d] or [B][H][S][d]).
+ *      q_out may be q itself (and k_out k) when its strides are the dense ones;
+ *      other overlaps are not allowed.
+ * q_weight, k_weight: bf16 [d], or NULL for no norm of that tensor.  eps >= 0.
+ * positions: int32 [n_axes][B][S], any values (negative ones too), or NULL:
+ *      position s on every axis.  1 <= n_axes <= 4.  An axis >= n_axes in the
+ *      plan is recorded as ATTN_ERR_DEVICE_BOUNDS and its pair not rotated.
+ * rope: the plan, or NULL with rotary_dim 0 for no rotation.  rotary_dim is a
+ *      multiple of 8, at most d (else ATTN_ERR_UNSUPPORTED).
+ */
+attn_status_t attn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
+                                const void *q_weight, const void *k_weight, float eps,
+                                const int32_t *positions, int n_axes,
+                                const attn_rope_pair_t *rope, int rotary_dim, int interleaved,
+                                int B, int S, int Hq, int Hkv, int d, int layout,
+                                size_t q_stride_b, size_t q_stride_s, size_t q_stride_h,
+                                size_t k_stride_b, size_t k_stride_s, size_t k_stride_h, void *stream);
+
+/*
+ * attn_append_paged -- write new tokens' keys and values into the paged cache
+ * that attn_fwd_paged and attn_decode_paged read, with the norm and rotation
+ * of attn_qk_norm_rope applied to k (and q) on the way.
+ *
+ * q: bf16 [total][Hq][d] or NULL (q_out, q_weight and Hq are then not read);
+ * k, v: bf16 [total][Hkv][d].  Token t's heads lie at t * stride (in elements, a
+ *      multiple of 8, at least the heads' d elements each), dense within a
+ *      token.
+ * q_out: bf16 [total][Hq][d], dense; may be q itself when q_stride is Hq * d.
+ * k_pages, v_pages: bf16 [num_pages][16][Hkv][d], written at the new tokens'
+ *      slots only.
+ * cu_seqlens: DEVICE int32 [B+1]; sequence b's new tokens are rows
+ *      cu_seqlens[b] .. cu_seqlens[b+1]-1; or NULL: one token per sequence
+ *      (total == B).
+ * seqlens_k: DEVICE int32 [B], the keys in each cache WITH the new tokens, as
+ *      attn_fwd_paged takes them: new token i of n goes to position
+ *      seqlens_k[b] - n + i.  So the same arrays serve the append and the
+ *      attention after it.
+ * positions: int32 [n_axes][total], or NULL: the token's position in the cache.
+ * Rows of no sequence are neither read into the cache nor written to q_out.
+ * Offsets out of order or range, a length below the sequence's new tokens or
+ * past the table, and a page outside [0, num_pages) are recorded as
+ * ATTN_ERR_DEVICE_BOUNDS; the tokens they concern are skipped (a bad page: only
+ * their keys and values).  No two tokens of a call may share a slot.  Other
+ * arguments as in attn_qk_norm_rope.
+ */
+attn_status_t attn_append_paged(const void *q, const void *k, const void *v, void *q_out,
+                                void *k_pages, void *v_pages,
+                                const int32_t *block_table, const int32_t *seqlens_k, const int32_t *cu_seqlens,
+                                const void *q_weight, const void *k_weight, float eps,
+                                const int32_t *positions, int n_axes,
+                                const attn_rope_pair_t *rope, int rotary_dim, int interleaved,
+                                int B, int total, int Hq, int Hkv, int d, int page_size,
+                                int num_pages, int max_blocks_per_seq,
+                                size_t q_stride, size_t k_stride, size_t v_stride, void *stream);
+
+/*
+ * ATTN_Q4_BLOCK_BYTES -- a cache held in 4 bits.
+ *
+ * The cache is uint8 [num_pages][Hkv][ATTN_Q4_BLOCK_BYTES]: one block holds the
+ * keys and values of 16 tokens of one KV head, in 5 bits an element (5/16 of the
+ * bf16 pages).  Each token's 32-channel group g has a bf16 scale s and center z
+ * and a code n in 0..15 per channel; the channel's value is z + s (n - 7.5).
+ * The group's bf16 values x (those the bf16 cache would hold) give
+ *
+ *     z = bf16(max / 2 + min / 2),  s = bf16(max(max - z, z - min) * (2 / 15)),
+ *     n = round((x - z) / s + 7.5), half to even, kept within 0..15; 0 where s is 0
+ *
+ * each step in fp32.  A group with a non-finite member gets z = s = NaN (and
+ * reads back as NaN).  Byte offsets in a block, for token t = 0..15 of the page:
+ *
+ *     0    key codes:   the 32-bit word of channels 8w .. 8w+7 (channel 8w + i in
+ *                       bits 4i ..) at 64 t + 16 (w % 4) + 4 (w / 4), w = 0..15
+ *     1024 value codes: the 16-bit half-word of channels 32g + 4r .. + 3 (channel
+ *                       32g + 4r + i in bits 4i ..) at 1024 + 128 r + 32 ((t % 8) / 2)
+ *                       + 16 ((t / 8) ^ (r % 2)) + 8 (t % 2) + 2 g, r = 0..7, g = 0..3
+ *     2048 key scales bf16 [16 tokens][4],    2176 key centers bf16 [16 tokens][4]
+ *     2304 value scales bf16 [16 tokens][4],  2432 value centers bf16 [4][16 tokens]
+ *
+ * (the orders in which the tensor-core fragments of the decode kernel take them).
+ */
+#define ATTN_Q4_BLOCK_BYTES 2560
+
+/*
+ * attn_append_paged_q4 -- attn_append_paged into a cache held in 4 bits: k after
+ * its norm and rotation, and v, are rounded to bf16 and then quantised as above.
+ * cache must be 16-byte aligned.  Other arguments and errors as there.
+ */
+attn_status_t attn_append_paged_q4(const void *q, const void *k, const void *v, void *q_out, void *cache,
+                                   const int32_t *block_table, const int32_t *seqlens_k, const int32_t *cu_seqlens,
+                                   const void *q_weight, const void *k_weight, float eps,
+                                   const int32_t *positions, int n_axes,
+                                   const attn_rope_pair_t *rope, int rotary_dim, int interleaved,
+                                   int B, int total, int Hq, int Hkv, int d, int page_size,
+                                   int num_pages, int max_blocks_per_seq,
+                                   size_t q_stride, size_t k_stride, size_t v_stride, void *stream);
+
+/*
+ * attn_gather_paged_q4 -- read sequences back from a cache held in 4 bits:
+ * k_out, v_out: bf16 [total_k][Hkv][d]; sequence b's seqlens[b] tokens go to the
+ * rows from cu_seqlens_k[b] on (DEVICE int32 [B+1]; cu_seqlens_k[b+1] -
+ * cu_seqlens_k[b] must equal seqlens[b]), each element z + s (n - 7.5) rounded
+ * to bf16 once: the k and v of attn_fwd_varlen.  Rows of no sequence are not
+ * written.  Offsets or lengths out of range are recorded as
+ * ATTN_ERR_DEVICE_BOUNDS and their sequence skipped; a page outside
+ * [0, num_pages) is recorded too and reads as zeros.
+ */
+attn_status_t attn_gather_paged_q4(const void *cache, const int32_t *block_table, const int32_t *seqlens,
+                                   const int32_t *cu_seqlens_k, void *k_out, void *v_out,
+                                   int B, int Hkv, int total_k, int d, int page_size,
+                                   int num_pages, int max_blocks_per_seq, void *stream);
+
+/*
+ * attn_decode_q4_workspace_bytes -- bytes of device workspace
+ * attn_decode_paged_q4 needs: a pure function of the arguments, 0 for invalid
+ * ones.
+ */
+size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int d, int max_blocks_per_seq);
+
+/*
+ * attn_decode_paged_q4 -- attn_decode_paged over a cache held in 4 bits: softmax
+ * attention of one query per sequence over the values that the codes stand for
+ * (not rounded to bf16), split over the keys and merged by log-sum-exp.
+ * q, block_table, seqlens, out, lse, scale and the errors as in
+ * attn_decode_paged; workspace at least attn_decode_q4_workspace_bytes(...)
+ * bytes, 256-byte aligned, its contents on entry of no matter.  Slots past a
+ * sequence's end may hold anything.  Deterministic.
+ */
+attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32_t *block_table,
+                                   const int32_t *seqlens, void *out, float *lse,
+                                   int B, int Hq, int Hkv, int d, int page_size,
+                                   int num_pages, int max_blocks_per_seq, float scale,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * attn_fwd_paged_q4 -- attn_fwd_paged over a cache held in 4 bits (chunked
+ * prefill): the caches are read back once into the workspace as bf16 (the
+ * values of attn_gather_paged_q4: z + s (n - 7.5) rounded once) and the packed
+ * prefill runs over them, so that no row block pays for the unpacking again.
+ * max_total_k: an upper bound, known on the host, of the sum of seqlens_k (the
+ *      sum itself is best).  A sequence whose length lies outside
+ *      [0, 16 * max_blocks_per_seq] or goes past the bound counts as empty (its
+ *      rows get O = 0 and lse = -inf) and is recorded as ATTN_ERR_DEVICE_BOUNDS.
+ * workspace: at least attn_fwd_paged_q4_workspace_bytes(...) bytes, 256-byte
+ *      aligned; its contents on entry do not matter.
+ * Other arguments and errors as in attn_fwd_paged.
+ */
+size_t attn_fwd_paged_q4_workspace_bytes(int B, int Hkv, int d, int max_total_k);
+
+attn_status_t attn_fwd_paged_q4(const void *q, const void *cache, const int32_t *block_table,
+                                const int32_t *seqlens_k, const int32_t *cu_seqlens_q, void *out, float *lse,
+                                int B, int Hq, int Hkv, int total_q, int max_seqlen_q, int d, int page_size,
+                                int num_pages, int max_blocks_per_seq, int max_total_k,
+                                int causal, float scale, int round_mode,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * attn_lse_merge -- merge key-range partial results by log-sum-exp (the merge
  * step of the Flash-Decoding style split).  For each row r:
  *     M = max_s lse_parts[r][s];  lse = M + ln sum_s exp(lse_parts[r][s] - M)
