@@ -216,7 +216,8 @@ attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32
     attn_status_t st = attn::check_decode_args(q, cache, cache, block_table, seqlens, out, lse, B, Hq, Hkv, d,
                                                page_size, num_pages, max_blocks_per_seq, scale);
     if (st != ATTN_OK) return st;
-    if ((int64_t)max_blocks_per_seq * 16 > 0x7fffffff) return ATTN_ERR_INVALID_ARG;
+    // Key positions are 32-bit; rows, and splits of at most 256 pages, are grid axes.
+    if ((int64_t)max_blocks_per_seq > 65535 * 256 || (int64_t)B * Hq > 0x7fffffff) return ATTN_ERR_INVALID_ARG;
     const size_t need = attn_decode_q4_workspace_bytes(B, Hq, Hkv, d, max_blocks_per_seq);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
     attn::DecodeQ4Params p = {};

@@ -1,13 +1,10 @@
 // cache_q4.cu -- reading a 4-bit cache: attn_gather_paged_q4 (back to packed
-// bf16 keys and values), the offsets of attn_fwd_paged_q4, and attention for
-// single tokens.
+// bf16 keys and values) and the offsets of attn_fwd_paged_q4.
 #include <cstdint>
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "cache_ops.h"
 #include "common.cuh"
-#include "norm_rope.cuh"
 #include "q4.cuh"
 
 namespace attn {
@@ -137,53 +134,6 @@ __global__ void __launch_bounds__(OFF_THREADS) offsets_kernel(const int32_t *seq
     }
 }
 
-// Simple decode: one warp per query row, four channels a lane.
-__global__ void __launch_bounds__(128) decode_simple_kernel(const DecodeQ4Params p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (int64_t)p.B * p.Hq) return;
-    const int b = (int)(row / p.Hq), hq = (int)(row % p.Hq), h = hq / (p.Hq / p.Hkv);
-    int L = p.seqlens[b];
-    if (L < 0 || L > p.max_blocks * PAGE) {
-        if (lane == 0) report_status(p.status, kStatusDeviceBounds, kSiteQ4Seqlen);
-        L = 0;
-    }
-    const uint2 qu = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.q) + row * D)[lane];
-    const float q[4] = {bf_lo(qu.x), bf_hi(qu.x), bf_lo(qu.y), bf_hi(qu.y)};
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    const int g = lane >> 3;
-    for (int t0 = 0; t0 < L; t0 += PAGE) {
-        const int page = p.block_table[(int64_t)b * p.max_blocks + t0 / PAGE];
-        if (page < 0 || page >= p.num_pages) {
-            if (lane == 0) report_status(p.status, kStatusDeviceBounds, kSiteQ4Table);
-            continue;
-        }
-        const uint8_t *blk = static_cast<const uint8_t *>(p.cache) + ((int64_t)page * p.Hkv + h) * BLOCK;
-        for (int t = 0; t < min(PAGE, L - t0); ++t) {
-            const uint32_t kc = *reinterpret_cast<const uint16_t *>(blk + k_word(t, lane >> 1) + 2 * (lane & 1));
-            const uint32_t vc = *reinterpret_cast<const uint16_t *>(blk + v_half(t, g, lane & 7));
-            const float ks = bf16_at(blk + K_SCALES + t * 8 + g * 2), kz = bf16_at(blk + K_CENTERS + t * 8 + g * 2);
-            const float vs = bf16_at(blk + V_SCALES + t * 8 + g * 2), vz = bf16_at(blk + V_CENTERS + g * 32 + t * 2);
-            float s = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s = fmaf(q[j], value_of(kc >> (4 * j) & 15, ks, kz), s);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-            s *= p.scale_log2;
-            const float mn = fmaxf(m, s);
-            const float a = m == -INFINITY ? 0.f : ptx::ex2(m - mn), e = ptx::ex2(s - mn);
-            m = mn;
-            l = l * a + e;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = fmaf(e, value_of(vc >> (4 * j) & 15, vs, vz), o[j] * a);
-        }
-    }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + row * D)[lane] =
-        make_uint2(ptx::pack_bf16x2(o[0] * inv, o[1] * inv), ptx::pack_bf16x2(o[2] * inv, o[3] * inv));
-    if (p.lse && lane == 0) p.lse[row] = l > 0.f || l != l ? (m + ptx::lg2(l)) * 0.6931471805599453f : -INFINITY;
-}
-
 }  // namespace q4
 
 cudaError_t launch_gather_q4(const GatherQ4Params &p, cudaStream_t stream) {
@@ -197,17 +147,6 @@ cudaError_t launch_gather_q4(const GatherQ4Params &p, cudaStream_t stream) {
 cudaError_t launch_q4_offsets(const int32_t *seqlens, int32_t *cu_k, int32_t *lens_out, int B, int max_blocks,
                               int max_total, unsigned *status, cudaStream_t stream) {
     q4::offsets_kernel<<<1, q4::OFF_THREADS, 0, stream>>>(seqlens, cu_k, lens_out, B, max_blocks, max_total, status);
-    return cudaGetLastError();
-}
-
-void decode_q4_split_plan(int B, int Hq, int Hkv, int max_blocks, int *nsplit, int *pages_per_split) {
-    *nsplit = 1;
-    *pages_per_split = max_blocks;
-}
-
-cudaError_t launch_decode_q4(const DecodeQ4Params &p, cudaStream_t stream) {
-    const int64_t grid = ((int64_t)p.B * p.Hq + 3) / 4;
-    q4::decode_simple_kernel<<<(unsigned)grid, 128, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
