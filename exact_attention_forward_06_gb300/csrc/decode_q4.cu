@@ -46,16 +46,18 @@ using q4::D;
 using q4::PAGE;
 
 constexpr int NW = 4;    // warps = page streams
-constexpr int NST = 5;   // pages in flight per warp
+constexpr int NST = 3;   // page pairs in flight per warp
 constexpr int COLS = 8;  // query heads per CTA (MMA columns)
 constexpr int NT = NW * 32;
-constexpr int CTAS_PER_SM = 4;
-constexpr int RING = NW * NST * BLOCK;
+constexpr int CTAS_PER_SM = 3;
+constexpr int STAGE = 2 * BLOCK;
+constexpr int RING = NW * NST * STAGE;
 constexpr int SMEM = RING + NW * NST * 8 + 16;  // ring, barriers, abort flag
 constexpr int MERGE_ROW = D + 2;
 static_assert(NW * COLS * MERGE_ROW * 4 <= RING, "the merge reuses the ring");
 static_assert(CTAS_PER_SM * (SMEM + 1024) <= 233472, "CTAs per SM");
-constexpr int MAX_PAGES_PER_SPLIT = 64 * NW;  // two table entries a lane
+constexpr int MAX_PAGES_PER_SPLIT = 64 * NW;  // a pair of table entries a lane
+constexpr float RAISE = 8.f;  // a score this far (in log2) above the running max raises it
 constexpr int TARGET_CTAS = 2048;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -77,11 +79,39 @@ __device__ __forceinline__ float group_f(uint2 s, int g) {
     return g & 1 ? hi_f(u) : lo_f(u);
 }
 
+// One page's words in registers, as the lane's fragments take them.
+struct PageWords {
+    uint4 ka, kb;    // key codes of tokens r4 and r4 + 8, channels 32 g + 8 c4 ..
+    uint4 va, vb;    // value codes of tokens 2 c4, 2 c4 + 1 and those + 8
+    uint2 ksa, ksb;  // key scales of tokens r4 and r4 + 8, all groups
+    uint2 kza, kzb;  // key centers
+    uint2 vsa, vsb;  // value scales
+    uint32_t vza, vzb;  // value centers of group r4 % 4, tokens 2 c4, 2 c4 + 1 and those + 8
+};
+
+__device__ __forceinline__ void load_page(PageWords &w, const uint8_t *blk, int r4, int c4) {
+    w.ka = *reinterpret_cast<const uint4 *>(blk + r4 * 64 + c4 * 16);
+    w.kb = *reinterpret_cast<const uint4 *>(blk + r4 * 64 + c4 * 16 + 512);
+    const uint8_t *v = blk + r4 * 128 + c4 * 32;
+    w.va = *reinterpret_cast<const uint4 *>(v + q4::V_CODES + ((r4 & 1) << 4));
+    w.vb = *reinterpret_cast<const uint4 *>(v + q4::V_CODES + (((r4 & 1) ^ 1) << 4));
+    const uint8_t *par = blk + r4 * 8;
+    w.ksa = *reinterpret_cast<const uint2 *>(par + q4::K_SCALES);
+    w.ksb = *reinterpret_cast<const uint2 *>(par + q4::K_SCALES + 64);
+    w.kza = *reinterpret_cast<const uint2 *>(par + q4::K_CENTERS);
+    w.kzb = *reinterpret_cast<const uint2 *>(par + q4::K_CENTERS + 64);
+    w.vsa = *reinterpret_cast<const uint2 *>(par + q4::V_SCALES);
+    w.vsb = *reinterpret_cast<const uint2 *>(par + q4::V_SCALES + 64);
+    const uint8_t *z = blk + q4::V_CENTERS + (r4 & 3) * 32 + c4 * 4;
+    w.vza = *reinterpret_cast<const uint32_t *>(z);
+    w.vzb = *reinterpret_cast<const uint32_t *>(z + 16);
+}
+
 __global__ void __launch_bounds__(NT, CTAS_PER_SM) split_kernel(const DecodeQ4Params p, int col_blocks) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r4 = lane >> 2, c4 = lane & 3;
-    uint8_t *ring = smem + warp * NST * BLOCK;
+    uint8_t *ring = smem + warp * NST * STAGE;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING) + warp * NST;
     volatile int *abort_flag = reinterpret_cast<int *>(smem + RING + NW * NST * 8);
 
@@ -108,11 +138,27 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) split_kernel(const DecodeQ4Pa
         }
         return;
     }
-    // This warp's pages: page0 + warp + NW * i, i < n.
-    const int n = warp < np ? (np - warp + NW - 1) / NW : 0;
-    const int32_t *row = p.block_table + (int64_t)b * p.max_blocks + page0 + warp;
-    const int tab0 = lane < n ? __ldg(row + NW * lane) : -1;
-    const int tab1 = lane + 32 < n ? __ldg(row + NW * (lane + 32)) : -1;
+    // This warp's page pairs: pages page0 + 2 (warp + NW i) and the next, i < n.
+    // Lane i holds pair i's pages (-1: none, or a bad entry) and their numbers
+    // of keys.
+    const int npairs = (np + 1) / 2;
+    const int n = warp < npairs ? (npairs - warp + NW - 1) / NW : 0;
+    int tab0 = -1, tab1 = -1, nv0 = 0, nv1 = 0;
+    if (lane < n) {
+        const int first = 2 * (warp + NW * lane);
+        const int32_t *row = p.block_table + (int64_t)b * p.max_blocks + page0 + first;
+        tab0 = __ldg(row);
+        if (first + 1 < np) tab1 = __ldg(row + 1);
+        const bool bad0 = tab0 < 0 || tab0 >= p.num_pages;
+        const bool bad1 = first + 1 < np && (tab1 < 0 || tab1 >= p.num_pages);
+        if (bad0 || bad1) report_status(p.status, kStatusDeviceBounds, kSiteQ4Table);
+        if (bad0) tab0 = -1;
+        if (bad1) tab1 = -1;
+        const int left = L - (page0 + first) * PAGE;
+        nv0 = bad0 ? 0 : min(PAGE, left);
+        nv1 = tab1 < 0 ? 0 : min(PAGE, left - PAGE);
+    }
+    const unsigned whole = __ballot_sync(0xffffffffu, nv0 == PAGE && nv1 == PAGE);
 
     if (lane == 0) {
         for (int s = 0; s < NST; ++s) ptx::mbar_init(full + s, 1);
@@ -125,17 +171,13 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) split_kernel(const DecodeQ4Pa
     const uint64_t pol = ptx::policy_evict_first();
     const uint8_t *cache = static_cast<const uint8_t *>(p.cache) + (int64_t)h * BLOCK;
     const int64_t page_step = (int64_t)p.Hkv * BLOCK;
-    auto page_of = [&](int i) { return __shfl_sync(0xffffffffu, i < 32 ? tab0 : tab1, i & 31); };
     auto issue = [&](int i, int slot) {
-        const int phys = page_of(i);
+        const int t0 = __shfl_sync(0xffffffffu, tab0, i), t1 = __shfl_sync(0xffffffffu, tab1, i);
         if (lane == 0) {
-            if (phys >= 0 && phys < p.num_pages) {
-                ptx::mbar_arrive_expect_tx(full + slot, BLOCK);
-                ptx::bulk_load(ring + slot * BLOCK, cache + phys * page_step, BLOCK, full + slot, pol);
-            } else {
-                report_status(p.status, kStatusDeviceBounds, kSiteQ4Table);
-                ptx::mbar_arrive(full + slot);
-            }
+            uint8_t *dst = ring + slot * STAGE;
+            ptx::mbar_arrive_expect_tx(full + slot, (t0 >= 0 ? BLOCK : 0) + (t1 >= 0 ? BLOCK : 0));
+            if (t0 >= 0) ptx::bulk_load(dst, cache + t0 * page_step, BLOCK, full + slot, pol);
+            if (t1 >= 0) ptx::bulk_load(dst + BLOCK, cache + t1 * page_step, BLOCK, full + slot, pol);
         }
     };
     const int ahead = min(n, NST);
@@ -143,10 +185,13 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) split_kernel(const DecodeQ4Pa
 
     // Q^T as the B operand: head r4 (zero past the CTA's columns), the channels
     // 32 g + 8 c4 + (j, j + 4), j = 0..3, in the order of a key word's pairs.
-    uint32_t qb[4][4];
-    float qs[4];  // sum over the group's channels
+    // qz, qo: B operands of the centers' and the scales' products.  k = 2 c4,
+    // 2 c4 + 1 and 2 c4 + 8 are group c4's Q_g (or -23.5 Q_g) in three bf16
+    // parts, k = 2 c4 + 9 is zero.
+    uint32_t qb[4][4], qz0, qz1, qo0, qo1;
     {
         const uint4 *qrow = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + (row0 + r4) * D);
+        float x = 0.f;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const uint4 v = r4 < cols ? __ldg(qrow + 4 * g + c4) : make_uint4(0, 0, 0, 0);
@@ -158,28 +203,20 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) split_kernel(const DecodeQ4Pa
                       ((lo_f(v.z) + hi_f(v.z)) + (lo_f(v.w) + hi_f(v.w)));
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);
-            qs[g] = s;
+            if (g == c4) x = s;
         }
+        auto parts = [](float v, uint32_t &b0, uint32_t &b1) {
+            const uint32_t h0 = ptx::pack_bf16x2(v, 0.f) & 0xffffu;
+            const float v1 = v - lo_f(h0);
+            const uint32_t h1 = ptx::pack_bf16x2(v1, 0.f) & 0xffffu;
+            b0 = h0 | h1 << 16;
+            b1 = ptx::pack_bf16x2(v1 - lo_f(h1), 0.f) & 0xffffu;
+        };
+        parts(x, qz0, qz1);
+        parts(-23.5f * x, qo0, qo1);
     }
-    // Initial accumulators of the group products, for heads 2 c4 and 2 c4 + 1.
-    float q_init[4][2];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        q_init[g][0] = -23.5f * __shfl_sync(0xffffffffu, qs[g], 8 * c4);
-        q_init[g][1] = -23.5f * __shfl_sync(0xffffffffu, qs[g], 8 * c4 + 4);
-    }
-    // B operand of the key centers' product: k = 2 c4, 2 c4 + 1 and 2 c4 + 8 are
-    // group c4's sum in three parts, k = 2 c4 + 9 is zero.
-    uint32_t qz0, qz1;
-    {
-        const float x = c4 == 0 ? qs[0] : c4 == 1 ? qs[1] : c4 == 2 ? qs[2] : qs[3];
-        const uint32_t h0 = ptx::pack_bf16x2(x, 0.f) & 0xffffu;
-        const float x1 = x - lo_f(h0);
-        const uint32_t h1 = ptx::pack_bf16x2(x1, 0.f) & 0xffffu;
-        const float x2 = x1 - lo_f(h1);
-        qz0 = h0 | h1 << 16;
-        qz1 = ptx::pack_bf16x2(x2, 0.f) & 0xffffu;
-    }
+    // The byte selector that doubles group c4's entry of four bf16.
+    const uint32_t own = 0x1010u + 0x2222u * c4;
 
     const float sl2 = p.scale_log2;
     // Running max (log2 units) and row sum of heads 2 c4, 2 c4 + 1.  acc[2 g + i]:
@@ -188,86 +225,102 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) split_kernel(const DecodeQ4Pa
     float m[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
     float acc[8][4], off[4][4], cen[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    for (int t = 0; t < 8; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
 #pragma unroll
     for (int g = 0; g < 4; ++g) off[g][0] = off[g][1] = off[g][2] = off[g][3] = 0.f;
 
     int slot = 0, i = 0;
     uint32_t parity = 0;
     for (; i < n; ++i) {
-        const int phys = page_of(i);
-        const bool ok = phys >= 0 && phys < p.num_pages;
         if (!wait_bounded(full + slot, parity, wc, kSiteQ4Page)) break;
-        const uint8_t *blk = ring + slot * BLOCK;
-        // The page's words to registers, then the slot goes back at once.
-        const uint4 ka = *reinterpret_cast<const uint4 *>(blk + r4 * 64 + c4 * 16);
-        const uint4 kb = *reinterpret_cast<const uint4 *>(blk + (r4 + 8) * 64 + c4 * 16);
-        const uint8_t *vp = blk + q4::V_CODES + r4 * 128 + c4 * 32;
-        const uint4 va = *reinterpret_cast<const uint4 *>(vp + ((r4 & 1) << 4));
-        const uint4 vb = *reinterpret_cast<const uint4 *>(vp + (((r4 & 1) ^ 1) << 4));
-        const uint2 ksa = *reinterpret_cast<const uint2 *>(blk + q4::K_SCALES + r4 * 8);
-        const uint2 ksb = *reinterpret_cast<const uint2 *>(blk + q4::K_SCALES + (r4 + 8) * 8);
-        const uint32_t kza = *reinterpret_cast<const uint16_t *>(blk + q4::K_CENTERS + r4 * 8 + c4 * 2);
-        const uint32_t kzb = *reinterpret_cast<const uint16_t *>(blk + q4::K_CENTERS + (r4 + 8) * 8 + c4 * 2);
-        uint2 vsa = *reinterpret_cast<const uint2 *>(blk + q4::V_SCALES + r4 * 8);
-        uint2 vsb = *reinterpret_cast<const uint2 *>(blk + q4::V_SCALES + (r4 + 8) * 8);
-        uint32_t vza = *reinterpret_cast<const uint32_t *>(blk + q4::V_CENTERS + (r4 & 3) * 32 + c4 * 4);
-        uint32_t vzb = *reinterpret_cast<const uint32_t *>(blk + q4::V_CENTERS + (r4 & 3) * 32 + c4 * 4 + 16);
+        const uint8_t *blk = ring + slot * STAGE;
+        PageWords w[2];
+        load_page(w[0], blk, r4, c4);
+        load_page(w[1], blk + BLOCK, r4, c4);
+        // The pair is in registers: its slot goes back at once.
         __syncwarp();
         if (i + NST < n) issue(i + NST, slot);
         if (++slot == NST) {
             slot = 0;
             parity ^= 1;
         }
-        if (!ok) continue;  // the page's keys count as absent
-        const int nvalid = L - (page0 + warp + NW * i) * PAGE;  // >= 1
-
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        {
-            const uint32_t a[4] = {kza * 0x10001u, kzb * 0x10001u, kza * 0x10001u, kzb * 0x10001u};
-            ptx::mma_bf16_16816(s, a, qz0, qz1);
-        }
+        float s[2][4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const uint32_t wa = g == 0 ? ka.x : g == 1 ? ka.y : g == 2 ? ka.z : ka.w;
-            const uint32_t wb = g == 0 ? kb.x : g == 1 ? kb.y : g == 2 ? kb.z : kb.w;
-            const float init[4] = {q_init[g][0], q_init[g][1], q_init[g][0], q_init[g][1]};
-            float d[4];
-            const uint32_t a0[4] = {code_pair<0>(wa), code_pair<0>(wb), code_pair<1>(wa), code_pair<1>(wb)};
-            ptx::mma_bf16_16816(d, a0, qb[g][0], qb[g][1], init);
-            const uint32_t a1[4] = {code_pair<2>(wa), code_pair<2>(wb), code_pair<3>(wa), code_pair<3>(wb)};
-            ptx::mma_bf16_16816(d, a1, qb[g][2], qb[g][3]);
-            const float fa = group_f(ksa, g), fb = group_f(ksb, g);
-            s[0] = fmaf(fa, d[0], s[0]);
-            s[1] = fmaf(fa, d[1], s[1]);
-            s[2] = fmaf(fb, d[2], s[2]);
-            s[3] = fmaf(fb, d[3], s[3]);
-        }
-        // s[0], s[1]: token r4, heads 2 c4, 2 c4 + 1; s[2], s[3]: token r4 + 8.
+        for (int u = 0; u < 2; ++u) {
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t za = __byte_perm(w[u].kza.x, w[u].kza.y, own), zb = __byte_perm(w[u].kzb.x, w[u].kzb.y, own);
+            const uint32_t sa = __byte_perm(w[u].ksa.x, w[u].ksa.y, own), sb = __byte_perm(w[u].ksb.x, w[u].ksb.y, own);
+            const uint32_t az[4] = {za, zb, za, zb}, as[4] = {sa, sb, sa, sb};
+            ptx::mma_bf16_16816(s[u], az, qz0, qz1, zero);
+            ptx::mma_bf16_16816(s[u], as, qo0, qo1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] *= sl2;
-        if (nvalid < PAGE) {
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t wa = g == 0 ? w[u].ka.x : g == 1 ? w[u].ka.y : g == 2 ? w[u].ka.z : w[u].ka.w;
+                const uint32_t wb = g == 0 ? w[u].kb.x : g == 1 ? w[u].kb.y : g == 2 ? w[u].kb.z : w[u].kb.w;
+                float d[4];
+                const uint32_t a0[4] = {code_pair<0>(wa), code_pair<0>(wb), code_pair<1>(wa), code_pair<1>(wb)};
+                ptx::mma_bf16_16816(d, a0, qb[g][0], qb[g][1], zero);
+                const uint32_t a1[4] = {code_pair<2>(wa), code_pair<2>(wb), code_pair<3>(wa), code_pair<3>(wb)};
+                ptx::mma_bf16_16816(d, a1, qb[g][2], qb[g][3]);
+                const float fa = group_f(w[u].ksa, g), fb = group_f(w[u].ksb, g);
+                s[u][0] = fmaf(fa, d[0], s[u][0]);
+                s[u][1] = fmaf(fa, d[1], s[u][1]);
+                s[u][2] = fmaf(fb, d[2], s[u][2]);
+                s[u][3] = fmaf(fb, d[3], s[u][3]);
+            }
+        }
+        // s[u][0], s[u][1]: token r4 of page u, heads 2 c4, 2 c4 + 1; [2], [3]:
+        // token r4 + 8.  x: over the running max, in log2 units.
+        float x[2][4];
+        auto over = [&]() {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[u][j] = fmaf(s[u][j], sl2, -m[j & 1]);
+        };
+        over();
+        const bool all = whole >> i & 1;
+        if (!all) {
             // Slots past the end hold arbitrary bits: their scores, and the
             // parameters that would meet a zero probability, are replaced.
-            if (r4 >= nvalid) {
-                s[0] = s[1] = -INFINITY;
-                vsa = make_uint2(0, 0);
-            }
-            if (r4 + 8 >= nvalid) {
-                s[2] = s[3] = -INFINITY;
-                vsb = make_uint2(0, 0);
-            }
-            vza &= (2 * c4 < nvalid ? 0x0000ffffu : 0u) | (2 * c4 + 1 < nvalid ? 0xffff0000u : 0u);
-            vzb &= (2 * c4 + 8 < nvalid ? 0x0000ffffu : 0u) | (2 * c4 + 9 < nvalid ? 0xffff0000u : 0u);
-        }
-        float pm0 = fmaxf(s[0], s[2]), pm1 = fmaxf(s[1], s[3]);
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            pm0 = fmaxf(pm0, __shfl_xor_sync(0xffffffffu, pm0, o));
-            pm1 = fmaxf(pm1, __shfl_xor_sync(0xffffffffu, pm1, o));
+            for (int u = 0; u < 2; ++u) {
+                const int nv = __shfl_sync(0xffffffffu, u ? nv1 : nv0, i);
+                if (r4 >= nv) {
+                    s[u][0] = s[u][1] = 0.f;
+                    x[u][0] = x[u][1] = -INFINITY;
+                    w[u].vsa = make_uint2(0, 0);
+                }
+                if (r4 + 8 >= nv) {
+                    s[u][2] = s[u][3] = 0.f;
+                    x[u][2] = x[u][3] = -INFINITY;
+                    w[u].vsb = make_uint2(0, 0);
+                }
+                w[u].vza &= (2 * c4 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 1 < nv ? 0xffff0000u : 0u);
+                w[u].vzb &= (2 * c4 + 8 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 9 < nv ? 0xffff0000u : 0u);
+            }
         }
-        if (__any_sync(0xffffffffu, pm0 > m[0] || pm1 > m[1])) {
-            const float m0 = fmaxf(m[0], pm0), m1 = fmaxf(m[1], pm1);
+        // The running max follows only when a score is RAISE above it (the first
+        // keys are: the max is -inf): probabilities then stay below 2^RAISE,
+        // which costs the sums nothing, and a raise, with its shuffles and the
+        // rescaling, is rare instead of nearly every page.
+        const float top0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+        const float top1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+        if (__any_sync(0xffffffffu, top0 > RAISE || top1 > RAISE)) {
+            float y0 = -INFINITY, y1 = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                y0 = fmaxf(y0, fmaxf(x[u][0] == -INFINITY ? -INFINITY : s[u][0] * sl2,
+                                     x[u][2] == -INFINITY ? -INFINITY : s[u][2] * sl2));
+                y1 = fmaxf(y1, fmaxf(x[u][1] == -INFINITY ? -INFINITY : s[u][1] * sl2,
+                                     x[u][3] == -INFINITY ? -INFINITY : s[u][3] * sl2));
+            }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, o));
+                y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, o));
+            }
+            const float m0 = fmaxf(m[0], y0), m1 = fmaxf(m[1], y1);
             const float a0 = m[0] == -INFINITY ? (m0 == -INFINITY ? 1.f : 0.f) : ptx::ex2(m[0] - m0);
             const float a1 = m[1] == -INFINITY ? (m1 == -INFINITY ? 1.f : 0.f) : ptx::ex2(m[1] - m1);
             lsum[0] *= a0;
@@ -288,33 +341,39 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) split_kernel(const DecodeQ4Pa
             cen[1] *= a1;
             m[0] = m0;
             m[1] = m1;
-        }
-        const float ms0 = m[0] == -INFINITY ? 0.f : m[0];
-        const float ms1 = m[1] == -INFINITY ? 0.f : m[1];
-        const float p0 = ptx::ex2(s[0] - ms0), p1 = ptx::ex2(s[1] - ms1);
-        const float p2 = ptx::ex2(s[2] - ms0), p3 = ptx::ex2(s[3] - ms1);
-        lsum[0] += p0 + p2;
-        lsum[1] += p1 + p3;
-        {
-            const uint32_t a[4] = {vza, vza, vzb, vzb};
-            ptx::mma_bf16_16816(cen, a, ptx::movmatrix_trans(ptx::pack_bf16x2(p0, p1)),
-                                ptx::movmatrix_trans(ptx::pack_bf16x2(p2, p3)));
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (x[u][j] != -INFINITY) x[u][j] = fmaf(s[u][j], sl2, -m[j & 1]);
         }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const float fa = group_f(vsa, g), fb = group_f(vsb, g);
-            // P'^T as the B operand: tokens 2 c4 (+ 1) and 2 c4 + 8 (+ 9), head r4.
-            const uint32_t b0 = ptx::movmatrix_trans(ptx::pack_bf16x2(p0 * fa, p1 * fa));
-            const uint32_t b1 = ptx::movmatrix_trans(ptx::pack_bf16x2(p2 * fb, p3 * fb));
-            const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
-            const uint32_t wa = __byte_perm(g < 2 ? va.x : va.y, g < 2 ? va.z : va.w, sel);
-            const uint32_t wb = __byte_perm(g < 2 ? vb.x : vb.y, g < 2 ? vb.z : vb.w, sel);
-            const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
-            ptx::mma_bf16_16816(acc[2 * g], a0, b0, b1);
-            const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
-            ptx::mma_bf16_16816(acc[2 * g + 1], a1, b0, b1);
-            const uint32_t a2[4] = {0xC1BCC1BCu, 0xC1BCC1BCu, 0xC1BCC1BCu, 0xC1BCC1BCu};  // -23.5
-            ptx::mma_bf16_16816(off[g], a2, b0, b1);
+        for (int u = 0; u < 2; ++u) {
+            const float p0 = ptx::ex2(x[u][0]), p1 = ptx::ex2(x[u][1]);
+            const float p2 = ptx::ex2(x[u][2]), p3 = ptx::ex2(x[u][3]);
+            lsum[0] += p0 + p2;
+            lsum[1] += p1 + p3;
+            {
+                const uint32_t a[4] = {w[u].vza, w[u].vza, w[u].vzb, w[u].vzb};
+                ptx::mma_bf16_16816(cen, a, ptx::movmatrix_trans(ptx::pack_bf16x2(p0, p1)),
+                                    ptx::movmatrix_trans(ptx::pack_bf16x2(p2, p3)));
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float fa = group_f(w[u].vsa, g), fb = group_f(w[u].vsb, g);
+                // P'^T as the B operand: tokens 2 c4 (+ 1) and 2 c4 + 8 (+ 9), head r4.
+                const uint32_t b0 = ptx::movmatrix_trans(ptx::pack_bf16x2(p0 * fa, p1 * fa));
+                const uint32_t b1 = ptx::movmatrix_trans(ptx::pack_bf16x2(p2 * fb, p3 * fb));
+                const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
+                const uint32_t wa = __byte_perm(g < 2 ? w[u].va.x : w[u].va.y, g < 2 ? w[u].va.z : w[u].va.w, sel);
+                const uint32_t wb = __byte_perm(g < 2 ? w[u].vb.x : w[u].vb.y, g < 2 ? w[u].vb.z : w[u].vb.w, sel);
+                const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
+                ptx::mma_bf16_16816(acc[2 * g], a0, b0, b1);
+                const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
+                ptx::mma_bf16_16816(acc[2 * g + 1], a1, b0, b1);
+                const uint32_t a2[4] = {0xC1BCC1BCu, 0xC1BCC1BCu, 0xC1BCC1BCu, 0xC1BCC1BCu};  // -23.5
+                ptx::mma_bf16_16816(off[g], a2, b0, b1);
+            }
         }
     }
     // Row sums over the tokens of the fragments (row groups r4).
@@ -436,6 +495,7 @@ void decode_q4_split_plan(int B, int Hq, int Hkv, int max_blocks, int *nsplit, i
     const int64_t want = (dq4::TARGET_CTAS + groups - 1) / groups;
     int64_t pps = (max_blocks + want - 1) / want;
     if (pps < 16) pps = 16;
+    pps += pps & 1;  // whole pairs
     if (pps > dq4::MAX_PAGES_PER_SPLIT) pps = dq4::MAX_PAGES_PER_SPLIT;
     *pages_per_split = (int)pps;
     *nsplit = (int)((max_blocks + pps - 1) / pps);
