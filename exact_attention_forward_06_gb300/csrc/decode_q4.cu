@@ -79,27 +79,56 @@ __device__ __forceinline__ float group_f(uint2 s, int g) {
     return g & 1 ? hi_f(u) : lo_f(u);
 }
 
+// d = a b + c (mma m16n8k16, bf16 in, fp32 out), and the transpose of an 8x8
+// matrix: plain functions of their operands, so that the compiler may interleave
+// the two pages' chains.
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{0f00000000, 0f00000000, 0f00000000, 0f00000000};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 // One page's words in registers, as the lane's fragments take them.
-struct PageWords {
-    uint4 ka, kb;    // key codes of tokens r4 and r4 + 8, channels 32 g + 8 c4 ..
-    uint4 va, vb;    // value codes of tokens 2 c4, 2 c4 + 1 and those + 8
-    uint2 ksa, ksb;  // key scales of tokens r4 and r4 + 8, all groups
-    uint2 kza, kzb;  // key centers
-    uint2 vsa, vsb;  // value scales
-    uint32_t vza, vzb;  // value centers of group r4 % 4, tokens 2 c4, 2 c4 + 1 and those + 8
+struct KeyWords {
+    uint4 ka, kb;    // codes of tokens r4 and r4 + 8, channels 32 g + 8 c4 ..
+    uint2 ksa, ksb;  // scales of tokens r4 and r4 + 8, all groups
+    uint2 kza, kzb;  // centers
+};
+struct ValueWords {
+    uint4 va, vb;       // codes of tokens 2 c4, 2 c4 + 1 and those + 8
+    uint2 vsa, vsb;     // scales of tokens r4 and r4 + 8, all groups
+    uint32_t vza, vzb;  // centers of group r4 % 4, tokens 2 c4, 2 c4 + 1 and those + 8
 };
 
-__device__ __forceinline__ void load_page(PageWords &w, const uint8_t *blk, int r4, int c4) {
+__device__ __forceinline__ void load_keys(KeyWords &w, const uint8_t *blk, int r4, int c4) {
     w.ka = *reinterpret_cast<const uint4 *>(blk + r4 * 64 + c4 * 16);
     w.kb = *reinterpret_cast<const uint4 *>(blk + r4 * 64 + c4 * 16 + 512);
-    const uint8_t *v = blk + r4 * 128 + c4 * 32;
-    w.va = *reinterpret_cast<const uint4 *>(v + q4::V_CODES + ((r4 & 1) << 4));
-    w.vb = *reinterpret_cast<const uint4 *>(v + q4::V_CODES + (((r4 & 1) ^ 1) << 4));
     const uint8_t *par = blk + r4 * 8;
     w.ksa = *reinterpret_cast<const uint2 *>(par + q4::K_SCALES);
     w.ksb = *reinterpret_cast<const uint2 *>(par + q4::K_SCALES + 64);
     w.kza = *reinterpret_cast<const uint2 *>(par + q4::K_CENTERS);
     w.kzb = *reinterpret_cast<const uint2 *>(par + q4::K_CENTERS + 64);
+}
+
+__device__ __forceinline__ void load_values(ValueWords &w, const uint8_t *blk, int r4, int c4) {
+    const uint8_t *v = blk + r4 * 128 + c4 * 32;
+    w.va = *reinterpret_cast<const uint4 *>(v + q4::V_CODES + ((r4 & 1) << 4));
+    w.vb = *reinterpret_cast<const uint4 *>(v + q4::V_CODES + (((r4 & 1) ^ 1) << 4));
+    const uint8_t *par = blk + r4 * 8;
     w.vsa = *reinterpret_cast<const uint2 *>(par + q4::V_SCALES);
     w.vsb = *reinterpret_cast<const uint2 *>(par + q4::V_SCALES + 64);
     const uint8_t *z = blk + q4::V_CENTERS + (r4 & 3) * 32 + c4 * 4;
@@ -234,35 +263,26 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) split_kernel(const DecodeQ4Pa
     for (; i < n; ++i) {
         if (!wait_bounded(full + slot, parity, wc, kSiteQ4Page)) break;
         const uint8_t *blk = ring + slot * STAGE;
-        PageWords w[2];
-        load_page(w[0], blk, r4, c4);
-        load_page(w[1], blk + BLOCK, r4, c4);
-        // The pair is in registers: its slot goes back at once.
-        __syncwarp();
-        if (i + NST < n) issue(i + NST, slot);
-        if (++slot == NST) {
-            slot = 0;
-            parity ^= 1;
-        }
         float s[2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint32_t za = __byte_perm(w[u].kza.x, w[u].kza.y, own), zb = __byte_perm(w[u].kzb.x, w[u].kzb.y, own);
-            const uint32_t sa = __byte_perm(w[u].ksa.x, w[u].ksa.y, own), sb = __byte_perm(w[u].ksb.x, w[u].ksb.y, own);
+            KeyWords k;
+            load_keys(k, blk + u * BLOCK, r4, c4);
+            const uint32_t za = __byte_perm(k.kza.x, k.kza.y, own), zb = __byte_perm(k.kzb.x, k.kzb.y, own);
+            const uint32_t sa = __byte_perm(k.ksa.x, k.ksa.y, own), sb = __byte_perm(k.ksb.x, k.ksb.y, own);
             const uint32_t az[4] = {za, zb, za, zb}, as[4] = {sa, sb, sa, sb};
-            ptx::mma_bf16_16816(s[u], az, qz0, qz1, zero);
-            ptx::mma_bf16_16816(s[u], as, qo0, qo1);
+            mma_zero(s[u], az, qz0, qz1);
+            mma(s[u], as, qo0, qo1);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const uint32_t wa = g == 0 ? w[u].ka.x : g == 1 ? w[u].ka.y : g == 2 ? w[u].ka.z : w[u].ka.w;
-                const uint32_t wb = g == 0 ? w[u].kb.x : g == 1 ? w[u].kb.y : g == 2 ? w[u].kb.z : w[u].kb.w;
+                const uint32_t wa = g == 0 ? k.ka.x : g == 1 ? k.ka.y : g == 2 ? k.ka.z : k.ka.w;
+                const uint32_t wb = g == 0 ? k.kb.x : g == 1 ? k.kb.y : g == 2 ? k.kb.z : k.kb.w;
                 float d[4];
                 const uint32_t a0[4] = {code_pair<0>(wa), code_pair<0>(wb), code_pair<1>(wa), code_pair<1>(wb)};
-                ptx::mma_bf16_16816(d, a0, qb[g][0], qb[g][1], zero);
+                mma_zero(d, a0, qb[g][0], qb[g][1]);
                 const uint32_t a1[4] = {code_pair<2>(wa), code_pair<2>(wb), code_pair<3>(wa), code_pair<3>(wb)};
-                ptx::mma_bf16_16816(d, a1, qb[g][2], qb[g][3]);
-                const float fa = group_f(w[u].ksa, g), fb = group_f(w[u].ksb, g);
+                mma(d, a1, qb[g][2], qb[g][3]);
+                const float fa = group_f(k.ksa, g), fb = group_f(k.ksb, g);
                 s[u][0] = fmaf(fa, d[0], s[u][0]);
                 s[u][1] = fmaf(fa, d[1], s[u][1]);
                 s[u][2] = fmaf(fb, d[2], s[u][2]);
@@ -281,23 +301,13 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) split_kernel(const DecodeQ4Pa
         over();
         const bool all = whole >> i & 1;
         if (!all) {
-            // Slots past the end hold arbitrary bits: their scores, and the
-            // parameters that would meet a zero probability, are replaced.
+            // Slots past the end hold arbitrary bits: their scores are replaced
+            // here, the values' parameters below.
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int nv = __shfl_sync(0xffffffffu, u ? nv1 : nv0, i);
-                if (r4 >= nv) {
-                    s[u][0] = s[u][1] = 0.f;
-                    x[u][0] = x[u][1] = -INFINITY;
-                    w[u].vsa = make_uint2(0, 0);
-                }
-                if (r4 + 8 >= nv) {
-                    s[u][2] = s[u][3] = 0.f;
-                    x[u][2] = x[u][3] = -INFINITY;
-                    w[u].vsb = make_uint2(0, 0);
-                }
-                w[u].vza &= (2 * c4 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 1 < nv ? 0xffff0000u : 0u);
-                w[u].vzb &= (2 * c4 + 8 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 9 < nv ? 0xffff0000u : 0u);
+                if (r4 >= nv) x[u][0] = x[u][1] = -INFINITY;
+                if (r4 + 8 >= nv) x[u][2] = x[u][3] = -INFINITY;
             }
         }
         // The running max follows only when a score is RAISE above it (the first
@@ -353,27 +363,45 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) split_kernel(const DecodeQ4Pa
             const float p2 = ptx::ex2(x[u][2]), p3 = ptx::ex2(x[u][3]);
             lsum[0] += p0 + p2;
             lsum[1] += p1 + p3;
+            ValueWords w;
+            load_values(w, blk + u * BLOCK, r4, c4);
+            if (u == 1) {
+                // The pair has been read: its slot goes back.
+                __syncwarp();
+                if (i + NST < n) issue(i + NST, slot);
+            }
+            if (!all) {
+                const int nv = __shfl_sync(0xffffffffu, u ? nv1 : nv0, i);
+                if (r4 >= nv) w.vsa = make_uint2(0, 0);
+                if (r4 + 8 >= nv) w.vsb = make_uint2(0, 0);
+                w.vza &= (2 * c4 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 1 < nv ? 0xffff0000u : 0u);
+                w.vzb &= (2 * c4 + 8 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 9 < nv ? 0xffff0000u : 0u);
+            }
             {
-                const uint32_t a[4] = {w[u].vza, w[u].vza, w[u].vzb, w[u].vzb};
-                ptx::mma_bf16_16816(cen, a, ptx::movmatrix_trans(ptx::pack_bf16x2(p0, p1)),
-                                    ptx::movmatrix_trans(ptx::pack_bf16x2(p2, p3)));
+                const uint32_t a[4] = {w.vza, w.vza, w.vzb, w.vzb};
+                mma(cen, a, transpose8(ptx::pack_bf16x2(p0, p1)),
+                                    transpose8(ptx::pack_bf16x2(p2, p3)));
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const float fa = group_f(w[u].vsa, g), fb = group_f(w[u].vsb, g);
+                const float fa = group_f(w.vsa, g), fb = group_f(w.vsb, g);
                 // P'^T as the B operand: tokens 2 c4 (+ 1) and 2 c4 + 8 (+ 9), head r4.
-                const uint32_t b0 = ptx::movmatrix_trans(ptx::pack_bf16x2(p0 * fa, p1 * fa));
-                const uint32_t b1 = ptx::movmatrix_trans(ptx::pack_bf16x2(p2 * fb, p3 * fb));
+                const uint32_t b0 = transpose8(ptx::pack_bf16x2(p0 * fa, p1 * fa));
+                const uint32_t b1 = transpose8(ptx::pack_bf16x2(p2 * fb, p3 * fb));
                 const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
-                const uint32_t wa = __byte_perm(g < 2 ? w[u].va.x : w[u].va.y, g < 2 ? w[u].va.z : w[u].va.w, sel);
-                const uint32_t wb = __byte_perm(g < 2 ? w[u].vb.x : w[u].vb.y, g < 2 ? w[u].vb.z : w[u].vb.w, sel);
+                const uint32_t wa = __byte_perm(g < 2 ? w.va.x : w.va.y, g < 2 ? w.va.z : w.va.w, sel);
+                const uint32_t wb = __byte_perm(g < 2 ? w.vb.x : w.vb.y, g < 2 ? w.vb.z : w.vb.w, sel);
                 const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
-                ptx::mma_bf16_16816(acc[2 * g], a0, b0, b1);
+                mma(acc[2 * g], a0, b0, b1);
                 const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
-                ptx::mma_bf16_16816(acc[2 * g + 1], a1, b0, b1);
+                mma(acc[2 * g + 1], a1, b0, b1);
                 const uint32_t a2[4] = {0xC1BCC1BCu, 0xC1BCC1BCu, 0xC1BCC1BCu, 0xC1BCC1BCu};  // -23.5
-                ptx::mma_bf16_16816(off[g], a2, b0, b1);
+                mma(off[g], a2, b0, b1);
             }
+        }
+        if (++slot == NST) {
+            slot = 0;
+            parity ^= 1;
         }
     }
     // Row sums over the tokens of the fragments (row groups r4).
