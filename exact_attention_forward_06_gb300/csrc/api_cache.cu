@@ -202,11 +202,10 @@ attn_status_t attn_gather_paged_q4(const void *cache, const int32_t *block_table
 
 size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int d, int max_blocks_per_seq) {
     if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d != 128 || max_blocks_per_seq < 1) return 0;
-    int ns = 1, pps = 1;
-    attn::decode_q4_split_plan(B, Hq, Hkv, max_blocks_per_seq, &ns, &pps);
-    // o_part [rows][nsplit][d] fp32, then lse_part [rows][nsplit] fp32, each 256-B aligned.
-    const size_t parts = (size_t)B * Hq * ns;
-    return align256(parts * d * 4) + align256(parts * 4);
+    if ((int64_t)B * ((max_blocks_per_seq + (int64_t)1) / 2) > 0x7fffffff) return 0;
+    // o_part [CTAs][2][8][d] fp32, lse_part [CTAs][2][8] fp32, cuts [CTAs] of 16 bytes, each 256-B aligned.
+    const size_t ctas = (size_t)attn::decode_q4_max_ctas(B, Hq, Hkv, max_blocks_per_seq);
+    return align256(ctas * 16 * d * 4) + align256(ctas * 16 * 4) + align256(ctas * 16);
 }
 
 attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32_t *block_table,
@@ -216,8 +215,10 @@ attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32
     attn_status_t st = attn::check_decode_args(q, cache, cache, block_table, seqlens, out, lse, B, Hq, Hkv, d,
                                                page_size, num_pages, max_blocks_per_seq, scale);
     if (st != ATTN_OK) return st;
-    // Key positions are 32-bit; rows, and splits of at most 256 pages, are grid axes.
-    if ((int64_t)max_blocks_per_seq > 65535 * 256 || (int64_t)B * Hq > 0x7fffffff) return ATTN_ERR_INVALID_ARG;
+    // Key positions, rows and the sum of all sequences' page pairs are 32-bit.
+    if ((int64_t)max_blocks_per_seq * 16 > 0x7fffffff - 64 || (int64_t)B * Hq > 0x7fffffff ||
+        (int64_t)B * (((int64_t)max_blocks_per_seq + 1) / 2) > 0x7fffffff)
+        return ATTN_ERR_INVALID_ARG;
     const size_t need = attn_decode_q4_workspace_bytes(B, Hq, Hkv, d, max_blocks_per_seq);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
     attn::DecodeQ4Params p = {};
@@ -227,10 +228,11 @@ attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32
     p.seqlens = seqlens;
     p.out = out;
     p.lse = lse;
-    attn::decode_q4_split_plan(B, Hq, Hkv, max_blocks_per_seq, &p.nsplit, &p.pages_per_split);
-    p.o_part = static_cast<float *>(workspace);
-    p.lse_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
-                                           align256((size_t)B * Hq * p.nsplit * d * 4));
+    const size_t ctas = (size_t)attn::decode_q4_max_ctas(B, Hq, Hkv, max_blocks_per_seq);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.o_part = reinterpret_cast<float *>(ws);
+    p.lse_part = reinterpret_cast<float *>(ws + align256(ctas * 16 * d * 4));
+    p.cuts = reinterpret_cast<int4 *>(ws + align256(ctas * 16 * d * 4) + align256(ctas * 16 * 4));
     p.B = B;
     p.Hq = Hq;
     p.Hkv = Hkv;
@@ -239,7 +241,7 @@ attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     int sms;
     if ((st = attn::device_state(&sms, &p.status, &p.budget_ns)) != ATTN_OK) return st;
-    return attn::launch_decode_q4(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return attn::launch_decode_q4(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 size_t attn_fwd_paged_q4_workspace_bytes(int B, int Hkv, int d, int max_total_k) {

@@ -56,9 +56,12 @@ struct DecodeQ4Params {
     const int32_t *block_table, *seqlens;
     void *out;
     float *lse;
-    float *o_part;    // [B * Hq][nsplit][d], nsplit > 1 only
-    float *lse_part;  // [B * Hq][nsplit]
-    int B, Hq, Hkv, num_pages, max_blocks, nsplit, pages_per_split;
+    // Partial results of the shares that cut a sequence, for each CTA its first
+    // and its last segment: normalised outputs and log2-sum-exp2 of 8 heads.
+    float *o_part;    // [CTAs][2][8][d]
+    float *lse_part;  // [CTAs][2][8]
+    int4 *cuts;       // [CTAs]
+    int B, Hq, Hkv, num_pages, max_blocks;
     float scale_log2;
     unsigned *status;
     uint64_t budget_ns;
@@ -71,7 +74,8 @@ cudaError_t launch_gather_q4(const GatherQ4Params &p, cudaStream_t stream);
 // takes the sum past max_total, counts as 0 and is reported.
 cudaError_t launch_q4_offsets(const int32_t *seqlens, int32_t *cu_k, int32_t *lens_out, int B, int max_blocks,
                               int max_total, unsigned *status, cudaStream_t stream);
-void decode_q4_split_plan(int B, int Hq, int Hkv, int max_blocks, int *nsplit, int *pages_per_split);
-cudaError_t launch_decode_q4(const DecodeQ4Params &p, cudaStream_t stream);
+// CTAs at most, a pure function of the shape: the workspace's size goes by it.
+int decode_q4_max_ctas(int B, int Hq, int Hkv, int max_blocks);
+cudaError_t launch_decode_q4(const DecodeQ4Params &p, int sm_count, cudaStream_t stream);
 
 }  // namespace attn

@@ -25,11 +25,20 @@
 //   reads its operands as 16-byte words without bank conflicts, and a value
 //   pair of two tokens is one byte permutation.
 //
-// Each warp streams pages w, w + 4, .. of the CTA's split through a ring of its
-// own (one bulk copy a page, issued by its lane 0 as soon as the page's words
-// are in registers): no producer warp and no barrier between warps until the
-// four partial results meet at the end.  Scores, sums and outputs are fp32; P and
-// P' are rounded to bf16 for the product alone, the row sum adds the fp32 values.
+// The work is cut into equal shares, one for each of three CTAs per SM: the page
+// pairs of all sequences and KV heads in one row, CTA c taking the c-th part of
+// it.  A share is a few segments (a run of one sequence's pages for one KV head);
+// a segment that is a whole sequence is finished by its CTA, the parts of a cut
+// one go to the workspace and are merged by log-sum-exp in the order of the keys.
+// Ragged lengths thus cost nothing: against a grid of fixed splits over the
+// table's width, the same page loop took 177 us instead of SHARED_US on 64
+// sequences of 0 to 16384 tokens.
+//
+// In a segment each warp streams page pairs w, w + 4, .. through a ring of its own
+// (bulk copies issued by its lane 0 as soon as a slot has been read): no producer
+// warp and no barrier between warps until the four partial results meet at the
+// segment's end.  Scores, sums and outputs are fp32; P and P' are rounded to
+// bf16 for the product alone, the row sum adds the fp32 values.
 #include <cstdint>
 #include <type_traits>
 #include <cuda_runtime.h>
@@ -52,15 +61,13 @@ constexpr int NT = NW * 32;
 constexpr int CTAS_PER_SM = 3;
 constexpr int STAGE = 2 * BLOCK;
 constexpr int RING = NW * NST * STAGE;
-constexpr int SMEM = RING + NW * NST * 8 + 16;  // ring, barriers, abort flag
-constexpr int MERGE_ROW = D + 2;
-static_assert(NW * COLS * MERGE_ROW * 4 <= RING, "the merge reuses the ring");
+constexpr int EXCHANGE = 36 * 32 * 4;  // one warp's partial result: 36 words a lane
+constexpr int SMEM = RING + 2 * EXCHANGE + NW * NST * 8 + 64;  // ring, exchange, barriers, small words
 static_assert(CTAS_PER_SM * (SMEM + 1024) <= 233472, "CTAs per SM");
-constexpr int MAX_PAGES_PER_SPLIT = 64 * NW;  // a pair of table entries a lane
+constexpr int MIN_PAIRS = 4;           // pairs a CTA takes at least, unless there is a KV head for each
+constexpr int MAX_CTAS = 3 * 152;      // shares at most: the workspace's size goes by it
 constexpr float RAISE = 8.f;  // a score this far (in log2) above the running max raises it
-constexpr int TARGET_CTAS = 2048;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr float LOG2E = 1.4426950408889634f;
 
 // Codes j and j + 4 of a word as the bf16 pair (16 + n, 16 + n').
 template <int J>
@@ -136,356 +143,508 @@ __device__ __forceinline__ void load_values(ValueWords &w, const uint8_t *blk, i
     w.vzb = *reinterpret_cast<const uint32_t *>(z + 16);
 }
 
-__global__ void __launch_bounds__(NT, CTAS_PER_SM) split_kernel(const DecodeQ4Params p, int col_blocks) {
+// Page pairs of a sequence; 0 for a length outside the table.
+__device__ __forceinline__ int pairs_of(int L, int max_blocks) {
+    return L < 0 || L > max_blocks * PAGE ? 0 : (L + 2 * PAGE - 1) / (2 * PAGE);
+}
+
+// What the merge finds out about a cut run that begins in share c: its first
+// row, its query heads and how many shares it spans (0: none).
+struct CutRun {
+    int row0, cols, parts;
+};
+
+__global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Params p, int col_blocks) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r4 = lane >> 2, c4 = lane & 3;
     uint8_t *ring = smem + warp * NST * STAGE;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING) + warp * NST;
-    volatile int *abort_flag = reinterpret_cast<int *>(smem + RING + NW * NST * 8);
+    float *exchange = reinterpret_cast<float *>(smem + RING) + lane;  // [half][word][lane]
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING + 2 * EXCHANGE) + warp * NST;
+    int *words = reinterpret_cast<int *>(smem + RING + 2 * EXCHANGE + NW * NST * 8);
+    volatile int *abort_flag = words;
+    int64_t *found = reinterpret_cast<int64_t *>(words + 2);  // [0] all pairs, [1] pairs before words[1]'s sequence
+    int *scan = words + 6;                                    // [NW]
 
-    const int G = p.Hq / p.Hkv;
-    const int h = blockIdx.x / col_blocks, col0 = (blockIdx.x - h * col_blocks) * COLS;
+    // CTAs of one share that differ in the column block alone are neighbours, so
+    // that their reads of the same pages meet in L2.
+    const int blk = blockIdx.x % col_blocks, share = blockIdx.x / col_blocks;
+    const int G = p.Hq / p.Hkv, col0 = blk * COLS;
     const int cols = min(COLS, G - col0);
-    const int split = blockIdx.y, b = blockIdx.z;
-    const int64_t row0 = (int64_t)b * p.Hq + h * G + col0;
 
-    const int L_raw = __ldg(p.seqlens + b);
-    const bool bad_len = L_raw < 0 || L_raw > p.max_blocks * PAGE;
-    if (bad_len && threadIdx.x == 0 && split == 0 && blockIdx.x == 0)
-        report_status(p.status, kStatusDeviceBounds, kSiteQ4Seqlen);
-    const int L = bad_len ? 0 : L_raw;
-    const int page0 = split * p.pages_per_split;
-    const int np = min(p.pages_per_split, (L + PAGE - 1) / PAGE - page0);
-    if (np <= 0) {
-        // Nothing here; the merge does not read this split's partial.  With a
-        // single split there is no merge, and the row is empty.
-        if (p.nsplit == 1) {
-            for (int i = threadIdx.x; i < cols * D / 2; i += NT)
-                reinterpret_cast<uint32_t *>(p.out)[row0 * (D / 2) + i] = 0u;
-            if (p.lse && threadIdx.x < cols) p.lse[row0 + threadIdx.x] = -INFINITY;
-        }
-        return;
+    // All pairs, and the sequence in which the share begins: a thread sums a run
+    // of sequences, the sums are scanned.
+    const int per = (p.B + NT - 1) / NT;
+    const int b_lo = min(p.B, (int)threadIdx.x * per), b_hi = min(p.B, b_lo + per);
+    int mine = 0;  // at most 2^31: B * max_blocks / 2 is bounded by the caller
+    for (int b = b_lo; b < b_hi; ++b) mine += pairs_of(__ldg(p.seqlens + b), p.max_blocks);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
     }
-    // This warp's page pairs: pages page0 + 2 (warp + NW i) and the next, i < n.
-    // Lane i holds pair i's pages (-1: none, or a bad entry) and their numbers
-    // of keys.
-    const int npairs = (np + 1) / 2;
-    const int n = warp < npairs ? (npairs - warp + NW - 1) / NW : 0;
-    int tab0 = -1, tab1 = -1, nv0 = 0, nv1 = 0;
-    if (lane < n) {
-        const int first = 2 * (warp + NW * lane);
-        const int32_t *row = p.block_table + (int64_t)b * p.max_blocks + page0 + first;
-        tab0 = __ldg(row);
-        if (first + 1 < np) tab1 = __ldg(row + 1);
-        const bool bad0 = tab0 < 0 || tab0 >= p.num_pages;
-        const bool bad1 = first + 1 < np && (tab1 < 0 || tab1 >= p.num_pages);
-        if (bad0 || bad1) report_status(p.status, kStatusDeviceBounds, kSiteQ4Table);
-        if (bad0) tab0 = -1;
-        if (bad1) tab1 = -1;
-        const int left = L - (page0 + first) * PAGE;
-        nv0 = bad0 ? 0 : min(PAGE, left);
-        nv1 = tab1 < 0 ? 0 : min(PAGE, left - PAGE);
-    }
-    const unsigned whole = __ballot_sync(0xffffffffu, nv0 == PAGE && nv1 == PAGE);
-
+    if (lane == 31) scan[warp] = incl;
     if (lane == 0) {
         for (int s = 0; s < NST; ++s) ptx::mbar_init(full + s, 1);
         if (warp == 0) *abort_flag = 0;
         ptx::fence_mbar_init();
     }
     __syncthreads();
-    const WaitCtx wc{abort_flag, p.status, p.budget_ns};
-
-    const uint64_t pol = ptx::policy_evict_first();
-    const uint8_t *cache = static_cast<const uint8_t *>(p.cache) + (int64_t)h * BLOCK;
-    const int64_t page_step = (int64_t)p.Hkv * BLOCK;
-    auto issue = [&](int i, int slot) {
-        const int t0 = __shfl_sync(0xffffffffu, tab0, i), t1 = __shfl_sync(0xffffffffu, tab1, i);
-        if (lane == 0) {
-            uint8_t *dst = ring + slot * STAGE;
-            ptx::mbar_arrive_expect_tx(full + slot, (t0 >= 0 ? BLOCK : 0) + (t1 >= 0 ? BLOCK : 0));
-            if (t0 >= 0) ptx::bulk_load(dst, cache + t0 * page_step, BLOCK, full + slot, pol);
-            if (t1 >= 0) ptx::bulk_load(dst + BLOCK, cache + t1 * page_step, BLOCK, full + slot, pol);
-        }
-    };
-    const int ahead = min(n, NST);
-    for (int i = 0; i < ahead; ++i) issue(i, i);
-
-    // Q^T as the B operand: head r4 (zero past the CTA's columns), the channels
-    // 32 g + 8 c4 + (j, j + 4), j = 0..3, in the order of a key word's pairs.
-    // qz, qo: B operands of the centers' and the scales' products.  k = 2 c4,
-    // 2 c4 + 1 and 2 c4 + 8 are group c4's Q_g (or -23.5 Q_g) in three bf16
-    // parts, k = 2 c4 + 9 is zero.
-    uint32_t qb[4][4], qz0, qz1, qo0, qo1;
-    {
-        const uint4 *qrow = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + (row0 + r4) * D);
-        float x = 0.f;
+    int64_t before = 0, all = 0;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const uint4 v = r4 < cols ? __ldg(qrow + 4 * g + c4) : make_uint4(0, 0, 0, 0);
-            qb[g][0] = __byte_perm(v.x, v.z, 0x5410);
-            qb[g][1] = __byte_perm(v.x, v.z, 0x7632);
-            qb[g][2] = __byte_perm(v.y, v.w, 0x5410);
-            qb[g][3] = __byte_perm(v.y, v.w, 0x7632);
-            float s = ((lo_f(v.x) + hi_f(v.x)) + (lo_f(v.y) + hi_f(v.y))) +
-                      ((lo_f(v.z) + hi_f(v.z)) + (lo_f(v.w) + hi_f(v.w)));
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            if (g == c4) x = s;
-        }
-        auto parts = [](float v, uint32_t &b0, uint32_t &b1) {
-            const uint32_t h0 = ptx::pack_bf16x2(v, 0.f) & 0xffffu;
-            const float v1 = v - lo_f(h0);
-            const uint32_t h1 = ptx::pack_bf16x2(v1, 0.f) & 0xffffu;
-            b0 = h0 | h1 << 16;
-            b1 = ptx::pack_bf16x2(v1 - lo_f(h1), 0.f) & 0xffffu;
-        };
-        parts(x, qz0, qz1);
-        parts(-23.5f * x, qo0, qo1);
+    for (int w = 0; w < NW; ++w) {
+        if (w < warp) before += scan[w];
+        all += scan[w];
     }
-    // The byte selector that doubles group c4's entry of four bf16.
-    const uint32_t own = 0x1010u + 0x2222u * c4;
-
-    const float sl2 = p.scale_log2;
-    // Running max (log2 units) and row sum of heads 2 c4, 2 c4 + 1.  acc[2 g + i]:
-    // channels 32 g + 4 r4 + 2 i (+ 1) times those heads; off[g]: the group's
-    // offset (the same in every row); cen: the centers' term of group r4 % 4.
-    float m[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
-    float acc[8][4], off[4][4], cen[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int t = 0; t < 8; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) off[g][0] = off[g][1] = off[g][2] = off[g][3] = 0.f;
-
-    int slot = 0, i = 0;
-    uint32_t parity = 0;
-    for (; i < n; ++i) {
-        if (!wait_bounded(full + slot, parity, wc, kSiteQ4Page)) break;
-        const uint8_t *blk = ring + slot * STAGE;
-        float s[2][4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            KeyWords k;
-            load_keys(k, blk + u * BLOCK, r4, c4);
-            const uint32_t za = __byte_perm(k.kza.x, k.kza.y, own), zb = __byte_perm(k.kzb.x, k.kzb.y, own);
-            const uint32_t sa = __byte_perm(k.ksa.x, k.ksa.y, own), sb = __byte_perm(k.ksb.x, k.ksb.y, own);
-            const uint32_t az[4] = {za, zb, za, zb}, as[4] = {sa, sb, sa, sb};
-            mma_zero(s[u], az, qz0, qz1);
-            mma(s[u], as, qo0, qo1);
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const uint32_t wa = g == 0 ? k.ka.x : g == 1 ? k.ka.y : g == 2 ? k.ka.z : k.ka.w;
-                const uint32_t wb = g == 0 ? k.kb.x : g == 1 ? k.kb.y : g == 2 ? k.kb.z : k.kb.w;
-                float d[4];
-                const uint32_t a0[4] = {code_pair<0>(wa), code_pair<0>(wb), code_pair<1>(wa), code_pair<1>(wb)};
-                mma_zero(d, a0, qb[g][0], qb[g][1]);
-                const uint32_t a1[4] = {code_pair<2>(wa), code_pair<2>(wb), code_pair<3>(wa), code_pair<3>(wb)};
-                mma(d, a1, qb[g][2], qb[g][3]);
-                const float fa = group_f(k.ksa, g), fb = group_f(k.ksb, g);
-                s[u][0] = fmaf(fa, d[0], s[u][0]);
-                s[u][1] = fmaf(fa, d[1], s[u][1]);
-                s[u][2] = fmaf(fb, d[2], s[u][2]);
-                s[u][3] = fmaf(fb, d[3], s[u][3]);
-            }
+    before += incl - mine;  // pairs before this thread's run
+    const int64_t total = all * p.Hkv;
+    // No more shares than there is work for, and none without a pair.
+    const int64_t items = (int64_t)p.B * p.Hkv, fill = (total + MIN_PAIRS - 1) / MIN_PAIRS;
+    const int64_t shares = min(min((int64_t)(gridDim.x / col_blocks), total), max(items, fill));
+    const int64_t u0 = share < shares ? total * share / shares : total;
+    const int64_t u1 = share < shares ? total * (share + 1) / shares : total;
+    if (u0 < u1 && u0 >= before * p.Hkv && u0 < (before + mine) * p.Hkv) {
+        int b = b_lo;
+        int64_t pre = before;
+        for (;; ++b) {
+            const int np = pairs_of(__ldg(p.seqlens + b), p.max_blocks);
+            if (u0 < (pre + np) * p.Hkv) break;
+            pre += np;
         }
-        // s[u][0], s[u][1]: token r4 of page u, heads 2 c4, 2 c4 + 1; [2], [3]:
-        // token r4 + 8.  x: over the running max, in log2 units.
-        float x[2][4];
-        auto over = [&]() {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[u][j] = fmaf(s[u][j], sl2, -m[j & 1]);
-        };
-        over();
-        const bool all = whole >> i & 1;
-        if (!all) {
-            // Slots past the end hold arbitrary bits: their scores are replaced
-            // here, the values' parameters below.
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int nv = __shfl_sync(0xffffffffu, u ? nv1 : nv0, i);
-                if (r4 >= nv) x[u][0] = x[u][1] = -INFINITY;
-                if (r4 + 8 >= nv) x[u][2] = x[u][3] = -INFINITY;
-            }
-        }
-        // The running max follows only when a score is RAISE above it (the first
-        // keys are: the max is -inf): probabilities then stay below 2^RAISE,
-        // which costs the sums nothing, and a raise, with its shuffles and the
-        // rescaling, is rare instead of nearly every page.
-        const float top0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-        const float top1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-        if (__any_sync(0xffffffffu, top0 > RAISE || top1 > RAISE)) {
-            float y0 = -INFINITY, y1 = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                y0 = fmaxf(y0, fmaxf(x[u][0] == -INFINITY ? -INFINITY : s[u][0] * sl2,
-                                     x[u][2] == -INFINITY ? -INFINITY : s[u][2] * sl2));
-                y1 = fmaxf(y1, fmaxf(x[u][1] == -INFINITY ? -INFINITY : s[u][1] * sl2,
-                                     x[u][3] == -INFINITY ? -INFINITY : s[u][3] * sl2));
-            }
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, o));
-                y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, o));
-            }
-            const float m0 = fmaxf(m[0], y0), m1 = fmaxf(m[1], y1);
-            const float a0 = m[0] == -INFINITY ? (m0 == -INFINITY ? 1.f : 0.f) : ptx::ex2(m[0] - m0);
-            const float a1 = m[1] == -INFINITY ? (m1 == -INFINITY ? 1.f : 0.f) : ptx::ex2(m[1] - m1);
-            lsum[0] *= a0;
-            lsum[1] *= a1;
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                acc[t][0] *= a0;
-                acc[t][1] *= a1;
-                acc[t][2] *= a0;
-                acc[t][3] *= a1;
-            }
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                off[g][0] *= a0;
-                off[g][1] *= a1;
-            }
-            cen[0] *= a0;
-            cen[1] *= a1;
-            m[0] = m0;
-            m[1] = m1;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (x[u][j] != -INFINITY) x[u][j] = fmaf(s[u][j], sl2, -m[j & 1]);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const float p0 = ptx::ex2(x[u][0]), p1 = ptx::ex2(x[u][1]);
-            const float p2 = ptx::ex2(x[u][2]), p3 = ptx::ex2(x[u][3]);
-            lsum[0] += p0 + p2;
-            lsum[1] += p1 + p3;
-            ValueWords w;
-            load_values(w, blk + u * BLOCK, r4, c4);
-            if (u == 1) {
-                // The pair has been read: its slot goes back.
-                __syncwarp();
-                if (i + NST < n) issue(i + NST, slot);
-            }
-            if (!all) {
-                const int nv = __shfl_sync(0xffffffffu, u ? nv1 : nv0, i);
-                if (r4 >= nv) w.vsa = make_uint2(0, 0);
-                if (r4 + 8 >= nv) w.vsb = make_uint2(0, 0);
-                w.vza &= (2 * c4 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 1 < nv ? 0xffff0000u : 0u);
-                w.vzb &= (2 * c4 + 8 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 9 < nv ? 0xffff0000u : 0u);
-            }
-            {
-                const uint32_t a[4] = {w.vza, w.vza, w.vzb, w.vzb};
-                mma(cen, a, transpose8(ptx::pack_bf16x2(p0, p1)),
-                                    transpose8(ptx::pack_bf16x2(p2, p3)));
-            }
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float fa = group_f(w.vsa, g), fb = group_f(w.vsb, g);
-                // P'^T as the B operand: tokens 2 c4 (+ 1) and 2 c4 + 8 (+ 9), head r4.
-                const uint32_t b0 = transpose8(ptx::pack_bf16x2(p0 * fa, p1 * fa));
-                const uint32_t b1 = transpose8(ptx::pack_bf16x2(p2 * fb, p3 * fb));
-                const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
-                const uint32_t wa = __byte_perm(g < 2 ? w.va.x : w.va.y, g < 2 ? w.va.z : w.va.w, sel);
-                const uint32_t wb = __byte_perm(g < 2 ? w.vb.x : w.vb.y, g < 2 ? w.vb.z : w.vb.w, sel);
-                const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
-                mma(acc[2 * g], a0, b0, b1);
-                const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
-                mma(acc[2 * g + 1], a1, b0, b1);
-                const uint32_t a2[4] = {0xC1BCC1BCu, 0xC1BCC1BCu, 0xC1BCC1BCu, 0xC1BCC1BCu};  // -23.5
-                mma(off[g], a2, b0, b1);
-            }
-        }
-        if (++slot == NST) {
-            slot = 0;
-            parity ^= 1;
-        }
+        words[1] = b;
+        found[1] = pre;
     }
-    // Row sums over the tokens of the fragments (row groups r4).
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-        lsum[0] += __shfl_xor_sync(0xffffffffu, lsum[0], o);
-        lsum[1] += __shfl_xor_sync(0xffffffffu, lsum[1], o);
-    }
-    // After a wait that gave up: let this warp's copies in flight land first.
-    for (int j = i; j < min(n, i + NST); ++j) drain_wait(full + j % NST, (j / NST) & 1, wc);
-    __syncthreads();  // every warp has read its pages: the ring becomes the merge's scratch
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (*abort_flag) return;
-    float *merge = reinterpret_cast<float *>(smem);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int hc = 2 * c4 + j;
-        float *dst = merge + (warp * COLS + hc) * MERGE_ROW;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const float add = off[g][j] + __shfl_sync(0xffffffffu, cen[j], 4 * g + c4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dst[32 * g + 4 * r4 + i] = acc[2 * g + i / 2][2 * (i & 1) + j] + add;
-        }
-        if (r4 == 0) {
-            dst[D] = m[j];
-            dst[D + 1] = lsum[j];
+    // Empty sequences (and lengths outside the table, which are reported) belong
+    // to no share: their rows are written here.
+    if (blk == 0) {
+        for (int b = share; b < p.B; b += gridDim.x / col_blocks) {
+            const int L = __ldg(p.seqlens + b);
+            if (pairs_of(L, p.max_blocks) > 0) continue;
+            if (L != 0 && threadIdx.x == 0) report_status(p.status, kStatusDeviceBounds, kSiteQ4Seqlen);
+            for (int i = threadIdx.x; i < p.Hq * (D / 8); i += NT)
+                reinterpret_cast<uint4 *>(p.out)[(int64_t)b * p.Hq * (D / 8) + i] = make_uint4(0, 0, 0, 0);
+            if (p.lse)
+                for (int i = threadIdx.x; i < p.Hq; i += NT) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
         }
     }
     __syncthreads();
-    // Merge the page streams: thread = channel, loop over heads.
-    const int e = threadIdx.x;
-    for (int c = 0; c < cols; ++c) {
-        float M = -INFINITY;
+    CutRun cut = {0, 0, 0};
+    const WaitCtx wc{abort_flag, p.status, p.budget_ns};
+    const uint64_t pol = col_blocks == 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
+    const int64_t page_step = (int64_t)p.Hkv * BLOCK;
+    // The byte selector that doubles group c4's entry of four bf16.
+    const uint32_t own = 0x1010u + 0x2222u * c4;
+    const float sl2 = p.scale_log2;
+    int slot = 0;
+    uint32_t parity = 0;
+
+    int b = 0, h = 0, L = 0, seq_pairs = 0, first = 0;  // the segment: sequence, KV head, first pair
+    if (u0 < u1) {
+        b = words[1];
+        L = __ldg(p.seqlens + b);
+        seq_pairs = pairs_of(L, p.max_blocks);
+        const int64_t rem = u0 - found[1] * p.Hkv;
+        h = (int)(rem / seq_pairs);
+        first = (int)(rem - (int64_t)h * seq_pairs);
+    }
+    for (int64_t u = u0; u < u1;) {
+        const int count = (int)min((int64_t)(seq_pairs - first), u1 - u);  // this segment's pairs
+        const int64_t row0 = (int64_t)b * p.Hq + h * G + col0;
+        const uint8_t *cache = static_cast<const uint8_t *>(p.cache) + (int64_t)h * BLOCK;
+        const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
+        const int last_page = (L + PAGE - 1) / PAGE;
+        const int n = warp < count ? (count - warp + NW - 1) / NW : 0;  // this warp's: first + warp + NW i
+
+        // A batch of up to 32 pairs: lane j holds pair base + j's pages (-1: none,
+        // or a bad entry) and their numbers of keys.
+        int tab0, tab1, nv0, nv1;
+        unsigned whole;
+        auto load_table = [&](int base) {
+            tab0 = tab1 = -1;
+            nv0 = nv1 = 0;
+            if (base + lane < n) {
+                const int page = 2 * (first + warp + NW * (base + lane));
+                tab0 = __ldg(table + page);
+                const bool two = page + 1 < last_page;
+                if (two) tab1 = __ldg(table + page + 1);
+                const bool bad0 = tab0 < 0 || tab0 >= p.num_pages;
+                const bool bad1 = two && (tab1 < 0 || tab1 >= p.num_pages);
+                if (bad0 || bad1) report_status(p.status, kStatusDeviceBounds, kSiteQ4Table);
+                if (bad0) tab0 = -1;
+                if (bad1) tab1 = -1;
+                const int left = L - page * PAGE;
+                nv0 = bad0 ? 0 : min(PAGE, left);
+                nv1 = tab1 < 0 ? 0 : min(PAGE, left - PAGE);
+            }
+            whole = __ballot_sync(0xffffffffu, nv0 == PAGE && nv1 == PAGE);
+        };
+        auto issue = [&](int i, int to) {  // pair i of the batch
+            const int t0 = __shfl_sync(0xffffffffu, tab0, i), t1 = __shfl_sync(0xffffffffu, tab1, i);
+            if (lane == 0) {
+                uint8_t *dst = ring + to * STAGE;
+                ptx::mbar_arrive_expect_tx(full + to, (t0 >= 0 ? BLOCK : 0) + (t1 >= 0 ? BLOCK : 0));
+                if (t0 >= 0) ptx::bulk_load(dst, cache + t0 * page_step, BLOCK, full + to, pol);
+                if (t1 >= 0) ptx::bulk_load(dst + BLOCK, cache + t1 * page_step, BLOCK, full + to, pol);
+            }
+        };
+        auto issue_first = [&](int m) {  // the batch's first pairs, all slots being free
+            int to = slot;
+            for (int i = 0; i < min(m, NST); ++i) {
+                issue(i, to);
+                to = to + 1 == NST ? 0 : to + 1;
+            }
+        };
+        load_table(0);
+        issue_first(min(n, 32));
+
+        // Q^T as the B operand: head r4 (zero past the CTA's columns), the channels
+        // 32 g + 8 c4 + (j, j + 4), j = 0..3, in the order of a key word's pairs.
+        // qz, qo: B operands of the centers' and the scales' products.  k = 2 c4,
+        // 2 c4 + 1 and 2 c4 + 8 are group c4's Q_g (or -23.5 Q_g) in three bf16
+        // parts, k = 2 c4 + 9 is zero.
+        uint32_t qb[4][4], qz0, qz1, qo0, qo1;
+        {
+            const uint4 *qrow = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + (row0 + r4) * D);
+            float x = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, merge[(w * COLS + c) * MERGE_ROW + D]);
-        float Ls = 0.f, o = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float *src = merge + (w * COLS + c) * MERGE_ROW;
-            // A stream without a finite score has only zeros, or NaN, to add.
-            const float f = src[D] == -INFINITY ? 1.f : ptx::ex2(src[D] - M);
-            Ls += src[D + 1] * f;
-            o += src[e] * f;
+            for (int g = 0; g < 4; ++g) {
+                const uint4 v = r4 < cols ? __ldg(qrow + 4 * g + c4) : make_uint4(0, 0, 0, 0);
+                qb[g][0] = __byte_perm(v.x, v.z, 0x5410);
+                qb[g][1] = __byte_perm(v.x, v.z, 0x7632);
+                qb[g][2] = __byte_perm(v.y, v.w, 0x5410);
+                qb[g][3] = __byte_perm(v.y, v.w, 0x7632);
+                float s = ((lo_f(v.x) + hi_f(v.x)) + (lo_f(v.y) + hi_f(v.y))) +
+                          ((lo_f(v.z) + hi_f(v.z)) + (lo_f(v.w) + hi_f(v.w)));
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                if (g == c4) x = s;
+            }
+            auto parts = [](float v, uint32_t &b0, uint32_t &b1) {
+                const uint32_t h0 = ptx::pack_bf16x2(v, 0.f) & 0xffffu;
+                const float v1 = v - lo_f(h0);
+                const uint32_t h1 = ptx::pack_bf16x2(v1, 0.f) & 0xffffu;
+                b0 = h0 | h1 << 16;
+                b1 = ptx::pack_bf16x2(v1 - lo_f(h1), 0.f) & 0xffffu;
+            };
+            parts(x, qz0, qz1);
+            parts(-23.5f * x, qo0, qo1);
         }
-        const bool any = Ls != 0.f;  // NaN included
-        o = any ? o / Ls : 0.f;
-        const float lse = any ? (M + ptx::lg2(Ls)) * LN2 : -INFINITY;
-        const int64_t r = row0 + c;
-        if (p.nsplit == 1) {
-            static_cast<uint16_t *>(p.out)[r * D + e] = (uint16_t)(ptx::pack_bf16x2(o, 0.f) & 0xffffu);
-            if (p.lse && e == 0) p.lse[r] = lse;
-        } else {
-            p.o_part[(r * p.nsplit + split) * D + e] = o;
-            if (e == 0) p.lse_part[r * p.nsplit + split] = lse;
+
+        // Running max (log2 units) and row sum of heads 2 c4, 2 c4 + 1.  acc[2 g + i]:
+        // channels 32 g + 4 r4 + 2 i (+ 1) times those heads; off[g]: the group's
+        // offset (the same in every row); cen: the centers' term of group r4 % 4.
+        float m[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
+        float acc[8][4], off[4][4], cen[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < 8; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) off[g][0] = off[g][1] = off[g][2] = off[g][3] = 0.f;
+
+        int base = 0, left = n;
+        while (left > 0) {
+            const int batch = min(left, 32);
+            int i = 0;
+            for (; i < batch; ++i) {
+                if (!wait_bounded(full + slot, parity, wc, kSiteQ4Page)) break;
+                const uint8_t *blk = ring + slot * STAGE;
+                float s[2][4];
+        #pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    KeyWords k;
+                    load_keys(k, blk + u * BLOCK, r4, c4);
+                    const uint32_t za = __byte_perm(k.kza.x, k.kza.y, own), zb = __byte_perm(k.kzb.x, k.kzb.y, own);
+                    const uint32_t sa = __byte_perm(k.ksa.x, k.ksa.y, own), sb = __byte_perm(k.ksb.x, k.ksb.y, own);
+                    const uint32_t az[4] = {za, zb, za, zb}, as[4] = {sa, sb, sa, sb};
+                    mma_zero(s[u], az, qz0, qz1);
+                    mma(s[u], as, qo0, qo1);
+        #pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint32_t wa = g == 0 ? k.ka.x : g == 1 ? k.ka.y : g == 2 ? k.ka.z : k.ka.w;
+                        const uint32_t wb = g == 0 ? k.kb.x : g == 1 ? k.kb.y : g == 2 ? k.kb.z : k.kb.w;
+                        float d[4];
+                        const uint32_t a0[4] = {code_pair<0>(wa), code_pair<0>(wb), code_pair<1>(wa), code_pair<1>(wb)};
+                        mma_zero(d, a0, qb[g][0], qb[g][1]);
+                        const uint32_t a1[4] = {code_pair<2>(wa), code_pair<2>(wb), code_pair<3>(wa), code_pair<3>(wb)};
+                        mma(d, a1, qb[g][2], qb[g][3]);
+                        const float fa = group_f(k.ksa, g), fb = group_f(k.ksb, g);
+                        s[u][0] = fmaf(fa, d[0], s[u][0]);
+                        s[u][1] = fmaf(fa, d[1], s[u][1]);
+                        s[u][2] = fmaf(fb, d[2], s[u][2]);
+                        s[u][3] = fmaf(fb, d[3], s[u][3]);
+                    }
+                }
+                // s[u][0], s[u][1]: token r4 of page u, heads 2 c4, 2 c4 + 1; [2], [3]:
+                // token r4 + 8.  x: over the running max, in log2 units.
+                float x[2][4];
+                auto over = [&]() {
+        #pragma unroll
+                    for (int u = 0; u < 2; ++u)
+        #pragma unroll
+                        for (int j = 0; j < 4; ++j) x[u][j] = fmaf(s[u][j], sl2, -m[j & 1]);
+                };
+                over();
+                const bool all = whole >> i & 1;
+                if (!all) {
+                    // Slots past the end hold arbitrary bits: their scores are replaced
+                    // here, the values' parameters below.
+        #pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int nv = __shfl_sync(0xffffffffu, u ? nv1 : nv0, i);
+                        if (r4 >= nv) x[u][0] = x[u][1] = -INFINITY;
+                        if (r4 + 8 >= nv) x[u][2] = x[u][3] = -INFINITY;
+                    }
+                }
+                // The running max follows only when a score is RAISE above it (the first
+                // keys are: the max is -inf): probabilities then stay below 2^RAISE,
+                // which costs the sums nothing, and a raise, with its shuffles and the
+                // rescaling, is rare instead of nearly every page.
+                const float top0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+                const float top1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+                if (__any_sync(0xffffffffu, top0 > RAISE || top1 > RAISE)) {
+                    float y0 = -INFINITY, y1 = -INFINITY;
+        #pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        y0 = fmaxf(y0, fmaxf(x[u][0] == -INFINITY ? -INFINITY : s[u][0] * sl2,
+                                             x[u][2] == -INFINITY ? -INFINITY : s[u][2] * sl2));
+                        y1 = fmaxf(y1, fmaxf(x[u][1] == -INFINITY ? -INFINITY : s[u][1] * sl2,
+                                             x[u][3] == -INFINITY ? -INFINITY : s[u][3] * sl2));
+                    }
+        #pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) {
+                        y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, o));
+                        y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, o));
+                    }
+                    const float m0 = fmaxf(m[0], y0), m1 = fmaxf(m[1], y1);
+                    const float a0 = m[0] == -INFINITY ? (m0 == -INFINITY ? 1.f : 0.f) : ptx::ex2(m[0] - m0);
+                    const float a1 = m[1] == -INFINITY ? (m1 == -INFINITY ? 1.f : 0.f) : ptx::ex2(m[1] - m1);
+                    lsum[0] *= a0;
+                    lsum[1] *= a1;
+        #pragma unroll
+                    for (int t = 0; t < 8; ++t) {
+                        acc[t][0] *= a0;
+                        acc[t][1] *= a1;
+                        acc[t][2] *= a0;
+                        acc[t][3] *= a1;
+                    }
+        #pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        off[g][0] *= a0;
+                        off[g][1] *= a1;
+                    }
+                    cen[0] *= a0;
+                    cen[1] *= a1;
+                    m[0] = m0;
+                    m[1] = m1;
+        #pragma unroll
+                    for (int u = 0; u < 2; ++u)
+        #pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (x[u][j] != -INFINITY) x[u][j] = fmaf(s[u][j], sl2, -m[j & 1]);
+                }
+        #pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float p0 = ptx::ex2(x[u][0]), p1 = ptx::ex2(x[u][1]);
+                    const float p2 = ptx::ex2(x[u][2]), p3 = ptx::ex2(x[u][3]);
+                    lsum[0] += p0 + p2;
+                    lsum[1] += p1 + p3;
+                    ValueWords w;
+                    load_values(w, blk + u * BLOCK, r4, c4);
+                    if (u == 1) {
+                        // The pair has been read: its slot goes back.
+                        __syncwarp();
+                        if (i + NST < batch) issue(i + NST, slot);
+                    }
+                    if (!all) {
+                        const int nv = __shfl_sync(0xffffffffu, u ? nv1 : nv0, i);
+                        if (r4 >= nv) w.vsa = make_uint2(0, 0);
+                        if (r4 + 8 >= nv) w.vsb = make_uint2(0, 0);
+                        w.vza &= (2 * c4 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 1 < nv ? 0xffff0000u : 0u);
+                        w.vzb &= (2 * c4 + 8 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 9 < nv ? 0xffff0000u : 0u);
+                    }
+                    {
+                        const uint32_t a[4] = {w.vza, w.vza, w.vzb, w.vzb};
+                        mma(cen, a, transpose8(ptx::pack_bf16x2(p0, p1)),
+                                            transpose8(ptx::pack_bf16x2(p2, p3)));
+                    }
+        #pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float fa = group_f(w.vsa, g), fb = group_f(w.vsb, g);
+                        // P'^T as the B operand: tokens 2 c4 (+ 1) and 2 c4 + 8 (+ 9), head r4.
+                        const uint32_t b0 = transpose8(ptx::pack_bf16x2(p0 * fa, p1 * fa));
+                        const uint32_t b1 = transpose8(ptx::pack_bf16x2(p2 * fb, p3 * fb));
+                        const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
+                        const uint32_t wa = __byte_perm(g < 2 ? w.va.x : w.va.y, g < 2 ? w.va.z : w.va.w, sel);
+                        const uint32_t wb = __byte_perm(g < 2 ? w.vb.x : w.vb.y, g < 2 ? w.vb.z : w.vb.w, sel);
+                        const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
+                        mma(acc[2 * g], a0, b0, b1);
+                        const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
+                        mma(acc[2 * g + 1], a1, b0, b1);
+                        const uint32_t a2[4] = {0xC1BCC1BCu, 0xC1BCC1BCu, 0xC1BCC1BCu, 0xC1BCC1BCu};  // -23.5
+                        mma(off[g], a2, b0, b1);
+                    }
+                }
+                if (++slot == NST) {
+                    slot = 0;
+                    parity ^= 1;
+                }
+            }
+            if (i < batch) {
+                // A wait gave up: let this warp's copies in flight land first.
+                for (int j = i; j < min(batch, i + NST); ++j) {
+                    drain_wait(full + slot, parity, wc);
+                    if (++slot == NST) {
+                        slot = 0;
+                        parity ^= 1;
+                    }
+                }
+                break;
+            }
+            left -= batch;
+            base += batch;
+            if (left > 0) {
+                load_table(base);
+                issue_first(min(left, 32));
+            }
+        }
+        // The offsets' and centers' terms, and the row sums over the tokens of the
+        // fragments (row groups r4).
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float add = off[g][j] + __shfl_sync(0xffffffffu, cen[j], 4 * g + c4);
+                acc[2 * g][j] += add;
+                acc[2 * g][2 + j] += add;
+                acc[2 * g + 1][j] += add;
+                acc[2 * g + 1][2 + j] += add;
+            }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) lsum[j] += __shfl_xor_sync(0xffffffffu, lsum[j], o);
+        }
+        // The four warps' results meet in two rounds: 2 and 3 into 0 and 1, then 1
+        // into 0, a lane's words with the same lane's.
+        auto give = [&](int half) {
+            float *x = exchange + half * (EXCHANGE / 4);
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[(4 * t + k) * 32] = acc[t][k];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                x[(32 + j) * 32] = m[j];
+                x[(34 + j) * 32] = lsum[j];
+            }
+        };
+        auto take = [&](int half) {
+            const float *x = exchange + half * (EXCHANGE / 4);
+            float fa[2], fb[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float mo = x[(32 + j) * 32], mx = fmaxf(m[j], mo);
+                // A side without a finite score has only zeros, or NaN, to add.
+                fa[j] = m[j] == -INFINITY ? 1.f : ptx::ex2(m[j] - mx);
+                fb[j] = mo == -INFINITY ? 1.f : ptx::ex2(mo - mx);
+                lsum[j] = lsum[j] * fa[j] + x[(34 + j) * 32] * fb[j];
+                m[j] = mx;
+            }
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[t][k] = acc[t][k] * fa[k & 1] + x[(4 * t + k) * 32] * fb[k & 1];
+        };
+        __syncthreads();  // the exchange of the segment before has been read
+        if (warp >= 2) give(warp - 2);
+        __syncthreads();
+        if (*abort_flag) {  // a wait gave up: nothing more is written, or merged from here
+            if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+            return;
+        }
+        if (warp < 2) take(warp);
+        if (warp == 1) {
+            __syncwarp();
+            give(1);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            take(1);
+            const bool done = count == seq_pairs;  // the whole sequence: no merge
+            const int64_t part = ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * COLS;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = 2 * c4 + j;
+                if (c >= cols) continue;
+                const bool any = lsum[j] != 0.f;  // NaN included
+                const float inv = any ? 1.f / lsum[j] : 0.f;
+                const float l2 = any ? m[j] + ptx::lg2(lsum[j]) : -INFINITY;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float o0 = any ? acc[2 * g][j] * inv : 0.f, o1 = any ? acc[2 * g][2 + j] * inv : 0.f;
+                    const float o2 = any ? acc[2 * g + 1][j] * inv : 0.f;
+                    const float o3 = any ? acc[2 * g + 1][2 + j] * inv : 0.f;
+                    if (done)
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + (row0 + c) * D + 32 * g + 4 * r4) =
+                            make_uint2(ptx::pack_bf16x2(o0, o1), ptx::pack_bf16x2(o2, o3));
+                    else
+                        *reinterpret_cast<float4 *>(p.o_part + (part + c) * D + 32 * g + 4 * r4) =
+                            make_float4(o0, o1, o2, o3);
+                }
+                if (r4 == 0) {
+                    if (!done) p.lse_part[part + c] = l2;
+                    else if (p.lse) p.lse[row0 + c] = l2 * LN2;
+                }
+            }
+        }
+        if (first == 0 && count < seq_pairs) {
+            // The sequence goes on in the next shares, up to the one that holds
+            // its last pair, unit u + seq_pairs - 1.
+            const int64_t last = ((u + seq_pairs) * shares + total - 1) / total - 1;
+            cut.row0 = (int)row0;
+            cut.cols = cols;
+            cut.parts = (int)(last - share) + 1;
+        }
+        u += count;
+        first = 0;
+        if (++h == p.Hkv && u < u1) {
+            h = 0;
+            do {
+                L = __ldg(p.seqlens + ++b);
+                seq_pairs = pairs_of(L, p.max_blocks);
+            } while (seq_pairs == 0);
         }
     }
+    if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(cut.row0, cut.cols, cut.parts, 0);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Merge of the splits that hold keys: one CTA per row, a warp takes every
-// MERGE_WARPS-th split, four channels a lane; the order is fixed.
+// Merge of the cut runs: CTA (c, i) does head i of the run that begins in share
+// c, if one does.  Warp w takes every MERGE_WARPS-th part, four channels a lane;
+// the order is fixed.
 constexpr int MERGE_WARPS = 8;
-__global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const DecodeQ4Params p) {
+__global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const DecodeQ4Params p, int col_blocks) {
     __shared__ float part[MERGE_WARPS][D];
     __shared__ float part_m[MERGE_WARPS], part_l[MERGE_WARPS];
-    const int64_t r = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int L = __ldg(p.seqlens + r / p.Hq);
-    const int pages = L < 0 || L > p.max_blocks * PAGE ? 0 : (L + PAGE - 1) / PAGE;
-    const int used = (pages + p.pages_per_split - 1) / p.pages_per_split;
-    // Launched as a programmatic dependent of the split kernel: its partials are
+    // Launched as a programmatic dependent of the share kernel: its partials are
     // visible from here on.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const float *ls = p.lse_part + r * p.nsplit;
-    const float4 *os = reinterpret_cast<const float4 *>(p.o_part + r * p.nsplit * D) + lane;
+    const int4 cut = p.cuts[blockIdx.x];
+    const int c = blockIdx.y, parts = cut.z;
+    if (c >= cut.y || parts == 0) return;
+    const int64_t r = (int64_t)cut.x + c;
+    // The first part is this share's last one, the others are the next shares'
+    // first ones (of the same column block).
+    auto row_of = [&](int s) { return ((int64_t)(blockIdx.x + s * col_blocks) * 2 + (s == 0 ? 1 : 0)) * COLS + c; };
     float M = -INFINITY;
-    for (int s = warp; s < used; s += MERGE_WARPS) M = fmaxf(M, ls[s]);
+    for (int s = warp; s < parts; s += MERGE_WARPS) M = fmaxf(M, p.lse_part[row_of(s)]);
     float l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int s = warp; s < used; s += MERGE_WARPS) {
-        const float x = ls[s];
-        const float w = x == -INFINITY ? 0.f : ptx::ex2((x - (M == -INFINITY ? 0.f : M)) * LOG2E);  // NaN stays
-        const float4 v = os[s * (D / 4)];
+    for (int s = warp; s < parts; s += MERGE_WARPS) {
+        const int64_t at = row_of(s);
+        const float x = p.lse_part[at];
+        const float w = x == -INFINITY ? 0.f : ptx::ex2(x - (M == -INFINITY ? 0.f : M));  // NaN stays
+        const float4 v = reinterpret_cast<const float4 *>(p.o_part + at * D)[lane];
         l += w;
         o.x = fmaf(w, v.x, o.x);
         o.y = fmaf(w, v.y, o.y);
@@ -504,50 +663,55 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const DecodeQ4P
     for (int w = 0; w < MERGE_WARPS; ++w) Mt = fmaxf(Mt, part_m[w]);
 #pragma unroll
     for (int w = 0; w < MERGE_WARPS; ++w) {
-        const float f = part_m[w] == -INFINITY ? 1.f : ptx::ex2((part_m[w] - Mt) * LOG2E);  // no finite one: 0 or NaN
+        const float f = part_m[w] == -INFINITY ? 1.f : ptx::ex2(part_m[w] - Mt);  // no finite one: 0 or NaN
         Lt += part_l[w] * f;
         ot += part[w][threadIdx.x] * f;
     }
     const bool any = Lt != 0.f;
     ot = any ? ot / Lt : 0.f;
     static_cast<uint16_t *>(p.out)[r * D + threadIdx.x] = (uint16_t)(ptx::pack_bf16x2(ot, 0.f) & 0xffffu);
-    if (p.lse && threadIdx.x == 0) p.lse[r] = any ? Mt + ptx::lg2(Lt) * LN2 : -INFINITY;
+    if (p.lse && threadIdx.x == 0) p.lse[r] = any ? (Mt + ptx::lg2(Lt)) * LN2 : -INFINITY;
+}
+
+// CTAs: shares times column blocks.
+int grid_of(int B, int Hq, int Hkv, int max_blocks, int max_ctas) {
+    const int col_blocks = (Hq / Hkv + COLS - 1) / COLS;
+    const int64_t items = (int64_t)B * Hkv;
+    const int64_t fill = (items * ((max_blocks + 1) / 2) + MIN_PAIRS - 1) / MIN_PAIRS;
+    int64_t shares = max_ctas / col_blocks;
+    if (shares > (items > fill ? items : fill)) shares = items > fill ? items : fill;
+    if (shares < 1) shares = 1;
+    return (int)shares * col_blocks;
 }
 
 }  // namespace dq4
 
-// Key-split plan, a pure function of the shape: about TARGET_CTAS CTAs over
-// the KV heads' column blocks, 16 .. 256 pages per split.
-void decode_q4_split_plan(int B, int Hq, int Hkv, int max_blocks, int *nsplit, int *pages_per_split) {
-    const int64_t groups = (int64_t)B * Hkv * ((Hq / Hkv + dq4::COLS - 1) / dq4::COLS);
-    const int64_t want = (dq4::TARGET_CTAS + groups - 1) / groups;
-    int64_t pps = (max_blocks + want - 1) / want;
-    if (pps < 16) pps = 16;
-    pps += pps & 1;  // whole pairs
-    if (pps > dq4::MAX_PAGES_PER_SPLIT) pps = dq4::MAX_PAGES_PER_SPLIT;
-    *pages_per_split = (int)pps;
-    *nsplit = (int)((max_blocks + pps - 1) / pps);
+int decode_q4_max_ctas(int B, int Hq, int Hkv, int max_blocks) {
+    return dq4::grid_of(B, Hq, Hkv, max_blocks, dq4::MAX_CTAS);
 }
 
-cudaError_t launch_decode_q4(const DecodeQ4Params &p, cudaStream_t stream) {
+cudaError_t launch_decode_q4(const DecodeQ4Params &p, int sm_count, cudaStream_t stream) {
     const int col_blocks = (p.Hq / p.Hkv + dq4::COLS - 1) / dq4::COLS;
+    const int resident = dq4::CTAS_PER_SM * sm_count;
+    const int grid = dq4::grid_of(p.B, p.Hq, p.Hkv, p.max_blocks, resident < dq4::MAX_CTAS ? resident : dq4::MAX_CTAS);
     static thread_local int configured_device = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (configured_device != dev) {
-        e = cudaFuncSetAttribute(dq4::split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dq4::SMEM);
+        e = cudaFuncSetAttribute(dq4::share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dq4::SMEM);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(dq4::split_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+            e = cudaFuncSetAttribute(dq4::share_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
         configured_device = dev;
     }
-    dq4::split_kernel<<<dim3(p.Hkv * col_blocks, p.nsplit, p.B), dq4::NT, dq4::SMEM, stream>>>(p, col_blocks);
+    dq4::share_kernel<<<grid, dq4::NT, dq4::SMEM, stream>>>(p, col_blocks);
     e = cudaGetLastError();
-    if (e != cudaSuccess || p.nsplit == 1) return e;
+    // One sequence with a share for each KV head is never cut.
+    if (e != cudaSuccess || (p.B == 1 && grid / col_blocks == p.Hkv)) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.Hq));
+    cfg.gridDim = dim3(grid, p.Hq / p.Hkv < dq4::COLS ? p.Hq / p.Hkv : dq4::COLS);
     cfg.blockDim = dim3(dq4::MERGE_WARPS * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -555,7 +719,7 @@ cudaError_t launch_decode_q4(const DecodeQ4Params &p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dq4::merge_kernel, p);
+    return cudaLaunchKernelEx(&cfg, dq4::merge_kernel, p, col_blocks);
 }
 
 }  // namespace attn
