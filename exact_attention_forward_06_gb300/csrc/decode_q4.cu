@@ -69,12 +69,17 @@ constexpr int MAX_CTAS = 3 * 152;      // shares at most: the workspace's size g
 constexpr float RAISE = 8.f;  // a score this far (in log2) above the running max raises it
 constexpr float LN2 = 0.6931471805599453f;
 
-// Codes j and j + 4 of a word as the bf16 pair (16 + n, 16 + n').
+// Codes j and j + 4 of a word as a bf16 pair: (16 + n, 16 + n'), for j = 0 (whose
+// bits need no shift there) (128 + n, 128 + n').
 template <int J>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-    const uint32_t s = J == 0 ? w << 3 : w >> (4 * J - 3);
     uint32_t r;
-    asm("lop3.b32 %0, %1, 0x00780078, %2, 0xEA;" : "=r"(r) : "r"(s), "r"(0x41804180u));  // (s & mask) | 16.0
+    if (J == 0)
+        asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(r) : "r"(w), "r"(0x43004300u));  // (w & mask) | 128.0
+    else
+        asm("lop3.b32 %0, %1, 0x00780078, %2, 0xEA;"
+            : "=r"(r)
+            : "r"(w >> (J == 0 ? 0 : 4 * J - 3)), "r"(0x41804180u));  // | 16.0
     return r;
 }
 
@@ -103,6 +108,13 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Products of two bf16 pairs, each rounded to bf16.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -117,7 +129,7 @@ struct KeyWords {
 };
 struct ValueWords {
     uint4 va, vb;       // codes of tokens 2 c4, 2 c4 + 1 and those + 8
-    uint2 vsa, vsb;     // scales of tokens r4 and r4 + 8, all groups
+    uint4 vsa, vsb;     // scales of tokens 2 c4, 2 c4 + 1 and those + 8, all groups
     uint32_t vza, vzb;  // centers of group r4 % 4, tokens 2 c4, 2 c4 + 1 and those + 8
 };
 
@@ -135,9 +147,8 @@ __device__ __forceinline__ void load_values(ValueWords &w, const uint8_t *blk, i
     const uint8_t *v = blk + r4 * 128 + c4 * 32;
     w.va = *reinterpret_cast<const uint4 *>(v + q4::V_CODES + ((r4 & 1) << 4));
     w.vb = *reinterpret_cast<const uint4 *>(v + q4::V_CODES + (((r4 & 1) ^ 1) << 4));
-    const uint8_t *par = blk + r4 * 8;
-    w.vsa = *reinterpret_cast<const uint2 *>(par + q4::V_SCALES);
-    w.vsb = *reinterpret_cast<const uint2 *>(par + q4::V_SCALES + 64);
+    w.vsa = *reinterpret_cast<const uint4 *>(blk + q4::V_SCALES + c4 * 16);
+    w.vsb = *reinterpret_cast<const uint4 *>(blk + q4::V_SCALES + c4 * 16 + 64);
     const uint8_t *z = blk + q4::V_CENTERS + (r4 & 3) * 32 + c4 * 4;
     w.vza = *reinterpret_cast<const uint32_t *>(z);
     w.vzb = *reinterpret_cast<const uint32_t *>(z + 16);
@@ -300,13 +311,13 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
 
         // Q^T as the B operand: head r4 (zero past the CTA's columns), the channels
         // 32 g + 8 c4 + (j, j + 4), j = 0..3, in the order of a key word's pairs.
-        // qz, qo: B operands of the centers' and the scales' products.  k = 2 c4,
-        // 2 c4 + 1 and 2 c4 + 8 are group c4's Q_g (or -23.5 Q_g) in three bf16
-        // parts, k = 2 c4 + 9 is zero.
+        // qz, qo: B operands of the centers' and the scales' products, two each: at
+        // k = 2 c4, 2 c4 + 1 (centers) and 2 c4 + 8, 2 c4 + 9 (scales) the first two
+        // bf16 parts of group c4's Q_g and of its offset, then the third part.
         uint32_t qb[4][4], qz0, qz1, qo0, qo1;
         {
             const uint4 *qrow = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + (row0 + r4) * D);
-            float x = 0.f;
+            float x = 0.f, y = 0.f;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const uint4 v = r4 < cols ? __ldg(qrow + 4 * g + c4) : make_uint4(0, 0, 0, 0);
@@ -316,9 +327,16 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
                 qb[g][3] = __byte_perm(v.y, v.w, 0x7632);
                 float s = ((lo_f(v.x) + hi_f(v.x)) + (lo_f(v.y) + hi_f(v.y))) +
                           ((lo_f(v.z) + hi_f(v.z)) + (lo_f(v.w) + hi_f(v.w)));
+                // 23.5 of every channel and 112 more of channels 0 and 4 of each eight
+                float t = fmaf(112.f, lo_f(v.x) + lo_f(v.z), 23.5f * s);
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
+                t += __shfl_xor_sync(0xffffffffu, t, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
-                if (g == c4) x = s;
+                t += __shfl_xor_sync(0xffffffffu, t, 2);
+                if (g == c4) {
+                    x = s;
+                    y = -t;
+                }
             }
             auto parts = [](float v, uint32_t &b0, uint32_t &b1) {
                 const uint32_t h0 = ptx::pack_bf16x2(v, 0.f) & 0xffffu;
@@ -328,12 +346,12 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
                 b1 = ptx::pack_bf16x2(v1 - lo_f(h1), 0.f) & 0xffffu;
             };
             parts(x, qz0, qz1);
-            parts(-23.5f * x, qo0, qo1);
+            parts(y, qo0, qo1);
         }
 
         // Running max (log2 units) and row sum of heads 2 c4, 2 c4 + 1.  acc[2 g + i]:
         // channels 32 g + 4 r4 + 2 i (+ 1) times those heads; off[g]: the group's
-        // offset (the same in every row); cen: the centers' term of group r4 % 4.
+        // offsets (of its first channel in four, and of the others); cen: the centers' term of group r4 % 4.
         float m[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
         float acc[8][4], off[4][4], cen[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -353,12 +371,12 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
                 for (int u = 0; u < 2; ++u) {
                     KeyWords k;
                     load_keys(k, blk + u * BLOCK, r4, c4);
-                    const uint32_t za = __byte_perm(k.kza.x, k.kza.y, own), zb = __byte_perm(k.kzb.x, k.kzb.y, own);
-                    const uint32_t sa = __byte_perm(k.ksa.x, k.ksa.y, own), sb = __byte_perm(k.ksb.x, k.ksb.y, own);
-                    const uint32_t az[4] = {za, zb, za, zb}, as[4] = {sa, sb, sa, sb};
-                    mma_zero(s[u], az, qz0, qz1);
-                    mma(s[u], as, qo0, qo1);
-        #pragma unroll
+                    const uint32_t zs[4] = {
+                        __byte_perm(k.kza.x, k.kza.y, own), __byte_perm(k.kzb.x, k.kzb.y, own),
+                        __byte_perm(k.ksa.x, k.ksa.y, own), __byte_perm(k.ksb.x, k.ksb.y, own)};
+                    mma_zero(s[u], zs, qz0, qo0);
+                    mma(s[u], zs, qz1, qo1);
+#pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t wa = g == 0 ? k.ka.x : g == 1 ? k.ka.y : g == 2 ? k.ka.z : k.ka.w;
                         const uint32_t wb = g == 0 ? k.kb.x : g == 1 ? k.kb.y : g == 2 ? k.kb.z : k.kb.w;
@@ -431,6 +449,8 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
                     for (int g = 0; g < 4; ++g) {
                         off[g][0] *= a0;
                         off[g][1] *= a1;
+                        off[g][2] *= a0;
+                        off[g][3] *= a1;
                     }
                     cen[0] *= a0;
                     cen[1] *= a1;
@@ -457,30 +477,34 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
                     }
                     if (!all) {
                         const int nv = __shfl_sync(0xffffffffu, u ? nv1 : nv0, i);
-                        if (r4 >= nv) w.vsa = make_uint2(0, 0);
-                        if (r4 + 8 >= nv) w.vsb = make_uint2(0, 0);
+                        if (2 * c4 >= nv) w.vsa.x = w.vsa.y = 0;
+                        if (2 * c4 + 1 >= nv) w.vsa.z = w.vsa.w = 0;
+                        if (2 * c4 + 8 >= nv) w.vsb.x = w.vsb.y = 0;
+                        if (2 * c4 + 9 >= nv) w.vsb.z = w.vsb.w = 0;
                         w.vza &= (2 * c4 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 1 < nv ? 0xffff0000u : 0u);
                         w.vzb &= (2 * c4 + 8 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 9 < nv ? 0xffff0000u : 0u);
                     }
+                    // P^T as the B operand: tokens 2 c4 (+ 1) and 2 c4 + 8 (+ 9), head r4.
+                    const uint32_t pt0 = transpose8(ptx::pack_bf16x2(p0, p1));
+                    const uint32_t pt1 = transpose8(ptx::pack_bf16x2(p2, p3));
                     {
                         const uint32_t a[4] = {w.vza, w.vza, w.vzb, w.vzb};
-                        mma(cen, a, transpose8(ptx::pack_bf16x2(p0, p1)),
-                                            transpose8(ptx::pack_bf16x2(p2, p3)));
+                        mma(cen, a, pt0, pt1);
                     }
-        #pragma unroll
+#pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const float fa = group_f(w.vsa, g), fb = group_f(w.vsb, g);
-                        // P'^T as the B operand: tokens 2 c4 (+ 1) and 2 c4 + 8 (+ 9), head r4.
-                        const uint32_t b0 = transpose8(ptx::pack_bf16x2(p0 * fa, p1 * fa));
-                        const uint32_t b1 = transpose8(ptx::pack_bf16x2(p2 * fb, p3 * fb));
                         const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
+                        const uint32_t b0 =
+                            mul_bf16x2(pt0, __byte_perm(g < 2 ? w.vsa.x : w.vsa.y, g < 2 ? w.vsa.z : w.vsa.w, sel));
+                        const uint32_t b1 =
+                            mul_bf16x2(pt1, __byte_perm(g < 2 ? w.vsb.x : w.vsb.y, g < 2 ? w.vsb.z : w.vsb.w, sel));
                         const uint32_t wa = __byte_perm(g < 2 ? w.va.x : w.va.y, g < 2 ? w.va.z : w.va.w, sel);
                         const uint32_t wb = __byte_perm(g < 2 ? w.vb.x : w.vb.y, g < 2 ? w.vb.z : w.vb.w, sel);
                         const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
                         mma(acc[2 * g], a0, b0, b1);
                         const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
                         mma(acc[2 * g + 1], a1, b0, b1);
-                        const uint32_t a2[4] = {0xC1BCC1BCu, 0xC1BCC1BCu, 0xC1BCC1BCu, 0xC1BCC1BCu};  // -23.5
+                        const uint32_t a2[4] = {0xC300C300u, 0xC180C180u, 0xC300C300u, 0xC180C180u};  // -128, -16
                         mma(off[g], a2, b0, b1);
                     }
                 }
@@ -513,8 +537,10 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const float add = off[g][j] + __shfl_sync(0xffffffffu, cen[j], 4 * g + c4);
-                acc[2 * g][j] += add;
+                // off: -128 and -16 times the sum of the P'; 7.5 more of it to take off.
+                const float c = __shfl_sync(0xffffffffu, cen[j], 4 * g + c4);
+                const float half = 0.46875f * off[g][2 + j], add = off[g][2 + j] + half + c;
+                acc[2 * g][j] += off[g][j] + half + c;
                 acc[2 * g][2 + j] += add;
                 acc[2 * g + 1][j] += add;
                 acc[2 * g + 1][2 + j] += add;
