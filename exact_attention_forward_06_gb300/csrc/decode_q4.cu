@@ -54,7 +54,7 @@ using q4::BLOCK;
 using q4::D;
 using q4::PAGE;
 
-constexpr int NW = 4;    // warps = page streams
+constexpr int NW = 4;    // warps = page streams, and groups of a head
 constexpr int NST = 3;   // page pairs in flight per warp
 constexpr int COLS = 8;  // query heads per CTA (MMA columns)
 constexpr int NT = NW * 32;
@@ -62,7 +62,8 @@ constexpr int CTAS_PER_SM = 3;
 constexpr int STAGE = 2 * BLOCK;
 constexpr int RING = NW * NST * STAGE;
 constexpr int EXCHANGE = 36 * 32 * 4;  // one warp's partial result: 36 words a lane
-constexpr int SMEM = RING + 2 * EXCHANGE + NW * NST * 8 + 64;  // ring, exchange, barriers, small words
+constexpr int Q_FRAGS = 4 * 32 * 16;   // a lane's query fragments, 16 bytes a group
+constexpr int SMEM = RING + 2 * EXCHANGE + Q_FRAGS + NW * NST * 8 + 64;  // ring, exchange, queries, barriers, words
 static_assert(CTAS_PER_SM * (SMEM + 1024) <= 233472, "CTAs per SM");
 constexpr int MIN_PAIRS = 4;           // pairs a CTA takes at least, unless there is a KV head for each
 constexpr int MAX_CTAS = 3 * 152;      // shares at most: the workspace's size goes by it
@@ -106,6 +107,16 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], 
         "{0f00000000, 0f00000000, 0f00000000, 0f00000000};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A pair's values n - 7.5, exactly: 23.5 off the codes as 16 + n.
+template <int J>
+__device__ __forceinline__ uint32_t value_pair(uint32_t w) {
+    uint32_t r, d;
+    const uint32_t t = J == 0 ? w << 3 : w >> (J == 0 ? 0 : 4 * J - 3);
+    asm("lop3.b32 %0, %1, 0x00780078, %2, 0xEA;" : "=r"(r) : "r"(t), "r"(0x41804180u));
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(r), "r"(0xC1BCC1BCu));
+    return d;
 }
 
 // Products of two bf16 pairs, each rounded to bf16.
@@ -171,8 +182,9 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
     const int r4 = lane >> 2, c4 = lane & 3;
     uint8_t *ring = smem + warp * NST * STAGE;
     float *exchange = reinterpret_cast<float *>(smem + RING) + lane;  // [half][word][lane]
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING + 2 * EXCHANGE) + warp * NST;
-    int *words = reinterpret_cast<int *>(smem + RING + 2 * EXCHANGE + NW * NST * 8);
+    uint4 *q_frag = reinterpret_cast<uint4 *>(smem + RING + 2 * EXCHANGE) + lane;  // [g * 32]
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING + 2 * EXCHANGE + Q_FRAGS) + warp * NST;
+    int *words = reinterpret_cast<int *>(smem + RING + 2 * EXCHANGE + Q_FRAGS + NW * NST * 8);
     volatile int *abort_flag = words;
     int64_t *found = reinterpret_cast<int64_t *>(words + 2);  // [0] all pairs, [1] pairs before words[1]'s sequence
     int *scan = words + 6;                                    // [NW]
@@ -314,17 +326,18 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
         // qz, qo: B operands of the centers' and the scales' products, two each: at
         // k = 2 c4, 2 c4 + 1 (centers) and 2 c4 + 8, 2 c4 + 9 (scales) the first two
         // bf16 parts of group c4's Q_g and of its offset, then the third part.
-        uint32_t qb[4][4], qz0, qz1, qo0, qo1;
+        // The fragments are the same in every warp and stay in shared memory: one
+        // 16-byte read a group and page is cheaper than 16 registers.
+        uint32_t qz0, qz1, qo0, qo1;
         {
             const uint4 *qrow = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + (row0 + r4) * D);
             float x = 0.f, y = 0.f;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const uint4 v = r4 < cols ? __ldg(qrow + 4 * g + c4) : make_uint4(0, 0, 0, 0);
-                qb[g][0] = __byte_perm(v.x, v.z, 0x5410);
-                qb[g][1] = __byte_perm(v.x, v.z, 0x7632);
-                qb[g][2] = __byte_perm(v.y, v.w, 0x5410);
-                qb[g][3] = __byte_perm(v.y, v.w, 0x7632);
+                if (warp == g)
+                    q_frag[g * 32] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                                __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
                 float s = ((lo_f(v.x) + hi_f(v.x)) + (lo_f(v.y) + hi_f(v.y))) +
                           ((lo_f(v.z) + hi_f(v.z)) + (lo_f(v.w) + hi_f(v.w)));
                 // 23.5 of every channel and 112 more of channels 0 and 4 of each eight
@@ -349,15 +362,14 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
             parts(y, qo0, qo1);
         }
 
+        __syncthreads();
         // Running max (log2 units) and row sum of heads 2 c4, 2 c4 + 1.  acc[2 g + i]:
         // channels 32 g + 4 r4 + 2 i (+ 1) times those heads; off[g]: the group's
         // offsets (of its first channel in four, and of the others); cen: the centers' term of group r4 % 4.
         float m[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
-        float acc[8][4], off[4][4], cen[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[8][4], cen[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int t = 0; t < 8; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) off[g][0] = off[g][1] = off[g][2] = off[g][3] = 0.f;
 
         int base = 0, left = n;
         while (left > 0) {
@@ -380,11 +392,12 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t wa = g == 0 ? k.ka.x : g == 1 ? k.ka.y : g == 2 ? k.ka.z : k.ka.w;
                         const uint32_t wb = g == 0 ? k.kb.x : g == 1 ? k.kb.y : g == 2 ? k.kb.z : k.kb.w;
+                        const uint4 qb = q_frag[g * 32];
                         float d[4];
                         const uint32_t a0[4] = {code_pair<0>(wa), code_pair<0>(wb), code_pair<1>(wa), code_pair<1>(wb)};
-                        mma_zero(d, a0, qb[g][0], qb[g][1]);
+                        mma_zero(d, a0, qb.x, qb.y);
                         const uint32_t a1[4] = {code_pair<2>(wa), code_pair<2>(wb), code_pair<3>(wa), code_pair<3>(wb)};
-                        mma(d, a1, qb[g][2], qb[g][3]);
+                        mma(d, a1, qb.z, qb.w);
                         const float fa = group_f(k.ksa, g), fb = group_f(k.ksb, g);
                         s[u][0] = fmaf(fa, d[0], s[u][0]);
                         s[u][1] = fmaf(fa, d[1], s[u][1]);
@@ -445,13 +458,6 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
                         acc[t][2] *= a0;
                         acc[t][3] *= a1;
                     }
-        #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        off[g][0] *= a0;
-                        off[g][1] *= a1;
-                        off[g][2] *= a0;
-                        off[g][3] *= a1;
-                    }
                     cen[0] *= a0;
                     cen[1] *= a1;
                     m[0] = m0;
@@ -500,12 +506,10 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
                             mul_bf16x2(pt1, __byte_perm(g < 2 ? w.vsb.x : w.vsb.y, g < 2 ? w.vsb.z : w.vsb.w, sel));
                         const uint32_t wa = __byte_perm(g < 2 ? w.va.x : w.va.y, g < 2 ? w.va.z : w.va.w, sel);
                         const uint32_t wb = __byte_perm(g < 2 ? w.vb.x : w.vb.y, g < 2 ? w.vb.z : w.vb.w, sel);
-                        const uint32_t a0[4] = {code_pair<0>(wa), code_pair<1>(wa), code_pair<0>(wb), code_pair<1>(wb)};
+                        const uint32_t a0[4] = {value_pair<0>(wa), value_pair<1>(wa), value_pair<0>(wb), value_pair<1>(wb)};
                         mma(acc[2 * g], a0, b0, b1);
-                        const uint32_t a1[4] = {code_pair<2>(wa), code_pair<3>(wa), code_pair<2>(wb), code_pair<3>(wb)};
+                        const uint32_t a1[4] = {value_pair<2>(wa), value_pair<3>(wa), value_pair<2>(wb), value_pair<3>(wb)};
                         mma(acc[2 * g + 1], a1, b0, b1);
-                        const uint32_t a2[4] = {0xC300C300u, 0xC180C180u, 0xC300C300u, 0xC180C180u};  // -128, -16
-                        mma(off[g], a2, b0, b1);
                     }
                 }
                 if (++slot == NST) {
@@ -537,10 +541,8 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                // off: -128 and -16 times the sum of the P'; 7.5 more of it to take off.
-                const float c = __shfl_sync(0xffffffffu, cen[j], 4 * g + c4);
-                const float half = 0.46875f * off[g][2 + j], add = off[g][2 + j] + half + c;
-                acc[2 * g][j] += off[g][j] + half + c;
+                const float add = __shfl_sync(0xffffffffu, cen[j], 4 * g + c4);
+                acc[2 * g][j] += add;
                 acc[2 * g][2 + j] += add;
                 acc[2 * g + 1][j] += add;
                 acc[2 * g + 1][2 + j] += add;
