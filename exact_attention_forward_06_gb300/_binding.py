@@ -7,7 +7,6 @@ missing this module raises immediately -- there is no fallback path.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import fractions
 import math
@@ -443,36 +442,65 @@ Q4_BLOCK_BYTES = 2560  # one page of one KV head in the 4-bit cache (ATTN_Q4_BLO
 _PI = fractions.Fraction("3.14159265358979323846264338327950288419716939937510582")
 
 
-def _on_current_device(*tensors):
-    """The library launches on the current device: every tensor must live there."""
-    want = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != want:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{want}")
+# The operators below run in a few microseconds on small calls, so their checks
+# take one cheap pass per tensor: _in gives the tensor's address, and anything
+# out of order goes to _refuse, which says what.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_device = torch._C._cuda_getDevice
+_bf16 = torch.bfloat16
+_i32 = torch.int32
 
 
-def _on_stream(stream):
-    """Outputs and workspaces made here belong to the stream that writes them."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _strided(t, name):
-    """A CUDA bf16 tensor whose last dimension is contiguous (the others may be strided)."""
+def _refuse(t, name, dtype, dev, contiguous=True):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() < 2 or t.stride(-1) != 1:
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not contiguous and (t.dim() < 2 or t.stride(-1) != 1):
         raise ValueError(f"{name} must be contiguous in its last dimension")
+    raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+
+
+def _in(t, name, dtype, dev):
+    """The address of a contiguous tensor of dtype on the current device dev."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, dev)
+
+
+def _opt(t, name, dtype, dev):
+    return None if t is None else _in(t, name, dtype, dev)
+
+
+def _in_strided(t, name, dev):
+    """The address of a bf16 tensor that is contiguous in its last dimension (the others may be strided)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is _bf16 and t.get_device() == dev and t.dim() >= 2 and
+            t.stride(-1) == 1):
+        return t.data_ptr()
+    _refuse(t, name, _bf16, dev, contiguous=False)
+
+
+def _current():
+    """The device that the library launches on: the current one (-2, which no tensor is on: there is none)."""
+    try:
+        return _device()
+    except RuntimeError:
+        return -2
+
+
+def _empty(shape, dtype, device, stream):
+    """An output or workspace, which belongs to the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _step(t, dim):
     # the stride of a dimension of length one is never used, whatever it says
     return 0 if t.shape[dim] == 1 else t.stride(dim)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
 
 
 def rope_table(inv_freq, axes=None, *, device="cuda"):
@@ -498,34 +526,30 @@ def rope_table(inv_freq, axes=None, *, device="cuda"):
     return torch.tensor(rows, dtype=torch.int64).to(device)
 
 
-def _rotate_args(q_weight, k_weight, eps, positions, pos_shape, rope, interleaved):
+def _rotate_args(q_weight, k_weight, eps, positions, pos_shape, rope, interleaved, dev):
     """The norm and rotation arguments of a call, checked, in the C order."""
+    wq = _opt(q_weight, "q_weight", _bf16, dev)
+    wk = _opt(k_weight, "k_weight", _bf16, dev)
     for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _dev_tensor(w, n, torch.bfloat16)
-            if w.shape != (128,):
-                raise ValueError(f"{n} must have 128 elements")
+        if w is not None and w.shape != (128,):
+            raise ValueError(f"{n} must have 128 elements")
     n_axes = 1
+    pos = None
     if positions is not None:
-        _dev_tensor(positions, "positions", torch.int32)
-        if tuple(positions.shape) == pos_shape:
-            pass
-        elif positions.dim() == len(pos_shape) + 1 and tuple(positions.shape[1:]) == pos_shape:
-            n_axes = positions.shape[0]
-        else:
-            raise ValueError(f"positions must be {list(pos_shape)} or [axes, {', '.join(map(str, pos_shape))}], "
-                             f"got {list(positions.shape)}")
-    rotary_dim = 0
-    if rope is not None:
-        _dev_tensor(rope, "rope", torch.int64)
-        if rope.dim() != 2 or rope.shape[1] != 2:
-            raise ValueError("rope must be a table made by rope_table")
-        rotary_dim = 2 * rope.shape[0]
-        if positions is None:
-            n_axes = 4  # the default position is the same on every axis
-    _on_current_device(q_weight, k_weight, positions, rope)
-    return [_ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), n_axes, _ptr(rope), rotary_dim,
-            int(bool(interleaved))]
+        pos = _in(positions, "positions", _i32, dev)
+        shape = positions.shape
+        if shape != pos_shape:
+            if len(shape) != len(pos_shape) + 1 or shape[1:] != pos_shape:
+                raise ValueError(f"positions must be {list(pos_shape)} or [axes, {', '.join(map(str, pos_shape))}], "
+                                 f"got {list(shape)}")
+            n_axes = shape[0]
+    if rope is None:
+        return wq, wk, eps, pos, n_axes, None, 0, interleaved
+    plan = _in(rope, "rope", torch.int64, dev)
+    if rope.dim() != 2 or rope.shape[1] != 2:
+        raise ValueError("rope must be a table made by rope_table")
+    # the default position is the same on every axis
+    return wq, wk, eps, pos, n_axes if pos else 4, plan, 2 * rope.shape[0], interleaved
 
 
 def qk_norm_rope(q, k=None, *, rope=None, positions=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -538,83 +562,100 @@ def qk_norm_rope(q, k=None, *, rope=None, positions=None, q_weight=None, k_weigh
     axis; q_weight, k_weight: bf16 [128], None for no norm.  Returns (q_out, k_out), dense in the layout (k_out None
     without k); q_out may be q itself when it is dense.
     """
-    lib = load()
+    lib = _lib or load()
     if layout not in LAYOUTS:
         raise ValueError(f"layout must be 'bshd' or 'bhsd', got {layout!r}")
-    _strided(q, "q")
+    dev = _current()
+    qp = _in_strided(q, "q", dev)
+    kp = None if k is None else _in_strided(k, "k", dev)
+    shape = q.shape
+    k_shape = None if k is None else k.shape
+    if len(shape) == 4:
+        b_dim, s_dim, h_dim = (0, 1, 2) if layout == "bshd" else (0, 2, 1)
+        B = shape[0]
+        pos_shape = (B, shape[s_dim])
+    elif len(shape) == 3 and layout == "bshd":
+        b_dim, s_dim, h_dim = None, 0, 1
+        B = 1
+        pos_shape = (shape[0],)
+    else:
+        raise ValueError("q and k must be 4-D, or both packed [total, H, 128] (layout 'bshd')")
+    S, Hq, d = shape[s_dim], shape[h_dim], shape[-1]
+    Hkv = 0
     if k is not None:
-        _strided(k, "k")
-    packed = q.dim() == 3
-    if packed and layout != "bshd":
-        raise ValueError("packed tensors are [total, H, 128] (layout 'bshd')")
-    if q.dim() not in (3, 4) or (k is not None and k.dim() != q.dim()):
-        raise ValueError("q and k must be 4-D, or both packed 3-D")
-    q4, k4 = (q.unsqueeze(0), None if k is None else k.unsqueeze(0)) if packed else (q, k)
-    s_dim, h_dim = (1, 2) if layout == "bshd" else (2, 1)
-    B, S, Hq, d = q4.shape[0], q4.shape[s_dim], q4.shape[h_dim], q4.shape[3]
-    Hkv = 0 if k is None else k4.shape[h_dim]
-    if k is not None and (k4.shape[0] != B or k4.shape[s_dim] != S or k4.shape[3] != d):
-        raise ValueError("q and k must have the same batch, positions and head dimension")
-    for o, x, n in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        if o is not None:
-            _dev_tensor(o, n, torch.bfloat16)
-            if x is None or o.shape != x.shape:
-                raise ValueError(f"{n} must have its input's shape")
-    args = _rotate_args(q_weight, k_weight, eps, positions, (S,) if packed else (B, S), rope, interleaved)
-    _on_current_device(q, k, q_out, k_out)
-    with _on_stream(stream):
-        if q_out is None:
-            q_out = torch.empty(q.shape, device=q.device, dtype=torch.bfloat16)
-        if k_out is None and k is not None:
-            k_out = torch.empty(k.shape, device=k.device, dtype=torch.bfloat16)
-    steps = [_step(q4, i) for i in (0, s_dim, h_dim)] + ([0] * 3 if k is None else
-                                                         [_step(k4, i) for i in (0, s_dim, h_dim)])
-    rc = lib.attn_qk_norm_rope(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), *args, B, S, Hq, Hkv, d,
-                               LAYOUTS[layout], *steps, _stream(stream))
-    _check(rc, "attn_qk_norm_rope")
+        if len(k_shape) != len(shape) or k_shape[s_dim] != S or k_shape[-1] != d or (b_dim == 0 and k_shape[0] != B):
+            raise ValueError("q and k must have the same batch, positions and head dimension")
+        Hkv = k_shape[h_dim]
+    args = _rotate_args(q_weight, k_weight, eps, positions, pos_shape, rope, interleaved, dev)
+    if q_out is None:
+        q_out = _empty(shape, _bf16, q.device, stream)
+        qo = q_out.data_ptr()
+    else:
+        qo = _in(q_out, "q_out", _bf16, dev)
+        if q_out.shape != shape:
+            raise ValueError("q_out must have q's shape")
+    ko = None
+    if k_out is not None:
+        ko = _in(k_out, "k_out", _bf16, dev)
+        if k is None or k_out.shape != k_shape:
+            raise ValueError("k_out must have k's shape")
+    elif k is not None:
+        k_out = _empty(k_shape, _bf16, q.device, stream)
+        ko = k_out.data_ptr()
+    rc = lib.attn_qk_norm_rope(
+        qp, kp, qo, ko, *args, B, S, Hq, Hkv, d, LAYOUTS[layout],
+        0 if b_dim is None else _step(q, 0), _step(q, s_dim), _step(q, h_dim),
+        0 if b_dim is None or k is None else _step(k, 0), 0 if k is None else _step(k, s_dim),
+        0 if k is None else _step(k, h_dim), _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "attn_qk_norm_rope")
     return q_out, k_out
 
 
-def _append(fn_name, q, k, v, pools, Hkv_pool, num_pages, page_size, block_table, seqlens, cu_seqlens, rope, positions,
-            q_weight, k_weight, eps, interleaved, q_out, stream):
-    lib = load()
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        if t is None and n == "q":
-            continue
-        _strided(t, n)
-        if t.dim() != 3 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            raise ValueError(f"{n} must be [tokens, H, 128] with the heads of a token contiguous")
-    for t, n in ((block_table, "block_table"), (seqlens, "seqlens")):
-        _dev_tensor(t, n, torch.int32)
-    if cu_seqlens is not None:
-        _dev_tensor(cu_seqlens, "cu_seqlens", torch.int32)
-    total, Hkv, d = k.shape
+def _append(fn, q, k, v, pools, Hkv_pool, num_pages, page_size, block_table, seqlens, cu_seqlens, rope, positions,
+            q_weight, k_weight, eps, interleaved, q_out, stream, dev):
+    qp = None if q is None else _in_strided(q, "q", dev)
+    kp, vp = _in_strided(k, "k", dev), _in_strided(v, "v", dev)
+    table, lens = _in(block_table, "block_table", _i32, dev), _in(seqlens, "seqlens", _i32, dev)
+    cu = _opt(cu_seqlens, "cu_seqlens", _i32, dev)
+    shape, table_shape = k.shape, block_table.shape
+    if len(shape) != 3 or v.shape != shape:
+        raise ValueError("k and v must be [tokens, Hkv, 128], of the same shape")
+    total, Hkv, d = shape
     B = seqlens.numel()
-    if v.shape != k.shape or (q is not None and (q.shape[0] != total or q.shape[2] != d)):
-        raise ValueError("q, k, v must have the same tokens and head dimension, k and v the same heads")
+    Hq, q_step = 0, 0
+    if q is not None:
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != total or q_shape[2] != d:
+            raise ValueError("q must be [tokens, Hq, 128], of the tokens and head dimension of k")
+        Hq = q_shape[1]
+        q_step = q.stride(0) if total > 1 else Hq * d
+    for t, n, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv)):
+        if h > 1 and t.stride(1) != d:
+            raise ValueError(f"{n} must have the heads of a token contiguous")
     if Hkv != Hkv_pool:
         raise ValueError(f"the cache has {Hkv_pool} KV heads, k and v have {Hkv}")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    if len(table_shape) != 2 or table_shape[0] != B:
         raise ValueError("block_table must have one row per sequence")
-    if cu_seqlens is None and total != B:
-        raise ValueError("without cu_seqlens there is one new token per sequence")
-    if cu_seqlens is not None and cu_seqlens.numel() != B + 1:
+    if cu is None:
+        if total != B:
+            raise ValueError("without cu_seqlens there is one new token per sequence")
+    elif cu_seqlens.numel() != B + 1:
         raise ValueError("cu_seqlens must have B + 1 entries")
+    qo = None
     if q_out is not None:
-        _dev_tensor(q_out, "q_out", torch.bfloat16)
-        if q is None or q_out.shape != q.shape:
+        qo = _in(q_out, "q_out", _bf16, dev)
+        if q is None or q_out.shape != q_shape:
             raise ValueError("q_out must have q's shape")
-    args = _rotate_args(q_weight, k_weight, eps, positions, (total,), rope, interleaved)
-    _on_current_device(q, k, v, *pools, block_table, seqlens, cu_seqlens, q_out)
+    args = _rotate_args(q_weight, k_weight, eps, positions, (total,), rope, interleaved, dev)
     if q is not None and q_out is None:
-        with _on_stream(stream):
-            q_out = torch.empty(q.shape, device=q.device, dtype=torch.bfloat16)
-    steps = [0 if t is None else (t.shape[1] * d if total == 1 else t.stride(0)) for t in (q, k, v)]
-    rc = getattr(lib, fn_name)(_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), *[t.data_ptr() for t in pools],
-                               block_table.data_ptr(), seqlens.data_ptr(), _ptr(cu_seqlens), *args, B, total,
-                               0 if q is None else q.shape[1], Hkv, d, page_size, num_pages, block_table.shape[1],
-                               *steps, _stream(stream))
-    _check(rc, fn_name)
+        q_out = _empty(q_shape, _bf16, q.device, stream)
+        qo = q_out.data_ptr()
+    rc = fn(qp, kp, vp, qo, *pools, table, lens, cu, *args, B, total, Hq, Hkv, d, page_size, num_pages,
+            table_shape[1], q_step, k.stride(0) if total > 1 else Hkv * d, v.stride(0) if total > 1 else Hkv * d,
+            _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, fn.__name__)
     return q_out
 
 
@@ -628,61 +669,67 @@ def append_paged(q, k, v, k_pages, v_pages, block_table, seqlens, cu_seqlens=Non
     sequence).  positions: int32 [total] or [axes, total], default: each token's position in its cache.  Returns
     q_out [total, Hq, 128] (None without q): the q of fwd_paged or decode_paged over the same arrays.
     """
-    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        _dev_tensor(t, n, torch.bfloat16)
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+    lib = _lib or load()
+    dev = _current()
+    pools = _in(k_pages, "k_pages", _bf16, dev), _in(v_pages, "v_pages", _bf16, dev)
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [num_pages, 16, Hkv, 128]")
-    num_pages, page_size, Hkv, d = k_pages.shape
+    num_pages, page_size, Hkv, d = shape
     if isinstance(k, torch.Tensor) and k.shape[-1] != d:
         raise ValueError("k and the pages must have the same head dimension")
-    return _append("attn_append_paged", q, k, v, (k_pages, v_pages), Hkv, num_pages, page_size, block_table, seqlens,
-                   cu_seqlens, rope, positions, q_weight, k_weight, eps, interleaved, q_out, stream)
+    return _append(lib.attn_append_paged, q, k, v, pools, Hkv, num_pages, page_size, block_table, seqlens, cu_seqlens,
+                   rope, positions, q_weight, k_weight, eps, interleaved, q_out, stream, dev)
 
 
-def _q4_cache(cache):
-    _dev_tensor(cache, "cache", torch.uint8)
-    if cache.dim() != 3 or cache.shape[2] != Q4_BLOCK_BYTES:
+def _q4_cache(cache, dev):
+    """Address, pages and KV heads of a 4-bit cache."""
+    ptr = _in(cache, "cache", torch.uint8, dev)
+    shape = cache.shape
+    if len(shape) != 3 or shape[2] != Q4_BLOCK_BYTES:
         raise ValueError(f"cache must be [num_pages, Hkv, {Q4_BLOCK_BYTES}]")
-    return cache.shape[0], cache.shape[1]
+    return ptr, shape[0], shape[1]
 
 
 def append_paged_q4(q, k, v, cache, block_table, seqlens, cu_seqlens=None, *, rope=None, positions=None,
                     q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None, stream=None):
     """append_paged into a cache held in 4 bits: cache [num_pages, Hkv, Q4_BLOCK_BYTES] uint8, updated in place."""
-    num_pages, Hkv = _q4_cache(cache)
-    return _append("attn_append_paged_q4", q, k, v, (cache,), Hkv, num_pages, 16, block_table, seqlens, cu_seqlens,
-                   rope, positions, q_weight, k_weight, eps, interleaved, q_out, stream)
+    lib = _lib or load()
+    dev = _current()
+    ptr, num_pages, Hkv = _q4_cache(cache, dev)
+    return _append(lib.attn_append_paged_q4, q, k, v, (ptr,), Hkv, num_pages, 16, block_table, seqlens, cu_seqlens,
+                   rope, positions, q_weight, k_weight, eps, interleaved, q_out, stream, dev)
 
 
 def gather_paged_q4(cache, block_table, seqlens, cu_seqlens_k, *, total_k=None, k_out=None, v_out=None, stream=None):
     """Read sequences back from a 4-bit cache: (k, v) bf16 [total_k, Hkv, 128], sequence b's seqlens[b] tokens from row
     cu_seqlens_k[b] on -- the k and v of fwd_varlen.  total_k, when omitted, is read from the outputs given or the
     offsets (a synchronisation)."""
-    lib = load()
-    num_pages, Hkv = _q4_cache(cache)
-    for t, n in ((block_table, "block_table"), (seqlens, "seqlens"), (cu_seqlens_k, "cu_seqlens_k")):
-        _dev_tensor(t, n, torch.int32)
+    lib = _lib or load()
+    dev = _current()
+    ptr, num_pages, Hkv = _q4_cache(cache, dev)
+    table, lens = _in(block_table, "block_table", _i32, dev), _in(seqlens, "seqlens", _i32, dev)
+    cu = _in(cu_seqlens_k, "cu_seqlens_k", _i32, dev)
+    table_shape = block_table.shape
     B = seqlens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or cu_seqlens_k.numel() != B + 1:
+    if len(table_shape) != 2 or table_shape[0] != B or cu_seqlens_k.numel() != B + 1:
         raise ValueError("block_table must have B rows and cu_seqlens_k B + 1 entries")
     for o, n in ((k_out, "k_out"), (v_out, "v_out")):
         if o is not None:
-            _dev_tensor(o, n, torch.bfloat16)
+            _in(o, n, _bf16, dev)
             if o.dim() != 3 or o.shape[1:] != (Hkv, 128) or (total_k is not None and o.shape[0] != total_k):
                 raise ValueError(f"{n} must be [total_k, Hkv, 128]")
             total_k = o.shape[0]
-    _on_current_device(cache, block_table, seqlens, cu_seqlens_k, k_out, v_out)
     if total_k is None:
         total_k = max(1, int(cu_seqlens_k[-1]))
-    with _on_stream(stream):
-        if k_out is None:
-            k_out = torch.empty((total_k, Hkv, 128), device=cache.device, dtype=torch.bfloat16)
-        if v_out is None:
-            v_out = torch.empty((total_k, Hkv, 128), device=cache.device, dtype=torch.bfloat16)
-    rc = lib.attn_gather_paged_q4(cache.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(),
-                                  cu_seqlens_k.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, Hkv, int(total_k),
-                                  128, 16, num_pages, block_table.shape[1], _stream(stream))
-    _check(rc, "attn_gather_paged_q4")
+    if k_out is None:
+        k_out = _empty((total_k, Hkv, 128), _bf16, cache.device, stream)
+    if v_out is None:
+        v_out = _empty((total_k, Hkv, 128), _bf16, cache.device, stream)
+    rc = lib.attn_gather_paged_q4(ptr, table, lens, cu, k_out.data_ptr(), v_out.data_ptr(), B, Hkv, total_k, 128, 16,
+                                  num_pages, table_shape[1], _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "attn_gather_paged_q4")
     return k_out, v_out
 
 
@@ -691,48 +738,51 @@ def decode_q4_workspace_bytes(B: int, Hq: int, Hkv: int, d: int, max_blocks_per_
     return int(load().attn_decode_q4_workspace_bytes(B, Hq, Hkv, d, max_blocks_per_seq))
 
 
+def _attn_out(out, lse, shape, lse_shape, device, stream, dev):
+    """out and lse as given (checked) or made, and their addresses."""
+    if out is None:
+        out = _empty(shape, _bf16, device, stream)
+        op = out.data_ptr()
+    else:
+        op = _in(out, "out", _bf16, dev)
+        if out.shape != shape:
+            raise ValueError(f"out must be {list(shape)}")
+    if lse is None:
+        lse = _empty(lse_shape, torch.float32, device, stream)
+        return out, lse, op, lse.data_ptr()
+    if lse is False:
+        return out, None, op, None
+    lp = _in(lse, "lse", torch.float32, dev)
+    if lse.shape != lse_shape:
+        raise ValueError(f"lse must be {list(lse_shape)}")
+    return out, lse, op, lp
+
+
 def decode_paged_q4(q, cache, block_table, seqlens, *, scale=None, out=None, lse=None, workspace=None, stream=None):
     """One decode step over a cache held in 4 bits (the arguments of decode_paged, with one cache tensor
     [num_pages, Hkv, Q4_BLOCK_BYTES] uint8).  Returns (out [B, Hq, 128] bf16, lse [B, Hq] fp32)."""
-    lib = load()
-    num_pages, Hkv = _q4_cache(cache)
-    _dev_tensor(q, "q", torch.bfloat16)
-    for t, n in ((block_table, "block_table"), (seqlens, "seqlens")):
-        _dev_tensor(t, n, torch.int32)
-    if q.dim() != 3 or block_table.dim() != 2 or block_table.shape[0] != q.shape[0] or seqlens.numel() != q.shape[0]:
+    lib = _lib or load()
+    dev = _current()
+    ptr, num_pages, Hkv = _q4_cache(cache, dev)
+    qp = _in(q, "q", _bf16, dev)
+    table, lens = _in(block_table, "block_table", _i32, dev), _in(seqlens, "seqlens", _i32, dev)
+    shape, table_shape = q.shape, block_table.shape
+    if len(shape) != 3 or len(table_shape) != 2 or table_shape[0] != shape[0] or seqlens.numel() != shape[0]:
         raise ValueError("q must be [B, Hq, 128], block_table [B, max_blocks] and seqlens [B]")
-    B, Hq, d = q.shape
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    _attn_out(out, lse, q.shape, (B, Hq))
-    _on_current_device(q, cache, block_table, seqlens, out, workspace, None if lse is False else lse)
-    need = decode_q4_workspace_bytes(B, Hq, Hkv, d, block_table.shape[1])
-    if workspace is not None:
-        _dev_tensor(workspace, "workspace", torch.uint8)
-    with _on_stream(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
-        if workspace is None:
-            workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
-        rc = lib.attn_decode_paged_q4(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(),
-                                      out.data_ptr(), None if lse is False else lse.data_ptr(), B, Hq, Hkv, d, 16,
-                                      num_pages, block_table.shape[1], float(scale), workspace.data_ptr(),
-                                      workspace.numel(), _stream(stream))
-    _check(rc, "attn_decode_paged_q4")
-    return out, (None if lse is False else lse)
-
-
-def _attn_out(out, lse, out_shape, lse_shape):
-    if out is not None:
-        _dev_tensor(out, "out", torch.bfloat16)
-        if out.shape != out_shape:
-            raise ValueError(f"out must be {list(out_shape)}")
-    if lse is not None and lse is not False:
-        _dev_tensor(lse, "lse", torch.float32)
-        if tuple(lse.shape) != lse_shape:
-            raise ValueError(f"lse must be {list(lse_shape)}")
+    B, Hq, d = shape
+    out, lse, op, lp = _attn_out(out, lse, shape, (B, Hq), q.device, stream, dev)
+    if workspace is None:
+        need = lib.attn_decode_q4_workspace_bytes(B, Hq, Hkv, d, table_shape[1])
+        workspace = _empty(max(need, 1), torch.uint8, q.device, stream)
+        wp = workspace.data_ptr()
+    else:
+        wp = _in(workspace, "workspace", torch.uint8, dev)
+    rc = lib.attn_decode_paged_q4(qp, ptr, table, lens, op, lp, B, Hq, Hkv, d, 16, num_pages, table_shape[1],
+                                  1.0 / math.sqrt(d) if scale is None else scale, wp, workspace.numel(),
+                                  _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "attn_decode_paged_q4")
+    return out, lse
 
 
 def fwd_paged_q4_workspace_bytes(B: int, Hkv: int, d: int, max_total_k: int) -> int:
@@ -745,44 +795,39 @@ def fwd_paged_q4(q, cache, block_table, seqlens_k, cu_seqlens_q, *, max_seqlen_q
     """Prefill of packed query chunks against a cache held in 4 bits (the arguments of fwd_paged, with one cache tensor
     [num_pages, Hkv, Q4_BLOCK_BYTES] uint8).  max_total_k bounds the sum of seqlens_k; it and max_seqlen_q, when
     omitted, are read from the device (a synchronisation).  Returns (out [total_q, Hq, 128] bf16, lse [Hq, total_q])."""
-    lib = load()
-    num_pages, Hkv = _q4_cache(cache)
-    _dev_tensor(q, "q", torch.bfloat16)
-    for t, n in ((block_table, "block_table"), (seqlens_k, "seqlens_k"), (cu_seqlens_q, "cu_seqlens_q")):
-        _dev_tensor(t, n, torch.int32)
+    lib = _lib or load()
     if rounding not in ROUNDING:
         raise ValueError(f"rounding must be one of {sorted(ROUNDING)}, got {rounding!r}")
-    if q.dim() != 3:
-        raise ValueError("q must be [total_q, Hq, 128]")
-    total_q, Hq, d = q.shape
+    dev = _current()
+    ptr, num_pages, Hkv = _q4_cache(cache, dev)
+    qp = _in(q, "q", _bf16, dev)
+    table, lens = _in(block_table, "block_table", _i32, dev), _in(seqlens_k, "seqlens_k", _i32, dev)
+    cu = _in(cu_seqlens_q, "cu_seqlens_q", _i32, dev)
+    shape, table_shape = q.shape, block_table.shape
     B = seqlens_k.numel()
-    if cu_seqlens_q.numel() != B + 1 or block_table.dim() != 2 or block_table.shape[0] != B:
+    if len(shape) != 3:
+        raise ValueError("q must be [total_q, Hq, 128]")
+    if cu_seqlens_q.numel() != B + 1 or len(table_shape) != 2 or table_shape[0] != B:
         raise ValueError("cu_seqlens_q must have B + 1 entries and block_table B rows")
-    _attn_out(out, lse, q.shape, (Hq, total_q))
-    if workspace is not None:
-        _dev_tensor(workspace, "workspace", torch.uint8)
-    _on_current_device(q, cache, block_table, seqlens_k, cu_seqlens_q, out, workspace, None if lse is False else lse)
+    total_q, Hq, d = shape
     if max_seqlen_q is None:
         max_seqlen_q = max(1, int(torch.diff(cu_seqlens_q).max()))
     if max_total_k is None:
         max_total_k = max(1, int(seqlens_k.sum()))
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    need = fwd_paged_q4_workspace_bytes(B, Hkv, d, int(max_total_k))
-    with _on_stream(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((Hq, total_q), device=q.device, dtype=torch.float32)
-        if workspace is None:
-            workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
-        rc = lib.attn_fwd_paged_q4(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seqlens_k.data_ptr(),
-                                   cu_seqlens_q.data_ptr(), out.data_ptr(), None if lse is False else lse.data_ptr(),
-                                   B, Hq, Hkv, total_q, int(max_seqlen_q), d, 16, num_pages, block_table.shape[1],
-                                   int(max_total_k), int(bool(causal)), float(scale), ROUNDING[rounding],
-                                   workspace.data_ptr(), workspace.numel(), _stream(stream))
-    _check(rc, "attn_fwd_paged_q4")
-    return out, (None if lse is False else lse)
+    out, lse, op, lp = _attn_out(out, lse, shape, (Hq, total_q), q.device, stream, dev)
+    if workspace is None:
+        need = lib.attn_fwd_paged_q4_workspace_bytes(B, Hkv, d, max_total_k)
+        workspace = _empty(max(need, 1), torch.uint8, q.device, stream)
+        wp = workspace.data_ptr()
+    else:
+        wp = _in(workspace, "workspace", torch.uint8, dev)
+    rc = lib.attn_fwd_paged_q4(qp, ptr, table, lens, cu, op, lp, B, Hq, Hkv, total_q, max_seqlen_q, d, 16, num_pages,
+                               table_shape[1], max_total_k, bool(causal), 1.0 / math.sqrt(d) if scale is None else scale,
+                               ROUNDING[rounding], wp, workspace.numel(),
+                               _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "attn_fwd_paged_q4")
+    return out, lse
 
 
 def lse_merge(o_parts, lse_parts, *, out=None, lse=None, stream=None, rounding="rtne"):
