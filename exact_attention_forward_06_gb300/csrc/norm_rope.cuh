@@ -8,9 +8,14 @@
 // Lanes past the plan's pairs hold eight of the channels from R on, which only
 // take the norm.  The norm's sum runs over the 16 lanes in a fixed order.
 //
-// Angles: position * turns modulo 2^64 is the exact fraction of a turn; its
-// upper 32 bits as a signed number of half turns go to sincospi, whose argument
-// in [-1, 1) needs no range reduction.
+// The norm's weights are multiplied into the token's cosines and sines, once for
+// all its rows; the root is applied to the rotated pair: with the weights u, w of a
+// pair's channels, (a, b) -> r (a u cos - b w sin, a u sin + b w cos).
+//
+// Angles: position * turns modulo 2^64 is the exact fraction of a turn.  Its upper
+// 32 bits, to the nearest quarter turn and the rest x in [-pi/4, pi/4], go to the
+// Taylor series of sine (to x^9; the next term is below 2^-29) and cosine (to
+// x^10; below 2^-33): half the instructions of a general sine and cosine of x.
 #pragma once
 
 #include <cstdint>
@@ -48,6 +53,26 @@ struct LaneTurn {
     float c[4], s[4];
 };
 
+// Sine and cosine of `frac` / 2^32 of a turn.
+__device__ __forceinline__ void sincos_turn(uint32_t frac, float &s, float &c) {
+    const uint32_t quarter = (frac + 0x20000000u) >> 30;
+    const float x = (float)(int32_t)(frac - (quarter << 30)) * 1.4629180792671596e-09f;  // 2 pi / 2^32
+    const float x2 = x * x;
+    float sn = fmaf(x2, 2.7557319224e-06f, -1.9841269841e-04f);  // 1/9!, -1/7!
+    sn = fmaf(x2, sn, 8.3333333333e-03f);                        // 1/5!
+    sn = fmaf(x2, sn, -1.6666666667e-01f);                       // -1/3!
+    sn = fmaf(x2 * x, sn, x);
+    float cs = fmaf(x2, -2.7557319224e-07f, 2.4801587302e-05f);  // -1/10!, 1/8!
+    cs = fmaf(x2, cs, -1.3888888889e-03f);                       // -1/6!
+    cs = fmaf(x2, cs, 4.1666666667e-02f);                        // 1/4!
+    cs = fmaf(x2, cs, -0.5f);
+    cs = fmaf(x2, cs, 1.f);
+    // A quarter turn on: (sin, cos) -> (cos, -sin).
+    const float a = quarter & 1 ? cs : sn, b = quarter & 1 ? sn : cs;
+    s = __uint_as_float(__float_as_uint(a) ^ (quarter & 2) << 30);
+    c = __uint_as_float(__float_as_uint(b) ^ ((quarter + 1) & 2) << 30);
+}
+
 // pos_stride: tokens per axis in p.positions; `token` indexes them; without
 // positions every axis has the position `pos0`.
 __device__ __forceinline__ LaneTurn lane_turn(const RotateParams &p, int l, int64_t token, int64_t pos_stride,
@@ -59,18 +84,25 @@ __device__ __forceinline__ LaneTurn lane_turn(const RotateParams &p, int l, int6
         t.s[j] = 0.f;
     }
     if (8 * l >= p.rotary_dim) return t;
+    uint4 e[4];
+    int pos[4];
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e[j] = __ldg(reinterpret_cast<const uint4 *>(p.rope) + 4 * l + j);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const uint4 e = __ldg(reinterpret_cast<const uint4 *>(p.rope) + 4 * l + j);
-        const uint64_t turns = (uint64_t)e.y << 32 | e.x;
-        if (e.z >= (uint32_t)p.n_axes) {
-            report_status(p.status, kStatusDeviceBounds, kSiteRopeAxis);
-            continue;
-        }
-        const int pos = p.positions ? __ldg(p.positions + (int64_t)e.z * pos_stride + token) : pos0;
-        const uint64_t frac = (uint64_t)(int64_t)pos * turns;
-        // half turns in [-1, 1): the signed upper word over 2^31
-        sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &t.s[j], &t.c[j]);
+        const bool known = e[j].z < (uint32_t)p.n_axes;
+        bad = bad || !known;
+        pos[j] = p.positions && known ? __ldg(p.positions + (int64_t)e[j].z * pos_stride + token) : pos0;
+        if (!known) e[j].x = e[j].y = 0;  // not rotated
+    }
+    if (bad) report_status(p.status, kStatusDeviceBounds, kSiteRopeAxis);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        // The upper word of the 64-bit product, of a signed position.
+        uint32_t frac = __umulhi((uint32_t)pos[j], e[j].x) + (uint32_t)pos[j] * e[j].y;
+        if (pos[j] < 0) frac -= e[j].x;
+        sincos_turn(frac, t.s[j], t.c[j]);
     }
     return t;
 }
@@ -106,51 +138,87 @@ __device__ __forceinline__ void store_row(void *row, const LanePieces &lp, const
     }
 }
 
-// Norm (weight row w, or nullptr) and rotation of the lane's eight channels;
-// all 16 lanes of `mask` take part.
+// The lane's pairs (first, second channel) of a row, and back.
 template <bool INTER>
-__device__ __forceinline__ LaneRow norm_rotate(const LaneRow &in, const LaneRow *w, float eps, const LaneTurn &t,
-                                               bool rotates, unsigned mask) {
-    float x[4] = {bf_lo(in.a.x), bf_hi(in.a.x), bf_lo(in.a.y), bf_hi(in.a.y)};
-    float y[4] = {bf_lo(in.b.x), bf_hi(in.b.x), bf_lo(in.b.y), bf_hi(in.b.y)};
-    if (w) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(mask, ss, off, 16);
-        const float inv = 1.f / sqrtf(fmaf(ss, 1.f / 128.f, eps));
-        const float wa[4] = {bf_lo(w->a.x), bf_hi(w->a.x), bf_lo(w->a.y), bf_hi(w->a.y)};
-        const float wb[4] = {bf_lo(w->b.x), bf_hi(w->b.x), bf_lo(w->b.y), bf_hi(w->b.y)};
+__device__ __forceinline__ void unpack(const LaneRow &r, float (&a)[4], float (&b)[4]) {
+    if (INTER) {
+        const uint32_t w[4] = {r.a.x, r.a.y, r.b.x, r.b.y};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            x[j] = x[j] * inv * wa[j];
-            y[j] = y[j] * inv * wb[j];
+            a[j] = bf_lo(w[j]);
+            b[j] = bf_hi(w[j]);
         }
+    } else {
+        a[0] = bf_lo(r.a.x), a[1] = bf_hi(r.a.x), a[2] = bf_lo(r.a.y), a[3] = bf_hi(r.a.y);
+        b[0] = bf_lo(r.b.x), b[1] = bf_hi(r.b.x), b[2] = bf_lo(r.b.y), b[3] = bf_hi(r.b.y);
+    }
+}
+
+template <bool INTER>
+__device__ __forceinline__ LaneRow pack(const float (&a)[4], const float (&b)[4]) {
+    LaneRow r;
+    if (INTER) {
+        r.a = make_uint2(ptx::pack_bf16x2(a[0], b[0]), ptx::pack_bf16x2(a[1], b[1]));
+        r.b = make_uint2(ptx::pack_bf16x2(a[2], b[2]), ptx::pack_bf16x2(a[3], b[3]));
+    } else {
+        r.a = make_uint2(ptx::pack_bf16x2(a[0], a[1]), ptx::pack_bf16x2(a[2], a[3]));
+        r.b = make_uint2(ptx::pack_bf16x2(b[0], b[1]), ptx::pack_bf16x2(b[2], b[3]));
+    }
+    return r;
+}
+
+// The factors of one tensor's rows at one token: weights times cosines and
+// sines (a lane that does not rotate: the weights).
+struct LaneFactors {
+    float ac[4], bs[4], as[4], bc[4];
+};
+
+template <bool INTER>
+__device__ __forceinline__ LaneFactors lane_factors(const LaneTurn &t, const void *weight, const LanePieces &lp) {
+    float u[4] = {1.f, 1.f, 1.f, 1.f}, w[4] = {1.f, 1.f, 1.f, 1.f};
+    if (weight) unpack<INTER>(load_row<INTER>(weight, lp), u, w);
+    LaneFactors f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f.ac[j] = u[j] * t.c[j];
+        f.bs[j] = w[j] * t.s[j];
+        f.as[j] = u[j] * t.s[j];
+        f.bc[j] = w[j] * t.c[j];
+    }
+    return f;
+}
+
+// Norm (when asked) and rotation of the lane's eight channels; all 16 lanes of
+// `mask` take part.
+template <bool INTER>
+__device__ __forceinline__ LaneRow norm_rotate(const LaneRow &in, bool norm, float eps, const LaneFactors &f,
+                                               bool rotates, unsigned mask) {
+    float a[4], b[4], x[4], y[4];
+    unpack<INTER>(in, a, b);
+    float inv = 1.f;
+    if (norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(mask, ss, off, 16);
+        inv = rsqrtf(fmaf(ss, 1.f / 128.f, eps));
     }
     if (rotates) {
-        if (INTER) {  // pairs 0, 1 in x, pairs 2, 3 in y
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float a = x[2 * j], b = x[2 * j + 1], c = y[2 * j], d = y[2 * j + 1];
-                x[2 * j] = a * t.c[j] - b * t.s[j];
-                x[2 * j + 1] = a * t.s[j] + b * t.c[j];
-                y[2 * j] = c * t.c[2 + j] - d * t.s[2 + j];
-                y[2 * j + 1] = c * t.s[2 + j] + d * t.c[2 + j];
-            }
-        } else {
+        for (int j = 0; j < 4; ++j) {
+            x[j] = (a[j] * f.ac[j] - b[j] * f.bs[j]) * inv;
+            y[j] = (a[j] * f.as[j] + b[j] * f.bc[j]) * inv;
+        }
+    } else {
+        // (not the general form with a sine of zero: infinities stay where they are)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float a = x[j], b = y[j];
-                x[j] = a * t.c[j] - b * t.s[j];
-                y[j] = a * t.s[j] + b * t.c[j];
-            }
+        for (int j = 0; j < 4; ++j) {
+            x[j] = a[j] * f.ac[j] * inv;
+            y[j] = b[j] * f.bc[j] * inv;
         }
     }
-    LaneRow r;
-    r.a = make_uint2(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]));
-    r.b = make_uint2(ptx::pack_bf16x2(y[0], y[1]), ptx::pack_bf16x2(y[2], y[3]));
-    return r;
+    return pack<INTER>(x, y);
 }
 
 }  // namespace attn
