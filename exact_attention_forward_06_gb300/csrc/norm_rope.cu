@@ -29,27 +29,27 @@ struct Chunks {
 };
 
 struct Place {
-    int64_t token;  // this half-warp's token
-    int chunk;      // of the token's chunks, the tensors' one after the other
+    int64_t token;  // this half-warp's token (the last one again for half-warps past it)
+    bool there;     // whether the half-warp has a token of its own
+    int chunk;      // of the token's chunks, the tensors' one after the other: the same in the whole block
     int l;          // lane 0 .. 15
-    unsigned mask;  // the half-warp's lanes
 };
 
 // blockIdx.x: token block x chunk, the chunks of a token block adjacent.
-__device__ __forceinline__ Place place(int chunks) {
+__device__ __forceinline__ Place place(int chunks, int64_t tokens) {
     Place p;
     const unsigned tb = blockIdx.x / (unsigned)chunks;
-    p.token = (int64_t)tb * HALVES + (threadIdx.x >> 4);
+    const int64_t t = (int64_t)tb * HALVES + (threadIdx.x >> 4);
+    p.there = t < tokens;
+    p.token = p.there ? t : tokens - 1;
     p.chunk = (int)(blockIdx.x - tb * (unsigned)chunks);
     p.l = threadIdx.x & 15;
-    p.mask = 0xffffu << (threadIdx.x & 16);
     return p;
 }
 
 template <bool INTER, int U>
 __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormRopeParams p, Chunks cq, Chunks ck) {
-    const Place at = place(cq.chunks + ck.chunks);
-    if (at.token >= (int64_t)p.B * p.S) return;
+    const Place at = place(cq.chunks + ck.chunks, (int64_t)p.B * p.S);
     const int b = (int)(at.token / p.S), s = (int)(at.token - (int64_t)b * p.S);
     const LanePieces lp = lane_pieces<INTER>(at.l, p.r.rotary_dim);
     const bool is_q = at.chunk < cq.chunks;
@@ -73,42 +73,45 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormRopeParams
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if (u >= n) break;
-        const LaneRow y = norm_rotate<INTER>(x[u], weight != nullptr, p.r.eps, f, lp.rotates, at.mask);
-        store_row<INTER>(out + u * out_step, lp, y);
+        const LaneRow y = norm_rotate<INTER>(x[u], weight != nullptr, p.r.eps, f, lp.rotates);
+        if (at.there) store_row<INTER>(out + u * out_step, lp, y);
     }
 }
 
 // Where a new token goes: its sequence's position for it, and its page (-1: a
 // bad table entry, already reported).  Returns false when the token belongs to
-// no sequence or its sequence is malformed (reported).
+// no sequence or its sequence is malformed (reported).  The whole warp takes part.
 __device__ __forceinline__ bool locate(const AppendParams &p, const Place &at, int *slot, int64_t *page) {
     const int t = (int)at.token;
     int b = t, begin = t, end = t + 1;
+    bool ok = true;
+    *slot = 0;
+    *page = -1;
     if (p.cu) {
         // The last b with cu[b] <= t, by 16 probes a round.
-        int lo = 0, hi = p.B;
-        while (hi - lo > 1) {
-            const int step = (hi - lo + 15) >> 4;
+        int lo = 0;
+        for (int len = p.B; len > 1;) {
+            const int step = (len + 15) >> 4;
             const int i = lo + (at.l + 1) * step;
-            const bool le = i < hi && __ldg(p.cu + i) <= t;
-            const int n = __popc(__ballot_sync(at.mask, le) & at.mask);
-            lo += n * step;
-            hi = min(hi, lo + step);
+            const bool le = (at.l + 1) * step < len && i < p.B && __ldg(p.cu + i) <= t;
+            const unsigned votes = __ballot_sync(0xffffffffu, le) >> (threadIdx.x & 16);
+            lo += __popc(votes & 0xffffu) * step;
+            len = step;
         }
         b = lo;
         begin = __ldg(p.cu + b);
         end = __ldg(p.cu + b + 1);
         if (t < begin || t >= end) {
+            ok = false;
             // Before the first or behind the last sequence: nobody's row.
             const bool nobody = t < __ldg(p.cu) || t >= __ldg(p.cu + p.B);
             if (!nobody && at.l == 0) report_status(p.r.status, kStatusDeviceBounds, kSiteAppendOffsets);
-            return false;
-        }
-        if (begin < 0 || end > p.total) {
+        } else if (begin < 0 || end > p.total) {
+            ok = false;
             if (at.l == 0) report_status(p.r.status, kStatusDeviceBounds, kSiteAppendOffsets);
-            return false;
         }
     }
+    if (!ok) return false;
     const int L = __ldg(p.seqlens + b);
     if (L < end - begin || L > p.max_blocks * 16) {
         if (at.l == 0) report_status(p.r.status, kStatusDeviceBounds, kSiteAppendSlot);
@@ -116,45 +119,52 @@ __device__ __forceinline__ bool locate(const AppendParams &p, const Place &at, i
     }
     *slot = L - (end - t);
     const int pg = __ldg(p.block_table + (int64_t)b * p.max_blocks + *slot / 16);
-    const bool ok = pg >= 0 && pg < p.num_pages;
-    if (!ok && at.l == 0) report_status(p.r.status, kStatusDeviceBounds, kSiteAppendSlot);
-    *page = ok ? pg : -1;
+    if (pg >= 0 && pg < p.num_pages)
+        *page = pg;
+    else if (at.l == 0)
+        report_status(p.r.status, kStatusDeviceBounds, kSiteAppendSlot);
     return true;
 }
 
-// Eight consecutive channels 8 l .. 8 l + 7 of a row, as held for quantising.
-__device__ __forceinline__ void quantise_store(uint8_t *block, int t, bool is_v, int l, uint4 v, unsigned mask) {
-    float x[8] = {bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y), bf_lo(v.z), bf_hi(v.z), bf_lo(v.w), bf_hi(v.w)};
-    float hi = x[0], lo = x[0];
-    bool finite = true;
+// Quantises a head row, eight consecutive channels 8 l .. 8 l + 7 a lane, into token
+// t's place in its block (when `there`; the whole warp takes part).
+__device__ __forceinline__ void quantise_store(uint8_t *block, int t, bool is_v, int l, uint4 v, bool there) {
+    constexpr unsigned mask = 0xffffffffu;
+    const float x[8] = {bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y), bf_lo(v.z), bf_hi(v.z), bf_lo(v.w), bf_hi(v.w)};
+    float hi = x[0], lo = x[0], zero = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         hi = fmaxf(hi, x[j]);
         lo = fminf(lo, x[j]);
-        finite = finite && fabsf(x[j]) < INFINITY;  // false for NaN
+        zero = fmaf(x[j], 0.f, zero);  // 0, or NaN when a member is not finite
     }
     // A group is 32 channels: four lanes.
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
         hi = fmaxf(hi, __shfl_xor_sync(mask, hi, off, 16));
         lo = fminf(lo, __shfl_xor_sync(mask, lo, off, 16));
-        finite = __shfl_xor_sync(mask, finite ? 1 : 0, off, 16) && finite;
+        zero += __shfl_xor_sync(mask, zero, off, 16);
     }
-    const q4::GroupScale gs = q4::group_scale(hi, lo, finite);
-    uint32_t word = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) word |= q4::code_of(x[j], gs) << (4 * j);
+    const q4::GroupScale gs = q4::group_scale(hi, lo, zero == 0.f);
+    const uint32_t word = q4::code_word(x, gs);
     const int g = l >> 2;
     if (!is_v) {
+        if (!there) return;
         *reinterpret_cast<uint32_t *>(block + q4::k_word(t, l)) = word;
         if ((l & 3) == 0) {
             *reinterpret_cast<uint16_t *>(block + q4::K_SCALES + t * 8 + g * 2) = gs.s;
             *reinterpret_cast<uint16_t *>(block + q4::K_CENTERS + t * 8 + g * 2) = gs.z;
         }
     } else {
-        const int r = 2 * (l & 3);
-        *reinterpret_cast<uint16_t *>(block + q4::v_half(t, g, r)) = (uint16_t)word;
-        *reinterpret_cast<uint16_t *>(block + q4::v_half(t, g, r + 1)) = (uint16_t)(word >> 16);
+        // The word's halves are r = 2 (l % 4) and the next of group g.  Two exchanges
+        // bring the four groups of one r together: lanes of even g take the even
+        // r, those of odd g the odd one; then g = 0, 1 hold all eight bytes.
+        const uint32_t w1 = __shfl_xor_sync(mask, word, 4, 16);
+        const uint32_t two = g & 1 ? __byte_perm(w1, word, 0x7632) : __byte_perm(word, w1, 0x5410);
+        const uint32_t rest = __shfl_xor_sync(mask, two, 8, 16);
+        if (!there) return;
+        if (g < 2)
+            *reinterpret_cast<uint2 *>(block + q4::v_half(t, 0, 2 * (l & 3) + g)) = make_uint2(two, rest);
         if ((l & 3) == 0) {
             *reinterpret_cast<uint16_t *>(block + q4::V_SCALES + t * 8 + g * 2) = gs.s;
             *reinterpret_cast<uint16_t *>(block + q4::V_CENTERS + g * 32 + t * 2) = gs.z;
@@ -167,8 +177,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p, C
     // Q4: the lane layout of a rotated row goes to eight consecutive channels
     // a lane through shared memory, one row per half-warp.
     __shared__ __align__(16) uint16_t turn_row[Q4 && !INTER ? HALVES : 1][Q4 && !INTER ? D : 8];
-    const Place at = place(cq.chunks + 2 * ckv.chunks);
-    if (at.token >= p.total) return;
+    const Place at = place(cq.chunks + 2 * ckv.chunks, p.total);
     const bool is_q = at.chunk < cq.chunks, is_v = at.chunk >= cq.chunks + ckv.chunks;
     const Chunks c = is_q ? cq : ckv;
     const int H = is_q ? p.Hq : p.Hkv;
@@ -186,11 +195,12 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p, C
         if (u < n) x[u] = load_row<INTER>(in + u * D, lp);
     int slot = 0;
     int64_t page = -1;
-    if (!locate(p, at, &slot, &page)) return;
+    const bool owned = locate(p, at, &slot, &page) && at.there;
     const void *weight = is_q ? p.r.q_weight : is_v ? nullptr : p.r.k_weight;
     LaneFactors f;
     if (!is_v) f = lane_factors<INTER>(lane_turn(p.r, at.l, at.token, p.total, slot), weight, lp);
-    if (!is_q && page < 0) return;
+    const bool there = owned && (is_q || page >= 0);
+    if (page < 0) page = 0;  // (nothing is written there)
     uint16_t *out = is_q ? static_cast<uint16_t *>(p.q_out) + (at.token * p.Hq + h0) * D
                          : static_cast<uint16_t *>(is_v ? p.v_pages : p.k_pages) +
                                ((page * 16 + (slot & 15)) * p.Hkv + h0) * D;
@@ -199,20 +209,20 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p, C
     for (int u = 0; u < U; ++u) {
         if (u >= n) break;
         LaneRow y = x[u];
-        if (!is_v) y = norm_rotate<INTER>(x[u], weight != nullptr, p.r.eps, f, lp.rotates, at.mask);
+        if (!is_v) y = norm_rotate<INTER>(x[u], weight != nullptr, p.r.eps, f, lp.rotates);
         if (is_q || !Q4) {
-            store_row<INTER>(out + u * D, lp, y);
+            if (there) store_row<INTER>(out + u * D, lp, y);
             continue;
         }
         uint4 v = make_uint4(y.a.x, y.a.y, y.b.x, y.b.y);
         if (!INTER && !is_v) {
             uint16_t *mine = turn_row[threadIdx.x >> 4];
-            __syncwarp(at.mask);  // the row before has been read
+            __syncwarp();  // the row before has been read
             store_row<false>(mine, lp, y);
-            __syncwarp(at.mask);
+            __syncwarp();
             v = *reinterpret_cast<const uint4 *>(mine + 8 * at.l);
         }
-        quantise_store(block + (int64_t)u * q4::BLOCK, slot & 15, is_v, at.l, v, at.mask);
+        quantise_store(block + (int64_t)u * q4::BLOCK, slot & 15, is_v, at.l, v, there);
     }
 }
 

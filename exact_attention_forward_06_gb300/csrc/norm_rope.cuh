@@ -188,11 +188,12 @@ __device__ __forceinline__ LaneFactors lane_factors(const LaneTurn &t, const voi
     return f;
 }
 
-// Norm (when asked) and rotation of the lane's eight channels; all 16 lanes of
-// `mask` take part.
+// Norm (when asked) and rotation of the lane's eight channels; the whole warp
+// takes part (a mask of the half-warp's lanes, known only at run time, costs every
+// shuffle a dozen instructions).
 template <bool INTER>
 __device__ __forceinline__ LaneRow norm_rotate(const LaneRow &in, bool norm, float eps, const LaneFactors &f,
-                                               bool rotates, unsigned mask) {
+                                               bool rotates) {
     float a[4], b[4], x[4], y[4];
     unpack<INTER>(in, a, b);
     float inv = 1.f;
@@ -201,7 +202,7 @@ __device__ __forceinline__ LaneRow norm_rotate(const LaneRow &in, bool norm, flo
 #pragma unroll
         for (int j = 0; j < 4; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
 #pragma unroll
-        for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(mask, ss, off, 16);
+        for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off, 16);
         inv = rsqrtf(fmaf(ss, 1.f / 128.f, eps));
     }
     if (rotates) {

@@ -41,13 +41,40 @@ __device__ __forceinline__ GroupScale group_scale(float hi, float lo, bool finit
     return GroupScale{(uint16_t)z, (uint16_t)s};
 }
 
-// The code of x.  A true division: the definition's rounding, not that of a
-// multiplication by a reciprocal.
-__device__ __forceinline__ uint32_t code_of(float x, GroupScale gs) {
-    const float s = __uint_as_float((uint32_t)gs.s << 16);
+// The codes of eight channels of one group as a word (channel j in bits 4 j ..).
+// The definition's quotient (x - z) / s is a true division, and ties are common
+// (x is z plus a whole number of steps for about one bf16 value in 150), so its
+// rounding matters.  Within the range where nothing over- or underflows it comes
+// from Markstein's correction: with r = 1/s correctly rounded, q = d r and the
+// exact remainder d - q s (one fused operation), q + remainder * r is the
+// correctly rounded quotient (s has eight significant bits, so the theorem's
+// exception, a divisor of all ones, does not arise).
+__device__ __forceinline__ uint32_t code_word(const float (&x)[8], GroupScale gs) {
+    const float z = __uint_as_float((uint32_t)gs.z << 16), s = __uint_as_float((uint32_t)gs.s << 16);
     if (!(s > 0.f)) return 0;
-    const float t = __fadd_rn(__fdiv_rn(__fsub_rn(x, __uint_as_float((uint32_t)gs.z << 16)), s), 7.5f);
-    return (uint32_t)fminf(fmaxf(rintf(t), 0.f), 15.f);
+    constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, in the low bits
+    uint32_t word = 0;
+    if (s > 7.8886090522101181e-31f && s < 1.2676506002282294e30f) {  // 2^-100, 2^100
+        const float r = __frcp_rn(s);
+#pragma unroll
+        for (int j = 7; j >= 0; --j) {
+            const float d = __fsub_rn(x[j], z);
+            const float q = __fmul_rn(d, r);
+            const float t = __fadd_rn(__fmaf_rn(__fmaf_rn(-q, s, d), r, q), 7.5f);
+            word = word * 16 + (__float_as_uint(__fadd_rn(fminf(fmaxf(t, 0.f), 15.f), MAGIC)) - 0x4B400000u);
+        }
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+            float d = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i == j) d = __fsub_rn(x[i], z);
+            const float t = __fadd_rn(__fdiv_rn(d, s), 7.5f);
+            word |= (__float_as_uint(__fadd_rn(fminf(fmaxf(t, 0.f), 15.f), MAGIC)) - 0x4B400000u) << (4 * j);
+        }
+    }
+    return word;
 }
 
 }  // namespace q4
