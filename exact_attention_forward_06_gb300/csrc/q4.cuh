@@ -25,14 +25,21 @@ __host__ __device__ constexpr int v_half(int t, int g, int r) {
     return V_CODES + r * 128 + ((t & 7) >> 1) * 32 + (((t >> 3) ^ (r & 1)) << 4) + (t & 1) * 8 + g * 2;
 }
 
+// Largest of two bf16 pairs, half by half; NaN if either is.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Center and scale (bf16 bits) of a group with largest member hi and smallest
-// lo, all bf16 values; `finite` says whether every member is finite.
+// lo (either not finite: some member is not).
 struct GroupScale {
     uint16_t z, s;
 };
 
-__device__ __forceinline__ GroupScale group_scale(float hi, float lo, bool finite) {
-    if (!finite) return GroupScale{0x7fff, 0x7fff};
+__device__ __forceinline__ GroupScale group_scale(float hi, float lo) {
+    if (!(fabsf(hi) < INFINITY && fabsf(lo) < INFINITY)) return GroupScale{0x7fff, 0x7fff};
     const float mid = __fadd_rn(__fmul_rn(0.5f, hi), __fmul_rn(0.5f, lo));
     const uint32_t z = ptx::pack_bf16x2(mid, 0.f) & 0xffffu;
     const float zf = __uint_as_float(z << 16);
@@ -48,7 +55,9 @@ __device__ __forceinline__ GroupScale group_scale(float hi, float lo, bool finit
 // from Markstein's correction: with r = 1/s correctly rounded, q = d r and the
 // exact remainder d - q s (one fused operation), q + remainder * r is the
 // correctly rounded quotient (s has eight significant bits, so the theorem's
-// exception, a divisor of all ones, does not arise).
+// exception, a divisor of all ones, does not arise).  There the definition's clamp
+// has nothing to do either: s is within 2^-9 of (largest |x - z|) * 2 / 15, so the
+// sum lies within 0.02 of 0 .. 15.
 __device__ __forceinline__ uint32_t code_word(const float (&x)[8], GroupScale gs) {
     const float z = __uint_as_float((uint32_t)gs.z << 16), s = __uint_as_float((uint32_t)gs.s << 16);
     if (!(s > 0.f)) return 0;
@@ -61,7 +70,7 @@ __device__ __forceinline__ uint32_t code_word(const float (&x)[8], GroupScale gs
             const float d = __fsub_rn(x[j], z);
             const float q = __fmul_rn(d, r);
             const float t = __fadd_rn(__fmaf_rn(__fmaf_rn(-q, s, d), r, q), 7.5f);
-            word = word * 16 + (__float_as_uint(__fadd_rn(fminf(fmaxf(t, 0.f), 15.f), MAGIC)) - 0x4B400000u);
+            word = word * 16 + (__float_as_uint(__fadd_rn(t, MAGIC)) - 0x4B400000u);
         }
     } else {
 #pragma unroll 1
