@@ -185,10 +185,14 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const AppendParams p
                          : is_v ? static_cast<const uint16_t *>(p.v) + at.token * p.v_stride
                                 : static_cast<const uint16_t *>(p.k) + at.token * p.k_stride;
     in += h0 * D;
+    // Rows that are quantised go through a rolled loop, the next two rows' loads in
+    // flight: unrolled, their code is eight times as long and spills.
+    constexpr int AHEAD = 2;
+    const bool rolled = Q4 && !is_q;
     LaneRow x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        if (u < n) x[u] = load_row<INTER>(in + u * D, lp);
+        if (u < n && (u < AHEAD || !rolled)) x[u] = load_row<INTER>(in + u * D, lp);
     int slot = 0;
     int64_t page = -1;
     const bool owned = locate(p, at, &slot, &page) && at.there;
@@ -197,28 +201,37 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const AppendParams p
     if (!is_v) f = lane_factors<INTER>(lane_turn(p.r, at.l, at.token, p.total, slot), weight, lp);
     const bool there = owned && (is_q || page >= 0);
     if (page < 0) page = 0;  // (nothing is written there)
+    if (rolled) {
+        uint8_t *block = static_cast<uint8_t *>(p.cache) + (page * p.Hkv + h0) * q4::BLOCK;
+        LaneRow now = x[0], next = x[1];
+#pragma unroll 1
+        for (int u = 0; u < n; ++u) {
+            LaneRow y = now;
+            now = next;
+            if (u + AHEAD < n) next = load_row<INTER>(in + (u + AHEAD) * D, lp);
+            if (!is_v) y = norm_rotate<INTER>(y, weight != nullptr, p.r.eps, f, lp.rotates);
+            uint4 v = make_uint4(y.a.x, y.a.y, y.b.x, y.b.y);
+            if (!INTER && !is_v) {
+                uint16_t *mine = turn_row[threadIdx.x >> 4];
+                __syncwarp();  // the row before has been read
+                store_row<false>(mine, lp, y);
+                __syncwarp();
+                v = *reinterpret_cast<const uint4 *>(mine + 8 * at.l);
+            }
+            quantise_store(block, slot & 15, is_v, at.l, v, there);
+            block += q4::BLOCK;
+        }
+        return;
+    }
     uint16_t *out = is_q ? static_cast<uint16_t *>(p.q_out) + (at.token * p.Hq + h0) * D
                          : static_cast<uint16_t *>(is_v ? p.v_pages : p.k_pages) +
                                ((page * 16 + (slot & 15)) * p.Hkv + h0) * D;
-    uint8_t *block = static_cast<uint8_t *>(p.cache) + (page * p.Hkv + h0) * q4::BLOCK;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if (u >= n) break;
         LaneRow y = x[u];
         if (!is_v) y = norm_rotate<INTER>(x[u], weight != nullptr, p.r.eps, f, lp.rotates);
-        if (is_q || !Q4) {
-            if (there) store_row<INTER>(out + u * D, lp, y);
-            continue;
-        }
-        uint4 v = make_uint4(y.a.x, y.a.y, y.b.x, y.b.y);
-        if (!INTER && !is_v) {
-            uint16_t *mine = turn_row[threadIdx.x >> 4];
-            __syncwarp();  // the row before has been read
-            store_row<false>(mine, lp, y);
-            __syncwarp();
-            v = *reinterpret_cast<const uint4 *>(mine + 8 * at.l);
-        }
-        quantise_store(block + (int64_t)u * q4::BLOCK, slot & 15, is_v, at.l, v, there);
+        if (there) store_row<INTER>(out + u * D, lp, y);
     }
 }
 
