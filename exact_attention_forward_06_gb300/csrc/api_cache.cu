@@ -192,7 +192,7 @@ attn_status_t attn_gather_paged_q4(const void *cache, const int32_t *block_table
     attn_status_t st = check_table(block_table, seqlens, B, Hkv, d, page_size, num_pages, max_blocks_per_seq);
     if (st != ATTN_OK) return st;
     if (((int64_t)total_k / 16 + B) * Hkv > 0x7fffffff) return ATTN_ERR_INVALID_ARG;
-    attn::GatherQ4Params p = {cache, block_table, seqlens, cu_seqlens_k, k_out, v_out,
+    attn::GatherQ4Params p = {cache, block_table, seqlens, cu_seqlens_k, nullptr, k_out, v_out,
                               B, Hkv, total_k, num_pages, max_blocks_per_seq, nullptr};
     int sms;
     uint64_t budget;
@@ -246,8 +246,8 @@ attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32
 
 size_t attn_fwd_paged_q4_workspace_bytes(int B, int Hkv, int d, int max_total_k) {
     if (B < 1 || Hkv < 1 || d != 128 || max_total_k < 1) return 0;
-    // offsets [B + 1] and lengths [B] int32, then k and v [max_total_k][Hkv][d] bf16.
-    return align256(((size_t)2 * B + 1) * 4) + 2 * align256((size_t)max_total_k * Hkv * d * 2);
+    // offsets [B + 1] int32, then k and v [max_total_k][Hkv][d] bf16.
+    return align256(((size_t)B + 1) * 4) + 2 * align256((size_t)max_total_k * Hkv * d * 2);
 }
 
 attn_status_t attn_fwd_paged_q4(const void *q, const void *cache, const int32_t *block_table,
@@ -277,12 +277,10 @@ attn_status_t attn_fwd_paged_q4(const void *q, const void *cache, const int32_t 
     if ((st = attn::device_state(&sms, &status, &budget)) != ATTN_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    int32_t *cu_k = reinterpret_cast<int32_t *>(ws), *lens = cu_k + B + 1;
-    uint8_t *k = ws + align256(((size_t)2 * B + 1) * 4);
+    int32_t *cu_k = reinterpret_cast<int32_t *>(ws);
+    uint8_t *k = ws + align256(((size_t)B + 1) * 4);
     uint8_t *v = k + align256((size_t)max_total_k * Hkv * d * 2);
-    if (attn::launch_q4_offsets(seqlens_k, cu_k, lens, B, max_blocks_per_seq, max_total_k, status, s) != cudaSuccess)
-        return ATTN_ERR_CUDA;
-    const attn::GatherQ4Params g = {cache, block_table, lens, cu_k, k, v,
+    const attn::GatherQ4Params g = {cache, block_table, seqlens_k, nullptr, cu_k, k, v,
                                     B, Hkv, max_total_k, num_pages, max_blocks_per_seq, status};
     if (attn::launch_gather_q4(g, s) != cudaSuccess) return ATTN_ERR_CUDA;
     const int64_t longest = (int64_t)max_blocks_per_seq * 16;

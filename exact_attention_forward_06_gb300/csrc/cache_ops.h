@@ -45,7 +45,9 @@ struct AppendParams {
 
 struct GatherQ4Params {
     const void *cache;
-    const int32_t *block_table, *seqlens, *cu_k;
+    const int32_t *block_table, *seqlens;
+    const int32_t *cu_k;  // offsets, or nullptr: made from seqlens and written to
+    int32_t *cu_out;      // [B + 1]
     void *k_out, *v_out;
     int B, Hkv, total_k, num_pages, max_blocks;
     unsigned *status;
@@ -70,10 +72,6 @@ struct DecodeQ4Params {
 cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_gather_q4(const GatherQ4Params &p, cudaStream_t stream);
-// cu_k[0 .. B] from seqlens; a length outside [0, 16 max_blocks], or one that
-// takes the sum past max_total, counts as 0 and is reported.
-cudaError_t launch_q4_offsets(const int32_t *seqlens, int32_t *cu_k, int32_t *lens_out, int B, int max_blocks,
-                              int max_total, unsigned *status, cudaStream_t stream);
 // CTAs at most, a pure function of the shape: the workspace's size goes by it.
 int decode_q4_max_ctas(int B, int Hq, int Hkv, int max_blocks);
 cudaError_t launch_decode_q4(const DecodeQ4Params &p, int sm_count, cudaStream_t stream);

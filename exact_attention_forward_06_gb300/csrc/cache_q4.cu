@@ -1,5 +1,5 @@
 // cache_q4.cu -- reading a 4-bit cache: attn_gather_paged_q4 (back to packed
-// bf16 keys and values) and the offsets of attn_fwd_paged_q4.
+// bf16 keys and values), with given offsets or (for attn_fwd_paged_q4) its own.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -31,17 +31,14 @@ __device__ __forceinline__ uint4 unpack_word(uint32_t word, float s, float z) {
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// One warp per page and KV head.  Item j of total_k / 16 + B candidate pages
-// belongs to the last sequence b with cu_k[b] / 16 + b <= j, as its page
-// j - (cu_k[b] / 16 + b): every sequence of L tokens gets at least ceil(L / 16)
-// candidates whatever the other lengths, without a sum over the sequences.
-__global__ void __launch_bounds__(GWARPS * 32) gather_kernel(const GatherQ4Params p) {
-    __shared__ __align__(16) uint8_t stage[GWARPS][BLOCK];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t item = (int64_t)blockIdx.x * GWARPS + warp;
-    const int h = (int)(item % p.Hkv);
-    const int64_t j = item / p.Hkv;
-    if (j >= (int64_t)p.total_k / PAGE + p.B) return;
+// Where a warp's item lies: its sequence, the sequence's first row and length.
+struct Found {
+    int b, begin, L;
+    bool ok;
+};
+
+// The last sequence b with cu_k[b] / 16 + b <= j, from given offsets.
+__device__ __forceinline__ Found find_given(const GatherQ4Params &p, int64_t j, int lane) {
     int lo = 0, hi = p.B;
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) >> 5;
@@ -50,13 +47,117 @@ __global__ void __launch_bounds__(GWARPS * 32) gather_kernel(const GatherQ4Param
         lo += __popc(__ballot_sync(0xffffffffu, le)) * step;
         hi = min(hi, lo + step);
     }
-    const int begin = __ldg(p.cu_k + lo), end = __ldg(p.cu_k + lo + 1);
-    const int L = __ldg(p.seqlens + lo);
-    const int64_t first = (int64_t)begin / PAGE + lo;
-    if (begin < 0 || end > p.total_k || L != end - begin || L < 0 || L > p.max_blocks * PAGE) {
-        if (lane == 0) report_status(p.status, kStatusDeviceBounds, kSiteQ4Offsets);
+    const int begin = __ldg(p.cu_k + lo), end = __ldg(p.cu_k + lo + 1), L = __ldg(p.seqlens + lo);
+    const bool ok = begin >= 0 && end <= p.total_k && L == end - begin && L >= 0 && L <= p.max_blocks * PAGE;
+    return Found{lo, begin, L, ok};
+}
+
+__device__ __forceinline__ int length_of(const GatherQ4Params &p, int b) {
+    const int L = __ldg(p.seqlens + b);
+    return L < 0 || L > p.max_blocks * PAGE ? 0 : L;
+}
+
+// The same from the lengths alone, for offsets that begin at 0 and leave no gaps:
+// a thread sums a run of sequences, the sums are scanned, and the warp looks for
+// its item among the runs and then within one.  A length outside the table counts
+// as 0; the sequences that go past total_k come last and are left out.  Block 0
+// writes the offsets, and reports.
+struct RunSums {
+    int64_t start[GWARPS * 32];
+    int64_t warp_sum[GWARPS];
+    int last;
+};
+
+__device__ __forceinline__ Found find_own(const GatherQ4Params &p, int64_t j, int lane, RunSums &runs) {
+    constexpr int THREADS = GWARPS * 32;
+    const int per = (p.B + THREADS - 1) / THREADS;
+    const int b_lo = min(p.B, (int)threadIdx.x * per), b_hi = min(p.B, b_lo + per);
+    int64_t mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += length_of(p, b);
+    int64_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+    }
+    const int warp = threadIdx.x >> 5;
+    if (lane == 31) runs.warp_sum[warp] = incl;
+    if (threadIdx.x == 0) runs.last = 0;
+    __syncthreads();
+    int64_t before = incl - mine;
+    for (int w = 0; w < warp; ++w) before += runs.warp_sum[w];
+    runs.start[threadIdx.x] = before;
+    if (blockIdx.x == 0) {
+        int64_t end = before;
+        int last = 0;  // the largest offset within the bound
+        for (int b = b_lo; b < b_hi; ++b) {
+            const int L = length_of(p, b);
+            end += L;
+            if (end <= p.total_k) last = (int)end;
+            if (L != __ldg(p.seqlens + b) || (end > p.total_k && L > 0))
+                report_status(p.status, kStatusDeviceBounds, kSiteQ4Offsets);
+        }
+        atomicMax(&runs.last, last);
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        int64_t end = before;
+        if (threadIdx.x == 0) p.cu_out[0] = 0;
+        for (int b = b_lo; b < b_hi; ++b) {
+            end += length_of(p, b);
+            p.cu_out[b + 1] = (int)min(end, (int64_t)runs.last);
+        }
+    }
+    int n = 0;
+    for (int r = lane; r < THREADS; r += 32)
+        n += __popc(__ballot_sync(0xffffffffu, r * per < p.B && runs.start[r] / PAGE + r * per <= j));
+    int b = (n - 1) * per;
+    int64_t begin = runs.start[n - 1];
+    Found f{b, 0, 0, false};
+    for (int c = 0; c < per; c += 32) {
+        const bool in = c + lane < per && b + c + lane < p.B;
+        const int L = in ? length_of(p, b + c + lane) : 0;
+        int64_t end = L;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, end, off);
+            if (lane >= off) end += o;
+        }
+        const int64_t at = begin + end - L;
+        const int k = __popc(__ballot_sync(0xffffffffu, in && at / PAGE + b + c + lane <= j));
+        if (k == 0) break;
+        f.b = b + c + k - 1;
+        f.L = __shfl_sync(0xffffffffu, L, k - 1);
+        const int64_t first = __shfl_sync(0xffffffffu, at, k - 1);
+        f.ok = first + f.L <= p.total_k;
+        f.begin = f.ok ? (int)first : 0;
+        if (k < 32) break;
+        begin += __shfl_sync(0xffffffffu, end, 31);
+    }
+    return f;
+}
+
+// One warp per page and KV head.  Item j of total_k / 16 + B candidate pages
+// belongs to the last sequence b with cu_k[b] / 16 + b <= j, as its page
+// j - (cu_k[b] / 16 + b): every sequence of L tokens gets at least ceil(L / 16)
+// candidates whatever the other lengths, without a sum over the sequences'
+// pages.  OWN: the offsets come from the lengths.
+template <bool OWN>
+__global__ void __launch_bounds__(GWARPS * 32) gather_kernel(const GatherQ4Params p) {
+    __shared__ __align__(16) uint8_t stage[GWARPS][BLOCK];
+    __shared__ RunSums runs[1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t item = (int64_t)blockIdx.x * GWARPS + warp;
+    const int h = (int)(item % p.Hkv);
+    const int64_t j = item / p.Hkv;
+    const Found f = OWN ? find_own(p, j, lane, runs[0]) : find_given(p, j, lane);
+    if (j >= (int64_t)p.total_k / PAGE + p.B) return;
+    if (!f.ok) {
+        if (!OWN && lane == 0) report_status(p.status, kStatusDeviceBounds, kSiteQ4Offsets);
         return;
     }
+    const int lo = f.b, begin = f.begin, L = f.L;
+    const int64_t first = (int64_t)begin / PAGE + lo;
     const int64_t t0 = (j - first) * PAGE;
     if (j < first || t0 >= L) return;
     const int page = __ldg(p.block_table + (int64_t)lo * p.max_blocks + (j - first));
@@ -85,68 +186,16 @@ __global__ void __launch_bounds__(GWARPS * 32) gather_kernel(const GatherQ4Param
     }
 }
 
-// One CTA: offsets of the packed keys from the cache lengths.
-constexpr int OFF_THREADS = 1024;
-__global__ void __launch_bounds__(OFF_THREADS) offsets_kernel(const int32_t *seqlens, int32_t *cu_k,
-                                                              int32_t *lens_out, int B, int max_blocks, int max_total,
-                                                              unsigned *status) {
-    __shared__ int64_t warp_sum[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t base = 0;  // of this round of OFF_THREADS sequences
-    if (threadIdx.x == 0) cu_k[0] = 0;
-    for (int b0 = 0; b0 < B; b0 += OFF_THREADS) {
-        const int b = b0 + threadIdx.x;
-        int L = b < B ? seqlens[b] : 0;
-        bool bad = L < 0 || L > max_blocks * PAGE;
-        if (bad) L = 0;
-        int64_t sum = L;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, sum, off);
-            if (lane >= off) sum += o;
-        }
-        if (lane == 31) warp_sum[warp] = sum;
-        __syncthreads();
-        int64_t before = base, all = base;
-        for (int i = 0; i < 32; ++i) {
-            if (i < warp) before += warp_sum[i];
-            all += warp_sum[i];
-        }
-        // Past the bound: this sequence and those after it count as empty.
-        const int64_t end = before + sum;
-        if (end > max_total && L > 0) {
-            bad = true;
-            L = 0;
-        }
-        if (b < B) {
-            cu_k[b + 1] = (int32_t)(end > max_total ? -1 : end);
-            lens_out[b] = L;
-            if (bad) report_status(status, kStatusDeviceBounds, kSiteQ4Offsets);
-        }
-        base = all;
-        __syncthreads();
-    }
-    __syncthreads();
-    // The offsets past the bound stay at the last one within it.
-    if (base > max_total && threadIdx.x == 0) {
-        for (int b = 0; b < B; ++b)
-            if (cu_k[b + 1] < 0) cu_k[b + 1] = cu_k[b];
-    }
-}
-
 }  // namespace q4
 
 cudaError_t launch_gather_q4(const GatherQ4Params &p, cudaStream_t stream) {
     const int64_t items = ((int64_t)p.total_k / q4::PAGE + p.B) * p.Hkv;
     const int64_t grid = (items + q4::GWARPS - 1) / q4::GWARPS;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    q4::gather_kernel<<<(unsigned)grid, q4::GWARPS * 32, 0, stream>>>(p);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_q4_offsets(const int32_t *seqlens, int32_t *cu_k, int32_t *lens_out, int B, int max_blocks,
-                              int max_total, unsigned *status, cudaStream_t stream) {
-    q4::offsets_kernel<<<1, q4::OFF_THREADS, 0, stream>>>(seqlens, cu_k, lens_out, B, max_blocks, max_total, status);
+    if (p.cu_k)
+        q4::gather_kernel<false><<<(unsigned)grid, q4::GWARPS * 32, 0, stream>>>(p);
+    else
+        q4::gather_kernel<true><<<(unsigned)grid, q4::GWARPS * 32, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
