@@ -69,6 +69,26 @@ struct DecodeQ4Params {
     uint64_t budget_ns;
 };
 
+// Launches a kernel as a programmatic dependent of the work before it on the
+// stream: its blocks may be set up while that work finishes.  Such a kernel
+// begins with ptx::wait_for_prior_work() (griddepcontrol.wait), before it reads
+// or writes anything.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                             Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_gather_q4(const GatherQ4Params &p, cudaStream_t stream);

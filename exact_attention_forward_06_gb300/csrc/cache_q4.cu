@@ -146,6 +146,8 @@ template <bool OWN>
 __global__ void __launch_bounds__(GWARPS * 32) gather_kernel(const GatherQ4Params p) {
     __shared__ __align__(16) uint8_t stage[GWARPS][BLOCK];
     __shared__ RunSums runs[1];
+    ptx::wait_for_prior_work();
+    ptx::allow_next_work();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t item = (int64_t)blockIdx.x * GWARPS + warp;
     const int h = (int)(item % p.Hkv);
@@ -192,11 +194,8 @@ cudaError_t launch_gather_q4(const GatherQ4Params &p, cudaStream_t stream) {
     const int64_t items = ((int64_t)p.total_k / q4::PAGE + p.B) * p.Hkv;
     const int64_t grid = (items + q4::GWARPS - 1) / q4::GWARPS;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    if (p.cu_k)
-        q4::gather_kernel<false><<<(unsigned)grid, q4::GWARPS * 32, 0, stream>>>(p);
-    else
-        q4::gather_kernel<true><<<(unsigned)grid, q4::GWARPS * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(p.cu_k ? q4::gather_kernel<false> : q4::gather_kernel<true>, (unsigned)grid, q4::GWARPS * 32, 0,
+                            stream, p);
 }
 
 }  // namespace attn

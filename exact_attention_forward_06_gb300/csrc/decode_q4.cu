@@ -178,6 +178,7 @@ struct CutRun {
 
 __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Params p, int col_blocks) {
     extern __shared__ __align__(128) uint8_t smem[];
+    ptx::wait_for_prior_work();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r4 = lane >> 2, c4 = lane & 3;
     uint8_t *ring = smem + warp * NST * STAGE;
@@ -642,7 +643,7 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
         }
     }
     if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(cut.row0, cut.cols, cut.parts, 0);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    ptx::allow_next_work();
 }
 
 // Merge of the cut runs: CTA (c, i) does head i of the run that begins in share
@@ -655,7 +656,8 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const DecodeQ4P
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Launched as a programmatic dependent of the share kernel: its partials are
     // visible from here on.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    ptx::wait_for_prior_work();
+    ptx::allow_next_work();
     const int4 cut = p.cuts[blockIdx.x];
     const int c = blockIdx.y, parts = cut.z;
     if (c >= cut.y || parts == 0) return;
@@ -734,20 +736,11 @@ cudaError_t launch_decode_q4(const DecodeQ4Params &p, int sm_count, cudaStream_t
         if (e != cudaSuccess) return e;
         configured_device = dev;
     }
-    dq4::share_kernel<<<grid, dq4::NT, dq4::SMEM, stream>>>(p, col_blocks);
-    e = cudaGetLastError();
+    e = launch_dependent(dq4::share_kernel, grid, dq4::NT, dq4::SMEM, stream, p, col_blocks);
     // One sequence with a share for each KV head is never cut.
     if (e != cudaSuccess || (p.B == 1 && grid / col_blocks == p.Hkv)) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, p.Hq / p.Hkv < dq4::COLS ? p.Hq / p.Hkv : dq4::COLS);
-    cfg.blockDim = dim3(dq4::MERGE_WARPS * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dq4::merge_kernel, p, col_blocks);
+    const int heads = p.Hq / p.Hkv < dq4::COLS ? p.Hq / p.Hkv : dq4::COLS;
+    return launch_dependent(dq4::merge_kernel, dim3(grid, heads), dq4::MERGE_WARPS * 32, 0, stream, p, col_blocks);
 }
 
 }  // namespace attn

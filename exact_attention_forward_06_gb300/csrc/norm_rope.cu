@@ -49,6 +49,8 @@ __device__ __forceinline__ Place place(int chunks, int64_t tokens) {
 
 template <bool INTER, int U>
 __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormRopeParams p, Chunks cq, Chunks ck) {
+    ptx::wait_for_prior_work();
+    ptx::allow_next_work();
     const Place at = place(cq.chunks + ck.chunks, (int64_t)p.B * p.S);
     const int b = (int)(at.token / p.S), s = (int)(at.token - (int64_t)b * p.S);
     const LanePieces lp = lane_pieces<INTER>(at.l, p.r.rotary_dim);
@@ -173,6 +175,8 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const AppendParams p
     // Q4: the lane layout of a rotated row goes to eight consecutive channels
     // a lane through shared memory, one row per half-warp.
     __shared__ __align__(16) uint16_t turn_row[Q4 && !INTER ? HALVES : 1][Q4 && !INTER ? D : 8];
+    ptx::wait_for_prior_work();
+    ptx::allow_next_work();
     const Place at = place(cq.chunks + 2 * ckv.chunks, p.total);
     const bool is_q = at.chunk < cq.chunks, is_v = at.chunk >= cq.chunks + ckv.chunks;
     const Chunks c = is_q ? cq : ckv;
@@ -258,11 +262,8 @@ cudaError_t norm_rope_u(const NormRopeParams &p, cudaStream_t stream) {
     const nr::Chunks cq = chunks_of(p.Hq, U), ck = chunks_of(p.Hkv, U);
     unsigned grid;
     if (!row_grid((int64_t)p.B * p.S, cq.chunks + ck.chunks, &grid)) return cudaErrorInvalidValue;
-    if (p.r.interleaved)
-        nr::norm_rope_kernel<true, U><<<grid, nr::THREADS, 0, stream>>>(p, cq, ck);
-    else
-        nr::norm_rope_kernel<false, U><<<grid, nr::THREADS, 0, stream>>>(p, cq, ck);
-    return cudaGetLastError();
+    if (p.r.interleaved) return launch_dependent(nr::norm_rope_kernel<true, U>, grid, nr::THREADS, 0, stream, p, cq, ck);
+    return launch_dependent(nr::norm_rope_kernel<false, U>, grid, nr::THREADS, 0, stream, p, cq, ck);
 }
 
 template <int U>
@@ -270,18 +271,12 @@ cudaError_t append_u(const AppendParams &p, cudaStream_t stream) {
     const nr::Chunks cq = chunks_of(p.Hq, U), ckv = chunks_of(p.Hkv, U);
     unsigned grid;
     if (!row_grid(p.total, cq.chunks + 2 * ckv.chunks, &grid)) return cudaErrorInvalidValue;
-    if (p.cache) {
-        if (p.r.interleaved)
-            nr::append_kernel<true, true, U><<<grid, nr::THREADS, 0, stream>>>(p, cq, ckv);
-        else
-            nr::append_kernel<false, true, U><<<grid, nr::THREADS, 0, stream>>>(p, cq, ckv);
-    } else {
-        if (p.r.interleaved)
-            nr::append_kernel<true, false, U><<<grid, nr::THREADS, 0, stream>>>(p, cq, ckv);
-        else
-            nr::append_kernel<false, false, U><<<grid, nr::THREADS, 0, stream>>>(p, cq, ckv);
-    }
-    return cudaGetLastError();
+    if (p.cache && p.r.interleaved)
+        return launch_dependent(nr::append_kernel<true, true, U>, grid, nr::THREADS, 0, stream, p, cq, ckv);
+    if (p.cache) return launch_dependent(nr::append_kernel<false, true, U>, grid, nr::THREADS, 0, stream, p, cq, ckv);
+    if (p.r.interleaved)
+        return launch_dependent(nr::append_kernel<true, false, U>, grid, nr::THREADS, 0, stream, p, cq, ckv);
+    return launch_dependent(nr::append_kernel<false, false, U>, grid, nr::THREADS, 0, stream, p, cq, ckv);
 }
 
 }  // namespace

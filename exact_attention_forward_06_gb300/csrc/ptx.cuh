@@ -170,6 +170,15 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
     return p;
 }
 
+// ---------------------------------------------------------------- programmatic dependent launch
+
+// Waits until the grids this one depends on have completed and their writes
+// are visible.
+__device__ __forceinline__ void wait_for_prior_work() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets the next dependent grid be set up (it still waits for this one's end).
+__device__ __forceinline__ void allow_next_work() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- named barriers
 
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
