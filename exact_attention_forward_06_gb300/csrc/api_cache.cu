@@ -203,9 +203,10 @@ attn_status_t attn_gather_paged_q4(const void *cache, const int32_t *block_table
 size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int d, int max_blocks_per_seq) {
     if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d != 128 || max_blocks_per_seq < 1) return 0;
     if ((int64_t)B * ((max_blocks_per_seq + (int64_t)1) / 2) > 0x7fffffff) return 0;
-    // o_part [CTAs][2][8][d] fp32, lse_part [CTAs][2][8] fp32, cuts [CTAs] of 16 bytes, each 256-B aligned.
-    const size_t ctas = (size_t)attn::decode_q4_max_ctas(B, Hq, Hkv, max_blocks_per_seq);
-    return align256(ctas * 16 * d * 4) + align256(ctas * 16 * 4) + align256(ctas * 16);
+    // o_part [rows][d] fp32, lse_part [rows] fp32, cuts [CTAs] of 16 bytes, each 256-B aligned.
+    size_t ctas = 0;
+    const size_t rows = attn::decode_q4_partial_rows(B, Hq, Hkv, max_blocks_per_seq, &ctas);
+    return align256(rows * d * 4) + align256(rows * 4) + align256(ctas * 16);
 }
 
 attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32_t *block_table,
@@ -228,11 +229,12 @@ attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32
     p.seqlens = seqlens;
     p.out = out;
     p.lse = lse;
-    const size_t ctas = (size_t)attn::decode_q4_max_ctas(B, Hq, Hkv, max_blocks_per_seq);
+    size_t ctas = 0;
+    const size_t rows = attn::decode_q4_partial_rows(B, Hq, Hkv, max_blocks_per_seq, &ctas);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.o_part = reinterpret_cast<float *>(ws);
-    p.lse_part = reinterpret_cast<float *>(ws + align256(ctas * 16 * d * 4));
-    p.cuts = reinterpret_cast<int4 *>(ws + align256(ctas * 16 * d * 4) + align256(ctas * 16 * 4));
+    p.lse_part = reinterpret_cast<float *>(ws + align256(rows * d * 4));
+    p.cuts = reinterpret_cast<int4 *>(ws + align256(rows * d * 4) + align256(rows * 4));
     p.B = B;
     p.Hq = Hq;
     p.Hkv = Hkv;

@@ -59,9 +59,9 @@ struct DecodeQ4Params {
     void *out;
     float *lse;
     // Partial results of the shares that cut a sequence, for each CTA its first
-    // and its last segment: normalised outputs and log2-sum-exp2 of 8 heads.
-    float *o_part;    // [CTAs][2][8][d]
-    float *lse_part;  // [CTAs][2][8]
+    // and its last segment: normalised outputs and log2-sum-exp2 of its heads.
+    float *o_part;    // [CTAs][2][heads][d]
+    float *lse_part;  // [CTAs][2][heads]
     int4 *cuts;       // [CTAs]
     int B, Hq, Hkv, num_pages, max_blocks;
     float scale_log2;
@@ -92,8 +92,9 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, s
 cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_gather_q4(const GatherQ4Params &p, cudaStream_t stream);
-// CTAs at most, a pure function of the shape: the workspace's size goes by it.
-int decode_q4_max_ctas(int B, int Hq, int Hkv, int max_blocks);
+// Rows of o_part and lse_part, and CTAs, at most: a pure function of the shape,
+// the workspace's size goes by them.
+size_t decode_q4_partial_rows(int B, int Hq, int Hkv, int max_blocks, size_t *ctas);
 cudaError_t launch_decode_q4(const DecodeQ4Params &p, int sm_count, cudaStream_t stream);
 
 }  // namespace attn

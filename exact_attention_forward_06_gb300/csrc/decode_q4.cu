@@ -2,45 +2,50 @@
 // (attn_decode_paged_q4): a key split and its log-sum-exp merge.
 //
 // A page of one KV head is one 2560-byte block, read once: 4096 codes and 256
-// parameters for 4 flops a code and query head, so HBM bandwidth is the bound
-// as long as a page's arithmetic fits in the time its bytes take (about 110 SM
-// clocks at the measured copy bandwidth).  That budget, about four instructions
-// per eight codes, decides the form:
+// parameters for 4 flops a code and query head.  At the measured copy bandwidth
+// its bytes take about 110 SM clocks, in which the SM's four schedulers issue at
+// most 440 instructions, half of that to the integer pipe, so the arithmetic decides
+// the form as much as the bytes do:
 //
-// - Codes go to the tensor cores without being turned into values.  A code n
+// - Codes go to the tensor cores without being turned into cache values.  A code n
 //   moved to bits 3..6 of a bf16 whose other bits say 16.0 is the number 16 + n
-//   exactly (one shift and one and/or per two codes); the offset to n - 7.5 is
-//   -23.5 and is taken off after the product.
-// - S^T = K Q^T (mma m16n8k16, the page's 16 tokens as rows, up to eight query
-//   heads of the KV head as columns), group by group of 32 channels:
-//       s_t += scale_tg * (sum_c q_c (16 + n_tc) - 23.5 Q_g) + center_tg * Q_g,
-//   Q_g = sum of the group's q.  -23.5 Q_g is the product's initial accumulator;
-//   the centers' term is one product for all groups, with Q_g cut into three
-//   bf16 parts (24 bits).
-// - O^T += V^T P^T: a group's scale goes to the probability, P'_t = P_t scale_tg
-//   (rounded to bf16 as P is); the offset is one product per group with a
-//   constant matrix of -23.5, so it takes off exactly what the rounded P' brought
-//   in; the centers' term is one product with the unscaled P.
+//   exactly: a shift and an and/or for two codes.  (Codes that need no shift to
+//   bits 0..3 become 128 + n.)
+// - S^T = K Q^T (mma m16n8k16, the page's 16 tokens as rows, eight query heads of
+//   the KV head as columns), a product for each group of 32 channels:
+//       s_t += scale_tg * (sum_c q_c (off_c + n_tc) - Off_g) + center_tg * Q_g,
+//   with Q_g the sum of the group's q and Off_g the q's sum weighted with the
+//   offsets to n - 7.5.  Both last terms are two more products for all groups at
+//   once, Q_g and Off_g cut into three bf16 parts (24 bits).
+// - O^T += V^T P^T: value codes become n - 7.5 by one packed addition, and a group's
+//   scale goes to the probability, P'_t = P_t scale_tg, in the operand's layout;
+//   the centers' term is one product with the unscaled P.
 // - The byte order of the block (q4.cuh) is that of the fragments: every lane
 //   reads its operands as 16-byte words without bank conflicts, and a value
 //   pair of two tokens is one byte permutation.
+// - Two pages a step share the wait, the vote on the running max and the loop.
 //
-// The work is cut into equal shares, one for each of three CTAs per SM: the page
-// pairs of all sequences and KV heads in one row, CTA c taking the c-th part of
-// it.  A share is a few segments (a run of one sequence's pages for one KV head);
-// a segment that is a whole sequence is finished by its CTA, the parts of a cut
-// one go to the workspace and are merged by log-sum-exp in the order of the keys.
-// Ragged lengths thus cost nothing: against a grid of fixed splits over the
-// table's width, the same page loop took 177 us instead of SHARED_US on 64
-// sequences of 0 to 16384 tokens.
+// The work is cut into equal shares, one for each CTA that the GPU holds at once:
+// the page pairs of all sequences and KV heads in one row, CTA c taking the c-th
+// part of it.  A share is a few segments (a run of one sequence's pages for one KV
+// head); a segment that is a whole sequence is finished by its CTA, the parts of
+// a cut one go to the workspace and are merged by log-sum-exp in the order of the
+// keys.  Ragged lengths thus cost nothing: with a grid of fixed splits over the
+// table's width the same page loop took 177 us instead of 168.
 //
 // In a segment each warp streams page pairs w, w + 4, .. through a ring of its own
 // (bulk copies issued by its lane 0 as soon as a slot has been read): no producer
 // warp and no barrier between warps until the four partial results meet at the
-// segment's end.  Scores, sums and outputs are fp32; P and P' are rounded to
-// bf16 for the product alone, the row sum adds the fp32 values.
+// segment's end.  Scores, sums and outputs are fp32.  P is rounded to bf16 for its
+// products, and P' once more, each by 2^-9 of itself at most, as in the bf16
+// decode; the row sum adds the fp32 values.
+//
+// Measured on 64 sequences of 0 to 16384 tokens, 64 / 8 heads (758 MB): 154 us,
+// 4.9 TB/s, 0.73 of the copy bandwidth; the copies alone take 124 us, the
+// arithmetic alone 135.  On 32 sequences of 1024 to 8192 tokens, 32 / 8 heads (177
+// MB): 47 us, 0.56; half the MMA columns are empty there, and about 6 us are the
+// two launches' ends.
 #include <cstdint>
-#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "cache_ops.h"
@@ -54,20 +59,29 @@ using q4::BLOCK;
 using q4::D;
 using q4::PAGE;
 
-constexpr int NW = 4;    // warps = page streams, and groups of a head
-constexpr int NST = 3;   // page pairs in flight per warp
-constexpr int COLS = 8;  // query heads per CTA (MMA columns)
+constexpr int NW = 4;  // warps = page streams, and groups of a head
 constexpr int NT = NW * 32;
-constexpr int CTAS_PER_SM = 3;
 constexpr int STAGE = 2 * BLOCK;
-constexpr int RING = NW * NST * STAGE;
-constexpr int EXCHANGE = 36 * 32 * 4;  // one warp's partial result: 36 words a lane
-constexpr int Q_FRAGS = 4 * 32 * 16;   // a lane's query fragments, 16 bytes a group
-constexpr int SMEM = RING + 2 * EXCHANGE + Q_FRAGS + NW * NST * 8 + 64;  // ring, exchange, queries, barriers, words
-static_assert(CTAS_PER_SM * (SMEM + 1024) <= 233472, "CTAs per SM");
+
+// A CTA works for 8 * TILES query heads of a KV head, an MMA column each.  With more
+// heads to a KV head than eight, two tiles share the unpacking of a page, which is
+// two thirds of its instructions, at the price of registers: two CTAs an SM.
+template <int TILES>
+struct Shape {
+    static constexpr int COLS = 8 * TILES;
+    static constexpr int CTAS_PER_SM = TILES == 1 ? 3 : 2;
+    static constexpr int MAX_CTAS = CTAS_PER_SM * 152;   // shares at most: the workspace's size goes by it
+    static constexpr int NST = TILES == 1 ? 3 : 4;       // page pairs in flight per warp
+    static constexpr int RING = NW * NST * STAGE;
+    static constexpr int EXCHANGE = 36 * TILES * 32 * 4;  // one warp's partial result: 36 words a lane and tile
+    static constexpr int Q_FRAGS = 4 * TILES * 32 * 16;   // a lane's query fragments, 16 bytes a group and tile
+    static constexpr int BARRIERS = RING + 2 * EXCHANGE + Q_FRAGS;
+    static constexpr int WORDS = BARRIERS + NW * NST * 8;
+    static constexpr int SMEM = WORDS + 64;
+    static_assert(CTAS_PER_SM * (SMEM + 1024) <= 233472, "CTAs per SM");
+};
 constexpr int MIN_PAIRS = 4;           // pairs a CTA takes at least, unless there is a KV head for each
-constexpr int MAX_CTAS = 3 * 152;      // shares at most: the workspace's size goes by it
-constexpr float RAISE = 8.f;  // a score this far (in log2) above the running max raises it
+constexpr float RAISE = 8.f;  // room (in log2) left above a running max when it is set
 constexpr float LN2 = 0.6931471805599453f;
 
 // Codes j and j + 4 of a word as a bf16 pair: (16 + n, 16 + n'), for j = 0 (whose
@@ -176,16 +190,20 @@ struct CutRun {
     int row0, cols, parts;
 };
 
-__global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Params p, int col_blocks) {
+template <int TILES>
+__global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
+    share_kernel(const DecodeQ4Params p, int col_blocks) {
+    using S = Shape<TILES>;
+    constexpr int NST = S::NST, COLS = S::COLS;
     extern __shared__ __align__(128) uint8_t smem[];
     ptx::wait_for_prior_work();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r4 = lane >> 2, c4 = lane & 3;
     uint8_t *ring = smem + warp * NST * STAGE;
-    float *exchange = reinterpret_cast<float *>(smem + RING) + lane;  // [half][word][lane]
-    uint4 *q_frag = reinterpret_cast<uint4 *>(smem + RING + 2 * EXCHANGE) + lane;  // [g * 32]
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING + 2 * EXCHANGE + Q_FRAGS) + warp * NST;
-    int *words = reinterpret_cast<int *>(smem + RING + 2 * EXCHANGE + Q_FRAGS + NW * NST * 8);
+    float *exchange = reinterpret_cast<float *>(smem + S::RING) + lane;                   // [half][word][lane]
+    uint4 *q_frag = reinterpret_cast<uint4 *>(smem + S::RING + 2 * S::EXCHANGE) + lane;  // [(4 tile + g) * 32]
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::BARRIERS) + warp * NST;
+    int *words = reinterpret_cast<int *>(smem + S::WORDS);
     volatile int *abort_flag = words;
     int64_t *found = reinterpret_cast<int64_t *>(words + 2);  // [0] all pairs, [1] pairs before words[1]'s sequence
     int *scan = words + 6;                                    // [NW]
@@ -329,16 +347,19 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
         // bf16 parts of group c4's Q_g and of its offset, then the third part.
         // The fragments are the same in every warp and stay in shared memory: one
         // 16-byte read a group and page is cheaper than 16 registers.
-        uint32_t qz0, qz1, qo0, qo1;
-        {
-            const uint4 *qrow = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + (row0 + r4) * D);
+        uint32_t qz0[TILES], qz1[TILES], qo0[TILES], qo1[TILES];
+#pragma unroll
+        for (int c = 0; c < TILES; ++c) {
+            const uint4 *qrow =
+                reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + (row0 + 8 * c + r4) * D);
             float x = 0.f, y = 0.f;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const uint4 v = r4 < cols ? __ldg(qrow + 4 * g + c4) : make_uint4(0, 0, 0, 0);
+                const uint4 v = 8 * c + r4 < cols ? __ldg(qrow + 4 * g + c4) : make_uint4(0, 0, 0, 0);
                 if (warp == g)
-                    q_frag[g * 32] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                                __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+                    q_frag[(4 * c + g) * 32] =
+                        make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                   __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
                 float s = ((lo_f(v.x) + hi_f(v.x)) + (lo_f(v.y) + hi_f(v.y))) +
                           ((lo_f(v.z) + hi_f(v.z)) + (lo_f(v.w) + hi_f(v.w)));
                 // 23.5 of every channel and 112 more of channels 0 and 4 of each eight
@@ -359,19 +380,27 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
                 b0 = h0 | h1 << 16;
                 b1 = ptx::pack_bf16x2(v1 - lo_f(h1), 0.f) & 0xffffu;
             };
-            parts(x, qz0, qz1);
-            parts(y, qo0, qo1);
+            parts(x, qz0[c], qz1[c]);
+            parts(y, qo0[c], qo1[c]);
+        }
+        __syncthreads();
+        // Of each tile: the exponents' reference (log2 units) and row sum of heads 2 c4, 2 c4 + 1;
+        // acc[2 g + i]: channels 32 g + 4 r4 + 2 i (+ 1) times those heads; cen: the
+        // centers' term of group r4 % 4.
+        float m[TILES][2], lsum[TILES][2], acc[TILES][8][4], cen[TILES][4];
+#pragma unroll
+        for (int c = 0; c < TILES; ++c) {
+            m[c][0] = m[c][1] = -INFINITY;
+            lsum[c][0] = lsum[c][1] = 0.f;
+            cen[c][0] = cen[c][1] = cen[c][2] = cen[c][3] = 0.f;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) acc[c][t][0] = acc[c][t][1] = acc[c][t][2] = acc[c][t][3] = 0.f;
         }
 
-        __syncthreads();
-        // Running max (log2 units) and row sum of heads 2 c4, 2 c4 + 1.  acc[2 g + i]:
-        // channels 32 g + 4 r4 + 2 i (+ 1) times those heads; off[g]: the group's
-        // offsets (of its first channel in four, and of the others); cen: the centers' term of group r4 % 4.
-        float m[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
-        float acc[8][4], cen[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int t = 0; t < 8; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-
+        // Exponents' reference: running max + RAISE - lim.  Probabilities lie below
+        // 2^lim; lim is set once, by the size of the first values (below).
+        float lim = 0.f;
+        bool fresh = true;
         int base = 0, left = n;
         while (left > 0) {
             const int batch = min(left, 32);
@@ -379,102 +408,141 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
             for (; i < batch; ++i) {
                 if (!wait_bounded(full + slot, parity, wc, kSiteQ4Page)) break;
                 const uint8_t *blk = ring + slot * STAGE;
-                float s[2][4];
-        #pragma unroll
+                float s[2][TILES][4];
+#pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     KeyWords k;
                     load_keys(k, blk + u * BLOCK, r4, c4);
                     const uint32_t zs[4] = {
                         __byte_perm(k.kza.x, k.kza.y, own), __byte_perm(k.kzb.x, k.kzb.y, own),
                         __byte_perm(k.ksa.x, k.ksa.y, own), __byte_perm(k.ksb.x, k.ksb.y, own)};
-                    mma_zero(s[u], zs, qz0, qo0);
-                    mma(s[u], zs, qz1, qo1);
+#pragma unroll
+                    for (int c = 0; c < TILES; ++c) {
+                        mma_zero(s[u][c], zs, qz0[c], qo0[c]);
+                        mma(s[u][c], zs, qz1[c], qo1[c]);
+                    }
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t wa = g == 0 ? k.ka.x : g == 1 ? k.ka.y : g == 2 ? k.ka.z : k.ka.w;
                         const uint32_t wb = g == 0 ? k.kb.x : g == 1 ? k.kb.y : g == 2 ? k.kb.z : k.kb.w;
-                        const uint4 qb = q_frag[g * 32];
-                        float d[4];
                         const uint32_t a0[4] = {code_pair<0>(wa), code_pair<0>(wb), code_pair<1>(wa), code_pair<1>(wb)};
-                        mma_zero(d, a0, qb.x, qb.y);
                         const uint32_t a1[4] = {code_pair<2>(wa), code_pair<2>(wb), code_pair<3>(wa), code_pair<3>(wb)};
-                        mma(d, a1, qb.z, qb.w);
                         const float fa = group_f(k.ksa, g), fb = group_f(k.ksb, g);
-                        s[u][0] = fmaf(fa, d[0], s[u][0]);
-                        s[u][1] = fmaf(fa, d[1], s[u][1]);
-                        s[u][2] = fmaf(fb, d[2], s[u][2]);
-                        s[u][3] = fmaf(fb, d[3], s[u][3]);
+#pragma unroll
+                        for (int c = 0; c < TILES; ++c) {
+                            const uint4 qb = q_frag[(4 * c + g) * 32];
+                            float d[4];
+                            mma_zero(d, a0, qb.x, qb.y);
+                            mma(d, a1, qb.z, qb.w);
+                            s[u][c][0] = fmaf(fa, d[0], s[u][c][0]);
+                            s[u][c][1] = fmaf(fa, d[1], s[u][c][1]);
+                            s[u][c][2] = fmaf(fb, d[2], s[u][c][2]);
+                            s[u][c][3] = fmaf(fb, d[3], s[u][c][3]);
+                        }
                     }
                 }
-                // s[u][0], s[u][1]: token r4 of page u, heads 2 c4, 2 c4 + 1; [2], [3]:
-                // token r4 + 8.  x: over the running max, in log2 units.
-                float x[2][4];
-                auto over = [&]() {
-        #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-        #pragma unroll
-                        for (int j = 0; j < 4; ++j) x[u][j] = fmaf(s[u][j], sl2, -m[j & 1]);
-                };
-                over();
+                // s[u][c][0], [1]: token r4 of page u, heads 8 c + 2 c4, + 1; [2], [3]:
+                // token r4 + 8.  x: over the reference, in log2 units.
+                float x[2][TILES][4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int c = 0; c < TILES; ++c)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[u][c][j] = fmaf(s[u][c][j], sl2, -m[c][j & 1]);
                 const bool all = whole >> i & 1;
                 if (!all) {
                     // Slots past the end hold arbitrary bits: their scores are replaced
                     // here, the values' parameters below.
-        #pragma unroll
+#pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int nv = __shfl_sync(0xffffffffu, u ? nv1 : nv0, i);
-                        if (r4 >= nv) x[u][0] = x[u][1] = -INFINITY;
-                        if (r4 + 8 >= nv) x[u][2] = x[u][3] = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < TILES; ++c) {
+                            if (r4 >= nv) x[u][c][0] = x[u][c][1] = -INFINITY;
+                            if (r4 + 8 >= nv) x[u][c][2] = x[u][c][3] = -INFINITY;
+                        }
                     }
                 }
-                // The running max follows only when a score is RAISE above it (the first
-                // keys are: the max is -inf): probabilities then stay below 2^RAISE,
-                // which costs the sums nothing, and a raise, with its shuffles and the
+                // The reference follows only when a score goes past the room left above
+                // the running max (the first keys do: it is -inf).  Probabilities then lie
+                // below 2^lim with the largest near 2^(lim - RAISE), which costs their
+                // bf16 and the sums nothing, and a raise, with its shuffles and the
                 // rescaling, is rare instead of nearly every page.
-                const float top0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-                const float top1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-                if (__any_sync(0xffffffffu, top0 > RAISE || top1 > RAISE)) {
-                    float y0 = -INFINITY, y1 = -INFINITY;
-        #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        y0 = fmaxf(y0, fmaxf(x[u][0] == -INFINITY ? -INFINITY : s[u][0] * sl2,
-                                             x[u][2] == -INFINITY ? -INFINITY : s[u][2] * sl2));
-                        y1 = fmaxf(y1, fmaxf(x[u][1] == -INFINITY ? -INFINITY : s[u][1] * sl2,
-                                             x[u][3] == -INFINITY ? -INFINITY : s[u][3] * sl2));
+                float top = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int c = 0; c < TILES; ++c)
+                        top = fmaxf(top, fmaxf(fmaxf(x[u][c][0], x[u][c][1]), fmaxf(x[u][c][2], x[u][c][3])));
+                if (__any_sync(0xffffffffu, top > lim)) {
+                    if (fresh) {
+                        // 2^lim times the first values is about 1, so that a probability
+                        // times a scale stays in the middle of bf16's range whatever
+                        // the values' size.  (lim >= -60: the smallest probabilities
+                        // that count stay above fp32's; <= 100: their sum stays below.)
+                        fresh = false;
+                        const int t = lane & 15;
+                        const uint8_t *page = blk + (lane >> 4) * BLOCK;
+                        uint32_t big = 0;
+                        const int nv = __shfl_sync(0xffffffffu, nv0, i), nx = __shfl_sync(0xffffffffu, nv1, i);
+                        if (t < (lane >> 4 ? nx : nv)) {
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const uint32_t sc = *reinterpret_cast<const uint16_t *>(page + q4::V_SCALES + t * 8 + g * 2);
+                                const uint32_t z =
+                                    *reinterpret_cast<const uint16_t *>(page + q4::V_CENTERS + g * 32 + t * 2) & 0x7fffu;
+                                if (sc < 0x7f80u) big = max(big, sc ? sc + (3u << 7) : 0u);  // largest value: 7.5 scales
+                                if (z < 0x7f80u) big = max(big, z);
+                            }
+                        }
+                        big = __reduce_max_sync(0xffffffffu, big);
+                        if (big) lim = fminf(fmaxf(127.f - (float)(big >> 7), -60.f), 100.f);
                     }
-        #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) {
-                        y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, o));
-                        y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, o));
+#pragma unroll
+                    for (int c = 0; c < TILES; ++c) {
+                        float y[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (x[u][c][j] != -INFINITY) y[j & 1] = fmaxf(y[j & 1], s[u][c][j] * sl2);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1)
+                                y[j] = fmaxf(y[j], __shfl_xor_sync(0xffffffffu, y[j], o));
+                            const float mx = fmaxf(m[c][j], y[j] + (RAISE - lim));
+                            const float a = m[c][j] == -INFINITY ? (mx == -INFINITY ? 1.f : 0.f) : ptx::ex2(m[c][j] - mx);
+                            lsum[c][j] *= a;
+                            cen[c][j] *= a;
+#pragma unroll
+                            for (int t = 0; t < 8; ++t) {
+                                acc[c][t][j] *= a;
+                                acc[c][t][2 + j] *= a;
+                            }
+                            m[c][j] = mx;
+                        }
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (x[u][c][j] != -INFINITY) x[u][c][j] = fmaf(s[u][c][j], sl2, -m[c][j & 1]);
                     }
-                    const float m0 = fmaxf(m[0], y0), m1 = fmaxf(m[1], y1);
-                    const float a0 = m[0] == -INFINITY ? (m0 == -INFINITY ? 1.f : 0.f) : ptx::ex2(m[0] - m0);
-                    const float a1 = m[1] == -INFINITY ? (m1 == -INFINITY ? 1.f : 0.f) : ptx::ex2(m[1] - m1);
-                    lsum[0] *= a0;
-                    lsum[1] *= a1;
-        #pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        acc[t][0] *= a0;
-                        acc[t][1] *= a1;
-                        acc[t][2] *= a0;
-                        acc[t][3] *= a1;
-                    }
-                    cen[0] *= a0;
-                    cen[1] *= a1;
-                    m[0] = m0;
-                    m[1] = m1;
-        #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-        #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (x[u][j] != -INFINITY) x[u][j] = fmaf(s[u][j], sl2, -m[j & 1]);
                 }
-        #pragma unroll
+#pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const float p0 = ptx::ex2(x[u][0]), p1 = ptx::ex2(x[u][1]);
-                    const float p2 = ptx::ex2(x[u][2]), p3 = ptx::ex2(x[u][3]);
-                    lsum[0] += p0 + p2;
-                    lsum[1] += p1 + p3;
+                    // P^T as the B operand: tokens 2 c4 (+ 1) and 2 c4 + 8 (+ 9), head r4.
+                    uint32_t pt0[TILES], pt1[TILES];
+#pragma unroll
+                    for (int c = 0; c < TILES; ++c) {
+                        const float p0 = ptx::ex2(x[u][c][0]), p1 = ptx::ex2(x[u][c][1]);
+                        const float p2 = ptx::ex2(x[u][c][2]), p3 = ptx::ex2(x[u][c][3]);
+                        lsum[c][0] += p0 + p2;
+                        lsum[c][1] += p1 + p3;
+                        pt0[c] = transpose8(ptx::pack_bf16x2(p0, p1));
+                        pt1[c] = transpose8(ptx::pack_bf16x2(p2, p3));
+                    }
                     ValueWords w;
                     load_values(w, blk + u * BLOCK, r4, c4);
                     if (u == 1) {
@@ -491,26 +559,26 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
                         w.vza &= (2 * c4 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 1 < nv ? 0xffff0000u : 0u);
                         w.vzb &= (2 * c4 + 8 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 9 < nv ? 0xffff0000u : 0u);
                     }
-                    // P^T as the B operand: tokens 2 c4 (+ 1) and 2 c4 + 8 (+ 9), head r4.
-                    const uint32_t pt0 = transpose8(ptx::pack_bf16x2(p0, p1));
-                    const uint32_t pt1 = transpose8(ptx::pack_bf16x2(p2, p3));
                     {
                         const uint32_t a[4] = {w.vza, w.vza, w.vzb, w.vzb};
-                        mma(cen, a, pt0, pt1);
+#pragma unroll
+                        for (int c = 0; c < TILES; ++c) mma(cen[c], a, pt0[c], pt1[c]);
                     }
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
-                        const uint32_t b0 =
-                            mul_bf16x2(pt0, __byte_perm(g < 2 ? w.vsa.x : w.vsa.y, g < 2 ? w.vsa.z : w.vsa.w, sel));
-                        const uint32_t b1 =
-                            mul_bf16x2(pt1, __byte_perm(g < 2 ? w.vsb.x : w.vsb.y, g < 2 ? w.vsb.z : w.vsb.w, sel));
+                        const uint32_t sa = __byte_perm(g < 2 ? w.vsa.x : w.vsa.y, g < 2 ? w.vsa.z : w.vsa.w, sel);
+                        const uint32_t sb = __byte_perm(g < 2 ? w.vsb.x : w.vsb.y, g < 2 ? w.vsb.z : w.vsb.w, sel);
                         const uint32_t wa = __byte_perm(g < 2 ? w.va.x : w.va.y, g < 2 ? w.va.z : w.va.w, sel);
                         const uint32_t wb = __byte_perm(g < 2 ? w.vb.x : w.vb.y, g < 2 ? w.vb.z : w.vb.w, sel);
                         const uint32_t a0[4] = {value_pair<0>(wa), value_pair<1>(wa), value_pair<0>(wb), value_pair<1>(wb)};
-                        mma(acc[2 * g], a0, b0, b1);
                         const uint32_t a1[4] = {value_pair<2>(wa), value_pair<3>(wa), value_pair<2>(wb), value_pair<3>(wb)};
-                        mma(acc[2 * g + 1], a1, b0, b1);
+#pragma unroll
+                        for (int c = 0; c < TILES; ++c) {
+                            const uint32_t b0 = mul_bf16x2(pt0[c], sa), b1 = mul_bf16x2(pt1[c], sb);
+                            mma(acc[c][2 * g], a0, b0, b1);
+                            mma(acc[c][2 * g + 1], a1, b0, b1);
+                        }
                     }
                 }
                 if (++slot == NST) {
@@ -536,51 +604,71 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
                 issue_first(min(left, 32));
             }
         }
-        // The offsets' and centers' terms, and the row sums over the tokens of the
-        // fragments (row groups r4).
+        // The centers' term, and the row sums over the tokens of the fragments (row
+        // groups r4).
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int c = 0; c < TILES; ++c)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float add = __shfl_sync(0xffffffffu, cen[j], 4 * g + c4);
-                acc[2 * g][j] += add;
-                acc[2 * g][2 + j] += add;
-                acc[2 * g + 1][j] += add;
-                acc[2 * g + 1][2 + j] += add;
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float add = __shfl_sync(0xffffffffu, cen[c][j], 4 * g + c4);
+                    acc[c][2 * g][j] += add;
+                    acc[c][2 * g][2 + j] += add;
+                    acc[c][2 * g + 1][j] += add;
+                    acc[c][2 * g + 1][2 + j] += add;
+                }
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) lsum[c][j] += __shfl_xor_sync(0xffffffffu, lsum[c][j], o);
+                // Normalised, with the log-sum-exp as the reference: warps need not agree
+                // on theirs.
+                const bool any = lsum[c][j] != 0.f;  // NaN included
+                const float inv = any ? 1.f / lsum[c][j] : 0.f;
+                m[c][j] = any ? m[c][j] + ptx::lg2(lsum[c][j]) : -INFINITY;
+                lsum[c][j] = any ? 1.f : 0.f;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    acc[c][t][j] *= inv;
+                    acc[c][t][2 + j] *= inv;
+                }
             }
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) lsum[j] += __shfl_xor_sync(0xffffffffu, lsum[j], o);
-        }
         // The four warps' results meet in two rounds: 2 and 3 into 0 and 1, then 1
         // into 0, a lane's words with the same lane's.
         auto give = [&](int half) {
-            float *x = exchange + half * (EXCHANGE / 4);
+            float *x = exchange + half * (S::EXCHANGE / 4);
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
+            for (int c = 0; c < TILES; ++c, x += 36 * 32) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[(4 * t + k) * 32] = acc[t][k];
+                for (int t = 0; t < 8; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                x[(32 + j) * 32] = m[j];
-                x[(34 + j) * 32] = lsum[j];
+                    for (int k = 0; k < 4; ++k) x[(4 * t + k) * 32] = acc[c][t][k];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    x[(32 + j) * 32] = m[c][j];
+                    x[(34 + j) * 32] = lsum[c][j];
+                }
             }
         };
         auto take = [&](int half) {
-            const float *x = exchange + half * (EXCHANGE / 4);
-            float fa[2], fb[2];
+            const float *x = exchange + half * (S::EXCHANGE / 4);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float mo = x[(32 + j) * 32], mx = fmaxf(m[j], mo);
-                // A side without a finite score has only zeros, or NaN, to add.
-                fa[j] = m[j] == -INFINITY ? 1.f : ptx::ex2(m[j] - mx);
-                fb[j] = mo == -INFINITY ? 1.f : ptx::ex2(mo - mx);
-                lsum[j] = lsum[j] * fa[j] + x[(34 + j) * 32] * fb[j];
-                m[j] = mx;
+            for (int c = 0; c < TILES; ++c, x += 36 * 32) {
+                float fa[2], fb[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // (an empty side has zeros to add; a NaN stays one)
+                    const float mo = x[(32 + j) * 32], mx = fmaxf(m[c][j], mo);
+                    fa[j] = m[c][j] == -INFINITY ? 0.f : ptx::ex2(m[c][j] - mx);
+                    fb[j] = mo == -INFINITY ? 0.f : ptx::ex2(mo - mx);
+                    lsum[c][j] = lsum[c][j] * fa[j] + x[(34 + j) * 32] * fb[j];
+                    m[c][j] = mx;
+                }
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[c][t][k] = acc[c][t][k] * fa[k & 1] + x[(4 * t + k) * 32] * fb[k & 1];
             }
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[t][k] = acc[t][k] * fa[k & 1] + x[(4 * t + k) * 32] * fb[k & 1];
         };
         __syncthreads();  // the exchange of the segment before has been read
         if (warp >= 2) give(warp - 2);
@@ -600,29 +688,32 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
             const bool done = count == seq_pairs;  // the whole sequence: no merge
             const int64_t part = ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * COLS;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = 2 * c4 + j;
-                if (c >= cols) continue;
-                const bool any = lsum[j] != 0.f;  // NaN included
-                const float inv = any ? 1.f / lsum[j] : 0.f;
-                const float l2 = any ? m[j] + ptx::lg2(lsum[j]) : -INFINITY;
+            for (int c = 0; c < TILES; ++c)
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float o0 = any ? acc[2 * g][j] * inv : 0.f, o1 = any ? acc[2 * g][2 + j] * inv : 0.f;
-                    const float o2 = any ? acc[2 * g + 1][j] * inv : 0.f;
-                    const float o3 = any ? acc[2 * g + 1][2 + j] * inv : 0.f;
-                    if (done)
-                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + (row0 + c) * D + 32 * g + 4 * r4) =
-                            make_uint2(ptx::pack_bf16x2(o0, o1), ptx::pack_bf16x2(o2, o3));
-                    else
-                        *reinterpret_cast<float4 *>(p.o_part + (part + c) * D + 32 * g + 4 * r4) =
-                            make_float4(o0, o1, o2, o3);
+                for (int j = 0; j < 2; ++j) {
+                    const int col = 8 * c + 2 * c4 + j;
+                    if (col >= cols) continue;
+                    const bool any = lsum[c][j] != 0.f;  // NaN included
+                    const float inv = any ? 1.f / lsum[c][j] : 0.f;
+                    const float l2 = any ? m[c][j] + ptx::lg2(lsum[c][j]) : -INFINITY;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float o0 = any ? acc[c][2 * g][j] * inv : 0.f;
+                        const float o1 = any ? acc[c][2 * g][2 + j] * inv : 0.f;
+                        const float o2 = any ? acc[c][2 * g + 1][j] * inv : 0.f;
+                        const float o3 = any ? acc[c][2 * g + 1][2 + j] * inv : 0.f;
+                        const int64_t at = 32 * g + 4 * r4;
+                        if (done)
+                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + (row0 + col) * D + at) =
+                                make_uint2(ptx::pack_bf16x2(o0, o1), ptx::pack_bf16x2(o2, o3));
+                        else
+                            *reinterpret_cast<float4 *>(p.o_part + (part + col) * D + at) = make_float4(o0, o1, o2, o3);
+                    }
+                    if (r4 == 0) {
+                        if (!done) p.lse_part[part + col] = l2;
+                        else if (p.lse) p.lse[row0 + col] = l2 * LN2;
+                    }
                 }
-                if (r4 == 0) {
-                    if (!done) p.lse_part[part + c] = l2;
-                    else if (p.lse) p.lse[row0 + c] = l2 * LN2;
-                }
-            }
         }
         if (first == 0 && count < seq_pairs) {
             // The sequence goes on in the next shares, up to the one that holds
@@ -650,7 +741,8 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) share_kernel(const DecodeQ4Pa
 // c, if one does.  Warp w takes every MERGE_WARPS-th part, four channels a lane;
 // the order is fixed.
 constexpr int MERGE_WARPS = 8;
-__global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const DecodeQ4Params p, int col_blocks) {
+__global__ void __launch_bounds__(MERGE_WARPS * 32)
+    merge_kernel(const DecodeQ4Params p, int col_blocks, int cta_cols) {
     __shared__ float part[MERGE_WARPS][D];
     __shared__ float part_m[MERGE_WARPS], part_l[MERGE_WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -664,7 +756,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const DecodeQ4P
     const int64_t r = (int64_t)cut.x + c;
     // The first part is this share's last one, the others are the next shares'
     // first ones (of the same column block).
-    auto row_of = [&](int s) { return ((int64_t)(blockIdx.x + s * col_blocks) * 2 + (s == 0 ? 1 : 0)) * COLS + c; };
+    auto row_of = [&](int s) { return ((int64_t)(blockIdx.x + s * col_blocks) * 2 + (s == 0 ? 1 : 0)) * cta_cols + c; };
     float M = -INFINITY;
     for (int s = warp; s < parts; s += MERGE_WARPS) M = fmaxf(M, p.lse_part[row_of(s)]);
     float l = 0.f;
@@ -703,44 +795,62 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const DecodeQ4P
     if (p.lse && threadIdx.x == 0) p.lse[r] = any ? (Mt + ptx::lg2(Lt)) * LN2 : -INFINITY;
 }
 
-// CTAs: shares times column blocks.
-int grid_of(int B, int Hq, int Hkv, int max_blocks, int max_ctas) {
-    const int col_blocks = (Hq / Hkv + COLS - 1) / COLS;
+// Column blocks of a KV head's G query heads, and CTAs: shares times those.
+struct Grid {
+    int tiles, cols, col_blocks, ctas;
+};
+
+Grid grid_of(int B, int Hq, int Hkv, int max_blocks, int sm_count) {
+    const int G = Hq / Hkv;
+    Grid g;
+    g.tiles = G > 8 ? 2 : 1;
+    g.cols = 8 * g.tiles;
+    g.col_blocks = (G + g.cols - 1) / g.cols;
+    const int per_sm = g.tiles == 2 ? Shape<2>::CTAS_PER_SM : Shape<1>::CTAS_PER_SM;
+    const int most = g.tiles == 2 ? Shape<2>::MAX_CTAS : Shape<1>::MAX_CTAS;
+    const int resident = sm_count > 0 && per_sm * sm_count < most ? per_sm * sm_count : most;
     const int64_t items = (int64_t)B * Hkv;
     const int64_t fill = (items * ((max_blocks + 1) / 2) + MIN_PAIRS - 1) / MIN_PAIRS;
-    int64_t shares = max_ctas / col_blocks;
+    int64_t shares = resident / g.col_blocks;
     if (shares > (items > fill ? items : fill)) shares = items > fill ? items : fill;
     if (shares < 1) shares = 1;
-    return (int)shares * col_blocks;
+    g.ctas = (int)shares * g.col_blocks;
+    return g;
 }
 
-}  // namespace dq4
-
-int decode_q4_max_ctas(int B, int Hq, int Hkv, int max_blocks) {
-    return dq4::grid_of(B, Hq, Hkv, max_blocks, dq4::MAX_CTAS);
-}
-
-cudaError_t launch_decode_q4(const DecodeQ4Params &p, int sm_count, cudaStream_t stream) {
-    const int col_blocks = (p.Hq / p.Hkv + dq4::COLS - 1) / dq4::COLS;
-    const int resident = dq4::CTAS_PER_SM * sm_count;
-    const int grid = dq4::grid_of(p.B, p.Hq, p.Hkv, p.max_blocks, resident < dq4::MAX_CTAS ? resident : dq4::MAX_CTAS);
+template <int TILES>
+cudaError_t launch_shares(const DecodeQ4Params &p, const Grid &g, cudaStream_t stream) {
     static thread_local int configured_device = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (configured_device != dev) {
-        e = cudaFuncSetAttribute(dq4::share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dq4::SMEM);
+        e = cudaFuncSetAttribute(share_kernel<TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<TILES>::SMEM);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(dq4::share_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+            e = cudaFuncSetAttribute(share_kernel<TILES>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
         configured_device = dev;
     }
-    e = launch_dependent(dq4::share_kernel, grid, dq4::NT, dq4::SMEM, stream, p, col_blocks);
+    return launch_dependent(share_kernel<TILES>, g.ctas, NT, Shape<TILES>::SMEM, stream, p, g.col_blocks);
+}
+
+}  // namespace dq4
+
+size_t decode_q4_partial_rows(int B, int Hq, int Hkv, int max_blocks, size_t *ctas) {
+    const dq4::Grid g = dq4::grid_of(B, Hq, Hkv, max_blocks, 0);
+    *ctas = (size_t)g.ctas;
+    return (size_t)g.ctas * 2 * g.cols;
+}
+
+cudaError_t launch_decode_q4(const DecodeQ4Params &p, int sm_count, cudaStream_t stream) {
+    const dq4::Grid g = dq4::grid_of(p.B, p.Hq, p.Hkv, p.max_blocks, sm_count);
+    const cudaError_t e = g.tiles == 2 ? dq4::launch_shares<2>(p, g, stream) : dq4::launch_shares<1>(p, g, stream);
     // One sequence with a share for each KV head is never cut.
-    if (e != cudaSuccess || (p.B == 1 && grid / col_blocks == p.Hkv)) return e;
-    const int heads = p.Hq / p.Hkv < dq4::COLS ? p.Hq / p.Hkv : dq4::COLS;
-    return launch_dependent(dq4::merge_kernel, dim3(grid, heads), dq4::MERGE_WARPS * 32, 0, stream, p, col_blocks);
+    if (e != cudaSuccess || (p.B == 1 && g.ctas / g.col_blocks == p.Hkv)) return e;
+    const int G = p.Hq / p.Hkv;
+    return launch_dependent(dq4::merge_kernel, dim3(g.ctas, G < g.cols ? G : g.cols), dq4::MERGE_WARPS * 32, 0, stream, p,
+                            g.col_blocks, g.cols);
 }
 
 }  // namespace attn

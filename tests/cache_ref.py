@@ -148,14 +148,13 @@ def attend(q, k, v, scale, hidden=None):
 def check_decode_q4(got, lse, q, cache, table, lens, scale, what=""):
     """attn_decode_paged_q4 against 64 bits.
 
-    Key codes enter the products as n + 0.5, and as n + 32 with the query over 16; the offsets (up to 39.5) are taken off
-    after them.  Queries enter as f16 of an exact scaling, off by 2^-28 of the head's largest at most.  Scores are fp32
-    sums of 128 products: errors of a few steps (16 at most) of the terms' sum,
-    e = 16 * 2^-24 * scale * sum |q| (48 s + |z|), which the queries' 128 * 15 s * 2^-28 of the largest |q| is within; a
-    weight is then off by that share and by ex2's and the merge's few steps (2^-20 in all).  A probability is rounded to
-    bf16, and its product with a scale once more: the value's two parts are off by (1 + HALF)^2 - 1 = 2 HALF + HALF^2 of
-    w |s (n - 7.5)| and HALF of w |z|; fp32 accumulation adds 16 * 2^-24 of 8 w s.  The output is rounded once.  lse
-    moves by at most the largest score error and ln's 2^-20."""
+    Key codes enter the products as 16 + n or 128 + n, the offset is taken off after them; value codes enter as n - 7.5.
+    Scores are fp32 sums of 128 products q s (n + 128) at most: errors of a few steps (16 at most) of the terms' sum,
+    e = 16 * 2^-24 * scale * sum |q| (144 s + |z|); a weight is then off by that share and by ex2's and the merge's few
+    steps (2^-20 in all).  A probability is rounded to bf16, and its product with a scale once more: the value's two
+    parts are off by (1 + HALF)^2 - 1 = 2 HALF + HALF^2 of w |s (n - 7.5)| and HALF of w |z|; fp32 accumulation adds
+    16 * 2^-24 of 8 w s.  Below the normal range a step of a product is 2^-133.  The output is rounded once.  lse moves
+    by at most the largest score error and ln's 2^-20."""
     got, lse = got.double().cpu(), lse.double().cpu()
     Hq = q.shape[1]
     for b, L in enumerate(lens):
@@ -166,7 +165,7 @@ def check_decode_q4(got, lse, q, cache, table, lens, scale, what=""):
         kp, vp = read_tokens(cache, table[b], L)
         out, ref_lse, w = attend(qb, values(kp), values(vp), scale)
         G = Hq // cache.shape[1]
-        terms = (48 * kp[1] + kp[2].abs()).repeat_interleave(G, 1)
+        terms = (144 * kp[1] + kp[2].abs()).repeat_interleave(G, 1)
         e = 16 * 2.0 ** -24 * scale * torch.einsum("nhd,lhd->hnl", qb.abs(), terms).amax(-1)     # [Hq, 1]
         share = 2 * e + 2.0 ** -20
         mag = ((2 + HALF) * (vp[1] * (vp[0] - 7.5)).abs() + vp[2].abs()).repeat_interleave(G, 1)
