@@ -9,17 +9,15 @@
 //
 // - Codes go to the tensor cores without being turned into cache values.  A code n
 //   moved to bits 3..6 of a bf16 whose other bits say 16.0 is the number 16 + n
-//   exactly: a shift and an and/or for two codes.  (Codes that need no shift to
-//   bits 0..3 become 128 + n.)
+//   exactly: a shift and an and/or for two codes.
 // - S^T = K Q^T (mma m16n8k16, the page's 16 tokens as rows, eight query heads of
 //   the KV head as columns), a product for each group of 32 channels:
-//       s_t += scale_tg * (sum_c q_c (off_c + n_tc) - Off_g) + center_tg * Q_g,
-//   with Q_g the sum of the group's q and Off_g the q's sum weighted with the
-//   offsets to n - 7.5.  Both last terms are two more products for all groups at
-//   once, Q_g and Off_g cut into three bf16 parts (24 bits).
+//       s_t += scale_tg * (sum_c q_c (16 + n_tc) - 23.5 Q_g) + center_tg * Q_g,
+//   with Q_g the sum of the group's q.  Both terms with Q_g are two more products
+//   for all groups at once, Q_g and -23.5 Q_g cut into three bf16 parts (24 bits).
 // - O^T += V^T P^T: value codes become n - 7.5 by one packed addition, and a group's
-//   scale goes to the probability, P'_t = P_t scale_tg, in the operand's layout;
-//   the centers' term is one product with the unscaled P.
+//   scale goes to the probability, P'_t = P_t scale_tg; the centers' term is one
+//   product with the unscaled P.
 // - The byte order of the block (q4.cuh) is that of the fragments: every lane
 //   reads its operands as 16-byte words without bank conflicts, and a value
 //   pair of two tokens is one byte permutation.
@@ -36,15 +34,17 @@
 // In a segment each warp streams page pairs w, w + 4, .. through a ring of its own
 // (bulk copies issued by its lane 0 as soon as a slot has been read): no producer
 // warp and no barrier between warps until the four partial results meet at the
-// segment's end.  Scores, sums and outputs are fp32.  P is rounded to bf16 for its
-// products, and P' once more, each by 2^-9 of itself at most, as in the bf16
-// decode; the row sum adds the fp32 values.
+// segment's end.  Scores, sums and outputs are fp32.  P' is rounded to f16 (2^-12 of
+// itself at most), P to bf16 for the centers; the row sum adds the fp32 values.
+// With P' in bf16, as the bf16 decode's P, the output's error against 64 bits was
+// 2.4e-3 (its own rounding alone makes 1.7e-3) instead of 1.8e-3, in 0.97 of the time.
 //
-// Measured on 64 sequences of 0 to 16384 tokens, 64 / 8 heads (758 MB): 154 us,
-// 4.9 TB/s, 0.73 of the copy bandwidth; the copies alone take 124 us, the
-// arithmetic alone 135.  On 32 sequences of 1024 to 8192 tokens, 32 / 8 heads (177
-// MB): 47 us, 0.56; half the MMA columns are empty there, and about 6 us are the
-// two launches' ends.
+// Measured on 64 sequences of 0 to 16384 tokens, 64 / 8 heads (758 MB): 167 us,
+// 4.5 TB/s, 0.67 of the copy bandwidth; the copies alone take 124 us, the
+// arithmetic alone about 145.  On 32 sequences of 1024 to 8192 tokens, 32 / 8 heads
+// (177 MB): 50 us, 0.52; half the MMA columns are empty there, and about 6 us are
+// the two launches' ends.  3 sequences of about 100 thousand tokens, 32 / 1 heads
+// (55 MB): 49 us, the unpacking of two tiles' pages twice.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -81,20 +81,16 @@ struct Shape {
     static_assert(CTAS_PER_SM * (SMEM + 1024) <= 233472, "CTAs per SM");
 };
 constexpr int MIN_PAIRS = 4;           // pairs a CTA takes at least, unless there is a KV head for each
-constexpr float RAISE = 8.f;  // room (in log2) left above a running max when it is set
+constexpr float RAISE = 8.f;  // a score this far (in log2) above the running max raises it
 constexpr float LN2 = 0.6931471805599453f;
 
-// Codes j and j + 4 of a word as a bf16 pair: (16 + n, 16 + n'), for j = 0 (whose
-// bits need no shift there) (128 + n, 128 + n').
+// Codes j and j + 4 of a word as the bf16 pair (16 + n, 16 + n').
 template <int J>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
     uint32_t r;
-    if (J == 0)
-        asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(r) : "r"(w), "r"(0x43004300u));  // (w & mask) | 128.0
-    else
-        asm("lop3.b32 %0, %1, 0x00780078, %2, 0xEA;"
-            : "=r"(r)
-            : "r"(w >> (J == 0 ? 0 : 4 * J - 3)), "r"(0x41804180u));  // | 16.0
+    asm("lop3.b32 %0, %1, 0x00780078, %2, 0xEA;"  // (bits & mask) | 16.0
+        : "=r"(r)
+        : "r"(J == 0 ? w << 3 : w >> (J == 0 ? 0 : 4 * J - 3)), "r"(0x41804180u));
     return r;
 }
 
@@ -123,17 +119,32 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A pair's values n - 7.5, exactly: 23.5 off the codes as 16 + n.
+// A pair's values n - 7.5 as f16, exactly: a code moved to bits 6..9 of an f16 that
+// otherwise says 16.0 is 16 + n, 23.5 comes off.
 template <int J>
 __device__ __forceinline__ uint32_t value_pair(uint32_t w) {
     uint32_t r, d;
-    const uint32_t t = J == 0 ? w << 3 : w >> (J == 0 ? 0 : 4 * J - 3);
-    asm("lop3.b32 %0, %1, 0x00780078, %2, 0xEA;" : "=r"(r) : "r"(t), "r"(0x41804180u));
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(r), "r"(0xC1BCC1BCu));
+    const uint32_t t = J == 0 ? w << 6 : J == 1 ? w << 2 : w >> (J < 2 ? 0 : 4 * J - 6);
+    asm("lop3.b32 %0, %1, 0x03c003c0, %2, 0xEA;" : "=r"(r) : "r"(t), "r"(0x4c004c00u));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(r), "r"(0xcde0cde0u));
     return d;
 }
 
-// Products of two bf16 pairs, each rounded to bf16.
+// mma with f16 operands.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Products of two bf16 pairs (exact by a power of two).
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -154,7 +165,7 @@ struct KeyWords {
 };
 struct ValueWords {
     uint4 va, vb;       // codes of tokens 2 c4, 2 c4 + 1 and those + 8
-    uint4 vsa, vsb;     // scales of tokens 2 c4, 2 c4 + 1 and those + 8, all groups
+    uint2 vsa, vsb;     // scales of tokens r4 and r4 + 8, all groups
     uint32_t vza, vzb;  // centers of group r4 % 4, tokens 2 c4, 2 c4 + 1 and those + 8
 };
 
@@ -172,8 +183,8 @@ __device__ __forceinline__ void load_values(ValueWords &w, const uint8_t *blk, i
     const uint8_t *v = blk + r4 * 128 + c4 * 32;
     w.va = *reinterpret_cast<const uint4 *>(v + q4::V_CODES + ((r4 & 1) << 4));
     w.vb = *reinterpret_cast<const uint4 *>(v + q4::V_CODES + (((r4 & 1) ^ 1) << 4));
-    w.vsa = *reinterpret_cast<const uint4 *>(blk + q4::V_SCALES + c4 * 16);
-    w.vsb = *reinterpret_cast<const uint4 *>(blk + q4::V_SCALES + c4 * 16 + 64);
+    w.vsa = *reinterpret_cast<const uint2 *>(blk + q4::V_SCALES + r4 * 8);
+    w.vsb = *reinterpret_cast<const uint2 *>(blk + q4::V_SCALES + r4 * 8 + 64);
     const uint8_t *z = blk + q4::V_CENTERS + (r4 & 3) * 32 + c4 * 4;
     w.vza = *reinterpret_cast<const uint32_t *>(z);
     w.vzb = *reinterpret_cast<const uint32_t *>(z + 16);
@@ -344,7 +355,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
         // 32 g + 8 c4 + (j, j + 4), j = 0..3, in the order of a key word's pairs.
         // qz, qo: B operands of the centers' and the scales' products, two each: at
         // k = 2 c4, 2 c4 + 1 (centers) and 2 c4 + 8, 2 c4 + 9 (scales) the first two
-        // bf16 parts of group c4's Q_g and of its offset, then the third part.
+        // bf16 parts of group c4's Q_g and of -23.5 Q_g, then the third part.
         // The fragments are the same in every warp and stay in shared memory: one
         // 16-byte read a group and page is cheaper than 16 registers.
         uint32_t qz0[TILES], qz1[TILES], qo0[TILES], qo1[TILES];
@@ -352,7 +363,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
         for (int c = 0; c < TILES; ++c) {
             const uint4 *qrow =
                 reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + (row0 + 8 * c + r4) * D);
-            float x = 0.f, y = 0.f;
+            float x = 0.f;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const uint4 v = 8 * c + r4 < cols ? __ldg(qrow + 4 * g + c4) : make_uint4(0, 0, 0, 0);
@@ -362,16 +373,9 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                                    __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
                 float s = ((lo_f(v.x) + hi_f(v.x)) + (lo_f(v.y) + hi_f(v.y))) +
                           ((lo_f(v.z) + hi_f(v.z)) + (lo_f(v.w) + hi_f(v.w)));
-                // 23.5 of every channel and 112 more of channels 0 and 4 of each eight
-                float t = fmaf(112.f, lo_f(v.x) + lo_f(v.z), 23.5f * s);
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
-                t += __shfl_xor_sync(0xffffffffu, t, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
-                t += __shfl_xor_sync(0xffffffffu, t, 2);
-                if (g == c4) {
-                    x = s;
-                    y = -t;
-                }
+                if (g == c4) x = s;
             }
             auto parts = [](float v, uint32_t &b0, uint32_t &b1) {
                 const uint32_t h0 = ptx::pack_bf16x2(v, 0.f) & 0xffffu;
@@ -381,10 +385,10 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                 b1 = ptx::pack_bf16x2(v1 - lo_f(h1), 0.f) & 0xffffu;
             };
             parts(x, qz0[c], qz1[c]);
-            parts(y, qo0[c], qo1[c]);
+            parts(-23.5f * x, qo0[c], qo1[c]);
         }
         __syncthreads();
-        // Of each tile: the exponents' reference (log2 units) and row sum of heads 2 c4, 2 c4 + 1;
+        // Of each tile: running max (log2 units) and row sum of heads 2 c4, 2 c4 + 1;
         // acc[2 g + i]: channels 32 g + 4 r4 + 2 i (+ 1) times those heads; cen: the
         // centers' term of group r4 % 4.
         float m[TILES][2], lsum[TILES][2], acc[TILES][8][4], cen[TILES][4];
@@ -397,10 +401,10 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
             for (int t = 0; t < 8; ++t) acc[c][t][0] = acc[c][t][1] = acc[c][t][2] = acc[c][t][3] = 0.f;
         }
 
-        // Exponents' reference: running max + RAISE - lim.  Probabilities lie below
-        // 2^lim; lim is set once, by the size of the first values (below).
-        float lim = 0.f;
-        bool fresh = true;
+        // The value scales' common factor, a power of two as a bf16 pair, and the size
+        // (bf16 bits) from which a scale is too large for it (at first: any).
+        constexpr uint32_t ONE = 0x3f803f80u;
+        uint32_t vf = ONE, vf_limit = 1;
         int base = 0, left = n;
         while (left > 0) {
             const int batch = min(left, 32);
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                     }
                 }
                 // s[u][c][0], [1]: token r4 of page u, heads 8 c + 2 c4, + 1; [2], [3]:
-                // token r4 + 8.  x: over the reference, in log2 units.
+                // token r4 + 8.  x: over the running max, in log2 units.
                 float x[2][TILES][4];
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
@@ -450,6 +454,11 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                     for (int c = 0; c < TILES; ++c)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) x[u][c][j] = fmaf(s[u][c][j], sl2, -m[c][j & 1]);
+                // The scales of one token's values for the check below: lane = page x token.
+                const uint2 vs =
+                    *reinterpret_cast<const uint2 *>(blk + (lane >> 4) * BLOCK + q4::V_SCALES + (lane & 15) * 8);
+                uint32_t big = __vmaxu2(vs.x, vs.y);
+                big = max(big & 0xffffu, big >> 16);
                 const bool all = whole >> i & 1;
                 if (!all) {
                     // Slots past the end hold arbitrary bits: their scores are replaced
@@ -462,42 +471,46 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                             if (r4 >= nv) x[u][c][0] = x[u][c][1] = -INFINITY;
                             if (r4 + 8 >= nv) x[u][c][2] = x[u][c][3] = -INFINITY;
                         }
+                        if (u == lane >> 4 && (lane & 15) >= nv) big = 0;
                     }
                 }
-                // The reference follows only when a score goes past the room left above
-                // the running max (the first keys do: it is -inf).  Probabilities then lie
-                // below 2^lim with the largest near 2^(lim - RAISE), which costs their
-                // bf16 and the sums nothing, and a raise, with its shuffles and the
-                // rescaling, is rare instead of nearly every page.
+                // The running max follows only when a score is RAISE above it (the first
+                // keys are: it is -inf).  Probabilities then lie below 2^RAISE with the
+                // largest from 1 on, which costs the sums nothing, and a raise, with its
+                // shuffles and the rescaling, is rare instead of nearly every page.
                 float top = -INFINITY;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int c = 0; c < TILES; ++c)
                         top = fmaxf(top, fmaxf(fmaxf(x[u][c][0], x[u][c][1]), fmaxf(x[u][c][2], x[u][c][3])));
-                if (__any_sync(0xffffffffu, top > lim)) {
-                    if (fresh) {
-                        // 2^lim times the first values is about 1, so that a probability
-                        // times a scale stays in the middle of bf16's range whatever
-                        // the values' size.  (lim >= -60: the smallest probabilities
-                        // that count stay above fp32's; <= 100: their sum stays below.)
-                        fresh = false;
-                        const int t = lane & 15;
-                        const uint8_t *page = blk + (lane >> 4) * BLOCK;
-                        uint32_t big = 0;
-                        const int nv = __shfl_sync(0xffffffffu, nv0, i), nx = __shfl_sync(0xffffffffu, nv1, i);
-                        if (t < (lane >> 4 ? nx : nv)) {
+                // Probability times scale goes to the product as f16 (11 bits: the values'
+                // part of the output then loses nothing against its own rounding), so
+                // it has to stay below 2^16 and, where it counts, above f16's last steps.
+                // Scales below 2^7 are taken as they are when the first pages' largest
+                // is from 2^-10 on; otherwise, and when one outgrows its limit, all are
+                // multiplied by the power of two that brings the largest to 2^5.
+                if (__any_sync(0xffffffffu, top > RAISE || big >= vf_limit)) {
+                    uint32_t largest = 0;  // finite scale of this lane's token
+                    if (big) {
+                        const uint32_t h[4] = {vs.x & 0xffffu, vs.x >> 16, vs.y & 0xffffu, vs.y >> 16};
 #pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const uint32_t sc = *reinterpret_cast<const uint16_t *>(page + q4::V_SCALES + t * 8 + g * 2);
-                                const uint32_t z =
-                                    *reinterpret_cast<const uint16_t *>(page + q4::V_CENTERS + g * 32 + t * 2) & 0x7fffu;
-                                if (sc < 0x7f80u) big = max(big, sc ? sc + (3u << 7) : 0u);  // largest value: 7.5 scales
-                                if (z < 0x7f80u) big = max(big, z);
-                            }
-                        }
-                        big = __reduce_max_sync(0xffffffffu, big);
-                        if (big) lim = fminf(fmaxf(127.f - (float)(big >> 7), -60.f), 100.f);
+                        for (int g = 0; g < 4; ++g) largest = max(largest, h[g] < 0x7f80u ? h[g] : 0u);
+                    }
+                    const uint32_t e = __reduce_max_sync(0xffffffffu, largest) >> 7;  // exponent + 127
+                    const bool plain = vf == ONE && e >= 117 && e < 134;
+                    const uint32_t limit = plain ? 134u << 7 : min((e + 2) << 7, 0x7f80u);
+                    if (limit > vf_limit) {
+                        const uint32_t f = plain ? 127u << 7 : min(259u - e, 254u) << 7;  // 2^(5 - exponent)
+                        const float ratio = __uint_as_float(f << 16) / lo_f(vf);
+                        vf = f * 0x10001u;
+                        vf_limit = limit;
+#pragma unroll
+                        for (int c = 0; c < TILES; ++c)
+#pragma unroll
+                            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) acc[c][t][j] *= ratio;
                     }
 #pragma unroll
                     for (int c = 0; c < TILES; ++c) {
@@ -512,7 +525,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1)
                                 y[j] = fmaxf(y[j], __shfl_xor_sync(0xffffffffu, y[j], o));
-                            const float mx = fmaxf(m[c][j], y[j] + (RAISE - lim));
+                            const float mx = fmaxf(m[c][j], y[j]);
                             const float a = m[c][j] == -INFINITY ? (mx == -INFINITY ? 1.f : 0.f) : ptx::ex2(m[c][j] - mx);
                             lsum[c][j] *= a;
                             cen[c][j] *= a;
@@ -532,16 +545,13 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    // P^T as the B operand: tokens 2 c4 (+ 1) and 2 c4 + 8 (+ 9), head r4.
-                    uint32_t pt0[TILES], pt1[TILES];
+                    float p[TILES][4];
 #pragma unroll
                     for (int c = 0; c < TILES; ++c) {
-                        const float p0 = ptx::ex2(x[u][c][0]), p1 = ptx::ex2(x[u][c][1]);
-                        const float p2 = ptx::ex2(x[u][c][2]), p3 = ptx::ex2(x[u][c][3]);
-                        lsum[c][0] += p0 + p2;
-                        lsum[c][1] += p1 + p3;
-                        pt0[c] = transpose8(ptx::pack_bf16x2(p0, p1));
-                        pt1[c] = transpose8(ptx::pack_bf16x2(p2, p3));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) p[c][j] = ptx::ex2(x[u][c][j]);
+                        lsum[c][0] += p[c][0] + p[c][2];
+                        lsum[c][1] += p[c][1] + p[c][3];
                     }
                     ValueWords w;
                     load_values(w, blk + u * BLOCK, r4, c4);
@@ -552,32 +562,36 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                     }
                     if (!all) {
                         const int nv = __shfl_sync(0xffffffffu, u ? nv1 : nv0, i);
-                        if (2 * c4 >= nv) w.vsa.x = w.vsa.y = 0;
-                        if (2 * c4 + 1 >= nv) w.vsa.z = w.vsa.w = 0;
-                        if (2 * c4 + 8 >= nv) w.vsb.x = w.vsb.y = 0;
-                        if (2 * c4 + 9 >= nv) w.vsb.z = w.vsb.w = 0;
+                        if (r4 >= nv) w.vsa = make_uint2(0, 0);
+                        if (r4 + 8 >= nv) w.vsb = make_uint2(0, 0);
                         w.vza &= (2 * c4 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 1 < nv ? 0xffff0000u : 0u);
                         w.vzb &= (2 * c4 + 8 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 9 < nv ? 0xffff0000u : 0u);
+                    }
+                    if (vf != ONE) {
+                        w.vsa = make_uint2(mul_bf16x2(w.vsa.x, vf), mul_bf16x2(w.vsa.y, vf));
+                        w.vsb = make_uint2(mul_bf16x2(w.vsb.x, vf), mul_bf16x2(w.vsb.y, vf));
                     }
                     {
                         const uint32_t a[4] = {w.vza, w.vza, w.vzb, w.vzb};
 #pragma unroll
-                        for (int c = 0; c < TILES; ++c) mma(cen[c], a, pt0[c], pt1[c]);
+                        for (int c = 0; c < TILES; ++c)
+                            mma(cen[c], a, transpose8(ptx::pack_bf16x2(p[c][0], p[c][1])),
+                                transpose8(ptx::pack_bf16x2(p[c][2], p[c][3])));
                     }
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
-                        const uint32_t sa = __byte_perm(g < 2 ? w.vsa.x : w.vsa.y, g < 2 ? w.vsa.z : w.vsa.w, sel);
-                        const uint32_t sb = __byte_perm(g < 2 ? w.vsb.x : w.vsb.y, g < 2 ? w.vsb.z : w.vsb.w, sel);
+                        const float fa = group_f(w.vsa, g), fb = group_f(w.vsb, g);
                         const uint32_t wa = __byte_perm(g < 2 ? w.va.x : w.va.y, g < 2 ? w.va.z : w.va.w, sel);
                         const uint32_t wb = __byte_perm(g < 2 ? w.vb.x : w.vb.y, g < 2 ? w.vb.z : w.vb.w, sel);
                         const uint32_t a0[4] = {value_pair<0>(wa), value_pair<1>(wa), value_pair<0>(wb), value_pair<1>(wb)};
                         const uint32_t a1[4] = {value_pair<2>(wa), value_pair<3>(wa), value_pair<2>(wb), value_pair<3>(wb)};
 #pragma unroll
                         for (int c = 0; c < TILES; ++c) {
-                            const uint32_t b0 = mul_bf16x2(pt0[c], sa), b1 = mul_bf16x2(pt1[c], sb);
-                            mma(acc[c][2 * g], a0, b0, b1);
-                            mma(acc[c][2 * g + 1], a1, b0, b1);
+                            const uint32_t b0 = transpose8(pack_f16x2(p[c][0] * fa, p[c][1] * fa));
+                            const uint32_t b1 = transpose8(pack_f16x2(p[c][2] * fb, p[c][3] * fb));
+                            mma_f16(acc[c][2 * g], a0, b0, b1);
+                            mma_f16(acc[c][2 * g + 1], a1, b0, b1);
                         }
                     }
                 }
@@ -604,32 +618,28 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                 issue_first(min(left, 32));
             }
         }
-        // The centers' term, and the row sums over the tokens of the fragments (row
-        // groups r4).
+        // The row sums over the tokens of the fragments (row groups r4), and each warp's
+        // output, normalised, with the centers' term: its reference is then the
+        // log-sum-exp, and warps need not agree on theirs or on the scales' factor.
+        const float vf_back = 1.f / lo_f(vf);
 #pragma unroll
         for (int c = 0; c < TILES; ++c)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float add = __shfl_sync(0xffffffffu, cen[c][j], 4 * g + c4);
-                    acc[c][2 * g][j] += add;
-                    acc[c][2 * g][2 + j] += add;
-                    acc[c][2 * g + 1][j] += add;
-                    acc[c][2 * g + 1][2 + j] += add;
-                }
-#pragma unroll
                 for (int o = 4; o < 32; o <<= 1) lsum[c][j] += __shfl_xor_sync(0xffffffffu, lsum[c][j], o);
-                // Normalised, with the log-sum-exp as the reference: warps need not agree
-                // on theirs.
                 const bool any = lsum[c][j] != 0.f;  // NaN included
                 const float inv = any ? 1.f / lsum[c][j] : 0.f;
                 m[c][j] = any ? m[c][j] + ptx::lg2(lsum[c][j]) : -INFINITY;
                 lsum[c][j] = any ? 1.f : 0.f;
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    acc[c][t][j] *= inv;
-                    acc[c][t][2 + j] *= inv;
+                for (int g = 0; g < 4; ++g) {
+                    const float add = __shfl_sync(0xffffffffu, cen[c][j], 4 * g + c4) * inv;
+#pragma unroll
+                    for (int t = 2 * g; t < 2 * g + 2; ++t) {
+                        acc[c][t][j] = fmaf(acc[c][t][j] * inv, vf_back, add);
+                        acc[c][t][2 + j] = fmaf(acc[c][t][2 + j] * inv, vf_back, add);
+                    }
                 }
             }
         // The four warps' results meet in two rounds: 2 and 3 into 0 and 1, then 1

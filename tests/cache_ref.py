@@ -148,13 +148,14 @@ def attend(q, k, v, scale, hidden=None):
 def check_decode_q4(got, lse, q, cache, table, lens, scale, what=""):
     """attn_decode_paged_q4 against 64 bits.
 
-    Key codes enter the products as 16 + n or 128 + n, the offset is taken off after them; value codes enter as n - 7.5.
-    Scores are fp32 sums of 128 products q s (n + 128) at most: errors of a few steps (16 at most) of the terms' sum,
-    e = 16 * 2^-24 * scale * sum |q| (144 s + |z|); a weight is then off by that share and by ex2's and the merge's few
-    steps (2^-20 in all).  A probability is rounded to bf16, and its product with a scale once more: the value's two
-    parts are off by (1 + HALF)^2 - 1 = 2 HALF + HALF^2 of w |s (n - 7.5)| and HALF of w |z|; fp32 accumulation adds
-    16 * 2^-24 of 8 w s.  Below the normal range a step of a product is 2^-133.  The output is rounded once.  lse moves
-    by at most the largest score error and ln's 2^-20."""
+    Key codes enter the products as 16 + n, the offset is taken off after them; value codes enter as n - 7.5.
+    Scores are fp32 sums of 128 products q s (n + 16): errors of a few steps (16 at most) of the terms' sum,
+    e = 16 * 2^-24 * scale * sum |q| (32 s + |z|); a weight is then off by that share and by ex2's and the merge's few
+    steps (2^-20 in all).  The centers meet probabilities in bf16: HALF of w |z|.  The codes meet probability times scale
+    in f16: 2^-11 of w |s (n - 7.5)|, and for the smallest ones half of f16's last step, 2^-25, times |n - 7.5| <= 7.5,
+    for each key, over the row sum, which is at least 1 / (the largest weight), in units of 1 or, where scales are far
+    from it, of at most 2^-5 of the largest scale.  fp32 accumulation adds 16 * 2^-24 of 8 w s.  The output is rounded
+    once.  lse moves by at most the largest score error and ln's 2^-20."""
     got, lse = got.double().cpu(), lse.double().cpu()
     Hq = q.shape[1]
     for b, L in enumerate(lens):
@@ -165,14 +166,17 @@ def check_decode_q4(got, lse, q, cache, table, lens, scale, what=""):
         kp, vp = read_tokens(cache, table[b], L)
         out, ref_lse, w = attend(qb, values(kp), values(vp), scale)
         G = Hq // cache.shape[1]
-        terms = (144 * kp[1] + kp[2].abs()).repeat_interleave(G, 1)
+        terms = (32 * kp[1] + kp[2].abs()).repeat_interleave(G, 1)
         e = 16 * 2.0 ** -24 * scale * torch.einsum("nhd,lhd->hnl", qb.abs(), terms).amax(-1)     # [Hq, 1]
         share = 2 * e + 2.0 ** -20
-        mag = ((2 + HALF) * (vp[1] * (vp[0] - 7.5)).abs() + vp[2].abs()).repeat_interleave(G, 1)
-        acc = (8 * vp[1]).repeat_interleave(G, 1)
-        wm = torch.einsum("hnl,lhd->nhd", w, mag)
-        bound = HALF * out.abs() + (1 + HALF) * (wm * (HALF + share[:, 0, None]) +
-                                                 2.0 ** -20 * torch.einsum("hnl,lhd->nhd", w, acc)) + 2.0 ** -133
+        codes = (vp[1] * (vp[0] - 7.5)).abs().repeat_interleave(G, 1)
+        centers = vp[2].abs().repeat_interleave(G, 1)
+        wc, wz, ws = (torch.einsum("hnl,lhd->nhd", w, t) for t in (codes, centers, (8 * vp[1]).repeat_interleave(G, 1)))
+        top = vp[1].max()
+        unit = max(1.0 if 2.0 ** -10 <= top < 2.0 ** 7 else 0.0, float(top) * 2.0 ** -5)
+        small = (L * 7.5 * 2.0 ** -25 * unit) * w.amax(-1)                                       # [Hq, 1]
+        bound = HALF * out.abs() + (1 + HALF) * (wc * (2.0 ** -11 + share[:, 0, None]) + wz * (HALF + share[:, 0, None]) +
+                                                 small + 2.0 ** -20 * ws) + 2.0 ** -133
         err = (got[b] - out[0]).abs()
         assert torch.isfinite(got[b]).all() and (err <= bound[0]).all(), \
             f"{what}: sequence {b} (L={L}): worst excess {(err - bound[0]).max():.3g}"
