@@ -449,6 +449,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _device = torch._C._cuda_getDevice
 _bf16 = torch.bfloat16
 _i32 = torch.int32
+_i64 = torch.int64
 
 
 def _refuse(t, name, dtype, dev, contiguous=True):
@@ -465,20 +466,21 @@ def _refuse(t, name, dtype, dev, contiguous=True):
 
 def _in(t, name, dtype, dev):
     """The address of a contiguous tensor of dtype on the current device dev."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass  # not a tensor
     _refuse(t, name, dtype, dev)
-
-
-def _opt(t, name, dtype, dev):
-    return None if t is None else _in(t, name, dtype, dev)
 
 
 def _in_strided(t, name, dev):
     """The address of a bf16 tensor that is contiguous in its last dimension (the others may be strided)."""
-    if (isinstance(t, torch.Tensor) and t.dtype is _bf16 and t.get_device() == dev and t.dim() >= 2 and
-            t.stride(-1) == 1):
-        return t.data_ptr()
+    try:
+        if t.dtype is _bf16 and t.get_device() == dev and t.dim() >= 2 and t.stride(-1) == 1:
+            return t.data_ptr()
+    except AttributeError:
+        pass  # not a tensor
     _refuse(t, name, _bf16, dev, contiguous=False)
 
 
@@ -496,11 +498,6 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _step(t, dim):
-    # the stride of a dimension of length one is never used, whatever it says
-    return 0 if t.shape[dim] == 1 else t.stride(dim)
 
 
 def rope_table(inv_freq, axes=None, *, device="cuda"):
@@ -528,13 +525,16 @@ def rope_table(inv_freq, axes=None, *, device="cuda"):
 
 def _rotate_args(q_weight, k_weight, eps, positions, pos_shape, rope, interleaved, dev):
     """The norm and rotation arguments of a call, checked, in the C order."""
-    wq = _opt(q_weight, "q_weight", _bf16, dev)
-    wk = _opt(k_weight, "k_weight", _bf16, dev)
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and w.shape != (128,):
-            raise ValueError(f"{n} must have 128 elements")
+    wq = wk = pos = None
     n_axes = 1
-    pos = None
+    if q_weight is not None:
+        wq = _in(q_weight, "q_weight", _bf16, dev)
+        if q_weight.shape != (128,):
+            raise ValueError("q_weight must have 128 elements")
+    if k_weight is not None:
+        wk = _in(k_weight, "k_weight", _bf16, dev)
+        if k_weight.shape != (128,):
+            raise ValueError("k_weight must have 128 elements")
     if positions is not None:
         pos = _in(positions, "positions", _i32, dev)
         shape = positions.shape
@@ -545,11 +545,12 @@ def _rotate_args(q_weight, k_weight, eps, positions, pos_shape, rope, interleave
             n_axes = shape[0]
     if rope is None:
         return wq, wk, eps, pos, n_axes, None, 0, interleaved
-    plan = _in(rope, "rope", torch.int64, dev)
-    if rope.dim() != 2 or rope.shape[1] != 2:
+    plan = _in(rope, "rope", _i64, dev)
+    shape = rope.shape
+    if len(shape) != 2 or shape[1] != 2:
         raise ValueError("rope must be a table made by rope_table")
     # the default position is the same on every axis
-    return wq, wk, eps, pos, n_axes if pos else 4, plan, 2 * rope.shape[0], interleaved
+    return wq, wk, eps, pos, n_axes if pos else 4, plan, 2 * shape[0], interleaved
 
 
 def qk_norm_rope(q, k=None, *, rope=None, positions=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -602,11 +603,14 @@ def qk_norm_rope(q, k=None, *, rope=None, positions=None, q_weight=None, k_weigh
     elif k is not None:
         k_out = _empty(k_shape, _bf16, q.device, stream)
         ko = k_out.data_ptr()
+    # the stride of a dimension of length one is never used, whatever it says
+    qs = q.stride()
+    ks = (0,) * len(qs) if k is None else k.stride()
+    many, long = b_dim == 0 and B > 1, S > 1
     rc = lib.attn_qk_norm_rope(
-        qp, kp, qo, ko, *args, B, S, Hq, Hkv, d, LAYOUTS[layout],
-        0 if b_dim is None else _step(q, 0), _step(q, s_dim), _step(q, h_dim),
-        0 if b_dim is None or k is None else _step(k, 0), 0 if k is None else _step(k, s_dim),
-        0 if k is None else _step(k, h_dim), _raw_stream(dev) if stream is None else stream.cuda_stream)
+        qp, kp, qo, ko, *args, B, S, Hq, Hkv, d, LAYOUTS[layout], qs[0] if many else 0, qs[s_dim] if long else 0,
+        qs[h_dim] if Hq > 1 else 0, ks[0] if many else 0, ks[s_dim] if long else 0, ks[h_dim] if Hkv > 1 else 0,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "attn_qk_norm_rope")
     return q_out, k_out
@@ -617,22 +621,21 @@ def _append(fn, q, k, v, pools, Hkv_pool, num_pages, page_size, block_table, seq
     qp = None if q is None else _in_strided(q, "q", dev)
     kp, vp = _in_strided(k, "k", dev), _in_strided(v, "v", dev)
     table, lens = _in(block_table, "block_table", _i32, dev), _in(seqlens, "seqlens", _i32, dev)
-    cu = _opt(cu_seqlens, "cu_seqlens", _i32, dev)
+    cu = None if cu_seqlens is None else _in(cu_seqlens, "cu_seqlens", _i32, dev)
     shape, table_shape = k.shape, block_table.shape
     if len(shape) != 3 or v.shape != shape:
         raise ValueError("k and v must be [tokens, Hkv, 128], of the same shape")
     total, Hkv, d = shape
     B = seqlens.numel()
-    Hq, q_step = 0, 0
+    ks, vs = k.stride(), v.stride()
+    qs, Hq = None, 0
     if q is not None:
-        q_shape = q.shape
+        q_shape, qs = q.shape, q.stride()
         if len(q_shape) != 3 or q_shape[0] != total or q_shape[2] != d:
             raise ValueError("q must be [tokens, Hq, 128], of the tokens and head dimension of k")
         Hq = q_shape[1]
-        q_step = q.stride(0) if total > 1 else Hq * d
-    for t, n, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv)):
-        if h > 1 and t.stride(1) != d:
-            raise ValueError(f"{n} must have the heads of a token contiguous")
+    if (Hq > 1 and qs[1] != d) or (Hkv > 1 and (ks[1] != d or vs[1] != d)):
+        raise ValueError("q, k and v must have the heads of a token contiguous")
     if Hkv != Hkv_pool:
         raise ValueError(f"the cache has {Hkv_pool} KV heads, k and v have {Hkv}")
     if len(table_shape) != 2 or table_shape[0] != B:
@@ -652,7 +655,7 @@ def _append(fn, q, k, v, pools, Hkv_pool, num_pages, page_size, block_table, seq
         q_out = _empty(q_shape, _bf16, q.device, stream)
         qo = q_out.data_ptr()
     rc = fn(qp, kp, vp, qo, *pools, table, lens, cu, *args, B, total, Hq, Hkv, d, page_size, num_pages,
-            table_shape[1], q_step, k.stride(0) if total > 1 else Hkv * d, v.stride(0) if total > 1 else Hkv * d,
+            table_shape[1], *((0 if q is None else qs[0], ks[0], vs[0]) if total > 1 else (Hq * d, Hkv * d, Hkv * d)),
             _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, fn.__name__)
@@ -676,8 +679,8 @@ def append_paged(q, k, v, k_pages, v_pages, block_table, seqlens, cu_seqlens=Non
     if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [num_pages, 16, Hkv, 128]")
     num_pages, page_size, Hkv, d = shape
-    if isinstance(k, torch.Tensor) and k.shape[-1] != d:
-        raise ValueError("k and the pages must have the same head dimension")
+    if d != 128:
+        raise ValueError("k_pages and v_pages must be [num_pages, 16, Hkv, 128]")
     return _append(lib.attn_append_paged, q, k, v, pools, Hkv, num_pages, page_size, block_table, seqlens, cu_seqlens,
                    rope, positions, q_weight, k_weight, eps, interleaved, q_out, stream, dev)
 
