@@ -81,7 +81,9 @@ struct Shape {
     static_assert(CTAS_PER_SM * (SMEM + 1024) <= 233472, "CTAs per SM");
 };
 constexpr int MIN_PAIRS = 4;           // pairs a CTA takes at least, unless there is a KV head for each
-constexpr float RAISE = 8.f;  // a score this far (in log2) above the running max raises it
+constexpr int SLACK_BITS = 8;          // a score this far (in log2) above the largest so far raises the reference
+constexpr float SLACK = SLACK_BITS;
+constexpr int ROOM = 8;  // bits of P given up for scales that grow, before their pages are checked one by one
 constexpr float LN2 = 0.6931471805599453f;
 
 // Codes j and j + 4 of a word as the bf16 pair (16 + n, 16 + n').
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
             parts(-23.5f * x, qo0[c], qo1[c]);
         }
         __syncthreads();
-        // Of each tile: running max (log2 units) and row sum of heads 2 c4, 2 c4 + 1;
+        // Of each tile: running reference (log2 units, see below) and row sum of heads 2 c4, 2 c4 + 1;
         // acc[2 g + i]: channels 32 g + 4 r4 + 2 i (+ 1) times those heads; cen: the
         // centers' term of group r4 % 4.
         float m[TILES][2], lsum[TILES][2], acc[TILES][8][4], cen[TILES][4];
@@ -401,10 +403,13 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
             for (int t = 0; t < 8; ++t) acc[c][t][0] = acc[c][t][1] = acc[c][t][2] = acc[c][t][3] = 0.f;
         }
 
-        // The value scales' common factor, a power of two as a bf16 pair, and the size
-        // (bf16 bits) from which a scale is too large for it (at first: any).
+        // The values' range (see below): the common factor of their scales, a power of two
+        // as a bf16 pair, the size (bf16 bits) from which a scale is too large (at first:
+        // any), and how far above the running reference m a score may lie.
         constexpr uint32_t ONE = 0x3f803f80u;
         uint32_t vf = ONE, vf_limit = 1;
+        float reach = SLACK;
+        int room = 0;  // bits by which `reach` may still shrink
         int base = 0, left = n;
         while (left > 0) {
             const int batch = min(left, 32);
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                     }
                 }
                 // s[u][c][0], [1]: token r4 of page u, heads 8 c + 2 c4, + 1; [2], [3]:
-                // token r4 + 8.  x: over the running max, in log2 units.
+                // token r4 + 8.  x: over the reference m, in log2 units.
                 float x[2][TILES][4];
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
@@ -474,58 +479,107 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                         if (u == lane >> 4 && (lane & 15) >= nv) big = 0;
                     }
                 }
-                // The running max follows only when a score is RAISE above it (the first
-                // keys are: it is -inf).  Probabilities then lie below 2^RAISE with the
-                // largest from 1 on, which costs the sums nothing, and a raise, with its
-                // shuffles and the rescaling, is rare instead of nearly every page.
+                // Probability times scale goes to the product as f16 (11 bits: the values'
+                // part of the output then loses nothing against its own rounding), so
+                // it has to stay below 2^16 and, where it counts, above f16's last steps.
+                // P is taken over a reference m of each head, below its largest score: what a
+                // usual scale (2^e, found in the first pages) makes of the largest P then is
+                // 2^5 or 2^6, and a token 2^19 times less likely still keeps 11 bits.  As
+                // long as no score lies `reach` above m and no scale reaches vf_limit,
+                // 2^15 over 2^reach, nothing can overflow and nothing is done.  Otherwise the
+                // pages' products are bounded head by head, and m follows where it must: a
+                // token that a head does not attend to takes no bits from it, whatever its
+                // scale.  m follows a score SLACK bits late, so raises, with their shuffles
+                // and rescaling, are rare instead of nearly every page.
                 float top = -INFINITY;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int c = 0; c < TILES; ++c)
                         top = fmaxf(top, fmaxf(fmaxf(x[u][c][0], x[u][c][1]), fmaxf(x[u][c][2], x[u][c][3])));
-                // Probability times scale goes to the product as f16 (11 bits: the values'
-                // part of the output then loses nothing against its own rounding), so
-                // it has to stay below 2^16 and, where it counts, above f16's last steps.
-                // Scales below 2^7 are taken as they are when the first pages' largest
-                // is from 2^-10 on; otherwise, and when one outgrows its limit, all are
-                // multiplied by the power of two that brings the largest to 2^5.
-                if (__any_sync(0xffffffffu, top > RAISE || big >= vf_limit)) {
+                if (__any_sync(0xffffffffu, top > reach || big >= vf_limit)) {
                     uint32_t largest = 0;  // finite scale of this lane's token
                     if (big) {
                         const uint32_t h[4] = {vs.x & 0xffffu, vs.x >> 16, vs.y & 0xffffu, vs.y >> 16};
 #pragma unroll
                         for (int g = 0; g < 4; ++g) largest = max(largest, h[g] < 0x7f80u ? h[g] : 0u);
                     }
-                    const uint32_t e = __reduce_max_sync(0xffffffffu, largest) >> 7;  // exponent + 127
-                    const bool plain = vf == ONE && e >= 117 && e < 134;
-                    const uint32_t limit = plain ? 134u << 7 : min((e + 2) << 7, 0x7f80u);
-                    if (limit > vf_limit) {
-                        const uint32_t f = plain ? 127u << 7 : min(259u - e, 254u) << 7;  // 2^(5 - exponent)
-                        const float ratio = __uint_as_float(f << 16) / lo_f(vf);
-                        vf = f * 0x10001u;
-                        vf_limit = limit;
+                    const uint32_t most = __reduce_max_sync(0xffffffffu, largest);
+                    const int e = (int)(most >> 7);  // exponent + 127
+                    bool first_scales = false;
+                    if (vf_limit == 1) {
+                        first_scales = most != 0;
+                        if (first_scales) {
+                            // The tokens' mean exponent, or the largest where that is at most 3 more.
+                            const unsigned some = __ballot_sync(0xffffffffu, largest != 0);
+                            const int mean = (int)(__reduce_add_sync(0xffffffffu, largest >> 7) / __popc(some));
+                            const int usual = min(e, mean + 3);
+                            int factor = 127;  // of vf; 2^-10 .. 2^6 are taken as they are
+                            if (usual >= 117 && usual < 134) {
+                                reach = (float)(5 + SLACK_BITS + 127 - usual);
+                                room = ROOM;
+                            } else {
+                                factor = max(1, min(259 - usual, 254));  // 2^(5 - exponent)
+                            }
+                            vf = (uint32_t)factor * 0x800080u;
+                            vf_limit = (uint32_t)max(1, min(142 - (int)reach - (factor - 127), 255)) << 7;
+                        }
+                    } else if (most >= vf_limit) {
+                        const int ev = (int)(vf >> 23) - 127;
+                        if (e + ev >= 227) {
+                            // 2^100 times too large: all start again from this scale.
+                            const int factor = max(1, 259 - e);
+                            const float ratio = __uint_as_float((uint32_t)factor << 23) / lo_f(vf);
+                            vf = (uint32_t)factor * 0x800080u;
+                            reach = SLACK;
+                            room = 0;
+                            vf_limit = (uint32_t)min(134 - (factor - 127), 255) << 7;
 #pragma unroll
-                        for (int c = 0; c < TILES; ++c)
+                            for (int c = 0; c < TILES; ++c)
 #pragma unroll
-                            for (int t = 0; t < 8; ++t)
+                                for (int t = 0; t < 8; ++t)
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) acc[c][t][j] *= ratio;
+                                    for (int j = 0; j < 4; ++j) acc[c][t][j] *= ratio;
+                        } else {
+                            // Larger than usual: the limit follows for a few bits.
+                            const int up = min(e + 1 - (int)(vf_limit >> 7), room);
+                            room -= up;
+                            reach -= (float)up;
+                            vf_limit += (uint32_t)up << 7;
+                        }
                     }
+                    const float lift = reach - SLACK;  // the largest score's distance from m
+                    // A bound on log2 of the scales' size, of this lane's token; log2 vf.
+                    const float size = largest ? (float)((int)(largest >> 7) - 126) : -INFINITY;
+                    const float vf_log2 = (float)((int)(vf >> 23) - 127);
+                    const float sizes[2][2] = {
+                        {__shfl_sync(0xffffffffu, size, r4), __shfl_sync(0xffffffffu, size, r4 + 8)},
+                        {__shfl_sync(0xffffffffu, size, r4 + 16), __shfl_sync(0xffffffffu, size, r4 + 24)}};
 #pragma unroll
                     for (int c = 0; c < TILES; ++c) {
-                        float y[2] = {-INFINITY, -INFINITY};
+                        // The largest score, and the largest log2 of probability times scale.
+                        float y[2] = {-INFINITY, -INFINITY}, z[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                if (x[u][c][j] != -INFINITY) y[j & 1] = fmaxf(y[j & 1], s[u][c][j] * sl2);
+                                if (x[u][c][j] != -INFINITY) {
+                                    const float v = s[u][c][j] * sl2;
+                                    y[j & 1] = fmaxf(y[j & 1], v);
+                                    z[j & 1] = fmaxf(z[j & 1], v + sizes[u][j >> 1]);
+                                }
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                            for (int o = 4; o < 32; o <<= 1)
+                            for (int o = 4; o < 32; o <<= 1) {
                                 y[j] = fmaxf(y[j], __shfl_xor_sync(0xffffffffu, y[j], o));
-                            const float mx = fmaxf(m[c][j], y[j]);
+                                z[j] = fmaxf(z[j], __shfl_xor_sync(0xffffffffu, z[j], o));
+                            }
+                            z[j] += vf_log2;
+                            // (with the first scales, m may go down: acc is still 0)
+                            float mx = first_scales ? m[c][j] - lift : m[c][j];
+                            if (first_scales || y[j] - m[c][j] > reach || z[j] - m[c][j] > 15.f)
+                                mx = fmaxf(mx, fmaxf(y[j] - lift, z[j] - 7.f));
                             const float a = m[c][j] == -INFINITY ? (mx == -INFINITY ? 1.f : 0.f) : ptx::ex2(m[c][j] - mx);
                             lsum[c][j] *= a;
                             cen[c][j] *= a;

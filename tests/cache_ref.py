@@ -145,6 +145,49 @@ def attend(q, k, v, scale, hidden=None):
     return torch.einsum("hnl,lhd->nhd", w, vv), lse.T, w
 
 
+def reference_unit(scales):
+    """2^(e + 3) for the largest e that a warp's first page pair with a scale can give as its usual exponent: the
+    tokens' mean one, or the pair's largest where that is at most 3 more.  scales [L, 4] of one KV head."""
+    top = scales.double().amax(-1)
+    top = torch.cat([top, torch.zeros(-len(top) % (2 * PAGE))]).view(-1, 2 * PAGE)
+    ex = torch.where(top > 0, torch.floor(torch.log2(top.clamp_min(2.0 ** -127))), torch.zeros_like(top))
+    n = (top > 0).sum(-1)
+    usual = torch.minimum(torch.where(top > 0, ex, ex - 1000).amax(-1), torch.floor(ex.sum(-1) / n.clamp_min(1)) + 3)
+    return 2.0 ** (float(usual[n > 0].max()) + 3) if (n > 0).any() else 0.0
+
+
+def check_decode_q4_mixed(got, lse, q, cache, table, lens, scale, what=""):
+    """check_decode_q4 for values of very different scales.  The same terms, but a key's weight is off by its own
+    score's error and the weighted mean of the others', and f16's last steps are counted in the units that the kernel
+    promises: P is taken over a reference below the head's largest score so that a usual scale 2^e makes at least 2^5
+    of the largest P, 8 bits less where larger scales follow (2^-25 of that is w_max 2^(e + 3) 2^-25), or, where a
+    product P s lies 2^15 above, so that the largest is 2^5 or more."""
+    got, lse = got.double().cpu(), lse.double().cpu()
+    Hq, Hkv = q.shape[1], cache.shape[1]
+    G = Hq // Hkv
+    for b, L in enumerate(lens):
+        qb = q[b:b + 1].double()
+        kp, vp = read_tokens(cache, table[b], L)
+        out, ref_lse, w = attend(qb, values(kp), values(vp), scale)
+        terms = (32 * kp[1] + kp[2].abs()).repeat_interleave(G, 1)
+        e = 16 * 2.0 ** -24 * scale * torch.einsum("nhd,lhd->hnl", qb.abs(), terms)              # [Hq, 1, L]
+        ws = w * (e + (w * e).sum(-1, keepdim=True) + 2.0 ** -20)
+        codes = (vp[1] * (vp[0] - 7.5)).abs().repeat_interleave(G, 1)
+        centers = vp[2].abs().repeat_interleave(G, 1)
+        s8 = vp[1].repeat_interleave(G, 1)
+        mix = lambda a, t: torch.einsum("hnl,lhd->nhd", a, t)  # noqa: E731
+        unit = torch.tensor([reference_unit(vp[1][:, h, ::GROUP]) for h in range(Hkv)]).repeat_interleave(G)
+        largest = torch.einsum("hnl,lh->hnl", w, s8.amax(-1)).amax(-1)[:, 0]                     # [Hq]
+        small = (L * 7.5 * 2.0 ** -25) * torch.maximum(unit * w.amax(-1)[:, 0], largest * 2.0 ** -5)
+        bound = HALF * out.abs() + (1 + HALF) * (mix(w, codes) * 2.0 ** -11 + mix(ws, codes) + mix(w, centers) * HALF +
+                                                 mix(ws, centers) + small[:, None] + 2.0 ** -17 * mix(w, s8)) + 2.0 ** -133
+        err = (got[b] - out[0]).abs()
+        assert torch.isfinite(got[b]).all() and (err <= bound[0]).all(), \
+            f"{what}: sequence {b} (L={L}): worst ratio {(err / bound[0]).max():.3g}, {(err > bound[0]).sum()} elements"
+        lerr = (lse[b] - ref_lse[0]).abs()
+        assert (lerr <= e.amax(-1)[:, 0] + 2.0 ** -20 * (1 + ref_lse[0].abs())).all(), f"{what}: lse off by {lerr.max():.3g}"
+
+
 def check_decode_q4(got, lse, q, cache, table, lens, scale, what=""):
     """attn_decode_paged_q4 against 64 bits.
 

@@ -100,6 +100,56 @@ def test_decode_extreme_values_and_queries(A):
         R.check_decode_q4(out, lse, q, cache, table, [L], SCALE, f"v {v_scale} k {k_scale} q {q_scale}")
 
 
+def _mixed(lens, Hkv, G, kind, seed):
+    """(q, cache, table): channel 0 of the queries is 8 (-8 in every fourth head), so that a key's channel 0 decides
+    how likely its token is."""
+    g = torch.Generator().manual_seed(seed)
+    pages = [(x + 15) // 16 for x in lens]
+    table = torch.zeros(len(lens), max(pages), dtype=torch.int32)
+    perm = torch.randperm(sum(pages), generator=g).to(torch.int32)
+    cache = torch.full((sum(pages), Hkv, R.BLOCK), 0xff, dtype=torch.uint8)
+    off = 0
+    for b, L in enumerate(lens):
+        table[b, :pages[b]] = perm[off:off + pages[b]]
+        off += pages[b]
+        t = torch.arange(L)
+        k, v = (torch.randn(L, Hkv, 128, generator=g) for _ in range(2))
+        if kind.startswith("hidden"):                  # large values that most heads do not attend to
+            rare = torch.rand(L, Hkv, generator=g) < 0.02
+            rare[0] = False
+            k[..., 0][rare] = -40.0
+            v[rare] *= 2.0 ** int(kind[6:])
+        elif kind == "sink":                           # small values behind a likely token with next to none
+            v *= 2.0 ** -7
+            v[0] *= 2.0 ** -6
+            k[0, :, 0] = 14.0
+        elif kind == "growing":
+            v *= 2.0 ** (t / L * 60 - 30)[:, None, None]
+        elif kind == "shrinking":
+            v *= 2.0 ** (30 - t / L * 60)[:, None, None]
+        else:                                          # zeros, or tiny values, in the first pages
+            v[:L * 2 // 3] *= 0.0 if kind == "zeros" else 2.0 ** -100
+        for h in range(Hkv):
+            R.write_tokens(cache, table[b].long()[t // 16], t % 16, torch.full_like(t, h), k[:, h].to(torch.bfloat16),
+                           v[:, h].to(torch.bfloat16))
+    q = torch.randn(len(lens), Hkv * G, 128, generator=g)
+    q[..., 0] = 8.0
+    q[:, 3::4, 0] = -8.0
+    return q.to(torch.bfloat16), cache, table
+
+
+@pytest.mark.parametrize("kind", ["hidden12", "hidden20", "hidden36", "sink", "growing", "shrinking", "zeros", "tiny"])
+@pytest.mark.parametrize("lens,Hkv,G", [([600, 33, 2, 64, 2000], 2, 4), ([1500] * 24, 8, 4), ([700, 47, 1900], 2, 12)])
+def test_decode_values_of_very_different_scales(A, lens, Hkv, G, kind):
+    """A token that a head does not attend to takes no precision from it, whatever its scale; scales that grow and
+    shrink by 2^60 along a sequence; pages of zeros or of next to nothing before the others."""
+    q, cache, table = _mixed(lens, Hkv, G, kind, seed=len(lens) + G)
+    out, lse = A.decode_paged_q4(q.cuda(), cache.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert A.device_status()[0] == 0
+    R.check_decode_q4_mixed(out, lse, q, cache, table, lens, SCALE, kind)
+
+
 def test_decode_is_deterministic_and_takes_given_outputs(A):
     q, cache, table, dl, out, lse = _decode(A, [900, 1, 3000], 8, 2, seed=7)
     ws = torch.full((A.decode_q4_workspace_bytes(3, 8, 2, 128, table.shape[1]),), 0xff, dtype=torch.uint8, device="cuda")
