@@ -669,7 +669,7 @@ def append_paged(q, k, v, k_pages, v_pages, block_table, seqlens, cu_seqlens=Non
     q [total, Hq, 128] (or None), k and v [total, Hkv, 128] bf16, the sequences' new tokens back to back (views of a
     fused projection need no copy); k_pages, v_pages [num_pages, 16, Hkv, 128] bf16, updated in place; block_table
     [B, max_blocks], seqlens [B] (the lengths WITH the new tokens) and cu_seqlens [B + 1] int32 (None: one token per
-    sequence).  positions: int32 [total] or [axes, total], default: each token's position in its cache.  Returns
+    sequence, none where the length is 0).  positions: int32 [total] or [axes, total], default: each token's position in its cache.  Returns
     q_out [total, Hq, 128] (None without q): the q of fwd_paged or decode_paged over the same arrays.
     """
     lib = _lib or load()

@@ -7,6 +7,12 @@
 // rows of one token (norm_rope.cuh has the lane layout): their loads are all in
 // flight before the first is used, and the token's angles are computed once for
 // the U rows.
+//
+// Measured on one GB300 (copy bandwidth 6781 GB/s): norm and rotation of 32760
+// tokens, 12 + 12 heads (403 MB) 71 us, 0.84 of it; the append of 18 thousand
+// tokens, 32 / 8 heads, into bf16 pages (464 MB) 73 us, 0.94.  Into the 4-bit cache
+// the same tokens take 95 us: there the quantisation's instructions are the bound
+// (3.1 of 4 issued per clock).
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -82,7 +88,8 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormRopeParams
 
 // Where a new token goes: its sequence's position for it, and its page (-1: a
 // bad table entry, already reported).  Returns false when the token belongs to
-// no sequence or its sequence is malformed (reported).  The whole warp takes part.
+// no sequence, its row is idle or its sequence is malformed (reported).  The
+// whole warp takes part.
 __device__ __forceinline__ bool locate(const AppendParams &p, const Place &at, int *slot, int64_t *page) {
     const int t = (int)at.token;
     int b = t, begin = t, end = t + 1;
@@ -115,6 +122,7 @@ __device__ __forceinline__ bool locate(const AppendParams &p, const Place &at, i
     }
     if (!ok) return false;
     const int L = __ldg(p.seqlens + b);
+    if (L == 0 && !p.cu) return false;  // an idle row of a batch of single tokens
     if (L < end - begin || L > p.max_blocks * 16) {
         if (at.l == 0) report_status(p.r.status, kStatusDeviceBounds, kSiteAppendSlot);
         return false;

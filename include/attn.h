@@ -430,7 +430,9 @@ attn_status_t attn_qk_norm_rope(const void *q, const void *k, void *q_out, void 
  *      seqlens_k[b] - n + i.  So the same arrays serve the append and the
  *      attention after it.
  * positions: int32 [n_axes][total], or NULL: the token's position in the cache.
- * Rows of no sequence are neither read into the cache nor written to q_out.
+ * Rows of no sequence are neither read into the cache nor written to q_out, nor,
+ * without cu_seqlens, are rows whose seqlens_k is 0 (idle rows of a batch of
+ * fixed size, whose attention is 0).
  * Offsets out of order or range, a length below the sequence's new tokens or
  * past the table, and a page outside [0, num_pages) are recorded as
  * ATTN_ERR_DEVICE_BOUNDS; the tokens they concern are skipped (a bad page: only

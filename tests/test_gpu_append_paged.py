@@ -277,3 +277,77 @@ def test_captured_appends_replay_with_new_lengths(A):
     qe = A.append_paged(dq, dk, dv, ke, ve, dt, dl, rope=rope)
     torch.cuda.synchronize()
     assert torch.equal(kpc, ke) and torch.equal(vpc, ve) and torch.equal(q_out, qe) and A.device_status()[0] == 0
+
+
+def test_idle_rows_of_a_batch_of_single_tokens(A):
+    """A batch of fixed size: rows of length 0 are skipped by the append and attend to nothing."""
+    qkv, q, k, v, kp, vp, table, lens, cu = _case((1,) * 5, (14, 0, 16, 0, 100), 4, 2, seed=41)
+    lens[[1, 3]] = 0
+    dq, dk, dv = _split(qkv.cuda(), 4, 2)
+    live = [0, 2, 4]
+    want_k, want_v = kp.cuda(), vp.cuda()
+    want_q = A.append_paged(dq[live], dk[live], dv[live], want_k, want_v, table[live].cuda(), lens[live].cuda())
+    ke, ve = kp.cuda(), vp.cuda()
+    q_out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    A.append_paged(dq, dk, dv, ke, ve, table.cuda(), lens.cuda(), q_out=q_out)
+    cache = torch.zeros(kp.shape[0], 2, R.BLOCK, dtype=torch.uint8, device="cuda")
+    q4_out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    A.append_paged_q4(dq, dk, dv, cache, table.cuda(), lens.cuda(), q_out=q4_out)
+    out, lse = A.decode_paged_q4(q4_out, cache, table.cuda(), lens.cuda())
+    assert A.device_status()[0] == 0
+    assert torch.equal(ke, want_k) and torch.equal(ve, want_v)
+    assert torch.equal(q_out[live], want_q) and torch.equal(q4_out, q_out) and (q_out[[1, 3]] == 7.0).all()
+    assert (out[[1, 3]] == 0).all() and torch.isneginf(lse[[1, 3]]).all() and torch.isfinite(lse[live]).all()
+    # with offsets, a sequence of no length that has a token is still an error
+    A.append_paged(dq, dk, dv, ke, ve, table.cuda(), lens.cuda(), cu.cuda())
+    assert A.device_status()[0] == 6
+
+
+def test_queries_in_place(A):
+    qkv, q, k, v, kp, vp, table, lens, cu = _case((3, 1, 18, 0, 9), (14, 0, 16, 5, 100), 6, 2, seed=42, pad=4)
+    rope = A.rope_table(R.inv_freq(96))
+    w = (torch.rand(128) + 0.5).to(torch.bfloat16).cuda()
+    for inter in (False, True):
+        for fn, pools in ((A.append_paged, (kp.cuda(), vp.cuda())),
+                          (A.append_paged_q4, (torch.zeros(kp.shape[0], 2, R.BLOCK, dtype=torch.uint8).cuda(),))):
+            rest = (k.contiguous().cuda(), v.contiguous().cuda(), *pools, table.cuda(), lens.cuda(), cu.cuda())
+            want = fn(q.contiguous().cuda(), *rest, rope=rope, q_weight=w, interleaved=inter)
+            mine = q.contiguous().cuda()
+            assert fn(mine, *rest, rope=rope, q_weight=w, interleaved=inter, q_out=mine) is mine
+            n = int(cu[-1])
+            assert torch.equal(mine[:n], want[:n]) and torch.equal(mine[n:].cpu(), q[n:])
+    assert A.device_status()[0] == 0
+
+
+def test_offsets_past_32_bits(A):
+    """Pages behind the 2^31st element of the bf16 pools and the 2^32nd byte of the 4-bit cache."""
+    Hkv, P = 8, 270000
+    if torch.cuda.get_device_properties(0).total_memory < 2**35:
+        pytest.skip("needs 16 GB")
+    new, lens = (20, 1), torch.tensor([36, 18], dtype=torch.int32)
+    g = torch.Generator().manual_seed(43)
+    k, v = (torch.randn(21, Hkv, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.randn(2, 16, 128, generator=g).to(torch.bfloat16).cuda()
+    cu = torch.tensor((0,) + new).cumsum(0).to(torch.int32).cuda()
+    cu_k = torch.tensor([0, 36, 54], dtype=torch.int32).cuda()
+    res = []
+    for pages, first in ((6, 0), (P, P - 6)):
+        table = (torch.tensor([[5, 0, 3], [1, 4, -1]], dtype=torch.int32) + first).clamp_min(-1).cuda()
+        kp, vp = (torch.empty(pages, 16, Hkv, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        kp[first:] = 0
+        vp[first:] = 0
+        A.append_paged(None, k, v, kp, vp, table, lens.cuda(), cu)
+        part = [kp[first:].clone(), vp[first:].clone()]
+        del kp, vp
+        cache = torch.empty(2 * pages if first else pages, Hkv, R.BLOCK, dtype=torch.uint8, device="cuda")
+        skip = cache.shape[0] - pages
+        cache[skip + first:] = 0
+        table += skip
+        A.append_paged_q4(None, k, v, cache, table, lens.cuda(), cu)
+        out, lse = A.decode_paged_q4(q, cache, table, lens.cuda())
+        kk, vv = A.gather_paged_q4(cache, table, lens.cuda(), cu_k)
+        o2, l2 = A.fwd_paged_q4(q, cache, table, lens.cuda(), torch.tensor([0, 1, 2], dtype=torch.int32).cuda())
+        assert A.device_status()[0] == 0
+        res.append(part + [cache[skip + first:].clone(), out, lse, kk, vv, o2, l2])
+        del cache
+    assert all(torch.equal(a, b) for a, b in zip(*res))
