@@ -7,17 +7,21 @@
 // most 440 instructions, half of that to the integer pipe, so the arithmetic decides
 // the form as much as the bytes do:
 //
-// - Codes go to the tensor cores without being turned into cache values.  A code n
-//   moved to bits 3..6 of a bf16 whose other bits say 16.0 is the number 16 + n
-//   exactly: a shift and an and/or for two codes.
+// - Codes go to the tensor cores without being turned into cache values.  A bf16
+//   whose bits are those of a code n in its own place (bits 0..3 or 4..7) and zero
+//   elsewhere is the number n 2^-133 or n 2^-129, subnormal or just above: a mask
+//   makes the operand of two codes, a shift brings the other half of the word.  The
+//   queries carry the powers of two, 2^k and 2^(k-4), k at most 100.
 // - S^T = K Q^T (mma m16n8k16, the page's 16 tokens as rows, eight query heads of
 //   the KV head as columns), a product for each group of 32 channels:
-//       s_t += scale_tg * (sum_c q_c (16 + n_tc) - 23.5 Q_g) + center_tg * Q_g,
+//       s_t += scale_tg * (sum_c q_c n_tc - 7.5 Q_g) + center_tg * Q_g,
 //   with Q_g the sum of the group's q.  Both terms with Q_g are two more products
-//   for all groups at once, Q_g and -23.5 Q_g cut into three bf16 parts (24 bits).
-// - O^T += V^T P^T: value codes become n - 7.5 by one packed addition, and a group's
-//   scale goes to the probability, P'_t = P_t scale_tg; the centers' term is one
-//   product with the unscaled P.
+//   for all groups at once, Q_g and -7.5 Q_g cut into three bf16 parts (24 bits).
+// - O^T += V^T P^T: value codes are f16 in their own places too, and become n - 7.5
+//   (times 2^-9) by one packed multiply-add; a group's scale goes to the probability,
+//   P'_t = P_t scale_tg; the centers' term is one product with the unscaled P.  (Masked
+//   codes as they are, with 7.5 sum P' from four more products, took 152 us
+//   where this takes 149: a product is dearer than eight packed multiply-adds.)
 // - The byte order of the block (q4.cuh) is that of the fragments: every lane
 //   reads its operands as 16-byte words without bank conflicts, and a value
 //   pair of two tokens is one byte permutation.
@@ -29,7 +33,7 @@
 // head); a segment that is a whole sequence is finished by its CTA, the parts of
 // a cut one go to the workspace and are merged by log-sum-exp in the order of the
 // keys.  Ragged lengths thus cost nothing: with a grid of fixed splits over the
-// table's width the same page loop took 177 us instead of 168.
+// table's width an earlier page loop took 177 us instead of 168.
 //
 // In a segment each warp streams page pairs w, w + 4, .. through a ring of its own
 // (bulk copies issued by its lane 0 as soon as a slot has been read): no producer
@@ -39,12 +43,13 @@
 // With P' in bf16, as the bf16 decode's P, the output's error against 64 bits was
 // 2.4e-3 (its own rounding alone makes 1.7e-3) instead of 1.8e-3, in 0.97 of the time.
 //
-// Measured on 64 sequences of 0 to 16384 tokens, 64 / 8 heads (758 MB): 167 us,
-// 4.5 TB/s, 0.67 of the copy bandwidth; the copies alone take 124 us, the
-// arithmetic alone about 145.  On 32 sequences of 1024 to 8192 tokens, 32 / 8 heads
-// (177 MB): 50 us, 0.52; half the MMA columns are empty there, and about 6 us are
-// the two launches' ends.  3 sequences of about 100 thousand tokens, 32 / 1 heads
-// (55 MB): 49 us, the unpacking of two tiles' pages twice.
+// Measured on 64 sequences of 0 to 16384 tokens, 64 / 8 heads (758 MB): 152 us,
+// 5.0 TB/s, 0.74 of the copy bandwidth; the copies alone take 124 us.  On 32 sequences
+// of 1024 to 8192 tokens, 32 / 8 heads (177 MB): 46.5 us, 0.56; half the MMA columns are
+// empty there, and about 6 us are the two launches' ends.  3 sequences of about 100
+// thousand tokens, 32 / 1 heads (55 MB): 48 us, the unpacking of two tiles' pages twice
+// (with one tile a CTA, four times: 50).  With codes as 16 + n and n - 7.5, each by a
+// shift and an and/or (and an addition), these took 167, 50 and 49 us.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -86,14 +91,10 @@ constexpr float SLACK = SLACK_BITS;
 constexpr int ROOM = 8;  // bits of P given up for scales that grow, before their pages are checked one by one
 constexpr float LN2 = 0.6931471805599453f;
 
-// Codes j and j + 4 of a word as the bf16 pair (16 + n, 16 + n').
+// Codes J and J + 4 of a word as a bf16 pair: n 2^-133 (even J) or n 2^-129 (odd J).
 template <int J>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, 0x00780078, %2, 0xEA;"  // (bits & mask) | 16.0
-        : "=r"(r)
-        : "r"(J == 0 ? w << 3 : w >> (J == 0 ? 0 : 4 * J - 3)), "r"(0x41804180u));
-    return r;
+    return (J < 2 ? w : w >> 8) & (J & 1 ? 0x00f000f0u : 0x000f000fu);
 }
 
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
@@ -121,16 +122,19 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A pair's values n - 7.5 as f16, exactly: a code moved to bits 6..9 of an f16 that
-// otherwise says 16.0 is 16 + n, 23.5 comes off.
+// A pair's values (n - 7.5) 2^-9 as f16, exactly.  A code in bits 0..3 of an f16
+// whose other bits are zero is the (subnormal) number n 2^-24, one in bits 4..7
+// n 2^-20: for two of a half-word's four codes no shift, one multiply-add.
 template <int J>
 __device__ __forceinline__ uint32_t value_pair(uint32_t w) {
-    uint32_t r, d;
-    const uint32_t t = J == 0 ? w << 6 : J == 1 ? w << 2 : w >> (J < 2 ? 0 : 4 * J - 6);
-    asm("lop3.b32 %0, %1, 0x03c003c0, %2, 0xEA;" : "=r"(r) : "r"(t), "r"(0x4c004c00u));
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(r), "r"(0xcde0cde0u));
+    uint32_t d;
+    const uint32_t t = (J < 2 ? w : w >> 8) & (J & 1 ? 0x00f000f0u : 0x000f000fu);
+    asm("fma.rn.f16x2 %0, %1, %2, %3;"
+        : "=r"(d)
+        : "r"(t), "r"(J & 1 ? 0x68006800u : 0x78007800u), "r"(0xa380a380u));  // 2^11 or 2^15, -7.5 * 2^-9
     return d;
 }
+constexpr float VALUE_STEPS = 512.f;  // 2^9
 
 // mma with f16 operands.
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -290,7 +294,6 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
     const int64_t page_step = (int64_t)p.Hkv * BLOCK;
     // The byte selector that doubles group c4's entry of four bf16.
     const uint32_t own = 0x1010u + 0x2222u * c4;
-    const float sl2 = p.scale_log2;
     int slot = 0;
     uint32_t parity = 0;
 
@@ -357,24 +360,45 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
         // 32 g + 8 c4 + (j, j + 4), j = 0..3, in the order of a key word's pairs.
         // qz, qo: B operands of the centers' and the scales' products, two each: at
         // k = 2 c4, 2 c4 + 1 (centers) and 2 c4 + 8, 2 c4 + 9 (scales) the first two
-        // bf16 parts of group c4's Q_g and of -23.5 Q_g, then the third part.
+        // bf16 parts of group c4's Q_g and of -7.5 Q_g, then the third part.
         // The fragments are the same in every warp and stay in shared memory: one
         // 16-byte read a group and page is cheaper than 16 registers.
+        // A head's all carry 2^k, k such that its largest q stays below 2^127: scores come
+        // out times 2^(k - 133), which goes into the softmax's factor sl2.
+        float sl2[TILES][2];
         uint32_t qz0[TILES], qz1[TILES], qo0[TILES], qo1[TILES];
 #pragma unroll
         for (int c = 0; c < TILES; ++c) {
             const uint4 *qrow =
                 reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + (row0 + 8 * c + r4) * D);
+            uint4 v[4];
+            uint32_t largest = 0;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                v[g] = 8 * c + r4 < cols ? __ldg(qrow + 4 * g + c4) : make_uint4(0, 0, 0, 0);
+                constexpr uint32_t SIZE = 0x7fff7fffu;
+                largest = __vmaxu2(largest, __vmaxu2(__vmaxu2(v[g].x & SIZE, v[g].y & SIZE),
+                                                     __vmaxu2(v[g].z & SIZE, v[g].w & SIZE)));
+            }
+            largest = max(largest & 0xffffu, largest >> 16);
+            largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
+            largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
+            const int k = max(7, min(100, 253 - (int)(largest >> 7)));
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                sl2[c][j] = p.scale_log2 * __uint_as_float((uint32_t)(260 - __shfl_sync(0xffffffffu, k, 4 * (2 * c4 + j)))
+                                                           << 23);  // 2^(133 - k)
+            const uint32_t even = (uint32_t)(k + 127) * 0x800080u, odd = (uint32_t)(k + 123) * 0x800080u;
             float x = 0.f;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const uint4 v = 8 * c + r4 < cols ? __ldg(qrow + 4 * g + c4) : make_uint4(0, 0, 0, 0);
                 if (warp == g)
-                    q_frag[(4 * c + g) * 32] =
-                        make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                   __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-                float s = ((lo_f(v.x) + hi_f(v.x)) + (lo_f(v.y) + hi_f(v.y))) +
-                          ((lo_f(v.z) + hi_f(v.z)) + (lo_f(v.w) + hi_f(v.w)));
+                    q_frag[(4 * c + g) * 32] = make_uint4(mul_bf16x2(__byte_perm(v[g].x, v[g].z, 0x5410), even),
+                                                          mul_bf16x2(__byte_perm(v[g].x, v[g].z, 0x7632), odd),
+                                                          mul_bf16x2(__byte_perm(v[g].y, v[g].w, 0x5410), even),
+                                                          mul_bf16x2(__byte_perm(v[g].y, v[g].w, 0x7632), odd));
+                float s = ((lo_f(v[g].x) + hi_f(v[g].x)) + (lo_f(v[g].y) + hi_f(v[g].y))) +
+                          ((lo_f(v[g].z) + hi_f(v[g].z)) + (lo_f(v[g].w) + hi_f(v[g].w)));
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
                 if (g == c4) x = s;
@@ -386,8 +410,9 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                 b0 = h0 | h1 << 16;
                 b1 = ptx::pack_bf16x2(v1 - lo_f(h1), 0.f) & 0xffffu;
             };
+            x *= __uint_as_float((uint32_t)(k - 6) << 23);  // 2^(k - 133)
             parts(x, qz0[c], qz1[c]);
-            parts(-23.5f * x, qo0[c], qo1[c]);
+            parts(-7.5f * x, qo0[c], qo1[c]);
         }
         __syncthreads();
         // Of each tile: running reference (log2 units, see below) and row sum of heads 2 c4, 2 c4 + 1;
@@ -458,7 +483,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
 #pragma unroll
                     for (int c = 0; c < TILES; ++c)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) x[u][c][j] = fmaf(s[u][c][j], sl2, -m[c][j & 1]);
+                        for (int j = 0; j < 4; ++j) x[u][c][j] = fmaf(s[u][c][j], sl2[c][j & 1], -m[c][j & 1]);
                 // The scales of one token's values for the check below: lane = page x token.
                 const uint2 vs =
                     *reinterpret_cast<const uint2 *>(blk + (lane >> 4) * BLOCK + q4::V_SCALES + (lane & 15) * 8);
@@ -564,7 +589,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 if (x[u][c][j] != -INFINITY) {
-                                    const float v = s[u][c][j] * sl2;
+                                    const float v = __fmul_rn(s[u][c][j], sl2[c][j & 1]);
                                     y[j & 1] = fmaxf(y[j & 1], v);
                                     z[j & 1] = fmaxf(z[j & 1], v + sizes[u][j >> 1]);
                                 }
@@ -576,7 +601,9 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                                 z[j] = fmaxf(z[j], __shfl_xor_sync(0xffffffffu, z[j], o));
                             }
                             z[j] += vf_log2;
-                            // (with the first scales, m may go down: acc is still 0)
+                            // (with the first scales, m may go down: acc is still 0; products are
+                            // rounded on their own here, or scores of 2^31, whose last step
+                            // is above the exponential's range, would miss their own maximum)
                             float mx = first_scales ? m[c][j] - lift : m[c][j];
                             if (first_scales || y[j] - m[c][j] > reach || z[j] - m[c][j] > 15.f)
                                 mx = fmaxf(mx, fmaxf(y[j] - lift, z[j] - 7.f));
@@ -594,7 +621,8 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                         for (int u = 0; u < 2; ++u)
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                if (x[u][c][j] != -INFINITY) x[u][c][j] = fmaf(s[u][c][j], sl2, -m[c][j & 1]);
+                                if (x[u][c][j] != -INFINITY)
+                                    x[u][c][j] = __fsub_rn(__fmul_rn(s[u][c][j], sl2[c][j & 1]), m[c][j & 1]);
                     }
                 }
 #pragma unroll
@@ -691,8 +719,8 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                     const float add = __shfl_sync(0xffffffffu, cen[c][j], 4 * g + c4) * inv;
 #pragma unroll
                     for (int t = 2 * g; t < 2 * g + 2; ++t) {
-                        acc[c][t][j] = fmaf(acc[c][t][j] * inv, vf_back, add);
-                        acc[c][t][2 + j] = fmaf(acc[c][t][2 + j] * inv, vf_back, add);
+                        acc[c][t][j] = fmaf(acc[c][t][j] * (inv * VALUE_STEPS), vf_back, add);
+                        acc[c][t][2 + j] = fmaf(acc[c][t][2 + j] * (inv * VALUE_STEPS), vf_back, add);
                     }
                 }
             }

@@ -191,8 +191,8 @@ def check_decode_q4_mixed(got, lse, q, cache, table, lens, scale, what=""):
 def check_decode_q4(got, lse, q, cache, table, lens, scale, what=""):
     """attn_decode_paged_q4 against 64 bits.
 
-    Key codes enter the products as 16 + n, the offset is taken off after them; value codes enter as n - 7.5.
-    Scores are fp32 sums of 128 products q s (n + 16): errors of a few steps (16 at most) of the terms' sum,
+    Key codes enter the products as they are (n <= 15), 7.5 is taken off after them; value codes enter as n - 7.5.
+    Scores are fp32 sums of 128 products q s n and 7.5 q s: errors of a few steps (16 at most) of the terms' sum,
     e = 16 * 2^-24 * scale * sum |q| (32 s + |z|); a weight is then off by that share and by ex2's and the merge's few
     steps (2^-20 in all).  The centers meet probabilities in bf16: HALF of w |z|.  The codes meet probability times scale
     in f16: 2^-11 of w |s (n - 7.5)|, and for the smallest ones half of f16's last step, 2^-25, times |n - 7.5| <= 7.5,

@@ -150,6 +150,31 @@ def test_decode_values_of_very_different_scales(A, lens, Hkv, G, kind):
     R.check_decode_q4_mixed(out, lse, q, cache, table, lens, SCALE, kind)
 
 
+@pytest.mark.parametrize("Hq", [8, 16])
+def test_decode_heads_of_very_different_queries(A, Hq):
+    """Queries of 2^-60 to 2^118 beside the usual ones; heads of NaN or infinities leave the others' bits alone."""
+    lens = [150, 40, 1]
+    cache, table, dl = _cache(lens, 1, seed=70)
+    q = torch.randn(3, Hq, 128, generator=torch.Generator().manual_seed(71))
+    run = lambda q: A.decode_paged_q4(q.cuda(), cache.cuda(), table.cuda(), dl.cuda())  # noqa: E731
+    for big in (30, 100, 118):
+        x = q.clone()
+        x[:, 1] *= 2.0 ** big
+        x[:, 3] *= 2.0 ** -60
+        out, lse = run(x.to(torch.bfloat16))
+        R.check_decode_q4(out, lse, x.to(torch.bfloat16), cache, table, lens, SCALE, f"2^{big}")
+    x = q.to(torch.bfloat16)
+    x[:, 2] = x[:, 5] = 0
+    clean = run(x)
+    x[:, 2], x[:, 5] = float("nan"), float("inf")
+    x[1, 5, 7:] = 0
+    out, lse = run(x)
+    assert A.device_status()[0] == 0
+    rest = [h for h in range(Hq) if h not in (2, 5)]
+    assert torch.equal(out[:, rest], clean[0][:, rest]) and torch.equal(lse[:, rest], clean[1][:, rest])
+    assert torch.isnan(out[:, 2].float()).all()
+
+
 def test_decode_is_deterministic_and_takes_given_outputs(A):
     q, cache, table, dl, out, lse = _decode(A, [900, 1, 3000], 8, 2, seed=7)
     ws = torch.full((A.decode_q4_workspace_bytes(3, 8, 2, 128, table.shape[1]),), 0xff, dtype=torch.uint8, device="cuda")
