@@ -36,7 +36,7 @@
 // table's width an earlier page loop took 177 us instead of 168.
 //
 // In a segment each warp streams page pairs w, w + 4, .. through a ring of its own
-// (bulk copies issued by its lane 0 as soon as a slot has been read): no producer
+// (bulk copies issued by one of its lanes as soon as a slot has been read): no producer
 // warp and no barrier between warps until the four partial results meet at the
 // segment's end.  Scores, sums and outputs are fp32.  P' is rounded to f16 (2^-12 of
 // itself at most), P to bf16 for the centers; the row sum adds the fp32 values.
@@ -337,13 +337,12 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
             }
             whole = __ballot_sync(0xffffffffu, nv0 == PAGE && nv1 == PAGE);
         };
-        auto issue = [&](int i, int to) {  // pair i of the batch
-            const int t0 = __shfl_sync(0xffffffffu, tab0, i), t1 = __shfl_sync(0xffffffffu, tab1, i);
-            if (lane == 0) {
+        auto issue = [&](int i, int to) {  // pair i of the batch, by the lane that holds it
+            if (lane == i) {
                 uint8_t *dst = ring + to * STAGE;
-                ptx::mbar_arrive_expect_tx(full + to, (t0 >= 0 ? BLOCK : 0) + (t1 >= 0 ? BLOCK : 0));
-                if (t0 >= 0) ptx::bulk_load(dst, cache + t0 * page_step, BLOCK, full + to, pol);
-                if (t1 >= 0) ptx::bulk_load(dst + BLOCK, cache + t1 * page_step, BLOCK, full + to, pol);
+                ptx::mbar_arrive_expect_tx(full + to, (tab0 >= 0 ? BLOCK : 0) + (tab1 >= 0 ? BLOCK : 0));
+                if (tab0 >= 0) ptx::bulk_load(dst, cache + tab0 * page_step, BLOCK, full + to, pol);
+                if (tab1 >= 0) ptx::bulk_load(dst + BLOCK, cache + tab1 * page_step, BLOCK, full + to, pol);
             }
         };
         auto issue_first = [&](int m) {  // the batch's first pairs, all slots being free
@@ -491,8 +490,8 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                 big = max(big & 0xffffu, big >> 16);
                 const bool all = whole >> i & 1;
                 if (!all) {
-                    // Slots past the end hold arbitrary bits: their scores are replaced
-                    // here, the values' parameters below.
+                    // Slots past the end hold arbitrary bits: their scores are replaced,
+                    // and in shared memory the values' parameters.
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int nv = __shfl_sync(0xffffffffu, u ? nv1 : nv0, i);
@@ -501,8 +500,17 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                             if (r4 >= nv) x[u][c][0] = x[u][c][1] = -INFINITY;
                             if (r4 + 8 >= nv) x[u][c][2] = x[u][c][3] = -INFINITY;
                         }
-                        if (u == lane >> 4 && (lane & 15) >= nv) big = 0;
+                        if (u == lane >> 4 && (lane & 15) >= nv) {
+                            big = 0;
+                            uint8_t *mine = ring + slot * STAGE + u * BLOCK;
+                            *reinterpret_cast<uint2 *>(mine + q4::V_SCALES + (lane & 15) * 8) = make_uint2(0, 0);
+#pragma unroll
+                            for (int g = 0; g < 4; ++g)
+                                *reinterpret_cast<uint16_t *>(mine + q4::V_CENTERS + g * 32 + (lane & 15) * 2) = 0;
+                        }
                     }
+                    ptx::fence_proxy_async_smem();  // (the slot's next copy comes after these writes)
+                    __syncwarp();
                 }
                 // Probability times scale goes to the product as f16 (11 bits: the values'
                 // part of the output then loses nothing against its own rounding), so
@@ -641,13 +649,6 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                         // The pair has been read: its slot goes back.
                         __syncwarp();
                         if (i + NST < batch) issue(i + NST, slot);
-                    }
-                    if (!all) {
-                        const int nv = __shfl_sync(0xffffffffu, u ? nv1 : nv0, i);
-                        if (r4 >= nv) w.vsa = make_uint2(0, 0);
-                        if (r4 + 8 >= nv) w.vsb = make_uint2(0, 0);
-                        w.vza &= (2 * c4 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 1 < nv ? 0xffff0000u : 0u);
-                        w.vzb &= (2 * c4 + 8 < nv ? 0x0000ffffu : 0u) | (2 * c4 + 9 < nv ? 0xffff0000u : 0u);
                     }
                     if (vf != ONE) {
                         w.vsa = make_uint2(mul_bf16x2(w.vsa.x, vf), mul_bf16x2(w.vsa.y, vf));
