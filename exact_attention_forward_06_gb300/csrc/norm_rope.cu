@@ -25,7 +25,7 @@ namespace attn {
 namespace nr {
 
 constexpr int D = 128;
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 constexpr int HALVES = THREADS / 16;  // half-warps, one token each
 
 // The rows of a token go to half-warps in chunks of one tensor's heads: `chunks`
@@ -176,10 +176,11 @@ __device__ __forceinline__ void quantise_store(uint8_t *block, int t, bool is_v,
     }
 }
 
-// Four blocks an SM: the quantising branch would otherwise take 85 registers and
-// leave the query rows, two thirds of the work, three (187 us against 176).
+// Seven blocks an SM: the quantising branch would otherwise take 85 registers and
+// leave the query rows, two thirds of the work, too few warps (five blocks: 161 us
+// with the read-back against 147; nine, which spill: 154).
 template <bool INTER, bool Q4, int U>
-__global__ void __launch_bounds__(THREADS, 4) append_kernel(const AppendParams p, Chunks cq, Chunks ckv) {
+__global__ void __launch_bounds__(THREADS, 7) append_kernel(const AppendParams p, Chunks cq, Chunks ckv) {
     // Q4: the lane layout of a rotated row goes to eight consecutive channels
     // a lane through shared memory, one row per half-warp.
     __shared__ __align__(16) uint16_t turn_row[Q4 && !INTER ? HALVES : 1][Q4 && !INTER ? D : 8];
