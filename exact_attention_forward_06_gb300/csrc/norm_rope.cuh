@@ -170,7 +170,7 @@ __device__ __forceinline__ LaneRow pack(const float (&a)[4], const float (&b)[4]
 // The factors of one tensor's rows at one token: weights times cosines and
 // sines (a lane that does not rotate: the weights).
 struct LaneFactors {
-    float ac[4], bs[4], as[4], bc[4];
+    float2 ac[2], bs[2], as[2], bc[2];  // bs: of the other sign
 };
 
 template <bool INTER>
@@ -179,11 +179,11 @@ __device__ __forceinline__ LaneFactors lane_factors(const LaneTurn &t, const voi
     if (weight) unpack<INTER>(load_row<INTER>(weight, lp), u, w);
     LaneFactors f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        f.ac[j] = u[j] * t.c[j];
-        f.bs[j] = w[j] * t.s[j];
-        f.as[j] = u[j] * t.s[j];
-        f.bc[j] = w[j] * t.c[j];
+    for (int j = 0; j < 2; ++j) {
+        f.ac[j] = make_float2(u[2 * j] * t.c[2 * j], u[2 * j + 1] * t.c[2 * j + 1]);
+        f.bs[j] = make_float2(-w[2 * j] * t.s[2 * j], -w[2 * j + 1] * t.s[2 * j + 1]);
+        f.as[j] = make_float2(u[2 * j] * t.s[2 * j], u[2 * j + 1] * t.s[2 * j + 1]);
+        f.bc[j] = make_float2(w[2 * j] * t.c[2 * j], w[2 * j + 1] * t.c[2 * j + 1]);
     }
     return f;
 }
@@ -196,28 +196,40 @@ __device__ __forceinline__ LaneRow norm_rotate(const LaneRow &in, bool norm, flo
                                                bool rotates) {
     float a[4], b[4], x[4], y[4];
     unpack<INTER>(in, a, b);
+    const float2 a2[2] = {make_float2(a[0], a[1]), make_float2(a[2], a[3])};
+    const float2 b2[2] = {make_float2(b[0], b[1]), make_float2(b[2], b[3])};
     float inv = 1.f;
     if (norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
+        const float2 s2 = ptx::fma2(a2[0], a2[0], ptx::mul2(a2[1], a2[1]));
+        const float2 t2 = ptx::fma2(b2[0], b2[0], ptx::mul2(b2[1], b2[1]));
+        const float2 u2 = ptx::add2(s2, t2);
+        float ss = u2.x + u2.y;
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off, 16);
         inv = rsqrtf(fmaf(ss, 1.f / 128.f, eps));
     }
+    const float2 inv2 = make_float2(inv, inv);
+    float2 x2[2], y2[2];
     if (rotates) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[j] = (a[j] * f.ac[j] - b[j] * f.bs[j]) * inv;
-            y[j] = (a[j] * f.as[j] + b[j] * f.bc[j]) * inv;
+        for (int j = 0; j < 2; ++j) {
+            x2[j] = ptx::mul2(ptx::fma2(b2[j], f.bs[j], ptx::mul2(a2[j], f.ac[j])), inv2);
+            y2[j] = ptx::mul2(ptx::fma2(b2[j], f.bc[j], ptx::mul2(a2[j], f.as[j])), inv2);
         }
     } else {
         // (not the general form with a sine of zero: infinities stay where they are)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[j] = a[j] * f.ac[j] * inv;
-            y[j] = b[j] * f.bc[j] * inv;
+        for (int j = 0; j < 2; ++j) {
+            x2[j] = ptx::mul2(ptx::mul2(a2[j], f.ac[j]), inv2);
+            y2[j] = ptx::mul2(ptx::mul2(b2[j], f.bc[j]), inv2);
         }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        x[2 * j] = x2[j].x;
+        x[2 * j + 1] = x2[j].y;
+        y[2 * j] = y2[j].x;
+        y[2 * j + 1] = y2[j].y;
     }
     return pack<INTER>(x, y);
 }

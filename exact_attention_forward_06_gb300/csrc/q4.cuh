@@ -64,13 +64,15 @@ __device__ __forceinline__ uint32_t code_word(const float (&x)[8], GroupScale gs
     constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, in the low bits
     uint32_t word = 0;
     if (s > 7.8886090522101181e-31f && s < 1.2676506002282294e30f) {  // 2^-100, 2^100
-        const float r = __frcp_rn(s);
+        const float r1 = __frcp_rn(s);
+        const float2 r = make_float2(r1, r1), minus_z = make_float2(-z, -z), minus_s = make_float2(-s, -s);
 #pragma unroll
-        for (int j = 7; j >= 0; --j) {
-            const float d = __fsub_rn(x[j], z);
-            const float q = __fmul_rn(d, r);
-            const float t = __fadd_rn(__fmaf_rn(__fmaf_rn(-q, s, d), r, q), 7.5f);
-            word = word * 16 + (__float_as_uint(__fadd_rn(t, MAGIC)) - 0x4B400000u);
+        for (int j = 6; j >= 0; j -= 2) {
+            const float2 d = ptx::add2(make_float2(x[j], x[j + 1]), minus_z);
+            const float2 q = ptx::mul2(d, r);
+            const float2 exact = ptx::fma2(ptx::fma2(q, minus_s, d), r, q);
+            const float2 t = ptx::add2(ptx::add2(exact, make_float2(7.5f, 7.5f)), make_float2(MAGIC, MAGIC));
+            word = (word * 16 + (__float_as_uint(t.y) - 0x4B400000u)) * 16 + (__float_as_uint(t.x) - 0x4B400000u);
         }
     } else {
 #pragma unroll 1
