@@ -53,24 +53,31 @@ struct LaneTurn {
     float c[4], s[4];
 };
 
-// Sine and cosine of `frac` / 2^32 of a turn.
-__device__ __forceinline__ void sincos_turn(uint32_t frac, float &s, float &c) {
-    const uint32_t quarter = (frac + 0x20000000u) >> 30;
-    const float x = (float)(int32_t)(frac - (quarter << 30)) * 1.4629180792671596e-09f;  // 2 pi / 2^32
-    const float x2 = x * x;
-    float sn = fmaf(x2, 2.7557319224e-06f, -1.9841269841e-04f);  // 1/9!, -1/7!
-    sn = fmaf(x2, sn, 8.3333333333e-03f);                        // 1/5!
-    sn = fmaf(x2, sn, -1.6666666667e-01f);                       // -1/3!
-    sn = fmaf(x2 * x, sn, x);
-    float cs = fmaf(x2, -2.7557319224e-07f, 2.4801587302e-05f);  // -1/10!, 1/8!
-    cs = fmaf(x2, cs, -1.3888888889e-03f);                       // -1/6!
-    cs = fmaf(x2, cs, 4.1666666667e-02f);                        // 1/4!
-    cs = fmaf(x2, cs, -0.5f);
-    cs = fmaf(x2, cs, 1.f);
-    // A quarter turn on: (sin, cos) -> (cos, -sin).
-    const float a = quarter & 1 ? cs : sn, b = quarter & 1 ? sn : cs;
-    s = __uint_as_float(__float_as_uint(a) ^ (quarter & 2) << 30);
-    c = __uint_as_float(__float_as_uint(b) ^ ((quarter + 1) & 2) << 30);
+// Sines and cosines of two angles, `frac` / 2^32 of a turn each.
+__device__ __forceinline__ void sincos_turns(uint32_t frac0, uint32_t frac1, float (&s)[2], float (&c)[2]) {
+    const auto all = [](float v) { return make_float2(v, v); };
+    const uint32_t quarter[2] = {(frac0 + 0x20000000u) >> 30, (frac1 + 0x20000000u) >> 30};
+    const float2 x = ptx::mul2(make_float2((float)(int32_t)(frac0 - (quarter[0] << 30)),
+                                           (float)(int32_t)(frac1 - (quarter[1] << 30))),
+                               all(1.4629180792671596e-09f));  // 2 pi / 2^32
+    const float2 x2 = ptx::mul2(x, x);
+    float2 sn = ptx::fma2(x2, all(2.7557319224e-06f), all(-1.9841269841e-04f));  // 1/9!, -1/7!
+    sn = ptx::fma2(x2, sn, all(8.3333333333e-03f));                             // 1/5!
+    sn = ptx::fma2(x2, sn, all(-1.6666666667e-01f));                            // -1/3!
+    sn = ptx::fma2(ptx::mul2(x2, x), sn, x);
+    float2 cs = ptx::fma2(x2, all(-2.7557319224e-07f), all(2.4801587302e-05f));  // -1/10!, 1/8!
+    cs = ptx::fma2(x2, cs, all(-1.3888888889e-03f));                            // -1/6!
+    cs = ptx::fma2(x2, cs, all(4.1666666667e-02f));                             // 1/4!
+    cs = ptx::fma2(x2, cs, all(-0.5f));
+    cs = ptx::fma2(x2, cs, all(1.f));
+    const float sns[2] = {sn.x, sn.y}, css[2] = {cs.x, cs.y};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        // A quarter turn on: (sin, cos) -> (cos, -sin).
+        const float a = quarter[j] & 1 ? css[j] : sns[j], b = quarter[j] & 1 ? sns[j] : css[j];
+        s[j] = __uint_as_float(__float_as_uint(a) ^ (quarter[j] & 2) << 30);
+        c[j] = __uint_as_float(__float_as_uint(b) ^ ((quarter[j] + 1) & 2) << 30);
+    }
 }
 
 // pos_stride: tokens per axis in p.positions; `token` indexes them; without
@@ -98,11 +105,18 @@ __device__ __forceinline__ LaneTurn lane_turn(const RotateParams &p, int l, int6
     }
     if (bad) report_status(p.status, kStatusDeviceBounds, kSiteRopeAxis);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        // The upper word of the 64-bit product, of a signed position.
-        uint32_t frac = __umulhi((uint32_t)pos[j], e[j].x) + (uint32_t)pos[j] * e[j].y;
-        if (pos[j] < 0) frac -= e[j].x;
-        sincos_turn(frac, t.s[j], t.c[j]);
+    for (int j = 0; j < 4; j += 2) {
+        uint32_t frac[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // The upper word of the 64-bit product, of a signed position.
+            frac[i] = __umulhi((uint32_t)pos[j + i], e[j + i].x) + (uint32_t)pos[j + i] * e[j + i].y;
+            if (pos[j + i] < 0) frac[i] -= e[j + i].x;
+        }
+        float s[2], c[2];
+        sincos_turns(frac[0], frac[1], s, c);
+        t.s[j] = s[0], t.s[j + 1] = s[1];
+        t.c[j] = c[0], t.c[j + 1] = c[1];
     }
     return t;
 }
