@@ -12,22 +12,23 @@ namespace q4 {
 
 constexpr int GWARPS = 8;
 
-// Value of channel 8 w + j's code in the word, given the group's scale and center.
-__device__ __forceinline__ float value_of(uint32_t n, float s, float z) {
-    // s (n - 7.5) is exact in fp32 (8 + 5 bits), the sum rounds once
-    return fmaf(s, (float)n - 7.5f, z);
-}
-
 __device__ __forceinline__ float bf16_at(const uint8_t *p) {
     return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(p) << 16);
 }
 
-// A word's eight values, rounded to bf16.
+// A word's eight values, rounded to bf16.  A code in bits 1..4 of a float whose other
+// bits are those of 2^22 is 2^22 + n; the offset comes off exactly, s (n - 7.5) is exact
+// in fp32 (8 + 5 bits), and the sum rounds once.
 __device__ __forceinline__ uint4 unpack_word(uint32_t word, float s, float z) {
     uint32_t r[4];
+    const float2 s2 = make_float2(s, s), z2 = make_float2(z, z), off = make_float2(-4194311.5f, -4194311.5f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        r[j] = ptx::pack_bf16x2(value_of(word >> (8 * j) & 15, s, z), value_of(word >> (8 * j + 4) & 15, s, z));
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = (j == 0 ? word << 1 : word >> (j == 0 ? 0 : 8 * j - 1)) & 0x1e, hi = word >> (8 * j + 3) & 0x1e;
+        const float2 n = make_float2(__uint_as_float(0x4a800000u | lo), __uint_as_float(0x4a800000u | hi));
+        const float2 v = ptx::fma2(s2, ptx::add2(n, off), z2);
+        r[j] = ptx::pack_bf16x2(v.x, v.y);
+    }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 

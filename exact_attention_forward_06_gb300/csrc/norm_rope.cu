@@ -176,11 +176,12 @@ __device__ __forceinline__ void quantise_store(uint8_t *block, int t, bool is_v,
     }
 }
 
-// Seven blocks an SM: the quantising branch would otherwise take 85 registers and
-// leave the query rows, two thirds of the work, too few warps (five blocks: 161 us
-// with the read-back against 147; nine, which spill: 154).
+// Seven blocks an SM, eight for the 4-bit cache: its quantising branch would otherwise
+// take 85 registers and leave the query rows, two thirds of the work, too few warps
+// (with the read-back, 6, 7, 8 blocks: 148, 144, 141 us; the bf16 append, 7, 8: 69.9,
+// 70.7).
 template <bool INTER, bool Q4, int U>
-__global__ void __launch_bounds__(THREADS, 7) append_kernel(const AppendParams p, Chunks cq, Chunks ckv) {
+__global__ void __launch_bounds__(THREADS, Q4 ? 8 : 7) append_kernel(const AppendParams p, Chunks cq, Chunks ckv) {
     // Q4: the lane layout of a rotated row goes to eight consecutive channels
     // a lane through shared memory, one row per half-warp.
     __shared__ __align__(16) uint16_t turn_row[Q4 && !INTER ? HALVES : 1][Q4 && !INTER ? D : 8];
