@@ -1,14 +1,17 @@
-"""ctypes binding of libattn.so (the C ABI in include/attn.h).
+"""ctypes binding of libattn.so (the C ABI in include/attn.h), with a quicker
+way (_quick.so, csrc/binding.cpp) for the operators whose calls take a few
+microseconds.
 
 Argument marshalling only: every step of the computation runs in the CUDA
 library.  PyTorch owns the device memory and the stream; tensors are passed by
-``data_ptr()`` and the current stream by handle.  If the compiled library is
+``data_ptr()`` and the current stream by handle.  If a compiled library is
 missing this module raises immediately -- there is no fallback path.
 """
 from __future__ import annotations
 
 import ctypes
 import fractions
+import importlib
 import math
 import os
 import threading
@@ -17,6 +20,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIBRARY_PATH = os.path.join(_PKG, "libattn.so")
+QUICK_PATH = os.path.join(_PKG, "_quick.so")
 
 ATTN_OK = 0
 STATUS_NAMES = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_CUDA",
@@ -25,6 +29,7 @@ LAYOUTS = {"bshd": 0, "bhsd": 1}
 
 _lock = threading.Lock()
 _lib = None
+_quick = None  # _quick.so: the quick way into the operators around the paged cache
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
@@ -41,14 +46,16 @@ class AttnError(RuntimeError):
 
 def load():
     """Load libattn.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _quick
     with _lock:
         if _lib is None:
-            if not os.path.exists(LIBRARY_PATH):
-                raise RuntimeError(
-                    f"{LIBRARY_PATH} is missing: build the CUDA library first "
-                    "(python -c 'import __graft_entry__ as g; g.build()')")
+            for path in (LIBRARY_PATH, QUICK_PATH):
+                if not os.path.exists(path):
+                    raise RuntimeError(
+                        f"{path} is missing: build the CUDA library first "
+                        "(python -c 'import __graft_entry__ as g; g.build()')")
             lib = ctypes.CDLL(LIBRARY_PATH)
+            _quick = importlib.import_module("._quick", __package__)
             fwd_args = [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p]
             lib.attn_fwd.argtypes = fwd_args
             lib.attn_fwd_simple.argtypes = fwd_args
@@ -442,9 +449,13 @@ Q4_BLOCK_BYTES = 2560  # one page of one KV head in the 4-bit cache (ATTN_Q4_BLO
 _PI = fractions.Fraction("3.14159265358979323846264338327950288419716939937510582")
 
 
-# The operators below run in a few microseconds on small calls, so their checks
-# take one cheap pass per tensor: _in gives the tensor's address, and anything
-# out of order goes to _refuse, which says what.
+# The operators below run in a few microseconds on small calls, less than Python
+# takes to look at their tensors.  So a call first goes to _quick (csrc/binding.cpp),
+# which checks, makes the outputs and launches, and which returns None, having
+# launched nothing, when anything is not plainly in order.  Then, and on a stream of
+# the caller's, the function's own body runs: it checks one thing after the other and
+# says what is wrong.  _in gives a tensor's address, and anything out of order
+# goes to _refuse.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _device = torch._C._cuda_getDevice
 _bf16 = torch.bfloat16
@@ -566,6 +577,11 @@ def qk_norm_rope(q, k=None, *, rope=None, positions=None, q_weight=None, k_weigh
     lib = _lib or load()
     if layout not in LAYOUTS:
         raise ValueError(f"layout must be 'bshd' or 'bhsd', got {layout!r}")
+    if stream is None:
+        done = _quick.qk_norm_rope(q, k, q_weight, k_weight, eps, positions, rope, interleaved, LAYOUTS[layout], q_out,
+                                   k_out)
+        if done is not None:
+            return done
     dev = _current()
     qp = _in_strided(q, "q", dev)
     kp = None if k is None else _in_strided(k, "k", dev)
@@ -673,6 +689,11 @@ def append_paged(q, k, v, k_pages, v_pages, block_table, seqlens, cu_seqlens=Non
     q_out [total, Hq, 128] (None without q): the q of fwd_paged or decode_paged over the same arrays.
     """
     lib = _lib or load()
+    if stream is None:
+        done = _quick.append(q, k, v, k_pages, v_pages, block_table, seqlens, cu_seqlens, q_weight, k_weight, eps,
+                             positions, rope, interleaved, q_out) if v_pages is not None else None
+        if done is not None:
+            return done[0]
     dev = _current()
     pools = _in(k_pages, "k_pages", _bf16, dev), _in(v_pages, "v_pages", _bf16, dev)
     shape = k_pages.shape
@@ -698,6 +719,11 @@ def append_paged_q4(q, k, v, cache, block_table, seqlens, cu_seqlens=None, *, ro
                     q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None, stream=None):
     """append_paged into a cache held in 4 bits: cache [num_pages, Hkv, Q4_BLOCK_BYTES] uint8, updated in place."""
     lib = _lib or load()
+    if stream is None:
+        done = _quick.append(q, k, v, cache, None, block_table, seqlens, cu_seqlens, q_weight, k_weight, eps, positions,
+                             rope, interleaved, q_out)
+        if done is not None:
+            return done[0]
     dev = _current()
     ptr, num_pages, Hkv = _q4_cache(cache, dev)
     return _append(lib.attn_append_paged_q4, q, k, v, (ptr,), Hkv, num_pages, 16, block_table, seqlens, cu_seqlens,
@@ -709,6 +735,10 @@ def gather_paged_q4(cache, block_table, seqlens, cu_seqlens_k, *, total_k=None, 
     cu_seqlens_k[b] on -- the k and v of fwd_varlen.  total_k, when omitted, is read from the outputs given or the
     offsets (a synchronisation)."""
     lib = _lib or load()
+    if stream is None:
+        done = _quick.gather(cache, block_table, seqlens, cu_seqlens_k, total_k, k_out, v_out)
+        if done is not None:
+            return done
     dev = _current()
     ptr, num_pages, Hkv = _q4_cache(cache, dev)
     table, lens = _in(block_table, "block_table", _i32, dev), _in(seqlens, "seqlens", _i32, dev)
@@ -765,6 +795,10 @@ def decode_paged_q4(q, cache, block_table, seqlens, *, scale=None, out=None, lse
     """One decode step over a cache held in 4 bits (the arguments of decode_paged, with one cache tensor
     [num_pages, Hkv, Q4_BLOCK_BYTES] uint8).  Returns (out [B, Hq, 128] bf16, lse [B, Hq] fp32)."""
     lib = _lib or load()
+    if stream is None:
+        done = _quick.decode(q, scale, out, lse, cache, block_table, seqlens, workspace)
+        if done is not None:
+            return done
     dev = _current()
     ptr, num_pages, Hkv = _q4_cache(cache, dev)
     qp = _in(q, "q", _bf16, dev)
@@ -801,6 +835,11 @@ def fwd_paged_q4(q, cache, block_table, seqlens_k, cu_seqlens_q, *, max_seqlen_q
     lib = _lib or load()
     if rounding not in ROUNDING:
         raise ValueError(f"rounding must be one of {sorted(ROUNDING)}, got {rounding!r}")
+    if stream is None:
+        done = _quick.fwd(q, scale, out, lse, cache, block_table, seqlens_k, workspace, cu_seqlens_q, max_seqlen_q,
+                          max_total_k, causal, ROUNDING[rounding])
+        if done is not None:
+            return done
     dev = _current()
     ptr, num_pages, Hkv = _q4_cache(cache, dev)
     qp = _in(q, "q", _bf16, dev)

@@ -1,8 +1,10 @@
-"""Build libattn.so (the C-ABI CUDA library) in-tree with nvcc for sm_103a.
+"""Build libattn.so (the C-ABI CUDA library) in-tree with nvcc for sm_103a, and
+_quick.so (csrc/binding.cpp, the binding's quick way into it) with g++ against
+the installed torch.
 
 Each translation unit is compiled in parallel into ``_build/`` and linked into
-``exact_attention_forward_06_gb300/libattn.so``.  Rebuilds only when a source
-or header is newer than the library.  Usable as a script:
+``exact_attention_forward_06_gb300/``.  Rebuilds only when a source or header is
+newer than the libraries.  Usable as a script:
 ``python -m exact_attention_forward_06_gb300.build [--force] [--verbose]``.
 """
 from __future__ import annotations
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libattn.so")
+QUICK = os.path.join(PKG, "_quick.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -38,10 +42,10 @@ def sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(QUICK)):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    t = min(os.path.getmtime(LIB), os.path.getmtime(QUICK))
+    deps = sources() + [os.path.join(CSRC, "binding.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
 
@@ -59,23 +63,46 @@ def _compile(src: str, extra, verbose: bool) -> str:
     return obj
 
 
-def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile every .cu under csrc/ and link libattn.so; returns its path."""
-    if not force and not _stale():
-        return LIB
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra, verbose), srcs))
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs + \
-        ["-Xlinker", "-rpath=/usr/local/cuda/lib64"]
+def _run(cmd, what: str, verbose: bool):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding(verbose: bool):
+    """binding.cpp as an object, and what links it to torch."""
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE] + [x for i in inc for x in ("-isystem", i)] + \
+        [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-c", os.path.join(CSRC, "binding.cpp"),
+         "-o", obj]
+    _run(cmd, "g++ on binding.cpp", verbose)
+    lib = os.path.join(base, "lib")
+    return [obj, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"]
+
+
+def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    """Compile the sources under csrc/ and link libattn.so and _quick.so; returns libattn.so's path."""
+    if not force and not _stale():
+        return LIB
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    srcs = sources()
+    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(_compile_binding, verbose)
+        objs = list(ex.map(lambda s: _compile(s, extra, verbose), srcs))
+    tmp = LIB + f".tmp{os.getpid()}"
+    _run([nvcc()] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs +
+         ["-Xlinker", "-rpath=/usr/local/cuda/lib64"], "link", verbose)
     os.replace(tmp, LIB)
+    tmp = QUICK + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp] + binding.result() + ["-L", PKG, "-l:libattn.so", "-Wl,-rpath,$ORIGIN"],
+         "link of the binding", verbose)
+    os.replace(tmp, QUICK)
     return LIB
 
 

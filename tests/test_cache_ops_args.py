@@ -163,3 +163,13 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         A.gather_paged_q4(x, x, x, x)
     with pytest.raises(ValueError):
         A.qk_norm_rope(x, x, layout="bsdh")
+
+
+def test_quick_way_turns_down_what_is_not_in_order(lib):
+    """Wrong counts and kinds of arguments, and tensors that are not on a GPU: None, for the long way to say why."""
+    quick = _binding._quick
+    t = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
+    for name, n in (("qk_norm_rope", 11), ("append", 15), ("gather", 7), ("decode", 8), ("fwd", 13)):
+        fn = getattr(quick, name)
+        assert fn() is None and fn(*[None] * n) is None and fn(*["x"] * n) is None and fn(*[t] * n) is None
+        assert fn(*[t] * (n - 1)) is None
