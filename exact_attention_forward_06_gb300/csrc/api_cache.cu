@@ -203,10 +203,10 @@ attn_status_t attn_gather_paged_q4(const void *cache, const int32_t *block_table
 size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int d, int max_blocks_per_seq) {
     if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d != 128 || max_blocks_per_seq < 1) return 0;
     if ((int64_t)B * ((max_blocks_per_seq + (int64_t)1) / 2) > 0x7fffffff) return 0;
-    // o_part [rows][d] fp32, lse_part [rows] fp32, cuts [CTAs] of 16 bytes, each 256-B aligned.
+    // o_part [rows][d] fp32, lse_part [rows] fp32, cuts [CTAs][2] of 16 bytes, each 256-B aligned.
     size_t ctas = 0;
     const size_t rows = attn::decode_q4_partial_rows(B, Hq, Hkv, max_blocks_per_seq, &ctas);
-    return align256(rows * d * 4) + align256(rows * 4) + align256(ctas * 16);
+    return align256(rows * d * 4) + align256(rows * 4) + align256(ctas * 32);
 }
 
 attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32_t *block_table,

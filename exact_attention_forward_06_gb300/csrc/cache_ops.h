@@ -62,7 +62,7 @@ struct DecodeQ4Params {
     // and its last segment: normalised outputs and log2-sum-exp2 of its heads.
     float *o_part;    // [CTAs][2][heads][d]
     float *lse_part;  // [CTAs][2][heads]
-    int4 *cuts;       // [CTAs]
+    int4 *cuts;       // [CTAs][2]
     int B, Hq, Hkv, num_pages, max_blocks;
     float scale_log2;
     unsigned *status;

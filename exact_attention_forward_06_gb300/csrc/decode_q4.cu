@@ -43,13 +43,13 @@
 // With P' in bf16, as the bf16 decode's P, the output's error against 64 bits was
 // 2.4e-3 (its own rounding alone makes 1.7e-3) instead of 1.8e-3, in 0.97 of the time.
 //
-// Measured on 64 sequences of 0 to 16384 tokens, 64 / 8 heads (758 MB): 152 us,
-// 5.0 TB/s, 0.74 of the copy bandwidth; the copies alone take 124 us.  On 32 sequences
-// of 1024 to 8192 tokens, 32 / 8 heads (177 MB): 46.5 us, 0.56; half the MMA columns are
-// empty there, and about 6 us are the two launches' ends.  3 sequences of about 100
-// thousand tokens, 32 / 1 heads (55 MB): 48 us, the unpacking of two tiles' pages twice
-// (with one tile a CTA, four times: 50).  With codes as 16 + n and n - 7.5, each by a
-// shift and an and/or (and an addition), these took 167, 50 and 49 us.
+// Measured on 64 sequences of 0 to 16384 tokens, 64 / 8 heads (758 MB): 147 us,
+// 5.2 TB/s, 0.76 of the copy bandwidth; the copies alone take 120 us, the arithmetic
+// alone 139.  On 32 sequences of 1024 to 8192 tokens, 32 / 8 heads (177 MB): 45.2 us,
+// 0.58; half the MMA columns are empty there.  3 sequences of about 100 thousand tokens,
+// 32 / 1 heads (55 MB): 43.3 us, the unpacking of two tiles' pages twice (with one tile
+// a CTA, four times: 5 us more).  With codes as 16 + n and n - 7.5, each by a shift and
+// an and/or (and an addition), these took 167, 50 and 49 us.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -201,12 +201,6 @@ __device__ __forceinline__ int pairs_of(int L, int max_blocks) {
     return L < 0 || L > max_blocks * PAGE ? 0 : (L + 2 * PAGE - 1) / (2 * PAGE);
 }
 
-// What the merge finds out about a cut run that begins in share c: its first
-// row, its query heads and how many shares it spans (0: none).
-struct CutRun {
-    int row0, cols, parts;
-};
-
 template <int TILES>
 __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
     share_kernel(const DecodeQ4Params p, int col_blocks) {
@@ -222,8 +216,8 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::BARRIERS) + warp * NST;
     int *words = reinterpret_cast<int *>(smem + S::WORDS);
     volatile int *abort_flag = words;
-    int64_t *found = reinterpret_cast<int64_t *>(words + 2);  // [0] all pairs, [1] pairs before words[1]'s sequence
-    int *scan = words + 6;                                    // [NW]
+    int64_t *found = reinterpret_cast<int64_t *>(words + 2);  // [0] total, [1] pairs before words[1]'s sequence, [2] shares
+    int *scan = words + 8;                                    // [NW]
 
     // CTAs of one share that differ in the column block alone are neighbours, so
     // that their reads of the same pages meet in L2.
@@ -263,6 +257,10 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
     const int64_t shares = min(min((int64_t)(gridDim.x / col_blocks), total), max(items, fill));
     const int64_t u0 = share < shares ? total * share / shares : total;
     const int64_t u1 = share < shares ? total * (share + 1) / shares : total;
+    if (threadIdx.x == 0) {
+        found[0] = total;
+        found[2] = shares;
+    }
     if (u0 < u1 && u0 >= before * p.Hkv && u0 < (before + mine) * p.Hkv) {
         int b = b_lo;
         int64_t pre = before;
@@ -288,7 +286,9 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
         }
     }
     __syncthreads();
-    CutRun cut = {0, 0, 0};
+    // For the merge: the cut run that the share goes on with, and the one it begins, as
+    // first row, query heads, number of shares (0: none) and which of them this one is.
+    if (threadIdx.x < 2) p.cuts[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
     const WaitCtx wc{abort_flag, p.status, p.budget_ns};
     const uint64_t pol = col_blocks == 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
     const int64_t page_step = (int64_t)p.Hkv * BLOCK;
@@ -309,6 +309,16 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
     for (int64_t u = u0; u < u1;) {
         const int count = (int)min((int64_t)(seq_pairs - first), u1 - u);  // this segment's pairs
         const int64_t row0 = (int64_t)b * p.Hq + h * G + col0;
+        if (count < seq_pairs) {
+            // The run lies in the shares of its first and last pairs and all between.
+            if (threadIdx.x == (first == 0)) {
+                const int64_t all_units = found[0], n_shares = found[2], unit = u - first;
+                const int begin = (int)(((unit + 1) * n_shares + all_units - 1) / all_units - 1);
+                const int end = (int)(((unit + seq_pairs) * n_shares + all_units - 1) / all_units - 1);
+                p.cuts[2 * blockIdx.x + (first == 0)] =
+                    make_int4((int)row0, cols, end - begin + 1, (int)(blockIdx.x / col_blocks) - begin);
+            }
+        }
         const uint8_t *cache = static_cast<const uint8_t *>(p.cache) + (int64_t)h * BLOCK;
         const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
         const int last_page = (L + PAGE - 1) / PAGE;
@@ -767,7 +777,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
         if (warp >= 2) give(warp - 2);
         __syncthreads();
         if (*abort_flag) {  // a wait gave up: nothing more is written, or merged from here
-            if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+            if (threadIdx.x < 2) p.cuts[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
             return;
         }
         if (warp < 2) take(warp);
@@ -808,14 +818,6 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                     }
                 }
         }
-        if (first == 0 && count < seq_pairs) {
-            // The sequence goes on in the next shares, up to the one that holds
-            // its last pair, unit u + seq_pairs - 1.
-            const int64_t last = ((u + seq_pairs) * shares + total - 1) / total - 1;
-            cut.row0 = (int)row0;
-            cut.cols = cols;
-            cut.parts = (int)(last - share) + 1;
-        }
         u += count;
         first = 0;
         if (++h == p.Hkv && u < u1) {
@@ -826,66 +828,113 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
             } while (seq_pairs == 0);
         }
     }
-    if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(cut.row0, cut.cols, cut.parts, 0);
     ptx::allow_next_work();
 }
 
-// Merge of the cut runs: CTA (c, i) does head i of the run that begins in share
-// c, if one does.  Warp w takes every MERGE_WARPS-th part, four channels a lane;
-// the order is fixed.
+// Merge of the cut runs.  A run of few parts is merged by the CTA of the share in which
+// it begins, a warp a head; the heads of a longer one go to the CTAs of its shares in
+// turn, each head to eight warps that take every eighth part.  Four channels a lane; the
+// order is fixed.  It adds 2 to 4 us to the share kernel; with a CTA for each head of
+// each run, 3 to 9 (3 sequences of 100 thousand tokens: 41.1 us in all against 44.8).
 constexpr int MERGE_WARPS = 8;
+constexpr int SHORT_RUN = 8;
+constexpr int AHEAD = 4;  // parts in flight
 __global__ void __launch_bounds__(MERGE_WARPS * 32)
     merge_kernel(const DecodeQ4Params p, int col_blocks, int cta_cols) {
-    __shared__ float part[MERGE_WARPS][D];
+    __shared__ __align__(16) float part[MERGE_WARPS][D];
     __shared__ float part_m[MERGE_WARPS], part_l[MERGE_WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Launched as a programmatic dependent of the share kernel: its partials are
     // visible from here on.
     ptx::wait_for_prior_work();
     ptx::allow_next_work();
-    const int4 cut = p.cuts[blockIdx.x];
-    const int c = blockIdx.y, parts = cut.z;
-    if (c >= cut.y || parts == 0) return;
-    const int64_t r = (int64_t)cut.x + c;
-    // The first part is this share's last one, the others are the next shares'
-    // first ones (of the same column block).
-    auto row_of = [&](int s) { return ((int64_t)(blockIdx.x + s * col_blocks) * 2 + (s == 0 ? 1 : 0)) * cta_cols + c; };
-    float M = -INFINITY;
-    for (int s = warp; s < parts; s += MERGE_WARPS) M = fmaxf(M, p.lse_part[row_of(s)]);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = warp; s < parts; s += MERGE_WARPS) {
-        const int64_t at = row_of(s);
-        const float x = p.lse_part[at];
-        const float w = x == -INFINITY ? 0.f : ptx::ex2(x - (M == -INFINITY ? 0.f : M));  // NaN stays
-        const float4 v = reinterpret_cast<const float4 *>(p.o_part + at * D)[lane];
-        l += w;
-        o.x = fmaf(w, v.x, o.x);
-        o.y = fmaf(w, v.y, o.y);
-        o.z = fmaf(w, v.z, o.z);
-        o.w = fmaf(w, v.w, o.w);
-    }
-    reinterpret_cast<float4 *>(part[warp])[lane] = o;
-    if (lane == 0) {
-        part_m[warp] = M;
-        part_l[warp] = l;
-    }
-    __syncthreads();
-    if (threadIdx.x >= D) return;
-    float Mt = -INFINITY, Lt = 0.f, ot = 0.f;
+    const int4 cuts[2] = {p.cuts[2 * blockIdx.x], p.cuts[2 * blockIdx.x + 1]};
+    float M, l;
+    float4 o;
+    // Adds up head c's parts sub, sub + each, .. of a run that begins in CTA `from`.  The first
+    // part is its share's last one, the others are their shares' first.
+    auto add_parts = [&](int from, int parts, int c, int sub, int each) {
+        auto row_of = [&](int s) { return ((int64_t)(from + s * col_blocks) * 2 + (s == 0 ? 1 : 0)) * cta_cols + c; };
+        M = -INFINITY, l = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s0 = sub; s0 < parts; s0 += AHEAD * each) {
+            float x[AHEAD];
+            float4 v[AHEAD];
 #pragma unroll
-    for (int w = 0; w < MERGE_WARPS; ++w) Mt = fmaxf(Mt, part_m[w]);
+            for (int i = 0; i < AHEAD; ++i) {
+                const int s = s0 + i * each;
+                x[i] = -INFINITY;
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (s < parts) {
+                    x[i] = p.lse_part[row_of(s)];
+                    v[i] = reinterpret_cast<const float4 *>(p.o_part + row_of(s) * D)[lane];
+                }
+            }
+            float mx = M;
 #pragma unroll
-    for (int w = 0; w < MERGE_WARPS; ++w) {
-        const float f = part_m[w] == -INFINITY ? 1.f : ptx::ex2(part_m[w] - Mt);  // no finite one: 0 or NaN
-        Lt += part_l[w] * f;
-        ot += part[w][threadIdx.x] * f;
+            for (int i = 0; i < AHEAD; ++i) mx = fmaxf(mx, x[i]);
+            const float f = M == -INFINITY ? 1.f : ptx::ex2(M - mx);  // (before a finite one: 0 or NaN, which stays)
+            l *= f;
+            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+            M = mx;
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const float w = x[i] == -INFINITY ? 0.f : ptx::ex2(x[i] - (M == -INFINITY ? 0.f : M));  // NaN stays
+                l += w;
+                o.x = fmaf(w, v[i].x, o.x);
+                o.y = fmaf(w, v[i].y, o.y);
+                o.z = fmaf(w, v[i].z, o.z);
+                o.w = fmaf(w, v[i].w, o.w);
+            }
+        }
+    };
+    auto write_row = [&](int64_t r) {
+        const bool any = l != 0.f;
+        const float inv = any ? 1.f / l : 0.f;
+        reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + r * D)[lane] =
+            any ? make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv))
+                : make_uint2(0, 0);
+        if (p.lse && lane == 0) p.lse[r] = any ? (M + ptx::lg2(l)) * LN2 : -INFINITY;
+    };
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int row0 = cuts[e].x, cols = cuts[e].y, parts = cuts[e].z, index = cuts[e].w;
+        if (parts <= SHORT_RUN) {
+            if (index == 0 && parts > 0)
+                for (int c = warp; c < cols; c += MERGE_WARPS) {
+                    add_parts(blockIdx.x, parts, c, 0, 1);
+                    write_row((int64_t)row0 + c);
+                }
+            continue;
+        }
+        for (int c = index; c < cols; c += parts) {
+            add_parts((int)blockIdx.x - index * col_blocks, parts, c, warp, MERGE_WARPS);
+            reinterpret_cast<float4 *>(part[warp])[lane] = o;
+            if (lane == 0) {
+                part_m[warp] = M;
+                part_l[warp] = l;
+            }
+            __syncthreads();
+            if (warp == 0) {
+                M = -INFINITY, l = 0.f;
+                o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < MERGE_WARPS; ++w) M = fmaxf(M, part_m[w]);
+#pragma unroll
+                for (int w = 0; w < MERGE_WARPS; ++w) {
+                    const float f = part_m[w] == -INFINITY ? 1.f : ptx::ex2(part_m[w] - M);  // no finite one: 0 or NaN
+                    const float4 v = reinterpret_cast<const float4 *>(part[w])[lane];
+                    l += part_l[w] * f;
+                    o.x = fmaf(v.x, f, o.x);
+                    o.y = fmaf(v.y, f, o.y);
+                    o.z = fmaf(v.z, f, o.z);
+                    o.w = fmaf(v.w, f, o.w);
+                }
+                write_row((int64_t)row0 + c);
+            }
+            __syncthreads();
+        }
     }
-    const bool any = Lt != 0.f;
-    ot = any ? ot / Lt : 0.f;
-    static_cast<uint16_t *>(p.out)[r * D + threadIdx.x] = (uint16_t)(ptx::pack_bf16x2(ot, 0.f) & 0xffffu);
-    if (p.lse && threadIdx.x == 0) p.lse[r] = any ? (Mt + ptx::lg2(Lt)) * LN2 : -INFINITY;
 }
 
 // Column blocks of a KV head's G query heads, and CTAs: shares times those.
@@ -941,9 +990,7 @@ cudaError_t launch_decode_q4(const DecodeQ4Params &p, int sm_count, cudaStream_t
     const cudaError_t e = g.tiles == 2 ? dq4::launch_shares<2>(p, g, stream) : dq4::launch_shares<1>(p, g, stream);
     // One sequence with a share for each KV head is never cut.
     if (e != cudaSuccess || (p.B == 1 && g.ctas / g.col_blocks == p.Hkv)) return e;
-    const int G = p.Hq / p.Hkv;
-    return launch_dependent(dq4::merge_kernel, dim3(g.ctas, G < g.cols ? G : g.cols), dq4::MERGE_WARPS * 32, 0, stream, p,
-                            g.col_blocks, g.cols);
+    return launch_dependent(dq4::merge_kernel, g.ctas, dq4::MERGE_WARPS * 32, 0, stream, p, g.col_blocks, g.cols);
 }
 
 }  // namespace attn

@@ -77,6 +77,13 @@ def test_decode_long_and_wide_tables(A, lens, width):
     _decode(A, lens, 4, 1, seed=len(lens) + lens[0], width=width)
 
 
+@pytest.mark.parametrize("lens", [[1280], [300, 1152, 20, 1500], [30000, 9000, 5]])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 1), (16, 1), (32, 1), (20, 2)])
+def test_decode_merges_of_few_and_many_parts(A, Hq, Hkv, lens):
+    """Runs cut into two, into about as many parts as there are heads, and into far more."""
+    _decode(A, lens, Hq, Hkv, seed=90 + len(lens))
+
+
 def test_decode_peaked_scores_and_scales(A):
     _decode(A, [500, 33, 1200], 8, 2, seed=5, spread=30.0)
     for scale in (0.0, 1.0):
