@@ -9,10 +9,10 @@
 // the U rows.
 //
 // Measured on one GB300 (copy bandwidth 6781 GB/s): norm and rotation of 32760
-// tokens, 12 + 12 heads (403 MB) 71 us, 0.84 of it; the append of 18 thousand
-// tokens, 32 / 8 heads, into bf16 pages (464 MB) 73 us, 0.94.  Into the 4-bit cache
-// the same tokens take 95 us: there the quantisation's instructions are the bound
-// (3.1 of 4 issued per clock).
+// tokens, 12 + 12 heads (403 MB) 65 us, 0.91 of it; the append of 18 thousand
+// tokens, 32 / 8 heads, into bf16 pages (464 MB) 70.5 us, 0.97.  Into the 4-bit cache
+// the same tokens take 84 us: there the quantisation's instructions are the bound
+// (3.0 of 4 issued per clock).  With 256 threads a block these took 71, 73 and 95 us.
 #include <cstdint>
 #include <cuda_runtime.h>
 
