@@ -27,13 +27,14 @@
 //   pair of two tokens is one byte permutation.
 // - Two pages a step share the wait, the vote on the running max and the loop.
 //
-// The work is cut into equal shares, one for each CTA that the GPU holds at once:
-// the page pairs of all sequences and KV heads in one row, CTA c taking the c-th
-// part of it.  A share is a few segments (a run of one sequence's pages for one KV
-// head); a segment that is a whole sequence is finished by its CTA, the parts of
-// a cut one go to the workspace and are merged by log-sum-exp in the order of the
-// keys.  Ragged lengths thus cost nothing: with a grid of fixed splits over the
-// table's width an earlier page loop took 177 us instead of 168.
+// The work is cut into shares, one for each CTA that the GPU holds at once.  Where the
+// batch is large the shares are equal: the page pairs of all sequences and KV heads in
+// one row, CTA c taking the c-th part of it, a few segments (a run of one sequence's pages
+// for one KV head).  Where it is small a share is one segment.  A segment that is a whole
+// sequence is finished by its CTA, the parts of a cut one go to the workspace and are
+// merged by log-sum-exp in the order of the keys.  Ragged lengths thus cost nothing: with
+// a grid of fixed splits over the table's width an earlier page loop took 177 us instead
+// of 168.
 //
 // In a segment each warp streams page pairs w, w + 4, .. through a ring of its own
 // (bulk copies issued by one of its lanes as soon as a slot has been read): no producer
@@ -47,7 +48,7 @@
 // 5.2 TB/s, 0.76 of the copy bandwidth; the copies alone take 120 us, the arithmetic
 // alone 139.  On 32 sequences of 1024 to 8192 tokens, 32 / 8 heads (177 MB): 45.2 us,
 // 0.58; half the MMA columns are empty there.  3 sequences of about 100 thousand tokens,
-// 32 / 1 heads (55 MB): 43.3 us, the unpacking of two tiles' pages twice (with one tile
+// 32 / 1 heads (55 MB): 39 us, the unpacking of two tiles' pages twice (with one tile
 // a CTA, four times: 5 us more).  With codes as 16 + n and n - 7.5, each by a shift and
 // an and/or (and an addition), these took 167, 50 and 49 us.
 #include <cstdint>
@@ -82,7 +83,7 @@ struct Shape {
     static constexpr int Q_FRAGS = 4 * TILES * 32 * 16;   // a lane's query fragments, 16 bytes a group and tile
     static constexpr int BARRIERS = RING + 2 * EXCHANGE + Q_FRAGS;
     static constexpr int WORDS = BARRIERS + NW * NST * 8;
-    static constexpr int SMEM = WORDS + 64;
+    static constexpr int SMEM = WORDS + 128;
     static_assert(CTAS_PER_SM * (SMEM + 1024) <= 233472, "CTAs per SM");
 };
 constexpr int MIN_PAIRS = 4;           // pairs a CTA takes at least, unless there is a KV head for each
@@ -216,8 +217,11 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::BARRIERS) + warp * NST;
     int *words = reinterpret_cast<int *>(smem + S::WORDS);
     volatile int *abort_flag = words;
-    int64_t *found = reinterpret_cast<int64_t *>(words + 2);  // [0] total, [1] pairs before words[1]'s sequence, [2] shares
-    int *scan = words + 8;                                    // [NW]
+    // words[1]: the share's first sequence; [2], [3]: which part of how many its run is of its
+    // sequence (whole runs; else 0 and 0).  found: [0] total, [1] pairs before that
+    // sequence, [2] shares, [3], [4] the share's first unit and the one behind its last.
+    int64_t *found = reinterpret_cast<int64_t *>(words + 4);
+    int *scan = words + 16;  // [4][NW]
 
     // CTAs of one share that differ in the column block alone are neighbours, so
     // that their reads of the same pages meet in L2.
@@ -225,52 +229,131 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
     const int G = p.Hq / p.Hkv, col0 = blk * COLS;
     const int cols = min(COLS, G - col0);
 
-    // All pairs, and the sequence in which the share begins: a thread sums a run
-    // of sequences, the sums are scanned.
-    const int per = (p.B + NT - 1) / NT;
-    const int b_lo = min(p.B, (int)threadIdx.x * per), b_hi = min(p.B, b_lo + per);
-    int mine = 0;  // at most 2^31: B * max_blocks / 2 is bounded by the caller
-    for (int b = b_lo; b < b_hi; ++b) mine += pairs_of(__ldg(p.seqlens + b), p.max_blocks);
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+    // All pairs, the sequences with any and the longest: a thread sums a run of
+    // sequences, the sums are scanned; up to 32 sequences, each warp does all of it, a
+    // lane a sequence, and waits for no other.
+    const bool few = p.B <= 32;
+    const int per = few ? 1 : (p.B + NT - 1) / NT;
+    const int b_lo = min(p.B, (few ? lane : (int)threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
+    int mine = 0, some = 0, longest = 0;  // pairs: at most 2^31, B * max_blocks / 2 is bounded by the caller
+    for (int b = b_lo; b < b_hi; ++b) {
+        const int np = pairs_of(__ldg(p.seqlens + b), p.max_blocks);
+        mine += np;
+        some += np > 0;
+        longest = max(longest, np);
     }
-    if (lane == 31) scan[warp] = incl;
+    const auto inclusive = [&](int v) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += w;
+        }
+        return v;
+    };
+    const int incl = inclusive(mine);
+    some = __reduce_add_sync(0xffffffffu, some);
+    longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) {
         for (int s = 0; s < NST; ++s) ptx::mbar_init(full + s, 1);
         if (warp == 0) *abort_flag = 0;
         ptx::fence_mbar_init();
     }
-    __syncthreads();
-    int64_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        if (w < warp) before += scan[w];
-        all += scan[w];
-    }
-    before += incl - mine;  // pairs before this thread's run
-    const int64_t total = all * p.Hkv;
-    // No more shares than there is work for, and none without a pair.
-    const int64_t items = (int64_t)p.B * p.Hkv, fill = (total + MIN_PAIRS - 1) / MIN_PAIRS;
-    const int64_t shares = min(min((int64_t)(gridDim.x / col_blocks), total), max(items, fill));
-    const int64_t u0 = share < shares ? total * share / shares : total;
-    const int64_t u1 = share < shares ? total * (share + 1) / shares : total;
-    if (threadIdx.x == 0) {
-        found[0] = total;
-        found[2] = shares;
-    }
-    if (u0 < u1 && u0 >= before * p.Hkv && u0 < (before + mine) * p.Hkv) {
-        int b = b_lo;
-        int64_t pre = before;
-        for (;; ++b) {
-            const int np = pairs_of(__ldg(p.seqlens + b), p.max_blocks);
-            if (u0 < (pre + np) * p.Hkv) break;
-            pre += np;
+    int64_t before = incl - mine, all = __shfl_sync(0xffffffffu, incl, 31);  // (before: of this thread's run)
+    if (!few) {
+        if (lane == 31) {
+            scan[warp] = incl;
+            scan[NW + warp] = some;
+            scan[2 * NW + warp] = longest;
         }
-        words[1] = b;
-        found[1] = pre;
+        __syncthreads();
+        all = some = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) before += scan[w];
+            all += scan[w];
+            some += scan[NW + w];
+            longest = max(longest, scan[2 * NW + w]);
+        }
+    }
+    const int64_t total = all * p.Hkv, items = (int64_t)some * p.Hkv;
+    const int ctas = gridDim.x / col_blocks;
+    // Whole runs (a sequence and KV head), each cut into parts of at most `part` pairs, a CTA
+    // a part, where the CTAs suffice for that and the longest part is not much longer than
+    // an equal share: a share that takes parts of several runs pays for each the latency
+    // of about 16 pairs.  Else equal shares, no more than there is work for and none
+    // without a pair.  (16 sequences of 10 to 500 tokens, 32 / 8 heads: 9.8 us against 19 in
+    // equal shares; 3 of about 100 thousand, 32 / 1 heads: 37.7 against 40.9.)
+    uint32_t part = 0;
+    if (items <= ctas && longest <= MIN_PAIRS) {
+        part = max(1, longest);
+    } else if (items <= ctas && total < 0x7fffffff) {
+        const uint32_t units = (uint32_t)total, spare = (uint32_t)(ctas - (int)items);
+        part = spare ? max((uint32_t)MIN_PAIRS, (units + spare - 1) / spare) : (uint32_t)longest;
+        part = max(1u, min((uint32_t)longest, (part + NW - 1) / NW * NW));
+        if (part > units / (uint32_t)ctas + 16) part = 0;
+    }
+    if (part) {
+        const auto pieces_of = [&](int np) {
+            return (uint32_t)np <= part ? (int)(np > 0) : (int)(((uint32_t)np + part - 1) / part);
+        };
+        int pieces = 0;
+        for (int b = b_lo; b < b_hi; ++b) pieces += pieces_of(pairs_of(__ldg(p.seqlens + b), p.max_blocks));
+        const int upto = inclusive(pieces);
+        if (threadIdx.x == 0) found[3] = found[4] = 0;
+        int behind = upto - pieces;  // (at most as many as there are CTAs)
+        if (few) {
+            __syncwarp();
+        } else {
+            if (lane == 31) scan[3 * NW + warp] = upto;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) behind += scan[3 * NW + w];
+        }
+        if ((!few || warp == 0) && share >= behind * p.Hkv && share < (behind + pieces) * p.Hkv) {
+            int b = b_lo, np, n;
+            for (;; ++b) {
+                np = pairs_of(__ldg(p.seqlens + b), p.max_blocks);
+                n = pieces_of(np);
+                if (share < (behind + n) * p.Hkv) break;
+                behind += n;
+                before += np;
+            }
+            const uint32_t at = (uint32_t)(share - behind * p.Hkv);
+            uint32_t head = at, piece = 0, each = np, more = 0;  // (the first `more` pieces have one more than `each`)
+            if (n > 1) {
+                head = at / (uint32_t)n;
+                piece = at - head * n;
+                each = (uint32_t)np / (uint32_t)n;
+                more = np - each * n;
+            }
+            const int64_t run = before * p.Hkv + (int64_t)head * np + piece * each + min(piece, more);
+            words[1] = b;
+            words[2] = (int)piece;
+            words[3] = n;
+            found[1] = before;
+            found[3] = run;
+            found[4] = run + each + (piece < more);
+        }
+    } else {
+        const int64_t fill = (total + MIN_PAIRS - 1) / MIN_PAIRS;
+        const int64_t shares = min(min((int64_t)ctas, total), max((int64_t)p.B * p.Hkv, fill));
+        const int64_t lo = share < shares ? total * share / shares : total;
+        if (threadIdx.x == 0) {
+            words[3] = 0;
+            found[0] = total;
+            found[2] = shares;
+            found[3] = lo;
+            found[4] = share < shares ? total * (share + 1) / shares : total;
+        }
+        if ((!few || warp == 0) && share < shares && lo >= before * p.Hkv && lo < (before + mine) * p.Hkv) {
+            int b = b_lo;
+            for (;; ++b) {
+                const int np = pairs_of(__ldg(p.seqlens + b), p.max_blocks);
+                if (lo < (before + np) * p.Hkv) break;
+                before += np;
+            }
+            words[1] = b;
+            found[1] = before;
+        }
     }
     // Empty sequences (and lengths outside the table, which are reported) belong
     // to no share: their rows are written here.
@@ -286,6 +369,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
         }
     }
     __syncthreads();
+    const int64_t u0 = found[3], u1 = found[4];
     // For the merge: the cut run that the share goes on with, and the one it begins, as
     // first row, query heads, number of shares (0: none) and which of them this one is.
     if (threadIdx.x < 2) p.cuts[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
@@ -312,11 +396,14 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
         if (count < seq_pairs) {
             // The run lies in the shares of its first and last pairs and all between.
             if (threadIdx.x == (first == 0)) {
-                const int64_t all_units = found[0], n_shares = found[2], unit = u - first;
-                const int begin = (int)(((unit + 1) * n_shares + all_units - 1) / all_units - 1);
-                const int end = (int)(((unit + seq_pairs) * n_shares + all_units - 1) / all_units - 1);
-                p.cuts[2 * blockIdx.x + (first == 0)] =
-                    make_int4((int)row0, cols, end - begin + 1, (int)(blockIdx.x / col_blocks) - begin);
+                int parts = words[3], index = words[2];
+                if (parts == 0) {
+                    const int64_t all_units = found[0], n_shares = found[2], unit = u - first;
+                    const int begin = (int)(((unit + 1) * n_shares + all_units - 1) / all_units - 1);
+                    parts = (int)(((unit + seq_pairs) * n_shares + all_units - 1) / all_units - 1) - begin + 1;
+                    index = (int)(blockIdx.x / col_blocks) - begin;
+                }
+                p.cuts[2 * blockIdx.x + (first == 0)] = make_int4((int)row0, cols, parts, index);
             }
         }
         const uint8_t *cache = static_cast<const uint8_t *>(p.cache) + (int64_t)h * BLOCK;

@@ -84,6 +84,19 @@ def test_decode_merges_of_few_and_many_parts(A, Hq, Hkv, lens):
     _decode(A, lens, Hq, Hkv, seed=90 + len(lens))
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (16, 8)])
+@pytest.mark.parametrize("B,hi,long", [(1, 0, 0), (31, 0, 0), (32, 90, 0), (33, 90, 2500), (57, 260, 0), (60, 40, 700),
+                                       (130, 30, 0), (200, 33, 9000), (500, 20, 0)])
+def test_decode_ways_to_share_out_a_batch(A, B, hi, long, Hq, Hkv):
+    """Batches of up to and of more than 32 sequences, of nothing, of short ragged ones with a long one among them, with
+    fewer and with more KV heads than CTAs: whole runs, runs in parts and equal shares."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, hi + 1, (B,), generator=g).tolist()
+    if long:
+        lens[B // 2] = long
+    _decode(A, lens, Hq, Hkv, seed=B)
+
+
 def test_decode_peaked_scores_and_scales(A):
     _decode(A, [500, 33, 1200], 8, 2, seed=5, spread=30.0)
     for scale in (0.0, 1.0):
