@@ -294,8 +294,8 @@ cudaError_t append_u(const AppendParams &p, cudaStream_t stream) {
 // Rows a half-warp takes: the unrolled row count U that covers the tensors' heads
 // with the least work, a chunk's own (angles, factors, addresses) counting as three
 // rows and the unrolled but unused rows in full.  Measured on 12 + 12 heads (32760
-// tokens): U = 4 84 us, 6 72 us, 8 82 us; on 32 + 8 + 8 heads (about 18 thousand
-// tokens): 86, 86 and 74 us.
+// tokens): U = 4 70 us, 6 64 us, 8 67 us; on 32 + 8 + 8 heads (about 18 thousand
+// tokens): 79, 77 and 70 us.
 static int rows_per_chunk(int Hq, int Hkv, int kv_tensors) {
     int best = 0, best_cost = 0;
     for (int U : {8, 6, 4}) {
