@@ -986,8 +986,14 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int row0 = cuts[e].x, cols = cuts[e].y, parts = cuts[e].z, index = cuts[e].w;
+        // (Always within this call's rows, unless a call that runs at the same time has been
+        // given the same workspace: then nothing out of bounds is touched.)
+        if ((unsigned)(parts - 1) >= gridDim.x || (unsigned)index >= (unsigned)parts || cols > cta_cols) continue;
+        const int from = (int)blockIdx.x - index * col_blocks;
+        if (from < 0 || from + (parts - 1) * col_blocks >= (int)gridDim.x || (unsigned)row0 > (unsigned)(p.B * p.Hq - cols))
+            continue;
         if (parts <= SHORT_RUN) {
-            if (index == 0 && parts > 0)
+            if (index == 0)
                 for (int c = warp; c < cols; c += MERGE_WARPS) {
                     add_parts(blockIdx.x, parts, c, 0, 1);
                     write_row((int64_t)row0 + c);
@@ -995,7 +1001,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32)
             continue;
         }
         for (int c = index; c < cols; c += parts) {
-            add_parts((int)blockIdx.x - index * col_blocks, parts, c, warp, MERGE_WARPS);
+            add_parts(from, parts, c, warp, MERGE_WARPS);
             reinterpret_cast<float4 *>(part[warp])[lane] = o;
             if (lane == 0) {
                 part_m[warp] = M;

@@ -518,7 +518,8 @@ size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int d, int max_blo
  * (not rounded to bf16), split over the keys and merged by log-sum-exp.
  * q, block_table, seqlens, out, lse, scale and the errors as in
  * attn_decode_paged; workspace at least attn_decode_q4_workspace_bytes(...)
- * bytes, 256-byte aligned, its contents on entry of no matter.  Slots past a
+ * bytes, 256-byte aligned, its contents on entry of no matter (calls that may run
+ * at the same time, captured ones too, need one each).  Slots past a
  * sequence's end may hold anything.  Deterministic: the same call gives the same
  * bits.  (Where a sequence is cut goes by the lengths of the whole batch, so the
  * order of its sums, and with it the last bit, does too.)  Queries must be below
@@ -540,7 +541,8 @@ attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32
  *      [0, 16 * max_blocks_per_seq] or goes past the bound counts as empty (its
  *      rows get O = 0 and lse = -inf) and is recorded as ATTN_ERR_DEVICE_BOUNDS.
  * workspace: at least attn_fwd_paged_q4_workspace_bytes(...) bytes, 256-byte
- *      aligned; its contents on entry do not matter.
+ *      aligned; its contents on entry do not matter (one each for calls that may
+ *      run at the same time).
  * Other arguments and errors as in attn_fwd_paged.
  */
 size_t attn_fwd_paged_q4_workspace_bytes(int B, int Hkv, int d, int max_total_k);
