@@ -97,6 +97,16 @@ def test_decode_ways_to_share_out_a_batch(A, B, hi, long, Hq, Hkv):
     _decode(A, lens, Hq, Hkv, seed=B)
 
 
+@pytest.mark.parametrize("width", [32, 33, 34])
+@pytest.mark.parametrize("B,Hkv", [(1, 1), (3, 2), (57, 8), (58, 8)])
+def test_decode_around_the_width_that_is_never_cut(A, B, Hkv, width):
+    """Tables of 512 tokens, where no merge is launched, and just above; as many KV heads as there are CTAs, and more."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 16 * width + 1, (B,), generator=g).tolist()
+    lens[B // 2] = 16 * width
+    _decode(A, lens, 2 * Hkv, Hkv, seed=B + width, width=width)
+
+
 def test_decode_peaked_scores_and_scales(A):
     _decode(A, [500, 33, 1200], 8, 2, seed=5, spread=30.0)
     for scale in (0.0, 1.0):
