@@ -239,7 +239,7 @@ attn_status_t attn_fwd_rounded(const void *q, const void *k, const void *v, void
     attn::PrefillParams p;
     fill_prefill_params(&p, di, lse, B, Hq, Hkv, Sq, Sk, layout, causal, scale);
     p.round_mode = round_mode;
-    p.inject = g_inject.exchange(0);
+    p.inject = attn::take_inject(1);
     const bool bhsd = p.bhsd != 0;
     // Q and O boxes: one head x 128 positions, or with head packing the
     // group's G heads x 128 / G positions.
@@ -320,7 +320,7 @@ attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void 
     p.total_q = total_q;
     p.total_k = total_k;
     p.out = out;
-    p.inject = g_inject.exchange(0);
+    p.inject = attn::take_inject(1);
     const int64_t units = p.pair_heads ? (int64_t)B * Hkv * (p.G / 2) * p.n_m : (int64_t)B * Hq * ((p.n_m + 1) / 2);
     if (units > 0x7fffffff) return ATTN_ERR_INVALID_ARG;
     p.n_full_units = (int)units;
@@ -369,7 +369,7 @@ attn_status_t attn_fwd_paged(const void *q, const void *k_pages, const void *v_p
     p.seqlens_k = seqlens_k;
     p.max_blocks = max_blocks_per_seq;
     p.num_pages = num_pages;
-    p.inject = g_inject.exchange(0);
+    p.inject = attn::take_inject(1);
     const int64_t units = p.pair_heads ? (int64_t)B * Hkv * (p.G / 2) * p.n_m : (int64_t)B * Hq * ((p.n_m + 1) / 2);
     if (units > 0x7fffffff) return ATTN_ERR_INVALID_ARG;
     p.n_full_units = (int)units;
@@ -468,6 +468,10 @@ attn_status_t device_state(int *sm_count, unsigned **status, uint64_t *budget_ns
     *status = di->status;
     *budget_ns = budget();
     return ATTN_OK;
+}
+
+int take_inject(int mode) {
+    return g_inject.load(std::memory_order_relaxed) == mode && g_inject.compare_exchange_strong(mode, 0);
 }
 
 }  // namespace attn
@@ -577,7 +581,7 @@ attn_status_t attn_set_wait_budget_ns(uint64_t ns) {
 }
 
 attn_status_t attn_debug_inject(int mode) {
-    if (mode < 0 || mode > 1) return ATTN_ERR_INVALID_ARG;
+    if (mode < 0 || mode > 2) return ATTN_ERR_INVALID_ARG;
     g_inject.store(mode);
     return ATTN_OK;
 }

@@ -243,6 +243,7 @@ attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     int sms;
     if ((st = attn::device_state(&sms, &p.status, &p.budget_ns)) != ATTN_OK) return st;
+    p.inject = attn::take_inject(2);
     return attn::launch_decode_q4(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

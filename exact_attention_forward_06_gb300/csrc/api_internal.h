@@ -19,4 +19,7 @@ attn_status_t check_decode_args(const void *q, const void *k_pages, const void *
 // device is looked up once and must be one that the kernels are built for.
 attn_status_t device_state(int *sm_count, unsigned **status, uint64_t *budget_ns);
 
+// Whether attn_debug_inject has asked for this mode; the request is then cleared.
+int take_inject(int mode);
+
 }  // namespace attn

@@ -67,6 +67,7 @@ struct DecodeQ4Params {
     float scale_log2;
     unsigned *status;
     uint64_t budget_ns;
+    int inject;  // 1: the first two warps of each CTA issue no copy (fault-injection test)
 };
 
 // Launches a kernel as a programmatic dependent of the work before it on the

@@ -77,6 +77,16 @@ static __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t pari
     }
 }
 
+// The same wait by a whole warp, with one answer for all its lanes.  Where
+// warp-wide operations follow, a lane's own answer will not do: with the abort
+// flag raised while the phase completes, one lane may see the phase and the next
+// the flag, and the first would then wait for ever in a shuffle or a vote for
+// lanes that have left.
+static __device__ __forceinline__ bool warp_wait_bounded(uint64_t *bar, uint32_t parity, const WaitCtx &w,
+                                                         unsigned site) {
+    return __all_sync(0xffffffffu, wait_bounded(bar, parity, w, site));
+}
+
 // Wait by polling with the non-blocking test (the issuing threads, whose
 // reaction time is on the critical path).
 static __device__ __forceinline__ bool wait_spin(uint64_t *bar, uint32_t parity, const WaitCtx &w, unsigned site) {

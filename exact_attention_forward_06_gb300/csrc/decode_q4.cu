@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
             whole = __ballot_sync(0xffffffffu, nv0 == PAGE && nv1 == PAGE);
         };
         auto issue = [&](int i, int to) {  // pair i of the batch, by the lane that holds it
-            if (lane == i) {
+            if (lane == i && !(p.inject && warp < 2)) {  // (fault injection)
                 uint8_t *dst = ring + to * STAGE;
                 ptx::mbar_arrive_expect_tx(full + to, (tab0 >= 0 ? BLOCK : 0) + (tab1 >= 0 ? BLOCK : 0));
                 if (tab0 >= 0) ptx::bulk_load(dst, cache + tab0 * page_step, BLOCK, full + to, pol);
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
             const int batch = min(left, 32);
             int i = 0;
             for (; i < batch; ++i) {
-                if (!wait_bounded(full + slot, parity, wc, kSiteQ4Page)) break;
+                if (!warp_wait_bounded(full + slot, parity, wc, kSiteQ4Page)) break;
                 const uint8_t *blk = ring + slot * STAGE;
                 float s[2][TILES][4];
 #pragma unroll
