@@ -522,6 +522,7 @@ static attn_status_t decode_impl(const void *q, const void *k_new, const void *v
     p.v_new = v_new;
     p.k_pool = const_cast<void *>(k_pages);
     p.v_pool = const_cast<void *>(v_pages);
+    p.inject = attn::take_inject(2);
     if (attn::launch_decode(mk, mv, p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
     return ATTN_OK;
 }

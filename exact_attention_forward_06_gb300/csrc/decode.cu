@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(NTHREADS, 3)
             // stream from pushing other work's data out of L2.
             const uint64_t pol = ptx::policy_evict_first();
             int issued = 0;
-            for (int i = 0; i < np; ++i) {
+            for (int i = 0; i < np && !p.inject; ++i) {  // (fault injection: issue nothing)
                 const int slot = i % NST;
                 const int round = i / NST;
                 if (round > 0 && !wait_bounded(empty + slot, (round - 1) & 1, wc, kSiteDecodeEmpty)) break;
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(NTHREADS, 3)
 
         for (int i = warp; i < np; i += NCW) {
             const int slot = i % NST;
-            if (!wait_bounded(full + slot, (i / NST) & 1, wc, kSiteDecodeFull)) break;
+            if (!warp_wait_bounded(full + slot, (i / NST) & 1, wc, kSiteDecodeFull)) break;
             // A page whose block-table entry could not be read holds nothing of
             // the sequence: it is skipped.
             if (stage_bad[slot] == 0) {

@@ -101,6 +101,7 @@ struct DecodeParams {
     const void *v_new;
     void *k_pool;
     void *v_pool;
+    int inject;  // 1: the producers issue nothing (fault-injection test)
 };
 
 void decode_split_plan(int B, int Hq, int max_blocks, int *nsplit, int *pages_per_split);

@@ -591,9 +591,10 @@ attn_status_t attn_set_wait_budget_ns(uint64_t ns);
  * kernel with the load-issuing warp told to issue nothing, so the other warps'
  * bounded waits expire, they record ATTN_ERR_TIMEOUT and the kernel exits
  * cleanly (no fault, no hang, nothing left in flight).  mode 2: the same for
- * the next attn_decode_paged_q4, the first two warps of each of whose CTAs
- * issue no copy.  A request clears itself with the launch that takes it; other
- * launches leave it.
+ * the next decode: over bf16 pages its load-issuing warps issue nothing, over
+ * the 4-bit cache (attn_decode_paged_q4) the first two warps of each CTA do not.
+ * A request clears itself with the launch that takes it; other launches leave
+ * it.
  */
 attn_status_t attn_debug_inject(int mode);
 
