@@ -84,7 +84,20 @@ static __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t pari
 // lanes that have left.
 static __device__ __forceinline__ bool warp_wait_bounded(uint64_t *bar, uint32_t parity, const WaitCtx &w,
                                                          unsigned site) {
-    return __all_sync(0xffffffffu, wait_bounded(bar, parity, w, site));
+    constexpr unsigned ALL = 0xffffffffu;
+    if (__all_sync(ALL, ptx::mbar_try(bar, parity))) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t it = 1;; ++it) {
+        if (__all_sync(ALL, ptx::mbar_try(bar, parity))) return true;
+        const bool late = (it & 15u) == 0 && ptx::globaltimer() - t0 > w.budget_ns;
+        if (__any_sync(ALL, late || *w.abort_flag)) {
+            if (late) {
+                *w.abort_flag = 1;
+                report_status(w.status, kStatusTimeout, site);
+            }
+            return false;
+        }
+    }
 }
 
 // Wait by polling with the non-blocking test (the issuing threads, whose
