@@ -401,13 +401,15 @@ __device__ __forceinline__ bool publish_unit(const SmemLayout &sm, const WaitCtx
     return true;
 }
 
-// Reader side (every lane of a reading warp): unit u of this CTA.  Returns
-// false when the CTA is giving up; w.n_kv = -1 marks the end of the list.
-// The caller hands the entry back (item_empty) once every lane has read it.
+// Reader side (one lane that polls, or every lane of a warp, with one answer
+// for all of them): unit u of this CTA.  Returns false when the CTA is giving
+// up; w.n_kv = -1 marks the end of the list.  The caller hands the entry
+// back (item_empty) once every lane has read it.
 __device__ __forceinline__ bool read_unit(const SmemLayout &sm, const WaitCtx &wc, int u, bool spin, Unit &w) {
     const int e = u % ITEM_RING;
     const uint32_t par = (uint32_t)((u / ITEM_RING) & 1);
-    if (!(spin ? wait_spin(sm.item_full(e), par, wc, kSiteItem) : wait_bounded(sm.item_full(e), par, wc, kSiteItem)))
+    if (!(spin ? wait_spin(sm.item_full(e), par, wc, kSiteItem)
+               : warp_wait_bounded(sm.item_full(e), par, wc, kSiteItem)))
         return false;
     const volatile int *d = sm.item_ring(e);
     w.b = d[0]; w.g = d[1]; w.h[0] = d[2]; w.h[1] = d[3]; w.s0[0] = d[4]; w.s0[1] = d[5]; w.n_kv = d[6];
@@ -867,6 +869,7 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
     int nb = 0;  // ring number of the unit's first K/V item
     int g0 = 0;  // running index of the unit's first score tile
     const bool leader = quarter == 0 && lane == 0;
+    bool left = false;  // out of the loop without the group's barrier
     int n_cmd = 0;  // store commands handed to this tile's store lane
     // The leader writes command n_cmd once the store lane has read the one
     // before (kind 0: no more tiles).
@@ -889,7 +892,10 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
         const bool got = read_unit(sm, wc, u, false, w);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(sm.item_empty(u % ITEM_RING));
-        if (!got || w.n_kv < 0) break;  // giving up, or the end of the list (every warp of the group alike)
+        if (!got || w.n_kv < 0) {  // giving up, or the end of the list
+            left = true;
+            break;
+        }
         // Selects, not a runtime index: an indexed Unit array would live in local memory.
         const int s0 = t ? w.s0[1] : w.s0[0];
         const int h0 = t ? w.h[1] : w.h[0];
@@ -908,6 +914,10 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
         // the tile's first position is its smallest
         const int lim_tile = p.causal ? min(s0 + w.Sk - w.Sq, w.Sk - 1) : w.Sk - 1;
         float m_run = -INFINITY, l_run = 0.f;
+        // Cleared by a wait that gives up.  A warp comes to the waits of its tiles
+        // converged and its lanes read the phase and the abort flag in the same
+        // instructions, so they give up alike (a vote at each of them would take
+        // 3.6% of a paged prefill).
         bool ok = true;
 
         // No rows of the sequence: pass the score and P turns on.  The wait for
@@ -1065,12 +1075,14 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
         // ring, then a TMA store from there.  Every warp of the group reaches
         // the group barrier once per unit, whether or not it gave up on a wait,
         // and the barrier ANDs everyone's "all well" so that the whole group
-        // takes the same decision to go on or to stop.
+        // takes the same decision to go on or to stop.  Tensor memory is read by
+        // whole warps, so a lane that gave up takes part; it stores nothing outside
+        // the staging slot, which is then handed to nobody.
         if (ok && w.n_kv > 0) ok = wait_bounded(sm.o_full(t), (uint32_t)((g0 + w.n_kv - 1) & 1), wc, kSiteEpilogueO);
         const int o_item = nb + 2 * w.n_kv + t;
         uint8_t *stage = sm.slot(o_item % NSLOT);
         if (ok) ok = wait_bounded(sm.kv_full(o_item % NSLOT), (uint32_t)((o_item / NSLOT) & 1), wc, kSiteEpilogueSlot);
-        if (!PACKED && ok && w.part >= 0) {
+        if (!PACKED && w.part >= 0) {
             // A key-range part of a split unit: its O (normalised within the range)
             // and log-sum-exp go to the workspace in fp32 for the merge kernel.
             ptx::tc_fence_after();
@@ -1087,11 +1099,11 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
                     float4 x = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
                                            __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
                     if (!(l_run > 0.f)) x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    dst[ch * 8 + i] = x;
+                    if (ok) dst[ch * 8 + i] = x;
                 }
             }
-            p.ws_lse[row * p.split_parts + w.part] = l_run > 0.f ? (m_run + ptx::lg2(l_run)) * LN2 : -INFINITY;
-        } else if (ok && !dead) {
+            if (ok) p.ws_lse[row * p.split_parts + w.part] = l_run > 0.f ? (m_run + ptx::lg2(l_run)) * LN2 : -INFINITY;
+        } else if (!dead) {
             ptx::tc_fence_after();
             const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
 #pragma unroll 1
@@ -1116,7 +1128,7 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
                         make_uint4(wv[4 * kk], wv[4 * kk + 1], wv[4 * kk + 2], wv[4 * kk + 3]);
                 }
             }
-            if (p.lse != nullptr && pos < w.Sq) {
+            if (p.lse != nullptr && pos < w.Sq && ok) {
                 const float lse = l_run > 0.f ? (m_run + ptx::lg2(l_run)) * LN2 : -INFINITY;
                 const int64_t li = PACKED ? (int64_t)head * p.total_q + w.q0 + pos
                                           : ((int64_t)w.b * p.Hq + head) * p.Sq + pos;
@@ -1153,6 +1165,11 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
         nb += ring_items(w);
         g0 += w.n_kv;
     }
+    // A warp that gives up on a unit it could not read may be alone in it: the
+    // group's others may have read the unit, and wait for all four warps at the
+    // unit's barrier.  So every warp comes to that barrier once a unit, the last
+    // time here, and one "not well" makes all of them leave.
+    if (left) ptx::named_bar_and(1 + t, 128, false);
     if (leader) send_cmd(0, 0, Coord4{0, 0, 0, 0});  // the store lane stops (if it still waits)
 }
 
