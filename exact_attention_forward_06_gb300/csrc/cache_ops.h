@@ -73,7 +73,9 @@ struct DecodeQ4Params {
 // Launches a kernel as a programmatic dependent of the work before it on the
 // stream: its blocks may be set up while that work finishes.  Such a kernel
 // begins with ptx::wait_for_prior_work() (griddepcontrol.wait), before it reads
-// or writes anything.
+// or writes anything.  It reads with ordinary loads only: the work before may still
+// be writing when its first blocks start, and the non-coherent loads of __ldg want
+// data that nobody writes as long as the kernel runs.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                              Args... args) {

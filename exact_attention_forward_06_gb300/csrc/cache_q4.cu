@@ -44,17 +44,17 @@ __device__ __forceinline__ Found find_given(const GatherQ4Params &p, int64_t j, 
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) >> 5;
         const int i = lo + (lane + 1) * step;
-        const bool le = i < hi && (int64_t)__ldg(p.cu_k + i) / PAGE + i <= j;
+        const bool le = i < hi && (int64_t)p.cu_k[i] / PAGE + i <= j;
         lo += __popc(__ballot_sync(0xffffffffu, le)) * step;
         hi = min(hi, lo + step);
     }
-    const int begin = __ldg(p.cu_k + lo), end = __ldg(p.cu_k + lo + 1), L = __ldg(p.seqlens + lo);
+    const int begin = p.cu_k[lo], end = p.cu_k[lo + 1], L = p.seqlens[lo];
     const bool ok = begin >= 0 && end <= p.total_k && L == end - begin && L >= 0 && L <= p.max_blocks * PAGE;
     return Found{lo, begin, L, ok};
 }
 
 __device__ __forceinline__ int length_of(const GatherQ4Params &p, int b) {
-    const int L = __ldg(p.seqlens + b);
+    const int L = p.seqlens[b];
     return L < 0 || L > p.max_blocks * PAGE ? 0 : L;
 }
 
@@ -95,7 +95,7 @@ __device__ __forceinline__ Found find_own(const GatherQ4Params &p, int64_t j, in
             const int L = length_of(p, b);
             end += L;
             if (end <= p.total_k) last = (int)end;
-            if (L != __ldg(p.seqlens + b) || (end > p.total_k && L > 0))
+            if (L != p.seqlens[b] || (end > p.total_k && L > 0))
                 report_status(p.status, kStatusDeviceBounds, kSiteQ4Offsets);
         }
         atomicMax(&runs.last, last);
@@ -166,15 +166,17 @@ __global__ void __launch_bounds__(GWARPS * 32) gather_kernel(const GatherQ4Param
     const int64_t first = (int64_t)begin / PAGE + lo;
     const int64_t t0 = (j - first) * PAGE;
     if (j < first || t0 >= L) return;
-    const int page = __ldg(p.block_table + (int64_t)lo * p.max_blocks + (j - first));
+    const int page = p.block_table[(int64_t)lo * p.max_blocks + (j - first)];
     const bool ok = page >= 0 && page < p.num_pages;
     if (!ok && lane == 0) report_status(p.status, kStatusDeviceBounds, kSiteQ4Table);
     uint4 *to = reinterpret_cast<uint4 *>(stage[warp]);
     const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.cache) +
                                                         ((int64_t)page * p.Hkv + h) * BLOCK);
+    uint4 part[BLOCK / 16 / 32];
 #pragma unroll
-    for (int i = 0; i < BLOCK / 16 / 32; ++i)
-        to[lane + 32 * i] = ok ? __ldg(from + lane + 32 * i) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < BLOCK / 16 / 32; ++i) part[i] = ok ? from[lane + 32 * i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < BLOCK / 16 / 32; ++i) to[lane + 32 * i] = part[i];
     __syncwarp();
     const uint8_t *blk = stage[warp];
     const int n = min(PAGE, L - (int)t0);

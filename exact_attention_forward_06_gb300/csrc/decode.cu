@@ -444,9 +444,7 @@ __global__ void __launch_bounds__(NTHREADS, 3)
 }
 
 // One CTA per row, one thread per head-dim element; splits merged in order.
-__global__ void __launch_bounds__(D) merge_kernel(const float *__restrict__ o_parts,
-                                                  const float *__restrict__ lse_parts,
-                                                  uint16_t *__restrict__ out, float *__restrict__ lse,
+__global__ void __launch_bounds__(D) merge_kernel(const float *o_parts, const float *lse_parts, uint16_t *out, float *lse,
                                                   int nsplit, int round_mode) {
     // Launched as a programmatic dependent of the split kernel: wait here
     // until that grid has completed and its partials are visible.

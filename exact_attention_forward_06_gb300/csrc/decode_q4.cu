@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
     // words[1]: the share's first sequence; [2], [3]: which part of how many its run is of its
     // sequence (whole runs; else 0 and 0).  found: [0] total, [1] pairs before that
     // sequence, [2] shares, [3], [4] the share's first unit and the one behind its last.
+    // words[14]: that sequence's length.
     int64_t *found = reinterpret_cast<int64_t *>(words + 4);
     int *scan = words + 16;  // [4][NW]
 
@@ -244,12 +245,16 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
     const int per = few ? 1 : (p.B + NT - 1) / NT;
     const int b_lo = min(p.B, (few ? lane : (int)threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
     int mine = 0, some = 0, longest = 0;  // pairs: at most 2^31, B * max_blocks / 2 is bounded by the caller
+    int len = 0;                          // (few: of the lane's sequence)
     for (int b = b_lo; b < b_hi; ++b) {
-        const int np = pairs_of(__ldg(p.seqlens + b), p.max_blocks);
+        len = p.seqlens[b];
+        const int np = pairs_of(len, p.max_blocks);
         mine += np;
         some += np > 0;
         longest = max(longest, np);
     }
+    // The length of a sequence of this thread's run, read again only where there are several.
+    const auto own_length = [&](int b) { return few ? len : p.seqlens[b]; };
     const auto inclusive = [&](int v) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
             return (uint32_t)np <= part ? (int)(np > 0) : (int)(((uint32_t)np + part - 1) / part);
         };
         int pieces = 0;
-        for (int b = b_lo; b < b_hi; ++b) pieces += pieces_of(pairs_of(__ldg(p.seqlens + b), p.max_blocks));
+        for (int b = b_lo; b < b_hi; ++b) pieces += pieces_of(pairs_of(own_length(b), p.max_blocks));
         const int upto = inclusive(pieces);
         if (threadIdx.x == 0) found[3] = found[4] = 0;
         int behind = upto - pieces;  // (at most as many as there are CTAs)
@@ -317,9 +322,10 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
             for (int w = 0; w < warp; ++w) behind += scan[3 * NW + w];
         }
         if ((!few || warp == 0) && share >= behind * p.Hkv && share < (behind + pieces) * p.Hkv) {
-            int b = b_lo, np, n;
+            int b = b_lo, L, np, n;
             for (;; ++b) {
-                np = pairs_of(__ldg(p.seqlens + b), p.max_blocks);
+                L = own_length(b);
+                np = pairs_of(L, p.max_blocks);
                 n = pieces_of(np);
                 if (share < (behind + n) * p.Hkv) break;
                 behind += n;
@@ -335,6 +341,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
             }
             const int64_t run = before * p.Hkv + (int64_t)head * np + piece * each + min(piece, more);
             words[1] = b;
+            words[14] = L;
             words[2] = (int)piece;
             words[3] = n;
             found[1] = before;
@@ -353,13 +360,15 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
             found[4] = share < shares ? total * (share + 1) / shares : total;
         }
         if ((!few || warp == 0) && share < shares && lo >= before * p.Hkv && lo < (before + mine) * p.Hkv) {
-            int b = b_lo;
+            int b = b_lo, L;
             for (;; ++b) {
-                const int np = pairs_of(__ldg(p.seqlens + b), p.max_blocks);
+                L = own_length(b);
+                const int np = pairs_of(L, p.max_blocks);
                 if (lo < (before + np) * p.Hkv) break;
                 before += np;
             }
             words[1] = b;
+            words[14] = L;
             found[1] = before;
         }
     }
@@ -367,7 +376,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
     // to no share: their rows are written here.
     if (blk == 0) {
         for (int b = share; b < p.B; b += gridDim.x / col_blocks) {
-            const int L = __ldg(p.seqlens + b);
+            const int L = few ? __shfl_sync(0xffffffffu, len, b) : p.seqlens[b];
             if (pairs_of(L, p.max_blocks) > 0) continue;
             if (L != 0 && threadIdx.x == 0) report_status(p.status, kStatusDeviceBounds, kSiteQ4Seqlen);
             for (int i = threadIdx.x; i < p.Hq * (D / 8); i += NT)
@@ -392,7 +401,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
     int b = 0, h = 0, L = 0, seq_pairs = 0, first = 0;  // the segment: sequence, KV head, first pair
     if (u0 < u1) {
         b = words[1];
-        L = __ldg(p.seqlens + b);
+        L = words[14];
         seq_pairs = pairs_of(L, p.max_blocks);
         const int64_t rem = u0 - found[1] * p.Hkv;
         h = (int)(rem / seq_pairs);
@@ -428,9 +437,9 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
             nv0 = nv1 = 0;
             if (base + lane < n) {
                 const int page = 2 * (first + warp + NW * (base + lane));
-                tab0 = __ldg(table + page);
+                tab0 = table[page];
                 const bool two = page + 1 < last_page;
-                if (two) tab1 = __ldg(table + page + 1);
+                if (two) tab1 = table[page + 1];
                 const bool bad0 = tab0 < 0 || tab0 >= p.num_pages;
                 const bool bad1 = two && (tab1 < 0 || tab1 >= p.num_pages);
                 if (bad0 || bad1) report_status(p.status, kStatusDeviceBounds, kSiteQ4Table);
@@ -457,6 +466,16 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
                 to = to + 1 == NST ? 0 : to + 1;
             }
         };
+        // The queries' loads go out before the wait for the table's.
+        uint4 q_words[TILES][4];
+#pragma unroll
+        for (int c = 0; c < TILES; ++c) {
+            const uint4 *qrow =
+                reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + (row0 + 8 * c + r4) * D);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                q_words[c][g] = 8 * c + r4 < cols ? qrow[4 * g + c4] : make_uint4(0, 0, 0, 0);
+        }
         load_table(0);
         issue_first(min(n, 32));
 
@@ -473,13 +492,10 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
         uint32_t qz0[TILES], qz1[TILES], qo0[TILES], qo1[TILES];
 #pragma unroll
         for (int c = 0; c < TILES; ++c) {
-            const uint4 *qrow =
-                reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + (row0 + 8 * c + r4) * D);
-            uint4 v[4];
+            const uint4(&v)[4] = q_words[c];
             uint32_t largest = 0;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                v[g] = 8 * c + r4 < cols ? __ldg(qrow + 4 * g + c4) : make_uint4(0, 0, 0, 0);
                 constexpr uint32_t SIZE = 0x7fff7fffu;
                 largest = __vmaxu2(largest, __vmaxu2(__vmaxu2(v[g].x & SIZE, v[g].y & SIZE),
                                                      __vmaxu2(v[g].z & SIZE, v[g].w & SIZE)));
@@ -918,7 +934,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
         if (++h == p.Hkv && u < u1) {
             h = 0;
             do {
-                L = __ldg(p.seqlens + ++b);
+                L = p.seqlens[++b];
                 seq_pairs = pairs_of(L, p.max_blocks);
             } while (seq_pairs == 0);
         }

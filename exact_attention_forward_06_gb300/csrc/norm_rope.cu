@@ -102,18 +102,18 @@ __device__ __forceinline__ bool locate(const AppendParams &p, const Place &at, i
         for (int len = p.B; len > 1;) {
             const int step = (len + 15) >> 4;
             const int i = lo + (at.l + 1) * step;
-            const bool le = (at.l + 1) * step < len && i < p.B && __ldg(p.cu + i) <= t;
+            const bool le = (at.l + 1) * step < len && i < p.B && p.cu[i] <= t;
             const unsigned votes = __ballot_sync(0xffffffffu, le) >> (threadIdx.x & 16);
             lo += __popc(votes & 0xffffu) * step;
             len = step;
         }
         b = lo;
-        begin = __ldg(p.cu + b);
-        end = __ldg(p.cu + b + 1);
+        begin = p.cu[b];
+        end = p.cu[b + 1];
         if (t < begin || t >= end) {
             ok = false;
             // Before the first or behind the last sequence: nobody's row.
-            const bool nobody = t < __ldg(p.cu) || t >= __ldg(p.cu + p.B);
+            const bool nobody = t < p.cu[0] || t >= p.cu[p.B];
             if (!nobody && at.l == 0) report_status(p.r.status, kStatusDeviceBounds, kSiteAppendOffsets);
         } else if (begin < 0 || end > p.total) {
             ok = false;
@@ -121,14 +121,14 @@ __device__ __forceinline__ bool locate(const AppendParams &p, const Place &at, i
         }
     }
     if (!ok) return false;
-    const int L = __ldg(p.seqlens + b);
+    const int L = p.seqlens[b];
     if (L == 0 && !p.cu) return false;  // an idle row of a batch of single tokens
     if (L < end - begin || L > p.max_blocks * 16) {
         if (at.l == 0) report_status(p.r.status, kStatusDeviceBounds, kSiteAppendSlot);
         return false;
     }
     *slot = L - (end - t);
-    const int pg = __ldg(p.block_table + (int64_t)b * p.max_blocks + *slot / 16);
+    const int pg = p.block_table[(int64_t)b * p.max_blocks + *slot / 16];
     if (pg >= 0 && pg < p.num_pages)
         *page = pg;
     else if (at.l == 0)

@@ -95,12 +95,12 @@ __device__ __forceinline__ LaneTurn lane_turn(const RotateParams &p, int l, int6
     int pos[4];
     bool bad = false;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) e[j] = __ldg(reinterpret_cast<const uint4 *>(p.rope) + 4 * l + j);
+    for (int j = 0; j < 4; ++j) e[j] = reinterpret_cast<const uint4 *>(p.rope)[4 * l + j];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const bool known = e[j].z < (uint32_t)p.n_axes;
         bad = bad || !known;
-        pos[j] = p.positions && known ? __ldg(p.positions + (int64_t)e[j].z * pos_stride + token) : pos0;
+        pos[j] = p.positions && known ? p.positions[(int64_t)e[j].z * pos_stride + token] : pos0;
         if (!known) e[j].x = e[j].y = 0;  // not rotated
     }
     if (bad) report_status(p.status, kStatusDeviceBounds, kSiteRopeAxis);
