@@ -38,6 +38,24 @@ struct Found {
     bool ok;
 };
 
+// Whether a sequence's offsets and length are in order.
+__device__ __forceinline__ bool in_order(const GatherQ4Params &p, int begin, int end, int L) {
+    return begin >= 0 && end <= p.total_k && L >= 0 && L <= p.max_blocks * PAGE && (int64_t)end - begin == L;
+}
+
+// Looks all given offsets over, in blocks of their own behind the items' (with offsets out
+// of order, no item need lead to a sequence).
+constexpr int CHECKS = 8;  // sequences a thread
+__device__ __forceinline__ void check_given(const GatherQ4Params &p, unsigned block) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < CHECKS; ++i) {
+        const int64_t b = ((int64_t)block * CHECKS + i) * (GWARPS * 32) + threadIdx.x;
+        if (b < p.B) bad = bad || !in_order(p, p.cu_k[b], p.cu_k[b + 1], p.seqlens[b]);
+    }
+    if (bad) report_status(p.status, kStatusDeviceBounds, kSiteQ4Offsets);
+}
+
 // The last sequence b with cu_k[b] / 16 + b <= j, from given offsets.
 __device__ __forceinline__ Found find_given(const GatherQ4Params &p, int64_t j, int lane) {
     int lo = 0, hi = p.B;
@@ -49,8 +67,7 @@ __device__ __forceinline__ Found find_given(const GatherQ4Params &p, int64_t j, 
         hi = min(hi, lo + step);
     }
     const int begin = p.cu_k[lo], end = p.cu_k[lo + 1], L = p.seqlens[lo];
-    const bool ok = begin >= 0 && end <= p.total_k && L == end - begin && L >= 0 && L <= p.max_blocks * PAGE;
-    return Found{lo, begin, L, ok};
+    return Found{lo, begin, L, in_order(p, begin, end, L)};
 }
 
 __device__ __forceinline__ int length_of(const GatherQ4Params &p, int b) {
@@ -147,21 +164,22 @@ __device__ __forceinline__ Found find_own(const GatherQ4Params &p, int64_t j, in
 // head.  3.2 bytes are written for each one read; the bound is HBM: 68 thousand
 // tokens of 8 heads (366 MB) take 57 us, 0.93 of the copy bandwidth.
 template <bool OWN>
-__global__ void __launch_bounds__(GWARPS * 32) gather_kernel(const GatherQ4Params p) {
+__global__ void __launch_bounds__(GWARPS * 32) gather_kernel(const GatherQ4Params p, unsigned item_blocks) {
     __shared__ __align__(16) uint8_t stage[GWARPS][BLOCK];
     __shared__ RunSums runs[1];
     ptx::wait_for_prior_work();
     ptx::allow_next_work();
+    if (!OWN && blockIdx.x >= item_blocks) {
+        check_given(p, blockIdx.x - item_blocks);
+        return;
+    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t item = (int64_t)blockIdx.x * GWARPS + warp;
     const int h = (int)(item % p.Hkv);
     const int64_t j = item / p.Hkv;
     const Found f = OWN ? find_own(p, j, lane, runs[0]) : find_given(p, j, lane);
     if (j >= (int64_t)p.total_k / PAGE + p.B) return;
-    if (!f.ok) {
-        if (!OWN && lane == 0) report_status(p.status, kStatusDeviceBounds, kSiteQ4Offsets);
-        return;
-    }
+    if (!f.ok) return;  // (reported by the blocks that look the offsets over)
     const int lo = f.b, begin = f.begin, L = f.L;
     const int64_t first = (int64_t)begin / PAGE + lo;
     const int64_t t0 = (j - first) * PAGE;
@@ -198,10 +216,12 @@ __global__ void __launch_bounds__(GWARPS * 32) gather_kernel(const GatherQ4Param
 
 cudaError_t launch_gather_q4(const GatherQ4Params &p, cudaStream_t stream) {
     const int64_t items = ((int64_t)p.total_k / q4::PAGE + p.B) * p.Hkv;
-    const int64_t grid = (items + q4::GWARPS - 1) / q4::GWARPS;
+    const int64_t blocks = (items + q4::GWARPS - 1) / q4::GWARPS;
+    constexpr int64_t per = q4::GWARPS * 32 * q4::CHECKS;
+    const int64_t grid = blocks + (p.cu_k ? (p.B + per - 1) / per : 0);
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
     return launch_dependent(p.cu_k ? q4::gather_kernel<false> : q4::gather_kernel<true>, (unsigned)grid, q4::GWARPS * 32, 0,
-                            stream, p);
+                            stream, p, (unsigned)blocks);
 }
 
 }  // namespace attn

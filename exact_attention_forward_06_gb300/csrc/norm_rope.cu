@@ -86,6 +86,22 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormRopeParams
     }
 }
 
+// Looks all offsets over, in blocks of their own behind the rows' (the row of a token need
+// not lead to the sequence whose offsets are wrong): in order, and within the rows.
+constexpr int CHECKS = 8;  // sequences a thread
+__device__ __forceinline__ void check_offsets(const AppendParams &p, unsigned block) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < CHECKS; ++i) {
+        const int64_t b = ((int64_t)block * CHECKS + i) * THREADS + threadIdx.x;
+        if (b < p.B) {
+            const int begin = p.cu[b], end = p.cu[b + 1];
+            bad = bad || begin < 0 || end < begin || end > p.total;
+        }
+    }
+    if (bad) report_status(p.r.status, kStatusDeviceBounds, kSiteAppendOffsets);
+}
+
 // Where a new token goes: its sequence's position for it, and its page (-1: a
 // bad table entry, already reported).  Returns false when the token belongs to
 // no sequence, its row is idle or its sequence is malformed (reported).  The
@@ -93,7 +109,6 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormRopeParams
 __device__ __forceinline__ bool locate(const AppendParams &p, const Place &at, int *slot, int64_t *page) {
     const int t = (int)at.token;
     int b = t, begin = t, end = t + 1;
-    bool ok = true;
     *slot = 0;
     *page = -1;
     if (p.cu) {
@@ -110,17 +125,9 @@ __device__ __forceinline__ bool locate(const AppendParams &p, const Place &at, i
         b = lo;
         begin = p.cu[b];
         end = p.cu[b + 1];
-        if (t < begin || t >= end) {
-            ok = false;
-            // Before the first or behind the last sequence: nobody's row.
-            const bool nobody = t < p.cu[0] || t >= p.cu[p.B];
-            if (!nobody && at.l == 0) report_status(p.r.status, kStatusDeviceBounds, kSiteAppendOffsets);
-        } else if (begin < 0 || end > p.total) {
-            ok = false;
-            if (at.l == 0) report_status(p.r.status, kStatusDeviceBounds, kSiteAppendOffsets);
-        }
+        // A row of no sequence, or of malformed offsets (check_offsets reports them).
+        if (t < begin || t >= end || begin < 0 || end > p.total) return false;
     }
-    if (!ok) return false;
     const int L = p.seqlens[b];
     if (L == 0 && !p.cu) return false;  // an idle row of a batch of single tokens
     if (L < end - begin || L > p.max_blocks * 16) {
@@ -181,12 +188,16 @@ __device__ __forceinline__ void quantise_store(uint8_t *block, int t, bool is_v,
 // (with the read-back, 6, 7, 8 blocks: 148, 144, 141 us; the bf16 append, 7, 8: 69.9,
 // 70.7).
 template <bool INTER, bool Q4, int U>
-__global__ void __launch_bounds__(THREADS, Q4 ? 8 : 7) append_kernel(const AppendParams p, Chunks cq, Chunks ckv) {
+__global__ void __launch_bounds__(THREADS, Q4 ? 8 : 7) append_kernel(const AppendParams p, Chunks cq, Chunks ckv, unsigned row_blocks) {
     // Q4: the lane layout of a rotated row goes to eight consecutive channels
     // a lane through shared memory, one row per half-warp.
     __shared__ __align__(16) uint16_t turn_row[Q4 && !INTER ? HALVES : 1][Q4 && !INTER ? D : 8];
     ptx::wait_for_prior_work();
     ptx::allow_next_work();
+    if (blockIdx.x >= row_blocks) {
+        check_offsets(p, blockIdx.x - row_blocks);
+        return;
+    }
     const Place at = place(cq.chunks + 2 * ckv.chunks, p.total);
     const bool is_q = at.chunk < cq.chunks, is_v = at.chunk >= cq.chunks + ckv.chunks;
     const Chunks c = is_q ? cq : ckv;
@@ -279,14 +290,13 @@ cudaError_t norm_rope_u(const NormRopeParams &p, cudaStream_t stream) {
 template <int U>
 cudaError_t append_u(const AppendParams &p, cudaStream_t stream) {
     const nr::Chunks cq = chunks_of(p.Hq, U), ckv = chunks_of(p.Hkv, U);
-    unsigned grid;
-    if (!row_grid(p.total, cq.chunks + 2 * ckv.chunks, &grid)) return cudaErrorInvalidValue;
-    if (p.cache && p.r.interleaved)
-        return launch_dependent(nr::append_kernel<true, true, U>, grid, nr::THREADS, 0, stream, p, cq, ckv);
-    if (p.cache) return launch_dependent(nr::append_kernel<false, true, U>, grid, nr::THREADS, 0, stream, p, cq, ckv);
-    if (p.r.interleaved)
-        return launch_dependent(nr::append_kernel<true, false, U>, grid, nr::THREADS, 0, stream, p, cq, ckv);
-    return launch_dependent(nr::append_kernel<false, false, U>, grid, nr::THREADS, 0, stream, p, cq, ckv);
+    unsigned rows;
+    if (!row_grid(p.total, cq.chunks + 2 * ckv.chunks, &rows)) return cudaErrorInvalidValue;
+    constexpr unsigned per = nr::THREADS * nr::CHECKS;
+    const unsigned grid = rows + (p.cu ? ((unsigned)p.B + per - 1) / per : 0);
+    const auto kernel = p.cache ? (p.r.interleaved ? nr::append_kernel<true, true, U> : nr::append_kernel<false, true, U>)
+                                : (p.r.interleaved ? nr::append_kernel<true, false, U> : nr::append_kernel<false, false, U>);
+    return launch_dependent(kernel, grid, nr::THREADS, 0, stream, p, cq, ckv, rows);
 }
 
 }  // namespace

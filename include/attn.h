@@ -433,10 +433,11 @@ attn_status_t attn_qk_norm_rope(const void *q, const void *k, void *q_out, void 
  * Rows of no sequence are neither read into the cache nor written to q_out, nor,
  * without cu_seqlens, are rows whose seqlens_k is 0 (idle rows of a batch of
  * fixed size, whose attention is 0).
- * Offsets out of order or range, a length below the sequence's new tokens or
- * past the table, and a page outside [0, num_pages) are recorded as
- * ATTN_ERR_DEVICE_BOUNDS; the tokens they concern are skipped (a bad page: only
- * their keys and values).  No two tokens of a call may share a slot.  Other
+ * Offsets out of order or range (all are looked over), a length below the new
+ * tokens of a sequence that has some or past the table, and a page outside
+ * [0, num_pages) are recorded as ATTN_ERR_DEVICE_BOUNDS; the tokens they concern
+ * are skipped (a bad page: only their keys and values; offsets out of order: a row
+ * of two sequences goes to one of them).  No two tokens of a call may share a slot.  Other
  * arguments as in attn_qk_norm_rope.
  */
 attn_status_t attn_append_paged(const void *q, const void *k, const void *v, void *q_out,
@@ -496,8 +497,8 @@ attn_status_t attn_append_paged_q4(const void *q, const void *k, const void *v, 
  * rows from cu_seqlens_k[b] on (DEVICE int32 [B+1]; cu_seqlens_k[b+1] -
  * cu_seqlens_k[b] must equal seqlens[b]), each element z + s (n - 7.5) rounded
  * to bf16 once: the k and v of attn_fwd_varlen.  Rows of no sequence are not
- * written.  Offsets or lengths out of range are recorded as
- * ATTN_ERR_DEVICE_BOUNDS and their sequence skipped; a page outside
+ * written.  Offsets or lengths out of order or range (all are looked over) are
+ * recorded as ATTN_ERR_DEVICE_BOUNDS and their sequence skipped; a page outside
  * [0, num_pages) is recorded too and reads as zeros.
  */
 attn_status_t attn_gather_paged_q4(const void *cache, const int32_t *block_table, const int32_t *seqlens,
