@@ -4,8 +4,11 @@ microseconds.
 
 Argument marshalling only: every step of the computation runs in the CUDA
 library.  PyTorch owns the device memory and the stream; tensors are passed by
-``data_ptr()`` and the current stream by handle.  If a compiled library is
-missing this module raises immediately -- there is no fallback path.
+``data_ptr()`` and the current stream by handle.  If the library is missing
+this module raises immediately -- there is no fallback path.  _quick.so is bound
+to the torch that it was built against; where it is missing or was built for
+another one, load() says so and its operators take the way through ctypes, a few
+microseconds a call longer.
 """
 from __future__ import annotations
 
@@ -15,12 +18,12 @@ import importlib
 import math
 import os
 import threading
+import warnings
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIBRARY_PATH = os.path.join(_PKG, "libattn.so")
-QUICK_PATH = os.path.join(_PKG, "_quick.so")
 
 ATTN_OK = 0
 STATUS_NAMES = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_CUDA",
@@ -44,18 +47,41 @@ class AttnError(RuntimeError):
         super().__init__(f"{what}: {STATUS_NAMES.get(code, code)}")
 
 
+class _NoQuick:
+    """In the place of _quick where it cannot be used: every call goes the long way."""
+    qk_norm_rope = append = gather = decode = fwd = staticmethod(lambda *args: None)
+
+
+def _load_quick():
+    """_quick, or (with a warning) what stands in for it."""
+    from . import build
+    built, here = build.built_abi(), build.abi_tag()
+    if not os.path.exists(build.QUICK) or built is None:
+        why = "is missing"
+    elif built != here:
+        why = f"was built for {built}; this is {here}"
+    else:
+        try:
+            return importlib.import_module("._quick", __package__)
+        except ImportError as e:
+            why = f"cannot be imported ({e})"
+    warnings.warn(f"{build.QUICK} {why}: the operators around the paged cache are called through ctypes, which takes "
+                  "about 10 us more a call (python -c 'import __graft_entry__ as g; g.build()' builds it)",
+                  RuntimeWarning, stacklevel=3)
+    return _NoQuick()
+
+
 def load():
     """Load libattn.so (raises if it has not been built)."""
     global _lib, _quick
     with _lock:
         if _lib is None:
-            for path in (LIBRARY_PATH, QUICK_PATH):
-                if not os.path.exists(path):
-                    raise RuntimeError(
-                        f"{path} is missing: build the CUDA library first "
-                        "(python -c 'import __graft_entry__ as g; g.build()')")
+            if not os.path.exists(LIBRARY_PATH):
+                raise RuntimeError(
+                    f"{LIBRARY_PATH} is missing: build the CUDA library first "
+                    "(python -c 'import __graft_entry__ as g; g.build()')")
             lib = ctypes.CDLL(LIBRARY_PATH)
-            _quick = importlib.import_module("._quick", __package__)
+            _quick = _load_quick()
             fwd_args = [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p]
             lib.attn_fwd.argtypes = fwd_args
             lib.attn_fwd_simple.argtypes = fwd_args

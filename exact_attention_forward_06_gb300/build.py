@@ -4,7 +4,8 @@ the installed torch.
 
 Each translation unit is compiled in parallel into ``_build/`` and linked into
 ``exact_attention_forward_06_gb300/``.  Rebuilds only when a source or header is
-newer than the libraries.  Usable as a script:
+newer than the libraries, or when _quick.so was built against another torch or
+Python (_quick.abi says which).  Usable as a script:
 ``python -m exact_attention_forward_06_gb300.build [--force] [--verbose]``.
 """
 from __future__ import annotations
@@ -24,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libattn.so")
 QUICK = os.path.join(PKG, "_quick.so")
+QUICK_ABI = os.path.join(PKG, "_quick.abi")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -41,8 +43,24 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def abi_tag() -> str:
+    """What _quick.so, unlike libattn.so, is bound to: the installed torch's C++ interface and the Python it runs in."""
+    import torch
+    return (f"torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"{sysconfig.get_config_var('SOABI')}")
+
+
+def built_abi():
+    """abi_tag() of the torch and Python that _quick.so was built against; None if it was not built."""
+    try:
+        with open(QUICK_ABI) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def _stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(QUICK)):
+    if not (os.path.exists(LIB) and os.path.exists(QUICK)) or built_abi() != abi_tag():
         return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(QUICK))
     deps = sources() + [os.path.join(CSRC, "binding.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
@@ -102,7 +120,11 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     tmp = QUICK + f".tmp{os.getpid()}"
     _run(["g++", "-shared", "-o", tmp] + binding.result() + ["-L", PKG, "-l:libattn.so", "-Wl,-rpath,$ORIGIN"],
          "link of the binding", verbose)
+    if os.path.exists(QUICK_ABI):
+        os.remove(QUICK_ABI)
     os.replace(tmp, QUICK)
+    with open(QUICK_ABI, "w") as f:
+        f.write(abi_tag())
     return LIB
 
 
