@@ -93,10 +93,7 @@ attn_status_t append_impl(const void *q, const void *k, const void *v, void *q_o
     p.q_stride = (int64_t)q_stride;
     p.k_stride = (int64_t)k_stride;
     p.v_stride = (int64_t)v_stride;
-    // The grid (one block per 16 tokens and head row at the finest) must fit.
-    if ((int64_t)p.Hq + 2 * (int64_t)Hkv > 65536 ||
-        (((int64_t)total + 15) / 16) * ((int64_t)p.Hq + 2 * (int64_t)Hkv) > 0x7fffffff)
-        return ATTN_ERR_INVALID_ARG;
+    if (!attn::append_fits(p)) return ATTN_ERR_INVALID_ARG;
     int sms;
     uint64_t budget;
     if ((st = attn::device_state(&sms, &p.r.status, &budget)) != ATTN_OK) return st;
@@ -142,9 +139,7 @@ attn_status_t attn_qk_norm_rope(const void *q, const void *k, void *q_out, void 
     };
     if (q_out == q && !dense(Hq, q_stride_b, q_stride_s, q_stride_h)) return ATTN_ERR_INVALID_ARG;
     if (k && k_out == k && !dense(Hkv, k_stride_b, k_stride_s, k_stride_h)) return ATTN_ERR_INVALID_ARG;
-    if ((int64_t)Hq + p.Hkv > 65536 ||
-        (((int64_t)B * S + 15) / 16) * ((int64_t)Hq + p.Hkv) > 0x7fffffff)
-        return ATTN_ERR_INVALID_ARG;
+    if (!attn::norm_rope_fits(p)) return ATTN_ERR_INVALID_ARG;
     p.q_stride[0] = (int64_t)q_stride_b;
     p.q_stride[1] = (int64_t)q_stride_s;
     p.q_stride[2] = (int64_t)q_stride_h;

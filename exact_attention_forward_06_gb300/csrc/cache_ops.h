@@ -92,6 +92,9 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Whether a launch's grid fits (the launches count on it).
+bool norm_rope_fits(const NormRopeParams &p);
+bool append_fits(const AppendParams &p);
 cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_gather_q4(const GatherQ4Params &p, cudaStream_t stream);

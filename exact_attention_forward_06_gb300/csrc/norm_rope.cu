@@ -270,19 +270,19 @@ nr::Chunks chunks_of(int H, int U) {
     return {chunks ? (H + chunks - 1) / chunks : 0, chunks};
 }
 
-// Token blocks x chunks; false when the grid does not fit.
-bool row_grid(int64_t tokens, int chunks, unsigned *grid) {
-    const int64_t n = (tokens + nr::HALVES - 1) / nr::HALVES * chunks;
-    if (n > 0x7fffffff) return false;
-    *grid = (unsigned)n;
-    return true;
+// Token blocks x chunks.
+int64_t row_blocks(int64_t tokens, int64_t chunks) { return (tokens + nr::HALVES - 1) / nr::HALVES * chunks; }
+
+// Blocks that look the offsets over.
+int64_t check_blocks(const AppendParams &p) {
+    constexpr int64_t per = nr::THREADS * nr::CHECKS;
+    return p.cu ? (p.B + per - 1) / per : 0;
 }
 
 template <int U>
 cudaError_t norm_rope_u(const NormRopeParams &p, cudaStream_t stream) {
     const nr::Chunks cq = chunks_of(p.Hq, U), ck = chunks_of(p.Hkv, U);
-    unsigned grid;
-    if (!row_grid((int64_t)p.B * p.S, cq.chunks + ck.chunks, &grid)) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)row_blocks((int64_t)p.B * p.S, cq.chunks + ck.chunks);
     if (p.r.interleaved) return launch_dependent(nr::norm_rope_kernel<true, U>, grid, nr::THREADS, 0, stream, p, cq, ck);
     return launch_dependent(nr::norm_rope_kernel<false, U>, grid, nr::THREADS, 0, stream, p, cq, ck);
 }
@@ -290,10 +290,8 @@ cudaError_t norm_rope_u(const NormRopeParams &p, cudaStream_t stream) {
 template <int U>
 cudaError_t append_u(const AppendParams &p, cudaStream_t stream) {
     const nr::Chunks cq = chunks_of(p.Hq, U), ckv = chunks_of(p.Hkv, U);
-    unsigned rows;
-    if (!row_grid(p.total, cq.chunks + 2 * ckv.chunks, &rows)) return cudaErrorInvalidValue;
-    constexpr unsigned per = nr::THREADS * nr::CHECKS;
-    const unsigned grid = rows + (p.cu ? ((unsigned)p.B + per - 1) / per : 0);
+    const unsigned rows = (unsigned)row_blocks(p.total, cq.chunks + 2 * ckv.chunks);
+    const unsigned grid = rows + (unsigned)check_blocks(p);
     const auto kernel = p.cache ? (p.r.interleaved ? nr::append_kernel<true, true, U> : nr::append_kernel<false, true, U>)
                                 : (p.r.interleaved ? nr::append_kernel<true, false, U> : nr::append_kernel<false, false, U>);
     return launch_dependent(kernel, grid, nr::THREADS, 0, stream, p, cq, ckv, rows);
@@ -316,6 +314,21 @@ static int rows_per_chunk(int Hq, int Hkv, int kv_tensors) {
         }
     }
     return best;
+}
+
+// The most heads that a token has; chunk counts are then far from overflowing.
+constexpr int64_t MAX_HEADS = 65536;
+
+bool norm_rope_fits(const NormRopeParams &p) {
+    if ((int64_t)p.Hq + p.Hkv > MAX_HEADS) return false;
+    const int U = rows_per_chunk(p.Hq, p.Hkv, 1);
+    return row_blocks((int64_t)p.B * p.S, chunks_of(p.Hq, U).chunks + chunks_of(p.Hkv, U).chunks) <= 0x7fffffff;
+}
+
+bool append_fits(const AppendParams &p) {
+    if (p.Hq + 2 * (int64_t)p.Hkv > MAX_HEADS) return false;
+    const int U = rows_per_chunk(p.Hq, p.Hkv, 2);
+    return row_blocks(p.total, chunks_of(p.Hq, U).chunks + 2 * chunks_of(p.Hkv, U).chunks) + check_blocks(p) <= 0x7fffffff;
 }
 
 cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream) {
