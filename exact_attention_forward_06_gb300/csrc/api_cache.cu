@@ -211,6 +211,8 @@ attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32
     attn_status_t st = attn::check_decode_args(q, cache, cache, block_table, seqlens, out, lse, B, Hq, Hkv, d,
                                                page_size, num_pages, max_blocks_per_seq, scale);
     if (st != ATTN_OK) return st;
+    // The kernel's factor scale * log2 e * 2^33 (queries below 2^27) has to stay finite.
+    if (!(scale < 0x1p94f)) return ATTN_ERR_INVALID_ARG;
     // Key positions, rows and the sum of all sequences' page pairs are 32-bit.
     if ((int64_t)max_blocks_per_seq * 16 > 0x7fffffff - 64 || (int64_t)B * Hq > 0x7fffffff ||
         (int64_t)B * (((int64_t)max_blocks_per_seq + 1) / 2) > 0x7fffffff)

@@ -523,8 +523,9 @@ size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int d, int max_blo
  * at the same time, captured ones too, need one each).  Slots past a
  * sequence's end may hold anything.  Deterministic: the same call gives the same
  * bits.  (Where a sequence is cut goes by the lengths of the whole batch, so the
- * order of its sums, and with it the last bit, does too.)  Queries must be below
- * 2^120 in size (a larger one makes its head NaN).
+ * order of its sums, and with it the last bit, does too.)  Queries, and
+ * their products with scale, must be below 2^120 in size (larger ones make their
+ * head NaN), and scale below 2^94 (else ATTN_ERR_INVALID_ARG).
  */
 attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32_t *block_table,
                                    const int32_t *seqlens, void *out, float *lse,
