@@ -477,9 +477,8 @@ _PI = fractions.Fraction("3.1415926535897932384626433832795028841971693993751058
 
 # The operators below run in a few microseconds on small calls, less than Python
 # takes to look at their tensors.  So a call first goes to _quick (csrc/binding.cpp),
-# which checks, makes the outputs and launches, and which returns None, having
-# launched nothing, when anything is not plainly in order.  Then, and on a stream of
-# the caller's, the function's own body runs: it checks one thing after the other and
+# which checks, makes the outputs and launches, and which returns None when anything
+# is not plainly in order, or a launch failed.  Then, and on a stream of the caller's, the function's own body runs: it checks one thing after the other and
 # says what is wrong.  _in gives a tensor's address, and anything out of order
 # goes to _refuse.
 _raw_stream = torch._C._cuda_getCurrentRawStream

@@ -6,8 +6,9 @@
 // attributes read one by one from Python, with thirty arguments through ctypes, took
 // 13 us a call.  Anything that is not plainly in order (a wrong type, shape,
 // device or layout, a length to be read from the device, a status that is not 0)
-// returns None, nothing having been launched: the caller then goes the long way,
-// which says what is wrong.
+// returns None: the caller then goes the long way, which says what is wrong.  Nothing
+// has been launched then, but where a launch failed: the first of a call's two may
+// have run, and runs again (it writes outputs and workspace only).
 #include <Python.h>
 
 #include <algorithm>

@@ -18,7 +18,7 @@ __device__ __forceinline__ float bf16_at(const uint8_t *p) {
 
 // A word's eight values, rounded to bf16.  A code in bits 1..4 of a float whose other
 // bits are those of 2^22 is 2^22 + n; the offset comes off exactly, s (n - 7.5) is exact
-// in fp32 (8 + 5 bits), and the sum rounds once.
+// in fp32 (8 + 5 bits), and the sum rounds to fp32 and then to bf16.
 __device__ __forceinline__ uint4 unpack_word(uint32_t word, float s, float z) {
     uint32_t r[4];
     const float2 s2 = make_float2(s, s), z2 = make_float2(z, z), off = make_float2(-4194311.5f, -4194311.5f);

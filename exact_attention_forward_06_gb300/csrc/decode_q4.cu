@@ -39,18 +39,21 @@
 // In a segment each warp streams page pairs w, w + 4, .. through a ring of its own
 // (bulk copies issued by one of its lanes as soon as a slot has been read): no producer
 // warp and no barrier between warps until the four partial results meet at the
-// segment's end.  Scores, sums and outputs are fp32.  P' is rounded to f16 (2^-12 of
+// segment's end.  Scores, sums and outputs are fp32.  P' is rounded to f16 (2^-11 of
 // itself at most), P to bf16 for the centers; the row sum adds the fp32 values.
 // With P' in bf16, as the bf16 decode's P, the output's error against 64 bits was
 // 2.4e-3 (its own rounding alone makes 1.7e-3) instead of 1.8e-3, in 0.97 of the time.
 //
-// Measured on 64 sequences of 0 to 16384 tokens, 64 / 8 heads (758 MB): 147 us,
+// Measured on 64 sequences of 0 to 16384 tokens, 64 / 8 heads (758 MB): 146.4 us,
 // 5.2 TB/s, 0.76 of the copy bandwidth; the copies alone take 120 us, the arithmetic
-// alone 139.  On 32 sequences of 1024 to 8192 tokens, 32 / 8 heads (177 MB): 45.2 us,
-// 0.58; half the MMA columns are empty there.  3 sequences of about 100 thousand tokens,
-// 32 / 1 heads (55 MB): 39 us, the unpacking of two tiles' pages twice (with one tile
-// a CTA, four times: 5 us more).  With codes as 16 + n and n - 7.5, each by a shift and
-// an and/or (and an addition), these took 167, 50 and 49 us.
+// alone 139.  On 32 sequences of 1024 to 8192 tokens, 32 / 8 heads (177 MB): 45.1 us,
+// 0.58.  There the starts and ends of segments cost: a share's 76 pairs lie in two
+// segments or three.  As many pairs with one run to a share (57 sequences of 2424) take
+// 37.0 us on the GPU against 44.1, as long with 8 heads to a KV head as with 4; 2 us are
+// the merge.  3 sequences of about 100 thousand tokens, 32 / 1 heads (55 MB): 38.7 us,
+// the unpacking of two tiles' pages twice (with one tile a CTA, four times: 5 us more).
+// With codes as 16 + n and n - 7.5, each by a shift and an and/or (and an addition),
+// these took 167, 50 and 49 us.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -945,7 +948,7 @@ __global__ void __launch_bounds__(NT, Shape<TILES>::CTAS_PER_SM)
 // Merge of the cut runs.  A run of few parts is merged by the CTA of the share in which
 // it begins, a warp a head; the heads of a longer one go to the CTAs of its shares in
 // turn, each head to eight warps that take every eighth part.  Four channels a lane; the
-// order is fixed.  It adds 2 to 4 us to the share kernel; with a CTA for each head of
+// order is fixed.  It adds 2 to 5 us to the share kernel; with a CTA for each head of
 // each run, 3 to 9 (3 sequences of 100 thousand tokens: 41.1 us in all against 44.8).
 constexpr int MERGE_WARPS = 8;
 constexpr int SHORT_RUN = 8;

@@ -384,7 +384,8 @@ typedef struct {
  *     (y_a, y_b) -> (y_a cos t - y_b sin t, y_a sin t + y_b cos t),
  *                   t = position[axis_i] * frequency_i, for each pair i
  *
- * computed in fp32 and rounded to bf16 once (to nearest even).  Pair i of
+ * computed in fp32 (a mean of squares above its range counts as infinite) and
+ * rounded to bf16 once (to nearest even).  Pair i of
  * rotary_dim / 2 is channels (i, i + rotary_dim / 2), or (2i, 2i + 1) with
  * interleaved != 0; channels from rotary_dim on are not rotated.
  *
@@ -496,7 +497,7 @@ attn_status_t attn_append_paged_q4(const void *q, const void *k, const void *v, 
  * k_out, v_out: bf16 [total_k][Hkv][d]; sequence b's seqlens[b] tokens go to the
  * rows from cu_seqlens_k[b] on (DEVICE int32 [B+1]; cu_seqlens_k[b+1] -
  * cu_seqlens_k[b] must equal seqlens[b]), each element z + s (n - 7.5) rounded
- * to bf16 once: the k and v of attn_fwd_varlen.  Rows of no sequence are not
+ * to fp32 and then to bf16: the k and v of attn_fwd_varlen.  Rows of no sequence are not
  * written.  Offsets or lengths out of order or range (all are looked over) are
  * recorded as ATTN_ERR_DEVICE_BOUNDS and their sequence skipped; a page outside
  * [0, num_pages) is recorded too and reads as zeros.
@@ -536,8 +537,9 @@ attn_status_t attn_decode_paged_q4(const void *q, const void *cache, const int32
 /*
  * attn_fwd_paged_q4 -- attn_fwd_paged over a cache held in 4 bits (chunked
  * prefill): the caches are read back once into the workspace as bf16 (the
- * values of attn_gather_paged_q4: z + s (n - 7.5) rounded once) and the packed
- * prefill runs over them, so that no row block pays for the unpacking again.
+ * values of attn_gather_paged_q4) and the packed prefill runs over them, so that
+ * no row block pays for the unpacking again.  That copy takes 512 bytes a key and
+ * KV head, 3.2 times what the cache holds for them.
  * max_total_k: an upper bound, known on the host, of the sum of seqlens_k (the
  *      sum itself is best).  A sequence whose length lies outside
  *      [0, 16 * max_blocks_per_seq] or goes past the bound counts as empty (its

@@ -8,7 +8,7 @@ MOST = 2**31 - 1
 
 
 @pytest.mark.parametrize("q4", [False, True])
-@pytest.mark.parametrize("Hq,Hkv", [(64, 8), (512, 1), (65536, 1)])   # 10, 66 and 8194 chunks of rows to eight tokens
+@pytest.mark.parametrize("Hq,Hkv", [(64, 8), (512, 1), (65536, 1)])   # at least 9 blocks to eight tokens
 def test_append_refuses_a_grid_that_does_not_fit(lib, q4, Hq, Hkv):  # noqa: F811
     assert _append(lib, q4, total=MOST, Hq=Hq, Hkv=Hkv, qs=Hq * 128, ks=Hkv * 128, vs=Hkv * 128) == 1
 
