@@ -56,8 +56,8 @@ __device__ __forceinline__ GroupScale group_scale(float hi, float lo) {
 // exact remainder d - q s (one fused operation), q + remainder * r is the
 // correctly rounded quotient (s has eight significant bits, so the theorem's
 // exception, a divisor of all ones, does not arise).  There the definition's clamp
-// has nothing to do either: s is within 2^-9 of (largest |x - z|) * 2 / 15, so the
-// sum lies within 0.02 of 0 .. 15.
+// has nothing to do either: s is within 2^-8 of (largest |x - z|) * 2 / 15, so the
+// sum lies within 0.03 of 0 .. 15.
 __device__ __forceinline__ uint32_t code_word(const float (&x)[8], GroupScale gs) {
     const float z = __uint_as_float((uint32_t)gs.z << 16), s = __uint_as_float((uint32_t)gs.s << 16);
     if (!(s > 0.f)) return 0;
