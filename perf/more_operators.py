@@ -46,7 +46,7 @@ def listed():
         # A full serving batch with trees of 64 tokens.
         dict(name="tree_32seq_64", op="tree", B=32, Hq=32, Hkv=8, n_lo=64, n_hi=64, chain=False, ctx_lo=960,
              ctx_hi=8128, mix=15),
-        # The same without drawing: one sequence's five tokens against the largest logit of each row. Latency.
+        # One sequence's five tokens against the largest logit of each row, nothing drawn: latency.
         dict(name="verify_1x5_greedy", op="verify", B=1, V=32768, n_lo=5, n_hi=5, chain=True, kind="greedy",
              dtype="bf16", mix=16),
         # An odd vocabulary in 32 bits, trees whose siblings are drawn from the draft's distribution one after the other.
@@ -222,7 +222,7 @@ def prepare(case, seed):
     s["q"] = randn(T, case["Hq"], D).bfloat16()
     if own:
         import exact_attention_forward_06_gb300 as A
-        need = A.fwd_tree_paged_workspace_bytes(case["Hq"], Hkv, D, N)
+        need = A.fwd_tree_paged_workspace_bytes(B, case["Hq"], Hkv, D, N)
         s["workspace"] = torch.empty(max(1, need), dtype=torch.uint8, device=device)
     return s
 
