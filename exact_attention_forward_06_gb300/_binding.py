@@ -125,6 +125,9 @@ def load():
             lib.attn_fwd_paged_q4_workspace_bytes.argtypes = [_i] * 4
             lib.attn_fwd_paged_q4_workspace_bytes.restype = _sz
             lib.attn_fwd_paged_q4.argtypes = [_p] * 7 + [_i] * 11 + [_f, _i, _p, _sz, _p]
+            lib.attn_fwd_tree_paged_workspace_bytes.argtypes = [_i] * 5
+            lib.attn_fwd_tree_paged_workspace_bytes.restype = _sz
+            lib.attn_fwd_tree_paged.argtypes = [_p] * 9 + [_i] * 9 + [_f, _i, _p, _sz, _p]
             lib.attn_status_string.argtypes = [_i]
             lib.attn_status_string.restype = ctypes.c_char_p
             lib.attn_version.restype = _i
@@ -133,7 +136,8 @@ def load():
                          "attn_lse_merge",
                          "attn_get_device_status", "attn_set_wait_budget_ns", "attn_debug_inject",
                          "attn_selftest_umma", "attn_qk_norm_rope", "attn_append_paged", "attn_append_paged_q4",
-                         "attn_gather_paged_q4", "attn_decode_paged_q4", "attn_fwd_paged_q4"):
+                         "attn_gather_paged_q4", "attn_decode_paged_q4", "attn_fwd_paged_q4",
+                         "attn_fwd_tree_paged"):
                 getattr(lib, name).restype = _i
             _lib = lib
     return _lib
@@ -894,6 +898,58 @@ def fwd_paged_q4(q, cache, block_table, seqlens_k, cu_seqlens_q, *, max_seqlen_q
                                _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "attn_fwd_paged_q4")
+    return out, lse
+
+
+TREE_MAX = 256  # tokens of a sequence's tree (ATTN_TREE_MAX)
+
+
+def fwd_tree_paged_workspace_bytes(B: int, Hq: int, Hkv: int, d: int, max_seqlen_q: int) -> int:
+    """Device workspace bytes fwd_tree_paged needs for this shape."""
+    return int(load().attn_fwd_tree_paged_workspace_bytes(B, Hq, Hkv, d, max_seqlen_q))
+
+
+def fwd_tree_paged(q, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, parents, *, max_seqlen_q=None, scale=None,
+                   out=None, lse=None, workspace=None, stream=None, rounding="rtne"):
+    """Attention of trees of drafted tokens against a paged KV cache (the tensors of fwd_paged; a sequence's tree is the
+    last tokens of its cache).
+
+    parents [total_q] int32: each token's parent by its place in its own sequence's tree, before its own, or -1.  A token
+    sees the keys before the tree, itself and its ancestors.  A tree has at most TREE_MAX tokens; max_seqlen_q, when
+    omitted, is read from the offsets (a synchronisation).  Returns (out [total_q, Hq, 128] bf16, lse [Hq, total_q]).
+    """
+    lib = _lib or load()
+    if rounding not in ROUNDING:
+        raise ValueError(f"rounding must be one of {sorted(ROUNDING)}, got {rounding!r}")
+    dev = _current()
+    qp, kp, vp = _in(q, "q", _bf16, dev), _in(k_pages, "k_pages", _bf16, dev), _in(v_pages, "v_pages", _bf16, dev)
+    table, lens = _in(block_table, "block_table", _i32, dev), _in(seqlens_k, "seqlens_k", _i32, dev)
+    cu, par = _in(cu_seqlens_q, "cu_seqlens_q", _i32, dev), _in(parents, "parents", _i32, dev)
+    shape, pool, table_shape = q.shape, k_pages.shape, block_table.shape
+    B = seqlens_k.numel()
+    if len(shape) != 3 or len(pool) != 4 or v_pages.shape != pool or pool[3] != shape[2]:
+        raise ValueError("q must be [total_q, Hq, 128] and the pools [num_pages, 16, Hkv, 128]")
+    total_q, Hq, d = shape
+    num_pages, page_size, Hkv, _ = pool
+    if cu_seqlens_q.numel() != B + 1 or len(table_shape) != 2 or table_shape[0] != B:
+        raise ValueError("cu_seqlens_q must have B + 1 entries and block_table B rows")
+    if parents.numel() != total_q:
+        raise ValueError("parents must have one entry per row of q")
+    if max_seqlen_q is None:
+        max_seqlen_q = max(1, int(torch.diff(cu_seqlens_q).max()))
+    out, lse, op, lp = _attn_out(out, lse, shape, (Hq, total_q), q.device, stream, dev)
+    if workspace is None:
+        need = lib.attn_fwd_tree_paged_workspace_bytes(B, Hq, Hkv, d, max_seqlen_q)
+        workspace = _empty(max(need, 1), torch.uint8, q.device, stream)
+        wp = workspace.data_ptr()
+    else:
+        wp = _in(workspace, "workspace", torch.uint8, dev)
+    rc = lib.attn_fwd_tree_paged(qp, kp, vp, table, lens, cu, par, op, lp, B, Hq, Hkv, total_q, max_seqlen_q, d,
+                                 page_size, num_pages, table_shape[1], 1.0 / math.sqrt(d) if scale is None else scale,
+                                 ROUNDING[rounding], wp, workspace.numel(),
+                                 _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "attn_fwd_tree_paged")
     return out, lse
 
 

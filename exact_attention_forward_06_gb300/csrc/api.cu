@@ -221,6 +221,10 @@ attn_status_t fill_prefill_params(attn::PrefillParams *p, const DeviceInfo *di, 
     p->seqlens_k = nullptr;
     p->max_blocks = 0;
     p->num_pages = 0;
+    p->parents = nullptr;
+    p->q = p->k_pool = p->v_pool = nullptr;
+    p->part_rows = 0;
+    p->first = nullptr;
     return ATTN_OK;
 }
 
@@ -386,6 +390,91 @@ attn_status_t attn_fwd_paged(const void *q, const void *k_pages, const void *v_p
                              static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return ATTN_ERR_CUDA;
     return ATTN_OK;
+}
+
+// Sizes of a tree launch's workspace: where each sequence begins, partial outputs, their log-sum-exps.
+static void tree_workspace(int B, int G, int max_seqlen_q, size_t *first, size_t *o, size_t *l) {
+    const size_t rows = (size_t)attn::kTreeMaxCtas * 2 * attn::tree_part_rows(G, max_seqlen_q);
+    const auto align256 = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    *first = align256(((size_t)B + 1) * 4);
+    *o = align256(rows * 128 * 4);
+    *l = align256(rows * 4);
+}
+
+size_t attn_fwd_tree_paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_seqlen_q) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > 128 || d != 128 || max_seqlen_q < 1 ||
+        max_seqlen_q > ATTN_TREE_MAX)
+        return 0;
+    size_t first, o, l;
+    tree_workspace(B, Hq / Hkv, max_seqlen_q, &first, &o, &l);
+    return first + o + l;
+}
+
+attn_status_t attn_fwd_tree_paged(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
+                                  const int32_t *seqlens_k, const int32_t *cu_seqlens_q, const int32_t *parents,
+                                  void *out, float *lse, int B, int Hq, int Hkv, int total_q, int max_seqlen_q, int d,
+                                  int page_size, int num_pages, int max_blocks_per_seq, float scale, int round_mode,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    if (!block_table || !seqlens_k || !cu_seqlens_q || !parents) return ATTN_ERR_INVALID_ARG;
+    for (const int32_t *x : {block_table, seqlens_k, cu_seqlens_q, parents})
+        if (reinterpret_cast<uintptr_t>(x) & 3u) return ATTN_ERR_INVALID_ARG;
+    if (num_pages < 1 || max_blocks_per_seq < 1 || (int64_t)num_pages * 16 > 0x7fffffff ||
+        (int64_t)max_blocks_per_seq * 16 > 0x7fffffff - 128)
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_fwd_args(q, k_pages, v_pages, out, lse, 1, Hq, Hkv, total_q, num_pages * 16, d,
+                                      ATTN_LAYOUT_BSHD, scale);
+    if (st != ATTN_OK) return st;
+    if (page_size != 16 || Hq / Hkv > 128) return ATTN_ERR_UNSUPPORTED;
+    if (B < 1 || max_seqlen_q < 1 || max_seqlen_q > ATTN_TREE_MAX) return ATTN_ERR_INVALID_ARG;
+    if (!valid_round_mode(round_mode)) return ATTN_ERR_INVALID_ARG;
+    // The line of K/V tiles, and the rows of the merge, are 32-bit.
+    const int pp = attn::tree_tile_positions(Hq / Hkv);
+    const int64_t blocks = (max_seqlen_q + 2 * pp - 1) / (2 * pp), tiles = ((int64_t)max_blocks_per_seq + 7) / 8;
+    const int64_t line = (int64_t)Hkv * blocks * tiles, rows = (int64_t)max_seqlen_q * Hq;
+    if (line > 0x7fffffff / B || rows > 0x7fffffff / B) return ATTN_ERR_INVALID_ARG;
+    const size_t need = attn_fwd_tree_paged_workspace_bytes(B, Hq, Hkv, d, max_seqlen_q);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need)
+        return ATTN_ERR_WORKSPACE;
+    DeviceInfo *di = nullptr;
+    if ((st = device_info(&di)) != ATTN_OK) return st;
+    attn::PrefillParams p;
+    fill_prefill_params(&p, di, lse, B, Hq, Hkv, max_seqlen_q, max_blocks_per_seq * 16, ATTN_LAYOUT_BSHD, 0, scale);
+    p.round_mode = round_mode;
+    p.cu_q = cu_seqlens_q;
+    p.prefetch_ahead = 0;
+    p.pack_heads = 1;
+    p.pack_pos = pp;
+    p.total_q = total_q;
+    p.out = out;
+    p.block_table = block_table;
+    p.seqlens_k = seqlens_k;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_pages = num_pages;
+    p.parents = parents;
+    p.q = q;
+    p.k_pool = k_pages;
+    p.v_pool = v_pages;
+    p.part_rows = attn::tree_part_rows(p.G, max_seqlen_q);
+    size_t first, o, l;
+    tree_workspace(B, p.G, max_seqlen_q, &first, &o, &l);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.first = reinterpret_cast<int *>(ws);
+    p.ws_o = reinterpret_cast<float *>(ws + first);
+    p.ws_lse = reinterpret_cast<float *>(ws + first + o);
+    p.inject = attn::take_inject(1);
+    const int sms = di->sm_count < attn::kTreeMaxCtas ? di->sm_count : attn::kTreeMaxCtas;
+    const int ctas = line * B < sms ? (int)(line * B) : sms;
+    p.n_items = ctas;  // (a CTA's items are its share: nothing is claimed)
+    CUtensorMap mq, mk, mv, mk8, mv8;
+    if (!make_map_4d(&mq, q, false, 1, total_q, Hq, d, pp, p.G) ||
+        !make_map_pool_groups(&mk, k_pages, num_pages, Hkv, d, 2) ||
+        !make_map_pool_groups(&mv, v_pages, num_pages, Hkv, d, 2) ||
+        !make_map_pool_groups(&mk8, k_pages, num_pages, Hkv, d, 16) ||
+        !make_map_pool_groups(&mv8, v_pages, num_pages, Hkv, d, 16))
+        return ATTN_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (attn::launch_prefill(mq, mk, mv, mq, mk8, mv8, p, ctas, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    return attn::launch_tree_merge(p, ctas, s) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 size_t attn_fwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int d, int causal) {

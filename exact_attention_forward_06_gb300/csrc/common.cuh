@@ -44,6 +44,8 @@ enum WaitSite : unsigned {
     kSiteQ4Table = 24,
     kSiteQ4Seqlen = 25,
     kSiteQ4Page = 26,
+    kSiteTreeOffsets = 27,
+    kSiteTreeParent = 28,
 };
 
 // First error wins; the site is informative only.

@@ -95,14 +95,19 @@ constexpr int ITEM_RING = 4;
 constexpr uint32_t ITEM_READERS = 2 + 8;
 // q_full[2], q_free[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[2], s_free[2],
 // p_full[2], o_full[2], fin, item_full[ITEM_RING], item_empty[ITEM_RING],
-// stage_ready[2], stage_taken[2]
+// stage_ready[2], stage_taken[2]; behind them the tensor-memory slot, the abort
+// flag, the item ring, the store commands and (trees) the flags of keys whose
+// values are not finite
 constexpr int NBARS = 2 + 2 + 2 * NSLOT + 2 + 2 + 2 + 2 + 1 + 2 * ITEM_RING + 2 + 2;
 constexpr uint32_t SMEM_MISC = 768;
 constexpr uint32_t SMEM_ALIGN = 1024;
 constexpr float RESCALE_LOG2 = 8.0f;  // move the running max past a 2^8 growth (and see softmax_wg)
 constexpr float LN2 = 0.6931471805599453f;
 
-static_assert(NBARS * 8 + 8 + 64 * ITEM_RING + 2 * 32 <= SMEM_MISC, "barrier area too small");
+// A tree's keys lie in at most three K/V tiles; a flag for each of a tile's 128 keys, per softmax group.
+constexpr int TREE_TILES = (kTreeMaxNodes + BN - 2) / BN + 1;
+static_assert(TREE_TILES == 3, "a tree's keys begin anywhere in their first tile");
+static_assert(NBARS * 8 + 8 + 64 * ITEM_RING + 2 * 32 + 2 * TREE_TILES * 16 <= SMEM_MISC, "barrier area too small");
 
 constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, 128, 0, 0);   // Q K^T: both K-major
 constexpr uint32_t IDESC_PV = ptx::idesc_bf16_f32(128, 128, 0, 1);  // P V: V is N(d)-major
@@ -149,6 +154,10 @@ struct SmemLayout {
     // four coordinates (first 64-column half).
     __device__ volatile int *stage_cmd(int t) const {
         return reinterpret_cast<volatile int *>(bars + NBARS + 1) + 16 * ITEM_RING + 8 * t;
+    }
+    // Keys of tree tile i whose values are not finite, as group t found them (four words).
+    __device__ volatile uint32_t *odd_keys(int t, int i) const {
+        return reinterpret_cast<volatile uint32_t *>(bars + NBARS + 1) + 16 * ITEM_RING + 16 + (t * TREE_TILES + i) * 4;
     }
     __device__ uint8_t *q_tile(int t) const { return base + (t ? SMEM_Q1 : SMEM_Q0); }
     // Ring slot s: a K or V tile, or a tile's output staging area.
@@ -285,7 +294,8 @@ __host__ __device__ __forceinline__ Unit unit_coords(const PrefillParams &p, int
 // part-major within a unit.  kPacked / kPaged: the unit's rows and keys are
 // those of its sequence; offsets that are out of order or out of range, or
 // lengths past the stated maxima, are reported and the unit does nothing.
-enum LaunchKind : int { kDense = 0, kPacked = 1, kPaged = 2 };
+// kTree: a segment of the CTA's share (tree_next).
+enum LaunchKind : int { kDense = 0, kPacked = 1, kPaged = 2, kTree = 3 };
 
 template <int KIND>
 __device__ __forceinline__ Unit decode_unit(const PrefillParams &p, int it) {
@@ -385,6 +395,157 @@ __device__ __forceinline__ Unit next_unit(const PrefillParams &p, bool first) {
     Unit end{};
     end.n_kv = -1;
     return end;
+}
+
+// ---- trees of drafted tokens: equal shares of all K/V tiles
+
+// One sequence's part of the line of K/V tiles: Hkv x row blocks x tiles.
+struct TreeSeq {
+    int q0, Sq, Sk, blocks, tiles, work;
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const PrefillParams &p, int b, bool report) {
+    TreeSeq s;
+    const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], Lk = p.seqlens_k[b];
+    // (an idle row, without tokens, may have any length that its table holds)
+    const bool bad =
+        q0 < 0 || q1 < q0 || q1 > p.total_q || q1 - q0 > p.Sq || Lk < q1 - q0 || Lk > p.max_blocks * 16;
+    if (bad && report) report_status(p.status, kStatusDeviceBounds, kSiteTreeOffsets);
+    s.q0 = bad ? 0 : q0;
+    s.Sq = bad ? 0 : q1 - q0;
+    s.Sk = bad ? 0 : Lk;
+    s.blocks = (s.Sq + 2 * p.pack_pos - 1) / (2 * p.pack_pos);
+    s.tiles = (s.Sk + BN - 1) / BN;
+    s.work = p.Hkv * s.blocks * s.tiles;
+    return s;
+}
+
+// How many CTAs share a line of `total` tiles, and where CTA c's share begins.
+__device__ __forceinline__ int tree_shares(int ctas, int total) { return min(ctas, max(total, 1)); }
+__device__ __forceinline__ int tree_share_begin(int c, int shares, int total) {
+    return (int)((int64_t)c * total / shares);
+}
+// The CTA whose share holds tile x.
+__device__ __forceinline__ int tree_share_of(int x, int shares, int total) {
+    return (int)((((int64_t)x + 1) * shares - 1) / total);
+}
+
+// What is left of a CTA's share: `left` tiles from tile `at` of sequence b on.
+struct TreeShare {
+    int b, at, left;
+    bool begun;  // a segment of it has been handed out
+};
+
+// The whole warp finds its CTA's share; CTA 0 writes where each sequence begins.
+__device__ __forceinline__ TreeShare tree_share(const PrefillParams &p, int lane) {
+    constexpr unsigned ALL = 0xffffffffu;
+    const bool writer = blockIdx.x == 0;
+    int total = 0;
+    for (int b = lane; b < p.B; b += 32) total += tree_seq(p, b, writer).work;
+    total = __reduce_add_sync(ALL, total);
+    const int shares = tree_shares(gridDim.x, total);
+    TreeShare sh{0, 0, 0, false};
+    const bool mine = (int)blockIdx.x < shares && total > 0;
+    const int lo = mine ? tree_share_begin(blockIdx.x, shares, total) : 0;
+    const int hi = mine ? tree_share_begin(blockIdx.x + 1, shares, total) : 0;
+    sh.left = hi - lo;
+    int base = 0;
+    bool found = sh.left == 0;
+    for (int b0 = 0; b0 < p.B && (writer || !found); b0 += 32) {
+        const int work = b0 + lane < p.B ? tree_seq(p, b0 + lane, false).work : 0;
+        int incl = work;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int up = __shfl_up_sync(ALL, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const int begin = base + incl - work;
+        if (writer && b0 + lane < p.B) p.first[b0 + lane] = begin;
+        const unsigned here = __ballot_sync(ALL, !found && begin <= lo && lo < begin + work);
+        if (here) {
+            const int l = __ffs(here) - 1;
+            sh.b = b0 + l;
+            sh.at = lo - __shfl_sync(ALL, begin, l);
+            found = true;
+        }
+        base += __shfl_sync(ALL, incl, 31);
+    }
+    if (writer && lane == 0) p.first[p.B] = total;
+    return sh;
+}
+
+// The next segment of the share (one thread): a run of one unit's K/V tiles.
+__device__ __forceinline__ Unit tree_next(const PrefillParams &p, TreeShare &sh) {
+    Unit w{};
+    w.n_kv = -1;
+    while (sh.left > 0) {
+        const TreeSeq s = tree_seq(p, sh.b, false);
+        if (sh.at >= s.work) {  // (sequences without work among them)
+            sh.at -= s.work;
+            ++sh.b;
+            continue;
+        }
+        const int unit = sh.at / s.tiles;
+        w.b = sh.b;
+        w.g = unit / s.blocks;
+        w.h[0] = w.h[1] = w.g * p.G;
+        w.s0[0] = unit % s.blocks * 2 * p.pack_pos;
+        w.s0[1] = w.s0[0] + p.pack_pos;
+        w.j_lo = sh.at - unit * s.tiles;
+        w.n_kv = min(s.tiles - w.j_lo, sh.left);
+        // A unit that other CTAs share is the first or the last segment of a share.
+        w.part = w.n_kv == s.tiles ? -1 : (sh.begun ? 1 : 0);
+        w.ws_row = ((int)blockIdx.x * 2 + max(w.part, 0)) * p.part_rows;
+        w.Sq = s.Sq;
+        w.Sk = s.Sk;
+        w.q0 = s.q0;
+        sh.begun = true;
+        sh.at += w.n_kv;
+        sh.left -= w.n_kv;
+        break;
+    }
+    return w;
+}
+
+// Which keys of the tile at kbase token `pos` of a tree sees: the keys before
+// the tree, itself and its ancestors.  One step up the tree is one load (from
+// L1 after the first); parents lie before their children, which bounds the walk.
+__device__ __forceinline__ void tree_visible(const PrefillParams &p, const Unit &w, int pos, bool valid, int kbase,
+                                             uint32_t (&vis)[4]) {
+    const int base = w.Sk - w.Sq;
+    const int before = valid ? min(max(base - kbase, 0), BN) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = min(max(before - 32 * i, 0), 32);
+        vis[i] = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+    }
+    for (int a = valid ? pos : -1; a >= 0;) {
+        const int key = base + a - kbase;
+        if (key < 0) break;
+        if (key < BN) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vis[i] |= (key >> 5) == i ? 1u << (key & 31) : 0u;
+        }
+        const int up = p.parents[w.q0 + a];
+        if (up >= a || up < -1) {
+            report_status(p.status, kStatusDeviceBounds, kSiteTreeParent);
+            break;
+        }
+        a = up;
+    }
+}
+
+// The values of key `key` of unit w, or nullptr where its page is not in the pool.
+__device__ __forceinline__ const uint4 *tree_row(const PrefillParams &p, const Unit &w, const void *pool, int key) {
+    const int page = p.block_table[(int64_t)w.b * p.max_blocks + key / 16];
+    if (page < 0 || page >= p.num_pages) return nullptr;
+    return reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pool) +
+                                           (((int64_t)page * 16 + key % 16) * p.Hkv + w.g) * D);
+}
+
+// Whether a packed pair of bf16 has an infinity or NaN.
+__device__ __forceinline__ bool odd_pair(uint32_t x) {
+    return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
 
 // Producer side: put unit w (n_kv = -1: end of the list) into ring entry
@@ -519,6 +680,7 @@ __device__ void producer(const PrefillParams &p, const SmemLayout &sm, const Wai
 // the copy then fills zeros.  When the tile's 8 pages are consecutive in the
 // pool (an engine that hands a sequence pages in order), lane 0 loads the
 // tile with one 128-row box of the run maps mk8/mv8 instead.
+template <int KIND>
 __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, const WaitCtx &wc, int lane,
                                const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mv,
                                const CUtensorMap *mk8, const CUtensorMap *mv8) {
@@ -533,7 +695,10 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
     // the item ring.
     Unit w;
     w.n_kv = -1;
-    if (lane == 0) w = next_unit<kPaged>(p, true);
+    TreeShare share{};
+    if (KIND == kTree) share = tree_share(p, lane);
+    auto next = [&](bool first) { return KIND == kTree ? tree_next(p, share) : next_unit<kPaged>(p, first); };
+    if (lane == 0) w = next(true);
     while (ok) {
         if (lane == 0) ok = publish_unit(sm, wc, u, w);
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
@@ -567,12 +732,17 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
                     ok = false;
                     break;
                 }
-                ptx::mbar_arrive_expect_tx(sm.q_full(t), TILE_BYTES);
-                load_tile(mq, sm.q_tile(t), sm.q_full(t), p.bhsd, t ? w.h[1] : w.h[0],
-                          w.q0 + (t ? w.s0[1] : w.s0[0]), w.tb, pol_q);
+                if (KIND == kTree && t == 1 && w.s0[1] >= w.Sq) {
+                    ptx::mbar_arrive(sm.q_full(t));  // no rows: nothing reads the tile
+                } else {
+                    // (a tree's tile is one box of pack_pos positions x G heads)
+                    ptx::mbar_arrive_expect_tx(sm.q_full(t), KIND == kTree ? p.pack_pos * p.G * D * 2 : TILE_BYTES);
+                    load_tile(mq, sm.q_tile(t), sm.q_full(t), p.bhsd, t ? w.h[1] : w.h[0],
+                              w.q0 + (t ? w.s0[1] : w.s0[0]), w.tb, pol_q);
+                }
                 ++qn[t];
             }
-            if (ok) nx = next_unit<kPaged>(p, false);  // the next unit while this one's Q loads
+            if (ok) nx = next(false);  // the next unit while this one's Q loads
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) {
             ok = false;
@@ -820,6 +990,25 @@ __device__ __forceinline__ float softmax_tile(const float2 (&s)[64], uint32_t (&
     return a.x + a.y;
 }
 
+// The same with a bit for each key that the row sees.
+__device__ __forceinline__ float softmax_tile_bits(const float2 (&s)[64], uint32_t (&pk)[64], float scale_log2,
+                                                   float m_sub, const uint32_t (&vis)[4]) {
+    const float2 c2 = make_float2(scale_log2, scale_log2);
+    const float2 n2 = make_float2(-m_sub, -m_sub);
+    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+        const float2 t = __ffma2_rn(s[i], c2, n2);
+        float2 pp;
+        pp.x = vis[i >> 4] >> (2 * i & 31) & 1u ? ptx::ex2(t.x) : 0.f;
+        pp.y = vis[i >> 4] >> (2 * i + 1 & 31) & 1u ? ptx::ex2(t.y) : 0.f;
+        acc[i & 1] = __fadd2_rn(acc[i & 1], pp);
+        pk[i] = ptx::pack_bf16x2(pp.x, pp.y);
+    }
+    const float2 a = __fadd2_rn(acc[0], acc[1]);
+    return a.x + a.y;
+}
+
 // Output stores of tile t, one lane of an otherwise idle control warp: for
 // each command of softmax group t, the TMA store of the staged tile (both
 // 64-column halves), then, once the store has read the slot, the slot goes
@@ -855,11 +1044,110 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     if (lane == 0) ptx::mbar_arrive(bar);
 }
 
+// The part of an output row that a tree's rows get from keys whose values are not
+// finite (see odd_key in softmax_wg): columns c0 .. c0 + 31 of row `pos` of `head`,
+// added to o.  Rare, so one key after the other in plain arithmetic.
+__device__ __forceinline__ void tree_add_odd(const PrefillParams &p, const SmemLayout &sm, const Unit &w, int t, int pos,
+                                          int head, float m_run, int c0, float (&o)[32]) {
+    const int base = w.Sk - w.Sq;
+    for (int a = pos; a >= 0;) {
+        const int key = base + a, tile = key / BN;
+        if (tile < w.j_lo) break;
+        if (tile < w.j_lo + w.n_kv && sm.odd_keys(t, tile - base / BN)[key % BN / 32] >> (key % 32) & 1u) {
+            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((int64_t)(w.q0 + pos) * p.Hq + head) * D;
+            const auto *k = reinterpret_cast<const __nv_bfloat16 *>(tree_row(p, w, p.k_pool, key));
+            const auto *v = reinterpret_cast<const __nv_bfloat16 *>(tree_row(p, w, p.v_pool, key));
+            float x = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < D; ++c) x = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), x);
+            const float pr = ptx::ex2(x * p.scale_log2 - (m_run == -INFINITY ? 0.f : m_run));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = fmaf(pr, __bfloat162float(v[c0 + c]), o[c]);
+        }
+        const int up = p.parents[w.q0 + a];
+        if (up >= a || up < -1) break;
+        a = up;
+    }
+}
+
+// Epilogue of a tree's tile: whole rows to out and lse, or a share's part of them
+// (normalised, with the log-sum-exp) to the workspace.  A thread holds a row; the
+// warp turns its 32 rows round in its part of the staging slot, 128 bytes a row at
+// a time, so that a store covers whole lines.
+__device__ __forceinline__ void tree_epilogue(const PrefillParams &p, const SmemLayout &sm, const Unit &w, uint32_t tO,
+                                              int t, int quarter, int lane, int pos, int head, bool valid, bool dead,
+                                              bool has_tree, float m_run, float l_run, uint8_t *stage, bool ok) {
+    if (dead) return;  // (the whole warp)
+    const int r = quarter * 32 + lane;
+    bool any_odd = false;
+    if (has_tree) {
+        const int first = (w.Sk - w.Sq) / BN;
+        for (int i = max(first, w.j_lo); i < w.j_lo + w.n_kv; ++i)
+            for (int k = 0; k < 4; ++k) any_odd = any_odd || sm.odd_keys(t, i - first)[k] != 0;
+    }
+    ptx::tc_fence_after();
+    // An empty row (no key of this share) gives zeros; NaN stays NaN.
+    const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
+    const float lse = l_run == 0.f ? -INFINITY : (m_run + ptx::lg2(l_run)) * LN2;
+    const bool part = w.part >= 0;
+    uint8_t *mine = stage + quarter * 32 * 128;  // 32 rows x 128 bytes, 16-byte chunks swizzled by row
+    const unsigned rows = __ballot_sync(0xffffffffu, valid && ok);
+    // bf16: 64 columns a turn; fp32: 32
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+        uint32_t o[32];
+        ptx::tmem_ld32(tO + ch * 32, o);
+        ptx::tmem_wait_ld();
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = l_run == 0.f ? 0.f : __uint_as_float(o[i]);
+        if (any_odd && valid) tree_add_odd(p, sm, w, t, pos, head, m_run, ch * 32, f);
+        if (part) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<float4 *>(mine + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                    make_float4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = pack_bf16x2_mode(f[8 * k + 2 * i] * inv, f[8 * k + 2 * i + 1] * inv, p.round_mode);
+                const int c = (ch & 1) * 4 + k;
+                *reinterpret_cast<uint4 *>(mine + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            if ((ch & 1) == 0) continue;
+        }
+        __syncwarp();
+        // eight lanes a row, four rows at a time
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+            const int row = it * 4 + (lane >> 3), c = lane & 7;
+            const int row_pos = __shfl_sync(0xffffffffu, pos, row), row_head = __shfl_sync(0xffffffffu, head, row);
+            if (!(rows >> row & 1u)) continue;
+            const uint4 x = *reinterpret_cast<const uint4 *>(mine + row * 128 + ((c ^ (row & 7)) << 4));
+            if (part)
+                reinterpret_cast<uint4 *>(p.ws_o + (int64_t)(w.ws_row + t * BM + quarter * 32 + row) * D + ch * 32)[c] = x;
+            else
+                reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                          ((int64_t)(w.q0 + row_pos) * p.Hq + row_head) * D + (ch >> 1) * 64)[c] = x;
+        }
+        __syncwarp();
+    }
+    if (!valid || !ok) return;
+    if (part)
+        p.ws_lse[w.ws_row + t * BM + r] = lse;
+    else if (p.lse != nullptr)
+        p.lse[(int64_t)head * p.total_q + w.q0 + pos] = lse;
+}
+
 template <int KIND>
 __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const WaitCtx &wc, uint32_t tmem_base,
                            int t, int quarter, int lane, const CUtensorMap *mo) {
     constexpr bool PACKED = KIND != kDense;  // per-sequence offsets: packed batches and paged caches
-    constexpr bool PAGED = KIND == kPaged;
+    constexpr bool PAGED = KIND == kPaged || KIND == kTree;
+    constexpr bool TREE = KIND == kTree;
     const int r = quarter * 32 + lane;  // row within the tile == TMEM lane
     const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16);
     const uint32_t tS = lanes + TM_S;     // shared score buffer
@@ -907,9 +1195,65 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
             pos = s0 + (p.bhsd ? r % p.pack_pos : r / p.G);
             head = h0 + hr;
         }
+        if (TREE) {  // row r of a tile: position r / G, head r % G
+            pos = s0 + r / p.G;
+            head = h0 + r % p.G;
+        }
+        const bool valid = TREE && r < p.pack_pos * p.G && pos < w.Sq;
         // A tile wholly past the sequence's end computes nothing (its MMA
-        // stream issues no products either) and stores nothing.
-        const bool dead = s0 >= w.Sq;
+        // stream issues no products either) and stores nothing.  Of a tree's
+        // tile, which is often part full, the same goes for a warp's 32 rows.
+        const bool dead = TREE ? !__any_sync(0xffffffffu, valid) : s0 >= w.Sq;
+        const bool dead_tile = s0 >= w.Sq;
+        const int tree0 = w.Sk - w.Sq;  // the tree's first key
+        const bool has_tree = TREE && !dead_tile && (w.j_lo + w.n_kv) * BN > tree0;
+        // Last tile of a packed or paged sequence: the V rows past its end hold
+        // other data (the next sequence's rows, or whatever a page's unused slots
+        // contain).  Their P is 0, but 0 * NaN is NaN, so each group zeroes those
+        // rows in shared memory once the tile has landed, before releasing its P
+        // (the two streams' P V products are not ordered; both groups write the
+        // same zeros).  `also`: this thread's row is zeroed wherever it lies.
+        auto blank_rows = [&](int j, bool also) -> bool {
+            const int item = nb + 2 * j + 1;
+            uint8_t *vt = sm.slot(item % NSLOT);
+            if (!wait_bounded(sm.kv_full(item % NSLOT), (uint32_t)((item / NSLOT) & 1), wc, kSiteSoftmaxV))
+                return false;
+            if ((w.j_lo + j) * BN + r >= w.Sk || also) {
+                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                // row r, both halves (dense or paged tile layout)
+                uint8_t *h0 = PAGED ? vt + (r >> 3) * PG_GROUP_BYTES + (r & 7) * 128 : vt + r * 128;
+                uint8_t *h1 = h0 + (PAGED ? PG_HALF_BYTES : HALF_BYTES);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    reinterpret_cast<uint4 *>(h0)[c] = z;
+                    reinterpret_cast<uint4 *>(h1)[c] = z;
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            return true;
+        };
+        // A key of the tree is hidden from some rows and seen by others.  If its
+        // values are not all finite, 0 times them would be NaN in the rows that do
+        // not see it: such a key's values are taken out of the tile (blank_rows)
+        // and added in the epilogue to the rows that do see it.  Thread r looks
+        // the tile's key r over.
+        auto odd_key = [&](int j) -> bool {
+            const int kbase = (w.j_lo + j) * BN, key = kbase + r;
+            uint32_t odd = 0;
+            if (key >= tree0 && key < w.Sk) {
+                const uint4 *v = tree_row(p, w, p.v_pool, key);
+                if (v != nullptr) {
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 x = v[i];
+                        odd |= odd_pair(x.x) | odd_pair(x.y) | odd_pair(x.z) | odd_pair(x.w);
+                    }
+                }
+            }
+            const uint32_t all = __ballot_sync(0xffffffffu, odd != 0);
+            if (lane == 0) sm.odd_keys(t, kbase / BN - tree0 / BN)[quarter] = all;
+            return odd != 0;
+        };
         const int lim_row = p.causal ? min(pos + w.Sk - w.Sq, w.Sk - 1) : w.Sk - 1;
         // the tile's first position is its smallest
         const int lim_tile = p.causal ? min(s0 + w.Sk - w.Sq, w.Sk - 1) : w.Sk - 1;
@@ -936,10 +1280,25 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
                 ok = false;
                 break;
             }
+            if (TREE && !dead_tile && (w.j_lo + j + 1) * BN > tree0) {  // its keys' values, for the tile's other rows
+                const bool odd = odd_key(j);
+                if (!blank_rows(j, odd)) {
+                    ok = false;
+                    break;
+                }
+            }
             warp_arrive(sm.p_full(t), lane);
         }
         for (int j = 0; !dead && j < w.n_kv; ++j) {
             const int g = g0 + j;
+            const int kbase = (w.j_lo + j) * BN;  // absolute first key of this tile
+            // (while the tile's scores are on their way)
+            uint32_t vis[4];
+            bool odd = false;
+            if (TREE && kbase + BN > tree0) {
+                tree_visible(p, w, pos, valid, kbase, vis);
+                odd = odd_key(j);
+            }
             if (!wait_bounded(sm.s_full(t), (uint32_t)(g & 1), wc, kSiteSoftmaxS)) {
                 ok = false;
                 break;
@@ -964,10 +1323,17 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
                     s[48 + i] = make_float2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]));
                 }
             }
-            const int kbase = (w.j_lo + j) * BN;  // absolute first key of this tile
-            const bool masked = kbase + BN - 1 > lim_tile;
+            const bool masked = kbase + BN - 1 > (TREE ? tree0 - 1 : lim_tile);
             float mx;
-            if (masked) {
+            if (TREE && masked) {
+                float2 sm2[64];
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    sm2[i].x = vis[i >> 4] >> (2 * i & 31) & 1u ? s[i].x : -INFINITY;
+                    sm2[i].y = vis[i >> 4] >> (2 * i + 1 & 31) & 1u ? s[i].y : -INFINITY;
+                }
+                mx = row_max(sm2);
+            } else if (masked) {
                 // Scores of keys the row may not see take no part in the max.
                 float2 sm2[64];
 #pragma unroll
@@ -991,7 +1357,8 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
             const float alpha = need ? ptx::ex2(m_run - m_new) : 1.f;
             const float m_sub = (m_new == -INFINITY) ? 0.f : m_new;
             uint32_t pk[64];
-            const float rowsum = masked ? softmax_tile<true>(s, pk, sl2, m_sub, kbase, lim_row)
+            const float rowsum = TREE && masked ? softmax_tile_bits(s, pk, sl2, m_sub, vis)
+                                 : masked ? softmax_tile<true>(s, pk, sl2, m_sub, kbase, lim_row)
                                         : softmax_tile<false>(s, pk, sl2, m_sub, kbase, lim_row);
             // P_t(g-1) and O_t are read / written by PV_t(g-1): wait for it before
             // overwriting P_t or rescaling O_t (normally it finished long ago).
@@ -1042,31 +1409,11 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
             ptx::tmem_wait_st();
             l_run = l_run * alpha + rowsum;
             m_run = m_new;
-            if (PACKED && kbase + BN > w.Sk) {
-                // Last tile of a packed or paged sequence: the V rows past its end
-                // hold other data (the next sequence's rows, or whatever a page's
-                // unused slots contain).  Their P is 0, but 0 * NaN is NaN, so each
-                // group zeroes those rows in shared memory once the tile has
-                // landed, before releasing its P (the two streams' P V products
-                // are not ordered; both groups write the same zeros).
-                const int item = nb + 2 * j + 1;
-                uint8_t *vt = sm.slot(item % NSLOT);
-                if (!wait_bounded(sm.kv_full(item % NSLOT), (uint32_t)((item / NSLOT) & 1), wc, kSiteSoftmaxV)) {
+            if (TREE ? masked : PACKED && kbase + BN > w.Sk) {
+                if (!blank_rows(j, odd)) {
                     ok = false;
                     break;
                 }
-                if (kbase + r >= w.Sk) {
-                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                    // row r, both halves (dense or paged tile layout)
-                    uint8_t *h0 = PAGED ? vt + (r >> 3) * PG_GROUP_BYTES + (r & 7) * 128 : vt + r * 128;
-                    uint8_t *h1 = h0 + (PAGED ? PG_HALF_BYTES : HALF_BYTES);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        reinterpret_cast<uint4 *>(h0)[c] = z;
-                        reinterpret_cast<uint4 *>(h1)[c] = z;
-                    }
-                }
-                ptx::fence_proxy_async_smem();
             }
             warp_arrive(sm.p_full(t), lane);
         }
@@ -1082,7 +1429,12 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
         const int o_item = nb + 2 * w.n_kv + t;
         uint8_t *stage = sm.slot(o_item % NSLOT);
         if (ok) ok = wait_bounded(sm.kv_full(o_item % NSLOT), (uint32_t)((o_item / NSLOT) & 1), wc, kSiteEpilogueSlot);
-        if (!PACKED && w.part >= 0) {
+        if (TREE) {
+            // Every warp's flags of its keys are there.  A warp that left comes to one
+            // barrier only: where this one says "not well", all of them leave here.
+            if (has_tree && !ptx::named_bar_and(1 + t, 128, ok && !*wc.abort_flag)) break;
+            tree_epilogue(p, sm, w, tO, t, quarter, lane, pos, head, valid, dead, has_tree, m_run, l_run, stage, ok);
+        } else if (!PACKED && w.part >= 0) {
             // A key-range part of a split unit: its O (normalised within the range)
             // and log-sum-exp go to the workspace in fp32 for the merge kernel.
             ptx::tc_fence_after();
@@ -1139,7 +1491,9 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
         ptx::fence_proxy_async_smem();
         if (!ptx::named_bar_and(1 + t, 128, ok && !*wc.abort_flag)) break;
         bool handed = false;  // the store lane releases the slot
-        if (PACKED && s0 + BM > w.Sq) {
+        if (TREE) {
+            // (the rows are stored, each warp's by itself)
+        } else if (PACKED && s0 + BM > w.Sq) {
             // Last row block of a packed sequence: a full box would spill into the
             // next sequence's rows, so each thread stores its own row (if valid)
             // from the swizzled staging tile; the group then waits for all rows
@@ -1236,8 +1590,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (warp < 4) {
         ptx::setmaxnreg_dec<REGS_CONTROL>();
         if (warp == 0) {
-            if (KIND == kPaged)
-                producer_paged(p, sm, wc, lane, &map_q, &map_k, &map_v, &map_k8, &map_v8);
+            if (KIND == kPaged || KIND == kTree)
+                producer_paged<KIND>(p, sm, wc, lane, &map_q, &map_k, &map_v, &map_k8, &map_v8);
             else if (lane == 0)
                 producer<KIND>(p, sm, wc, &map_q, &map_k, &map_v);
         } else if (warp == 3) {
@@ -1245,9 +1599,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         } else if (warp == 1 || warp == 2) {
             if (lane == 0) {
                 if (warp == 1)
-                    mma_stream<0, KIND == kPaged>(p, sm, wc, tmem_base);
+                    mma_stream<0, KIND == kPaged || KIND == kTree>(p, sm, wc, tmem_base);
                 else
-                    mma_stream<1, KIND == kPaged>(p, sm, wc, tmem_base);
+                    mma_stream<1, KIND == kPaged || KIND == kTree>(p, sm, wc, tmem_base);
                 // Whatever happened, wait until every product issued (by
                 // either stream) has completed before tensor memory is released.
                 ptx::umma_commit(sm.fin());
@@ -1300,11 +1654,15 @@ cudaError_t launch_prefill(const CUtensorMap &mq, const CUtensorMap &mk, const C
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(g1::prefill_kernel<g1::kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(g1::prefill_kernel<g1::kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         configured_device = dev;
     }
     // One instantiation per kind of launch, each with only its own paths.
-    if (p.block_table != nullptr)
+    if (p.parents != nullptr)
+        g1::prefill_kernel<g1::kTree><<<num_ctas, g1::NUM_THREADS, smem, stream>>>(mq, mk, mv, mo, mk8, mv8, p);
+    else if (p.block_table != nullptr)
         g1::prefill_kernel<g1::kPaged><<<num_ctas, g1::NUM_THREADS, smem, stream>>>(mq, mk, mv, mo, mk8, mv8, p);
     else if (p.cu_q != nullptr)
         g1::prefill_kernel<g1::kPacked><<<num_ctas, g1::NUM_THREADS, smem, stream>>>(mq, mk, mv, mo, mk8, mv8, p);
@@ -1405,6 +1763,98 @@ cudaError_t launch_prefill_merge(void *out, const PrefillParams &p, cudaStream_t
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, g1::merge_kernel, static_cast<__nv_bfloat16 *>(out), p);
+}
+
+namespace g1 {
+
+// Joins a tree launch's partials: WARPS warps a row of out, which take its parts in
+// turn, four columns a lane.  blockIdx.x: sequence x row (position x head).  Rows of
+// units that were not cut are there already.
+template <int WARPS>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const PrefillParams p, int ctas, int blocks_per_seq) {
+    ptx::wait_for_prior_work();
+    constexpr int ROWS = 8 / WARPS;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.x / blocks_per_seq;
+    const int idx = (blockIdx.x - b * blocks_per_seq) * ROWS + warp / WARPS;
+    const int pos = idx / p.Hq, h = idx - pos * p.Hq;
+    const TreeSeq s = tree_seq(p, b, false);
+    const int total = p.first[p.B], shares = tree_shares(ctas, total);
+    int c0 = 0, c1 = 0, us = 0, row = 0;
+    if (pos < s.Sq) {
+        const int g = h / p.G, blk = pos / (2 * p.pack_pos), rem = pos - blk * 2 * p.pack_pos;
+        const int t = rem >= p.pack_pos ? 1 : 0;
+        row = t * BM + (rem - t * p.pack_pos) * p.G + h - g * p.G;
+        us = p.first[b] + (g * s.blocks + blk) * s.tiles;
+        c0 = tree_share_of(us, shares, total);
+        c1 = tree_share_of(us + s.tiles - 1, shares, total);
+    }
+    const bool cut = c1 > c0;
+    if (WARPS == 1 && !cut) return;
+    // The part of CTA c: its share's first segment, or its last where it begins with another unit.
+    auto part_row = [&](int c) {
+        return ((int64_t)c * 2 + (tree_share_begin(c, shares, total) < us ? 1 : 0)) * p.part_rows + row;
+    };
+    float M = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (cut) {
+        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.ws_lse[part_row(c)]);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 8
+        for (int c = c0 + warp % WARPS; c <= c1; c += WARPS) {
+            const int64_t at = part_row(c);
+            const float4 x = reinterpret_cast<const float4 *>(p.ws_o + at * D)[lane];
+            const float wk = ptx::ex2((p.ws_lse[at] - ref) * 1.4426950408889634f);
+            sum += wk;
+            o.x = fmaf(wk, x.x, o.x);
+            o.y = fmaf(wk, x.y, o.y);
+            o.z = fmaf(wk, x.z, o.z);
+            o.w = fmaf(wk, x.w, o.w);
+        }
+    }
+    if (WARPS > 1) {
+        __shared__ float4 part_o[8][32];
+        __shared__ float part_sum[8];
+        part_o[warp][lane] = o;
+        if (lane == 0) part_sum[warp] = sum;
+        __syncthreads();
+        if (warp % WARPS != 0 || !cut) return;
+#pragma unroll
+        for (int k = 1; k < WARPS; ++k) {
+            const float4 x = part_o[warp + k][lane];
+            sum += part_sum[warp + k];
+            o.x += x.x;
+            o.y += x.y;
+            o.z += x.z;
+            o.w += x.w;
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + ((int64_t)(s.q0 + pos) * p.Hq + h) * D)[lane] =
+        make_uint2(pack_bf16x2_mode(o.x * inv, o.y * inv, p.round_mode), pack_bf16x2_mode(o.z * inv, o.w * inv, p.round_mode));
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[(int64_t)h * p.total_q + s.q0 + pos] = sum == 0.f ? -INFINITY : M + ptx::lg2(sum) * LN2;
+}
+
+}  // namespace g1
+
+cudaError_t launch_tree_merge(const PrefillParams &p, int ctas, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // Few rows: eight warps each, a row's parts may be many.
+    const int64_t rows = (int64_t)p.Sq * p.Hq;
+    const bool few = rows * p.B <= 4096;
+    const int per = (int)(few ? rows : (rows + 7) / 8);
+    cfg.gridDim = dim3((unsigned)(per * p.B));
+    return cudaLaunchKernelEx(&cfg, few ? g1::tree_merge_kernel<8> : g1::tree_merge_kernel<1>, p, ctas, per);
 }
 
 }  // namespace attn

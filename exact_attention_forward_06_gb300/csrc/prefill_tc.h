@@ -59,7 +59,30 @@ struct PrefillParams {
     const int *block_table;
     const int *seqlens_k;
     int max_blocks, num_pages;
+    // Trees of drafted tokens against the paged cache (parents == nullptr: none).
+    // The tokens of sequence b are the last of its cache, and token i's parent is
+    // token parents[cu_q[b] + i] < i of the same sequence (-1: none).  The K/V
+    // tiles of all (sequence, KV head, row block) units lie on one line, which
+    // the grid's CTAs share equally; a unit cut between CTAs leaves fp32
+    // partials, two at most a CTA, in ws_o [CTAs][2][part_rows][128] and
+    // ws_lse [CTAs][2][part_rows], and `first` [B + 1] says where on the line
+    // each sequence begins.
+    const int *parents;
+    const void *q, *k_pool, *v_pool;
+    int part_rows;
+    int *first;
 };
+
+// Row layout of a tree launch: positions a Q tile covers, rows of a partial.
+constexpr int kTreeMaxNodes = 256;
+constexpr int kTreeMaxCtas = 152;  // the SMs of a GB300
+inline int tree_tile_positions(int G) { return 128 / G; }
+inline int tree_part_rows(int G, int max_nodes) {
+    const int pp = tree_tile_positions(G);
+    return max_nodes <= pp ? max_nodes * G : 128 + (max_nodes - pp < pp ? max_nodes - pp : pp) * G;
+}
+// Joins the partials of cut units into out and lse.
+cudaError_t launch_tree_merge(const PrefillParams &p, int ctas, cudaStream_t stream);
 
 int prefill_smem_bytes();
 int prefill_num_units(const PrefillParams &p);

@@ -189,6 +189,47 @@ attn_status_t attn_fwd_paged(const void *q, const void *k_pages, const void *v_p
                              int page_size, int num_pages, int max_blocks_per_seq,
                              int causal, float scale, int round_mode, void *stream);
 
+/* The most tokens of a sequence's tree of drafted tokens. */
+#define ATTN_TREE_MAX 256
+
+/* Device workspace attn_fwd_tree_paged needs (a pure function; 0 if invalid). */
+size_t attn_fwd_tree_paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_seqlen_q);
+
+/*
+ * attn_fwd_tree_paged -- attention of trees of drafted tokens against a paged
+ * KV cache (speculative decoding), split over the keys.
+ *
+ * A sequence's tree is the last Lq tokens of its cache, its keys and values
+ * already appended (attn_append_paged, with each token's depth in `positions`).
+ * Token i of the tree sees the keys before the tree, itself and its ancestors:
+ * parents[i], that token's parent, and so on.
+ *
+ * q, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, out, lse: as
+ *      attn_fwd_paged; sequence b's tree is rows cu_seqlens_q[b] ..
+ *      cu_seqlens_q[b+1]-1, of at most max_seqlen_q tokens (1 .. ATTN_TREE_MAX;
+ *      it may exceed total_q).  Sequences without rows are skipped.
+ * parents: DEVICE int32 [total_q], each token's parent by its place in its own
+ *      sequence's tree (0 .. its own place - 1), or -1 for none (several tokens
+ *      may have none).
+ * workspace: DEVICE buffer of at least attn_fwd_tree_paged_workspace_bytes(...)
+ *      bytes, 256-byte aligned, owned by the caller, overwritten; calls that may
+ *      run at the same time need one each.
+ * A token is only affected by keys that it sees: keys and values of other
+ * branches, and slots past a sequence's length, may hold anything, NaN and
+ * infinities included.
+ * Hq / Hkv is at most 128 (ATTN_ERR_UNSUPPORTED), and the K/V tiles of all heads
+ * at most 2^31 - 1.  Offsets and lengths are checked as by attn_fwd_paged, and
+ * seqlens_k[b] must be at least the tree's size (otherwise the sequence is
+ * skipped); a parent outside its range counts as -1; all of these are recorded as
+ * ATTN_ERR_DEVICE_BOUNDS.  Deterministic.
+ */
+attn_status_t attn_fwd_tree_paged(const void *q, const void *k_pages, const void *v_pages,
+                                  const int32_t *block_table, const int32_t *seqlens_k,
+                                  const int32_t *cu_seqlens_q, const int32_t *parents, void *out, float *lse,
+                                  int B, int Hq, int Hkv, int total_q, int max_seqlen_q, int d, int page_size,
+                                  int num_pages, int max_blocks_per_seq, float scale, int round_mode,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
 /*
  * attn_fwd_host -- attn_fwd_rounded from and to HOST memory.
  *
