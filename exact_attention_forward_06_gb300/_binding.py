@@ -128,6 +128,8 @@ def load():
             lib.attn_fwd_tree_paged_workspace_bytes.argtypes = [_i] * 5
             lib.attn_fwd_tree_paged_workspace_bytes.restype = _sz
             lib.attn_fwd_tree_paged.argtypes = [_p] * 9 + [_i] * 9 + [_f, _i, _p, _sz, _p]
+            lib.attn_verify_tree.argtypes = [_p, _p, _i] + [_p] * 9 + [_i] * 4 + [_sz] * 3 + [_p]
+            lib.attn_compact_paged.argtypes = [_p] * 8 + [_i] * 9 + [_p]
             lib.attn_status_string.argtypes = [_i]
             lib.attn_status_string.restype = ctypes.c_char_p
             lib.attn_version.restype = _i
@@ -137,7 +139,7 @@ def load():
                          "attn_get_device_status", "attn_set_wait_budget_ns", "attn_debug_inject",
                          "attn_selftest_umma", "attn_qk_norm_rope", "attn_append_paged", "attn_append_paged_q4",
                          "attn_gather_paged_q4", "attn_decode_paged_q4", "attn_fwd_paged_q4",
-                         "attn_fwd_tree_paged"):
+                         "attn_fwd_tree_paged", "attn_verify_tree", "attn_compact_paged"):
                 getattr(lib, name).restype = _i
             _lib = lib
     return _lib
@@ -951,6 +953,121 @@ def fwd_tree_paged(q, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, pa
     if rc:
         _check(rc, "attn_fwd_tree_paged")
     return out, lse
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _rows(t, name, dtype, dev, shape):
+    """Address and row stride of a [rows, vocab] tensor whose rows are contiguous."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.dim() == 2 and t.stride(1) == 1:
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+            return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+    except AttributeError:
+        pass  # not a tensor
+    _refuse(t, name, dtype, dev, contiguous=False)
+
+
+def _out_i32(t, name, shape, like, stream, dev):
+    """An int32 output as given (checked) or made, and its address."""
+    if t is None:
+        t = _empty(shape, _i32, like.device, stream)
+        return t, t.data_ptr()
+    ptr = _in(t, name, _i32, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return t, ptr
+
+
+def verify_tree(logits, tokens, parents, cu_seqlens, *, draft_logits=None, temperature=None, uniforms=None, noise=None,
+                max_seqlen=None, path=None, out_tokens=None, counts=None, stream=None):
+    """Which drafted tokens of each sequence's tree are kept, and the token that follows them, from given random numbers.
+
+    logits [total, vocab] bf16 or fp32 (rows may be strided): the target's at every node; tokens, parents [total] and
+    cu_seqlens [B + 1] int32: the trees, each root first (the token emitted last) and every node behind its parent.
+    draft_logits: the distributions that every node's children were drawn from, like logits; None where they were chosen
+    in another way.  temperature [B] fp32 (<= 0: the largest logit), uniforms [total] fp32 in [0, 1) and noise
+    [B, vocab] fp32, exponential numbers; without temperature every sequence takes its largest logits and there are no
+    draft_logits, uniforms or noise.  max_seqlen (at most TREE_MAX), when omitted, is read from the offsets (a
+    synchronisation).
+
+    Returns (path, out_tokens, counts): int32 [B, max_seqlen] with counts[b] entries each and -1 behind, the kept nodes
+    (the root first) and the emitted tokens (those of the kept nodes after the root, and the last one).
+    """
+    lib = _lib or load()
+    dev = _current()
+    dtype = logits.dtype if isinstance(logits, torch.Tensor) and logits.dtype in _DTYPES else _bf16
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise TypeError("logits must be a CUDA tensor [total, vocab]")
+    shape = logits.shape
+    total, vocab = shape
+    lp, ls = _rows(logits, "logits", dtype, dev, shape)
+    tok, par = _in(tokens, "tokens", _i32, dev), _in(parents, "parents", _i32, dev)
+    cu = _in(cu_seqlens, "cu_seqlens", _i32, dev)
+    B = cu_seqlens.numel() - 1
+    if tokens.numel() != total or parents.numel() != total or B < 1:
+        raise ValueError("tokens and parents must have one entry per row of logits, cu_seqlens B + 1")
+    dp = tp = up = np_ = None
+    ds = ns = 0
+    if temperature is None:
+        if draft_logits is not None or uniforms is not None or noise is not None:
+            raise ValueError("draft_logits, uniforms and noise go with a temperature")
+    else:
+        tp = _in(temperature, "temperature", torch.float32, dev)
+        if uniforms is None or noise is None:
+            raise ValueError("drawing (temperature) needs uniforms and noise")
+        up = _in(uniforms, "uniforms", torch.float32, dev)
+        np_, ns = _rows(noise, "noise", torch.float32, dev, (B, vocab))
+        if temperature.numel() != B or uniforms.numel() != total:
+            raise ValueError("temperature must have B entries and uniforms one per row of logits")
+        if draft_logits is not None:
+            dp, ds = _rows(draft_logits, "draft_logits", dtype, dev, shape)
+    if max_seqlen is None:
+        max_seqlen = max(1, int(torch.diff(cu_seqlens).max()))
+    path, pp = _out_i32(path, "path", (B, max_seqlen), logits, stream, dev)
+    out_tokens, op = _out_i32(out_tokens, "out_tokens", (B, max_seqlen), logits, stream, dev)
+    counts, cp = _out_i32(counts, "counts", (B,), logits, stream, dev)
+    rc = lib.attn_verify_tree(lp, dp, _DTYPES[dtype], tok, par, cu, tp, up, np_, pp, op, cp, B, total, vocab, max_seqlen,
+                              ls, ds, ns, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "attn_verify_tree")
+    return path, out_tokens, counts
+
+
+def compact_paged(k_pages, v_pages, block_table, seqlens_k, cu_seqlens, path, counts, *, total=None, seqlens_out=None,
+                  stream=None):
+    """Cut a paged cache down to the accepted path of each sequence's tree (path and counts of verify_tree).
+
+    k_pages, v_pages [num_pages, 16, Hkv, 128] or [layers, num_pages, 16, Hkv, 128] bf16, updated in place; block_table,
+    seqlens_k (with the trees) and cu_seqlens as for fwd_tree_paged.  The kept nodes' keys and values move to the tree's
+    first places.  total bounds the offsets (default: B times path's width).  Returns the new lengths, int32 [B]
+    (seqlens_out, which must not be seqlens_k).
+    """
+    lib = _lib or load()
+    dev = _current()
+    kp, vp = _in(k_pages, "k_pages", _bf16, dev), _in(v_pages, "v_pages", _bf16, dev)
+    table, lens = _in(block_table, "block_table", _i32, dev), _in(seqlens_k, "seqlens_k", _i32, dev)
+    cu, pt, ct = _in(cu_seqlens, "cu_seqlens", _i32, dev), _in(path, "path", _i32, dev), _in(counts, "counts", _i32, dev)
+    pool, table_shape, path_shape = k_pages.shape, block_table.shape, path.shape
+    B = seqlens_k.numel()
+    if len(pool) not in (4, 5) or v_pages.shape != pool:
+        raise ValueError("k_pages and v_pages must be [num_pages, 16, Hkv, 128] or [layers, num_pages, 16, Hkv, 128]")
+    layers = 1 if len(pool) == 4 else pool[0]
+    num_pages, page_size, Hkv, d = pool[-4:]
+    if len(table_shape) != 2 or table_shape[0] != B or cu_seqlens.numel() != B + 1:
+        raise ValueError("block_table must have B rows and cu_seqlens B + 1 entries")
+    if len(path_shape) != 2 or path_shape[0] != B or counts.numel() != B:
+        raise ValueError("path must be [B, max_seqlen] and counts [B]")
+    if total is None:
+        total = max(1, B * path_shape[1])
+    seqlens_out, sp = _out_i32(seqlens_out, "seqlens_out", (B,), k_pages, stream, dev)
+    rc = lib.attn_compact_paged(kp, vp, table, lens, cu, pt, ct, sp, B, layers, Hkv, total, path_shape[1], d, page_size,
+                                num_pages, table_shape[1], _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "attn_compact_paged")
+    return seqlens_out
 
 
 def lse_merge(o_parts, lse_parts, *, out=None, lse=None, stream=None, rounding="rtne"):

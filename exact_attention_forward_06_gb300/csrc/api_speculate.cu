@@ -1,0 +1,120 @@
+// api_speculate.cu -- the C ABI of the operators around a tree of drafted tokens:
+// argument validation and launches of the verification and of the cache's
+// compaction.  Nothing here allocates device memory.
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "api_internal.h"
+#include "attn.h"
+#include "speculate.h"
+
+namespace {
+
+bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// A device pointer to 4-byte elements.
+bool ok4(const void *p) { return p != nullptr && aligned(p, 4); }
+
+bool overlap(const void *a, const void *b, size_t bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bytes && y < x + bytes;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_verify_tree(const void *logits, const void *draft_logits, int dtype, const int32_t *tokens,
+                               const int32_t *parents, const int32_t *cu_seqlens, const float *temperature,
+                               const float *uniforms, const float *noise, int32_t *path, int32_t *out_tokens,
+                               int32_t *counts, int B, int total, int vocab, int max_seqlen, size_t logits_stride,
+                               size_t draft_stride, size_t noise_stride, void *stream) {
+    if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_FP32) return ATTN_ERR_INVALID_ARG;
+    const uintptr_t size = dtype == ATTN_DTYPE_BF16 ? 2 : 4;
+    if (!logits || !aligned(logits, size) || (draft_logits && !aligned(draft_logits, size)))
+        return ATTN_ERR_INVALID_ARG;
+    if (!ok4(tokens) || !ok4(parents) || !ok4(cu_seqlens) || !ok4(path) || !ok4(out_tokens) || !ok4(counts))
+        return ATTN_ERR_INVALID_ARG;
+    // Drawing wants random numbers; without it there is nothing to be said of a draft's distribution.
+    if (temperature ? (!aligned(temperature, 4) || !ok4(uniforms) || !ok4(noise))
+                    : (draft_logits || uniforms || noise))
+        return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || total < 1 || vocab < 1 || vocab > 0x7fffffff - 64 || max_seqlen < 1 || max_seqlen > ATTN_TREE_MAX)
+        return ATTN_ERR_INVALID_ARG;
+    if (B > 0x7fffffff / 8) return ATTN_ERR_INVALID_ARG;
+    const size_t top = (size_t)1 << 40, V = (size_t)vocab;
+    if (logits_stride < V || logits_stride > top || (draft_logits && (draft_stride < V || draft_stride > top)) ||
+        (temperature && (noise_stride < V || noise_stride > top)))
+        return ATTN_ERR_INVALID_ARG;
+    attn::VerifyParams p = {};
+    p.logits = logits;
+    p.draft = draft_logits;
+    p.logits_stride = (int64_t)logits_stride;
+    p.draft_stride = (int64_t)draft_stride;
+    p.noise_stride = (int64_t)noise_stride;
+    p.tokens = tokens;
+    p.parents = parents;
+    p.cu = cu_seqlens;
+    p.temperature = temperature;
+    p.uniforms = uniforms;
+    p.noise = noise;
+    p.path = path;
+    p.out_tokens = out_tokens;
+    p.counts = counts;
+    p.B = B;
+    p.total = total;
+    p.V = vocab;
+    p.width = max_seqlen;
+    p.fp32 = dtype == ATTN_DTYPE_FP32 ? 1 : 0;
+    int sms;
+    uint64_t budget;
+    const attn_status_t st = attn::device_state(&sms, &p.status, &budget);
+    if (st != ATTN_OK) return st;
+    return attn::launch_verify(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status_t attn_compact_paged(void *k_pages, void *v_pages, const int32_t *block_table, const int32_t *seqlens_k,
+                                 const int32_t *cu_seqlens, const int32_t *path, const int32_t *counts,
+                                 int32_t *seqlens_out, int B, int layers, int Hkv, int total, int max_seqlen, int d,
+                                 int page_size, int num_pages, int max_blocks_per_seq, void *stream) {
+    if (!k_pages || !v_pages || !aligned(k_pages, 16) || !aligned(v_pages, 16)) return ATTN_ERR_INVALID_ARG;
+    if (!ok4(block_table) || !ok4(seqlens_k) || !ok4(cu_seqlens) || !ok4(path) || !ok4(counts) || !ok4(seqlens_out))
+        return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || layers < 1 || Hkv < 1 || total < 1 || num_pages < 1 || max_blocks_per_seq < 1 || max_seqlen < 1 ||
+        max_seqlen > ATTN_TREE_MAX)
+        return ATTN_ERR_INVALID_ARG;
+    if ((int64_t)num_pages * 16 > 0x7fffffff || (int64_t)max_blocks_per_seq * 16 > 0x7fffffff)
+        return ATTN_ERR_INVALID_ARG;
+    if (d != 128 || page_size != 16) return ATTN_ERR_UNSUPPORTED;
+    // One block a sequence and 128 columns of 16 bytes.
+    if ((int64_t)layers * 2 * Hkv > 0x7fffffff / 16 ||
+        ((int64_t)layers * 2 * Hkv * 16 + 127) / 128 > (int64_t)0x7fffffff / B)
+        return ATTN_ERR_INVALID_ARG;
+    // Every block reads the lengths: they are not replaced in place.
+    const size_t bytes = (size_t)B * 4;
+    if (overlap(seqlens_out, seqlens_k, bytes) || overlap(seqlens_out, counts, bytes)) return ATTN_ERR_INVALID_ARG;
+    attn::CompactParams p = {};
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.block_table = block_table;
+    p.seqlens = seqlens_k;
+    p.cu = cu_seqlens;
+    p.path = path;
+    p.counts = counts;
+    p.seqlens_out = seqlens_out;
+    p.B = B;
+    p.layers = layers;
+    p.Hkv = Hkv;
+    p.total = total;
+    p.width = max_seqlen;
+    p.num_pages = num_pages;
+    p.max_blocks = max_blocks_per_seq;
+    int sms;
+    uint64_t budget;
+    const attn_status_t st = attn::device_state(&sms, &p.status, &budget);
+    if (st != ATTN_OK) return st;
+    return attn::launch_compact(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -46,6 +46,11 @@ enum WaitSite : unsigned {
     kSiteQ4Page = 26,
     kSiteTreeOffsets = 27,
     kSiteTreeParent = 28,
+    kSiteVerifyOffsets = 29,
+    kSiteVerifyToken = 30,
+    kSiteCompactOffsets = 31,
+    kSiteCompactPath = 32,
+    kSiteCompactTable = 33,
 };
 
 // First error wins; the site is informative only.

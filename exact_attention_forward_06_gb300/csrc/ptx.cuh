@@ -206,6 +206,32 @@ __device__ __forceinline__ void wait_for_prior_work() { asm volatile("griddepcon
 // Lets the next dependent grid be set up (it still waits for this one's end).
 __device__ __forceinline__ void allow_next_work() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// ---------------------------------------------------------------- thread-block clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Every thread of the cluster arrives and waits; what they wrote before, in any
+// CTA's shared memory, is seen after.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// 16 bytes into the shared memory of the cluster's CTA `rank`, at the place that
+// `own` has in this CTA's.
+__device__ __forceinline__ void cluster_store(const void *own, uint32_t rank, float4 v) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+        "st.shared::cluster.v4.f32 [a], {%2, %3, %4, %5};\n\t}" ::"r"(smem_addr(own)),
+        "r"(rank), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+        : "memory");
+}
+
 // ---------------------------------------------------------------- named barriers
 
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {

@@ -1,0 +1,36 @@
+// speculate.h -- host-side interface of the kernels around a tree of drafted tokens:
+// verification against the target's probabilities, and the cache cut down to the
+// accepted path.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace attn {
+
+struct VerifyParams {
+    const void *logits, *draft;  // [total][V] bf16 or fp32; draft may be nullptr
+    int64_t logits_stride, draft_stride, noise_stride;  // elements per row
+    const int32_t *tokens, *parents, *cu;
+    const float *temperature;  // [B] or nullptr: no drawing anywhere
+    const float *uniforms;     // [total]
+    const float *noise;        // [B][V]
+    int32_t *path, *out_tokens, *counts;
+    int B, total, V, width;
+    int fp32;  // type of logits and draft
+    unsigned *status;
+};
+
+struct CompactParams {
+    void *k_pages, *v_pages;  // [layers][num_pages][16][Hkv][128] bf16
+    const int32_t *block_table, *seqlens, *cu, *path, *counts;
+    int32_t *seqlens_out;
+    int B, layers, Hkv, total, width, num_pages, max_blocks;
+    unsigned *status;
+};
+
+cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream);
+cudaError_t launch_compact(const CompactParams &p, cudaStream_t stream);
+
+}  // namespace attn

@@ -599,6 +599,89 @@ attn_status_t attn_fwd_paged_q4(const void *q, const void *cache, const int32_t 
                                 int causal, float scale, int round_mode,
                                 void *workspace, size_t workspace_bytes, void *stream);
 
+/* Element type of a tensor that comes in more than one. */
+typedef enum {
+    ATTN_DTYPE_BF16 = 0,
+    ATTN_DTYPE_FP32 = 1
+} attn_dtype_t;
+
+/*
+ * attn_verify_tree -- speculative decoding: which drafted tokens of each
+ * sequence's tree are kept, and the token that follows them, from given random
+ * numbers.  The emitted tokens are distributed as if drawn one by one from the
+ * target's probabilities.
+ *
+ * Sequence b's tree is rows cu_seqlens[b] .. cu_seqlens[b+1]-1, at most max_seqlen
+ * (1 .. ATTN_TREE_MAX) of them.  Row 0 is the root, the last token emitted
+ * before; parents are as in attn_fwd_tree_paged, and nodes that do not hang on the
+ * root are never reached.  From the root down, at node c with the target's
+ * distribution p = softmax(logits[c] / temperature[b]), c's children are tried in
+ * order, x a child's token and u its uniform number:
+ *   - with draft_logits, the children were drawn, independently, from q =
+ *     softmax(draft_logits[c] / temperature[b]): accepted if u q(x) < p(x); a
+ *     rejected child leaves p <- max(p - q, 0) / sum (p, where that sum is 0);
+ *   - without, the children were chosen in some other way (a draft's likeliest
+ *     tokens, a lookup): accepted if u < p(x); a rejected child leaves p without x,
+ *     normalised.
+ * The walk goes on at the first accepted child.  Where none is, the last token is
+ * argmax_i p_i / noise[b][i] of what is left of p: with independent exponential
+ * numbers, token i with probability p_i.  Ties go to the lowest index.
+ * temperature[b] <= 0 (or NaN), and temperature NULL for all sequences: the last
+ * token is the row's largest logit's, and the child with that token is accepted;
+ * draft_logits, uniforms and noise are not read.
+ *
+ * logits, draft_logits: [total] rows of vocab elements of `dtype` (an
+ *      attn_dtype_t), logits_stride / draft_stride elements apart; draft_logits may
+ *      be NULL, and must be where temperature is.  -inf leaves a token out, NaN
+ *      counts as -inf, and +inf as the largest finite fp32.
+ * tokens: int32 [total], each node's token (a root's is not looked at).
+ * temperature: fp32 [B] or NULL.  uniforms: fp32 [total] in [0, 1).  noise: fp32
+ *      [B] rows, noise_stride elements apart, of positive numbers (an element that
+ *      is not positive is never drawn).  Both NULL where temperature is.
+ * path: int32 [B][max_seqlen] (written): the kept nodes, the root first, by their
+ *      place in the tree; then -1.  counts: int32 [B] (written), how many; the root
+ *      counts, so 0 only where a sequence has no rows.
+ * out_tokens: int32 [B][max_seqlen] (written): the counts[b] emitted tokens, those of
+ *      path[1 ..] and the last one; then -1.  A row without any token left (all
+ *      logits -inf) emits -1.
+ * Tokens outside the vocabulary are never accepted, a parent outside its range
+ * counts as -1, and a sequence with bad offsets or more than max_seqlen rows gets no
+ * nodes; each is recorded as ATTN_ERR_DEVICE_BOUNDS.  logits and draft_logits need
+ * the alignment of their elements only; rows that are not 16-byte aligned are read a
+ * little more slowly.  Deterministic.  No workspace.
+ */
+attn_status_t attn_verify_tree(const void *logits, const void *draft_logits, int dtype, const int32_t *tokens,
+                               const int32_t *parents, const int32_t *cu_seqlens, const float *temperature,
+                               const float *uniforms, const float *noise, int32_t *path, int32_t *out_tokens,
+                               int32_t *counts, int B, int total, int vocab, int max_seqlen, size_t logits_stride,
+                               size_t draft_stride, size_t noise_stride, void *stream);
+
+/*
+ * attn_compact_paged -- cut a paged cache down to the accepted path of each
+ * sequence's tree.
+ *
+ * The tree is the last n = cu_seqlens[b+1] - cu_seqlens[b] tokens of sequence b's
+ * cache.  The keys and values of its nodes path[b][0 .. counts[b]-1] (ascending, as
+ * attn_verify_tree writes them) move to the tree's first places, in all layers and
+ * heads; the rows behind them are left as they were.
+ *
+ * k_pages, v_pages: bf16 [layers][num_pages][16][Hkv][128], updated in place (one
+ *      block table for all layers; layers = 1 for a pool of one layer).
+ * block_table, seqlens_k (the lengths with the trees), cu_seqlens: as
+ *      attn_fwd_tree_paged; total bounds cu_seqlens.
+ * path: int32 [B][max_seqlen]; counts: int32 [B], 0 .. n (0 drops the whole tree).
+ * seqlens_out: int32 [B] (written), seqlens_k[b] - n + counts[b]; must not overlap
+ *      seqlens_k or counts.
+ * A sequence with bad offsets, lengths, counts or path is left alone (seqlens_out =
+ * seqlens_k), a row whose page, old or new, lies outside the pool does not move; both
+ * are recorded as ATTN_ERR_DEVICE_BOUNDS.
+ */
+attn_status_t attn_compact_paged(void *k_pages, void *v_pages, const int32_t *block_table,
+                                 const int32_t *seqlens_k, const int32_t *cu_seqlens, const int32_t *path,
+                                 const int32_t *counts, int32_t *seqlens_out, int B, int layers, int Hkv, int total,
+                                 int max_seqlen, int d, int page_size, int num_pages, int max_blocks_per_seq,
+                                 void *stream);
+
 /*
  * attn_lse_merge -- merge key-range partial results by log-sum-exp (the merge
  * step of the Flash-Decoding style split).  For each row r:
