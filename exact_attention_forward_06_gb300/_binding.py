@@ -49,7 +49,7 @@ class AttnError(RuntimeError):
 
 class _NoQuick:
     """In the place of _quick where it cannot be used: every call goes the long way."""
-    qk_norm_rope = append = gather = decode = fwd = staticmethod(lambda *args: None)
+    qk_norm_rope = append = gather = decode = fwd = tree = verify = compact = staticmethod(lambda *args: None)
 
 
 def _load_quick():
@@ -923,6 +923,11 @@ def fwd_tree_paged(q, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, pa
     lib = _lib or load()
     if rounding not in ROUNDING:
         raise ValueError(f"rounding must be one of {sorted(ROUNDING)}, got {rounding!r}")
+    if stream is None:
+        done = _quick.tree(q, scale, out, lse, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, parents,
+                           max_seqlen_q, workspace, ROUNDING[rounding])
+        if done is not None:
+            return done
     dev = _current()
     qp, kp, vp = _in(q, "q", _bf16, dev), _in(k_pages, "k_pages", _bf16, dev), _in(v_pages, "v_pages", _bf16, dev)
     table, lens = _in(block_table, "block_table", _i32, dev), _in(seqlens_k, "seqlens_k", _i32, dev)
@@ -997,11 +1002,17 @@ def verify_tree(logits, tokens, parents, cu_seqlens, *, draft_logits=None, tempe
     (the root first) and the emitted tokens (those of the kept nodes after the root, and the last one).
     """
     lib = _lib or load()
+    if stream is None:
+        done = _quick.verify(logits, tokens, parents, cu_seqlens, draft_logits, temperature, uniforms, noise, max_seqlen,
+                             path, out_tokens, counts)
+        if done is not None:
+            return done
     dev = _current()
-    dtype = logits.dtype if isinstance(logits, torch.Tensor) and logits.dtype in _DTYPES else _bf16
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
-        raise TypeError("logits must be a CUDA tensor [total, vocab]")
-    shape = logits.shape
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dtype not in _DTYPES:
+        raise TypeError("logits must be a CUDA tensor of bfloat16 or float32")
+    dtype, shape = logits.dtype, logits.shape
+    if len(shape) != 2:
+        raise ValueError("logits must be [total, vocab]")
     total, vocab = shape
     lp, ls = _rows(logits, "logits", dtype, dev, shape)
     tok, par = _in(tokens, "tokens", _i32, dev), _in(parents, "parents", _i32, dev)
@@ -1046,6 +1057,10 @@ def compact_paged(k_pages, v_pages, block_table, seqlens_k, cu_seqlens, path, co
     (seqlens_out, which must not be seqlens_k).
     """
     lib = _lib or load()
+    if stream is None:
+        done = _quick.compact(k_pages, v_pages, block_table, seqlens_k, cu_seqlens, path, counts, total, seqlens_out)
+        if done is not None:
+            return done[0]
     dev = _current()
     kp, vp = _in(k_pages, "k_pages", _bf16, dev), _in(v_pages, "v_pages", _bf16, dev)
     table, lens = _in(block_table, "block_table", _i32, dev), _in(seqlens_k, "seqlens_k", _i32, dev)

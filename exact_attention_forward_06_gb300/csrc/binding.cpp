@@ -1,5 +1,5 @@
 // binding.cpp -- the quick way from Python into the operators around the paged
-// cache: one function per operator that looks at the tensors, makes the outputs and
+// cache and a tree of drafted tokens: one function per operator that looks at the tensors, makes the outputs and
 // calls the C ABI (attn.h).
 //
 // These operators run for 4 to 6 us on a decode step's few tokens, and ten tensors'
@@ -383,8 +383,135 @@ PyObject *fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// q, scale, out, lse, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, parents, max_seqlen_q, workspace, rounding
+PyObject *tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Reader r;
+    if (n != 13 || a[10] == Py_None) Py_RETURN_NONE;
+    Attention x(r, a);
+    if (!r.ok) Py_RETURN_NONE;
+    const at::Tensor *k = r.dense(a[4], BF16), *v = r.dense(a[5], BF16), *table = r.dense(a[6], I32);
+    const at::Tensor *lens = r.dense(a[7], I32), *cu = r.dense(a[8], I32), *parents = r.dense(a[9], I32);
+    if (!r.ok || k->dim() != 4 || v->sizes() != k->sizes() || k->size(3) != x.q->size(2) || table->dim() != 2)
+        Py_RETURN_NONE;
+    const int64_t B = lens->numel(), total = x.q->size(0), Hq = x.q->size(1);
+    if (cu->numel() != B + 1 || table->size(0) != B || parents->numel() != total) Py_RETURN_NONE;
+    x.lse_sizes(r, a[3], Hq, total);
+    const int b = r.narrow(B), hq = r.narrow(Hq), h = r.narrow(k->size(2)), t = r.narrow(total), d = r.narrow(x.q->size(2));
+    const int ps = r.narrow(k->size(1)), np = r.narrow(k->size(0)), mb = r.narrow(table->size(1));
+    const int longest = r.narrow(r.integer(a[10])), rounding = r.narrow(r.integer(a[12]));
+    if (!r.ok) Py_RETURN_NONE;
+    Output ws;
+    int64_t bytes = a[11] == Py_None ? std::max<int64_t>(1, (int64_t)attn_fwd_tree_paged_workspace_bytes(b, hq, h, d, longest)) : 0;
+    if (a[11] != Py_None) {
+        const at::Tensor *w = r.dense(a[11], U8);
+        bytes = w ? w->numel() : 0;
+        ws.ptr = at_of(w);
+    } else {
+        ws.take(r, a[11], U8, bytes, *k);
+    }
+    const auto ints = [](const at::Tensor *y) { return static_cast<const int32_t *>(y->data_ptr()); };
+    if (!r.ok || attn_fwd_tree_paged(x.q->data_ptr(), k->data_ptr(), v->data_ptr(), ints(table), ints(lens), ints(cu),
+                                     ints(parents), x.out.ptr, static_cast<float *>(x.lse.ptr), b, hq, h, t, longest, d, ps,
+                                     np, mb, x.scale, rounding, ws.ptr, (size_t)bytes, r.stream()) != ATTN_OK)
+        Py_RETURN_NONE;
+    return pair(x.out, x.lse);
+    END_HANDLE_TH_ERRORS
+}
+
+// A [rows, vocab] tensor whose rows are contiguous, and its row stride.
+struct Rows {
+    const at::Tensor *t = nullptr;
+    size_t stride = 0;
+
+    void read(Reader &r, PyObject *o, at::ScalarType type, int64_t rows, int64_t vocab) {
+        t = r.tensor(o, type);
+        r.ok = r.ok && t->dim() == 2 && t->size(0) == rows && t->size(1) == vocab && t->stride(1) == 1;
+        stride = !r.ok ? 0 : rows > 1 ? (size_t)t->stride(0) : (size_t)vocab;
+    }
+};
+
+// logits, tokens, parents, cu_seqlens, draft_logits, temperature, uniforms, noise, max_seqlen, path, out_tokens, counts
+PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Reader r;
+    if (n != 12 || a[8] == Py_None || !THPVariable_Check(a[0])) Py_RETURN_NONE;
+    const at::Tensor &l = THPVariable_Unpack(a[0]);
+    const at::ScalarType type = l.scalar_type();
+    if ((type != BF16 && type != F32) || l.dim() != 2) Py_RETURN_NONE;
+    const int64_t total = l.size(0), vocab = l.size(1);
+    Rows logits, draft, noise;
+    logits.read(r, a[0], type, total, vocab);
+    const at::Tensor *tokens = r.dense(a[1], I32), *parents = r.dense(a[2], I32), *cu = r.dense(a[3], I32);
+    if (!r.ok || tokens->numel() != total || parents->numel() != total) Py_RETURN_NONE;
+    const int64_t B = cu->numel() - 1;
+    const at::Tensor *temp = nullptr, *uniforms = nullptr;
+    if (a[5] != Py_None) {
+        temp = r.dense(a[5], F32);
+        uniforms = r.dense(a[6], F32);
+        noise.read(r, a[7], F32, B, vocab);
+        if (a[4] != Py_None) draft.read(r, a[4], type, total, vocab);
+        if (!r.ok || temp->numel() != B || uniforms->numel() != total) Py_RETURN_NONE;
+    } else if (a[4] != Py_None || a[6] != Py_None || a[7] != Py_None) {
+        Py_RETURN_NONE;
+    }
+    const int b = r.narrow(B), t = r.narrow(total), v = r.narrow(vocab), w = r.narrow(r.integer(a[8]));
+    if (!r.ok || b < 1) Py_RETURN_NONE;
+    const int64_t sizes[2] = {b, w};
+    Output path, out, counts;
+    path.take(r, a[9], I32, sizes, l);
+    out.take(r, a[10], I32, sizes, l);
+    counts.take(r, a[11], I32, at::IntArrayRef(sizes, 1), l);
+    const auto at4 = [](const at::Tensor *y) { return y ? static_cast<const float *>(y->data_ptr()) : nullptr; };
+    const auto ints = [](const at::Tensor *y) { return static_cast<const int32_t *>(y->data_ptr()); };
+    if (!r.ok || attn_verify_tree(l.data_ptr(), at_of(draft.t), type == BF16 ? ATTN_DTYPE_BF16 : ATTN_DTYPE_FP32, ints(tokens),
+                                  ints(parents), ints(cu), at4(temp), at4(uniforms), at4(noise.t),
+                                  static_cast<int32_t *>(path.ptr), static_cast<int32_t *>(out.ptr),
+                                  static_cast<int32_t *>(counts.ptr), b, t, v, w, logits.stride, draft.stride, noise.stride,
+                                  r.stream()) != ATTN_OK)
+        Py_RETURN_NONE;
+    PyObject *x = path.object(), *y = x ? out.object() : nullptr, *z = y ? counts.object() : nullptr;
+    PyObject *three = z ? PyTuple_Pack(3, x, y, z) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    Py_XDECREF(z);
+    return three;
+    END_HANDLE_TH_ERRORS
+}
+
+// k_pages, v_pages, block_table, seqlens_k, cu_seqlens, path, counts, total, seqlens_out.  Returns (seqlens_out,).
+PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Reader r;
+    if (n != 9) Py_RETURN_NONE;
+    const at::Tensor *k = r.dense(a[0], BF16), *v = r.dense(a[1], BF16), *table = r.dense(a[2], I32);
+    const at::Tensor *lens = r.dense(a[3], I32), *cu = r.dense(a[4], I32), *path = r.dense(a[5], I32);
+    const at::Tensor *counts = r.dense(a[6], I32);
+    if (!r.ok || (k->dim() != 4 && k->dim() != 5) || v->sizes() != k->sizes() || table->dim() != 2 || path->dim() != 2)
+        Py_RETURN_NONE;
+    const int64_t B = lens->numel(), at = k->dim() - 4;
+    if (table->size(0) != B || cu->numel() != B + 1 || path->size(0) != B || counts->numel() != B) Py_RETURN_NONE;
+    const int b = r.narrow(B), layers = at ? r.narrow(k->size(0)) : 1, np = r.narrow(k->size(at)), ps = r.narrow(k->size(at + 1));
+    const int h = r.narrow(k->size(at + 2)), d = r.narrow(k->size(at + 3)), mb = r.narrow(table->size(1));
+    const int w = r.narrow(path->size(1));
+    const int total = r.narrow(a[7] == Py_None ? std::max<int64_t>(1, B * path->size(1)) : r.integer(a[7]));
+    Output out;
+    out.take(r, a[8], I32, at::IntArrayRef(&B, 1), *k);
+    const auto ints = [](const at::Tensor *y) { return static_cast<const int32_t *>(y->data_ptr()); };
+    if (!r.ok || attn_compact_paged(k->data_ptr(), v->data_ptr(), ints(table), ints(lens), ints(cu), ints(path), ints(counts),
+                                    static_cast<int32_t *>(out.ptr), b, layers, h, total, w, d, ps, np, mb,
+                                    r.stream()) != ATTN_OK)
+        Py_RETURN_NONE;
+    PyObject *o = out.object();
+    PyObject *one = o ? PyTuple_Pack(1, o) : nullptr;
+    Py_XDECREF(o);
+    return one;
+    END_HANDLE_TH_ERRORS
+}
+
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(qk_norm_rope), METHOD(append), METHOD(gather), METHOD(decode), METHOD(fwd),
+                         METHOD(tree), METHOD(verify), METHOD(compact),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_quick", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
