@@ -224,6 +224,8 @@ attn_status_t fill_prefill_params(attn::PrefillParams *p, const DeviceInfo *di, 
     p->parents = nullptr;
     p->q = p->k_pool = p->v_pool = nullptr;
     p->part_rows = 0;
+    p->whole = 0;
+    p->unit_cost = 0;
     p->first = nullptr;
     return ATTN_OK;
 }
@@ -430,7 +432,7 @@ attn_status_t attn_fwd_tree_paged(const void *q, const void *k_pages, const void
     // The line of K/V tiles, and the rows of the merge, are 32-bit.
     const int pp = attn::tree_tile_positions(Hq / Hkv);
     const int64_t blocks = (max_seqlen_q + 2 * pp - 1) / (2 * pp), tiles = ((int64_t)max_blocks_per_seq + 7) / 8;
-    const int64_t line = (int64_t)Hkv * blocks * tiles, rows = (int64_t)max_seqlen_q * Hq;
+    const int64_t line = (int64_t)Hkv * blocks * (tiles + attn::kTreeCostTwo), rows = (int64_t)max_seqlen_q * Hq;
     if (line > 0x7fffffff / B || rows > 0x7fffffff / B) return ATTN_ERR_INVALID_ARG;
     const size_t need = attn_fwd_tree_paged_workspace_bytes(B, Hq, Hkv, d, max_seqlen_q);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need)
@@ -455,6 +457,8 @@ attn_status_t attn_fwd_tree_paged(const void *q, const void *k_pages, const void
     p.k_pool = k_pages;
     p.v_pool = v_pages;
     p.part_rows = attn::tree_part_rows(p.G, max_seqlen_q);
+    p.whole = tiles <= 2 ? 1 : 0;
+    p.unit_cost = max_seqlen_q > pp ? attn::kTreeCostTwo : attn::kTreeCostOne;
     size_t first, o, l;
     tree_workspace(B, p.G, max_seqlen_q, &first, &o, &l);
     uint8_t *ws = static_cast<uint8_t *>(workspace);

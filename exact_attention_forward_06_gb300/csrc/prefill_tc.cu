@@ -54,11 +54,13 @@
 // shows in O.  On unit-normal scores it fires on about 1 warp-tile in 10^4.
 // The rescale, when needed, is done by the softmax warp itself on its own 32
 // rows of O in tensor memory, after the previous P V product has completed.
+#include <algorithm>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "cache_ops.h"
 #include "common.cuh"
 #include "prefill_tc.h"
 
@@ -95,19 +97,21 @@ constexpr int ITEM_RING = 4;
 constexpr uint32_t ITEM_READERS = 2 + 8;
 // q_full[2], q_free[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[2], s_free[2],
 // p_full[2], o_full[2], fin, item_full[ITEM_RING], item_empty[ITEM_RING],
-// stage_ready[2], stage_taken[2]; behind them the tensor-memory slot, the abort
+// stage_ready[2], stage_taken[2], v_raw[NSLOT]; behind them the tensor-memory slot, the abort
 // flag, the item ring, the store commands and (trees) the flags of keys whose
 // values are not finite
-constexpr int NBARS = 2 + 2 + 2 * NSLOT + 2 + 2 + 2 + 2 + 1 + 2 * ITEM_RING + 2 + 2;
-constexpr uint32_t SMEM_MISC = 768;
+constexpr int NBARS = 2 + 2 + 2 * NSLOT + 2 + 2 + 2 + 2 + 1 + 2 * ITEM_RING + 2 + 2 + NSLOT;
+constexpr uint32_t SMEM_MISC = 896;
 constexpr uint32_t SMEM_ALIGN = 1024;
 constexpr float RESCALE_LOG2 = 8.0f;  // move the running max past a 2^8 growth (and see softmax_wg)
 constexpr float LN2 = 0.6931471805599453f;
 
-// A tree's keys lie in at most three K/V tiles; a flag for each of a tile's 128 keys, per softmax group.
+// A tree's keys lie in at most three K/V tiles; a flag for each of a tile's 128 keys, for the
+// last TREE_UNITS units (see tree_cleaner).
+constexpr int TREE_UNITS = 4;
 constexpr int TREE_TILES = (kTreeMaxNodes + BN - 2) / BN + 1;
 static_assert(TREE_TILES == 3, "a tree's keys begin anywhere in their first tile");
-static_assert(NBARS * 8 + 8 + 64 * ITEM_RING + 2 * 32 + 2 * TREE_TILES * 16 <= SMEM_MISC, "barrier area too small");
+static_assert(NBARS * 8 + 8 + 64 * ITEM_RING + 2 * 32 + TREE_UNITS * TREE_TILES * 16 <= SMEM_MISC, "barrier area too small");
 
 constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, 128, 0, 0);   // Q K^T: both K-major
 constexpr uint32_t IDESC_PV = ptx::idesc_bf16_f32(128, 128, 0, 1);  // P V: V is N(d)-major
@@ -155,9 +159,12 @@ struct SmemLayout {
     __device__ volatile int *stage_cmd(int t) const {
         return reinterpret_cast<volatile int *>(bars + NBARS + 1) + 16 * ITEM_RING + 8 * t;
     }
-    // Keys of tree tile i whose values are not finite, as group t found them (four words).
-    __device__ volatile uint32_t *odd_keys(int t, int i) const {
-        return reinterpret_cast<volatile uint32_t *>(bars + NBARS + 1) + 16 * ITEM_RING + 16 + (t * TREE_TILES + i) * 4;
+    // v_raw(s): a tree's V tile has landed in slot s and is to be cleaned (tree_cleaner).
+    __device__ uint64_t *v_raw(int s) const { return bars + 17 + 2 * NSLOT + 2 * ITEM_RING + s; }
+    // Keys of tree tile i of unit u whose values are not finite (four words).
+    __device__ volatile uint32_t *odd_keys(int u, int i) const {
+        return reinterpret_cast<volatile uint32_t *>(bars + NBARS + 1) + 16 * ITEM_RING + 16 +
+               (u % TREE_UNITS * TREE_TILES + i) * 4;
     }
     __device__ uint8_t *q_tile(int t) const { return base + (t ? SMEM_Q1 : SMEM_Q0); }
     // Ring slot s: a K or V tile, or a tile's output staging area.
@@ -399,9 +406,11 @@ __device__ __forceinline__ Unit next_unit(const PrefillParams &p, bool first) {
 
 // ---- trees of drafted tokens: equal shares of all K/V tiles
 
-// One sequence's part of the line of K/V tiles: Hkv x row blocks x tiles.
+// One sequence's part of the line: Hkv x row blocks x (K/V tiles and a unit's cost).
 struct TreeSeq {
-    int q0, Sq, Sk, blocks, tiles, work;
+    int q0, Sq, Sk, blocks, tiles;
+    int span;  // places of a unit on the line
+    int work;
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const PrefillParams &p, int b, bool report) {
@@ -416,21 +425,30 @@ __device__ __forceinline__ TreeSeq tree_seq(const PrefillParams &p, int b, bool 
     s.Sk = bad ? 0 : Lk;
     s.blocks = (s.Sq + 2 * p.pack_pos - 1) / (2 * p.pack_pos);
     s.tiles = (s.Sk + BN - 1) / BN;
-    s.work = p.Hkv * s.blocks * s.tiles;
+    s.span = p.whole ? 1 : s.tiles + p.unit_cost;
+    s.work = p.Hkv * s.blocks * s.span;
     return s;
 }
 
-// How many CTAs share a line of `total` tiles, and where CTA c's share begins.
-__device__ __forceinline__ int tree_shares(int ctas, int total) { return min(ctas, max(total, 1)); }
-__device__ __forceinline__ int tree_share_begin(int c, int shares, int total) {
-    return (int)((int64_t)c * total / shares);
-}
-// The CTA whose share holds tile x.
-__device__ __forceinline__ int tree_share_of(int x, int shares, int total) {
-    return (int)((((int64_t)x + 1) * shares - 1) / total);
-}
+// The line in equal shares, the first `more` of them one place longer.  On it a unit
+// has `unit_cost` places, for what it takes besides its tiles, and then its tiles: a
+// share has the tiles whose places lie in it.
+struct TreeLine {
+    int shares, each, more;
+    __device__ __forceinline__ TreeLine(int ctas, int total) {
+        shares = min(ctas, max(total, 1));
+        each = total / shares;
+        more = total - each * shares;
+    }
+    __device__ __forceinline__ int begin(int c) const { return c * each + min(c, more); }
+    // The CTA whose share holds place x.
+    __device__ __forceinline__ int of(int x) const {
+        const int longer = more * (each + 1);
+        return x < longer ? x / (each + 1) : more + (x - longer) / each;
+    }
+};
 
-// What is left of a CTA's share: `left` tiles from tile `at` of sequence b on.
+// What is left of a CTA's share: `left` places from place `at` of sequence b on.
 struct TreeShare {
     int b, at, left;
     bool begun;  // a segment of it has been handed out
@@ -440,19 +458,22 @@ struct TreeShare {
 __device__ __forceinline__ TreeShare tree_share(const PrefillParams &p, int lane) {
     constexpr unsigned ALL = 0xffffffffu;
     const bool writer = blockIdx.x == 0;
-    int total = 0;
-    for (int b = lane; b < p.B; b += 32) total += tree_seq(p, b, writer).work;
+    int total = 0, first_work = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        const int work = tree_seq(p, b, writer).work;
+        if (b == lane) first_work = work;
+        total += work;
+    }
     total = __reduce_add_sync(ALL, total);
-    const int shares = tree_shares(gridDim.x, total);
+    const TreeLine line(gridDim.x, total);
     TreeShare sh{0, 0, 0, false};
-    const bool mine = (int)blockIdx.x < shares && total > 0;
-    const int lo = mine ? tree_share_begin(blockIdx.x, shares, total) : 0;
-    const int hi = mine ? tree_share_begin(blockIdx.x + 1, shares, total) : 0;
-    sh.left = hi - lo;
+    const bool mine = (int)blockIdx.x < line.shares;
+    const int lo = mine ? line.begin(blockIdx.x) : 0;
+    sh.left = mine ? line.begin(blockIdx.x + 1) - lo : 0;
     int base = 0;
     bool found = sh.left == 0;
     for (int b0 = 0; b0 < p.B && (writer || !found); b0 += 32) {
-        const int work = b0 + lane < p.B ? tree_seq(p, b0 + lane, false).work : 0;
+        const int work = b0 == 0 ? first_work : b0 + lane < p.B ? tree_seq(p, b0 + lane, false).work : 0;
         int incl = work;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -485,14 +506,20 @@ __device__ __forceinline__ Unit tree_next(const PrefillParams &p, TreeShare &sh)
             ++sh.b;
             continue;
         }
-        const int unit = sh.at / s.tiles;
+        const int unit = sh.at / s.span, cost = s.span - s.tiles;
+        // The unit's tiles whose places lie in the share (cost < 0: units are places).
+        const int from = sh.at - unit * s.span, to = min(s.span, from + sh.left);
+        sh.at += to - from;
+        sh.left -= to - from;
+        w.j_lo = p.whole ? 0 : max(from - cost, 0);
+        const int n = (p.whole ? s.tiles : to - cost) - w.j_lo;
+        if (n <= 0) continue;
+        w.n_kv = n;
         w.b = sh.b;
         w.g = unit / s.blocks;
         w.h[0] = w.h[1] = w.g * p.G;
         w.s0[0] = unit % s.blocks * 2 * p.pack_pos;
         w.s0[1] = w.s0[0] + p.pack_pos;
-        w.j_lo = sh.at - unit * s.tiles;
-        w.n_kv = min(s.tiles - w.j_lo, sh.left);
         // A unit that other CTAs share is the first or the last segment of a share.
         w.part = w.n_kv == s.tiles ? -1 : (sh.begun ? 1 : 0);
         w.ws_row = ((int)blockIdx.x * 2 + max(w.part, 0)) * p.part_rows;
@@ -500,37 +527,51 @@ __device__ __forceinline__ Unit tree_next(const PrefillParams &p, TreeShare &sh)
         w.Sk = s.Sk;
         w.q0 = s.q0;
         sh.begun = true;
-        sh.at += w.n_kv;
-        sh.left -= w.n_kv;
         break;
     }
     return w;
 }
 
 // Which keys of the tile at kbase token `pos` of a tree sees: the keys before
-// the tree, itself and its ancestors.  One step up the tree is one load (from
-// L1 after the first); parents lie before their children, which bounds the walk.
-__device__ __forceinline__ void tree_visible(const PrefillParams &p, const Unit &w, int pos, bool valid, int kbase,
-                                             uint32_t (&vis)[4]) {
+// the tree, itself and its ancestors.  The whole warp takes part: a step of the
+// walk up goes to the start of a run of tokens in a row, each the next one's
+// parent (found in a ballot; runs end at multiples of 32), and one load further to
+// that token's parent, so a chain takes no more steps than a bush is deep.
+// Parents lie before their children, which bounds the walk.
+__device__ __forceinline__ void tree_visible(const PrefillParams &p, const Unit &w, int pos, bool valid, int lane,
+                                             int kbase, uint32_t (&vis)[4]) {
     const int base = w.Sk - w.Sq;
-    const int before = valid ? min(max(base - kbase, 0), BN) : 0;
+    uint32_t starts[kTreeMaxNodes / 32];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int n = min(max(before - 32 * i, 0), 32);
-        vis[i] = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+    for (int i = 0; i < kTreeMaxNodes / 32; ++i) {
+        starts[i] = 0;
+        if (32 * i < w.Sq) {
+            const int a = 32 * i + lane;
+            starts[i] = __ballot_sync(0xffffffffu, a >= w.Sq || p.parents[w.q0 + a] != a - 1);
+        }
     }
-    for (int a = valid ? pos : -1; a >= 0;) {
-        const int key = base + a - kbase;
-        if (key < 0) break;
-        if (key < BN) {
+    // Bits lo .. hi of the tile's 128 (hi may lie behind them, lo before them).
+    auto see = [&](int lo, int hi) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) vis[i] |= (key >> 5) == i ? 1u << (key & 31) : 0u;
+        for (int i = 0; i < 4; ++i) {
+            const int l = max(lo - 32 * i, 0), h = min(hi - 32 * i, 31);
+            if (l <= h) vis[i] |= (0xffffffffu >> (31 - h)) & (0xffffffffu << l);
         }
-        const int up = p.parents[w.q0 + a];
-        if (up >= a || up < -1) {
-            report_status(p.status, kStatusDeviceBounds, kSiteTreeParent);
-            break;
-        }
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) vis[i] = 0;
+    if (!valid) return;
+    see(0, base - kbase - 1);
+    for (int a = pos; base + a >= kbase;) {
+        uint32_t word = 0;
+#pragma unroll
+        for (int i = 0; i < kTreeMaxNodes / 32; ++i) word = (a >> 5) == i ? starts[i] : word;
+        word &= 0xffffffffu >> (31 - (a & 31));
+        const int first = (a & ~31) + (word ? 31 - __clz(word) : 0);
+        see(base + first - kbase, base + a - kbase);
+        const int up = p.parents[w.q0 + first];
+        if (up >= first || up < -1) report_status(p.status, kStatusDeviceBounds, kSiteTreeParent);
+        if (up >= first || up < 0) break;
         a = up;
     }
 }
@@ -579,8 +620,12 @@ __device__ __forceinline__ bool read_unit(const SmemLayout &sm, const WaitCtx &w
     return true;
 }
 
-// Ring items of a unit: its K/V tiles, then one output staging slot per Q tile.
-__device__ __forceinline__ int ring_items(const Unit &w) { return 2 * w.n_kv + 2; }
+// Ring items of a unit: its K/V tiles, then one output staging slot per Q tile
+// (a tree's rows go to memory from registers).
+template <int KIND>
+__device__ __forceinline__ int ring_items(const Unit &w) {
+    return 2 * w.n_kv + (KIND == kTree ? 0 : 2);
+}
 
 // ------------------------------------------------------------------ producer
 
@@ -644,7 +689,7 @@ __device__ void producer(const PrefillParams &p, const SmemLayout &sm, const Wai
         if (!ok) break;
         nx = next_unit<KIND>(p, false);
         if (p.prefetch_ahead > 0) prefetch_q(p, mq, nx);
-        const int total = ring_items(w);
+        const int total = ring_items<KIND>(w);
         for (int i = 0; i < total; ++i) {
             const int slot = n % NSLOT;
             if (n >= NSLOT && !wait_bounded(sm.kv_empty(slot), ((n / NSLOT) - 1) & 1, wc, kSiteProducerEmpty)) {
@@ -726,29 +771,43 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
         };
         int next_phys = -1;
         if (lane < BN / 16 && total > 0) next_phys = table_entry(0);
-        if (lane == 0) {
-            for (int t = 0; t < 2 && ok; ++t) {
-                if (qn[t] > 0 && !wait_bounded(sm.q_free(t), (qn[t] - 1) & 1, wc, kSiteProducerQ)) {
-                    ok = false;
-                    break;
+        // Q, once the previous unit's last S product has read its buffer, and the next
+        // unit while it loads.
+        auto load_q = [&]() {
+            if (lane == 0) {
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (qn[t] > 0 && !wait_bounded(sm.q_free(t), (qn[t] - 1) & 1, wc, kSiteProducerQ)) {
+                        ok = false;
+                        break;
+                    }
+                    if (KIND == kTree && t == 1 && w.s0[1] >= w.Sq) {
+                        ptx::mbar_arrive(sm.q_full(t));  // no rows: nothing reads the tile
+                    } else {
+                        // (a tree's tile is one box of pack_pos positions x G heads)
+                        ptx::mbar_arrive_expect_tx(sm.q_full(t), KIND == kTree ? p.pack_pos * p.G * D * 2 : TILE_BYTES);
+                        load_tile(mq, sm.q_tile(t), sm.q_full(t), p.bhsd, t ? w.h[1] : w.h[0],
+                                  w.q0 + (t ? w.s0[1] : w.s0[0]), w.tb, pol_q);
+                    }
+                    ++qn[t];
                 }
-                if (KIND == kTree && t == 1 && w.s0[1] >= w.Sq) {
-                    ptx::mbar_arrive(sm.q_full(t));  // no rows: nothing reads the tile
-                } else {
-                    // (a tree's tile is one box of pack_pos positions x G heads)
-                    ptx::mbar_arrive_expect_tx(sm.q_full(t), KIND == kTree ? p.pack_pos * p.G * D * 2 : TILE_BYTES);
-                    load_tile(mq, sm.q_tile(t), sm.q_full(t), p.bhsd, t ? w.h[1] : w.h[0],
-                              w.q0 + (t ? w.s0[1] : w.s0[0]), w.tb, pol_q);
-                }
-                ++qn[t];
+                if (ok) nx = next(false);
             }
-            if (ok) nx = next(false);  // the next unit while this one's Q loads
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        };
+        // A tree's units follow one another in a CTA, and waiting for Q first would let
+        // the ring run empty at each.  Its first three K/V items take slots that the
+        // previous unit frees whatever Q does; the fourth takes the last K tile's, and is
+        // free when Q is.
+        const int q_at = KIND == kTree && u > 1 ? min(3, total) : 0;
+        if (q_at == 0) {
+            load_q();
+            if (!ok) break;
         }
-        if (!__shfl_sync(0xffffffffu, ok, 0)) {
-            ok = false;
-            break;
-        }
-        for (int i = 0; i < total + 2; ++i) {
+        for (int i = 0; i < ring_items<KIND>(w); ++i) {
+            if (KIND == kTree && q_at > 0 && i == q_at) {
+                load_q();
+                if (!ok) break;
+            }
             const int slot = n % NSLOT;
             if (i < total && (i & 1) == 0 && lane < BN / 16) {
                 const int page = (w.j_lo + (i >> 1)) * (BN / 16) + lane;
@@ -758,14 +817,18 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
                 if (!ok_page && page < n_pages) report_status(p.status, kStatusDeviceBounds, kSitePagedTable);
                 page_row = ok_page ? phys * 16 : p.num_pages * 16;
             }
+            // (values of a tree's keys land for the cleaner, which passes them on)
+            uint64_t *full = KIND == kTree && i < total && (i & 1) && (w.j_lo + (i >> 1) + 1) * BN > w.Sk - w.Sq
+                                 ? sm.v_raw(slot)
+                                 : sm.kv_full(slot);
             bool got = true;
             if (lane == 0) {
                 got = n < NSLOT || wait_bounded(sm.kv_empty(slot), ((n / NSLOT) - 1) & 1, wc, kSiteProducerEmpty);
                 if (got) {
                     if (i < total)
-                        ptx::mbar_arrive_expect_tx(sm.kv_full(slot), TILE_BYTES);
+                        ptx::mbar_arrive_expect_tx(full, TILE_BYTES);
                     else
-                        ptx::mbar_arrive(sm.kv_full(slot));  // an output staging slot
+                        ptx::mbar_arrive(full);  // an output staging slot
                 }
             }
             if (!__shfl_sync(0xffffffffu, got, 0)) {
@@ -784,15 +847,16 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
                 // a page is one 4 KiB box at group page_row / 8, a run one box of 16.
                 if (run) {
                     if (lane == 0)
-                        ptx::tma_load_5d_hint(sm.slot(slot), (i & 1) ? mv8 : mk8, sm.kv_full(slot), 0, 0, 0,
+                        ptx::tma_load_5d_hint(sm.slot(slot), (i & 1) ? mv8 : mk8, full, 0, 0, 0,
                                               page_row / 8, w.g, pol_kv);
                 } else if (lane < BN / 16) {
-                    ptx::tma_load_5d_hint(sm.slot(slot) + lane * PAGE_BOX_BYTES, (i & 1) ? mv : mk, sm.kv_full(slot),
+                    ptx::tma_load_5d_hint(sm.slot(slot) + lane * PAGE_BOX_BYTES, (i & 1) ? mv : mk, full,
                                           0, 0, 0, page_row / 8, w.g, pol_kv);
                 }
             }
             ++n;
         }
+        if (KIND == kTree && ok && q_at == total) load_q();  // (a unit of one tile)
         if (lane == 0) w = nx;
     }
     // On the way out make sure no copy is still writing into shared memory.
@@ -800,6 +864,62 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
         for (int t = 0; t < 2; ++t)
             if (qn[t] > 0) drain_wait(sm.q_full(t), (qn[t] - 1) & 1, wc);
         for (int i = max(0, n - NSLOT); i < n; ++i) drain_wait(sm.kv_full(i % NSLOT), (i / NSLOT) & 1, wc);
+    }
+}
+
+// Cleans the V tiles of a tree's keys (one warp; in kTree it has no output stores
+// to issue).  Slots past the sequence's end hold whatever the page holds: their P
+// is 0, but 0 times NaN is NaN, so the rows become zeros.  A key of the tree is
+// hidden from some rows and seen by others: where its values are not all finite,
+// they are taken out as well, and added in the epilogue to the rows that see the
+// key (odd_keys).  Then the tile goes on to the products, as kv_full.
+// The flags of a unit stay until both softmax groups are done with it, TREE_UNITS
+// units later: with units of one tile, the copy of V(u + 4) takes the slot of K(u + 2),
+// which is free once S_0(u + 2) has been computed, for which group 1 has loaded its
+// scores of unit u + 1 (and group 0, for S_1(u + 1), before it).
+__device__ void tree_cleaner(const SmemLayout &sm, const WaitCtx &wc, int lane) {
+    int nb = 0;           // ring number of the unit's first K/V item
+    uint32_t phases = 0;  // bit s: parity of v_raw(s)
+    for (int u = 0;; ++u) {
+        Unit w;
+        const bool got = read_unit(sm, wc, u, false, w);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(sm.item_empty(u % ITEM_RING));
+        if (!got || w.n_kv < 0) return;
+        const int tree0 = w.Sk - w.Sq;
+        for (int j = max(tree0 / BN - w.j_lo, 0); j < w.n_kv; ++j) {
+            const int slot = (nb + 2 * j + 1) % NSLOT;
+            if (!warp_wait_bounded(sm.v_raw(slot), phases >> slot & 1u, wc, kSiteSoftmaxV)) return;
+            phases ^= 1u << slot;
+            const int kbase = (w.j_lo + j) * BN;
+            uint8_t *vt = sm.slot(slot);
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                const int r = q * 32 + lane, key = kbase + r;
+                uint8_t *row = vt + (r >> 3) * PG_GROUP_BYTES + (r & 7) * 128;
+                bool odd = false;
+                if (key >= tree0 && key < w.Sk) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {  // (in an order that keeps the lanes' rows in different banks)
+                        const uint4 x = *reinterpret_cast<const uint4 *>(row + (c >> 3) * PG_HALF_BYTES +
+                                                                         (((c & 7) ^ (r & 7)) << 4));
+                        odd = odd || odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w);
+                    }
+                }
+                if (odd || key >= w.Sk) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        *reinterpret_cast<uint4 *>(row + (c >> 3) * PG_HALF_BYTES + (((c & 7) ^ (r & 7)) << 4)) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                }
+                const uint32_t all = __ballot_sync(0xffffffffu, odd);
+                if (lane == 0) sm.odd_keys(u, kbase / BN - tree0 / BN)[q] = all;
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sm.kv_full(slot));
+        }
+        nb += ring_items<kTree>(w);
     }
 }
 
@@ -851,8 +971,9 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem_o, uint32_t tmem_p, uint6
 // product that reads it).  After a unit's last S product the stream commits
 // q_free[t]: once that product has completed, Q_t may be replaced by the next
 // unit's, while this unit's last softmax, P V and output still run.
-template <int T, bool PAGED>
+template <int T, int KIND>
 __device__ void mma_stream(const PrefillParams &p, const SmemLayout &sm, const WaitCtx &wc, uint32_t tmem_base) {
+    constexpr bool PAGED = KIND == kPaged || KIND == kTree;
     const uint64_t q_desc = ptx::desc_kmajor_sw128(ptx::smem_addr(sm.q_tile(T)));
     const uint32_t slot0 = ptx::smem_addr(sm.slot(0));
     auto slot_of = [](int n) { return n % NSLOT; };
@@ -945,7 +1066,7 @@ __device__ void mma_stream(const PrefillParams &p, const SmemLayout &sm, const W
                 if (!do_pv(j)) return;
             }
         }
-        nb += ring_items(w);
+        nb += ring_items<KIND>(w);
         g0 += w.n_kv;
     }
 }
@@ -990,25 +1111,6 @@ __device__ __forceinline__ float softmax_tile(const float2 (&s)[64], uint32_t (&
     return a.x + a.y;
 }
 
-// The same with a bit for each key that the row sees.
-__device__ __forceinline__ float softmax_tile_bits(const float2 (&s)[64], uint32_t (&pk)[64], float scale_log2,
-                                                   float m_sub, const uint32_t (&vis)[4]) {
-    const float2 c2 = make_float2(scale_log2, scale_log2);
-    const float2 n2 = make_float2(-m_sub, -m_sub);
-    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-    for (int i = 0; i < 64; ++i) {
-        const float2 t = __ffma2_rn(s[i], c2, n2);
-        float2 pp;
-        pp.x = vis[i >> 4] >> (2 * i & 31) & 1u ? ptx::ex2(t.x) : 0.f;
-        pp.y = vis[i >> 4] >> (2 * i + 1 & 31) & 1u ? ptx::ex2(t.y) : 0.f;
-        acc[i & 1] = __fadd2_rn(acc[i & 1], pp);
-        pk[i] = ptx::pack_bf16x2(pp.x, pp.y);
-    }
-    const float2 a = __fadd2_rn(acc[0], acc[1]);
-    return a.x + a.y;
-}
-
 // Output stores of tile t, one lane of an otherwise idle control warp: for
 // each command of softmax group t, the TMA store of the staged tile (both
 // 64-column halves), then, once the store has read the slot, the slot goes
@@ -1045,15 +1147,15 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
 }
 
 // The part of an output row that a tree's rows get from keys whose values are not
-// finite (see odd_key in softmax_wg): columns c0 .. c0 + 31 of row `pos` of `head`,
-// added to o.  Rare, so one key after the other in plain arithmetic.
-__device__ __forceinline__ void tree_add_odd(const PrefillParams &p, const SmemLayout &sm, const Unit &w, int t, int pos,
-                                          int head, float m_run, int c0, float (&o)[32]) {
+// finite (see tree_cleaner), added to o.  Rare, so one key after the other in plain
+// arithmetic.
+__device__ __forceinline__ void tree_add_odd(const PrefillParams &p, const SmemLayout &sm, const Unit &w, int u, int pos,
+                                             int head, float m_run, float *o) {
     const int base = w.Sk - w.Sq;
     for (int a = pos; a >= 0;) {
         const int key = base + a, tile = key / BN;
         if (tile < w.j_lo) break;
-        if (tile < w.j_lo + w.n_kv && sm.odd_keys(t, tile - base / BN)[key % BN / 32] >> (key % 32) & 1u) {
+        if (tile < w.j_lo + w.n_kv && sm.odd_keys(u, tile - base / BN)[key % BN / 32] >> (key % 32) & 1u) {
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((int64_t)(w.q0 + pos) * p.Hq + head) * D;
             const auto *k = reinterpret_cast<const __nv_bfloat16 *>(tree_row(p, w, p.k_pool, key));
             const auto *v = reinterpret_cast<const __nv_bfloat16 *>(tree_row(p, w, p.v_pool, key));
@@ -1061,8 +1163,8 @@ __device__ __forceinline__ void tree_add_odd(const PrefillParams &p, const SmemL
 #pragma unroll 1
             for (int c = 0; c < D; ++c) x = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), x);
             const float pr = ptx::ex2(x * p.scale_log2 - (m_run == -INFINITY ? 0.f : m_run));
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = fmaf(pr, __bfloat162float(v[c0 + c]), o[c]);
+#pragma unroll 1
+            for (int c = 0; c < D; ++c) o[c] = fmaf(pr, __bfloat162float(v[c]), o[c]);
         }
         const int up = p.parents[w.q0 + a];
         if (up >= a || up < -1) break;
@@ -1070,76 +1172,68 @@ __device__ __forceinline__ void tree_add_odd(const PrefillParams &p, const SmemL
     }
 }
 
-// Epilogue of a tree's tile: whole rows to out and lse, or a share's part of them
-// (normalised, with the log-sum-exp) to the workspace.  A thread holds a row; the
-// warp turns its 32 rows round in its part of the staging slot, 128 bytes a row at
-// a time, so that a store covers whole lines.
-__device__ __forceinline__ void tree_epilogue(const PrefillParams &p, const SmemLayout &sm, const Unit &w, uint32_t tO,
-                                              int t, int quarter, int lane, int pos, int head, bool valid, bool dead,
-                                              bool has_tree, float m_run, float l_run, uint8_t *stage, bool ok) {
-    if (dead) return;  // (the whole warp)
-    const int r = quarter * 32 + lane;
-    bool any_odd = false;
-    if (has_tree) {
-        const int first = (w.Sk - w.Sq) / BN;
-        for (int i = max(first, w.j_lo); i < w.j_lo + w.n_kv; ++i)
-            for (int k = 0; k < 4; ++k) any_odd = any_odd || sm.odd_keys(t, i - first)[k] != 0;
-    }
+// Epilogue of a warp's 32 rows of a tree's tile, a row a thread: whole rows to out and
+// lse, or a share's part of them (normalised, with the log-sum-exp) to the workspace.
+// A thread stores 32 bytes at a time, a whole sector, so nothing has to be turned round
+// in shared memory first; a part's 16 column groups of 8 are apart there, which puts the
+// warp's 32 sectors in a row.
+__device__ __forceinline__ void tree_epilogue(const PrefillParams &p, const SmemLayout &sm, const Unit &w, int u, uint32_t tO,
+                                              int pos, int head, bool valid, int lane, int row, float m_run, float l_run) {
+    uint32_t odd = 0;  // (of all the tree's tiles in this segment)
+    for (int first = (w.Sk - w.Sq) / BN, i = max(first, w.j_lo); i < w.j_lo + w.n_kv; ++i)
+        if (lane < 4) odd |= sm.odd_keys(u, i - first)[lane];
+    const bool any_odd = __any_sync(0xffffffffu, odd != 0);
     ptx::tc_fence_after();
+    uint32_t o[4][32];
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld32(tO + ch * 32, o[ch]);
+    ptx::tmem_wait_ld();
+    // The group's next P V product overwrites O, after its next P.
+    ptx::tc_fence_before();
     // An empty row (no key of this share) gives zeros; NaN stays NaN.
-    const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
-    const float lse = l_run == 0.f ? -INFINITY : (m_run + ptx::lg2(l_run)) * LN2;
-    const bool part = w.part >= 0;
-    uint8_t *mine = stage + quarter * 32 * 128;  // 32 rows x 128 bytes, 16-byte chunks swizzled by row
-    const unsigned rows = __ballot_sync(0xffffffffu, valid && ok);
-    // bf16: 64 columns a turn; fp32: 32
-#pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
-        uint32_t o[32];
-        ptx::tmem_ld32(tO + ch * 32, o);
-        ptx::tmem_wait_ld();
-        float f[32];
+    const bool empty = l_run == 0.f;
+    const float inv = empty ? 0.f : 1.0f / l_run;
+    const float lse = empty ? -INFINITY : (m_run + ptx::lg2(l_run)) * LN2;
+    if (!valid) return;
+    if (any_odd) {
+        float f[D];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] = l_run == 0.f ? 0.f : __uint_as_float(o[i]);
-        if (any_odd && valid) tree_add_odd(p, sm, w, t, pos, head, m_run, ch * 32, f);
-        if (part) {
+        for (int c = 0; c < D; ++c) f[c] = __uint_as_float(o[c >> 5][c & 31]);
+        tree_add_odd(p, sm, w, u, pos, head, m_run, f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<float4 *>(mine + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-                    make_float4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[i] = pack_bf16x2_mode(f[8 * k + 2 * i] * inv, f[8 * k + 2 * i + 1] * inv, p.round_mode);
-                const int c = (ch & 1) * 4 + k;
-                *reinterpret_cast<uint4 *>(mine + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-            }
-            if ((ch & 1) == 0) continue;
-        }
-        __syncwarp();
-        // eight lanes a row, four rows at a time
-#pragma unroll
-        for (int it = 0; it < 8; ++it) {
-            const int row = it * 4 + (lane >> 3), c = lane & 7;
-            const int row_pos = __shfl_sync(0xffffffffu, pos, row), row_head = __shfl_sync(0xffffffffu, head, row);
-            if (!(rows >> row & 1u)) continue;
-            const uint4 x = *reinterpret_cast<const uint4 *>(mine + row * 128 + ((c ^ (row & 7)) << 4));
-            if (part)
-                reinterpret_cast<uint4 *>(p.ws_o + (int64_t)(w.ws_row + t * BM + quarter * 32 + row) * D + ch * 32)[c] = x;
-            else
-                reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                          ((int64_t)(w.q0 + row_pos) * p.Hq + row_head) * D + (ch >> 1) * 64)[c] = x;
-        }
-        __syncwarp();
+        for (int c = 0; c < D; ++c) o[c >> 5][c & 31] = __float_as_uint(f[c]);
     }
-    if (!valid || !ok) return;
-    if (part)
-        p.ws_lse[w.ws_row + t * BM + r] = lse;
-    else if (p.lse != nullptr)
-        p.lse[(int64_t)head * p.total_q + w.q0 + pos] = lse;
+#pragma unroll
+    for (int c = 0; c < D; ++c) o[c >> 5][c & 31] = empty ? 0u : __float_as_uint(__uint_as_float(o[c >> 5][c & 31]) * inv);
+    if (w.part >= 0) {
+        float *dst = p.ws_o + (int64_t)w.ws_row * D + row * 8;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            uint32_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = o[k >> 2][(k & 3) * 8 + i];
+            ptx::store_32(dst + (int64_t)k * p.part_rows * 8, x);
+        }
+        p.ws_lse[w.ws_row + row] = lse;
+        return;
+    }
+    uint4 *dst = static_cast<uint4 *>(p.out) + ((int64_t)(w.q0 + pos) * p.Hq + head) * (D / 8);
+    const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        uint32_t x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = pack_bf16x2_mode(__uint_as_float(o[k >> 1][(k & 1) * 16 + 2 * i]),
+                                    __uint_as_float(o[k >> 1][(k & 1) * 16 + 2 * i + 1]), p.round_mode);
+        if (wide) {
+            ptx::store_32(dst + 2 * k, x);
+        } else {
+            dst[2 * k] = make_uint4(x[0], x[1], x[2], x[3]);
+            dst[2 * k + 1] = make_uint4(x[4], x[5], x[6], x[7]);
+        }
+    }
+    if (p.lse != nullptr) p.lse[(int64_t)head * p.total_q + w.q0 + pos] = lse;
 }
 
 template <int KIND>
@@ -1153,7 +1247,8 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
     const uint32_t tS = lanes + TM_S;     // shared score buffer
     const uint32_t tP = lanes + tm_p(t);  // this tile's bf16 P
     const uint32_t tO = lanes + tm_o(t);  // this tile's O accumulator
-    const float sl2 = p.scale_log2;
+    // (a tree's hidden scores become -inf, which a factor of 0 would make NaN)
+    const float sl2 = TREE ? fmaxf(p.scale_log2, 1e-30f) : p.scale_log2;
     int nb = 0;  // ring number of the unit's first K/V item
     int g0 = 0;  // running index of the unit's first score tile
     const bool leader = quarter == 0 && lane == 0;
@@ -1204,56 +1299,7 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
         // stream issues no products either) and stores nothing.  Of a tree's
         // tile, which is often part full, the same goes for a warp's 32 rows.
         const bool dead = TREE ? !__any_sync(0xffffffffu, valid) : s0 >= w.Sq;
-        const bool dead_tile = s0 >= w.Sq;
         const int tree0 = w.Sk - w.Sq;  // the tree's first key
-        const bool has_tree = TREE && !dead_tile && (w.j_lo + w.n_kv) * BN > tree0;
-        // Last tile of a packed or paged sequence: the V rows past its end hold
-        // other data (the next sequence's rows, or whatever a page's unused slots
-        // contain).  Their P is 0, but 0 * NaN is NaN, so each group zeroes those
-        // rows in shared memory once the tile has landed, before releasing its P
-        // (the two streams' P V products are not ordered; both groups write the
-        // same zeros).  `also`: this thread's row is zeroed wherever it lies.
-        auto blank_rows = [&](int j, bool also) -> bool {
-            const int item = nb + 2 * j + 1;
-            uint8_t *vt = sm.slot(item % NSLOT);
-            if (!wait_bounded(sm.kv_full(item % NSLOT), (uint32_t)((item / NSLOT) & 1), wc, kSiteSoftmaxV))
-                return false;
-            if ((w.j_lo + j) * BN + r >= w.Sk || also) {
-                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                // row r, both halves (dense or paged tile layout)
-                uint8_t *h0 = PAGED ? vt + (r >> 3) * PG_GROUP_BYTES + (r & 7) * 128 : vt + r * 128;
-                uint8_t *h1 = h0 + (PAGED ? PG_HALF_BYTES : HALF_BYTES);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    reinterpret_cast<uint4 *>(h0)[c] = z;
-                    reinterpret_cast<uint4 *>(h1)[c] = z;
-                }
-            }
-            ptx::fence_proxy_async_smem();
-            return true;
-        };
-        // A key of the tree is hidden from some rows and seen by others.  If its
-        // values are not all finite, 0 times them would be NaN in the rows that do
-        // not see it: such a key's values are taken out of the tile (blank_rows)
-        // and added in the epilogue to the rows that do see it.  Thread r looks
-        // the tile's key r over.
-        auto odd_key = [&](int j) -> bool {
-            const int kbase = (w.j_lo + j) * BN, key = kbase + r;
-            uint32_t odd = 0;
-            if (key >= tree0 && key < w.Sk) {
-                const uint4 *v = tree_row(p, w, p.v_pool, key);
-                if (v != nullptr) {
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 x = v[i];
-                        odd |= odd_pair(x.x) | odd_pair(x.y) | odd_pair(x.z) | odd_pair(x.w);
-                    }
-                }
-            }
-            const uint32_t all = __ballot_sync(0xffffffffu, odd != 0);
-            if (lane == 0) sm.odd_keys(t, kbase / BN - tree0 / BN)[quarter] = all;
-            return odd != 0;
-        };
         const int lim_row = p.causal ? min(pos + w.Sk - w.Sq, w.Sk - 1) : w.Sk - 1;
         // the tile's first position is its smallest
         const int lim_tile = p.causal ? min(s0 + w.Sk - w.Sq, w.Sk - 1) : w.Sk - 1;
@@ -1280,25 +1326,21 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
                 ok = false;
                 break;
             }
-            if (TREE && !dead_tile && (w.j_lo + j + 1) * BN > tree0) {  // its keys' values, for the tile's other rows
-                const bool odd = odd_key(j);
-                if (!blank_rows(j, odd)) {
-                    ok = false;
-                    break;
-                }
-            }
             warp_arrive(sm.p_full(t), lane);
+        }
+        // Which keys of the tree's tiles the row sees, found while the unit's first
+        // scores are on their way and kept in local memory until those tiles come.
+        uint32_t seen[TREE ? TREE_TILES : 1][4];
+        if (TREE && !dead) {
+#pragma unroll 1
+            for (int i = 0; i < TREE_TILES; ++i) {
+                const int tile = tree0 / BN + i;
+                if (tile >= w.j_lo && tile < w.j_lo + w.n_kv) tree_visible(p, w, pos, valid, lane, tile * BN, seen[i]);
+            }
         }
         for (int j = 0; !dead && j < w.n_kv; ++j) {
             const int g = g0 + j;
             const int kbase = (w.j_lo + j) * BN;  // absolute first key of this tile
-            // (while the tile's scores are on their way)
-            uint32_t vis[4];
-            bool odd = false;
-            if (TREE && kbase + BN > tree0) {
-                tree_visible(p, w, pos, valid, kbase, vis);
-                odd = odd_key(j);
-            }
             if (!wait_bounded(sm.s_full(t), (uint32_t)(g & 1), wc, kSiteSoftmaxS)) {
                 ok = false;
                 break;
@@ -1323,17 +1365,23 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
                     s[48 + i] = make_float2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]));
                 }
             }
-            const bool masked = kbase + BN - 1 > (TREE ? tree0 - 1 : lim_tile);
-            float mx;
-            if (TREE && masked) {
-                float2 sm2[64];
+            const bool masked = !TREE && kbase + BN - 1 > lim_tile;
+            if (TREE && kbase + BN > tree0) {
+                const uint32_t *tile = seen[kbase / BN - tree0 / BN];
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    sm2[i].x = vis[i >> 4] >> (2 * i & 31) & 1u ? s[i].x : -INFINITY;
-                    sm2[i].y = vis[i >> 4] >> (2 * i + 1 & 31) & 1u ? s[i].y : -INFINITY;
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t vis = tile[k];
+                    if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float2 &x = s[16 * k + i];
+                        x.x = vis >> (2 * i) & 1u ? x.x : -INFINITY;
+                        x.y = vis >> (2 * i + 1) & 1u ? x.y : -INFINITY;
+                    }
                 }
-                mx = row_max(sm2);
-            } else if (masked) {
+            }
+            float mx;
+            if (masked) {
                 // Scores of keys the row may not see take no part in the max.
                 float2 sm2[64];
 #pragma unroll
@@ -1357,8 +1405,7 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
             const float alpha = need ? ptx::ex2(m_run - m_new) : 1.f;
             const float m_sub = (m_new == -INFINITY) ? 0.f : m_new;
             uint32_t pk[64];
-            const float rowsum = TREE && masked ? softmax_tile_bits(s, pk, sl2, m_sub, vis)
-                                 : masked ? softmax_tile<true>(s, pk, sl2, m_sub, kbase, lim_row)
+            const float rowsum = masked ? softmax_tile<true>(s, pk, sl2, m_sub, kbase, lim_row)
                                         : softmax_tile<false>(s, pk, sl2, m_sub, kbase, lim_row);
             // P_t(g-1) and O_t are read / written by PV_t(g-1): wait for it before
             // overwriting P_t or rescaling O_t (normally it finished long ago).
@@ -1409,11 +1456,32 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
             ptx::tmem_wait_st();
             l_run = l_run * alpha + rowsum;
             m_run = m_new;
-            if (TREE ? masked : PACKED && kbase + BN > w.Sk) {
-                if (!blank_rows(j, odd)) {
+            if (!TREE && PACKED && kbase + BN > w.Sk) {
+                // Last tile of a packed or paged sequence: the V rows past its end
+                // hold other data (the next sequence's rows, or whatever a page's
+                // unused slots contain).  Their P is 0, but 0 * NaN is NaN, so each
+                // group zeroes those rows in shared memory once the tile has
+                // landed, before releasing its P (the two streams' P V products
+                // are not ordered; both groups write the same zeros).  (A tree's
+                // tiles come clean.)
+                const int item = nb + 2 * j + 1;
+                uint8_t *vt = sm.slot(item % NSLOT);
+                if (!wait_bounded(sm.kv_full(item % NSLOT), (uint32_t)((item / NSLOT) & 1), wc, kSiteSoftmaxV)) {
                     ok = false;
                     break;
                 }
+                if (kbase + r >= w.Sk) {
+                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                    // row r, both halves (dense or paged tile layout)
+                    uint8_t *h0 = PAGED ? vt + (r >> 3) * PG_GROUP_BYTES + (r & 7) * 128 : vt + r * 128;
+                    uint8_t *h1 = h0 + (PAGED ? PG_HALF_BYTES : HALF_BYTES);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        reinterpret_cast<uint4 *>(h0)[c] = z;
+                        reinterpret_cast<uint4 *>(h1)[c] = z;
+                    }
+                }
+                ptx::fence_proxy_async_smem();
             }
             warp_arrive(sm.p_full(t), lane);
         }
@@ -1426,15 +1494,19 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
         // whole warps, so a lane that gave up takes part; it stores nothing outside
         // the staging slot, which is then handed to nobody.
         if (ok && w.n_kv > 0) ok = wait_bounded(sm.o_full(t), (uint32_t)((g0 + w.n_kv - 1) & 1), wc, kSiteEpilogueO);
+        if (TREE) {
+            // Rows go to memory from registers: no slot, and no barrier of the group (a
+            // warp that gives up leaves alone, the others at their next wait).
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!dead) tree_epilogue(p, sm, w, u, tO, pos, head, valid, lane, t * BM + r, m_run, l_run);
+            nb += ring_items<KIND>(w);
+            g0 += w.n_kv;
+            continue;
+        }
         const int o_item = nb + 2 * w.n_kv + t;
         uint8_t *stage = sm.slot(o_item % NSLOT);
         if (ok) ok = wait_bounded(sm.kv_full(o_item % NSLOT), (uint32_t)((o_item / NSLOT) & 1), wc, kSiteEpilogueSlot);
-        if (TREE) {
-            // Every warp's flags of its keys are there.  A warp that left comes to one
-            // barrier only: where this one says "not well", all of them leave here.
-            if (has_tree && !ptx::named_bar_and(1 + t, 128, ok && !*wc.abort_flag)) break;
-            tree_epilogue(p, sm, w, tO, t, quarter, lane, pos, head, valid, dead, has_tree, m_run, l_run, stage, ok);
-        } else if (!PACKED && w.part >= 0) {
+        if (!PACKED && w.part >= 0) {
             // A key-range part of a split unit: its O (normalised within the range)
             // and log-sum-exp go to the workspace in fp32 for the merge kernel.
             ptx::tc_fence_after();
@@ -1491,9 +1563,7 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
         ptx::fence_proxy_async_smem();
         if (!ptx::named_bar_and(1 + t, 128, ok && !*wc.abort_flag)) break;
         bool handed = false;  // the store lane releases the slot
-        if (TREE) {
-            // (the rows are stored, each warp's by itself)
-        } else if (PACKED && s0 + BM > w.Sq) {
+        if (PACKED && s0 + BM > w.Sq) {
             // Last row block of a packed sequence: a full box would spill into the
             // next sequence's rows, so each thread stores its own row (if valid)
             // from the swizzled staging tile; the group then waits for all rows
@@ -1516,9 +1586,10 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
         // Otherwise the slot is free again now (one arrival for each of the two
         // streams that release K/V slots).
         if (leader && !handed) ptx::mbar_arrive_cnt(sm.kv_empty(o_item % NSLOT), 2);
-        nb += ring_items(w);
+        nb += ring_items<KIND>(w);
         g0 += w.n_kv;
     }
+    if (TREE) return;
     // A warp that gives up on a unit it could not read may be alone in it: the
     // group's others may have read the unit, and wait for all four warps at the
     // unit's barrier.  So every warp comes to that barrier once a unit, the last
@@ -1551,6 +1622,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         for (int s = 0; s < NSLOT; ++s) {
             ptx::mbar_init(sm.kv_full(s), 1);
+            ptx::mbar_init(sm.v_raw(s), 1);
             ptx::mbar_init(sm.kv_empty(s), 2);  // one release per issuing stream (or a staging slot's 2)
         }
         // Softmax-side barriers take one arrival per warp (lane 0, after the
@@ -1564,7 +1636,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ptx::mbar_init(sm.fin(), 2);  // one commit per issuing stream
         for (int i = 0; i < ITEM_RING; ++i) {
             ptx::mbar_init(sm.item_full(i), 1);
-            ptx::mbar_init(sm.item_empty(i), ITEM_READERS);
+            ptx::mbar_init(sm.item_empty(i), ITEM_READERS + (KIND == kTree ? 1 : 0));  // (and the cleaner)
         }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(sm.stage_ready(t), 1);
@@ -1577,6 +1649,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ptx::prefetch_tensormap(&map_v);
         ptx::prefetch_tensormap(&map_o);
     }
+    if (KIND == kTree) ptx::wait_for_prior_work();  // (launched as a programmatic dependent)
     if (warp == 1) {
         ptx::tmem_alloc(sm.tmem_slot(), 512);
         ptx::tmem_relinquish();
@@ -1595,13 +1668,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             else if (lane == 0)
                 producer<KIND>(p, sm, wc, &map_q, &map_k, &map_v);
         } else if (warp == 3) {
-            if (lane < 2) store_lane(sm, wc, lane, &map_o);
+            if (KIND == kTree)
+                tree_cleaner(sm, wc, lane);
+            else if (lane < 2)
+                store_lane(sm, wc, lane, &map_o);
         } else if (warp == 1 || warp == 2) {
             if (lane == 0) {
                 if (warp == 1)
-                    mma_stream<0, KIND == kPaged || KIND == kTree>(p, sm, wc, tmem_base);
+                    mma_stream<0, KIND>(p, sm, wc, tmem_base);
                 else
-                    mma_stream<1, KIND == kPaged || KIND == kTree>(p, sm, wc, tmem_base);
+                    mma_stream<1, KIND>(p, sm, wc, tmem_base);
                 // Whatever happened, wait until every product issued (by
                 // either stream) has completed before tensor memory is released.
                 ptx::umma_commit(sm.fin());
@@ -1661,8 +1737,9 @@ cudaError_t launch_prefill(const CUtensorMap &mq, const CUtensorMap &mk, const C
     }
     // One instantiation per kind of launch, each with only its own paths.
     if (p.parents != nullptr)
-        g1::prefill_kernel<g1::kTree><<<num_ctas, g1::NUM_THREADS, smem, stream>>>(mq, mk, mv, mo, mk8, mv8, p);
-    else if (p.block_table != nullptr)
+        return launch_dependent(g1::prefill_kernel<g1::kTree>, dim3(num_ctas), dim3(g1::NUM_THREADS), smem, stream, mq, mk,
+                                mv, mo, mk8, mv8, p);
+    if (p.block_table != nullptr)
         g1::prefill_kernel<g1::kPaged><<<num_ctas, g1::NUM_THREADS, smem, stream>>>(mq, mk, mv, mo, mk8, mv8, p);
     else if (p.cu_q != nullptr)
         g1::prefill_kernel<g1::kPacked><<<num_ctas, g1::NUM_THREADS, smem, stream>>>(mq, mk, mv, mo, mk8, mv8, p);
@@ -1767,94 +1844,138 @@ cudaError_t launch_prefill_merge(void *out, const PrefillParams &p, cudaStream_t
 
 namespace g1 {
 
-// Joins a tree launch's partials: WARPS warps a row of out, which take its parts in
-// turn, four columns a lane.  blockIdx.x: sequence x row (position x head).  Rows of
-// units that were not cut are there already.
-template <int WARPS>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const PrefillParams p, int ctas, int blocks_per_seq) {
+// Joins a tree launch's partials.  blockIdx.x: sequence, KV head, row block, and group
+// of the unit's rows; a warp takes ROWS of them one after another, four columns a lane,
+// or (SPLIT) all eight warps one row, whose parts they take in turn.  Units that were not
+// cut are there already.
+template <bool SPLIT, int ROWS>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const PrefillParams p, int ctas, int groups, int blocks) {
     ptx::wait_for_prior_work();
-    constexpr int ROWS = 8 / WARPS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.x / blocks_per_seq;
-    const int idx = (blockIdx.x - b * blocks_per_seq) * ROWS + warp / WARPS;
-    const int pos = idx / p.Hq, h = idx - pos * p.Hq;
+    const int unit = blockIdx.x / groups, group = blockIdx.x - unit * groups;
+    const int b = unit / (p.Hkv * blocks), gb = unit - b * p.Hkv * blocks, g = gb / blocks, blk = gb - g * blocks;
     const TreeSeq s = tree_seq(p, b, false);
-    const int total = p.first[p.B], shares = tree_shares(ctas, total);
-    int c0 = 0, c1 = 0, us = 0, row = 0;
-    if (pos < s.Sq) {
-        const int g = h / p.G, blk = pos / (2 * p.pack_pos), rem = pos - blk * 2 * p.pack_pos;
-        const int t = rem >= p.pack_pos ? 1 : 0;
-        row = t * BM + (rem - t * p.pack_pos) * p.G + h - g * p.G;
-        us = p.first[b] + (g * s.blocks + blk) * s.tiles;
-        c0 = tree_share_of(us, shares, total);
-        c1 = tree_share_of(us + s.tiles - 1, shares, total);
-    }
-    const bool cut = c1 > c0;
-    if (WARPS == 1 && !cut) return;
-    // The part of CTA c: its share's first segment, or its last where it begins with another unit.
-    auto part_row = [&](int c) {
-        return ((int64_t)c * 2 + (tree_share_begin(c, shares, total) < us ? 1 : 0)) * p.part_rows + row;
+    const int begin = p.first[b], total = p.first[p.B];
+    if (blk >= s.blocks) return;  // (total is not 0)
+    const TreeLine line(ctas, total);
+    const int us = begin + (g * s.blocks + blk) * s.span;
+    const int c0 = line.of(us + s.span - s.tiles), c1 = line.of(us + s.span - 1);
+    if (c0 == c1) return;
+    // The unit's positions in its two tiles; rows in tile order, the second tile's from 128 on.
+    const int left = s.Sq - blk * 2 * p.pack_pos, pos0 = min(left, p.pack_pos), pos1 = min(left - pos0, p.pack_pos);
+    const int rows0 = pos0 * p.G, rows = rows0 + pos1 * p.G;
+    // The part of CTA c: its share's first segment, or (only c0) its last where it begins with another unit.
+    const bool last0 = line.begin(c0) < us;
+    auto part_row = [&](int c) { return ((int64_t)c * 2 + (c == c0 && last0 ? 1 : 0)) * p.part_rows; };
+    // This lane's four columns of a part's row (column groups of eight are apart).
+    auto columns = [&](int64_t part, int row) {
+        return *reinterpret_cast<const float4 *>(p.ws_o + part * D + ((int64_t)(lane >> 1) * p.part_rows + row) * 8 +
+                                                 (lane & 1) * 4);
     };
-    float M = -INFINITY, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (cut) {
-        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.ws_lse[part_row(c)]);
+    auto finish = [&](int i, float4 o, float sum, float M) {
+        const int t = i >= rows0 ? 1 : 0, r = i - t * rows0;
+        const int pos = blk * 2 * p.pack_pos + t * p.pack_pos + r / p.G, h = g * p.G + r % p.G;
+        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + ((int64_t)(s.q0 + pos) * p.Hq + h) * D)[lane] =
+            make_uint2(pack_bf16x2_mode(o.x * inv, o.y * inv, p.round_mode),
+                       pack_bf16x2_mode(o.z * inv, o.w * inv, p.round_mode));
+        if (lane == 0 && p.lse != nullptr)
+            p.lse[(int64_t)h * p.total_q + s.q0 + pos] = sum == 0.f ? -INFINITY : M + ptx::lg2(sum) * LN2;
+    };
+    if (!SPLIT) {
+        // The parts in turn, with a running maximum of each row's log-sum-exps: every load of
+        // a part is independent, the rows' and the next part's.
+        const int i0 = (group * 8 + warp) * ROWS;
+        float M[ROWS], sum[ROWS];
+        float4 o[ROWS];
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            M[k] = -INFINITY;
+            sum[k] = 0.f;
+            o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll(8 / ROWS)
+        for (int c = c0; c <= c1; ++c) {
+            const int64_t at = part_row(c);
+            float l[ROWS];
+            float4 x[ROWS];
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k) {
+                const int i = min(i0 + k, rows - 1);
+                const int row = i >= rows0 ? BM + i - rows0 : i;
+                l[k] = p.ws_lse[at + row];
+                x[k] = columns(at, row);
+            }
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k) {
+                const float m = fmaxf(M[k], l[k]), ref = m == -INFINITY ? 0.f : m;
+                const float old = ptx::ex2((M[k] - ref) * 1.4426950408889634f);
+                const float wk = ptx::ex2((l[k] - ref) * 1.4426950408889634f);
+                sum[k] = fmaf(sum[k], old, wk);
+                o[k].x = fmaf(o[k].x, old, wk * x[k].x);
+                o[k].y = fmaf(o[k].y, old, wk * x[k].y);
+                o[k].z = fmaf(o[k].z, old, wk * x[k].z);
+                o[k].w = fmaf(o[k].w, old, wk * x[k].w);
+                M[k] = m;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k)
+            if (i0 + k < rows) finish(i0 + k, o[k], sum[k], M[k]);
+    } else {
+        __shared__ float4 part_o[8][32];
+        __shared__ float part_sum[8];
+        const int i = group;
+        if (i >= rows) return;
+        const int at = i >= rows0 ? BM + i - rows0 : i;
+        float M = -INFINITY, sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.ws_lse[part_row(c) + at]);
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
         const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll 8
-        for (int c = c0 + warp % WARPS; c <= c1; c += WARPS) {
-            const int64_t at = part_row(c);
-            const float4 x = reinterpret_cast<const float4 *>(p.ws_o + at * D)[lane];
-            const float wk = ptx::ex2((p.ws_lse[at] - ref) * 1.4426950408889634f);
+        for (int c = c0 + warp; c <= c1; c += 8) {
+            const float4 x = columns(part_row(c), at);
+            const float wk = ptx::ex2((p.ws_lse[part_row(c) + at] - ref) * 1.4426950408889634f);
             sum += wk;
             o.x = fmaf(wk, x.x, o.x);
             o.y = fmaf(wk, x.y, o.y);
             o.z = fmaf(wk, x.z, o.z);
             o.w = fmaf(wk, x.w, o.w);
         }
-    }
-    if (WARPS > 1) {
-        __shared__ float4 part_o[8][32];
-        __shared__ float part_sum[8];
         part_o[warp][lane] = o;
         if (lane == 0) part_sum[warp] = sum;
         __syncthreads();
-        if (warp % WARPS != 0 || !cut) return;
+        if (warp != 0) return;
 #pragma unroll
-        for (int k = 1; k < WARPS; ++k) {
-            const float4 x = part_o[warp + k][lane];
-            sum += part_sum[warp + k];
+        for (int k = 1; k < 8; ++k) {
+            const float4 x = part_o[k][lane];
+            sum += part_sum[k];
             o.x += x.x;
             o.y += x.y;
             o.z += x.z;
             o.w += x.w;
         }
+        finish(i, o, sum, M);
     }
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + ((int64_t)(s.q0 + pos) * p.Hq + h) * D)[lane] =
-        make_uint2(pack_bf16x2_mode(o.x * inv, o.y * inv, p.round_mode), pack_bf16x2_mode(o.z * inv, o.w * inv, p.round_mode));
-    if (lane == 0 && p.lse != nullptr)
-        p.lse[(int64_t)h * p.total_q + s.q0 + pos] = sum == 0.f ? -INFINITY : M + ptx::lg2(sum) * LN2;
 }
 
 }  // namespace g1
 
 cudaError_t launch_tree_merge(const PrefillParams &p, int ctas, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    // Few rows: eight warps each, a row's parts may be many.
-    const int64_t rows = (int64_t)p.Sq * p.Hq;
-    const bool few = rows * p.B <= 4096;
-    const int per = (int)(few ? rows : (rows + 7) / 8);
-    cfg.gridDim = dim3((unsigned)(per * p.B));
-    return cudaLaunchKernelEx(&cfg, few ? g1::tree_merge_kernel<8> : g1::tree_merge_kernel<1>, p, ctas, per);
+    if (p.whole) return cudaSuccess;  // (nothing is cut)
+    const int blocks = (p.Sq + 2 * p.pack_pos - 1) / (2 * p.pack_pos);
+    const int most = std::min(p.Sq, 2 * p.pack_pos) * p.G;  // rows of a unit
+    const int64_t units = (int64_t)p.B * p.Hkv * blocks;
+    const auto launch = [&](auto kernel, int groups) {
+        return launch_dependent(kernel, dim3((unsigned)(units * groups)), dim3(256), 0, stream, p, ctas, groups, blocks);
+    };
+    // Few units are cut into many parts each, and there are few rows: eight warps a row.
+    if (units * 8 <= ctas) return launch(g1::tree_merge_kernel<true, 1>, most);
+    // Otherwise a warp takes four rows, or one where that leaves SMs idle.
+    if (units * most >= 16 * 1024) return launch(g1::tree_merge_kernel<false, 4>, (most + 31) / 32);
+    return launch(g1::tree_merge_kernel<false, 1>, (most + 7) / 8);
 }
 
 }  // namespace attn

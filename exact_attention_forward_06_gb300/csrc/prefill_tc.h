@@ -65,17 +65,26 @@ struct PrefillParams {
     // tiles of all (sequence, KV head, row block) units lie on one line, which
     // the grid's CTAs share equally; a unit cut between CTAs leaves fp32
     // partials, two at most a CTA, in ws_o [CTAs][2][part_rows][128] and
-    // ws_lse [CTAs][2][part_rows], and `first` [B + 1] says where on the line
-    // each sequence begins.
+    // ws_lse [CTAs][2][part_rows] (a part of ws_o: [16][part_rows][8], column
+    // groups of eight apart), and `first` [B + 1] says where on the line each
+    // sequence begins.
     const int *parents;
     const void *q, *k_pool, *v_pool;
     int part_rows;
+    int whole;      // 1: the line is of units, none is cut
+    int unit_cost;  // places that a unit has on the line besides its tiles
     int *first;
 };
 
 // Row layout of a tree launch: positions a Q tile covers, rows of a partial.
 constexpr int kTreeMaxNodes = 256;
 constexpr int kTreeMaxCtas = 152;  // the SMs of a GB300
+// What a unit takes besides its K/V tiles, in tiles: its last tile's masks, its
+// output and the step to the next unit.  By a fit of the CTAs' times over their tiles
+// and units on one GB300 3.8 us a unit where one of the two Q tiles has rows (a tile:
+// 1.47 us, by the memory) and 10 us where both have (1.7 us, by the exponentials).
+constexpr int kTreeCostOne = 3;
+constexpr int kTreeCostTwo = 6;
 inline int tree_tile_positions(int G) { return 128 / G; }
 inline int tree_part_rows(int G, int max_nodes) {
     const int pp = tree_tile_positions(G);

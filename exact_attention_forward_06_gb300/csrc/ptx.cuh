@@ -232,6 +232,13 @@ __device__ __forceinline__ void cluster_store(const void *own, uint32_t rank, fl
         : "memory");
 }
 
+// 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void store_32(void *dst, const uint32_t (&x)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- named barriers
 
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {

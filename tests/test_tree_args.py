@@ -26,7 +26,7 @@ TREE = dict(q=256, k=512, v=1024, bt=4, sl=8, cu=12, par=4, out=2048, lse=4, B=2
     (dict(par=None), 1), (dict(par=6), 1), (dict(out=None), 1), (dict(out=2056), 1), (dict(lse=6), 1), (dict(B=0), 1),
     (dict(B=-1), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(Hq=9), 1), (dict(total=0), 1), (dict(longest=0), 1),
     (dict(longest=257), 1), (dict(d=64), 2), (dict(page=32), 2), (dict(npages=0), 1), (dict(npages=1 << 28), 1),
-    (dict(maxb=0), 1), (dict(maxb=1 << 27), 1), (dict(maxb=(1 << 27) - 1, B=1 << 8), 1),
+    (dict(maxb=0), 1), (dict(maxb=1 << 27), 1), (dict(maxb=(1 << 27) - 16, B=1 << 8), 1),
     (dict(Hq=258, Hkv=2), 2),                        # 129 query heads to a KV head
     (dict(B=1 << 26, Hq=1 << 4), 1),                 # rows of the merge past 2^31
     (dict(scale=float("nan")), 1), (dict(scale=-1.0), 1), (dict(mode=3), 1), (dict(mode=-1), 1), (dict(ws=None), 5),
