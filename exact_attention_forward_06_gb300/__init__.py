@@ -11,7 +11,7 @@ from ._binding import (AttnError, LIBRARY_PATH, Q4_BLOCK_BYTES, TREE_MAX, append
                        fwd_host_workspace_bytes, fwd_paged, fwd_paged_q4, fwd_paged_q4_workspace_bytes, fwd_simple,
                        fwd_tree_paged, fwd_tree_paged_workspace_bytes, fwd_varlen, fwd_workspace_bytes, gather_paged_q4,
                        load, lse_merge, qk_norm_rope, rope_table, selftest_umma, set_wait_budget_ns, set_workspace,
-                       status_string, verify_tree, version)
+                       status_string, verify_tree, verify_tree_workspace_bytes, version)
 
 __all__ = ["AttnError", "LIBRARY_PATH", "Q4_BLOCK_BYTES", "TREE_MAX", "append_paged", "append_paged_q4",
            "compact_paged", "debug_inject", "decode_paged", "decode_paged_append", "decode_paged_noalloc",
@@ -19,4 +19,5 @@ __all__ = ["AttnError", "LIBRARY_PATH", "Q4_BLOCK_BYTES", "TREE_MAX", "append_pa
            "fwd_host", "fwd_host_workspace_bytes", "fwd_paged", "fwd_paged_q4", "fwd_paged_q4_workspace_bytes",
            "fwd_simple", "fwd_tree_paged", "fwd_tree_paged_workspace_bytes", "fwd_varlen", "fwd_workspace_bytes",
            "gather_paged_q4", "load", "lse_merge", "qk_norm_rope", "rope_table", "selftest_umma",
-           "set_wait_budget_ns", "set_workspace", "status_string", "verify_tree", "version"]
+           "set_wait_budget_ns", "set_workspace", "status_string", "verify_tree", "verify_tree_workspace_bytes",
+           "version"]

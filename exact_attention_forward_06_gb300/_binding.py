@@ -128,7 +128,9 @@ def load():
             lib.attn_fwd_tree_paged_workspace_bytes.argtypes = [_i] * 5
             lib.attn_fwd_tree_paged_workspace_bytes.restype = _sz
             lib.attn_fwd_tree_paged.argtypes = [_p] * 9 + [_i] * 9 + [_f, _i, _p, _sz, _p]
-            lib.attn_verify_tree.argtypes = [_p, _p, _i] + [_p] * 9 + [_i] * 4 + [_sz] * 3 + [_p]
+            lib.attn_verify_tree_workspace_bytes.argtypes = [_i] * 6
+            lib.attn_verify_tree_workspace_bytes.restype = _sz
+            lib.attn_verify_tree.argtypes = [_p, _p, _i] + [_p] * 9 + [_i] * 4 + [_sz] * 3 + [_p, _sz, _p]
             lib.attn_compact_paged.argtypes = [_p] * 8 + [_i] * 9 + [_p]
             lib.attn_status_string.argtypes = [_i]
             lib.attn_status_string.restype = ctypes.c_char_p
@@ -986,8 +988,14 @@ def _out_i32(t, name, shape, like, stream, dev):
     return t, ptr
 
 
+def verify_tree_workspace_bytes(B: int, total: int, vocab: int, max_seqlen: int, dtype=torch.bfloat16,
+                                with_draft: bool = False) -> int:
+    """Device workspace bytes verify_tree needs for this shape."""
+    return int(load().attn_verify_tree_workspace_bytes(B, total, vocab, max_seqlen, _DTYPES[dtype], int(with_draft)))
+
+
 def verify_tree(logits, tokens, parents, cu_seqlens, *, draft_logits=None, temperature=None, uniforms=None, noise=None,
-                max_seqlen=None, path=None, out_tokens=None, counts=None, stream=None):
+                max_seqlen=None, path=None, out_tokens=None, counts=None, workspace=None, stream=None):
     """Which drafted tokens of each sequence's tree are kept, and the token that follows them, from given random numbers.
 
     logits [total, vocab] bf16 or fp32 (rows may be strided): the target's at every node; tokens, parents [total] and
@@ -1004,7 +1012,7 @@ def verify_tree(logits, tokens, parents, cu_seqlens, *, draft_logits=None, tempe
     lib = _lib or load()
     if stream is None:
         done = _quick.verify(logits, tokens, parents, cu_seqlens, draft_logits, temperature, uniforms, noise, max_seqlen,
-                             path, out_tokens, counts)
+                             path, out_tokens, counts, workspace)
         if done is not None:
             return done
     dev = _current()
@@ -1040,8 +1048,14 @@ def verify_tree(logits, tokens, parents, cu_seqlens, *, draft_logits=None, tempe
     path, pp = _out_i32(path, "path", (B, max_seqlen), logits, stream, dev)
     out_tokens, op = _out_i32(out_tokens, "out_tokens", (B, max_seqlen), logits, stream, dev)
     counts, cp = _out_i32(counts, "counts", (B,), logits, stream, dev)
+    if workspace is None:
+        need = lib.attn_verify_tree_workspace_bytes(B, total, vocab, max_seqlen, _DTYPES[dtype], dp is not None)
+        workspace = _empty(max(need, 1), torch.uint8, logits.device, stream)
+        wp = workspace.data_ptr()
+    else:
+        wp = _in(workspace, "workspace", torch.uint8, dev)
     rc = lib.attn_verify_tree(lp, dp, _DTYPES[dtype], tok, par, cu, tp, up, np_, pp, op, cp, B, total, vocab, max_seqlen,
-                              ls, ds, ns, _raw_stream(dev) if stream is None else stream.cuda_stream)
+                              ls, ds, ns, wp, workspace.numel(), _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "attn_verify_tree")
     return path, out_tokens, counts

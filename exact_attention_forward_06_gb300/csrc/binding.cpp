@@ -431,11 +431,12 @@ struct Rows {
     }
 };
 
-// logits, tokens, parents, cu_seqlens, draft_logits, temperature, uniforms, noise, max_seqlen, path, out_tokens, counts
+// logits, tokens, parents, cu_seqlens, draft_logits, temperature, uniforms, noise, max_seqlen, path, out_tokens, counts,
+// workspace
 PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     Reader r;
-    if (n != 12 || a[8] == Py_None || !THPVariable_Check(a[0])) Py_RETURN_NONE;
+    if (n != 13 || a[8] == Py_None || !THPVariable_Check(a[0])) Py_RETURN_NONE;
     const at::Tensor &l = THPVariable_Unpack(a[0]);
     const at::ScalarType type = l.scalar_type();
     if ((type != BF16 && type != F32) || l.dim() != 2) Py_RETURN_NONE;
@@ -462,13 +463,24 @@ PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
     path.take(r, a[9], I32, sizes, l);
     out.take(r, a[10], I32, sizes, l);
     counts.take(r, a[11], I32, at::IntArrayRef(sizes, 1), l);
+    if (!r.ok) Py_RETURN_NONE;
+    const int dtype = type == BF16 ? ATTN_DTYPE_BF16 : ATTN_DTYPE_FP32;
+    Output ws;
+    int64_t bytes = 0;
+    if (a[12] != Py_None) {
+        const at::Tensor *y = r.dense(a[12], U8);
+        bytes = y ? y->numel() : 0;
+        ws.ptr = at_of(y);
+    } else if ((bytes = (int64_t)attn_verify_tree_workspace_bytes(b, t, v, w, dtype, draft.t != nullptr)) > 0) {
+        ws.take(r, a[12], U8, bytes, l);
+    }
     const auto at4 = [](const at::Tensor *y) { return y ? static_cast<const float *>(y->data_ptr()) : nullptr; };
     const auto ints = [](const at::Tensor *y) { return static_cast<const int32_t *>(y->data_ptr()); };
-    if (!r.ok || attn_verify_tree(l.data_ptr(), at_of(draft.t), type == BF16 ? ATTN_DTYPE_BF16 : ATTN_DTYPE_FP32, ints(tokens),
+    if (!r.ok || attn_verify_tree(l.data_ptr(), at_of(draft.t), dtype, ints(tokens),
                                   ints(parents), ints(cu), at4(temp), at4(uniforms), at4(noise.t),
                                   static_cast<int32_t *>(path.ptr), static_cast<int32_t *>(out.ptr),
                                   static_cast<int32_t *>(counts.ptr), b, t, v, w, logits.stride, draft.stride, noise.stride,
-                                  r.stream()) != ATTN_OK)
+                                  ws.ptr, (size_t)bytes, r.stream()) != ATTN_OK)
         Py_RETURN_NONE;
     PyObject *x = path.object(), *y = x ? out.object() : nullptr, *z = y ? counts.object() : nullptr;
     PyObject *three = z ? PyTuple_Pack(3, x, y, z) : nullptr;

@@ -19,6 +19,13 @@ struct VerifyParams {
     int32_t *path, *out_tokens, *counts;
     int B, total, V, width;
     int fp32;  // type of logits and draft
+    // All rows summed up ahead of the walk, in `pieces` slices of `piece` tokens (0: a
+    // row when the walk comes to it): maximum and sum, or the largest logit's key.
+    int pieces, piece;
+    float2 *sums;  // [target, draft][total][pieces]
+    // Where every sequence's walk ended, kVerifyEndBytes each, and behind them a list of
+    // `width` numbers each; nullptr where nothing is drawn.
+    uint8_t *ends;
     unsigned *status;
 };
 
@@ -30,6 +37,9 @@ struct CompactParams {
     unsigned *status;
 };
 
+constexpr int kVerifyEndBytes = 64;
+// The slices of a row that are summed up ahead: `rows` rows in all.
+int verify_piece(int64_t rows, int vocab, int *pieces);
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream);
 cudaError_t launch_compact(const CompactParams &p, cudaStream_t stream);
 

@@ -7,15 +7,20 @@
 //     u q(x) < p(x),  a rejected child leaving  p <- max(p - q, 0) / sum,
 // and the walk goes on there, or none is and the last token is drawn from what is
 // left of p as argmax_i p_i / e_i: of independent exponential numbers e_i / p_i the
-// smallest is that of i with probability p_i.  Only rows on the path are read; the
-// other nodes' rows, most of a tree, are not.
+// smallest is that of i with probability p_i.
 //
-// A cluster of CTAs works on a sequence, each on a slice of the vocabulary.  A step
-// of the walk is one pass over the node's row(s) for the maximum and the sum of the
-// exponentials, kept per thread and joined once (the children's own logits are
-// fetched meanwhile), an exchange through the cluster's shared memory, and the
-// decision, which every thread of every CTA takes by itself from the same numbers
-// in the same order.
+// Three kernels.  sums_kernel (short trees only) takes maximum and sum of the
+// exponentials of all rows, which is what decisions need of a row besides the
+// children's own logits; it reads rows that the walk may not come to, but all at once.
+// verify_kernel walks, a cluster of CTAs a sequence, each on a slice of the vocabulary:
+// where a row's sums are not there it takes them (one pass, an exchange through the
+// cluster's shared memory), then every thread of every CTA decides by itself, from the
+// same numbers in the same order.  race_kernel draws the last tokens.  The bound is the
+// rows' bytes where there are many sequences, and the chain of row after row where
+// there are few.  The kernels run through their code once, so it is kept short (rolled
+// loops): with chunks of 32 elements unrolled, in one kernel, half the time went to
+// fetching instructions.
+#include <algorithm>
 #include <cfloat>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -29,9 +34,13 @@
 namespace attn {
 namespace vf {
 
-constexpr int THREADS = 512;
+constexpr int THREADS = 512;      // of verify_kernel
 constexpr int WARPS = THREADS / 32;
+constexpr int RACE_THREADS = 256;  // of race_kernel
+constexpr int RACE_BLOCKS = 4;     // of it an SM
+constexpr int SUM_THREADS = 128;  // of sums_kernel
 constexpr int MAX_CLUSTER = 8;
+constexpr int WALK_END_BYTES = kVerifyEndBytes;
 constexpr unsigned ALL = 0xffffffffu;
 
 // Eight consecutive elements of a row, as they are in memory.
@@ -39,40 +48,51 @@ template <typename T>
 struct Chunk;
 template <>
 struct Chunk<__nv_bfloat16> {
-    uint4 w;
+    uint32_t w[4];
+    __device__ __forceinline__ void none() { w[0] = w[1] = w[2] = w[3] = 0xff80ff80u; }  // -inf
     __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool vec) {
         if (vec) {
-            w = *reinterpret_cast<const uint4 *>(p);
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
         } else {
             const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
-            w = make_uint4(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16, h[4] | (uint32_t)h[5] << 16,
-                           h[6] | (uint32_t)h[7] << 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
         }
     }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(v[i] << 16);
-            x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-        }
+    __device__ __forceinline__ float2 pair(int i) const {
+        return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+    // The largest element (NaN aside), or -inf.
+    __device__ __forceinline__ float top() const {
+        const auto h = [&](int i) { return *reinterpret_cast<const __nv_bfloat162 *>(w + i); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(h(0), h(1)), __hmax2(h(2), h(3)));
+        return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
     }
 };
 template <>
 struct Chunk<float> {
-    float4 a, b;
+    float2 w[4];
+    __device__ __forceinline__ void none() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = make_float2(-INFINITY, -INFINITY);
+    }
     __device__ __forceinline__ void load(const float *p, bool vec) {
         if (vec) {
-            a = reinterpret_cast<const float4 *>(p)[0];
-            b = reinterpret_cast<const float4 *>(p)[1];
+            const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+            w[0] = make_float2(a.x, a.y), w[1] = make_float2(a.z, a.w);
+            w[2] = make_float2(b.x, b.y), w[3] = make_float2(b.z, b.w);
         } else {
-            a = make_float4(p[0], p[1], p[2], p[3]);
-            b = make_float4(p[4], p[5], p[6], p[7]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = make_float2(p[2 * i], p[2 * i + 1]);
         }
     }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    __device__ __forceinline__ float2 pair(int i) const { return w[i]; }
+    __device__ __forceinline__ float top() const {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = ptx::max3(m, w[i].x, w[i].y);
+        return m;
     }
 };
 
@@ -81,53 +101,102 @@ __device__ __forceinline__ float value(float x) { return x; }
 
 __device__ __forceinline__ bool vec_ok(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// The weight exp((x - m) / T) of a logit, c = log2 e / T: 0 for NaN and -inf (and where
-// m is -inf: nothing is left), 1 for +inf (m is then the largest finite number).  x - m
-// is taken before the scaling: with c folded in (one operation less) the rounding of m c
-// would go into every weight.
-__device__ __forceinline__ float weight(float x, float m, float c) {
-    return ptx::ex2(fminf(fmaxf((x - m) * c, -INFINITY), 0.f));
+// The weight exp((x - m) / T) of a logit below a row's largest, m, c = log2 e / T: 0 for
+// NaN and -inf (and where m is -inf: nothing is left), 1 for +inf (m is then the largest
+// finite number).
+__device__ __noinline__ float odd_weight(float x, float m, float c) {
+    return ptx::ex2(fminf(fmaxf((x - fminf(m, FLT_MAX)) * c, -INFINITY), 0.f));
 }
 
-// A running maximum and sum of weights.
-struct Soft {
-    float m = -INFINITY, s = 0.f;
-    __device__ __forceinline__ void add(const float (&x)[8], float c) {
-        float t = m;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t = fmaxf(t, x[i]);
-        t = fminf(t, FLT_MAX);
-        if (t > m) {
-            s *= weight(m, t, c);
-            m = t;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += weight(x[i], m, c);
+// A row's largest logit m and r = m c, rounded.  Weights are taken relative to r, which
+// the rounding leaves a little off m c: as every weight and every sum goes by the same r,
+// or by the difference of two of them, that cancels, and a weight is one FFMA and one
+// exponential.  Whatever does not come out as a number up to 1 (with rounding) goes the
+// long way.
+struct Top {
+    float m, r;
+    __device__ __forceinline__ Top(float largest, float c) : m(fminf(largest, FLT_MAX)) {
+        r = largest == -INFINITY ? 0.f : m * c;
+        if (!(fabsf(r) <= FLT_MAX)) r = NAN;  // m c is out of range: every weight goes the long way
     }
-    __device__ __forceinline__ void join(float m2, float s2, float c) {
-        const float t = fmaxf(m, m2);
-        s = s * weight(m, t, c) + s2 * weight(m2, t, c);
-        m = t;
+    __device__ __forceinline__ float weight(float x, float c) const {
+        const float f = ptx::ex2(fmaf(x, c, -r));
+        return f <= 2.f ? f : odd_weight(x, m, c);
     }
+    // What a sum relative to another maximum, m2, is multiplied with: by its r, not by m2 c.
+    __device__ __forceinline__ float step(float m2, float c) const { return ptx::ex2(__fmul_rn(m2, c) - r); }
+    static __device__ __forceinline__ bool is_weight(float f) { return f <= 2.f; }
 };
 
-// The largest value and its index, the lowest of equal ones (-1: none).
-struct Best {
-    float v;
-    int i = -1;
-    __device__ __forceinline__ void join(float v2, int i2) {
-        if (i2 >= 0 && (i < 0 || v2 > v || (v2 == v && i2 < i))) {
-            v = v2;
-            i = i2;
+// A maximum and a sum of weights relative to it.
+struct Soft {
+    float m = -INFINITY, s = 0.f;
+    // One more logit.
+    __device__ __forceinline__ void add(float x, float c) {
+        const Top t(fmaxf(m, x), c);
+        raise(t, c);
+        s += t.weight(x, c);
+    }
+    __device__ __forceinline__ void raise(const Top &t, float c) {
+        if (t.m > m) {
+            const float f = t.step(m, c);
+            s *= Top::is_weight(f) ? f : odd_weight(m, t.m, c);
+            m = t.m;
         }
     }
+    // Another thread's or CTA's sum.
+    __device__ __forceinline__ void add(float m2, float s2, float c) {
+        const Top t(fmaxf(m, m2), c);
+        raise(t, c);
+        const float f = t.step(m2, c);
+        s += s2 * (Top::is_weight(f) ? f : odd_weight(m2, t.m, c));
+    }
+    template <typename T>
+    __device__ __forceinline__ void add(const Chunk<T> &x, float c);
 };
+
+// The slow way for a chunk with NaN or an infinity in it.
+template <typename T>
+__device__ __noinline__ float odd_sum(Chunk<T> x, float m, float c) {
+    float all = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) all += odd_weight(x.pair(i).x, m, c) + odd_weight(x.pair(i).y, m, c);
+    return all;
+}
+
+template <typename T>
+__device__ __forceinline__ void Soft::add(const Chunk<T> &x, float c) {
+    const Top t(fmaxf(m, x.top()), c);
+    raise(t, c);
+    const float2 c2 = make_float2(c, c), r2 = make_float2(-t.r, -t.r);
+    float2 sum[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 e = ptx::fma2(x.pair(i), c2, r2), w = make_float2(ptx::ex2(e.x), ptx::ex2(e.y));
+        sum[i & 1] = i < 2 ? w : ptx::add2(sum[i & 1], w);
+    }
+    const float2 both = ptx::add2(sum[0], sum[1]);
+    const float all = both.x + both.y;
+    s += all <= 16.f ? all : odd_sum(x, t.m, c);
+}
+
+// The largest value and its index, the lowest of equal ones: the value's order in the
+// upper half of a word, the index from above in the lower (0: none).
+__device__ __forceinline__ unsigned long long best_key(float v, int i) {
+    const uint32_t u = __float_as_uint(v + 0.f);  // (-0 is 0)
+    const uint32_t order = u & 0x80000000u ? ~u : u | 0x80000000u;
+    return i < 0 ? 0ull : (unsigned long long)order << 32 | (0xffffffffu - (uint32_t)i);
+}
+__device__ __forceinline__ int best_index(unsigned long long k) {
+    return k == 0 ? -1 : (int)(0xffffffffu - (uint32_t)k);
+}
 
 struct Shared {
     float4 warp[WARPS];
     float4 slot[2][MAX_CLUSTER];  // what each CTA of the cluster has, for even and odd exchanges
     int parent[ATTN_TREE_MAX], token[ATTN_TREE_MAX], path[ATTN_TREE_MAX];
     float u[ATTN_TREE_MAX], px[ATTN_TREE_MAX], qx[ATTN_TREE_MAX];
+    float4 stat[ATTN_TREE_MAX];     // rows that were summed up ahead: maximum and sum of target and draft
     float inv_left[ATTN_TREE_MAX];  // 1 / what was left after each rejected sibling (0: nothing, p stays)
 };
 
@@ -142,101 +211,357 @@ __device__ __forceinline__ const float4 *exchange(Shared &sh, int &turn, uint32_
     return slots;
 }
 
-// Joins a number over the CTA's threads and then the cluster, always in the same order.
-template <typename Join>
-__device__ __forceinline__ float4 reduce(Shared &sh, int &turn, uint32_t ctas, uint32_t rank, float4 x, Join join) {
+// The sums of a set of threads' weights in two rows, each relative to its own maximum,
+// relative to the common ones: the maxima first, then one step each for the sums.
+__device__ __forceinline__ void warp_soft(float4 &x, float c) {
+    float mp = x.x, mq = x.z;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        const float4 y = make_float4(__shfl_xor_sync(ALL, x.x, o), __shfl_xor_sync(ALL, x.y, o),
-                                     __shfl_xor_sync(ALL, x.z, o), __shfl_xor_sync(ALL, x.w, o));
-        // the lower lane's number first, in both lanes
-        x = (threadIdx.x & o) ? join(y, x) : join(x, y);
+        mp = fmaxf(mp, __shfl_xor_sync(ALL, mp, o));
+        mq = fmaxf(mq, __shfl_xor_sync(ALL, mq, o));
     }
-    if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = x;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        x = sh.warp[threadIdx.x % WARPS];
+    const Top p(mp, c), q(mq, c);
+    float fp = p.step(x.x, c), fq = q.step(x.z, c);
+    if (!(Top::is_weight(fp) && Top::is_weight(fq))) {
+        fp = odd_weight(x.x, mp, c);
+        fq = odd_weight(x.z, mq, c);
+    }
+    x = make_float4(mp, x.y * fp, mq, x.w * fq);
 #pragma unroll
-        for (int o = WARPS / 2; o > 0; o >>= 1) {
-            const float4 y = make_float4(__shfl_xor_sync(ALL, x.x, o), __shfl_xor_sync(ALL, x.y, o),
-                                         __shfl_xor_sync(ALL, x.z, o), __shfl_xor_sync(ALL, x.w, o));
-            x = (threadIdx.x & o) ? join(y, x) : join(x, y);
+    for (int o = 16; o > 0; o >>= 1) {
+        x.y += __shfl_xor_sync(ALL, x.y, o);
+        x.w += __shfl_xor_sync(ALL, x.w, o);
+    }
+}
+
+// Numbers of all threads joined over each warp, the CTA and the cluster, always in the
+// same order, so that every thread of the cluster has the same result.
+struct Cluster {
+    Shared &sh;
+    uint32_t ctas, rank;
+    int turn = 0;
+
+    // After a warp's part is in x (in lane 0 at least): join(x) over the warps' parts in a
+    // warp's first lanes.
+    template <typename Join>
+    __device__ __forceinline__ const float4 *share(float4 x, float4 none, Join join) {
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) sh.warp[threadIdx.x >> 5] = x;
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            x = lane < WARPS ? sh.warp[lane] : none;
+            x = join(x);
+        }
+        return exchange(sh, turn, ctas, rank, x);
+    }
+    __device__ __forceinline__ void soft(Soft &p, Soft &q, float c) {
+        float4 x = make_float4(p.m, p.s, q.m, q.s);
+        warp_soft(x, c);
+        const float4 *slots = share(x, make_float4(-INFINITY, 0.f, -INFINITY, 0.f), [c](float4 y) {
+            warp_soft(y, c);
+            return y;
+        });
+        float4 all[MAX_CLUSTER];
+        p.m = q.m = -INFINITY;
+#pragma unroll
+        for (uint32_t i = 0; i < MAX_CLUSTER; ++i) {
+            all[i] = slots[min(i, ctas - 1)];
+            p.m = fmaxf(p.m, all[i].x);
+            q.m = fmaxf(q.m, all[i].z);
+        }
+        p.s = q.s = 0.f;
+        const Top tp(p.m, c), tq(q.m, c);
+#pragma unroll
+        for (uint32_t i = 0; i < MAX_CLUSTER; ++i) {
+            float fp = tp.step(all[i].x, c), fq = tq.step(all[i].z, c);
+            if (!(Top::is_weight(fp) && Top::is_weight(fq))) {
+                fp = odd_weight(all[i].x, p.m, c);
+                fq = odd_weight(all[i].z, q.m, c);
+            }
+            p.s += i < ctas ? all[i].y * fp : 0.f;
+            q.s += i < ctas ? all[i].w * fq : 0.f;
         }
     }
-    const float4 *slots = exchange(sh, turn, ctas, rank, x);
-    float4 r = slots[0];
-    for (uint32_t i = 1; i < ctas; ++i) r = join(r, slots[i]);
-    return r;
-}
-
-// A slice [lo, hi) of a row in chunks of eight that begin on 16-byte boundaries of the
-// row, with single elements before and behind: body(first element, count, chunk of a,
-// chunk of b), b another row of the same type or nullptr.  A thread's elements come in
-// ascending order.
-template <typename T, int U, typename Body>
-__device__ __forceinline__ void each_chunk(const T *a, const T *b, int lo, int hi, Body body) {
-    const int head = min(hi - lo, (int)((-(reinterpret_cast<uintptr_t>(a + lo) / sizeof(T))) % (16 / sizeof(T))));
-    const int first = lo + head, chunks = (hi - first) / 8, tail = first + chunks * 8;
-    const bool vec = b == nullptr || vec_ok(b + first);
-    // fewer than eight before and eight behind
-    auto one = [&](int at, bool there) {
-        if (!there) return;
-        float xs[8], ys[8];
+    __device__ __forceinline__ float sum(float v) {
+        const auto over_warp = [](float4 x) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) xs[i] = ys[i] = -INFINITY;
-        xs[0] = value(a[at]);
-        if (b != nullptr) ys[0] = value(b[at]);
-        body(at, 1, xs, ys);
-    };
-    one(lo + (int)threadIdx.x, (int)threadIdx.x < head);
-    for (int c0 = threadIdx.x; c0 < chunks; c0 += U * THREADS) {
-        Chunk<T> x[U], y[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (c0 + i * THREADS < chunks) {
-                const int at = first + (c0 + i * THREADS) * 8;
-                x[i].load(a + at, true);
-                if (b != nullptr) y[i].load(b + at, vec);
-            }
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (c0 + i * THREADS < chunks) {
-                float xs[8], ys[8];
-                x[i].get(xs);
-                if (b != nullptr) y[i].get(ys);
-                body(first + (c0 + i * THREADS) * 8, 8, xs, ys);
-            }
+            for (int o = 16; o > 0; o >>= 1) x.x += __shfl_xor_sync(ALL, x.x, o);
+            return x;
+        };
+        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 *slots = share(over_warp(make_float4(v, 0.f, 0.f, 0.f)), none, over_warp);
+        float r = 0.f;
+        for (uint32_t i = 0; i < ctas; ++i) r += slots[i].x;
+        return r;
     }
-    one(tail + (int)threadIdx.x, (int)threadIdx.x < hi - tail);
+    // The index that goes with the largest key.
+    __device__ __forceinline__ int best(unsigned long long key) {
+        const auto pack = [](unsigned long long k) {
+            return make_float4(__uint_as_float((uint32_t)(k >> 32)), __uint_as_float((uint32_t)k), 0.f, 0.f);
+        };
+        const auto unpack = [](float4 x) {
+            return (unsigned long long)__float_as_uint(x.x) << 32 | __float_as_uint(x.y);
+        };
+        const auto over_warp = [&](float4 x) {
+            unsigned long long k = unpack(x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(ALL, k, o));
+            return pack(k);
+        };
+        const float4 *slots = share(over_warp(pack(key)), pack(0), over_warp);
+        unsigned long long r = 0;
+        for (uint32_t i = 0; i < ctas; ++i) r = max(r, unpack(slots[i]));
+        return best_index(r);
+    }
+};
+
+// A slice [lo, hi) of a row of the vocabulary, or of two of the same type (b may be
+// nullptr), in chunks of eight that begin on a's 16-byte boundaries, for NT threads.  Fewer
+// than eight elements before the first and behind the last come by themselves.
+template <typename T, int NT>
+struct Slice {
+    const T *a, *b;
+    int lo, hi, first, chunks;
+    bool vec;
+
+    __device__ __forceinline__ Slice(const T *a_, const T *b_, int lo_, int hi_) : a(a_), b(b_), lo(lo_), hi(hi_) {
+        const int head = (int)((-(reinterpret_cast<uintptr_t>(a + lo) / sizeof(T))) % (16 / sizeof(T)));
+        first = lo + min(hi - lo, head);
+        chunks = (hi - first) / 8;
+        vec = b == nullptr || vec_ok(b + first);
+    }
+    // This thread's part, in ascending order: many(first element, chunk of a, of b, of e),
+    // NT chunks from one to the next, one(element) for the others.  A chunk's successors are
+    // loaded before it is used (DEPTH of them); the loop stays rolled, its code is fetched once.
+    template <int DEPTH, bool E, typename Many, typename One>
+    __device__ __forceinline__ void each(const float *e, Many many, One one) const {
+        const int tail = first + chunks * 8;
+        const bool evec = E && vec_ok(e + first);
+        if (lo + (int)threadIdx.x < first) one(lo + (int)threadIdx.x);
+        Chunk<T> x[DEPTH + 1], y[DEPTH + 1];
+        Chunk<float> z[DEPTH + 1];
+        const auto fetch = [&](int d, int k) {
+            if (k >= chunks) return;
+            const int at = first + k * 8;
+            x[d].load(a + at, true);
+            if (b != nullptr) y[d].load(b + at, vec);
+            if (E) z[d].load(e + at, evec);
+        };
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) fetch(d, threadIdx.x + d * NT);
+#pragma unroll 1
+        for (int k = threadIdx.x; k < chunks; k += NT) {
+            fetch(DEPTH, k + DEPTH * NT);
+            many(first + k * 8, x[0], y[0], z[0]);
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d) {
+                x[d] = x[d + 1];
+                y[d] = y[d + 1];
+                if (E) z[d] = z[d + 1];
+            }
+        }
+        if (tail + (int)threadIdx.x < hi) one(tail + (int)threadIdx.x);
+    }
+    // The thread to whose part the element belongs (-1: none of this slice's).
+    __device__ __forceinline__ int owner(int at) const {
+        const int tail = first + chunks * 8;
+        if (at < lo || at >= hi) return -1;
+        return at < first ? at - lo : at >= tail ? at - tail : (at - first) / 8 % NT;
+    }
+    // Brings it into L2, a line a thread at a time.
+    static __device__ __forceinline__ void prefetch(const void *row, int lo, int hi, int size) {
+        const char *p = static_cast<const char *>(row) + (int64_t)lo * size;
+        const uint32_t bytes = (uint32_t)(hi - lo) * (uint32_t)size;  // (2^31 elements of a cluster's slice: below 2^32)
+        for (uint32_t i = threadIdx.x * 128; i < bytes; i += NT * 128) ptx::prefetch_l2(p + i);
+    }
+};
+
+// What a thread's part of a row's slice comes to: the largest logit's key where nothing
+// is drawn, else maximum and sum.
+template <typename T, int NT>
+__device__ __forceinline__ unsigned long long slice_best(const Slice<T, NT> &sl) {
+    float top = -INFINITY;
+    int where = -1;
+    const auto take = [&](float v, int i) {
+        if (v > top) {
+            top = v;
+            where = i;
+        }
+    };
+    sl.template each<3, false>(
+        nullptr,
+        [&](int at, const Chunk<T> &x, const Chunk<T> &, const Chunk<float> &) {
+            if (x.top() > top) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = x.pair(i);
+                    take(v.x, at + 2 * i);
+                    take(v.y, at + 2 * i + 1);
+                }
+            }
+        },
+        [&](int at) { take(value(sl.a[at]), at); });
+    return best_key(top, where);
+}
+template <typename T, int NT>
+__device__ __forceinline__ void slice_soft(const Slice<T, NT> &sl, Soft &p, Soft &q, float c) {
+    sl.template each<2, false>(
+        nullptr,
+        [&](int, const Chunk<T> &x, const Chunk<T> &y, const Chunk<float> &) {
+            p.add(x, c);
+            if (sl.b != nullptr) q.add(y, c);
+        },
+        [&](int at) {
+            p.add(value(sl.a[at]), c);
+            if (sl.b != nullptr) q.add(value(sl.b[at]), c);
+        });
 }
 
+// A sequence's rows, and how its temperature is taken.
+struct Sequence {
+    int begin, n;
+    bool bad, draws;
+    float c;
+    __device__ __forceinline__ Sequence(const VerifyParams &p, int b) {
+        begin = p.cu[b];
+        const int end = p.cu[b + 1];
+        bad = begin < 0 || end < begin || end > p.total || end - begin > p.width;
+        n = bad ? 0 : end - begin;
+        const float temp = p.temperature != nullptr ? p.temperature[b] : 0.f;
+        draws = temp > 0.f;  // (NaN: no)
+        // (bounded: the largest logit's 0 times it has to be 0)
+        c = draws ? fminf(1.4426950408889634f / temp, 1e30f) : 0.f;
+    }
+};
+
+// Sums all rows up ahead of the walk: a CTA a slice of a row (blockIdx.x: sequence, node,
+// target or draft, slice), its part to `sums`.  Few threads with many elements each: what a
+// thread does besides its elements (its row, the joining of sums) is worth a hundred.
 template <typename T>
-__global__ void __launch_bounds__(THREADS, 2) verify_kernel(const VerifyParams p, int slice) {
+__global__ void __launch_bounds__(SUM_THREADS) sums_kernel(const VerifyParams p) {
     ptx::wait_for_prior_work();
     ptx::allow_next_work();
-    constexpr int U = sizeof(T) == 2 ? 2 : 1;
+    constexpr int W = SUM_THREADS / 32;
+    __shared__ float4 warp[W];
+    const unsigned kinds = p.draft != nullptr ? 2 : 1;
+    const unsigned row_x = blockIdx.x / (unsigned)p.pieces, piece = blockIdx.x - row_x * (unsigned)p.pieces;
+    const unsigned node = row_x / kinds, kind = row_x - node * kinds;
+    const unsigned b = node / (unsigned)p.width, i = node - b * (unsigned)p.width;
+    const Sequence seq(p, b);
+    if ((int)i >= seq.n || (kind == 1 && !seq.draws)) return;
+    const int64_t row = seq.begin + (int)i;
+    const T *data = kind == 0 ? static_cast<const T *>(p.logits) + row * p.logits_stride
+                              : static_cast<const T *>(p.draft) + row * p.draft_stride;
+    const int lo = (int)piece * p.piece, hi = min(p.V, lo + p.piece), lane = threadIdx.x & 31;
+    const Slice<T, SUM_THREADS> sl(data, nullptr, lo, hi);
+    float2 *out = p.sums + ((int64_t)kind * p.total + row) * p.pieces + piece;
+    if (!seq.draws) {
+        auto *keys = reinterpret_cast<unsigned long long *>(warp);
+        unsigned long long k = slice_best(sl);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(ALL, k, o));
+        if (lane == 0) keys[threadIdx.x >> 5] = k;
+        __syncthreads();
+        if (threadIdx.x != 0) return;
+#pragma unroll
+        for (int j = 1; j < W; ++j) k = max(k, keys[j]);
+        *reinterpret_cast<unsigned long long *>(out) = k;
+        return;
+    }
+    Soft sp, none;
+    slice_soft(sl, sp, none, seq.c);
+    float4 v = make_float4(sp.m, sp.s, -INFINITY, 0.f);
+    warp_soft(v, seq.c);
+    if (lane == 0) warp[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    Soft all;
+#pragma unroll
+    for (int j = 0; j < W; ++j) all.add(warp[j].x, warp[j].y, seq.c);
+    *out = make_float2(all.m, all.s);
+}
+
+// What is left of p where `stages` siblings were rejected, one after the other: p - q, no
+// less than 0, times 1 / the sum of that (0: nothing was left, p stays); the sum of the last
+// stage is open where stages > known, which the race does not mind.
+__device__ __forceinline__ float rest(float pw, float qw, int stages, int known, const float *inv_left) {
+    for (int k = 0; k < stages; ++k) {
+        const float t = fmaxf(pw - qw, 0.f);
+        if (k == known)
+            pw = t;
+        else if (inv_left[k] > 0.f)
+            pw = t * inv_left[k];
+    }
+    return pw;
+}
+
+// The two distributions at a node, from the rows' maxima and sums.
+struct Node {
+    Top tp, tq;
+    float ip, iq, c;
+    bool plain;  // weights that are plain numbers need no second look (see Top)
+    __device__ __forceinline__ Node(const Soft &p, const Soft &q, float c_)
+        : tp(p.m, c_), tq(q.m, c_), ip(p.s > 0.f ? 1.f / p.s : 0.f), iq(q.s > 0.f ? 1.f / q.s : 0.f), c(c_) {
+        plain = tp.m < FLT_MAX && tp.r == tp.r && tq.m < FLT_MAX && tq.r == tq.r;
+    }
+    // p - q of a token in plain rows (q of a NaN: 0).
+    __device__ __forceinline__ float difference(float x, float y) const {
+        const float q = ptx::ex2(fmaf(y, c, -tq.r));
+        return fmaf(ptx::ex2(fmaf(x, c, -tp.r)), ip, -(q <= 2.f ? q : 0.f) * iq);
+    }
+};
+
+// The general case of what is left of a token's p, for a node's rows of any numbers.
+__device__ __noinline__ float odd_rest(float x, float y, float pm, float qm, float ip, float iq, float c, int stages,
+                                       int known, const float *inv_left) {
+    const float w = odd_weight(x, pm, c);
+    return stages == 0 ? w : rest(w * ip, odd_weight(y, qm, c) * iq, stages, known, inv_left);
+}
+
+// Where a sequence's walk has ended: what the race for its last token needs.
+struct WalkEnd {
+    int row;               // of logits (and draft); -1: nothing is drawn
+    int place;             // of the token in out_tokens
+    int rejected, known;   // children, and how many of them are in inv_left
+    float pm, ps, qm, qs;  // the rows' maxima and sums
+    float c;
+    unsigned done;              // CTAs of the race that have arrived
+    unsigned long long best;    // the largest key so far
+};
+static_assert(sizeof(WalkEnd) <= WALK_END_BYTES, "a sequence's place in the workspace");
+
+// The walk down a sequence's tree, a cluster of CTAs each.  AHEAD: the rows' sums are there.
+template <typename T, bool AHEAD>
+__global__ void __launch_bounds__(THREADS, 1) verify_kernel(const VerifyParams p, int slice) {
+    ptx::wait_for_prior_work();
+    ptx::allow_next_work();
+    ptx::cluster_arrive();
+    using Part = Slice<T, THREADS>;
     __shared__ Shared sh;
     const int tid = threadIdx.x;
     const uint32_t rank = ptx::cluster_rank(), ctas = (uint32_t)((p.V + slice - 1) / slice);
     const int b = blockIdx.x / ctas;
     const int lo = (int)rank * slice, hi = min(p.V, lo + slice);
-    const int begin = p.cu[b], end = p.cu[b + 1];
-    const bool bad = begin < 0 || end < begin || end > p.total || end - begin > p.width;
-    if (bad && rank == 0 && tid == 0) report_status(p.status, kStatusDeviceBounds, kSiteVerifyOffsets);
-    const int n = bad ? 0 : end - begin;
+    const Sequence seq(p, b);
+    const int begin = seq.begin, n = seq.n;
+    if (seq.bad && rank == 0 && tid == 0) report_status(p.status, kStatusDeviceBounds, kSiteVerifyOffsets);
     int32_t *path_out = p.path + (int64_t)b * p.width, *tokens_out = p.out_tokens + (int64_t)b * p.width;
-    if (n == 0) {  // (the same in every CTA of the cluster)
+    WalkEnd *walk_end = p.ends != nullptr ? reinterpret_cast<WalkEnd *>(p.ends + (int64_t)b * WALK_END_BYTES) : nullptr;
+    ptx::cluster_wait();  // every CTA of the cluster runs: its shared memory may be written
+    if (n == 0) {         // (the same in every CTA of the cluster)
         if (rank == 0) {
             for (int j = tid; j < p.width; j += THREADS) path_out[j] = tokens_out[j] = -1;
             if (tid == 0) p.counts[b] = 0;
+            if (tid == 0 && walk_end != nullptr) walk_end->row = -1;
         }
         return;
     }
-    const float temp = p.temperature != nullptr ? p.temperature[b] : 0.f;
-    const bool draws = temp > 0.f;  // (NaN: no)
-    // (bounded: the largest logit's 0 times it has to be 0)
-    const float c = draws ? fminf(1.4426950408889634f / temp, 1e30f) : 0.f;
-    const T *draft = draws ? static_cast<const T *>(p.draft) : nullptr;
+    const bool draws = seq.draws;
+    const float c = seq.c;
+    const T *logits = static_cast<const T *>(p.logits) + begin * p.logits_stride;
+    const T *draft = draws && p.draft != nullptr ? static_cast<const T *>(p.draft) + begin * p.draft_stride : nullptr;
+    // (the race reads it, whatever is accepted)
+    if (draws) Part::prefetch(p.noise + (int64_t)b * p.noise_stride, lo, hi, sizeof(float));
     for (int i = tid; i < n; i += THREADS) {
         int up = p.parents[begin + i], token = p.tokens[begin + i];
         if (up < -1 || up >= i) {
@@ -250,22 +575,44 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const VerifyParams p
         sh.parent[i] = up;
         sh.token[i] = token;
         sh.u[i] = draws ? p.uniforms[begin + i] : 0.f;
+        if (AHEAD) {
+            // Its own row's sums, and its logits in its parent's row.
+            if (draws) {
+                const bool there = up >= 0 && token >= 0;
+                const float px = there ? value(logits[up * p.logits_stride + token]) : -INFINITY;
+                const float qx = there && draft != nullptr ? value(draft[up * p.draft_stride + token]) : -INFINITY;
+                Soft s[2];
+#pragma unroll
+                for (int kind = 0; kind < 2; ++kind) {
+                    if (kind == 1 && draft == nullptr) break;
+                    const float2 *part = p.sums + ((int64_t)kind * p.total + begin + i) * p.pieces;
+#pragma unroll 4
+                    for (int k = 0; k < p.pieces; ++k) s[kind].add(part[k].x, part[k].y, c);
+                }
+                sh.stat[i] = make_float4(s[0].m, s[0].s, s[1].m, s[1].s);
+                sh.px[i] = px;
+                sh.qx[i] = qx;
+            } else {
+                const auto *part = reinterpret_cast<const unsigned long long *>(p.sums) + (int64_t)(begin + i) * p.pieces;
+                unsigned long long k = 0;
+#pragma unroll 4
+                for (int j = 0; j < p.pieces; ++j) k = max(k, part[j]);
+                sh.stat[i].x = __int_as_float(best_index(k));
+            }
+        }
     }
     __syncthreads();
 
-    int turn = 0, cur = 0, count = 1, last = -1;
+    Cluster all{sh, ctas, rank};
+    int cur = 0, count = 1, last = -1, rejected = 0, known = 0;
+    Soft sp, sq;
     for (;;) {
-        const T *row = static_cast<const T *>(p.logits) + (int64_t)(begin + cur) * p.logits_stride;
-        const T *drow = draft != nullptr ? draft + (int64_t)(begin + cur) * p.draft_stride : nullptr;
-        // The children's own logits, on their way during the pass.
-        float px = -INFINITY, qx = -INFINITY;
-        const bool child = tid < n && tid > cur && sh.parent[tid] == cur && sh.token[tid] >= 0;
-        if (child && draws) {
-            px = value(row[sh.token[tid]]);
-            if (drow != nullptr) qx = value(drow[sh.token[tid]]);
-        }
+        const T *row = logits + cur * p.logits_stride;
+        const T *drow = draft != nullptr ? draft + cur * p.draft_stride : nullptr;
         int next = -1;
-        // The node's children in order: f(child) says whether it is accepted.
+        // The node's children in order: f(child) says whether it is accepted.  (No thread
+        // writes to shared memory what another reads here without a barrier: a warp may
+        // be a node ahead of another.)
         auto each_child = [&](auto f) {
             for (int i0 = (cur + 1) & ~31; i0 < n && next < 0; i0 += 32) {
                 const int i = i0 + (tid & 31);
@@ -277,147 +624,91 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const VerifyParams p
             }
         };
         if (!draws) {
-            Best best;
-            best.v = -INFINITY;
-            each_chunk<T, U>(row, static_cast<const T *>(nullptr), lo, hi,
-                             [&](int at, int k, const float (&x)[8], const float (&)[8]) {
-#pragma unroll
-                                 for (int i = 0; i < 8; ++i)
-                                     if (x[i] > best.v) {
-                                         best.v = x[i];
-                                         best.i = at + i;
-                                     }
-                             });
-            const float4 r = reduce(sh, turn, ctas, rank, make_float4(best.v, __int_as_float(best.i), 0.f, 0.f),
-                                    [](float4 x, float4 y) {
-                                        Best q;
-                                        q.v = x.x;
-                                        q.i = __float_as_int(x.y);
-                                        q.join(y.x, __float_as_int(y.y));
-                                        return make_float4(q.v, __int_as_float(q.i), 0.f, 0.f);
-                                    });
-            last = __float_as_int(r.y);
+            if (AHEAD) {
+                last = __float_as_int(sh.stat[cur].x);
+            } else {
+                Part::prefetch(row, lo, hi, sizeof(T));
+                last = all.best(slice_best(Part(row, nullptr, lo, hi)));
+            }
             if (last >= 0) each_child([&](int k) { return sh.token[k] == last; });
         } else {
-            Soft sp, sq;
-            each_chunk<T, U>(row, drow, lo, hi, [&](int, int, const float (&x)[8], const float (&y)[8]) {
-                sp.add(x, c);
-                if (drow != nullptr) sq.add(y, c);
-            });
-            if (child) {
-                sh.px[tid] = px;
-                sh.qx[tid] = qx;
-            }
-            const float4 r = reduce(sh, turn, ctas, rank, make_float4(sp.m, sp.s, sq.m, sq.s), [c](float4 x, float4 y) {
-                Soft a, d;
-                a.m = x.x, a.s = x.y, d.m = x.z, d.s = x.w;
-                a.join(y.x, y.y, c);
-                d.join(y.z, y.w, c);
-                return make_float4(a.m, a.s, d.m, d.s);
-            });
-            const float mp = r.x, mq = r.z, ip = r.y > 0.f ? 1.f / r.y : 0.f, iq = r.w > 0.f ? 1.f / r.w : 0.f;
-            // Rejected siblings so far, and how many of them are in inv_left.
-            int rejected = 0, known = 0;
-            float left = r.y;  // without draft: what is left of the weights' sum
-            // What is left of p where `stages` siblings are rejected, with the last one's
-            // sum still open where stages > known.
-            auto rest = [&](float pw, float qw, int stages) {
-                for (int k = 0; k < stages; ++k) {
-                    const float t = fmaxf(pw - qw, 0.f);
-                    if (k == known)
-                        pw = t;
-                    else if (sh.inv_left[k] > 0.f)
-                        pw = t * sh.inv_left[k];
+            const Part rows(row, drow, lo, hi);
+            sp = sq = Soft();
+            if (AHEAD) {
+                const float4 st = sh.stat[cur];
+                sp.m = st.x, sp.s = st.y, sq.m = st.z, sq.s = st.w;
+            } else {
+                Part::prefetch(row, lo, hi, sizeof(T));
+                if (drow != nullptr) Part::prefetch(drow, lo, hi, sizeof(T));
+                // The children's own logits, on their way during the pass.
+                float px = -INFINITY, qx = -INFINITY;
+                const bool child = tid < n && tid > cur && sh.parent[tid] == cur && sh.token[tid] >= 0;
+                if (child) {
+                    px = value(row[sh.token[tid]]);
+                    if (drow != nullptr) qx = value(drow[sh.token[tid]]);
                 }
-                return pw;
-            };
-            auto rejected_token = [&](int token) {  // of this node's rejected children: the first `rejected`
-                int seen = 0;
-                for (int i = cur + 1; i < n && seen < rejected; ++i)
-                    if (sh.parent[i] == cur) {
-                        ++seen;
-                        if (sh.token[i] == token) return true;
-                    }
-                return false;
-            };
+                slice_soft(rows, sp, sq, c);
+                if (child) {
+                    sh.px[tid] = px;
+                    sh.qx[tid] = qx;
+                }
+                all.soft(sp, sq, c);
+            }
+            const Node node(sp, sq, c);
+            rejected = known = 0;
+            float left = sp.s;  // without draft: what is left of the weights' sum
             each_child([&](int k) {
-                const float w = sh.token[k] >= 0 ? weight(sh.px[k], mp, c) : 0.f;
+                const int token = sh.token[k];
+                const float w = token >= 0 ? node.tp.weight(sh.px[k], c) : 0.f;
                 if (draft == nullptr) {
-                    const float mine = w > 0.f && rejected > 0 && rejected_token(sh.token[k]) ? 0.f : w;
+                    bool again = false;  // the token of an earlier sibling, which has been rejected
+                    if (rejected > 0)
+                        for (int i0 = cur + 1; i0 < k; i0 += 32) {
+                            const int i = i0 + (tid & 31);
+                            again = again || __any_sync(ALL, i < k && sh.parent[i < k ? i : 0] == cur &&
+                                                                 sh.token[i < k ? i : 0] == token);
+                        }
+                    const float mine = again ? 0.f : w;
                     if (sh.u[k] * left < mine) return true;
                     left = fmaxf(left - mine, 0.f);
                 } else {
                     if (rejected > known) {  // the sum that the last rejection left
                         float sum = 0.f;
-                        each_chunk<T, 1>(row, drow, lo, hi, [&](int, int, const float (&x)[8], const float (&y)[8]) {
+                        const bool simple = node.plain && rejected == 1;
+                        const auto add = [&](float x, float y) {
+                            sum += simple ? fmaxf(node.difference(x, y), 0.f)
+                                          : odd_rest(x, y, sp.m, sq.m, node.ip, node.iq, c, rejected, known, sh.inv_left);
+                        };
+                        rows.template each<1, false>(
+                            nullptr,
+                            [&](int, const Chunk<T> &x, const Chunk<T> &y, const Chunk<float> &) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                sum += rest(weight(x[i], mp, c) * ip, weight(y[i], mq, c) * iq, rejected);
-                        });
-                        const float4 z = reduce(sh, turn, ctas, rank, make_float4(sum, 0.f, 0.f, 0.f),
-                                                [](float4 x, float4 y) { return make_float4(x.x + y.x, 0.f, 0.f, 0.f); });
-                        if (tid == 0) sh.inv_left[known] = z.x > 0.f ? 1.f / z.x : 0.f;
+                                for (int i = 0; i < 4; ++i) {
+                                    const float2 v = x.pair(i), q = y.pair(i);
+                                    add(v.x, q.x);
+                                    add(v.y, q.y);
+                                }
+                            },
+                            [&](int at) { add(value(row[at]), value(drow[at])); });
+                        const float z = all.sum(sum);
+                        if (tid == 0) sh.inv_left[known] = z > 0.f ? 1.f / z : 0.f;
                         __syncthreads();
                         ++known;
                     }
-                    const float q = sh.token[k] >= 0 ? weight(sh.qx[k], mq, c) * iq : 0.f;
-                    if (sh.u[k] * q < rest(w * ip, q, rejected)) return true;
+                    const float q = token >= 0 ? node.tq.weight(sh.qx[k], c) * node.iq : 0.f;
+                    if (sh.u[k] * q < rest(w * node.ip, q, rejected, known, sh.inv_left)) return true;
                 }
                 ++rejected;
                 return false;
             });
-            if (next < 0) {
-                // The race.  Where the last rejection left nothing, of what was left before it
-                // (without draft: of all tokens).
-                const float *noise = p.noise + (int64_t)b * p.noise_stride;
-                for (int attempt = 0; attempt < 2; ++attempt) {
-                    Best best;
-                    best.v = 0.f;
-                    const bool subtract = draft != nullptr && rejected > 0;
-                    each_chunk<T, 1>(row, subtract ? drow : static_cast<const T *>(nullptr), lo, hi,
-                                     [&](int at, int k, const float (&x)[8], const float (&y)[8]) {
-                                         Chunk<float> e8;
-                                         float e[8];
-                                         if (k == 8) {
-                                             e8.load(noise + at, vec_ok(noise + at));
-                                             e8.get(e);
-                                         } else {
-                                             e[0] = noise[at];
-                                         }
-#pragma unroll
-                                         for (int i = 0; i < 8; ++i) {
-                                             if (i >= k) break;
-                                             float w = weight(x[i], mp, c);
-                                             if (subtract) w = rest(w * ip, weight(y[i], mq, c) * iq, rejected);
-                                             if (!(w > 0.f)) continue;
-                                             const float v = __fdividef(w, e[i]);
-                                             if (v > best.v && (draft != nullptr || rejected == 0 || !rejected_token(at + i))) {
-                                                 best.v = v;
-                                                 best.i = at + i;
-                                             }
-                                         }
-                                     });
-                    const float4 z = reduce(sh, turn, ctas, rank, make_float4(best.v, __int_as_float(best.i), 0.f, 0.f),
-                                            [](float4 x, float4 y) {
-                                                Best q;
-                                                q.v = x.x;
-                                                q.i = __float_as_int(x.y);
-                                                q.join(y.x, __float_as_int(y.y));
-                                                return make_float4(q.v, __int_as_float(q.i), 0.f, 0.f);
-                                            });
-                    last = __float_as_int(z.y);
-                    if (last >= 0 || rejected == 0) break;
-                    rejected = draft != nullptr ? known : 0;
-                }
-            }
         }
         if (next < 0) break;
         if (tid == 0) sh.path[count] = next;
         ++count;
         cur = next;
     }
-    // No CTA may write into another's shared memory once that has left: the last exchange's
-    // barrier was behind its stores.
+    // (No CTA writes into another's shared memory once that has left: the last exchange's
+    // barrier was behind its stores.)
     __syncthreads();
     if (rank != 0) return;
     for (int j = tid; j < p.width; j += THREADS) {
@@ -425,19 +716,151 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const VerifyParams p
         tokens_out[j] = j < count - 1 ? sh.token[sh.path[j + 1]] : j == count - 1 ? last : -1;
     }
     if (tid == 0) p.counts[b] = count;
+    if (walk_end == nullptr) return;
+    if (tid == 0)
+        *walk_end = WalkEnd{draws ? begin + cur : -1, count - 1, rejected, known, sp.m, sp.s, sq.m, sq.s, c, 0u, 0ull};
+    // The rejected children's tokens are out of the race (without draft), or the sums that
+    // their rejections left.
+    if (draws && rejected > 0) {
+        auto *list = reinterpret_cast<float *>(p.ends + (int64_t)p.B * WALK_END_BYTES) + (int64_t)b * p.width;
+        if (draft != nullptr) {
+            for (int k = tid; k < known; k += THREADS) list[k] = sh.inv_left[k];
+        } else if (tid < 32) {
+            int k = 0;
+            for (int i0 = (cur + 1) & ~31; i0 < n; i0 += 32) {
+                const int i = i0 + tid;
+                const bool mine = i > cur && i < n && sh.parent[i < n ? i : 0] == cur;
+                const unsigned m = __ballot_sync(ALL, mine);
+                if (mine) list[k + __popc(m & ((1u << tid) - 1u))] = __int_as_float(sh.token[i]);
+                k += __popc(m);
+            }
+        }
+    }
 }
 
-}  // namespace vf
+// The race for the last tokens: argmax of what is left of p over the noise.  A CTA a slice
+// of a sequence's vocabulary; the largest key of all slices is found with atomics, whose
+// order changes nothing in it, and the CTA that comes last writes the token.
+template <typename T>
+__global__ void __launch_bounds__(RACE_THREADS, RACE_BLOCKS) race_kernel(const VerifyParams p, int slice, int slices) {
+    ptx::wait_for_prior_work();
+    ptx::allow_next_work();
+    constexpr int W = RACE_THREADS / 32;
+    __shared__ unsigned long long keys[W];
+    __shared__ float list[ATTN_TREE_MAX];  // the rejected tokens, or inv_left
+    __shared__ int final;
+    const int tid = threadIdx.x;
+    const int b = blockIdx.x / slices, piece = blockIdx.x - b * slices;
+    WalkEnd *walk_end = reinterpret_cast<WalkEnd *>(p.ends + (int64_t)b * WALK_END_BYTES);
+    const int at_row = walk_end->row;
+    if (at_row < 0) return;
+    const int place = walk_end->place, known = walk_end->known;
+    int rejected = walk_end->rejected;
+    Soft sp, sq;
+    sp.m = walk_end->pm, sp.s = walk_end->ps, sq.m = walk_end->qm, sq.s = walk_end->qs;
+    const float c = walk_end->c;
+    const Node node(sp, sq, c);
+    const T *row = static_cast<const T *>(p.logits) + at_row * p.logits_stride;
+    const T *drow = p.draft != nullptr ? static_cast<const T *>(p.draft) + at_row * p.draft_stride : nullptr;
+    const float *noise = p.noise + (int64_t)b * p.noise_stride;
+    const bool drafted = p.draft != nullptr;
+    {
+        const auto *from = reinterpret_cast<const float *>(p.ends + (int64_t)p.B * WALK_END_BYTES) + (int64_t)b * p.width;
+        for (int k = tid; k < (drafted ? known : rejected); k += RACE_THREADS) list[k] = from[k];
+    }
+    __syncthreads();
+    int lo = piece * slice, hi = min(p.V, lo + slice);
+    for (int attempt = 0;; ++attempt) {
+        const bool subtract = drafted && rejected > 0;
+        const Slice<T, RACE_THREADS> race(row, subtract ? drow : nullptr, lo, hi);
+        // Without draft the rejected tokens, all the node's children's, are out: only the
+        // threads that come to one look out for them.
+        const int outs = drafted ? 0 : rejected;
+        bool watch = false;
+        for (int k = 0; k < outs; ++k) watch = watch || race.owner(__float_as_int(list[k])) == tid;
+        float top = 0.f;
+        int where = -1;
+        const auto take = [&](float w, float e, int i) {
+            const float v = w * ptx::rcp(e);
+            if (v > top) {  // (no NaN: of 0 times infinity, or e's)
+                bool out = false;
+                if (watch)
+                    for (int k = 0; k < outs; ++k) out = out || __float_as_int(list[k]) == i;
+                if (!out) {
+                    top = v;
+                    where = i;
+                }
+            }
+        };
+        const auto run = [&](auto weight_of) {
+            race.template each<0, true>(
+                noise,
+                [&](int at, const Chunk<T> &x, const Chunk<T> &y, const Chunk<float> &e) {
+                    float w[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 v = x.pair(i), q = y.pair(i);
+                        w[2 * i] = weight_of(v.x, q.x);
+                        w[2 * i + 1] = weight_of(v.y, q.y);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) take(w[i], i & 1 ? e.pair(i >> 1).y : e.pair(i >> 1).x, at + i);
+                },
+                [&](int at) { take(weight_of(value(row[at]), subtract ? value(drow[at]) : 0.f), noise[at], at); });
+        };
+        if (node.plain && !subtract)
+            run([&](float x, float) { return ptx::ex2(fmaf(x, c, -node.tp.r)); });
+        else if (node.plain && rejected == 1 && known == 0)
+            run([&](float x, float y) { return node.difference(x, y); });
+        else
+            run([&](float x, float y) {
+                return odd_rest(x, y, sp.m, sq.m, node.ip, node.iq, c, subtract ? rejected : 0, known, list);
+            });
+        unsigned long long key = best_key(top, where);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(ALL, key, o));
+        if ((tid & 31) == 0) keys[tid >> 5] = key;
+        __syncthreads();
+        if (tid == 0) {
+#pragma unroll
+            for (int k = 1; k < W; ++k) key = max(key, keys[k]);
+            if (attempt == 0) {
+                atomicMax(&walk_end->best, key);
+                __threadfence();
+                final = atomicAdd(&walk_end->done, 1u) == (unsigned)slices - 1;
+                __threadfence();
+                key = atomicMax(&walk_end->best, 0ull);
+            }
+            // Where the last rejection left nothing, of what was left before it (without
+            // draft: of all tokens), the last CTA by itself: it takes rounding, or numbers
+            // not below 1, to get here.
+            if (final && (key != 0 || rejected == 0 || attempt > 0)) {
+                p.out_tokens[(int64_t)b * p.width + place] = best_index(key);
+                final = 0;
+            }
+        }
+        __syncthreads();
+        if (!final) return;
+        rejected = drafted ? known : 0;
+        lo = 0;
+        hi = p.V;
+    }
+}
 
-cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream) {
-    // CTAs a sequence: as many as keep two on every SM, a slice of 4096 tokens at least.
-    int ctas = vf::MAX_CLUSTER;
-    while (ctas > 1 && ((int64_t)p.B * ctas > 304 || (int64_t)(ctas - 1) * 4096 >= p.V)) ctas /= 2;
-    int slice = ((p.V + ctas - 1) / ctas + 7) & ~7;
+template <typename T>
+cudaError_t launch(const VerifyParams &p, cudaStream_t stream) {
+    if (p.pieces > 0) {
+        const int64_t blocks = (int64_t)p.B * p.width * (p.draft != nullptr ? 2 : 1) * p.pieces;
+        const cudaError_t e = launch_dependent(sums_kernel<T>, dim3((unsigned)blocks), dim3(SUM_THREADS), 0, stream, p);
+        if (e != cudaSuccess) return e;
+    }
+    // CTAs a sequence: one an SM, a slice of 4096 tokens at least.
+    int ctas = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_CLUSTER, ((int64_t)p.V + 4095) / 4096, 152 / p.B}));
+    const int slice = ((p.V + ctas - 1) / ctas + 7) & ~7;
     ctas = (p.V + slice - 1) / slice;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.B * ctas);
-    cfg.blockDim = dim3(vf::THREADS);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -447,7 +870,30 @@ cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, p.fp32 ? vf::verify_kernel<float> : vf::verify_kernel<__nv_bfloat16>, p, slice);
+    const cudaError_t e = p.pieces > 0 ? cudaLaunchKernelEx(&cfg, verify_kernel<T, true>, p, slice)
+                                       : cudaLaunchKernelEx(&cfg, verify_kernel<T, false>, p, slice);
+    if (e != cudaSuccess || p.temperature == nullptr) return e;
+    // The race: as many CTAs as all SMs hold at once, a slice of 2048 tokens at least.
+    const int64_t each = std::max(1, RACE_BLOCKS * 152 / p.B), even = (p.V + each - 1) / each;
+    const int part = (int)((std::min<int64_t>(p.V, std::max<int64_t>(even, 2048)) + 7) & ~(int64_t)7);
+    const int slices = (p.V + part - 1) / part;
+    return launch_dependent(race_kernel<T>, dim3((unsigned)p.B * slices), dim3(RACE_THREADS), 0, stream, p, part, slices);
+}
+
+}  // namespace vf
+
+int verify_piece(int64_t rows, int vocab, int *pieces) {
+    // Eight CTAs for every SM where that takes no slice below 4096 tokens, 16384 at most.
+    const int64_t most = 16384, even = (rows * vocab + 1215) / 1216;
+    int64_t piece = even < 4096 ? 4096 : even > most ? most : even;
+    if (piece * 64 < vocab) piece = ((int64_t)vocab + 63) / 64;  // (64 a row at most)
+    piece = (piece + 7) & ~(int64_t)7;
+    *pieces = (int)((vocab + piece - 1) / piece);
+    return (int)piece;
+}
+
+cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream) {
+    return p.fp32 ? vf::launch<float>(p, stream) : vf::launch<__nv_bfloat16>(p, stream);
 }
 
 }  // namespace attn

@@ -605,6 +605,10 @@ typedef enum {
     ATTN_DTYPE_FP32 = 1
 } attn_dtype_t;
 
+/* Device workspace attn_verify_tree needs (a pure function; 0 where the arguments
+ * are invalid).  with_draft: whether draft_logits are given. */
+size_t attn_verify_tree_workspace_bytes(int B, int total, int vocab, int max_seqlen, int dtype, int with_draft);
+
 /*
  * attn_verify_tree -- speculative decoding: which drafted tokens of each
  * sequence's tree are kept, and the token that follows them, from given random
@@ -648,13 +652,16 @@ typedef enum {
  * counts as -1, and a sequence with bad offsets or more than max_seqlen rows gets no
  * nodes; each is recorded as ATTN_ERR_DEVICE_BOUNDS.  logits and draft_logits need
  * the alignment of their elements only; rows that are not 16-byte aligned are read a
- * little more slowly.  Deterministic.  No workspace.
+ * little more slowly.  Deterministic.
+ * workspace: DEVICE buffer of at least attn_verify_tree_workspace_bytes(...) bytes,
+ *      256-byte aligned, overwritten, one for each call that may run at the same time.
  */
 attn_status_t attn_verify_tree(const void *logits, const void *draft_logits, int dtype, const int32_t *tokens,
                                const int32_t *parents, const int32_t *cu_seqlens, const float *temperature,
                                const float *uniforms, const float *noise, int32_t *path, int32_t *out_tokens,
                                int32_t *counts, int B, int total, int vocab, int max_seqlen, size_t logits_stride,
-                               size_t draft_stride, size_t noise_stride, void *stream);
+                               size_t draft_stride, size_t noise_stride, void *workspace, size_t workspace_bytes,
+                               void *stream);
 
 /*
  * attn_compact_paged -- cut a paged cache down to the accepted path of each

@@ -95,6 +95,7 @@ def test_largest_tree():
     check(make(33, [256, 256], 50, "draft", tree="chain", sharp=0.3))
     check(make(34, [256], 300, "top", tree="bush", sharp=0.1))
     check(make(35, [256], 300, "draft", tree="bush", sharp=4.0))     # a sum for every sibling that is rejected
+    check(make(36, [16, 9], 9000, "draft", tree="bush", sharp=4.0))
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])

@@ -52,7 +52,7 @@ def test_tree_workspace_bytes(lib):
 
 
 VERIFY = dict(logits=16, draft=32, dtype=0, tok=4, par=4, cu=4, temp=4, u=4, noise=4, path=4, out=4, counts=4, B=2, total=9,
-              V=100, width=8, ls=100, ds=100, ns=100)
+              V=100, width=8, ls=100, ds=100, ns=100, ws=256, wsb=1 << 20)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -64,7 +64,7 @@ VERIFY = dict(logits=16, draft=32, dtype=0, tok=4, par=4, cu=4, temp=4, u=4, noi
     (dict(counts=3), 1), (dict(B=0), 1), (dict(B=1 << 29), 1), (dict(total=0), 1), (dict(V=0), 1),
     (dict(V=(1 << 31) - 1, ls=1 << 31, ds=1 << 31, ns=1 << 31), 1), (dict(width=0), 1), (dict(width=257), 1),
     (dict(ls=99), 1), (dict(ds=99), 1), (dict(ns=99), 1), (dict(ls=1 << 41), 1), (dict(ds=1 << 41), 1),
-    (dict(ns=1 << 41), 1),
+    (dict(ns=1 << 41), 1), (dict(ws=None), 5), (dict(ws=260), 5), (dict(wsb=100), 5),
 ])
 def test_verify_rejects_before_any_launch(lib, kw, code):
     assert lib.attn_verify_tree(*dict(VERIFY, **kw).values(), None) == code
