@@ -427,6 +427,7 @@ attn_status_t attn_fwd_tree_paged(const void *q, const void *k_pages, const void
                                       ATTN_LAYOUT_BSHD, scale);
     if (st != ATTN_OK) return st;
     if (page_size != 16 || Hq / Hkv > 128) return ATTN_ERR_UNSUPPORTED;
+    if (out == q) return ATTN_ERR_INVALID_ARG;  // (several CTAs read a query)
     if (B < 1 || max_seqlen_q < 1 || max_seqlen_q > ATTN_TREE_MAX) return ATTN_ERR_INVALID_ARG;
     if (!valid_round_mode(round_mode)) return ATTN_ERR_INVALID_ARG;
     // The line of K/V tiles, and the rows of the merge, are 32-bit.

@@ -49,7 +49,9 @@ static void verify_workspace(int B, int total, int max_seqlen, bool draft, int p
 extern "C" {
 
 size_t attn_verify_tree_workspace_bytes(int B, int total, int vocab, int max_seqlen, int dtype, int with_draft) {
-    if (B < 1 || total < 1 || vocab < 1 || max_seqlen < 1 || max_seqlen > ATTN_TREE_MAX) return 0;
+    if (B < 1 || total < 1 || vocab < 1 || vocab > 1 << 28 || max_seqlen < 1 ||
+        max_seqlen > ATTN_TREE_MAX)
+        return 0;
     if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_FP32) return 0;
     int piece, pieces;
     size_t ends, sums;
@@ -74,7 +76,7 @@ attn_status_t attn_verify_tree(const void *logits, const void *draft_logits, int
     if (temperature ? (!aligned(temperature, 4) || !ok4(uniforms) || !ok4(noise))
                     : (draft_logits || uniforms || noise))
         return ATTN_ERR_INVALID_ARG;
-    if (B < 1 || total < 1 || vocab < 1 || vocab > 0x7fffffff - 64 || max_seqlen < 1 || max_seqlen > ATTN_TREE_MAX)
+    if (B < 1 || total < 1 || vocab < 1 || vocab > 1 << 28 || max_seqlen < 1 || max_seqlen > ATTN_TREE_MAX)
         return ATTN_ERR_INVALID_ARG;
     // Blocks: a cluster a sequence, and in the race a slice of 2048 tokens.
     if (B > 0x7fffffff / 8 || (int64_t)B * (((int64_t)vocab + 2047) / 2048) > 0x7fffffff) return ATTN_ERR_INVALID_ARG;

@@ -729,7 +729,7 @@ template <int KIND>
 __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, const WaitCtx &wc, int lane,
                                const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mv,
                                const CUtensorMap *mk8, const CUtensorMap *mv8) {
-    if (p.inject == 1) return;
+    if (KIND != kTree && p.inject == 1) return;
     const uint64_t pol_q = ptx::policy_evict_first();
     const uint64_t pol_kv = ptx::policy_evict_last();
     int n = 0;            // ring items issued
@@ -741,7 +741,10 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
     Unit w;
     w.n_kv = -1;
     TreeShare share{};
-    if (KIND == kTree) share = tree_share(p, lane);
+    if (KIND == kTree) {
+        share = tree_share(p, lane);  // (the merge goes by what CTA 0 writes there, whatever comes after)
+        if (p.inject == 1) return;
+    }
     auto next = [&](bool first) { return KIND == kTree ? tree_next(p, share) : next_unit<kPaged>(p, first); };
     if (lane == 0) w = next(true);
     while (ok) {

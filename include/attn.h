@@ -217,8 +217,8 @@ size_t attn_fwd_tree_paged_workspace_bytes(int B, int Hq, int Hkv, int d, int ma
  * A token is only affected by keys that it sees: keys and values of other
  * branches, and slots past a sequence's length, may hold anything, NaN and
  * infinities included.
- * Hq / Hkv is at most 128 (ATTN_ERR_UNSUPPORTED), and the K/V tiles of all heads
- * at most 2^31 - 1.  Offsets and lengths are checked as by attn_fwd_paged, and
+ * out must not be q.  Hq / Hkv is at most 128 (ATTN_ERR_UNSUPPORTED), and the K/V
+ * tiles of all heads at most 2^31 - 1.  Offsets and lengths are checked as by attn_fwd_paged, and
  * seqlens_k[b] must be at least the tree's size (otherwise the sequence is
  * skipped); a parent outside its range counts as -1; all of these are recorded as
  * ATTN_ERR_DEVICE_BOUNDS.  Deterministic.
@@ -635,7 +635,8 @@ size_t attn_verify_tree_workspace_bytes(int B, int total, int vocab, int max_seq
  * draft_logits, uniforms and noise are not read.
  *
  * logits, draft_logits: [total] rows of vocab elements of `dtype` (an
- *      attn_dtype_t), logits_stride / draft_stride elements apart; draft_logits may
+ *      attn_dtype_t; vocab at most 2^28), logits_stride / draft_stride elements apart;
+ *      draft_logits may
  *      be NULL, and must be where temperature is.  -inf leaves a token out, NaN
  *      counts as -inf, and +inf as the largest finite fp32.
  * tokens: int32 [total], each node's token (a root's is not looked at).
@@ -670,13 +671,15 @@ attn_status_t attn_verify_tree(const void *logits, const void *draft_logits, int
  * The tree is the last n = cu_seqlens[b+1] - cu_seqlens[b] tokens of sequence b's
  * cache.  The keys and values of its nodes path[b][0 .. counts[b]-1] (ascending, as
  * attn_verify_tree writes them) move to the tree's first places, in all layers and
- * heads; the rows behind them are left as they were.
+ * heads; the rows behind them are left as they were.  The pages of a tree are its
+ * sequence's alone.
  *
  * k_pages, v_pages: bf16 [layers][num_pages][16][Hkv][128], updated in place (one
  *      block table for all layers; layers = 1 for a pool of one layer).
  * block_table, seqlens_k (the lengths with the trees), cu_seqlens: as
  *      attn_fwd_tree_paged; total bounds cu_seqlens.
- * path: int32 [B][max_seqlen]; counts: int32 [B], 0 .. n (0 drops the whole tree).
+ * path: int32 [B][max_seqlen], max_seqlen at least every n; counts: int32 [B], 0 .. n
+ *      (0 drops the whole tree).
  * seqlens_out: int32 [B] (written), seqlens_k[b] - n + counts[b]; must not overlap
  *      seqlens_k or counts.
  * A sequence with bad offsets, lengths, counts or path is left alone (seqlens_out =
@@ -722,7 +725,8 @@ attn_status_t attn_set_wait_budget_ns(uint64_t ns);
 
 /*
  * attn_debug_inject -- host-side fault injection for the failure-detection
- * tests.  mode 0: off (default).  mode 1: the next attn_fwd launches its
+ * tests.  mode 0: off (default).  mode 1: the next attn_fwd (or its packed, paged or
+ * tree form) launches its
  * kernel with the load-issuing warp told to issue nothing, so the other warps'
  * bounded waits expire, they record ATTN_ERR_TIMEOUT and the kernel exits
  * cleanly (no fault, no hang, nothing left in flight).  mode 2: the same for

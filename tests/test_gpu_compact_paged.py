@@ -140,3 +140,23 @@ def test_captured_given_output_and_stream():
     g.replay()
     assert same(dk.cpu(), moved(b, k, paths)) and same(dv.cpu(), moved(b, v, paths))
     assert lens.tolist() == [100 + len(paths[0]), 7 + len(paths[1])]
+
+
+def test_pools_past_32_bit_offsets():
+    """The same batch with its pages at the end of a pool of more than 2^32 elements."""
+    b, k, v, paths, path, counts = make(6, [30, 64], [40, 9], 8, 0)
+    few = k.shape[0]
+    pages = (1 << 18) + few
+    dev = []
+    for pool in (k, v):
+        big = torch.empty((2, pages, 16, 8, 128), dtype=torch.bfloat16, device="cuda")
+        big[:, -few:] = pool.cuda()
+        dev.append(big)
+    table = torch.where(b.table >= 0, b.table + (pages - few), b.table)
+    A.compact_paged(*dev, table.cuda(), b.lens.cuda(), b.cu.cuda(), path.cuda(), counts.cuda())
+    for got, pool in zip(dev, (k, v)):
+        for layer in range(2):
+            assert same(got[layer, -few:].cpu(), moved(b, pool, paths))
+    assert A.device_status()[0] == 0
+    del dev, big, got
+    torch.cuda.empty_cache()

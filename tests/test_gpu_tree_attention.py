@@ -264,3 +264,68 @@ def test_another_stream():
         got = call(b)
     s.synchronize()
     check(b, got)
+
+
+def test_pool_past_32_bit_offsets():
+    """The same batch with its pages at the end of a pool of more than 2^32 elements, a key with infinite values too."""
+    b = Batch(30, [30, 64], [400, 1500], 16, 8)
+    t = b.lens_list[0] - 5
+    b.v[int(b.table[0, t // 16]), t % 16, 3, 7] = math.inf
+    want = call(b)
+    few, pages = b.k.shape[0], (1 << 18) + b.k.shape[0]
+    dev = []
+    for pool in (b.k, b.v):
+        big = torch.empty((pages, 16, 8, 128), dtype=torch.bfloat16, device="cuda")
+        big[-few:] = pool.cuda()
+        dev.append(big)
+    table = torch.where(b.table >= 0, b.table + (pages - few), b.table).cuda()
+    got = A.fwd_tree_paged(b.q.cuda(), *dev, table, b.lens.cuda(), b.cu.cuda(), b.parents.cuda(), max_seqlen_q=64)
+    assert torch.equal(got[0].nan_to_num(9.0), want[0].nan_to_num(9.0)) and torch.equal(got[1], want[1])
+    assert A.device_status()[0] == 0
+    del dev, big
+    torch.cuda.empty_cache()
+
+
+def test_out_that_is_16_byte_aligned_only():
+    b = Batch(31, [9, 5], [100, 700], 4, 2)
+    want = call(b)
+    flat = torch.empty(14 * 4 * 128 + 8, dtype=torch.bfloat16, device="cuda")
+    out = flat[8:].view(14, 4, 128)
+    got = call(b, out=out)
+    assert got[0] is out and torch.equal(out, want[0])
+
+
+def test_calls_at_the_same_time_with_a_workspace_each():
+    cases = [Batch(40 + i, [16, 40, 1], [900, 2000, 77], 16, 4) for i in range(2)]
+    dev = [[x.cuda() for x in (b.q, b.k, b.v, b.table, b.lens, b.cu, b.parents)] for b in cases]
+    want = [A.fwd_tree_paged(*d, max_seqlen_q=40) for d in dev]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(A.fwd_tree_paged(*dev[i], max_seqlen_q=40))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g[0], want[i][0]) and torch.equal(g[1], want[i][1]) for g in got[i])
+
+
+def test_expired_wait_is_reported_and_the_next_call_is_right():
+    """The load-issuing warps issue nothing: the other warps' bounded waits run out, nothing is left in flight."""
+    b = Batch(50, [16, 40, 1], [900, 2000, 77], 16, 4)
+    good = call(b)
+    ws = torch.full((A.fwd_tree_paged_workspace_bytes(3, 16, 4, 128, 40),), 0x7f, dtype=torch.uint8, device="cuda")
+    A.set_wait_budget_ns(20_000_000)          # 20 ms
+    try:
+        A.debug_inject(1)
+        call(b, workspace=ws)
+        code, site = A.device_status()
+        assert code == 4 and site == 19, (code, site)   # a work item that never came
+        assert A.device_status()[0] == 0
+    finally:
+        A.debug_inject(0)
+        A.set_wait_budget_ns(0)
+    again = call(b, workspace=ws)
+    assert A.device_status()[0] == 0
+    assert torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])

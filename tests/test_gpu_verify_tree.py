@@ -276,3 +276,61 @@ def test_first_token_is_distributed_as_the_target(kind):
     more = counts > 1
     share = torch.bincount(out[more, 1].long(), minlength=V).double() / int(more.sum())
     assert ((share - p.double()).abs() <= 5 * (p * (1 - p) / int(more.sum())).sqrt().double()).all(), share
+
+
+def test_rows_past_32_bit_offsets():
+    d = make(100, [6, 9], 1000, "draft")
+    stride = (1 << 28) + 24
+    ref = want(d)
+    wide = {}
+    for name in ("logits", "draft"):
+        big = torch.empty(14 * stride + 1000, dtype=torch.bfloat16, device="cuda")
+        view = big.as_strided((15, 1000), (stride, 1))
+        view.copy_(d[name])
+        wide[name] = view
+    got = call({**d, **wide})
+    for g, w in zip(got, ref):
+        assert torch.equal(g.cpu(), w)
+    del wide, view, big
+    torch.cuda.empty_cache()
+
+
+def test_more_sequences_than_sms():
+    check(make(101, [1 + i % 3 for i in range(400)], 5000, "draft", tree="chain", temps=[1.0, 0.0, 0.7]))
+
+
+@pytest.mark.parametrize("kind", ["greedy", "top", "draft"])
+def test_short_and_long_trees_alike(kind):
+    """Rows summed up ahead (few a sequence) or one by one: the same sequences alone and beside a long tree."""
+    d = make(102, [12, 200, 3], 3000, kind, tree="chain" if kind == "greedy" else "tree", temps=[1.0, 0.8])
+    whole = call(d)
+    check(d, whole)
+    for b in (0, 2):
+        rows = slice(int(d["cu"][b]), int(d["cu"][b + 1]))
+        one = {k: (v[rows] if k in ("logits", "draft", "tokens", "parents", "uniforms") else
+                   v[b:b + 1] if k in ("temperature", "noise") else v) if v is not None and k != "width" else v
+               for k, v in d.items()}
+        n = rows.stop - rows.start
+        one["cu"] = torch.tensor([0, n], dtype=torch.int32)
+        got = call(one, max_seqlen=n)
+        for g, w in zip(got, whole):
+            assert torch.equal(g[0], w[b, :n] if w.dim() == 2 else w[b])
+
+
+def test_calls_at_the_same_time_with_a_workspace_each():
+    cases = [make(110 + i, [5, 9, 3], 9000, "draft") for i in range(2)]
+    refs = [want(d) for d in cases]
+    dev = [{k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in d.items()} for d in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(A.verify_tree(dev[i]["logits"], dev[i]["tokens"], dev[i]["parents"], dev[i]["cu"],
+                                            draft_logits=dev[i]["draft"], temperature=dev[i]["temperature"],
+                                            uniforms=dev[i]["uniforms"], noise=dev[i]["noise"], max_seqlen=9))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(x.cpu(), w) for x, w in zip(g, refs[i]))

@@ -23,7 +23,7 @@ TREE = dict(q=256, k=512, v=1024, bt=4, sl=8, cu=12, par=4, out=2048, lse=4, B=2
 @pytest.mark.parametrize("kw,code", [
     (dict(q=None), 1), (dict(q=264), 1), (dict(k=None), 1), (dict(k=520), 1), (dict(v=None), 1), (dict(v=1032), 1),
     (dict(bt=None), 1), (dict(bt=6), 1), (dict(sl=None), 1), (dict(sl=7), 1), (dict(cu=None), 1), (dict(cu=2), 1),
-    (dict(par=None), 1), (dict(par=6), 1), (dict(out=None), 1), (dict(out=2056), 1), (dict(lse=6), 1), (dict(B=0), 1),
+    (dict(par=None), 1), (dict(par=6), 1), (dict(out=None), 1), (dict(out=2056), 1), (dict(out=256), 1), (dict(lse=6), 1), (dict(B=0), 1),
     (dict(B=-1), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(Hq=9), 1), (dict(total=0), 1), (dict(longest=0), 1),
     (dict(longest=257), 1), (dict(d=64), 2), (dict(page=32), 2), (dict(npages=0), 1), (dict(npages=1 << 28), 1),
     (dict(maxb=0), 1), (dict(maxb=1 << 27), 1), (dict(maxb=(1 << 27) - 16, B=1 << 8), 1),
@@ -62,7 +62,7 @@ VERIFY = dict(logits=16, draft=32, dtype=0, tok=4, par=4, cu=4, temp=4, u=4, noi
     (dict(temp=None, u=None, noise=None), 1), (dict(temp=None, draft=None, u=None), 1), (dict(u=None), 1),
     (dict(noise=None), 1), (dict(noise=6), 1), (dict(path=None), 1), (dict(out=None), 1), (dict(counts=None), 1),
     (dict(counts=3), 1), (dict(B=0), 1), (dict(B=1 << 29), 1), (dict(total=0), 1), (dict(V=0), 1),
-    (dict(V=(1 << 31) - 1, ls=1 << 31, ds=1 << 31, ns=1 << 31), 1), (dict(width=0), 1), (dict(width=257), 1),
+    (dict(V=(1 << 28) + 1, ls=1 << 31, ds=1 << 31, ns=1 << 31), 1), (dict(width=0), 1), (dict(width=257), 1),
     (dict(ls=99), 1), (dict(ds=99), 1), (dict(ns=99), 1), (dict(ls=1 << 41), 1), (dict(ds=1 << 41), 1),
     (dict(ns=1 << 41), 1), (dict(ws=None), 5), (dict(ws=260), 5), (dict(wsb=100), 5),
 ])
@@ -99,3 +99,20 @@ def test_binding_rejects_cpu_tensors(lib):
         A.verify_tree([1.0], i(4), i(4), i(2))
     with pytest.raises(TypeError, match="k_pages must be"):
         A.compact_paged(bf(4, 16, 2, 128), bf(4, 16, 2, 128), i(1, 4), i(1), i(2), i(1, 4), i(1))
+
+
+def test_verify_workspace_bytes(lib):
+    need = A.verify_tree_workspace_bytes
+    align = lambda x: (x + 255) // 256 * 256  # noqa: E731
+    bf, fp = torch.bfloat16, torch.float32
+    # up to 16 rows a sequence, the rows' sums come first: slices of 4096 to 16384 tokens
+    assert need(2, 9, 100, 8, bf) == align(2 * (64 + 32)) + 9 * 8
+    assert need(64, 320, 131072, 5, bf, True) == align(64 * (64 + 20)) + 320 * 2 * 8 * 8
+    assert need(1, 5, 32768, 5, fp) == align(64 + 20) + 5 * 8 * 8
+    assert need(4, 65, 131072, 40, bf) == align(4 * (64 + 160))
+    assert need(1, 16, 1 << 28, 16, bf) == align(64 + 64) + 16 * 64 * 8
+    for bad in ((0, 9, 100, 8), (2, 0, 100, 8), (2, 9, 0, 8), (2, 9, (1 << 28) + 1, 8), (2, 9, 100, 0), (2, 9, 100, 257)):
+        assert need(*bad) == 0
+    assert lib.attn_verify_tree_workspace_bytes(2, 9, 100, 8, 2, 0) == 0
+    a = dict(VERIFY, wsb=need(2, 9, 100, 8, bf, True) - 1)
+    assert lib.attn_verify_tree(*a.values(), None) == 5
