@@ -151,8 +151,8 @@ struct Soft {
         const float f = t.step(m2, c);
         s += s2 * (Top::is_weight(f) ? f : odd_weight(m2, t.m, c));
     }
-    template <typename T>
-    __device__ __forceinline__ void add(const Chunk<T> &x, float c);
+    template <typename T, int U>
+    __device__ __forceinline__ void add(const Chunk<T> (&x)[U], float c);
 };
 
 // The slow way for a chunk with NaN or an infinity in it.
@@ -164,20 +164,28 @@ __device__ __noinline__ float odd_sum(Chunk<T> x, float m, float c) {
     return all;
 }
 
-template <typename T>
-__device__ __forceinline__ void Soft::add(const Chunk<T> &x, float c) {
-    const Top t(fmaxf(m, x.top()), c);
+template <typename T, int U>
+__device__ __forceinline__ void Soft::add(const Chunk<T> (&x)[U], float c) {
+    float top = x[0].top();
+#pragma unroll
+    for (int u = 1; u < U; ++u) top = fmaxf(top, x[u].top());
+    const Top t(fmaxf(m, top), c);
     raise(t, c);
     const float2 c2 = make_float2(c, c), r2 = make_float2(-t.r, -t.r);
-    float2 sum[2];
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 e = ptx::fma2(x.pair(i), c2, r2), w = make_float2(ptx::ex2(e.x), ptx::ex2(e.y));
-        sum[i & 1] = i < 2 ? w : ptx::add2(sum[i & 1], w);
+    for (int i = 0; i < 4 * U; ++i) {
+        const float2 e = ptx::fma2(x[i >> 2].pair(i & 3), c2, r2);
+        sum[i & 1] = ptx::add2(sum[i & 1], make_float2(ptx::ex2(e.x), ptx::ex2(e.y)));
     }
     const float2 both = ptx::add2(sum[0], sum[1]);
-    const float all = both.x + both.y;
-    s += all <= 16.f ? all : odd_sum(x, t.m, c);
+    float all = both.x + both.y;
+    if (!(all <= 16.f * U)) {
+        all = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) all += odd_sum(x[u], t.m, c);
+    }
+    s += all;
 }
 
 // The largest value and its index, the lowest of equal ones: the value's order in the
@@ -330,35 +338,47 @@ struct Slice {
         chunks = (hi - first) / 8;
         vec = b == nullptr || vec_ok(b + first);
     }
-    // This thread's part, in ascending order: many(first element, chunk of a, of b, of e),
-    // NT chunks from one to the next, one(element) for the others.  A chunk's successors are
-    // loaded before it is used (DEPTH of them); the loop stays rolled, its code is fetched once.
-    template <int DEPTH, bool E, typename Many, typename One>
+    // This thread's part, in ascending order: many(first element, chunks of a, of b, of e),
+    // U chunks NT apart at a time (those behind the end hold -inf), one(element) for the
+    // others.  The next DEPTH times' chunks are loaded before they are used; the loop stays
+    // rolled, its code is fetched once.
+    template <int U, int DEPTH, bool E, typename Many, typename One>
     __device__ __forceinline__ void each(const float *e, Many many, One one) const {
         const int tail = first + chunks * 8;
         const bool evec = E && vec_ok(e + first);
         if (lo + (int)threadIdx.x < first) one(lo + (int)threadIdx.x);
-        Chunk<T> x[DEPTH + 1], y[DEPTH + 1];
-        Chunk<float> z[DEPTH + 1];
-        const auto fetch = [&](int d, int k) {
-            if (k >= chunks) return;
-            const int at = first + k * 8;
-            x[d].load(a + at, true);
-            if (b != nullptr) y[d].load(b + at, vec);
-            if (E) z[d].load(e + at, evec);
+        Chunk<T> x[DEPTH + 1][U], y[DEPTH + 1][U];
+        Chunk<float> z[DEPTH + 1][U];
+        const auto fetch = [&](int d, int k0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * NT;
+                if (k < chunks) {
+                    const int at = first + k * 8;
+                    x[d][u].load(a + at, true);
+                    if (b != nullptr) y[d][u].load(b + at, vec);
+                    if (E) z[d][u].load(e + at, evec);
+                } else if (U > 1) {
+                    x[d][u].none();
+                    y[d][u].none();
+                    if (E) z[d][u].none();
+                }
+            }
         };
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) fetch(d, threadIdx.x + d * NT);
+        for (int d = 0; d < DEPTH; ++d) fetch(d, threadIdx.x + d * U * NT);
 #pragma unroll 1
-        for (int k = threadIdx.x; k < chunks; k += NT) {
-            fetch(DEPTH, k + DEPTH * NT);
+        for (int k = threadIdx.x; k < chunks; k += U * NT) {
+            fetch(DEPTH, k + DEPTH * U * NT);
             many(first + k * 8, x[0], y[0], z[0]);
 #pragma unroll
-            for (int d = 0; d < DEPTH; ++d) {
-                x[d] = x[d + 1];
-                y[d] = y[d + 1];
-                if (E) z[d] = z[d + 1];
-            }
+            for (int d = 0; d < DEPTH; ++d)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    x[d][u] = x[d + 1][u];
+                    y[d][u] = y[d + 1][u];
+                    if (E) z[d][u] = z[d + 1][u];
+                }
         }
         if (tail + (int)threadIdx.x < hi) one(tail + (int)threadIdx.x);
     }
@@ -388,9 +408,10 @@ __device__ __forceinline__ unsigned long long slice_best(const Slice<T, NT> &sl)
             where = i;
         }
     };
-    sl.template each<3, false>(
+    sl.template each<1, 3, false>(
         nullptr,
-        [&](int at, const Chunk<T> &x, const Chunk<T> &, const Chunk<float> &) {
+        [&](int at, const Chunk<T>(&chunk)[1], const Chunk<T>(&)[1], const Chunk<float>(&)[1]) {
+            const Chunk<T> &x = chunk[0];
             if (x.top() > top) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -403,11 +424,11 @@ __device__ __forceinline__ unsigned long long slice_best(const Slice<T, NT> &sl)
         [&](int at) { take(value(sl.a[at]), at); });
     return best_key(top, where);
 }
-template <typename T, int NT>
+template <int U, int DEPTH, typename T, int NT>
 __device__ __forceinline__ void slice_soft(const Slice<T, NT> &sl, Soft &p, Soft &q, float c) {
-    sl.template each<2, false>(
+    sl.template each<U, DEPTH, false>(
         nullptr,
-        [&](int, const Chunk<T> &x, const Chunk<T> &y, const Chunk<float> &) {
+        [&](int, const Chunk<T>(&x)[U], const Chunk<T>(&y)[U], const Chunk<float>(&)[U]) {
             p.add(x, c);
             if (sl.b != nullptr) q.add(y, c);
         },
@@ -469,7 +490,7 @@ __global__ void __launch_bounds__(SUM_THREADS) sums_kernel(const VerifyParams p)
         return;
     }
     Soft sp, none;
-    slice_soft(sl, sp, none, seq.c);
+    slice_soft<4, 0>(sl, sp, none, seq.c);
     float4 v = make_float4(sp.m, sp.s, -INFINITY, 0.f);
     warp_soft(v, seq.c);
     if (lane == 0) warp[threadIdx.x >> 5] = v;
@@ -516,6 +537,12 @@ __device__ __noinline__ float odd_rest(float x, float y, float pm, float qm, flo
                                        int known, const float *inv_left) {
     const float w = odd_weight(x, pm, c);
     return stages == 0 ? w : rest(w * ip, odd_weight(y, qm, c) * iq, stages, known, inv_left);
+}
+
+// A token's p and q from its logits and the rows' maxima and sums (0 where there is none).
+__device__ __forceinline__ void child_probability(float4 x, float c, float &p, float &q) {
+    p = x.y > 0.f ? Top(x.x, c).weight(p, c) / x.y : 0.f;
+    q = x.w > 0.f ? Top(x.z, c).weight(q, c) / x.w : 0.f;
 }
 
 // Where a sequence's walk has ended: what the race for its last token needs.
@@ -575,30 +602,41 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(const VerifyParams p
         sh.parent[i] = up;
         sh.token[i] = token;
         sh.u[i] = draws ? p.uniforms[begin + i] : 0.f;
-        if (AHEAD) {
-            // Its own row's sums, and its logits in its parent's row.
+        if (AHEAD && draws) {  // its logits in its parent's row
+            const bool there = up >= 0 && token >= 0;
+            sh.px[i] = there ? value(logits[up * p.logits_stride + token]) : -INFINITY;
+            sh.qx[i] = there && draft != nullptr ? value(draft[up * p.draft_stride + token]) : -INFINITY;
+        }
+    }
+    if (AHEAD) {
+        // The rows' sums, a row a warp and a piece a lane.
+        const int lane = tid & 31;
+        for (int i = tid >> 5; i < n; i += WARPS) {
             if (draws) {
-                const bool there = up >= 0 && token >= 0;
-                const float px = there ? value(logits[up * p.logits_stride + token]) : -INFINITY;
-                const float qx = there && draft != nullptr ? value(draft[up * p.draft_stride + token]) : -INFINITY;
-                Soft s[2];
-#pragma unroll
-                for (int kind = 0; kind < 2; ++kind) {
-                    if (kind == 1 && draft == nullptr) break;
-                    const float2 *part = p.sums + ((int64_t)kind * p.total + begin + i) * p.pieces;
-#pragma unroll 4
-                    for (int k = 0; k < p.pieces; ++k) s[kind].add(part[k].x, part[k].y, c);
+                const float2 *part = p.sums + (int64_t)(begin + i) * p.pieces;
+                const float2 *dpart = part + (int64_t)p.total * p.pieces;
+                Soft a, d;
+                for (int k = lane; k < p.pieces; k += 32) {
+                    a.add(part[k].x, part[k].y, c);
+                    if (draft != nullptr) d.add(dpart[k].x, dpart[k].y, c);
                 }
-                sh.stat[i] = make_float4(s[0].m, s[0].s, s[1].m, s[1].s);
-                sh.px[i] = px;
-                sh.qx[i] = qx;
+                float4 x = make_float4(a.m, a.s, d.m, d.s);
+                warp_soft(x, c);
+                if (lane == 0) sh.stat[i] = x;
             } else {
                 const auto *part = reinterpret_cast<const unsigned long long *>(p.sums) + (int64_t)(begin + i) * p.pieces;
                 unsigned long long k = 0;
-#pragma unroll 4
-                for (int j = 0; j < p.pieces; ++j) k = max(k, part[j]);
-                sh.stat[i].x = __int_as_float(best_index(k));
+                for (int j = lane; j < p.pieces; j += 32) k = max(k, part[j]);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(ALL, k, o));
+                if (lane == 0) sh.stat[i].x = __int_as_float(best_index(k));
             }
+        }
+        __syncthreads();
+        for (int i = tid; draws && i < n; i += THREADS) {
+            // A child's probabilities at its parent.
+            const float4 x = sh.stat[max(sh.parent[i], 0)];
+            child_probability(x, c, sh.px[i], sh.qx[i]);
         }
     }
     __syncthreads();
@@ -647,19 +685,20 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(const VerifyParams p
                     px = value(row[sh.token[tid]]);
                     if (drow != nullptr) qx = value(drow[sh.token[tid]]);
                 }
-                slice_soft(rows, sp, sq, c);
+                slice_soft<1, 2>(rows, sp, sq, c);
+                all.soft(sp, sq, c);
                 if (child) {
+                    child_probability(make_float4(sp.m, sp.s, sq.m, sq.s), c, px, qx);
                     sh.px[tid] = px;
                     sh.qx[tid] = qx;
                 }
-                all.soft(sp, sq, c);
+                __syncthreads();
             }
-            const Node node(sp, sq, c);
             rejected = known = 0;
-            float left = sp.s;  // without draft: what is left of the weights' sum
+            float left = 1.f;  // without draft: what is left of p
             each_child([&](int k) {
                 const int token = sh.token[k];
-                const float w = token >= 0 ? node.tp.weight(sh.px[k], c) : 0.f;
+                const float w = token >= 0 ? sh.px[k] : 0.f;
                 if (draft == nullptr) {
                     bool again = false;  // the token of an earlier sibling, which has been rejected
                     if (rejected > 0)
@@ -673,18 +712,19 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(const VerifyParams p
                     left = fmaxf(left - mine, 0.f);
                 } else {
                     if (rejected > known) {  // the sum that the last rejection left
+                        const Node node(sp, sq, c);
                         float sum = 0.f;
                         const bool simple = node.plain && rejected == 1;
                         const auto add = [&](float x, float y) {
                             sum += simple ? fmaxf(node.difference(x, y), 0.f)
                                           : odd_rest(x, y, sp.m, sq.m, node.ip, node.iq, c, rejected, known, sh.inv_left);
                         };
-                        rows.template each<1, false>(
+                        rows.template each<1, 1, false>(
                             nullptr,
-                            [&](int, const Chunk<T> &x, const Chunk<T> &y, const Chunk<float> &) {
+                            [&](int, const Chunk<T>(&x)[1], const Chunk<T>(&y)[1], const Chunk<float>(&)[1]) {
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
-                                    const float2 v = x.pair(i), q = y.pair(i);
+                                    const float2 v = x[0].pair(i), q = y[0].pair(i);
                                     add(v.x, q.x);
                                     add(v.y, q.y);
                                 }
@@ -695,8 +735,8 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(const VerifyParams p
                         __syncthreads();
                         ++known;
                     }
-                    const float q = token >= 0 ? node.tq.weight(sh.qx[k], c) * node.iq : 0.f;
-                    if (sh.u[k] * q < rest(w * node.ip, q, rejected, known, sh.inv_left)) return true;
+                    const float q = token >= 0 ? sh.qx[k] : 0.f;
+                    if (sh.u[k] * q < rest(w, q, rejected, known, sh.inv_left)) return true;
                 }
                 ++rejected;
                 return false;
@@ -793,13 +833,14 @@ __global__ void __launch_bounds__(RACE_THREADS, RACE_BLOCKS) race_kernel(const V
             }
         };
         const auto run = [&](auto weight_of) {
-            race.template each<0, true>(
+            race.template each<1, 0, true>(
                 noise,
-                [&](int at, const Chunk<T> &x, const Chunk<T> &y, const Chunk<float> &e) {
+                [&](int at, const Chunk<T>(&x)[1], const Chunk<T>(&y)[1], const Chunk<float>(&z)[1]) {
+                    const Chunk<float> &e = z[0];
                     float w[8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 v = x.pair(i), q = y.pair(i);
+                        const float2 v = x[0].pair(i), q = y[0].pair(i);
                         w[2 * i] = weight_of(v.x, q.x);
                         w[2 * i + 1] = weight_of(v.y, q.y);
                     }
