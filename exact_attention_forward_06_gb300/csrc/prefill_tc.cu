@@ -731,7 +731,9 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
                                const CUtensorMap *mk8, const CUtensorMap *mv8) {
     if (KIND != kTree && p.inject == 1) return;
     const uint64_t pol_q = ptx::policy_evict_first();
-    const uint64_t pol_kv = ptx::policy_evict_last();
+    // (of trees with one row block a KV head's keys are read once)
+    const uint64_t pol_kv =
+        KIND == kTree && p.Sq <= 2 * p.pack_pos ? ptx::policy_evict_first() : ptx::policy_evict_last();
     int n = 0;            // ring items issued
     int qn[2] = {0, 0};   // Q loads issued per tile (lane 0)
     int u = 0;            // units handed out (lane 0)
