@@ -405,6 +405,23 @@ __device__ __forceinline__ Unit next_unit(const PrefillParams &p, bool first) {
 }
 
 // ---- trees of drafted tokens: equal shares of all K/V tiles
+//
+// kTree: attention of trees against the paged cache (attn_fwd_tree_paged).  A tile
+// holds floor(128 / G) positions x the G heads of a KV head, so a KV head's keys are
+// read once for up to 2 * floor(128 / G) tokens.  Trees are small and caches long:
+// units alone would leave SMs idle, and lengths are known on the device only.  So all
+// units' K/V tiles lie on one line, cut into a share for every CTA; a unit that is cut
+// leaves partial rows, joined by tree_merge_kernel (a second, dependent launch).
+// Besides the paged form's: a mask of ancestors on the tree's tiles (tree_visible), V
+// tiles cleaned by a warp of their own (tree_cleaner), the next unit's keys loaded
+// before its queries, rows stored from registers.
+// Measured on one GB300 (copy bandwidth 6696 GB/s): 32 sequences of 1024 to 8192 tokens,
+// 32 / 8 heads, five tokens each (704 MB) 121 us, 0.87 of it, of which the line takes
+// 110 at the copy's rate and the start 5; 64 tokens each (169 GFLOP) 167 us: 1.4 to 1.7
+// us a tile of 256 rows, between the exponentials' 1.1 and what the groups' waits for one
+// another add, and 5 to 9 us a unit.  Three caches of 60 to 131 thousand tokens, one KV
+// head for 32, trees of 17 to 61 (160 GFLOP) 150 us.  One sequence of 205 tokens, five
+// of them drafted: 10 us, a chain of launch, plan, loads, two tiles and the store.
 
 // One sequence's part of the line: Hkv x row blocks x (K/V tiles and a unit's cost).
 struct TreeSeq {
