@@ -97,10 +97,10 @@ constexpr int ITEM_RING = 4;
 constexpr uint32_t ITEM_READERS = 2 + 8;
 // q_full[2], q_free[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[2], s_free[2],
 // p_full[2], o_full[2], fin, item_full[ITEM_RING], item_empty[ITEM_RING],
-// stage_ready[2], stage_taken[2], v_raw[NSLOT]; behind them the tensor-memory slot, the abort
-// flag, the item ring, the store commands and (trees) the flags of keys whose
-// values are not finite
-constexpr int NBARS = 2 + 2 + 2 * NSLOT + 2 + 2 + 2 + 2 + 1 + 2 * ITEM_RING + 2 + 2 + NSLOT;
+// stage_ready[2], stage_taken[2]; behind them the tensor-memory slot, the abort flag,
+// the item ring, the store commands, and for trees v_raw[NSLOT] and the flags of keys
+// whose values are not finite
+constexpr int NBARS = 2 + 2 + 2 * NSLOT + 2 + 2 + 2 + 2 + 1 + 2 * ITEM_RING + 2 + 2;
 constexpr uint32_t SMEM_MISC = 896;
 constexpr uint32_t SMEM_ALIGN = 1024;
 constexpr float RESCALE_LOG2 = 8.0f;  // move the running max past a 2^8 growth (and see softmax_wg)
@@ -111,7 +111,7 @@ constexpr float LN2 = 0.6931471805599453f;
 constexpr int TREE_UNITS = 4;
 constexpr int TREE_TILES = (kTreeMaxNodes + BN - 2) / BN + 1;
 static_assert(TREE_TILES == 3, "a tree's keys begin anywhere in their first tile");
-static_assert(NBARS * 8 + 8 + 64 * ITEM_RING + 2 * 32 + TREE_UNITS * TREE_TILES * 16 <= SMEM_MISC, "barrier area too small");
+static_assert(NBARS * 8 + 8 + 64 * ITEM_RING + 2 * 32 + 8 * NSLOT + TREE_UNITS * TREE_TILES * 16 <= SMEM_MISC, "barrier area too small");
 
 constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, 128, 0, 0);   // Q K^T: both K-major
 constexpr uint32_t IDESC_PV = ptx::idesc_bf16_f32(128, 128, 0, 1);  // P V: V is N(d)-major
@@ -160,11 +160,11 @@ struct SmemLayout {
         return reinterpret_cast<volatile int *>(bars + NBARS + 1) + 16 * ITEM_RING + 8 * t;
     }
     // v_raw(s): a tree's V tile has landed in slot s and is to be cleaned (tree_cleaner).
-    __device__ uint64_t *v_raw(int s) const { return bars + 17 + 2 * NSLOT + 2 * ITEM_RING + s; }
+    __device__ uint64_t *v_raw(int s) const { return bars + NBARS + 1 + 8 * ITEM_RING + 8 + s; }
     // Keys of tree tile i of unit u whose values are not finite (four words).
     __device__ volatile uint32_t *odd_keys(int u, int i) const {
         return reinterpret_cast<volatile uint32_t *>(bars + NBARS + 1) + 16 * ITEM_RING + 16 +
-               (u % TREE_UNITS * TREE_TILES + i) * 4;
+               2 * NSLOT + (u % TREE_UNITS * TREE_TILES + i) * 4;
     }
     __device__ uint8_t *q_tile(int t) const { return base + (t ? SMEM_Q1 : SMEM_Q0); }
     // Ring slot s: a K or V tile, or a tile's output staging area.
@@ -742,15 +742,12 @@ __device__ void producer(const PrefillParams &p, const SmemLayout &sm, const Wai
 // the copy then fills zeros.  When the tile's 8 pages are consecutive in the
 // pool (an engine that hands a sequence pages in order), lane 0 loads the
 // tile with one 128-row box of the run maps mk8/mv8 instead.
-template <int KIND>
 __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, const WaitCtx &wc, int lane,
                                const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mv,
                                const CUtensorMap *mk8, const CUtensorMap *mv8) {
-    if (KIND != kTree && p.inject == 1) return;
+    if (p.inject == 1) return;
     const uint64_t pol_q = ptx::policy_evict_first();
-    // (of trees with one row block a KV head's keys are read once)
-    const uint64_t pol_kv =
-        KIND == kTree && p.Sq <= 2 * p.pack_pos ? ptx::policy_evict_first() : ptx::policy_evict_last();
+    const uint64_t pol_kv = ptx::policy_evict_last();
     int n = 0;            // ring items issued
     int qn[2] = {0, 0};   // Q loads issued per tile (lane 0)
     int u = 0;            // units handed out (lane 0)
@@ -759,13 +756,7 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
     // the item ring.
     Unit w;
     w.n_kv = -1;
-    TreeShare share{};
-    if (KIND == kTree) {
-        share = tree_share(p, lane);  // (the merge goes by what CTA 0 writes there, whatever comes after)
-        if (p.inject == 1) return;
-    }
-    auto next = [&](bool first) { return KIND == kTree ? tree_next(p, share) : next_unit<kPaged>(p, first); };
-    if (lane == 0) w = next(true);
+    if (lane == 0) w = next_unit<kPaged>(p, true);
     while (ok) {
         if (lane == 0) ok = publish_unit(sm, wc, u, w);
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
@@ -793,43 +784,24 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
         };
         int next_phys = -1;
         if (lane < BN / 16 && total > 0) next_phys = table_entry(0);
-        // Q, once the previous unit's last S product has read its buffer, and the next
-        // unit while it loads.
-        auto load_q = [&]() {
-            if (lane == 0) {
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (qn[t] > 0 && !wait_bounded(sm.q_free(t), (qn[t] - 1) & 1, wc, kSiteProducerQ)) {
-                        ok = false;
-                        break;
-                    }
-                    if (KIND == kTree && t == 1 && w.s0[1] >= w.Sq) {
-                        ptx::mbar_arrive(sm.q_full(t));  // no rows: nothing reads the tile
-                    } else {
-                        // (a tree's tile is one box of pack_pos positions x G heads)
-                        ptx::mbar_arrive_expect_tx(sm.q_full(t), KIND == kTree ? p.pack_pos * p.G * D * 2 : TILE_BYTES);
-                        load_tile(mq, sm.q_tile(t), sm.q_full(t), p.bhsd, t ? w.h[1] : w.h[0],
-                                  w.q0 + (t ? w.s0[1] : w.s0[0]), w.tb, pol_q);
-                    }
-                    ++qn[t];
+        if (lane == 0) {
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (qn[t] > 0 && !wait_bounded(sm.q_free(t), (qn[t] - 1) & 1, wc, kSiteProducerQ)) {
+                    ok = false;
+                    break;
                 }
-                if (ok) nx = next(false);
+                ptx::mbar_arrive_expect_tx(sm.q_full(t), TILE_BYTES);
+                load_tile(mq, sm.q_tile(t), sm.q_full(t), p.bhsd, t ? w.h[1] : w.h[0],
+                          w.q0 + (t ? w.s0[1] : w.s0[0]), w.tb, pol_q);
+                ++qn[t];
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-        };
-        // A tree's units follow one another in a CTA, and waiting for Q first would let
-        // the ring run empty at each.  Its first three K/V items take slots that the
-        // previous unit frees whatever Q does; the fourth takes the last K tile's, and is
-        // free when Q is.
-        const int q_at = KIND == kTree && u > 1 ? min(3, total) : 0;
-        if (q_at == 0) {
-            load_q();
-            if (!ok) break;
+            if (ok) nx = next_unit<kPaged>(p, false);  // the next unit while this one's Q loads
         }
-        for (int i = 0; i < ring_items<KIND>(w); ++i) {
-            if (KIND == kTree && q_at > 0 && i == q_at) {
-                load_q();
-                if (!ok) break;
-            }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) {
+            ok = false;
+            break;
+        }
+        for (int i = 0; i < total + 2; ++i) {
             const int slot = n % NSLOT;
             if (i < total && (i & 1) == 0 && lane < BN / 16) {
                 const int page = (w.j_lo + (i >> 1)) * (BN / 16) + lane;
@@ -839,18 +811,14 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
                 if (!ok_page && page < n_pages) report_status(p.status, kStatusDeviceBounds, kSitePagedTable);
                 page_row = ok_page ? phys * 16 : p.num_pages * 16;
             }
-            // (values of a tree's keys land for the cleaner, which passes them on)
-            uint64_t *full = KIND == kTree && i < total && (i & 1) && (w.j_lo + (i >> 1) + 1) * BN > w.Sk - w.Sq
-                                 ? sm.v_raw(slot)
-                                 : sm.kv_full(slot);
             bool got = true;
             if (lane == 0) {
                 got = n < NSLOT || wait_bounded(sm.kv_empty(slot), ((n / NSLOT) - 1) & 1, wc, kSiteProducerEmpty);
                 if (got) {
                     if (i < total)
-                        ptx::mbar_arrive_expect_tx(full, TILE_BYTES);
+                        ptx::mbar_arrive_expect_tx(sm.kv_full(slot), TILE_BYTES);
                     else
-                        ptx::mbar_arrive(full);  // an output staging slot
+                        ptx::mbar_arrive(sm.kv_full(slot));  // an output staging slot
                 }
             }
             if (!__shfl_sync(0xffffffffu, got, 0)) {
@@ -869,17 +837,125 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
                 // a page is one 4 KiB box at group page_row / 8, a run one box of 16.
                 if (run) {
                     if (lane == 0)
-                        ptx::tma_load_5d_hint(sm.slot(slot), (i & 1) ? mv8 : mk8, full, 0, 0, 0,
+                        ptx::tma_load_5d_hint(sm.slot(slot), (i & 1) ? mv8 : mk8, sm.kv_full(slot), 0, 0, 0,
                                               page_row / 8, w.g, pol_kv);
                 } else if (lane < BN / 16) {
-                    ptx::tma_load_5d_hint(sm.slot(slot) + lane * PAGE_BOX_BYTES, (i & 1) ? mv : mk, full,
+                    ptx::tma_load_5d_hint(sm.slot(slot) + lane * PAGE_BOX_BYTES, (i & 1) ? mv : mk, sm.kv_full(slot),
                                           0, 0, 0, page_row / 8, w.g, pol_kv);
                 }
             }
             ++n;
         }
-        if (KIND == kTree && ok && q_at == total) load_q();  // (a unit of one tile)
         if (lane == 0) w = nx;
+    }
+    // On the way out make sure no copy is still writing into shared memory.
+    if (lane == 0) {
+        for (int t = 0; t < 2; ++t)
+            if (qn[t] > 0) drain_wait(sm.q_full(t), (qn[t] - 1) & 1, wc);
+        for (int i = max(0, n - NSLOT); i < n; ++i) drain_wait(sm.kv_full(i % NSLOT), (i / NSLOT) & 1, wc);
+    }
+}
+
+// Trees: the same for the segments of the CTA's share, with no staging slots.  The units
+// follow one another closely, and waiting for Q first, as above, would let the ring run
+// empty at each: a unit's first three K/V items take slots that the unit before frees
+// whatever Q does, and the fourth takes its last K tile's, which is free when Q's buffer
+// is.  So Q (and the search for the next unit) comes before the fourth.
+__device__ void producer_tree(const PrefillParams &p, const SmemLayout &sm, const WaitCtx &wc, int lane,
+                              const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mv,
+                              const CUtensorMap *mk8, const CUtensorMap *mv8) {
+    TreeShare share = tree_share(p, lane);  // (the merge goes by what CTA 0 writes there, whatever comes after)
+    if (p.inject == 1) return;
+    const uint64_t pol_q = ptx::policy_evict_first();
+    // With one row block a KV head's keys are read once.
+    const uint64_t pol_kv = p.Sq <= 2 * p.pack_pos ? ptx::policy_evict_first() : ptx::policy_evict_last();
+    int n = 0;            // ring items issued
+    int qn[2] = {0, 0};   // Q loads issued per tile (lane 0)
+    int u = 0;            // units handed out
+    bool ok = true;
+    Unit w, nx;
+    w.n_kv = nx.n_kv = -1;
+    if (lane == 0) w = tree_next(p, share);
+    while (ok) {
+        if (lane == 0) ok = publish_unit(sm, wc, u, w);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        __syncwarp();
+        if (lane != 0) {
+            const volatile int *d = sm.item_ring(u % ITEM_RING);
+            w.b = d[0]; w.g = d[1]; w.n_kv = d[6]; w.j_lo = d[7]; w.Sq = d[10]; w.Sk = d[11];
+        }
+        if (w.n_kv < 0) break;  // end of the share
+        const int total = 2 * w.n_kv;
+        const int n_pages = (w.Sk + 15) / 16;
+        const int *row = p.block_table + (int64_t)w.b * p.max_blocks;
+        int page_row = p.num_pages * 16;  // this lane's page of the current tile (lanes < 8)
+        bool run = false;                 // the current tile's pages are one run in the pool
+        auto table_entry = [&](int jt) -> int {  // (read a tile ahead)
+            const int page = (w.j_lo + jt) * (BN / 16) + lane;
+            return page < n_pages ? row[page] : -1;
+        };
+        int next_phys = -1;
+        if (lane < BN / 16) next_phys = table_entry(0);
+        // A Q tile is one box of pack_pos positions x G heads; one without rows is not read.
+        auto load_q = [&]() {
+            if (lane == 0) {
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (qn[t] > 0 && !wait_bounded(sm.q_free(t), (qn[t] - 1) & 1, wc, kSiteProducerQ)) {
+                        ok = false;
+                        break;
+                    }
+                    const int s0 = t ? w.s0[1] : w.s0[0];
+                    if (s0 >= w.Sq) {
+                        ptx::mbar_arrive(sm.q_full(t));
+                    } else {
+                        ptx::mbar_arrive_expect_tx(sm.q_full(t), p.pack_pos * p.G * D * 2);
+                        load_tile(mq, sm.q_tile(t), sm.q_full(t), false, w.h[0], w.q0 + s0, 0, pol_q);
+                    }
+                    ++qn[t];
+                }
+                if (ok) nx = tree_next(p, share);
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        };
+        const int q_at = u > 0 ? min(3, total) : 0;
+        for (int i = 0; i < total; ++i) {
+            if (i == q_at) {
+                load_q();
+                if (!ok) break;
+            }
+            const int slot = n % NSLOT;
+            if ((i & 1) == 0 && lane < BN / 16) {
+                const int page = (w.j_lo + (i >> 1)) * (BN / 16) + lane;
+                const int phys = next_phys;
+                if ((i >> 1) + 1 < w.n_kv) next_phys = table_entry((i >> 1) + 1);
+                const bool ok_page = phys >= 0 && phys < p.num_pages;
+                if (!ok_page && page < n_pages) report_status(p.status, kStatusDeviceBounds, kSitePagedTable);
+                page_row = ok_page ? phys * 16 : p.num_pages * 16;
+            }
+            // (values of a tree's keys land for the cleaner, which passes them on)
+            uint64_t *full = (i & 1) && (w.j_lo + (i >> 1) + 1) * BN > w.Sk - w.Sq ? sm.v_raw(slot) : sm.kv_full(slot);
+            if (lane == 0) {
+                ok = n < NSLOT || wait_bounded(sm.kv_empty(slot), ((n / NSLOT) - 1) & 1, wc, kSiteProducerEmpty);
+                if (ok) ptx::mbar_arrive_expect_tx(full, TILE_BYTES);
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            if ((i & 1) == 0) {
+                const int first = __shfl_sync(0xffffffffu, page_row, 0);
+                run = __all_sync(0xffffffffu, lane >= BN / 16 || (page_row == first + 16 * lane && first < p.num_pages * 16));
+            }
+            if (run) {
+                if (lane == 0)
+                    ptx::tma_load_5d_hint(sm.slot(slot), (i & 1) ? mv8 : mk8, full, 0, 0, 0, page_row / 8, w.g, pol_kv);
+            } else if (lane < BN / 16) {
+                ptx::tma_load_5d_hint(sm.slot(slot) + lane * PAGE_BOX_BYTES, (i & 1) ? mv : mk, full, 0, 0, 0,
+                                      page_row / 8, w.g, pol_kv);
+            }
+            ++n;
+        }
+        if (ok && q_at == total) load_q();  // (a unit of one tile)
+        if (lane == 0) w = nx;
+        ++u;
     }
     // On the way out make sure no copy is still writing into shared memory.
     if (lane == 0) {
@@ -1362,7 +1438,6 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
         }
         for (int j = 0; !dead && j < w.n_kv; ++j) {
             const int g = g0 + j;
-            const int kbase = (w.j_lo + j) * BN;  // absolute first key of this tile
             if (!wait_bounded(sm.s_full(t), (uint32_t)(g & 1), wc, kSiteSoftmaxS)) {
                 ok = false;
                 break;
@@ -1387,6 +1462,7 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
                     s[48 + i] = make_float2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]));
                 }
             }
+            const int kbase = (w.j_lo + j) * BN;  // absolute first key of this tile
             const bool masked = !TREE && kbase + BN - 1 > lim_tile;
             if (TREE && kbase + BN > tree0) {
                 const uint32_t *tile = seen[kbase / BN - tree0 / BN];
@@ -1644,7 +1720,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         for (int s = 0; s < NSLOT; ++s) {
             ptx::mbar_init(sm.kv_full(s), 1);
-            ptx::mbar_init(sm.v_raw(s), 1);
+            if (KIND == kTree) ptx::mbar_init(sm.v_raw(s), 1);
             ptx::mbar_init(sm.kv_empty(s), 2);  // one release per issuing stream (or a staging slot's 2)
         }
         // Softmax-side barriers take one arrival per warp (lane 0, after the
@@ -1685,8 +1761,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (warp < 4) {
         ptx::setmaxnreg_dec<REGS_CONTROL>();
         if (warp == 0) {
-            if (KIND == kPaged || KIND == kTree)
-                producer_paged<KIND>(p, sm, wc, lane, &map_q, &map_k, &map_v, &map_k8, &map_v8);
+            if (KIND == kPaged)
+                producer_paged(p, sm, wc, lane, &map_q, &map_k, &map_v, &map_k8, &map_v8);
+            else if (KIND == kTree)
+                producer_tree(p, sm, wc, lane, &map_q, &map_k, &map_v, &map_k8, &map_v8);
             else if (lane == 0)
                 producer<KIND>(p, sm, wc, &map_q, &map_k, &map_v);
         } else if (warp == 3) {
