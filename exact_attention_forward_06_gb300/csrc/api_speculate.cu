@@ -35,7 +35,7 @@ static bool verify_ahead(int B, int total, int vocab, int max_seqlen, bool draft
     *pieces = 0;
     if (rows > 16 * (int64_t)B) return false;
     *piece = attn::verify_piece(rows * (draft ? 2 : 1), vocab, pieces);
-    if ((int64_t)B * max_seqlen * (draft ? 2 : 1) <= 0x7fffffff / *pieces) return true;
+    if ((int64_t)B * std::min(max_seqlen, 16) * (draft ? 2 : 1) <= 0x7fffffff / *pieces) return true;
     *pieces = 0;  // (more blocks than a launch has)
     return false;
 }

@@ -1944,23 +1944,46 @@ cudaError_t launch_prefill_merge(void *out, const PrefillParams &p, cudaStream_t
 
 namespace g1 {
 
-// Joins a tree launch's partials.  blockIdx.x: sequence, KV head, row block, and group
-// of the unit's rows; a warp takes ROWS of them one after another, four columns a lane,
-// or (SPLIT) all eight warps one row, whose parts they take in turn.  Units that were not
-// cut are there already.
+// Joins a tree launch's partials.  A warp takes ROWS rows of a cut unit, four columns a
+// lane, or (SPLIT, where few units have many parts) all eight warps one row, whose parts they
+// take in turn.  blockIdx.x: sequence, KV head, row block and group of rows; or, where there
+// are far fewer borders between shares than units, the border whose unit it is (of a unit's
+// several borders the first) and group of rows.
 template <bool SPLIT, int ROWS>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const PrefillParams p, int ctas, int groups, int blocks) {
+__global__ void __launch_bounds__(256) tree_merge_kernel(const PrefillParams p, int ctas, int groups, int blocks, bool borders) {
     ptx::wait_for_prior_work();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int unit = blockIdx.x / groups, group = blockIdx.x - unit * groups;
-    const int b = unit / (p.Hkv * blocks), gb = unit - b * p.Hkv * blocks, g = gb / blocks, blk = gb - g * blocks;
-    const TreeSeq s = tree_seq(p, b, false);
-    const int begin = p.first[b], total = p.first[p.B];
-    if (blk >= s.blocks) return;  // (total is not 0)
+    const int item = blockIdx.x / groups, group = blockIdx.x - item * groups;
+    const int total = p.first[p.B];
     const TreeLine line(ctas, total);
-    const int us = begin + (g * s.blocks + blk) * s.span;
+    int b, g, blk;
+    if (!borders) {
+        b = item / (p.Hkv * blocks);
+        const int gb = item - b * p.Hkv * blocks;
+        g = gb / blocks;
+        blk = gb - g * blocks;
+    } else {
+        if (item + 1 >= line.shares) return;
+        // The sequence that holds the border: the last one that begins there or before, by
+        // 32 probes a round.
+        const int x = line.begin(item + 1);
+        b = 0;
+        for (int len = p.B; len > 1;) {
+            const int step = (len + 31) >> 5, i = (lane + 1) * step;
+            const unsigned votes = __ballot_sync(0xffffffffu, i < len && p.first[b + i] <= x);
+            b += __popc(votes) * step;
+            len = min(step, len - __popc(votes) * step);
+        }
+        const TreeSeq s = tree_seq(p, b, false);
+        const int unit = (x - p.first[b]) / s.span;
+        g = unit / s.blocks;
+        blk = unit - g * s.blocks;
+    }
+    const TreeSeq s = tree_seq(p, b, false);
+    if (blk >= s.blocks) return;
+    const int us = p.first[b] + (g * s.blocks + blk) * s.span;
     const int c0 = line.of(us + s.span - s.tiles), c1 = line.of(us + s.span - 1);
-    if (c0 == c1) return;
+    if (c0 == c1 || (borders && c0 != item)) return;
     // The unit's positions in its two tiles; rows in tile order, the second tile's from 128 on.
     const int left = s.Sq - blk * 2 * p.pack_pos, pos0 = min(left, p.pack_pos), pos1 = min(left - pos0, p.pack_pos);
     const int rows0 = pos0 * p.G, rows = rows0 + pos1 * p.G;
@@ -2068,13 +2091,21 @@ cudaError_t launch_tree_merge(const PrefillParams &p, int ctas, cudaStream_t str
     const int blocks = (p.Sq + 2 * p.pack_pos - 1) / (2 * p.pack_pos);
     const int most = std::min(p.Sq, 2 * p.pack_pos) * p.G;  // rows of a unit
     const int64_t units = (int64_t)p.B * p.Hkv * blocks;
+    if (ctas < 2) return cudaSuccess;
+    // With more units than twice the borders most have no border, or (under a bound that no
+    // tree comes near) no rows: 32 trees of 5 tokens under a bound of 256, 62 us by borders
+    // and 71 by units; with as many units as borders the units' blocks take less (17 us
+    // against 19 of the 32 trees of 64).
+    const bool borders = units > 2 * kTreeMaxCtas;
+    const int64_t items = borders ? ctas - 1 : units;
     const auto launch = [&](auto kernel, int groups) {
-        return launch_dependent(kernel, dim3((unsigned)(units * groups)), dim3(256), 0, stream, p, ctas, groups, blocks);
+        return launch_dependent(kernel, dim3((unsigned)(items * groups)), dim3(256), 0, stream, p, ctas, groups, blocks,
+                                borders);
     };
     // Few units are cut into many parts each, and there are few rows: eight warps a row.
     if (units * 8 <= ctas) return launch(g1::tree_merge_kernel<true, 1>, most);
     // Otherwise a warp takes four rows, or one where that leaves SMs idle.
-    if (units * most >= 16 * 1024) return launch(g1::tree_merge_kernel<false, 4>, (most + 31) / 32);
+    if (items * most >= 16 * 1024) return launch(g1::tree_merge_kernel<false, 4>, (most + 31) / 32);
     return launch(g1::tree_merge_kernel<false, 1>, (most + 7) / 8);
 }
 

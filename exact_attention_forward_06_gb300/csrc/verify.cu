@@ -459,25 +459,15 @@ struct Sequence {
     }
 };
 
-// Sums all rows up ahead of the walk: a CTA a slice of a row (blockIdx.x: sequence, node,
-// target or draft, slice), its part to `sums`.  Few threads with many elements each: what a
-// thread does besides its elements (its row, the joining of sums) is worth a hundred.
+// Sums a slice of a row up for the walk.
 template <typename T>
-__global__ void __launch_bounds__(SUM_THREADS) sums_kernel(const VerifyParams p) {
-    ptx::wait_for_prior_work();
-    ptx::allow_next_work();
+__device__ __forceinline__ void sum_slice(const VerifyParams &p, const Sequence &seq, int kind, int i, int piece,
+                                          float4 (&warp)[SUM_THREADS / 32]) {
     constexpr int W = SUM_THREADS / 32;
-    __shared__ float4 warp[W];
-    const unsigned kinds = p.draft != nullptr ? 2 : 1;
-    const unsigned row_x = blockIdx.x / (unsigned)p.pieces, piece = blockIdx.x - row_x * (unsigned)p.pieces;
-    const unsigned node = row_x / kinds, kind = row_x - node * kinds;
-    const unsigned b = node / (unsigned)p.width, i = node - b * (unsigned)p.width;
-    const Sequence seq(p, b);
-    if ((int)i >= seq.n || (kind == 1 && !seq.draws)) return;
-    const int64_t row = seq.begin + (int)i;
+    const int64_t row = seq.begin + i;
     const T *data = kind == 0 ? static_cast<const T *>(p.logits) + row * p.logits_stride
                               : static_cast<const T *>(p.draft) + row * p.draft_stride;
-    const int lo = (int)piece * p.piece, hi = min(p.V, lo + p.piece), lane = threadIdx.x & 31;
+    const int lo = piece * p.piece, hi = min(p.V, lo + p.piece), lane = threadIdx.x & 31;
     const Slice<T, SUM_THREADS> sl(data, nullptr, lo, hi);
     float2 *out = p.sums + ((int64_t)kind * p.total + row) * p.pieces + piece;
     if (!seq.draws) {
@@ -504,6 +494,30 @@ __global__ void __launch_bounds__(SUM_THREADS) sums_kernel(const VerifyParams p)
 #pragma unroll
     for (int j = 0; j < W; ++j) all.add(warp[j].x, warp[j].y, seq.c);
     *out = make_float2(all.m, all.s);
+}
+
+// Sums all rows up ahead of the walk: a CTA a slice of a row (blockIdx.x: sequence, node,
+// target or draft, slice).  Few threads with many elements each: what a thread does besides
+// its elements (its row, the joining of sums) is worth a hundred.  MANY: `nodes` nodes of a
+// sequence at once, and a CTA takes every so manyth (a form of its own: the loop takes
+// registers, and a tenth of the time, from the other).
+template <typename T, bool MANY>
+__global__ void __launch_bounds__(SUM_THREADS) sums_kernel(const VerifyParams p, int nodes) {
+    ptx::wait_for_prior_work();
+    ptx::allow_next_work();
+    __shared__ float4 warp[SUM_THREADS / 32];
+    const unsigned kinds = p.draft != nullptr ? 2 : 1;
+    const unsigned row_x = blockIdx.x / (unsigned)p.pieces, piece = blockIdx.x - row_x * (unsigned)p.pieces;
+    const unsigned node = row_x / kinds, kind = row_x - node * kinds;
+    const unsigned b = node / (unsigned)nodes;
+    const Sequence seq(p, b);
+    int i = (int)(node - b * (unsigned)nodes);
+    if (i >= seq.n || (kind == 1 && !seq.draws)) return;
+    sum_slice<T>(p, seq, kind, i, piece, warp);
+    while (MANY && (i += nodes) < seq.n) {
+        __syncthreads();  // (the row before has been joined)
+        sum_slice<T>(p, seq, kind, i, piece, warp);
+    }
 }
 
 // What is left of p where `stages` siblings were rejected, one after the other: p - q, no
@@ -895,8 +909,14 @@ __global__ void __launch_bounds__(RACE_THREADS, RACE_BLOCKS) race_kernel(const V
 template <typename T>
 cudaError_t launch(const VerifyParams &p, cudaStream_t stream) {
     if (p.pieces > 0) {
-        const int64_t blocks = (int64_t)p.B * p.width * (p.draft != nullptr ? 2 : 1) * p.pieces;
-        const cudaError_t e = launch_dependent(sums_kernel<T>, dim3((unsigned)blocks), dim3(SUM_THREADS), 0, stream, p);
+        // Nodes of a sequence at once: as many as make 8192 blocks.  Under a bound that few
+        // trees come near, most of the blocks would find nothing to do: 64 trees of 1 to 8
+        // rows under a bound of 256 took 116 us with a block for every row, 28 like this.
+        const int64_t each = (int64_t)p.B * (p.draft != nullptr ? 2 : 1) * p.pieces;
+        const int nodes = (int)std::min<int64_t>(p.width, std::max<int64_t>(16, 8192 / each));
+        const int64_t blocks = (int64_t)p.B * nodes * (p.draft != nullptr ? 2 : 1) * p.pieces;
+        const cudaError_t e = launch_dependent(p.width > nodes ? sums_kernel<T, true> : sums_kernel<T, false>,
+                                               dim3((unsigned)blocks), dim3(SUM_THREADS), 0, stream, p, nodes);
         if (e != cudaSuccess) return e;
     }
     // CTAs a sequence: one an SM, a slice of 4096 tokens at least.

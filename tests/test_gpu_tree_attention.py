@@ -329,3 +329,21 @@ def test_expired_wait_is_reported_and_the_next_call_is_right():
     again = call(b, workspace=ws)
     assert A.device_status()[0] == 0
     assert torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
+
+
+def test_many_idle_rows_between_trees():
+    sizes = [0] * 500
+    ctx = [0] * 500
+    for at, n, c in ((0, 4, 900), (130, 7, 3000), (131, 1, 20), (499, 12, 700)):
+        sizes[at], ctx[at] = n, c
+    b = Batch(60, sizes, ctx, 8, 2)
+    check(b, call(b, max_seqlen_q=200))
+
+
+def test_bound_far_above_the_trees():
+    b = Batch(61, [3, 9, 5], [2000, 777, 130], 32, 8)
+    want = call(b)
+    got = call(b, max_seqlen_q=256)
+    check(b, got)
+    _, _, mass = b.attention()
+    assert ((got[0].double() - want[0].double()).abs().cpu() <= (2.0 ** -7 + 4e-4) * mass + 2.0 ** -7 * want[0].double().abs().cpu()).all()

@@ -334,3 +334,9 @@ def test_calls_at_the_same_time_with_a_workspace_each():
     for i in range(2):
         for g in got[i]:
             assert all(torch.equal(x.cpu(), w) for x, w in zip(g, refs[i]))
+
+
+@pytest.mark.parametrize("kind", ["greedy", "top", "draft"])
+def test_one_long_tree_among_short_ones(kind):
+    """Few rows a sequence on average, so all are summed up ahead, the long tree's one after another."""
+    check(make(120, [3, 1, 150, 2, 4, 1, 5, 2, 0, 1, 3, 2], 700, kind, temps=[1.0, 0.8, 0.0 if kind == "greedy" else 1.2]))
