@@ -164,6 +164,24 @@ def test_noise_that_is_not_positive_is_never_drawn():
     assert A.device_status()[0] == 0
 
 
+@pytest.mark.parametrize("bad", [0.0, -0.0, -1e-3, -math.inf])
+def test_noise_that_is_not_positive_where_a_drawn_child_was_rejected(bad):
+    # p: three quarters on token 4; q: on token 7, which is rejected and has p - q below 0
+    d = make(65, [2, 1], 16, "draft", tree="chain")
+    d["logits"][:] = 0.0
+    d["draft"][:] = 0.0
+    d["logits"][0, 4] = d["draft"][0, 7] = math.log(45.0)
+    d["tokens"][1] = 7
+    d["uniforms"][1] = 0.5
+    d["noise"][:] = bad
+    d["noise"][0, 4] = 1.0
+    d["noise"][1, 11] = 1.0
+    path, tokens, counts = call(d)
+    assert counts.tolist() == [1, 1] and tokens[:, 0].tolist() == [4, 11]
+    d["noise"][:] = bad
+    assert call(d)[1][:, 0].tolist() == [-1, -1]
+
+
 def test_equal_siblings_and_nothing_left():
     # the only two tokens are both children, and rejected although they have all the mass
     d = make(63, [4], 8, "top", tree="bush")
