@@ -427,7 +427,10 @@ attn_status_t attn_fwd_tree_paged(const void *q, const void *k_pages, const void
                                       ATTN_LAYOUT_BSHD, scale);
     if (st != ATTN_OK) return st;
     if (page_size != 16 || Hq / Hkv > 128) return ATTN_ERR_UNSUPPORTED;
-    if (out == q) return ATTN_ERR_INVALID_ARG;  // (several CTAs read a query)
+    // Several CTAs read a query.
+    const uintptr_t q_at = reinterpret_cast<uintptr_t>(q), out_at = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t q_bytes = (uintptr_t)total_q * Hq * d * 2;
+    if (q_at < out_at + q_bytes && out_at < q_at + q_bytes) return ATTN_ERR_INVALID_ARG;
     if (B < 1 || max_seqlen_q < 1 || max_seqlen_q > ATTN_TREE_MAX) return ATTN_ERR_INVALID_ARG;
     if (!valid_round_mode(round_mode)) return ATTN_ERR_INVALID_ARG;
     // The line of K/V tiles, and the rows of the merge, are 32-bit.

@@ -16,7 +16,7 @@ def lib():
     return A.load()
 
 
-TREE = dict(q=256, k=512, v=1024, bt=4, sl=8, cu=12, par=4, out=2048, lse=4, B=2, Hq=8, Hkv=2, total=9, longest=16, d=128,
+TREE = dict(q=256, k=512, v=1024, bt=4, sl=8, cu=12, par=4, out=1 << 20, lse=4, B=2, Hq=8, Hkv=2, total=9, longest=16, d=128,
             page=16, npages=10, maxb=4, scale=0.1, mode=0, ws=256, wsb=1 << 30)
 
 
@@ -24,6 +24,7 @@ TREE = dict(q=256, k=512, v=1024, bt=4, sl=8, cu=12, par=4, out=2048, lse=4, B=2
     (dict(q=None), 1), (dict(q=264), 1), (dict(k=None), 1), (dict(k=520), 1), (dict(v=None), 1), (dict(v=1032), 1),
     (dict(bt=None), 1), (dict(bt=6), 1), (dict(sl=None), 1), (dict(sl=7), 1), (dict(cu=None), 1), (dict(cu=2), 1),
     (dict(par=None), 1), (dict(par=6), 1), (dict(out=None), 1), (dict(out=2056), 1), (dict(out=256), 1), (dict(lse=6), 1), (dict(B=0), 1),
+    (dict(out=240 + 9 * 8 * 256), 1), (dict(q=(1 << 20) + 16), 1), (dict(q=(1 << 20) - 16), 1),  # out over q
     (dict(B=-1), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(Hq=9), 1), (dict(total=0), 1), (dict(longest=0), 1),
     (dict(longest=257), 1), (dict(d=64), 2), (dict(page=32), 2), (dict(npages=0), 1), (dict(npages=1 << 28), 1),
     (dict(maxb=0), 1), (dict(maxb=1 << 27), 1), (dict(maxb=(1 << 27) - 16, B=1 << 8), 1),
