@@ -420,7 +420,7 @@ __device__ __forceinline__ Unit next_unit(const PrefillParams &p, bool first) {
 // 110 at the copy's rate and the start 5; 64 tokens each (169 GFLOP) 167 us: 1.4 to 1.7
 // us a tile of 256 rows, between the exponentials' 1.1 and what the groups' waits for one
 // another add, and 5 to 9 us a unit.  Three caches of 60 to 131 thousand tokens, one KV
-// head for 32, trees of 17 to 61 (160 GFLOP) 150 us.  One sequence of 205 tokens, five
+// head for 32, trees of 17 to 61 (160 GFLOP) 147 us.  One sequence of 205 tokens, five
 // of them drafted: 10 us, a chain of launch, plan, loads, two tiles and the store.
 
 // One sequence's part of the line: Hkv x row blocks x (K/V tiles and a unit's cost).
@@ -2102,8 +2102,10 @@ cudaError_t launch_tree_merge(const PrefillParams &p, int ctas, cudaStream_t str
         return launch_dependent(kernel, dim3((unsigned)(items * groups)), dim3(256), 0, stream, p, ctas, groups, blocks,
                                 borders);
     };
-    // Few units are cut into many parts each, and there are few rows: eight warps a row.
-    if (units * 8 <= ctas) return launch(g1::tree_merge_kernel<true, 1>, most);
+    // Few units are cut into many parts each: eight warps a row. 8 units of 32 rows in 19 parts
+    // take 18.6 us so and 22.5 with a warp a row, 4 units in 38 parts 26.8 and 37.2; 15 or so
+    // units of up to 256 rows (three long sequences of one key head) 141.8 so and 137.6 with a warp.
+    if (units * 16 <= ctas) return launch(g1::tree_merge_kernel<true, 1>, most);
     // Otherwise a warp takes four rows, or one where that leaves SMs idle.
     if (items * most >= 16 * 1024) return launch(g1::tree_merge_kernel<false, 4>, (most + 31) / 32);
     return launch(g1::tree_merge_kernel<false, 1>, (most + 7) / 8);
