@@ -840,9 +840,10 @@ __global__ void __launch_bounds__(RACE_THREADS, RACE_BLOCKS) race_kernel(const V
         int where = -1;
         const auto take = [&](float w, float e, int i) {
             const float v = w * ptx::rcp(e);
-            if (v > top) {  // (no NaN: of 0 times infinity, or e's)
-                // (0 gives infinity, and what is left may be below 0 here, as noise may be)
-                bool out = !(e > 0.f);
+            // (no NaN: of 0 times infinity, or e's; e of 0 gives infinity, and where what is left
+            // may be below 0, e below 0 a number above)
+            if (v > top && e > 0.f) {
+                bool out = false;
                 if (watch)
                     for (int k = 0; k < outs; ++k) out = out || __float_as_int(list[k]) == i;
                 if (!out) {
