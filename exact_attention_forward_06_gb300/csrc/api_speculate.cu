@@ -26,14 +26,19 @@ bool overlap(const void *a, const void *b, size_t bytes) {
 
 // Whether all rows are summed up ahead of the walk, and in what slices.  That reads rows
 // that the walk may not come to, but all at once; the walk by itself waits for one row
-// after the other, 6 to 8 us each.  Rows of 131072 tokens, two or three of them on the
-// path: 16 sequences of 8 rows, with draft, 37 us ahead against 50; 8 of 16 rows 41 against
-// 51; 64 of 12 rows 112 against 166; but 8 trees of 64 rows, without draft, 48 against 23,
-// and 64 of 30 rows of 32000 tokens 49 against 34.  So: up to 16 rows a sequence.
-static bool verify_ahead(int B, int total, int vocab, int max_seqlen, bool draft, int *piece, int *pieces) {
+// after the other, 2 to 4 us each, with draft 4 to 8.  So: up to 16 rows a sequence, or few
+// bytes in all.  us ahead against not, rows of bf16:
+//   131072 tokens, with draft: chains, 16 of 8 rows 33 against 51, 64 of 12 rows 96 against
+//     202; trees, 8 of 16 rows 40 against 54, 16 of 16 rows 57 against 59, 16 of 24 rows
+//     (201 MB) 72 against 55, one of 120 rows (63 MB) 49 against 56, 4 of 48 (101) 45 against 28;
+//   without: 64 trees of 12 rows 64 against 72, 8 of 12 23 against 23, 8 of 24 (50 MB) 28
+//     against 26, one of 24 (6 MB) 17 against 21, one of 64 (17 MB) 21 against 20;
+//   32000 tokens, without: 64 of 16 rows 32 against 35, 64 of 30 (123 MB) 46 against 35.
+static bool verify_ahead(int B, int total, int vocab, int max_seqlen, int dtype, bool draft, int *piece, int *pieces) {
     const int64_t rows = std::min<int64_t>(total, (int64_t)B * max_seqlen);
+    const int64_t row = (int64_t)vocab * (dtype == ATTN_DTYPE_BF16 ? 2 : 4), few = (int64_t)(draft ? 32 : 16) << 20;
     *pieces = 0;
-    if (rows > 16 * (int64_t)B) return false;
+    if (rows > 16 * (int64_t)B && rows > few / row) return false;
     *piece = attn::verify_piece(rows * (draft ? 2 : 1), vocab, pieces);
     if ((int64_t)B * std::min(max_seqlen, 16) * (draft ? 2 : 1) <= 0x7fffffff / *pieces) return true;
     *pieces = 0;  // (more blocks than a launch has)
@@ -55,7 +60,7 @@ size_t attn_verify_tree_workspace_bytes(int B, int total, int vocab, int max_seq
     if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_FP32) return 0;
     int piece, pieces;
     size_t ends, sums;
-    verify_ahead(B, total, vocab, max_seqlen, with_draft != 0, &piece, &pieces);
+    verify_ahead(B, total, vocab, max_seqlen, dtype, with_draft != 0, &piece, &pieces);
     verify_workspace(B, total, max_seqlen, with_draft != 0, pieces, &ends, &sums);
     return ends + sums;
 }
@@ -104,7 +109,7 @@ attn_status_t attn_verify_tree(const void *logits, const void *draft_logits, int
     p.V = vocab;
     p.width = max_seqlen;
     p.fp32 = dtype == ATTN_DTYPE_FP32 ? 1 : 0;
-    verify_ahead(B, total, vocab, max_seqlen, draft_logits != nullptr, &p.piece, &p.pieces);
+    verify_ahead(B, total, vocab, max_seqlen, dtype, draft_logits != nullptr, &p.piece, &p.pieces);
     size_t ends, sums;
     verify_workspace(B, total, max_seqlen, draft_logits != nullptr, p.pieces, &ends, &sums);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < ends + sums) return ATTN_ERR_WORKSPACE;

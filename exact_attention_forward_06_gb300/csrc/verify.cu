@@ -22,8 +22,8 @@
 // fetching instructions.
 // Measured on one GB300, 131072 tokens: 64 sequences of five rows with their draft's (168
 // MB) 56 us, 31 of them the sums (5.4 TB/s); 16 trees of 40 to 64 rows, of which the walk
-// comes to two to nine, 25 us; five fp32 trees with 50001 tokens 18 us; one greedy chain
-// of five rows of 32768 tokens 6 to 10 us.
+// comes to two to nine, 26 us (62 where they were drawn from a draft's distributions); five
+// fp32 trees with 50001 tokens 18 us; one greedy chain of five rows of 32768 tokens 6 to 10 us.
 #include <algorithm>
 #include <cfloat>
 #include <cstdint>
@@ -225,7 +225,7 @@ __device__ __forceinline__ const float4 *exchange(Shared &sh, int &turn, uint32_
 
 // The sums of a set of threads' weights in two rows, each relative to its own maximum,
 // relative to the common ones: the maxima first, then one step each for the sums.
-__device__ __forceinline__ void warp_soft(float4 &x, float c) {
+__device__ __forceinline__ float4 warp_soft(float4 x, float c) {
     float mp = x.x, mq = x.z;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -244,6 +244,7 @@ __device__ __forceinline__ void warp_soft(float4 &x, float c) {
         x.y += __shfl_xor_sync(ALL, x.y, o);
         x.w += __shfl_xor_sync(ALL, x.w, o);
     }
+    return x;
 }
 
 // Numbers of all threads joined over each warp, the CTA and the cluster, always in the
@@ -268,31 +269,13 @@ struct Cluster {
     }
     __device__ __forceinline__ void soft(Soft &p, Soft &q, float c) {
         float4 x = make_float4(p.m, p.s, q.m, q.s);
-        warp_soft(x, c);
+        x = warp_soft(x, c);
         const float4 *slots = share(x, make_float4(-INFINITY, 0.f, -INFINITY, 0.f), [c](float4 y) {
-            warp_soft(y, c);
-            return y;
+            return warp_soft(y, c);
         });
-        float4 all[MAX_CLUSTER];
-        p.m = q.m = -INFINITY;
-#pragma unroll
-        for (uint32_t i = 0; i < MAX_CLUSTER; ++i) {
-            all[i] = slots[min(i, ctas - 1)];
-            p.m = fmaxf(p.m, all[i].x);
-            q.m = fmaxf(q.m, all[i].z);
-        }
-        p.s = q.s = 0.f;
-        const Top tp(p.m, c), tq(q.m, c);
-#pragma unroll
-        for (uint32_t i = 0; i < MAX_CLUSTER; ++i) {
-            float fp = tp.step(all[i].x, c), fq = tq.step(all[i].z, c);
-            if (!(Top::is_weight(fp) && Top::is_weight(fq))) {
-                fp = odd_weight(all[i].x, p.m, c);
-                fq = odd_weight(all[i].z, q.m, c);
-            }
-            p.s += i < ctas ? all[i].y * fp : 0.f;
-            q.s += i < ctas ? all[i].w * fq : 0.f;
-        }
+        const uint32_t lane = threadIdx.x & 31;
+        x = warp_soft(lane < ctas ? slots[lane] : make_float4(-INFINITY, 0.f, -INFINITY, 0.f), c);
+        p.m = x.x, p.s = x.y, q.m = x.z, q.s = x.w;
     }
     __device__ __forceinline__ float sum(float v) {
         const auto over_warp = [](float4 x) {
@@ -402,7 +385,7 @@ struct Slice {
 
 // What a thread's part of a row's slice comes to: the largest logit's key where nothing
 // is drawn, else maximum and sum.
-template <typename T, int NT>
+template <int DEPTH, typename T, int NT>
 __device__ __forceinline__ unsigned long long slice_best(const Slice<T, NT> &sl) {
     float top = -INFINITY;
     int where = -1;
@@ -412,7 +395,7 @@ __device__ __forceinline__ unsigned long long slice_best(const Slice<T, NT> &sl)
             where = i;
         }
     };
-    sl.template each<1, 3, false>(
+    sl.template each<1, DEPTH, false>(
         nullptr,
         [&](int at, const Chunk<T>(&chunk)[1], const Chunk<T>(&)[1], const Chunk<float>(&)[1]) {
             const Chunk<T> &x = chunk[0];
@@ -472,7 +455,7 @@ __device__ __forceinline__ void sum_slice(const VerifyParams &p, const Sequence 
     float2 *out = p.sums + ((int64_t)kind * p.total + row) * p.pieces + piece;
     if (!seq.draws) {
         auto *keys = reinterpret_cast<unsigned long long *>(warp);
-        unsigned long long k = slice_best(sl);
+        unsigned long long k = slice_best<3>(sl);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(ALL, k, o));
         if (lane == 0) keys[threadIdx.x >> 5] = k;
@@ -486,7 +469,7 @@ __device__ __forceinline__ void sum_slice(const VerifyParams &p, const Sequence 
     Soft sp, none;
     slice_soft<4, 0>(sl, sp, none, seq.c);
     float4 v = make_float4(sp.m, sp.s, -INFINITY, 0.f);
-    warp_soft(v, seq.c);
+    v = warp_soft(v, seq.c);
     if (lane == 0) warp[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x != 0) return;
@@ -543,10 +526,14 @@ struct Node {
         : tp(p.m, c_), tq(q.m, c_), ip(p.s > 0.f ? 1.f / p.s : 0.f), iq(q.s > 0.f ? 1.f / q.s : 0.f), c(c_) {
         plain = tp.m < FLT_MAX && tp.r == tp.r && tq.m < FLT_MAX && tq.r == tq.r;
     }
-    // p - q of a token in plain rows (q of a NaN: 0).
-    __device__ __forceinline__ float difference(float x, float y) const {
+    // The weights of a token in plain rows (q's of a NaN: 0), and p - q.
+    __device__ __forceinline__ float2 weights(float x, float y) const {
         const float q = ptx::ex2(fmaf(y, c, -tq.r));
-        return fmaf(ptx::ex2(fmaf(x, c, -tp.r)), ip, -(q <= 2.f ? q : 0.f) * iq);
+        return make_float2(ptx::ex2(fmaf(x, c, -tp.r)), q <= 2.f ? q : 0.f);
+    }
+    __device__ __forceinline__ float difference(float x, float y) const {
+        const float2 w = weights(x, y);
+        return fmaf(w.x, ip, -w.y * iq);
     }
 };
 
@@ -576,13 +563,16 @@ struct WalkEnd {
 static_assert(sizeof(WalkEnd) <= WALK_END_BYTES, "a sequence's place in the workspace");
 
 // The walk down a sequence's tree, a cluster of CTAs each.  AHEAD: the rows' sums are there.
-template <typename T, bool AHEAD>
+// KEEP: p and q of the slice's tokens stay in shared memory while a node's children are
+// rejected one after another (there is room for them, keep_bytes).
+template <typename T, bool AHEAD, bool KEEP>
 __global__ void __launch_bounds__(THREADS, 1) verify_kernel(const VerifyParams p, int slice) {
     ptx::wait_for_prior_work();
     ptx::allow_next_work();
     ptx::cluster_arrive();
     using Part = Slice<T, THREADS>;
     __shared__ Shared sh;
+    extern __shared__ float2 kept[];  // [place][THREADS]: p and q of this thread's tokens at a node
     const int tid = threadIdx.x;
     const uint32_t rank = ptx::cluster_rank(), ctas = (uint32_t)((p.V + slice - 1) / slice);
     const int b = blockIdx.x / ctas;
@@ -639,7 +629,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(const VerifyParams p
                     if (draft != nullptr) d.add(dpart[k].x, dpart[k].y, c);
                 }
                 float4 x = make_float4(a.m, a.s, d.m, d.s);
-                warp_soft(x, c);
+                x = warp_soft(x, c);
                 if (lane == 0) sh.stat[i] = x;
             } else {
                 const auto *part = reinterpret_cast<const unsigned long long *>(p.sums) + (int64_t)(begin + i) * p.pieces;
@@ -684,7 +674,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(const VerifyParams p
                 last = __float_as_int(sh.stat[cur].x);
             } else {
                 Part::prefetch(row, lo, hi, sizeof(T));
-                last = all.best(slice_best(Part(row, nullptr, lo, hi)));
+                last = all.best(slice_best<0>(Part(row, nullptr, lo, hi)));
             }
             if (last >= 0) each_child([&](int k) { return sh.token[k] == last; });
         } else {
@@ -703,7 +693,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(const VerifyParams p
                     px = value(row[sh.token[tid]]);
                     if (drow != nullptr) qx = value(drow[sh.token[tid]]);
                 }
-                slice_soft<1, 2>(rows, sp, sq, c);
+                slice_soft<1, 0>(rows, sp, sq, c);
                 all.soft(sp, sq, c);
                 if (child) {
                     child_probability(make_float4(sp.m, sp.s, sq.m, sq.s), c, px, qx);
@@ -713,6 +703,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(const VerifyParams p
                 __syncthreads();
             }
             rejected = known = 0;
+            int places = 0;    // tokens of this thread's in `kept`
             float left = 1.f;  // without draft: what is left of p
             each_child([&](int k) {
                 const int token = sh.token[k];
@@ -730,24 +721,44 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(const VerifyParams p
                     left = fmaxf(left - mine, 0.f);
                 } else {
                     if (rejected > known) {  // the sum that the last rejection left
-                        const Node node(sp, sq, c);
                         float sum = 0.f;
-                        const bool simple = node.plain && rejected == 1;
-                        const auto add = [&](float x, float y) {
-                            sum += simple ? fmaxf(node.difference(x, y), 0.f)
-                                          : odd_rest(x, y, sp.m, sq.m, node.ip, node.iq, c, rejected, known, sh.inv_left);
-                        };
-                        rows.template each<1, 1, false>(
-                            nullptr,
-                            [&](int, const Chunk<T>(&x)[1], const Chunk<T>(&y)[1], const Chunk<float>(&)[1]) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float2 v = x[0].pair(i), q = y[0].pair(i);
-                                    add(v.x, q.x);
-                                    add(v.y, q.y);
+                        if (KEEP && known > 0) {
+                            // (step by step what rest() does)
+                            const float inv = sh.inv_left[known - 1];
+                            for (int i = 0; i < places; ++i) {
+                                float2 x = kept[i * THREADS + tid];
+                                if (inv > 0.f) x.x = fmaxf(x.x - x.y, 0.f) * inv;
+                                kept[i * THREADS + tid] = x;
+                                sum += fmaxf(x.x - x.y, 0.f);
+                            }
+                        } else {
+                            const Node node(sp, sq, c);
+                            const bool simple = node.plain && rejected == 1;
+                            const auto add = [&](float x, float y) {
+                                if (KEEP) {
+                                    const float2 w = simple ? node.weights(x, y)
+                                                            : make_float2(odd_weight(x, sp.m, c), odd_weight(y, sq.m, c));
+                                    const float2 pq = make_float2(w.x * node.ip, w.y * node.iq);
+                                    kept[places++ * THREADS + tid] = pq;
+                                    sum += fmaxf(pq.x - pq.y, 0.f);
+                                } else {
+                                    sum += simple ? fmaxf(node.difference(x, y), 0.f)
+                                                  : odd_rest(x, y, sp.m, sq.m, node.ip, node.iq, c, rejected, known,
+                                                             sh.inv_left);
                                 }
-                            },
-                            [&](int at) { add(value(row[at]), value(drow[at])); });
+                            };
+                            rows.template each<1, 0, false>(
+                                nullptr,
+                                [&](int, const Chunk<T>(&x)[1], const Chunk<T>(&y)[1], const Chunk<float>(&)[1]) {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float2 v = x[0].pair(i), q = y[0].pair(i);
+                                        add(v.x, q.x);
+                                        add(v.y, q.y);
+                                    }
+                                },
+                                [&](int at) { add(value(row[at]), value(drow[at])); });
+                        }
                         const float z = all.sum(sum);
                         if (tid == 0) sh.inv_left[known] = z > 0.f ? 1.f / z : 0.f;
                         __syncthreads();
@@ -908,6 +919,17 @@ __global__ void __launch_bounds__(RACE_THREADS, RACE_BLOCKS) race_kernel(const V
     }
 }
 
+// The shared memory for a slice's p and q at a node: a thread has its chunks of eight, and two
+// tokens at the ends.  With it (slices of up to 24576 tokens) every sum after a node's first
+// needs no row and no exponential: rows of 131072 tokens, drawn trees of 40 to 64 rows, 16 of
+// them 64 us instead of 99; 32 of 8 to 16 rows of 32000 tokens 34 instead of 39.  Without it
+// the rows are read again for every sum, from L2.
+int64_t keep_bytes(int slice) {
+    return (((slice + 7) / 8 + THREADS - 1) / THREADS * 8 + 2) * (int64_t)(THREADS * sizeof(float2));
+}
+constexpr int KEEP_MOST = 200 * 1024;
+static_assert(KEEP_MOST + sizeof(Shared) <= 227 * 1024, "shared memory of a CTA");
+
 template <typename T>
 cudaError_t launch(const VerifyParams &p, cudaStream_t stream) {
     if (p.pieces > 0) {
@@ -925,8 +947,24 @@ cudaError_t launch(const VerifyParams &p, cudaStream_t stream) {
     int ctas = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_CLUSTER, ((int64_t)p.V + 4095) / 4096, 152 / p.B}));
     const int slice = ((p.V + ctas - 1) / ctas + 7) & ~7;
     ctas = (p.V + slice - 1) / slice;
+    const int64_t bytes = keep_bytes(slice);
+    const bool keep = p.draft != nullptr && bytes <= KEEP_MOST;
+    const auto kernel = keep ? (p.pieces > 0 ? verify_kernel<T, true, true> : verify_kernel<T, false, true>)
+                             : (p.pieces > 0 ? verify_kernel<T, true, false> : verify_kernel<T, false, false>);
+    if (keep) {
+        static thread_local int configured_device = -1;
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && configured_device != dev) {
+            for (auto k : {verify_kernel<T, true, true>, verify_kernel<T, false, true>})
+                if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, KEEP_MOST);
+            if (e == cudaSuccess) configured_device = dev;
+        }
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.B * ctas);
+    cfg.dynamicSmemBytes = keep ? (size_t)bytes : 0;
     cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -937,8 +975,7 @@ cudaError_t launch(const VerifyParams &p, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = p.pieces > 0 ? cudaLaunchKernelEx(&cfg, verify_kernel<T, true>, p, slice)
-                                       : cudaLaunchKernelEx(&cfg, verify_kernel<T, false>, p, slice);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, slice);
     if (e != cudaSuccess || p.temperature == nullptr) return e;
     // The race: as many CTAs as all SMs hold at once, a slice of 2048 tokens at least.
     const int64_t each = std::max(1, RACE_BLOCKS * 152 / p.B), even = (p.V + each - 1) / each;

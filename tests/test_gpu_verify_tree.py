@@ -182,6 +182,47 @@ def test_noise_that_is_not_positive_where_a_drawn_child_was_rejected(bad):
     assert call(d)[1][:, 0].tolist() == [-1, -1]
 
 
+@pytest.mark.parametrize("V", [24569, 24576, 24577, 24585, 26001])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_siblings_drawn_from_one_row_in_one_slice(V, dtype):
+    # so many sequences that each has one CTA, whose slice is as long as shared memory keeps, or longer
+    sizes = [0] * 80
+    sizes[3], sizes[41], sizes[79] = 9, 17, 6
+    d = make(90 + V % 7, sizes, V, "draft", dtype=dtype, tree="bush", sharp=2.0)
+    d["uniforms"][:] = 0.5 + d["uniforms"] / 2
+    check(d)
+    # with rows that begin anywhere, and numbers that are not plain
+    d["logits"][9, ::3] = math.nan
+    d["draft"][9, ::2] = -math.inf
+    d["logits"][0, 5] = math.inf
+    check(d)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tree", ["tree", "bush"])
+@pytest.mark.parametrize("kind", ["greedy", "top", "draft"])
+def test_large_trees_of_long_rows(kind, tree, dtype):
+    # more rows, and more bytes, than are summed up ahead: the walk sums up the rows that it comes to
+    d = make(98, [70, 3, 65], 131077, kind, dtype, tree=tree, temps=[1.0, 0.0, 0.7], sharp=8.0)
+    check(d)
+    gen = torch.Generator().manual_seed(99)
+    for name in ("logits", "draft"):
+        if d[name] is not None:
+            d[name][:, 7::3] = -math.inf
+            d[name][torch.randint(138, (40,), generator=gen), torch.randint(131077, (40,), generator=gen)] = math.nan
+    d["logits"][73, 99] = math.inf
+    check(d)
+
+
+def test_large_drawn_trees_in_one_slice():
+    sizes = [0] * 80
+    for b in (0, 8, 30, 31, 70, 79):
+        sizes[b] = 220
+    d = make(97, sizes, 24577, "draft", sharp=2.0)
+    d["uniforms"][:] = 0.5 + d["uniforms"] / 2
+    check(d)
+
+
 def test_equal_siblings_and_nothing_left():
     # the only two tokens are both children, and rejected although they have all the mass
     d = make(63, [4], 8, "top", tree="bush")
@@ -319,8 +360,8 @@ def test_more_sequences_than_sms():
 
 @pytest.mark.parametrize("kind", ["greedy", "top", "draft"])
 def test_short_and_long_trees_alike(kind):
-    """Rows summed up ahead (few a sequence) or one by one: the same sequences alone and beside a long tree."""
-    d = make(102, [12, 200, 3], 3000, kind, tree="chain" if kind == "greedy" else "tree", temps=[1.0, 0.8])
+    """Rows summed up ahead (few a sequence, or few bytes) or one by one: the same sequences alone and beside a long tree."""
+    d = make(102, [12, 200, 3], 90001, kind, tree="chain" if kind == "greedy" else "tree", temps=[1.0, 0.8])
     whole = call(d)
     check(d, whole)
     for b in (0, 2):
