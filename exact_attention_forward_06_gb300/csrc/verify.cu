@@ -922,14 +922,15 @@ __global__ void __launch_bounds__(RACE_THREADS, RACE_BLOCKS) race_kernel(const V
 }
 
 // The shared memory for a slice's p and q at a node: a thread has its chunks of eight, and two
-// tokens at the ends.  With it (slices of up to 24576 tokens) every sum after a node's first
+// tokens at the ends.  With it (slices of up to KEEP_TOKENS) every sum after a node's first
 // needs no row and no exponential: rows of 131072 tokens, drawn trees of 40 to 64 rows, 16 of
 // them 64 us instead of 99; 32 of 8 to 16 rows of 32000 tokens 34 instead of 39.  Without it
 // the rows are read again for every sum, from L2.
 int64_t keep_bytes(int slice) {
     return (((slice + 7) / 8 + THREADS - 1) / THREADS * 8 + 2) * (int64_t)(THREADS * sizeof(float2));
 }
-constexpr int KEEP_MOST = 200 * 1024;
+constexpr int KEEP_TOKENS = 24576;
+constexpr int KEEP_MOST = (KEEP_TOKENS / 8 / THREADS * 8 + 2) * THREADS * (int)sizeof(float2);
 static_assert(KEEP_MOST + sizeof(Shared) <= 227 * 1024, "shared memory of a CTA");
 
 template <typename T>
@@ -945,8 +946,26 @@ cudaError_t launch(const VerifyParams &p, cudaStream_t stream) {
                                                dim3((unsigned)blocks), dim3(SUM_THREADS), 0, stream, p, nodes);
         if (e != cudaSuccess) return e;
     }
-    // CTAs a sequence: one an SM, a slice of 4096 tokens at least.
-    int ctas = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_CLUSTER, ((int64_t)p.V + 4095) / 4096, 152 / p.B}));
+    // CTAs a sequence, with slices of 4096 tokens at least.  Walks that sum rows up: all eight as
+    // long as they run at once; with more sequences a second wave of CTAs evens their lengths
+    // out (131072 tokens, 40 rows: 64 sequences 58 us with four, 83 with the two that run at
+    // once, 45 46 us with six, 50 with three; 25 36 us with six, 42 with eight).  Rows summed up
+    // ahead: what a walk reads are the rows of rejected drawn children, most quickly in slices
+    // that shared memory keeps (32000 tokens, 128 sequences of 8 rows: 76 us with two, 113 with
+    // one, but chains of 131072, 100 of 5 rows, 85 against 79); a walk without temperature reads
+    // nothing and needs one (16 of 5 rows 8.4 us, 10.2 with eight).  Up to eight sequences take
+    // eight, more six (16 chains of 5 rows 26 us, 30 with eight).
+    const int per = 152 / p.B;
+    int want;
+    if (p.pieces == 0) {
+        want = per >= MAX_CLUSTER ? MAX_CLUSTER : std::min({6, 304 / p.B, (p.V + 8191) / 8192});
+    } else if (p.draft != nullptr) {
+        const int keeping = (p.V + KEEP_TOKENS - 1) / KEEP_TOKENS;
+        want = std::max(keeping <= per ? keeping : 2, std::min(per, p.B > 8 ? 6 : MAX_CLUSTER));
+    } else {
+        want = p.temperature != nullptr ? per : 1;
+    }
+    int ctas = std::max(1, std::min({MAX_CLUSTER, (p.V + 4095) / 4096, want}));
     const int slice = ((p.V + ctas - 1) / ctas + 7) & ~7;
     ctas = (p.V + slice - 1) / slice;
     const int64_t bytes = keep_bytes(slice);

@@ -182,10 +182,10 @@ def test_noise_that_is_not_positive_where_a_drawn_child_was_rejected(bad):
     assert call(d)[1][:, 0].tolist() == [-1, -1]
 
 
-@pytest.mark.parametrize("V", [24569, 24576, 24577, 24585, 26001])
+@pytest.mark.parametrize("V", [24569, 24576, 24577, 49145, 49152, 49153, 50001])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_siblings_drawn_from_one_row_in_one_slice(V, dtype):
-    # so many sequences that each has one CTA, whose slice is as long as shared memory keeps, or longer
+def test_siblings_drawn_from_one_row_in_long_slices(V, dtype):
+    # so many sequences that each has one CTA or two, whose slices are as long as shared memory keeps, or longer
     sizes = [0] * 80
     sizes[3], sizes[41], sizes[79] = 9, 17, 6
     d = make(90 + V % 7, sizes, V, "draft", dtype=dtype, tree="bush", sharp=2.0)
@@ -214,11 +214,11 @@ def test_large_trees_of_long_rows(kind, tree, dtype):
     check(d)
 
 
-def test_large_drawn_trees_in_one_slice():
+def test_large_drawn_trees_in_long_slices():
     sizes = [0] * 80
     for b in (0, 8, 30, 31, 70, 79):
         sizes[b] = 220
-    d = make(97, sizes, 24577, "draft", sharp=2.0)
+    d = make(97, sizes, 73729, "draft", sharp=2.0)
     d["uniforms"][:] = 0.5 + d["uniforms"] / 2
     check(d)
 
