@@ -26,19 +26,22 @@ bool overlap(const void *a, const void *b, size_t bytes) {
 
 // Whether all rows are summed up ahead of the walk, and in what slices.  That reads rows
 // that the walk may not come to, but all at once; the walk by itself waits for one row
-// after the other, 2 to 4 us each, with draft 4 to 8.  So: up to 16 rows a sequence, or few
-// bytes in all.  us ahead against not, rows of bf16:
-//   131072 tokens, with draft: chains, 16 of 8 rows 33 against 51, 64 of 12 rows 96 against
-//     202; trees, 8 of 16 rows 40 against 54, 16 of 16 rows 57 against 59, 16 of 24 rows
-//     (201 MB) 72 against 55, one of 120 rows (63 MB) 49 against 56, 4 of 48 (101) 45 against 28;
-//   without: 64 trees of 12 rows 64 against 72, 8 of 12 23 against 23, 8 of 24 (50 MB) 28
-//     against 26, one of 24 (6 MB) 17 against 21, one of 64 (17 MB) 21 against 20;
-//   32000 tokens, without: 64 of 16 rows 32 against 35, 64 of 30 (123 MB) 46 against 35.
+// after the other, 2 to 4 us each, with draft 4 to 8.  us ahead against not, rows of bf16:
+//   with draft, 131072 tokens: chains, 16 of 8 rows 31 against 51, 64 of 12 96 against 156;
+//     trees, 8 of 16 rows 41 against 53, 16 of 16 61 against 58, 16 of 24 (201 MB) 72 against
+//     55, one of 120 (63 MB) 49 against 56, 4 of 48 (101 MB) 45 against 28;
+//   without, trees: 64 of 5 rows of 131072 (84 MB) 44 against 47, 16 of 8 (34 MB) 27 against
+//     25, 16 of 16 (67 MB) 33 against 24, one of 24 (6 MB) 17 against 21, one of 64 (17 MB) 21
+//     against 20; of 32000, 64 of 8 rows (33 MB) 26 against 33, 64 of 16 (66 MB) 32 against 36,
+//     64 of 30 (123 MB) 46 against 35.
+// So, with draft: up to 16 rows a sequence, or 64 MB in all; without: 16 MB, or 64 where a
+// sequence has up to 16 rows.
 static bool verify_ahead(int B, int total, int vocab, int max_seqlen, int dtype, bool draft, int *piece, int *pieces) {
-    const int64_t rows = std::min<int64_t>(total, (int64_t)B * max_seqlen);
-    const int64_t row = (int64_t)vocab * (dtype == ATTN_DTYPE_BF16 ? 2 : 4), few = (int64_t)(draft ? 32 : 16) << 20;
+    const int64_t rows = std::min<int64_t>(total, (int64_t)B * max_seqlen), MB = 1 << 20;
+    const int64_t bytes = rows * vocab * (dtype == ATTN_DTYPE_BF16 ? 2 : 4) * (draft ? 2 : 1);
+    const bool few = rows <= 16 * (int64_t)B;
     *pieces = 0;
-    if (rows > 16 * (int64_t)B && rows > few / row) return false;
+    if (draft ? !few && bytes > 64 * MB : bytes > (few ? 64 : 16) * MB) return false;
     *piece = attn::verify_piece(rows * (draft ? 2 : 1), vocab, pieces);
     if ((int64_t)B * std::min(max_seqlen, 16) * (draft ? 2 : 1) <= 0x7fffffff / *pieces) return true;
     *pieces = 0;  // (more blocks than a launch has)

@@ -106,12 +106,13 @@ def test_verify_workspace_bytes(lib):
     need = A.verify_tree_workspace_bytes
     align = lambda x: (x + 255) // 256 * 256  # noqa: E731
     bf, fp = torch.bfloat16, torch.float32
-    # up to 16 rows a sequence, the rows' sums come first: slices of 4096 to 16384 tokens
+    # up to 16 rows a sequence (and 64 MB, without draft), the rows' sums come first: slices of 4096 to 16384 tokens
     assert need(2, 9, 100, 8, bf) == align(2 * (64 + 32)) + 9 * 8
     assert need(64, 320, 131072, 5, bf, True) == align(64 * (64 + 20)) + 320 * 2 * 8 * 8
     assert need(1, 5, 32768, 5, fp) == align(64 + 20) + 5 * 8 * 8
     assert need(4, 65, 131072, 40, bf) == align(4 * (64 + 160))
-    assert need(1, 16, 1 << 28, 16, bf) == align(64 + 64) + 16 * 64 * 8
+    assert need(1, 16, 1 << 28, 16, bf, True) == align(64 + 64) + 16 * 2 * 64 * 8
+    assert need(1, 16, 1 << 28, 16, bf) == align(64 + 64)
     for bad in ((0, 9, 100, 8), (2, 0, 100, 8), (2, 9, 0, 8), (2, 9, (1 << 28) + 1, 8), (2, 9, 100, 0), (2, 9, 100, 257)):
         assert need(*bad) == 0
     assert lib.attn_verify_tree_workspace_bytes(2, 9, 100, 8, 2, 0) == 0
