@@ -420,7 +420,7 @@ __device__ __forceinline__ Unit next_unit(const PrefillParams &p, bool first) {
 // 110 at the copy's rate and the start 5; 64 tokens each (169 GFLOP) 167 us: 1.4 to 1.7
 // us a tile of 256 rows, between the exponentials' 1.1 and what the groups' waits for one
 // another add, and 5 to 9 us a unit.  Three caches of 60 to 131 thousand tokens, one KV
-// head for 32, trees of 17 to 61 (160 GFLOP) 147 us.  One sequence of 205 tokens, five
+// head for 32, trees of 17 to 61 (160 GFLOP) 145 us.  One sequence of 205 tokens, five
 // of them drafted: 10 us, a chain of launch, plan, loads, two tiles and the store.
 
 // One sequence's part of the line: Hkv x row blocks x (K/V tiles and a unit's cost).

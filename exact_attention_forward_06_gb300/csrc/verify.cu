@@ -22,7 +22,7 @@
 // fetching instructions.
 // Measured on one GB300, 131072 tokens: 64 sequences of five rows with their draft's (168
 // MB) 56 us, 31 of them the sums (5.4 TB/s); 16 trees of 40 to 64 rows, of which the walk
-// comes to two to nine, 26 us (62 where they were drawn from a draft's distributions); five
+// comes to two to nine, 26 to 31 us (62 where they were drawn from a draft's distributions); five
 // fp32 trees with 50001 tokens 18 us; one greedy chain of five rows of 32768 tokens 6 to 10 us.
 #include <algorithm>
 #include <cfloat>
