@@ -469,7 +469,7 @@ attn_status_t attn_fwd_tree_paged(const void *q, const void *k_pages, const void
     p.first = reinterpret_cast<int *>(ws);
     p.ws_o = reinterpret_cast<float *>(ws + first);
     p.ws_lse = reinterpret_cast<float *>(ws + first + o);
-    p.inject = attn::take_inject(1);
+    p.inject = attn::take_inject(1) ? 1 : attn::take_inject(3) ? 2 : 0;
     const int sms = di->sm_count < attn::kTreeMaxCtas ? di->sm_count : attn::kTreeMaxCtas;
     const int ctas = line * B < sms ? (int)(line * B) : sms;
     p.n_items = ctas;  // (a CTA's items are its share: nothing is claimed)
@@ -679,7 +679,7 @@ attn_status_t attn_set_wait_budget_ns(uint64_t ns) {
 }
 
 attn_status_t attn_debug_inject(int mode) {
-    if (mode < 0 || mode > 2) return ATTN_ERR_INVALID_ARG;
+    if (mode < 0 || mode > 3) return ATTN_ERR_INVALID_ARG;
     g_inject.store(mode);
     return ATTN_OK;
 }

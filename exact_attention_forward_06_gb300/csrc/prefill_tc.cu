@@ -98,8 +98,8 @@ constexpr uint32_t ITEM_READERS = 2 + 8;
 // q_full[2], q_free[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[2], s_free[2],
 // p_full[2], o_full[2], fin, item_full[ITEM_RING], item_empty[ITEM_RING],
 // stage_ready[2], stage_taken[2]; behind them the tensor-memory slot, the abort flag,
-// the item ring, the store commands, and for trees v_raw[NSLOT] and the flags of keys
-// whose values are not finite
+// the item ring, the store commands, and for trees v_raw[NSLOT], the flags of keys
+// whose values are not finite and the cleaner's last word
 constexpr int NBARS = 2 + 2 + 2 * NSLOT + 2 + 2 + 2 + 2 + 1 + 2 * ITEM_RING + 2 + 2;
 constexpr uint32_t SMEM_MISC = 896;
 constexpr uint32_t SMEM_ALIGN = 1024;
@@ -111,7 +111,8 @@ constexpr float LN2 = 0.6931471805599453f;
 constexpr int TREE_UNITS = 4;
 constexpr int TREE_TILES = (kTreeMaxNodes + BN - 2) / BN + 1;
 static_assert(TREE_TILES == 3, "a tree's keys begin anywhere in their first tile");
-static_assert(NBARS * 8 + 8 + 64 * ITEM_RING + 2 * 32 + 8 * NSLOT + TREE_UNITS * TREE_TILES * 16 <= SMEM_MISC, "barrier area too small");
+static_assert(NBARS * 8 + 8 + 64 * ITEM_RING + 2 * 32 + 8 * NSLOT + TREE_UNITS * TREE_TILES * 16 + 4 <= SMEM_MISC,
+              "barrier area too small");
 
 constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, 128, 0, 0);   // Q K^T: both K-major
 constexpr uint32_t IDESC_PV = ptx::idesc_bf16_f32(128, 128, 0, 1);  // P V: V is N(d)-major
@@ -165,6 +166,12 @@ struct SmemLayout {
     __device__ volatile uint32_t *odd_keys(int u, int i) const {
         return reinterpret_cast<volatile uint32_t *>(bars + NBARS + 1) + 16 * ITEM_RING + 16 +
                2 * NSLOT + (u % TREE_UNITS * TREE_TILES + i) * 4;
+    }
+    // Once a tree's cleaner has left: the parities of the v_raw phases that it would have waited
+    // for next (bit s: slot s) and bit 31; 0 before.
+    __device__ volatile uint32_t *cleaner_left() const {
+        return reinterpret_cast<volatile uint32_t *>(bars + NBARS + 1) + 16 * ITEM_RING + 16 + 2 * NSLOT +
+               TREE_UNITS * TREE_TILES * 4;
     }
     __device__ uint8_t *q_tile(int t) const { return base + (t ? SMEM_Q1 : SMEM_Q0); }
     // Ring slot s: a K or V tile, or a tile's output staging area.
@@ -856,6 +863,23 @@ __device__ void producer_paged(const PrefillParams &p, const SmemLayout &sm, con
     }
 }
 
+// Drain ring item i of a tree.  The copy of a V tile that goes through the cleaner completes
+// v_raw, and kv_full only follows if the cleaner is there to pass it on; once that has left,
+// the one such copy that the slot can hold is that of the phase it left at.
+__device__ __forceinline__ void tree_drain(const SmemLayout &sm, const WaitCtx &wc, int i) {
+    const int slot = i % NSLOT;
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t it = 0;; ++it) {
+        if (ptx::mbar_try(sm.kv_full(slot), (i / NSLOT) & 1)) return;
+        const uint32_t left = *sm.cleaner_left();
+        if (left != 0 && ptx::mbar_test(sm.v_raw(slot), left >> slot & 1u)) return;
+        if ((it & 15u) == 0 && ptx::globaltimer() - t0 > wc.budget_ns) {
+            report_status(wc.status, kStatusTimeout, kSiteDrain);
+            return;
+        }
+    }
+}
+
 // Trees: the same for the segments of the CTA's share, with no staging slots.  The units
 // follow one another closely, and waiting for Q first, as above, would let the ring run
 // empty at each: a unit's first three K/V items take slots that the unit before frees
@@ -961,7 +985,7 @@ __device__ void producer_tree(const PrefillParams &p, const SmemLayout &sm, cons
     if (lane == 0) {
         for (int t = 0; t < 2; ++t)
             if (qn[t] > 0) drain_wait(sm.q_full(t), (qn[t] - 1) & 1, wc);
-        for (int i = max(0, n - NSLOT); i < n; ++i) drain_wait(sm.kv_full(i % NSLOT), (i / NSLOT) & 1, wc);
+        for (int i = max(0, n - NSLOT); i < n; ++i) tree_drain(sm, wc, i);
     }
 }
 
@@ -983,11 +1007,17 @@ __device__ void tree_cleaner(const SmemLayout &sm, const WaitCtx &wc, int lane) 
         const bool got = read_unit(sm, wc, u, false, w);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(sm.item_empty(u % ITEM_RING));
-        if (!got || w.n_kv < 0) return;
+        if (!got || w.n_kv < 0) {
+            if (lane == 0) *sm.cleaner_left() = phases | 0x80000000u;
+            return;
+        }
         const int tree0 = w.Sk - w.Sq;
         for (int j = max(tree0 / BN - w.j_lo, 0); j < w.n_kv; ++j) {
             const int slot = (nb + 2 * j + 1) % NSLOT;
-            if (!warp_wait_bounded(sm.v_raw(slot), phases >> slot & 1u, wc, kSiteSoftmaxV)) return;
+            if (!warp_wait_bounded(sm.v_raw(slot), phases >> slot & 1u, wc, kSiteSoftmaxV)) {
+                if (lane == 0) *sm.cleaner_left() = phases | 0x80000000u;
+                return;
+            }
             phases ^= 1u << slot;
             const int kbase = (w.j_lo + j) * BN;
             uint8_t *vt = sm.slot(slot);
@@ -1740,7 +1770,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ptx::mbar_init(sm.stage_ready(t), 1);
             ptx::mbar_init(sm.stage_taken(t), 1);
         }
-        *sm.abort_flag() = 0;
+        // (fault injection: raised from the start; a test of p.inject in the cleaner took 13% of three long caches)
+        *sm.abort_flag() = KIND == kTree ? p.inject >> 1 : 0;
+        if (KIND == kTree) *sm.cleaner_left() = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&map_q);
         ptx::prefetch_tensormap(&map_k);

@@ -23,7 +23,7 @@ struct PrefillParams {
     int n_pk;          // units per (batch, KV group) when packing: ceil(Sq / (2 * pack_pos))
     unsigned *status;  // device status word [code, site]
     uint64_t budget_ns;
-    int inject;        // 1: producer issues nothing (fault-injection test)
+    int inject;        // 1: producer issues nothing, 2: a tree's CTAs begin with the abort flag up (fault-injection tests)
     int round_mode;    // RoundMode of the bf16 output (epilogue and merge)
     // Tail split: units [0, n_full_units) run whole; each of the following
     // split_units units is cut into split_parts key ranges, one CTA each, whose

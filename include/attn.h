@@ -732,6 +732,10 @@ attn_status_t attn_set_wait_budget_ns(uint64_t ns);
  * cleanly (no fault, no hang, nothing left in flight).  mode 2: the same for
  * the next decode: over bf16 pages its load-issuing warps issue nothing, over
  * the 4-bit cache (attn_decode_paged_q4) the first two warps of each CTA do not.
+ * mode 3: every CTA of the next attn_fwd_tree_paged begins as if one of its waits
+ * had run out: copies that need no wait are issued, the other warps leave, and the
+ * call ends as soon as those copies have landed (nothing is recorded, and out and
+ * lse hold anything).
  * A request clears itself with the launch that takes it; other launches leave
  * it.
  */
