@@ -1465,6 +1465,7 @@ __device__ void softmax_wg(const PrefillParams &p, const SmemLayout &sm, const W
                 const int tile = tree0 / BN + i;
                 if (tile >= w.j_lo && tile < w.j_lo + w.n_kv) tree_visible(p, w, pos, valid, lane, tile * BN, seen[i]);
             }
+            __syncwarp();  // (the lanes' walks differ in length, and what follows wants the warp converged)
         }
         for (int j = 0; !dead && j < w.n_kv; ++j) {
             const int g = g0 + j;
