@@ -17,11 +17,6 @@ bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_
 // A device pointer to 4-byte elements.
 bool ok4(const void *p) { return p != nullptr && aligned(p, 4); }
 
-bool overlap(const void *a, const void *b, size_t bytes) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + bytes && y < x + bytes;
-}
-
 }  // namespace
 
 // Whether all rows are summed up ahead of the walk, and in what slices.  That reads rows
@@ -143,8 +138,10 @@ attn_status_t attn_compact_paged(void *k_pages, void *v_pages, const int32_t *bl
         ((int64_t)layers * 2 * Hkv * 16 + 127) / 128 > (int64_t)0x7fffffff / B)
         return ATTN_ERR_INVALID_ARG;
     // Every block reads the lengths: they are not replaced in place.
-    const size_t bytes = (size_t)B * 4;
-    if (overlap(seqlens_out, seqlens_k, bytes) || overlap(seqlens_out, counts, bytes)) return ATTN_ERR_INVALID_ARG;
+    const size_t ints = (size_t)B * 4, pool = (size_t)layers * num_pages * 16 * Hkv * 256;
+    if (attn::writes_overlap({{seqlens_out, ints}}, {{seqlens_k, ints}, {counts, ints}})) return ATTN_ERR_INVALID_ARG;
+    // A row's threads move it once: keys and values may be the same rows, and no others.
+    if (k_pages != v_pages && attn::writes_overlap({{k_pages, pool}, {v_pages, pool}}, {})) return ATTN_ERR_INVALID_ARG;
     attn::CompactParams p = {};
     p.k_pages = k_pages;
     p.v_pages = v_pages;
@@ -156,6 +153,7 @@ attn_status_t attn_compact_paged(void *k_pages, void *v_pages, const int32_t *bl
     p.seqlens_out = seqlens_out;
     p.B = B;
     p.layers = layers;
+    p.tensors = k_pages == v_pages ? 1 : 2;
     p.Hkv = Hkv;
     p.total = total;
     p.width = max_seqlen;

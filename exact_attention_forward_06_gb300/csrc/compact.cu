@@ -29,7 +29,8 @@ constexpr int THREADS = 128;
 constexpr int UNROLL = 8;
 constexpr int PAGE = 16;
 
-// blockIdx.x: sequence x block of 16-byte columns (layer, K or V, byte of the row).
+// blockIdx.x: sequence x block of 16-byte columns (layer, K or V where they are two pools, byte
+// of the row).
 __global__ void __launch_bounds__(THREADS) compact_kernel(const CompactParams p, int blocks_per_seq, int64_t columns) {
     ptx::wait_for_prior_work();
     ptx::allow_next_work();
@@ -81,9 +82,10 @@ __global__ void __launch_bounds__(THREADS) compact_kernel(const CompactParams p,
     const int64_t column = (int64_t)block * THREADS + tid;
     if (column >= columns) return;
     const int row_columns = p.Hkv * 16;
-    const int64_t part = column / row_columns;  // layer x (K, V)
-    uint4 *pool = static_cast<uint4 *>(part & 1 ? p.v_pages : p.k_pages) +
-                  (part >> 1) * p.num_pages * PAGE * row_columns + (column - part * row_columns);
+    const int64_t part = column / row_columns;  // layer x tensor
+    const int64_t layer = p.tensors == 2 ? part >> 1 : part;
+    uint4 *pool = static_cast<uint4 *>(p.tensors == 2 && (part & 1) ? p.v_pages : p.k_pages) +
+                  layer * p.num_pages * PAGE * row_columns + (column - part * row_columns);
     for (int j0 = first_move; j0 < count; j0 += UNROLL) {
         uint4 x[UNROLL];
 #pragma unroll
@@ -98,7 +100,7 @@ __global__ void __launch_bounds__(THREADS) compact_kernel(const CompactParams p,
 }  // namespace cp
 
 cudaError_t launch_compact(const CompactParams &p, cudaStream_t stream) {
-    const int64_t columns = (int64_t)p.layers * 2 * p.Hkv * 16;
+    const int64_t columns = (int64_t)p.layers * p.tensors * p.Hkv * 16;
     const int blocks = (int)((columns + cp::THREADS - 1) / cp::THREADS);
     return launch_dependent(cp::compact_kernel, dim3((unsigned)(blocks * p.B)), dim3(cp::THREADS), 0, stream, p, blocks,
                             columns);

@@ -34,6 +34,7 @@ struct CompactParams {
     const int32_t *block_table, *seqlens, *cu, *path, *counts;
     int32_t *seqlens_out;
     int B, layers, Hkv, total, width, num_pages, max_blocks;
+    int tensors;  // 1: K and V are one pool, whose rows move once
     unsigned *status;
 };
 

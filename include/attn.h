@@ -675,7 +675,8 @@ attn_status_t attn_verify_tree(const void *logits, const void *draft_logits, int
  * sequence's alone.
  *
  * k_pages, v_pages: bf16 [layers][num_pages][16][Hkv][128], updated in place (one
- *      block table for all layers; layers = 1 for a pool of one layer).
+ *      block table for all layers; layers = 1 for a pool of one layer).  They may be one
+ *      pool, and do not overlap otherwise.
  * block_table, seqlens_k (the lengths with the trees), cu_seqlens: as
  *      attn_fwd_tree_paged; total bounds cu_seqlens.
  * path: int32 [B][max_seqlen], max_seqlen at least every n; counts: int32 [B], 0 .. n
