@@ -1068,7 +1068,7 @@ def compact_paged(k_pages, v_pages, block_table, seqlens_k, cu_seqlens, path, co
     k_pages, v_pages [num_pages, 16, Hkv, 128] or [layers, num_pages, 16, Hkv, 128] bf16, updated in place; block_table,
     seqlens_k (with the trees) and cu_seqlens as for fwd_tree_paged.  The kept nodes' keys and values move to the tree's
     first places.  total bounds the offsets (default: B times path's width).  Returns the new lengths, int32 [B]
-    (seqlens_out, which must not be seqlens_k).
+    (seqlens_out, which must not overlap an input).
     """
     lib = _lib or load()
     if stream is None:

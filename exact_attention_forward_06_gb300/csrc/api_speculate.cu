@@ -137,9 +137,13 @@ attn_status_t attn_compact_paged(void *k_pages, void *v_pages, const int32_t *bl
     if ((int64_t)layers * 2 * Hkv > 0x7fffffff / 16 ||
         ((int64_t)layers * 2 * Hkv * 16 + 127) / 128 > (int64_t)0x7fffffff / B)
         return ATTN_ERR_INVALID_ARG;
-    // Every block reads the lengths: they are not replaced in place.
+    // Every block reads the lengths, offsets, paths and pages, in any order with the first
+    // block's new lengths.
     const size_t ints = (size_t)B * 4, pool = (size_t)layers * num_pages * 16 * Hkv * 256;
-    if (attn::writes_overlap({{seqlens_out, ints}}, {{seqlens_k, ints}, {counts, ints}})) return ATTN_ERR_INVALID_ARG;
+    if (attn::writes_overlap({{seqlens_out, ints}},
+                             {{seqlens_k, ints}, {counts, ints}, {cu_seqlens, ints + 4}, {path, ints * max_seqlen},
+                              {block_table, ints * max_blocks_per_seq}, {k_pages, pool}, {v_pages, pool}}))
+        return ATTN_ERR_INVALID_ARG;
     // A row's threads move it once: keys and values may be the same rows, and no others.
     if (k_pages != v_pages && attn::writes_overlap({{k_pages, pool}, {v_pages, pool}}, {})) return ATTN_ERR_INVALID_ARG;
     attn::CompactParams p = {};

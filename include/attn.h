@@ -682,7 +682,7 @@ attn_status_t attn_verify_tree(const void *logits, const void *draft_logits, int
  * path: int32 [B][max_seqlen], max_seqlen at least every n; counts: int32 [B], 0 .. n
  *      (0 drops the whole tree).
  * seqlens_out: int32 [B] (written), seqlens_k[b] - n + counts[b]; must not overlap
- *      seqlens_k or counts.
+ *      an input.
  * A sequence with bad offsets, lengths, counts or path is left alone (seqlens_out =
  * seqlens_k), a row whose page, old or new, lies outside the pool does not move; both
  * are recorded as ATTN_ERR_DEVICE_BOUNDS.
