@@ -1007,7 +1007,8 @@ def verify_tree(logits, tokens, parents, cu_seqlens, *, draft_logits=None, tempe
     synchronisation).
 
     Returns (path, out_tokens, counts): int32 [B, max_seqlen] with counts[b] entries each and -1 behind, the kept nodes
-    (the root first) and the emitted tokens (those of the kept nodes after the root, and the last one).
+    (the root first) and the emitted tokens (those of the kept nodes after the root, and the last one).  Outputs that are
+    given must not overlap an input or one another.
     """
     lib = _lib or load()
     if stream is None:

@@ -111,6 +111,20 @@ attn_status_t attn_verify_tree(const void *logits, const void *draft_logits, int
     size_t ends, sums;
     verify_workspace(B, total, max_seqlen, draft_logits != nullptr, p.pieces, &ends, &sums);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < ends + sums) return ATTN_ERR_WORKSPACE;
+    // A sequence's CTAs read its rows and numbers, and other sequences' CTAs theirs, in any
+    // order with what is written.
+    const size_t ints = (size_t)B * 4, rows = (size_t)total * 4, kept = ints * max_seqlen;
+    const size_t drawn = temperature ? 1 : 0, drafted = draft_logits ? 1 : 0;
+    if (attn::writes_overlap({{path, kept}, {out_tokens, kept}, {counts, ints}, {workspace, ends + sums}},
+                             {{logits, ((total - 1) * logits_stride + V) * size},
+                              {draft_logits, drafted * ((total - 1) * draft_stride + V) * size},
+                              {tokens, rows},
+                              {parents, rows},
+                              {cu_seqlens, ints + 4},
+                              {temperature, drawn * ints},
+                              {uniforms, drawn * rows},
+                              {noise, drawn * ((B - 1) * noise_stride + V) * 4}}))
+        return ATTN_ERR_INVALID_ARG;
     p.ends = temperature ? static_cast<uint8_t *>(workspace) : nullptr;
     p.sums = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + ends);
     int sms;

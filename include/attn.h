@@ -656,6 +656,8 @@ size_t attn_verify_tree_workspace_bytes(int B, int total, int vocab, int max_seq
  * little more slowly.  Deterministic.
  * workspace: DEVICE buffer of at least attn_verify_tree_workspace_bytes(...) bytes,
  *      256-byte aligned, overwritten, one for each call that may run at the same time.
+ * What is written (path, out_tokens, counts, workspace) must not overlap anything else:
+ * of strided rows, from the first one's beginning to the last one's end.
  */
 attn_status_t attn_verify_tree(const void *logits, const void *draft_logits, int dtype, const int32_t *tokens,
                                const int32_t *parents, const int32_t *cu_seqlens, const float *temperature,

@@ -33,3 +33,36 @@ def test_compact_refuses_lengths_over_an_input(lib, name, place):
 @pytest.mark.parametrize("v", [MB + 256, MB + POOL - 256, MB - POOL + 256])
 def test_compact_refuses_pools_over_parts_of_one_another(lib, v):
     assert lib.attn_compact_paged(*dict(COMPACT, v=v, k=MB).values(), None) == 1
+
+
+BV, TOTAL, V = 3, 9, 100
+VERIFY = dict(logits=MB, draft=2 * MB, dtype=0, tok=3 * MB, par=4 * MB, cu=5 * MB, temp=6 * MB, u=7 * MB, noise=8 * MB,
+              path=9 * MB, out=10 * MB, counts=11 * MB, B=BV, total=TOTAL, V=V, width=WIDTH, ls=V, ds=V + 20, ns=V + 4,
+              ws=12 * MB, wsb=MB)
+VERIFY_READS = dict(logits=((TOTAL - 1) * V + V) * 2, draft=((TOTAL - 1) * (V + 20) + V) * 2, tok=TOTAL * 4, par=TOTAL * 4,
+                    cu=(BV + 1) * 4, temp=BV * 4, u=TOTAL * 4, noise=((BV - 1) * (V + 4) + V) * 4)
+VERIFY_WRITES = dict(path=BV * WIDTH * 4, out=BV * WIDTH * 4, counts=BV * 4)
+
+
+def _verify(lib, **kw):
+    return lib.attn_verify_tree(*dict(VERIFY, **kw).values(), None)
+
+
+@pytest.mark.parametrize("read", VERIFY_READS)
+@pytest.mark.parametrize("written", VERIFY_WRITES)
+def test_verify_refuses_outputs_over_an_input(lib, read, written):
+    for at in (VERIFY[read], VERIFY[read] + VERIFY_READS[read] - 4, VERIFY[read] - VERIFY_WRITES[written] + 4):
+        assert _verify(lib, **{written: at}) == 1
+
+
+def test_verify_refuses_outputs_over_one_another(lib):
+    for a, b in (("path", "out"), ("path", "counts"), ("out", "counts")):
+        for at in (VERIFY[a], VERIFY[a] + VERIFY_WRITES[a] - 4, VERIFY[a] - VERIFY_WRITES[b] + 4):
+            assert _verify(lib, **{b: at}) == 1
+
+
+def test_verify_refuses_a_workspace_over_anything(lib):
+    need = A.verify_tree_workspace_bytes(BV, TOTAL, V, WIDTH, with_draft=True)
+    for name in list(VERIFY_READS) + list(VERIFY_WRITES):
+        assert _verify(lib, ws=VERIFY[name]) == 1
+        assert _verify(lib, ws=VERIFY[name] - need // 256 * 256) == 1
