@@ -427,10 +427,9 @@ attn_status_t attn_fwd_tree_paged(const void *q, const void *k_pages, const void
                                       ATTN_LAYOUT_BSHD, scale);
     if (st != ATTN_OK) return st;
     if (page_size != 16 || Hq / Hkv > 128) return ATTN_ERR_UNSUPPORTED;
-    // Several CTAs read a query.
-    const uintptr_t q_at = reinterpret_cast<uintptr_t>(q), out_at = reinterpret_cast<uintptr_t>(out);
-    const uintptr_t q_bytes = (uintptr_t)total_q * Hq * d * 2;
-    if (q_at < out_at + q_bytes && out_at < q_at + q_bytes) return ATTN_ERR_INVALID_ARG;
+    // Several CTAs read a query, and all of them the lengths, the pages and the trees.
+    const size_t row_bytes = (size_t)total_q * Hq * d * 2, lse_bytes = lse ? (size_t)total_q * Hq * 4 : 0;
+    if (attn::writes_overlap({{out, row_bytes}}, {{q, row_bytes}})) return ATTN_ERR_INVALID_ARG;
     if (B < 1 || max_seqlen_q < 1 || max_seqlen_q > ATTN_TREE_MAX) return ATTN_ERR_INVALID_ARG;
     if (!valid_round_mode(round_mode)) return ATTN_ERR_INVALID_ARG;
     // The line of K/V tiles, and the rows of the merge, are 32-bit.
@@ -441,6 +440,16 @@ attn_status_t attn_fwd_tree_paged(const void *q, const void *k_pages, const void
     const size_t need = attn_fwd_tree_paged_workspace_bytes(B, Hq, Hkv, d, max_seqlen_q);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need)
         return ATTN_ERR_WORKSPACE;
+    const size_t ints = (size_t)B * 4, pool = (size_t)num_pages * 16 * Hkv * d * 2;
+    if (attn::writes_overlap({{out, row_bytes}, {lse, lse_bytes}, {workspace, need}},
+                             {{q, row_bytes},
+                              {k_pages, pool},
+                              {v_pages, pool},
+                              {block_table, ints * max_blocks_per_seq},
+                              {seqlens_k, ints},
+                              {cu_seqlens_q, ints + 4},
+                              {parents, (size_t)total_q * 4}}))
+        return ATTN_ERR_INVALID_ARG;
     DeviceInfo *di = nullptr;
     if ((st = device_info(&di)) != ATTN_OK) return st;
     attn::PrefillParams p;

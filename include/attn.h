@@ -217,7 +217,7 @@ size_t attn_fwd_tree_paged_workspace_bytes(int B, int Hq, int Hkv, int d, int ma
  * A token is only affected by keys that it sees: keys and values of other
  * branches, and slots past a sequence's length, may hold anything, NaN and
  * infinities included.
- * out must not overlap q.  Hq / Hkv is at most 128 (ATTN_ERR_UNSUPPORTED), and the K/V
+ * out, lse and workspace must not overlap an input or one another.  Hq / Hkv is at most 128 (ATTN_ERR_UNSUPPORTED), and the K/V
  * tiles of all heads at most 2^31 - 1.  Offsets and lengths are checked as by attn_fwd_paged, and
  * seqlens_k[b] must be at least the tree's size (otherwise the sequence is
  * skipped); a parent outside its range counts as -1; all of these are recorded as

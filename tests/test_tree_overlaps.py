@@ -66,3 +66,36 @@ def test_verify_refuses_a_workspace_over_anything(lib):
     for name in list(VERIFY_READS) + list(VERIFY_WRITES):
         assert _verify(lib, ws=VERIFY[name]) == 1
         assert _verify(lib, ws=VERIFY[name] - need // 256 * 256) == 1
+
+
+BT, HQ, TQ = 3, 4, 9
+TREE = dict(q=MB, k=2 * MB, v=3 * MB, bt=4 * MB, sl=5 * MB, cu=6 * MB, par=7 * MB, out=8 * MB, lse=9 * MB, B=BT, Hq=HQ, Hkv=HKV,
+            total=TQ, longest=5, d=128, page=16, npages=PAGES, maxb=MAXB, scale=0.1, mode=0, ws=64 * MB, wsb=64 * MB)
+TREE_READS = dict(q=TQ * HQ * 256, k=PAGES * 16 * HKV * 256, v=PAGES * 16 * HKV * 256, bt=BT * MAXB * 4, sl=BT * 4,
+                  cu=(BT + 1) * 4, par=TQ * 4)
+TREE_WRITES = dict(out=TQ * HQ * 256, lse=TQ * HQ * 4)
+
+
+def _tree(lib, **kw):
+    return lib.attn_fwd_tree_paged(*dict(TREE, **kw).values(), None)
+
+
+@pytest.mark.parametrize("read", TREE_READS)
+def test_tree_attention_refuses_outputs_over_an_input(lib, read):
+    a, n = TREE[read], TREE_READS[read]
+    for at in (a, a + (n - 1) // 16 * 16, a - TREE_WRITES["out"] + 16):
+        assert _tree(lib, out=at) == 1
+    for at in (a, a + n - 4, a - TREE_WRITES["lse"] + 4):
+        assert _tree(lib, lse=at) == 1
+
+
+def test_tree_attention_refuses_outputs_over_one_another(lib):
+    for at in (TREE["out"], TREE["out"] + TREE_WRITES["out"] - 4, TREE["out"] - TREE_WRITES["lse"] + 4):
+        assert _tree(lib, lse=at) == 1
+
+
+def test_tree_attention_refuses_a_workspace_over_anything(lib):
+    need = A.fwd_tree_paged_workspace_bytes(BT, HQ, HKV, 128, 5)
+    for name in list(TREE_READS) + list(TREE_WRITES):
+        for at in (0, need // 2 // 256 * 256, (need - 1) // 256 * 256):
+            assert _tree(lib, **{name: TREE["ws"] + at}) == 1
