@@ -641,8 +641,9 @@ size_t attn_verify_tree_workspace_bytes(int B, int total, int vocab, int max_seq
  *      counts as -inf, and +inf as the largest finite fp32.
  * tokens: int32 [total], each node's token (a root's is not looked at).
  * temperature: fp32 [B] or NULL.  uniforms: fp32 [total] in [0, 1).  noise: fp32
- *      [B] rows, noise_stride elements apart, of positive numbers (an element that
- *      is not positive is never drawn).  Both NULL where temperature is.
+ *      [B] rows, noise_stride elements apart, of positive numbers from 2^-126 to 2^126,
+ *      as exponential numbers are (an element that is larger or not positive is never
+ *      drawn).  Both NULL where temperature is.
  * path: int32 [B][max_seqlen] (written): the kept nodes, the root first, by their
  *      place in the tree; then -1.  counts: int32 [B] (written), how many; the root
  *      counts, so 0 only where a sequence has no rows.
