@@ -21,16 +21,21 @@ bool ok4(const void *p) { return p != nullptr && aligned(p, 4); }
 
 // Whether all rows are summed up ahead of the walk, and in what slices.  That reads rows
 // that the walk may not come to, but all at once; the walk by itself waits for one row
-// after the other, 2 to 4 us each, with draft 4 to 8.  us ahead against not, rows of bf16:
-//   with draft, 131072 tokens: chains, 16 of 8 rows 31 against 51, 64 of 12 96 against 156;
-//     trees, 8 of 16 rows 41 against 53, 16 of 16 61 against 58, 16 of 24 (201 MB) 72 against
-//     55, one of 120 (63 MB) 49 against 56, 4 of 48 (101 MB) 45 against 28;
-//   without, trees: 64 of 5 rows of 131072 (84 MB) 44 against 47, 16 of 8 (34 MB) 27 against
-//     25, 16 of 16 (67 MB) 33 against 24, one of 24 (6 MB) 17 against 21, one of 64 (17 MB) 21
-//     against 20; of 32000, 64 of 8 rows (33 MB) 26 against 33, 64 of 16 (66 MB) 32 against 36,
-//     64 of 30 (123 MB) 46 against 35.
+// after the other, 2 to 4 us each, with draft 4 to 8.  us ahead against not, rows of 131072
+// tokens in bf16 where nothing else is said:
+//   with draft, chains: 16 of 8 rows 31 against 51, 64 of 5 58 against 95, 64 of 12 96 against
+//     156; trees, up to 16 rows: 8 of 16 41 against 54, 16 of 16 61 against 57, 32 of 8 101
+//     against 73, 64 of 5 164 against 119, 64 of 8 183 against 153, 64 of 16 220 against 155,
+//     the same 64 in fp32 59 against 95, 76 against 97 and 117 against 129; more rows: one of
+//     120 (60 MB) 49 against 56, 4 of 48 (96 MB) 45 against 29, 16 of 24 (192 MB) 72 against 55;
+//   without, trees: 64 of 4 rows (64 MB) 40 against 47, 64 of 5 (80 MB) 44 against 47, 16 of 8
+//     (32 MB) 27 against 25, 16 of 15 (60 MB) 31 against 32, 16 of 16 (64 MB) 33 against 24, one
+//     of 24 (6 MB) 18 against 21, one of 64 (16 MB) 21 against 21; of 32000, 64 of 8 rows (31
+//     MB) 27 against 34, 64 of 16 (62 MB) 33 against 37, 64 of 30 (117 MB) 46 against 35.
 // So, with draft: up to 16 rows a sequence, or 64 MB in all; without: 16 MB, or 64 where a
-// sequence has up to 16 rows.
+// sequence has up to 16 rows.  The host does not see whether trees are chains: the rule is
+// right for chains, which a draft model's tokens mostly are, and for fp32, and costs large
+// batches of short drawn trees in bf16 up to 42% more time.
 static bool verify_ahead(int B, int total, int vocab, int max_seqlen, int dtype, bool draft, int *piece, int *pieces) {
     const int64_t rows = std::min<int64_t>(total, (int64_t)B * max_seqlen), MB = 1 << 20;
     const int64_t bytes = rows * vocab * (dtype == ATTN_DTYPE_BF16 ? 2 : 4) * (draft ? 2 : 1);

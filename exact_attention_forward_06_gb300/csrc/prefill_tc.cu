@@ -425,10 +425,13 @@ __device__ __forceinline__ Unit next_unit(const PrefillParams &p, bool first) {
 // Measured on one GB300 (copy bandwidth 6696 GB/s): 32 sequences of 1024 to 8192 tokens,
 // 32 / 8 heads, five tokens each (704 MB) 121 us, 0.87 of it, of which the line takes
 // 110 at the copy's rate and the start 5; 64 tokens each (169 GFLOP) 167 us: 1.4 to 1.7
-// us a tile of 256 rows, between the exponentials' 1.1 and what the groups' waits for one
-// another add, and 5 to 9 us a unit.  Three caches of 60 to 131 thousand tokens, one KV
+// us a tile of 256 rows, 1.1 of them the exponentials and the rest the groups' waits for one
+// another, 5 to 9 us a unit, and the merge's 17; nothing is near its rate meanwhile (tensor
+// pipe 53%, HBM 58%, exponential unit 27%).  Three caches of 60 to 131 thousand tokens, one KV
 // head for 32, trees of 17 to 61 (160 GFLOP) 145 us.  One sequence of 205 tokens, five
-// of them drafted: 10 us, a chain of launch, plan, loads, two tiles and the store.
+// of them drafted: 10 us, a chain of launch, plan, loads, two tiles and the store, under a
+// table of at most 16 pages; under a wider one (2048 or 8192 pages), which is cut and merged
+// by its width, 1.4 us more.
 
 // One sequence's part of the line: Hkv x row blocks x (K/V tiles and a unit's cost).
 struct TreeSeq {

@@ -9,9 +9,11 @@
 // left of p as argmax_i p_i / e_i: of independent exponential numbers e_i / p_i the
 // smallest is that of i with probability p_i.
 //
-// Three kernels.  sums_kernel (short trees only) takes maximum and sum of the
+// Three kernels.  sums_kernel (where trees are short or their rows few bytes: the rule
+// is verify_ahead's) takes maximum and sum of the
 // exponentials of all rows, which is what decisions need of a row besides the
-// children's own logits; it reads rows that the walk may not come to, but all at once.
+// children's own logits; it reads rows that the walk may not come to, and draft rows of
+// nodes without children, which nothing asks for, but all at once.
 // verify_kernel walks, a cluster of CTAs a sequence, each on a slice of the vocabulary:
 // where a row's sums are not there it takes them (one pass, an exchange through the
 // cluster's shared memory), then every thread of every CTA decides by itself, from the
@@ -22,7 +24,7 @@
 // fetching instructions.
 // Measured on one GB300, 131072 tokens: 64 sequences of five rows with their draft's (168
 // MB) 56 us, 31 of them the sums (5.4 TB/s); 16 trees of 40 to 64 rows, of which the walk
-// comes to two to nine, 26 to 31 us (62 where they were drawn from a draft's distributions); five
+// comes to two to nine, 24 to 31 us (62 where they were drawn from a draft's distributions); five
 // fp32 trees with 50001 tokens 18 us; one greedy chain of five rows of 32768 tokens 6 to 10 us.
 #include <algorithm>
 #include <cfloat>
@@ -380,7 +382,7 @@ struct Slice {
     // Brings it into L2, a line a thread at a time.
     static __device__ __forceinline__ void prefetch(const void *row, int lo, int hi, int size) {
         const char *p = static_cast<const char *>(row) + (int64_t)lo * size;
-        const uint32_t bytes = (uint32_t)(hi - lo) * (uint32_t)size;  // (2^31 elements of a cluster's slice: below 2^32)
+        const uint32_t bytes = (uint32_t)(hi - lo) * (uint32_t)size;  // (a row has 2^28 elements at most)
         for (uint32_t i = threadIdx.x * 128; i < bytes; i += NT * 128) ptx::prefetch_l2(p + i);
     }
 };
@@ -924,7 +926,7 @@ __global__ void __launch_bounds__(RACE_THREADS, RACE_BLOCKS) race_kernel(const V
 // The shared memory for a slice's p and q at a node: a thread has its chunks of eight, and two
 // tokens at the ends.  With it (slices of up to KEEP_TOKENS) every sum after a node's first
 // needs no row and no exponential: rows of 131072 tokens, drawn trees of 40 to 64 rows, 16 of
-// them 64 us instead of 99; 32 of 8 to 16 rows of 32000 tokens 34 instead of 39.  Without it
+// them 62 us instead of 99; 32 of 8 to 16 rows of 32000 tokens 34 instead of 39.  Without it
 // the rows are read again for every sum, from L2.
 int64_t keep_bytes(int slice) {
     return (((slice + 7) / 8 + THREADS - 1) / THREADS * 8 + 2) * (int64_t)(THREADS * sizeof(float2));
