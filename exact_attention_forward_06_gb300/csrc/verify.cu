@@ -109,32 +109,56 @@ __device__ __forceinline__ float value(float x) { return x; }
 
 __device__ __forceinline__ bool vec_ok(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// The weight exp((x - m) / T) of a logit below a row's largest, m, c = log2 e / T: 0 for
-// NaN and -inf (and where m is -inf: nothing is left), 1 for +inf (m is then the largest
-// finite number).
-__device__ __noinline__ float odd_weight(float x, float m, float c) {
-    return ptx::ex2(fminf(fmaxf((x - fminf(m, FLT_MAX)) * c, -INFINITY), 0.f));
+// (x - m) c of two logits, c = log2 e / T, with no overflow on the way.
+__device__ __forceinline__ float odd_exponent(float x, float m, float c) {
+    return (0.5f * fminf(x, FLT_MAX) - 0.5f * fminf(m, FLT_MAX)) * c * 2.f;
 }
+
+__device__ __noinline__ float odd_weight(float x, float m, float c);
 
 // A row's largest logit m and r = m c, rounded.  Weights are taken relative to r, which
 // the rounding leaves a little off m c: as every weight and every sum goes by the same r,
 // or by the difference of two of them, that cancels, and a weight is one FFMA and one
-// exponential.  Whatever does not come out as a number up to 1 (with rounding) goes the
-// long way.
+// exponential.  r is off by half at most, up to 2^23: the largest weight is then up to
+// sqrt(2).  Beyond (very low temperatures, a row that is masked with the type's lowest
+// value) r is NaN, weights are relative to m c itself, and whatever does not come out as
+// a number up to 2 goes the long way.
 struct Top {
     float m, r;
+    static constexpr float MOST = 8388608.f;
     __device__ __forceinline__ Top(float largest, float c) : m(fminf(largest, FLT_MAX)) {
-        r = largest == -INFINITY ? 0.f : m * c;
-        if (!(fabsf(r) <= FLT_MAX)) r = NAN;  // m c is out of range: every weight goes the long way
+        r = largest == -INFINITY ? 0.f : __fmul_rn(m, c);
+        if (!(fabsf(r) <= MOST)) r = NAN;
     }
     __device__ __forceinline__ float weight(float x, float c) const {
         const float f = ptx::ex2(fmaf(x, c, -r));
         return f <= 2.f ? f : odd_weight(x, m, c);
     }
-    // What a sum relative to another maximum, m2, is multiplied with: by its r, not by m2 c.
-    __device__ __forceinline__ float step(float m2, float c) const { return ptx::ex2(__fmul_rn(m2, c) - r); }
+    // What a sum relative to another maximum, m2 (-inf: an empty sum), is multiplied with: by
+    // its r, not by m2 c.
+    __device__ __forceinline__ float step(float m2, float c) const {
+        const float r2 = __fmul_rn(m2, c), f = ptx::ex2(r2 - r);
+        return fabsf(r2) <= MOST || r2 == -INFINITY ? f : NAN;
+    }
     static __device__ __forceinline__ bool is_weight(float f) { return f <= 2.f; }
 };
+
+// The weight of a logit x of a row whose largest is m, the long way: 0 for NaN and -inf (and
+// where m is -inf: nothing is left), +inf counts as the largest finite number (as in m).
+__device__ __noinline__ float odd_weight(float x, float m, float c) {
+    if (!(x > -INFINITY) || m == -INFINITY) return 0.f;
+    const Top t(m, c);
+    return ptx::ex2(fminf(t.r == t.r ? fmaf(fminf(x, FLT_MAX), c, -t.r) : odd_exponent(x, m, c), 1.f));
+}
+
+// What a sum is multiplied with (see step) where one of the two maxima has no r, or neither.
+__device__ __noinline__ float odd_step(float m2, float m, float c) {
+    if (m2 == -INFINITY) return 0.f;
+    const Top a(m2, c), b(m, c);
+    const bool plain_a = a.r == a.r, plain_b = b.r == b.r;
+    return ptx::ex2(plain_a ? (plain_b ? a.r - b.r : fmaf(-b.m, c, a.r))
+                            : (plain_b ? fmaf(a.m, c, -b.r) : odd_exponent(a.m, b.m, c)));
+}
 
 // A maximum and a sum of weights relative to it.
 struct Soft {
@@ -148,7 +172,7 @@ struct Soft {
     __device__ __forceinline__ void raise(const Top &t, float c) {
         if (t.m > m) {
             const float f = t.step(m, c);
-            s *= Top::is_weight(f) ? f : odd_weight(m, t.m, c);
+            s *= Top::is_weight(f) ? f : odd_step(m, t.m, c);
             m = t.m;
         }
     }
@@ -157,7 +181,7 @@ struct Soft {
         const Top t(fmaxf(m, m2), c);
         raise(t, c);
         const float f = t.step(m2, c);
-        s += s2 * (Top::is_weight(f) ? f : odd_weight(m2, t.m, c));
+        s += s2 * (Top::is_weight(f) ? f : odd_step(m2, t.m, c));
     }
     template <typename T, int U>
     __device__ __forceinline__ void add(const Chunk<T> (&x)[U], float c);
@@ -239,8 +263,8 @@ __device__ __forceinline__ float4 warp_soft(float4 x, float c) {
     const Top p(mp, c), q(mq, c);
     float fp = p.step(x.x, c), fq = q.step(x.z, c);
     if (!(Top::is_weight(fp) && Top::is_weight(fq))) {
-        fp = odd_weight(x.x, mp, c);
-        fq = odd_weight(x.z, mq, c);
+        fp = odd_step(x.x, mp, c);
+        fq = odd_step(x.z, mq, c);
     }
     x = make_float4(mp, x.y * fp, mq, x.w * fq);
 #pragma unroll

@@ -655,6 +655,10 @@ size_t attn_verify_tree_workspace_bytes(int B, int total, int vocab, int max_seq
  * nodes; each is recorded as ATTN_ERR_DEVICE_BOUNDS.  logits and draft_logits need
  * the alignment of their elements only; rows that are not 16-byte aligned are read a
  * little more slowly.  Deterministic.
+ * Probabilities are fp32, whatever the temperature and however far from 0 the logits are:
+ * within about 2^-19 of themselves above a thousandth of the largest, 2^-15 at the least
+ * ones; below 2^-126 of it they are 0.  What siblings leave of p is
+ * as exact as a difference of such numbers.
  * workspace: DEVICE buffer of at least attn_verify_tree_workspace_bytes(...) bytes,
  *      256-byte aligned, overwritten, one for each call that may run at the same time.
  * What is written (path, out_tokens, counts, workspace) must not overlap anything else:
