@@ -1,6 +1,7 @@
 """Outputs of the tree operators that lie over their inputs are refused before any launch (CPU): blocks read the inputs in
 any order with other blocks' writes.  Only calls that have to be refused are made: addresses are made up."""
 import pytest
+import torch
 
 import exact_attention_forward_06_gb300 as A
 from exact_attention_forward_06_gb300 import _binding
@@ -9,6 +10,8 @@ from exact_attention_forward_06_gb300 import _binding
 @pytest.fixture(scope="module")
 def lib():
     import os
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up: a call that was not refused would launch")
     if not os.path.exists(_binding.LIBRARY_PATH):
         import __graft_entry__
         __graft_entry__.build()
